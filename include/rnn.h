@@ -278,6 +278,105 @@ int rnn_fwd_noalloc(const rnn_desc_t* desc, const void* Wx, const void* R, const
                     void* h_seq, float* hT, float* cT, float* nT, float* mT, void* stash,
                     int* device_status, void* stream);
 
+/* ---- Operators of language models around and beside the recurrences ------
+ *
+ * Root-mean-square norm with the residual's addition, over rows of N values:
+ *   h = x + residual (rounded to dtype),  r = 1 / sqrt(mean_n h^2 + eps),  y = h r weight
+ * dtype (RNN_F32 / RNN_BF16): type of x, residual, h and y [rows, N]; weight [N]
+ * fp32.  residual NULL = none; h NULL = not written (h may be x or residual).  The
+ * norm is taken of h as stored.  rstd [rows] fp32 (NULL = not written) is r, for the
+ * gradient.  scale NULL: y has dtype.  Otherwise y is 8-bit floating point (e4m3)
+ * and scale [rows, ceil(N/128)] fp32 holds, for each row and block of 128
+ * columns, max|y| / 448 (1 where that is zero); y holds y / scale, rounded
+ * to nearest even.  N == 0 is refused, rows == 0 a no-op.  Any N; widths that are
+ * a multiple of 16 bytes (of 8 values for e4m3) with 16-byte aligned pointers
+ * run the vector kernels.  Alignment: the element's.  No workspace, no device status. */
+int rnn_rms_norm(int32_t dtype, int32_t rows, int32_t N, float eps, const void* x,
+                 const void* residual, const float* weight, void* h, void* y, float* scale,
+                 float* rstd, void* stream);
+
+/* Its gradient from the stored h and rstd (an 8-bit output's rounding counts as the
+ * identity): with xh = h rstd,
+ *   dx = rstd (weight dy - xh mean_n(weight dy xh)) + dh,   dw = sum over rows of dy xh
+ * dx is the gradient of x and of residual alike; dh (NULL = 0) what reaches h from
+ * elsewhere.  dy, h, dh, dx [rows, N] in dtype (dx may be dh), dw [N] fp32 (NULL = not
+ * computed, then the workspace may be NULL).  Sums in fp32, in a fixed order.
+ * rows == 0 sets dw to zero.  Workspace: 256-byte aligned, size below. */
+size_t rnn_rms_norm_bwd_workspace_size(int32_t rows, int32_t N);
+int rnn_rms_norm_bwd(int32_t dtype, int32_t rows, int32_t N, const void* dy, const void* h,
+                     const float* weight, const float* rstd, const void* dh, void* dx, float* dw,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* A weight W [N, K] (dtype) in 8 bits: Wq [N, K] e4m3, Ws [ceil(N/128), ceil(K/128)]
+ * fp32, one scale (max|W| / 448, 1 where that is zero) for each 128 x 128 block. */
+int rnn_quantize_weight(int32_t dtype, int32_t N, int32_t K, const void* W, void* Wq, float* Ws,
+                        void* stream);
+
+/* rnn_input_proj in 8-bit floating point with a scale for each block of 128:
+ *   y[m, n] = sum_b xs[m, b] Ws[n/128, b] (sum_{k in block b} xq[m, k] Wq[n, k]) + bias[n]
+ * xq [M, K], Wq [N, K] e4m3; xs [M, ceil(K/128)] and Ws [ceil(N/128), ceil(K/128)] fp32
+ * (rnn_rms_norm's and rnn_quantize_weight's outputs); bias [N] fp32 (NULL =
+ * none); y [M, N] bf16, rounded once from the fp32 sum.  Requires K % 16 == 0,
+ * N % 8 == 0, M <= 8388480.  Alignment: xq, Wq, y 16 bytes, fp32 pointers 4, workspace
+ * 256 bytes and >= 256 bytes (status word at offset 0).  M == 0 is a no-op. */
+int rnn_input_proj_fp8(int32_t M, int32_t N, int32_t K, const void* xq, const float* xs,
+                       const void* Wq, const float* Ws, const float* bias, void* y,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Linear attention with a decay for each head, lambda_h = exp(log_decay[h]):
+ *   S_t = lambda S_{t-1} + k_t v_t^T,   o_t = scale q_t S_t      (S [Dk, Dv] fp32 per head)
+ * q, k [T, B, NH, Dk], v, o [T, B, NH, Dv] in dtype; Dk, Dv in {32, 64, 128, 256};
+ * log_decay [NH] fp32, <= 0 (a constant of the layer: no gradient; -inf forgets all);
+ * state0, stateT [B, NH, Dk, Dv] fp32 (NULL = zero / not written; stateT may be state0).
+ * lens [B] int32 (NULL = T for every row): tokens of a row that count, taken as at
+ * least 0 and at most T; the others are not read, their outputs are zero, and
+ * stateT is the state after the last one that counts.
+ * Operands may be strided views (of one fused projection, say): strides in elements
+ * for (token, row, head), the innermost dimension contiguous; st NULL = contiguous.
+ * RNN_BF16: tokens are taken in chunks of 64 on the tensor cores, scores and the
+ * state as an operand rounded to bf16 once, all sums and the state fp32.  A v that is not finite can reach
+ * the outputs of earlier tokens of its chunk.  RNN_F32: fp32 throughout.
+ * Alignment: 16 bytes for tensors and strides, 4 for log_decay and lens, workspace 256
+ * and >= rnn_linattn_workspace_size(desc, 0) bytes (status word at offset 0). */
+typedef struct {
+  int32_t dtype; /* rnn_dtype_t of q, k, v, o */
+  int32_t T, B, NH, Dk, Dv;
+  float scale;
+  int32_t flags; /* 0 */
+} rnn_linattn_desc_t;
+
+typedef struct {
+  int64_t q[3], k[3], v[3], o[3]; /* (token, row, head), elements */
+} rnn_linattn_strides_t;
+
+/* Bytes of device workspace of rnn_linattn_fwd (pass 0) / rnn_linattn_bwd (pass 1);
+ * 0 on an invalid desc. */
+size_t rnn_linattn_workspace_size(const rnn_linattn_desc_t* desc, int pass);
+
+int rnn_linattn_fwd(const rnn_linattn_desc_t* desc, const rnn_linattn_strides_t* st, const void* q,
+                    const void* k, const void* v, const float* log_decay, const int32_t* lens,
+                    const float* state0, void* o, float* stateT, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* Gradients of L = sum(o * dout) + sum(stateT * dstateT) from the forward's inputs (nothing
+ * is stashed): dq, dk [T, B, NH, Dk], dv [T, B, NH, Dv] contiguous in dtype, zero for
+ * tokens that do not count; dstate0 [B, NH, Dk, Dv] fp32 (NULL = not written; must not be
+ * dstateT).  dout has the strides st->o; dstateT NULL = zero.  Workspace as above (pass 1). */
+int rnn_linattn_bwd(const rnn_linattn_desc_t* desc, const rnn_linattn_strides_t* st, const void* q,
+                    const void* k, const void* v, const float* log_decay, const int32_t* lens,
+                    const float* state0, const void* dout, const float* dstateT, void* dq, void* dk,
+                    void* dv, float* dstate0, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/* One token (desc->T == 1) for each of B rows out of a cache of n_slots states
+ * [n_slots, NH, Dk, Dv] fp32, updated in place: row b uses state slots[b] (slots NULL: state
+ * b).  A row whose slot is not in [0, n_slots) has no state: its o is zero.  Two rows must
+ * not name the same slot.  o [B, NH, Dv] contiguous in dtype; token strides and st->o are
+ * not used.  Alignment as above.  No workspace, no device status. */
+int rnn_linattn_step(const rnn_linattn_desc_t* desc, const rnn_linattn_strides_t* st, const void* q,
+                     const void* k, const void* v, const float* log_decay, const int32_t* slots,
+                     int32_t n_slots, float* state, void* o, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

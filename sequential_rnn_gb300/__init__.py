@@ -5,7 +5,9 @@ entry points (``rnn_fwd``, ``rnn_bwd``, ...) take torch tensors (or None) and
 only marshal arguments: device pointers, sizes and the current CUDA stream.
 ``forward`` / ``backward`` additionally allocate the outputs with torch and
 raise ``RnnError`` on a non-OK status.  Every step of the recurrence runs in
-the library's CUDA kernels; there is no CPU fallback.
+the library's CUDA kernels; there is no CPU fallback.  ``lm`` adds the operators
+of language models (norm, 8-bit projection, linear attention); its names are
+exported here as well.
 """
 from __future__ import annotations
 
@@ -14,6 +16,8 @@ import ctypes
 import torch
 
 from . import _lib
+from . import lm as _lm
+from .lm import *  # noqa: F401,F403  (the operators of language models)
 from ._lib import (CELLS, DTYPES, RNN_BF16, RNN_F32, RNN_FLAG_H_BF16, RNN_FLAG_TEST_TIMEOUT,
                    RNN_FLAG_TRAIN, RNN_HOST_DIRECT,
                    STATUS, rnn_desc_t)
@@ -22,7 +26,7 @@ __all__ = ["RnnError", "make_desc", "rnn_workspace_size", "rnn_stash_size", "rnn
            "rnn_read_status", "rnn_sync_floor", "rnn_fwd_config", "rnn_status_str", "rnn_fwd_noalloc",
            "rnn_input_proj", "rnn_stack_workspace_size", "rnn_stack_fwd", "forward", "backward",
            "input_proj", "stack_forward", "rnn_plan", "rnn_fwd_host_workspace_size",
-           "rnn_fwd_host", "forward_host", "GATES"]
+           "rnn_fwd_host", "forward_host", "GATES"] + _lm.__all__
 
 GATES = {"lstm": 4, "gru": 3, "slstm": 4}
 

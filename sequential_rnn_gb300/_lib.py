@@ -30,7 +30,10 @@ DTYPES = {"f32": RNN_F32, "bf16": RNN_BF16}
 EXPORTS = ("rnn_workspace_size", "rnn_stash_size", "rnn_fwd", "rnn_bwd", "rnn_read_status",
            "rnn_sync_floor", "rnn_fwd_config", "rnn_status_str", "rnn_fwd_noalloc",
            "rnn_input_proj", "rnn_stack_workspace_size", "rnn_stack_fwd", "rnn_plan",
-           "rnn_fwd_host_workspace_size", "rnn_fwd_host")
+           "rnn_fwd_host_workspace_size", "rnn_fwd_host", "rnn_rms_norm",
+           "rnn_rms_norm_bwd_workspace_size", "rnn_rms_norm_bwd", "rnn_quantize_weight",
+           "rnn_input_proj_fp8", "rnn_linattn_workspace_size", "rnn_linattn_fwd",
+           "rnn_linattn_bwd", "rnn_linattn_step")
 
 
 class rnn_desc_t(ctypes.Structure):
@@ -39,10 +42,23 @@ class rnn_desc_t(ctypes.Structure):
                 ("flags", ctypes.c_int32), ("cluster", ctypes.c_int32)]
 
 
+class rnn_linattn_desc_t(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("T", ctypes.c_int32), ("B", ctypes.c_int32),
+                ("NH", ctypes.c_int32), ("Dk", ctypes.c_int32), ("Dv", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("flags", ctypes.c_int32)]
+
+
+class rnn_linattn_strides_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64 * 3) for n in ("q", "k", "v", "o")]
+
+
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _I = ctypes.c_int
+_I32 = ctypes.c_int32
 _DESC = ctypes.POINTER(rnn_desc_t)
+_LDESC = ctypes.POINTER(rnn_linattn_desc_t)
+_LST = ctypes.POINTER(rnn_linattn_strides_t)
 
 _SIGS = {
     "rnn_workspace_size": (_SZ, [_DESC, _I]),
@@ -60,6 +76,15 @@ _SIGS = {
     "rnn_plan": (_I, [_DESC, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)]),
     "rnn_fwd_host_workspace_size": (_SZ, [_DESC, ctypes.c_int32]),
     "rnn_fwd_host": (_I, [_DESC, ctypes.c_int32] + [_P] * 13 + [_SZ, _P]),
+    "rnn_rms_norm": (_I, [_I32] * 3 + [ctypes.c_float] + [_P] * 8),
+    "rnn_rms_norm_bwd_workspace_size": (_SZ, [_I32] * 2),
+    "rnn_rms_norm_bwd": (_I, [_I32] * 3 + [_P] * 8 + [_SZ, _P]),
+    "rnn_quantize_weight": (_I, [_I32] * 3 + [_P] * 4),
+    "rnn_input_proj_fp8": (_I, [_I32] * 3 + [_P] * 7 + [_SZ, _P]),
+    "rnn_linattn_workspace_size": (_SZ, [_LDESC, _I]),
+    "rnn_linattn_fwd": (_I, [_LDESC, _LST] + [_P] * 9 + [_SZ, _P]),
+    "rnn_linattn_bwd": (_I, [_LDESC, _LST] + [_P] * 13 + [_SZ, _P]),
+    "rnn_linattn_step": (_I, [_LDESC, _LST] + [_P] * 5 + [_I32] + [_P] * 3),
 }
 
 _lib = None

@@ -1,0 +1,88 @@
+// What the linear-attention kernels share: the place of a CTA, powers of the
+// decay, and the scan over the segments of the token axis.
+//
+// A long sequence is cut into segments so that its heads fill the GPU: one
+// launch sums each segment's own contribution to the state (from zero), the scan
+// turns these into the state at the start of every segment, and the main launch
+// runs all segments at once.
+#pragma once
+#include <cstdint>
+
+#include "lm.h"
+
+namespace srnn {
+
+// lambda^n, n >= 0 (lg = log2 lambda, possibly -inf)
+__device__ __forceinline__ float pw(float lg, int n) { return n == 0 ? 1.f : exp2f(lg * (float)n); }
+
+struct Where {
+  int job, b, h, bh, vt, seg;
+};
+__device__ __forceinline__ Where where_of(const LinAttnParams& p, int VT, int segs) {
+  Where w;
+  int i = blockIdx.x;
+  w.seg = i % segs;
+  i /= segs;
+  w.vt = i % VT;
+  i /= VT;
+  w.bh = i % (p.B * p.NH);
+  w.job = i / (p.B * p.NH);
+  w.b = w.bh / p.NH;
+  w.h = w.bh % p.NH;
+  return w;
+}
+__device__ __forceinline__ int row_len(const LinAttnParams& p, int b) {
+  if (p.lens == nullptr) return p.T;
+  const int n = p.lens[b];
+  return n < 0 ? 0 : (n > p.T ? p.T : n);
+}
+// segment states (slot s: the state segment s starts from): [segment][pass][head of a row][v tile] tiles of `tile` values
+__device__ __forceinline__ float* seg_state(const LinAttnParams& p, const Where& w, int seg, int VT,
+                                            int tile) {
+  return p.ws + ((((long long)seg * p.npass + w.job) * p.B * p.NH + w.bh) * VT + w.vt) * tile;
+}
+
+// Contributions of segments 0 .. nseg - 2 (in slots 1 ..) -> the states that the
+// segments start from, in place; slot 0 gets the initial state, so that the main
+// launch reads no initial state that it may be writing as the final one.  Order::at maps a place in a workspace tile to (dk, v).
+template <class Order>
+__global__ void __launch_bounds__(256)
+    linattn_scan_kernel(const __grid_constant__ LinAttnParams p, int seg_tokens) {
+  constexpr int TILE = Order::DK * Order::DVT, PER = TILE / 256;  // blocks of 256 per tile
+  const int VT = p.DV / Order::DVT;
+  const int e = (blockIdx.x % PER) * 256 + threadIdx.x;
+  int i = blockIdx.x / PER;
+  Where w;
+  w.vt = i % VT;
+  i /= VT;
+  w.bh = i % (p.B * p.NH);
+  w.job = i / (p.B * p.NH);
+  w.b = w.bh / p.NH;
+  w.h = w.bh % p.NH;
+  w.seg = 0;
+  const LinAttnPass& ps = p.pass[w.job];
+  const int len = row_len(p, w.b);
+  const int n = len > 0 ? (len - 1) / seg_tokens : 0;  // segments that another one follows
+  const float lam = pw(p.log_decay[w.h] * 1.4426950408889634f, seg_tokens);
+  int dk, v;
+  Order::at(e, dk, v);
+  v += w.vt * Order::DVT;
+  const float* in = ps.init ? ps.init + (long long)w.bh * Order::DK * p.DV : nullptr;
+  float s = in ? in[ps.init_t ? (long long)v * Order::DK + dk : (long long)dk * p.DV + v] : 0.f;
+  float* ws = seg_state(p, w, 0, VT, TILE) + e;
+  *ws = s;
+  const long long step = (long long)p.npass * p.B * p.NH * VT * TILE;
+  ws += step;
+  for (int k = 0; k < n; k += 8) {  // eight loads in flight
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = k + j < n ? ws[(k + j) * step] : 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      s = fmaf(lam, s, x[j]);
+      if (k + j < n) ws[(k + j) * step] = s;
+    }
+  }
+}
+
+}  // namespace srnn
