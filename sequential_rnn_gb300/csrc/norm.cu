@@ -145,12 +145,244 @@ __global__ void __launch_bounds__(256) norm_bwd_any_kernel(const NormBwdParams p
   }
 }
 
-// dw[n] = sum over the partial rows, in their order
+// ------------------------------------------------------- vector kernels --
+// Rows whose width and pointers allow 16-byte accesses (8 bf16 or 4 fp32 values)
+// and fit a CTA's registers.  W = 1: a warp per row (up to 128 vectors), else a
+// CTA per row.  A row's vectors v = t + i TPR stay in registers between the sum and the
+// output, so every byte moves once; 128 columns are 16 (bf16) or 32 (fp32)
+// neighbouring threads' vectors, which find the block's largest value by shuffles.
+template <class T>
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int E = 8;
+  static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
+    f[0] = bf16_lo(u.x), f[1] = bf16_hi(u.x), f[2] = bf16_lo(u.y), f[3] = bf16_hi(u.y);
+    f[4] = bf16_lo(u.z), f[5] = bf16_hi(u.z), f[6] = bf16_lo(u.w), f[7] = bf16_hi(u.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+  }
+};
+template <>
+struct Vec<float> {
+  static constexpr int E = 4;
+  static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[4]) {
+    f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y);
+    f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+  }
+};
+template <int E>
+__device__ __forceinline__ void load_weight(const float* w, int col, float (&f)[E]) {
+#pragma unroll
+  for (int j = 0; j < E; j += 4) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(w + col + j));
+    f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
+  }
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+constexpr int kRowsPerCta = 8;  // warp-per-row kernels: 256 threads
+
+template <class T, int NV, bool WARP, bool QUANT>
+__global__ void __launch_bounds__(WARP ? 256 : 1024) norm_vec_kernel(const NormParams p) {
+  constexpr int E = Vec<T>::E;
+  __shared__ float red[32];
+  const int TPR = WARP ? 32 : blockDim.x;
+  const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
+  const long long row = WARP ? (long long)blockIdx.x * kRowsPerCta + (threadIdx.x >> 5) : blockIdx.x;
+  if (WARP && row >= p.rows) return;
+  const int nv = p.N / E;
+  const uint4* x = reinterpret_cast<const uint4*>(p.x) + row * nv;
+  const uint4* res = reinterpret_cast<const uint4*>(p.residual) + row * nv;
+  uint4* h = reinterpret_cast<uint4*>(p.h) + row * nv;
+  uint4 hv[NV], rv[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = t + i * TPR;
+    hv[i] = v < nv ? x[v] : make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (p.residual) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = t + i * TPR;
+      rv[i] = v < nv ? res[v] : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float a[E];
+    Vec<T>::unpack(hv[i], a);
+    if (p.residual) {
+      float b[E];
+      Vec<T>::unpack(rv[i], b);
+#pragma unroll
+      for (int j = 0; j < E; ++j) a[j] += b[j];
+      hv[i] = Vec<T>::pack(a);  // the rounding of h
+      Vec<T>::unpack(hv[i], a);
+    }
+    const int v = t + i * TPR;
+    if (p.h && v < nv) h[v] = hv[i];
+#pragma unroll
+    for (int j = 0; j < E; ++j) ss += a[j] * a[j];
+  }
+  const float sum = WARP ? warp_sum(ss) : block_sum(ss, red);
+  const float r = rsqrtf(sum / (float)p.N + p.eps);
+  if (p.rstd && t == 0) p.rstd[row] = r;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = t + i * TPR;
+    if (!QUANT && v >= nv) break;
+    float y[E], w[E];
+    Vec<T>::unpack(hv[i], y);
+    load_weight<E>(p.weight, (v < nv ? v : 0) * E, w);  // (past the row y is zero)
+#pragma unroll
+    for (int j = 0; j < E; ++j) y[j] = v < nv ? y[j] * r * w[j] : 0.f;
+    if (!QUANT) {
+      reinterpret_cast<uint4*>(p.y)[row * nv + v] = Vec<T>::pack(y);
+      continue;
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < E; ++j) top = fmaxf(top, fabsf(y[j]));
+#pragma unroll
+    for (int o = kBlk / E / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float s = block_scale(top);
+    if (v >= nv) continue;
+    if (v % (kBlk / E) == 0) p.scale[row * ((p.N + kBlk - 1) / kBlk) + v / (kBlk / E)] = s;
+    uint32_t q[E / 4];
+#pragma unroll
+    for (int j = 0; j < E; j += 4) {
+      uint32_t u = 0;
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(
+            make_float2(y[j + k] / s, y[j + k + 1] / s), __NV_SATFINITE, __NV_E4M3);
+        u |= (uint32_t)two << (8 * k);
+      }
+      q[j / 4] = u;
+    }
+    uint8_t* dst = static_cast<uint8_t*>(p.y) + row * p.N + v * E;
+    if constexpr (E == 8)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+    else
+      *reinterpret_cast<uint32_t*>(dst) = q[0];
+  }
+}
+
+// Gradient: a persistent grid; every thread keeps its columns' share of dw in
+// registers over all of its rows.
+template <class T, int NV, bool WARP>
+__global__ void __launch_bounds__(256) norm_bwd_vec_kernel(const NormBwdParams p) {
+  constexpr int E = Vec<T>::E;
+  __shared__ float red[32];
+  const int TPR = WARP ? 32 : blockDim.x;
+  const int t = WARP ? (threadIdx.x & 31) : threadIdx.x, wp = threadIdx.x >> 5;
+  const int nv = p.N / E;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  float dw[NV][E];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < E; ++j) dw[i][j] = 0.f;
+  const long long first = WARP ? (long long)blockIdx.x * kRowsPerCta + wp : blockIdx.x;
+  const long long step = WARP ? (long long)gridDim.x * kRowsPerCta : gridDim.x;
+  for (long long row = first; row < p.rows; row += step) {
+    const uint4* dy = reinterpret_cast<const uint4*>(p.dy) + row * nv;
+    const uint4* h = reinterpret_cast<const uint4*>(p.h) + row * nv;
+    const uint4* dh = reinterpret_cast<const uint4*>(p.dh) + row * nv;
+    uint4 gv[NV], hv[NV], ev[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = t + i * TPR;
+      gv[i] = v < nv ? dy[v] : zero;
+      hv[i] = v < nv ? h[v] : zero;
+      ev[i] = p.dh && v < nv ? dh[v] : zero;
+    }
+    const float r = p.rstd[row];
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = t + i * TPR;
+      float g[E], a[E], w[E];
+      Vec<T>::unpack(gv[i], g);
+      Vec<T>::unpack(hv[i], a);
+      load_weight<E>(p.weight, (v < nv ? v : 0) * E, w);
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const float xh = a[j] * r;
+        dw[i][j] = fmaf(g[j], xh, dw[i][j]);
+        dot = fmaf(g[j] * w[j], xh, dot);
+      }
+    }
+    dot = (WARP ? warp_sum(dot) : block_sum(dot, red)) / (float)p.N;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = t + i * TPR;
+      if (v >= nv) break;
+      float g[E], a[E], e[E], w[E];
+      Vec<T>::unpack(gv[i], g);
+      Vec<T>::unpack(hv[i], a);
+      Vec<T>::unpack(ev[i], e);
+      load_weight<E>(p.weight, v * E, w);
+#pragma unroll
+      for (int j = 0; j < E; ++j) e[j] += r * (w[j] * g[j] - a[j] * r * dot);
+      reinterpret_cast<uint4*>(p.dx)[row * nv + v] = Vec<T>::pack(e);
+    }
+  }
+  if (p.dw == nullptr) return;
+  float* part = p.part + (long long)blockIdx.x * p.N;
+  if (WARP) {  // the CTA's warps one after the other, in shared memory
+    __shared__ float acc[NV * 32 * E];
+    for (int k = 0; k < kRowsPerCta; ++k) {
+      if (wp == k)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int j = 0; j < E; ++j) {
+            float* a = acc + (i * E + j) * 32 + t;
+            *a = k == 0 ? dw[i][j] : *a + dw[i][j];
+          }
+      __syncthreads();
+    }
+    for (int n = threadIdx.x; n < p.N; n += 256) {
+      const int v = n / E;
+      part[n] = acc[((v / 32) * E + n % E) * 32 + v % 32];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = t + i * TPR;
+      if (v >= nv) break;
+#pragma unroll
+      for (int j = 0; j < E; ++j) part[v * E + j] = dw[i][j];
+    }
+  }
+}
+
+// dw[n] = sum over the partial rows: 32 columns per CTA, eight threads of a column
+// take every eighth row, then meet in a fixed order
 __global__ void __launch_bounds__(256) norm_dw_kernel(const float* part, float* dw, int parts, int N) {
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
+  __shared__ float red[8][32];
+  const int c = threadIdx.x & 31, k = threadIdx.x >> 5, n = blockIdx.x * 32 + c;
   float s = 0.f;
-  for (int i = 0; i < parts; ++i) s += part[(long long)i * N + n];
+  if (n < N)
+#pragma unroll 8
+    for (int i = k; i < parts; i += 8) s += part[(long long)i * N + n];
+  red[k][c] = s;
+  __syncthreads();
+  if (k != 0 || n >= N) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) s += red[i][c];
   dw[n] = s;
 }
 
@@ -178,25 +410,77 @@ __global__ void __launch_bounds__(128)
 
 }  // namespace
 
-int launch_rms_norm(const NormParams& p, bool bf16, cudaStream_t s) {
-  const int grid = (int)(p.rows < 65536 ? p.rows : 65536);
-  if (bf16)
-    norm_any_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
-  else
-    norm_any_kernel<float><<<grid, 256, 0, s>>>(p);
+namespace {
+
+bool vec_ok(const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; }
+// threads of a CTA for a row of nv vectors, at most four each; 0: too wide
+int vec_threads(int nv) {
+  for (int t = 64; t <= 1024; t *= 2)
+    if (nv <= 4 * t) return t;
+  return 0;
+}
+
+template <class T, bool QUANT>
+int norm_typed(const NormParams& p, cudaStream_t s) {
+  constexpr int E = Vec<T>::E;
+  const bool vec = p.N % (QUANT ? 8 : E) == 0 && vec_ok(p.x) && vec_ok(p.residual) && vec_ok(p.h) &&
+                   vec_ok(p.weight) && vec_ok(p.y);
+  const int nv = p.N / E, th = vec_threads(nv);
+  if (!vec || th == 0) {
+    norm_any_kernel<T><<<(unsigned)(p.rows < 65536 ? p.rows : 65536), 256, 0, s>>>(p);
+  } else if (nv <= 128) {
+    const unsigned grid = (unsigned)((p.rows + kRowsPerCta - 1) / kRowsPerCta);
+    if (nv <= 64)
+      norm_vec_kernel<T, 2, true, QUANT><<<grid, 256, 0, s>>>(p);
+    else
+      norm_vec_kernel<T, 4, true, QUANT><<<grid, 256, 0, s>>>(p);
+  } else {
+    norm_vec_kernel<T, 4, false, QUANT><<<(unsigned)p.rows, th, 0, s>>>(p);
+  }
   return (int)cudaGetLastError();
 }
 
-int norm_bwd_parts(long long rows, int) { return (int)(rows < 608 ? rows : 608); }
+template <class T>
+int norm_bwd_typed(const NormBwdParams& p, cudaStream_t s) {
+  constexpr int E = Vec<T>::E;
+  const bool vec = p.N % E == 0 && vec_ok(p.dy) && vec_ok(p.h) && vec_ok(p.weight) &&
+                   vec_ok(p.dh) && vec_ok(p.dx);
+  const int nv = p.N / E;
+  int parts = norm_bwd_parts(p.rows, p.N);
+  if (!vec || nv > 8 * 256) {
+    norm_bwd_any_kernel<T><<<parts, 256, 0, s>>>(p);
+  } else if (nv <= 128) {
+    const long long ctas = (p.rows + kRowsPerCta - 1) / kRowsPerCta, cap = 2LL * sm_count();
+    parts = (int)(ctas < cap ? ctas : cap);
+    if (nv <= 64)
+      norm_bwd_vec_kernel<T, 2, true><<<parts, 256, 0, s>>>(p);
+    else
+      norm_bwd_vec_kernel<T, 4, true><<<parts, 256, 0, s>>>(p);
+  } else {
+    const int th = vec_threads(nv);
+    if (th != 0 && th <= 256)
+      norm_bwd_vec_kernel<T, 4, false><<<parts, th, 0, s>>>(p);
+    else
+      norm_bwd_vec_kernel<T, 8, false><<<parts, 256, 0, s>>>(p);
+  }
+  if (p.dw) norm_dw_kernel<<<(p.N + 31) / 32, 256, 0, s>>>(p.part, p.dw, parts, p.N);
+  return (int)cudaGetLastError();
+}
+
+}  // namespace
+
+int launch_rms_norm(const NormParams& p, bool bf16, cudaStream_t s) {
+  if (p.scale) return bf16 ? norm_typed<__nv_bfloat16, true>(p, s) : norm_typed<float, true>(p, s);
+  return bf16 ? norm_typed<__nv_bfloat16, false>(p, s) : norm_typed<float, false>(p, s);
+}
+
+int norm_bwd_parts(long long rows, int) {
+  const long long cap = 4LL * sm_count();
+  return (int)(rows < cap ? rows : cap);
+}
 
 int launch_rms_norm_bwd(const NormBwdParams& p, bool bf16, cudaStream_t s) {
-  const int parts = norm_bwd_parts(p.rows, p.N);
-  if (bf16)
-    norm_bwd_any_kernel<__nv_bfloat16><<<parts, 256, 0, s>>>(p);
-  else
-    norm_bwd_any_kernel<float><<<parts, 256, 0, s>>>(p);
-  if (p.dw) norm_dw_kernel<<<(p.N + 255) / 256, 256, 0, s>>>(p.part, p.dw, parts, p.N);
-  return (int)cudaGetLastError();
+  return bf16 ? norm_bwd_typed<__nv_bfloat16>(p, s) : norm_bwd_typed<float>(p, s);
 }
 
 int launch_quantize_weight(const void* W, bool bf16, int N, int K, void* Wq, float* Ws,
