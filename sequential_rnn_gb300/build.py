@@ -25,7 +25,8 @@ LIB_BC = os.path.join(PKG, "libsrnn_bc.so")
 
 SOURCES = ["capi.cu", "plan.cu", "runtime.cu", "fwd_f32.cu", "fwd_bf16_lstm.cu", "fwd_bf16_gru.cu", "fwd_bf16_slstm.cu",
            "floor.cu", "bwd_cell.cu", "grad_weights.cu", "tc_gemm.cu", "tc_gemm_pair.cu", "noalloc.cu",
-           "lm_capi.cu", "norm.cu", "proj_fp8.cu", "linattn.cu", "linattn_f32.cu", "linattn_step.cu"]
+           "lm_capi.cu", "norm.cu", "proj_fp8.cu", "linattn.cu", "linattn_f32.cu", "linattn_step.cu",
+           "linattn_tc.cu", "linattn_plan.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

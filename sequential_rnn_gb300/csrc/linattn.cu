@@ -78,9 +78,11 @@ __device__ __forceinline__ void state_of(int t, int i, int reg, int& dk, int& v)
 // workspace order of a state tile: quad by quad, the threads' float4 side by side
 template <class C>
 struct QuadOrder {
-  static constexpr int DK = C::DK, DVT = C::DVT;
-  static __device__ __forceinline__ void at(int e, int& dk, int& v) {
+  static constexpr int TILE = C::DK * C::DVT;
+  static __device__ __forceinline__ int tiles(const LinAttnParams& p) { return p.DV / C::DVT; }
+  static __device__ __forceinline__ void at(const LinAttnParams&, int tile, int e, int& dk, int& v) {
     state_of<C>((e / 4) % C::NT, e / (4 * C::NT), e & 3, dk, v);
+    v += tile * C::DVT;
   }
 };
 
@@ -409,7 +411,7 @@ int launch_dk(const LinAttnParams& p, cudaStream_t s) {
 
 }  // namespace
 
-int launch_linattn_bf16(const LinAttnParams& p, cudaStream_t s) {
+int launch_linattn_mma(const LinAttnParams& p, cudaStream_t s) {
   switch (p.DK) {
     case 32: return launch_dk<32>(p, s);
     case 64: return launch_dk<64>(p, s);

@@ -44,12 +44,12 @@ __device__ __forceinline__ float* seg_state(const LinAttnParams& p, const Where&
 
 // Contributions of segments 0 .. nseg - 2 (in slots 1 ..) -> the states that the
 // segments start from, in place; slot 0 gets the initial state, so that the main
-// launch reads no initial state that it may be writing as the final one.  Order::at maps a place in a workspace tile to (dk, v).
+// launch reads no initial state that it may be writing as the final one.  Order maps a place in a workspace tile to (dk, v).
 template <class Order>
 __global__ void __launch_bounds__(256)
     linattn_scan_kernel(const __grid_constant__ LinAttnParams p, int seg_tokens) {
-  constexpr int TILE = Order::DK * Order::DVT, PER = TILE / 256;  // blocks of 256 per tile
-  const int VT = p.DV / Order::DVT;
+  constexpr int TILE = Order::TILE, PER = TILE / 256;  // blocks of 256 per tile
+  const int VT = Order::tiles(p);
   const int e = (blockIdx.x % PER) * 256 + threadIdx.x;
   int i = blockIdx.x / PER;
   Where w;
@@ -65,10 +65,9 @@ __global__ void __launch_bounds__(256)
   const int n = len > 0 ? (len - 1) / seg_tokens : 0;  // segments that another one follows
   const float lam = pw(p.log_decay[w.h] * 1.4426950408889634f, seg_tokens);
   int dk, v;
-  Order::at(e, dk, v);
-  v += w.vt * Order::DVT;
-  const float* in = ps.init ? ps.init + (long long)w.bh * Order::DK * p.DV : nullptr;
-  float s = in ? in[ps.init_t ? (long long)v * Order::DK + dk : (long long)dk * p.DV + v] : 0.f;
+  Order::at(p, w.vt, e, dk, v);
+  const float* in = ps.init ? ps.init + (long long)w.bh * p.DK * p.DV : nullptr;
+  float s = in ? in[ps.init_t ? (long long)v * p.DK + dk : (long long)dk * p.DV + v] : 0.f;
   float* ws = seg_state(p, w, 0, VT, TILE) + e;
   *ws = s;
   const long long step = (long long)p.npass * p.B * p.NH * VT * TILE;

@@ -25,12 +25,13 @@ struct La32Cfg {
   static constexpr uint32_t FLOATS = 2 * kC32 * LD + kC32 * kV32 + kC32 * (kC32 + 1) + DK * kV32 + 3 * kC32;
   static constexpr uint32_t SMEM = FLOATS * 4;
 };
-template <int DK_>
+template <int DK>
 struct RowOrder {
-  static constexpr int DK = DK_, DVT = kV32;
-  static __device__ __forceinline__ void at(int e, int& dk, int& v) {
+  static constexpr int TILE = DK * kV32;
+  static __device__ __forceinline__ int tiles(const LinAttnParams& p) { return p.DV / kV32; }
+  static __device__ __forceinline__ void at(const LinAttnParams&, int tile, int e, int& dk, int& v) {
     dk = e / kV32;
-    v = e % kV32;
+    v = tile * kV32 + e % kV32;
   }
 };
 
@@ -223,27 +224,6 @@ int launch_linattn_f32(const LinAttnParams& p, cudaStream_t s) {
     case 256: return launch_dk<256>(p, s);
     default: return (int)cudaErrorInvalidValue;
   }
-}
-
-LinAttnPlan linattn_plan(bool bf16, int npass, int T, int B, int NH, int DK, int DV) {
-  const int chunk = bf16 ? 64 : kC32;
-  const int dvt = bf16 ? (DV % 64 == 0 ? 64 : 32) : kV32;
-  const int occ = bf16 ? (DK <= 64 ? 3 : (DK == 128 ? 2 : 1)) : (DK <= 64 ? 4 : (DK == 128 ? 3 : 2));
-  const long long nch = ((long long)T + chunk - 1) / chunk;
-  const long long base = (long long)npass * B * NH * (DV / dvt);
-  const long long cap = (long long)sm_count() * occ;
-  long long nseg = 1;
-  if (base > 0 && 2 * base <= cap) {
-    nseg = cap / base;
-    if (nseg > nch / 2) nseg = nch / 2;
-    if (nseg < 1) nseg = 1;
-  }
-  LinAttnPlan pl;
-  const long long per = nch > 0 ? (nch + nseg - 1) / nseg : 1;
-  pl.seg_chunks = (int)per;
-  pl.nseg = nch > 0 ? (int)((nch + per - 1) / per) : 1;
-  pl.ws_bytes = (size_t)(pl.nseg > 1 ? pl.nseg : 0) * npass * B * NH * DK * DV * sizeof(float);
-  return pl;
 }
 
 }  // namespace srnn

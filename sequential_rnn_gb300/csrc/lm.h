@@ -84,14 +84,20 @@ struct LinAttnParams {
   int T, B, NH, DK, DV;
   float* ws;               // segment states
   int nseg, seg_chunks;    // segments of the token axis, chunks in each
+  void* chunk_states;      // bf16 [pass][head of a row][chunk][DK][DV] (kLinAttnTc)
   int* status;
+  unsigned long long timeout_ns;
 };
+enum : int { kLinAttnF32 = 0, kLinAttnMma = 1, kLinAttnTc = 2 };
 struct LinAttnPlan {
+  int path;
   int nseg, seg_chunks;
-  size_t ws_bytes;  // segment states
+  size_t seg_bytes;    // segment states
+  size_t chunk_bytes;  // chunk states (kLinAttnTc)
 };
 LinAttnPlan linattn_plan(bool bf16, int npass, int T, int B, int NH, int DK, int DV);
-int launch_linattn_bf16(const LinAttnParams& p, cudaStream_t s);
+int launch_linattn_mma(const LinAttnParams& p, cudaStream_t s);
+int launch_linattn_tc(const LinAttnParams& p, cudaStream_t s);
 int launch_linattn_f32(const LinAttnParams& p, cudaStream_t s);
 
 struct LinAttnStepParams {

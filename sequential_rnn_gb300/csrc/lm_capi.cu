@@ -50,14 +50,17 @@ void set3(long long (&dst)[3], const St& s) {
   for (int i = 0; i < 3; ++i) dst[i] = s.s[i];
 }
 
+size_t plan_bytes(const LinAttnPlan& pl) {
+  return align_up(pl.seg_bytes, 256) + align_up(pl.chunk_bytes, 256);
+}
 // workspace of the gradient: the passes of dq and dk contract over Dv, dv's over Dk;
 // with equal sizes the three run as one launch
 size_t linattn_ws(const rnn_linattn_desc_t* d, int pass) {
   const bool bf16 = d->dtype == RNN_BF16;
-  if (pass == 0) return linattn_plan(bf16, 1, d->T, d->B, d->NH, d->Dk, d->Dv).ws_bytes;
-  if (d->Dk == d->Dv) return linattn_plan(bf16, 3, d->T, d->B, d->NH, d->Dk, d->Dv).ws_bytes;
-  const size_t a = linattn_plan(bf16, 2, d->T, d->B, d->NH, d->Dv, d->Dk).ws_bytes;
-  const size_t b = linattn_plan(bf16, 1, d->T, d->B, d->NH, d->Dk, d->Dv).ws_bytes;
+  if (pass == 0) return plan_bytes(linattn_plan(bf16, 1, d->T, d->B, d->NH, d->Dk, d->Dv));
+  if (d->Dk == d->Dv) return plan_bytes(linattn_plan(bf16, 3, d->T, d->B, d->NH, d->Dk, d->Dv));
+  const size_t a = plan_bytes(linattn_plan(bf16, 2, d->T, d->B, d->NH, d->Dv, d->Dk));
+  const size_t b = plan_bytes(linattn_plan(bf16, 1, d->T, d->B, d->NH, d->Dk, d->Dv));
   return a > b ? a : b;  // the two launches follow one another on the stream
 }
 
@@ -67,9 +70,13 @@ int run_passes(LinAttnParams& p, bool bf16, int DK, int DV, void* workspace, cud
   const LinAttnPlan pl = linattn_plan(bf16, p.npass, p.T, p.B, p.NH, DK, DV);
   p.nseg = pl.nseg;
   p.seg_chunks = pl.seg_chunks;
-  p.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + kStatusBytes);
+  char* ws = static_cast<char*>(workspace) + kStatusBytes;
+  p.ws = reinterpret_cast<float*>(ws);
+  p.chunk_states = ws + align_up(pl.seg_bytes, 256);
   p.status = static_cast<int*>(workspace);
-  return bf16 ? launch_linattn_bf16(p, s) : launch_linattn_f32(p, s);
+  p.timeout_ns = kTimeoutNs;
+  if (pl.path == kLinAttnTc) return launch_linattn_tc(p, s);
+  return pl.path == kLinAttnMma ? launch_linattn_mma(p, s) : launch_linattn_f32(p, s);
 }
 
 }  // namespace

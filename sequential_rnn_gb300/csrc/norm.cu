@@ -451,7 +451,8 @@ int norm_bwd_typed(const NormBwdParams& p, cudaStream_t s) {
     norm_bwd_any_kernel<T><<<parts, 256, 0, s>>>(p);
   } else if (nv <= 128) {
     const long long ctas = (p.rows + kRowsPerCta - 1) / kRowsPerCta, cap = 2LL * sm_count();
-    parts = (int)(ctas < cap ? ctas : cap);
+    if (ctas < parts) parts = (int)ctas;
+    if (cap < parts) parts = (int)cap;
     if (nv <= 64)
       norm_bwd_vec_kernel<T, 2, true><<<parts, 256, 0, s>>>(p);
     else
@@ -474,10 +475,7 @@ int launch_rms_norm(const NormParams& p, bool bf16, cudaStream_t s) {
   return bf16 ? norm_typed<__nv_bfloat16, false>(p, s) : norm_typed<float, false>(p, s);
 }
 
-int norm_bwd_parts(long long rows, int) {
-  const long long cap = 4LL * sm_count();
-  return (int)(rows < cap ? rows : cap);
-}
+int norm_bwd_parts(long long rows, int) { return (int)(rows < 608 ? rows : 608); }  // 4 x 152 SMs
 
 int launch_rms_norm_bwd(const NormBwdParams& p, bool bf16, cudaStream_t s) {
   return bf16 ? norm_bwd_typed<__nv_bfloat16>(p, s) : norm_bwd_typed<float>(p, s);
