@@ -7,16 +7,25 @@
 //   outputs  out = mask(x a^T) c + decay (x S), all chunks at once
 //
 // Split in two, only the cheap part (one product of the three) is sequential, and the
-// outputs fill the GPU with independent CTAs whose loads, MMAs and epilogues overlap one
-// another's; the chunk states cost 2 Dk Dv bytes per 128 tokens and head, written and
-// read once, mostly inside L2.
+// outputs are independent tiles for a persistent grid; the chunk states cost 2 Dk Dv
+// bytes per 128 tokens and head, written and read once, mostly inside L2.
 //
 // The states' CTA holds 128 (or 64) x 64 of S in fp32 registers.  c times its weight is split into
 // three bf16 terms (24 bits), so that the state does not lose to operand rounding what fp32
 // keeps; the three products of a chunk accumulate from zero, smallest first, in TMEM, and the
 // sum joins the decayed state in round-to-nearest.
-// Shared-memory tiles are rows of 64 values (128 bytes, 128-byte swizzle): the same tile
-// is a K-major operand (scores) and an MN-major one (state update, P c, x S).
+//
+// Both kernels have one control warp (one lane: TMA loads, MMA issue, buffer bookkeeping)
+// and 8 or 16 compute warps (terms of c, decay and mask of the scores, state and
+// output epilogues); mbarriers order them.  Tiles are rows of 64 values (128 bytes, 128-byte
+// swizzle): the same tile is a K-major operand (scores) and an MN-major one (state
+// update, P c, x S).  Loading through the copy engine matters: with cp.async from all threads
+// the copies of a tile took longer to issue (2,000-2,600 cycles) than its MMAs to run.
+//
+// A pass with reversed time loads the same ascending token rows (a box that begins before
+// token 0 reads zeros there): row i of a chunk is then its token 127 - i, and the mask
+// and the powers of the decay run the other way.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -31,101 +40,140 @@
 namespace srnn {
 namespace {
 
-constexpr int kTC = 128;                     // tokens per chunk
-constexpr int kTT = 256;                     // threads per CTA
-constexpr uint32_t kBlkBytes = kTC * 128;    // 128 rows x 64 columns
+constexpr int kTC = 128;                  // tokens per chunk
+constexpr uint32_t kBlkBytes = kTC * 128; // 128 rows x 64 columns
 
-__device__ __forceinline__ void zfill16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
+// tensor maps: x, a, c, out of each pass [T, B, NH, D]; chunk states as rows of DV
+struct TcMaps {
+  CUtensorMap x[kLinAttnPasses], a[kLinAttnPasses], c[kLinAttnPasses], out[kLinAttnPasses];
+  CUtensorMap s_load, s_store;
+  // 0 where the operand is shared by all heads / rows (its map has one)
+  int xh[kLinAttnPasses], xb[kLinAttnPasses], ah[kLinAttnPasses], ab[kLinAttnPasses];
+  int ch[kLinAttnPasses], cb[kLinAttnPasses];
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                            int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                             uint32_t src) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
+      : "memory");
 }
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-// offset of 16-byte chunk ch (of all blocks) of row r
+__device__ __forceinline__ void sts128(uint32_t at, const uint32_t* v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3])
+               : "memory");
+}
+// offset of 16-byte chunk ch of row r in a 64-column block
 __device__ __forceinline__ uint32_t blk_at(int r, int ch) {
-  return (uint32_t)(ch >> 3) * kBlkBytes + (uint32_t)(r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+  return (uint32_t)(r * 128 + ((ch ^ (r & 7)) << 4));
+}
+// N consecutive TMEM columns of this warp's lanes
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[N]) {
+  if constexpr (N == 32)
+    tmem_ld32(at, r);
+  else
+    tmem_ld16(at, r);
+}
+template <int N>
+__device__ __forceinline__ void reg_fence(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// A wait is bounded in time: one that runs out sets the status word and the CTA's
+// abort flag, on which every other wait gives up.
 struct TcWait {
   int* status;
   unsigned long long limit_ns;
   volatile int* abort_flag;
-};
-// mbarrier wait bounded in time: a wait that runs out sets the status word and the
-// CTA's abort flag
-__device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, const TcWait& w) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (;;) {
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
     if (mbar_try_wait(bar, parity)) return true;
-    if (*w.abort_flag) return false;
-    if (globaltimer_ns() - t0 > w.limit_ns) {
-      *w.abort_flag = 1;
-      atomicOr(w.status, kStatusTimeout);
-      return false;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > limit_ns) {
+        *abort_flag = 1;
+        atomicOr(status, kStatusTimeout);
+        return false;
+      }
     }
   }
+};
+// after an abort: a copy that was issued on `bar` lands before the CTA leaves
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > 10000000ull) break;
+}
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// 128 rows (tokens r0 ..) x D columns of a strided operand into swizzled blocks
-template <int D>
-__device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16* src, long long stride,
-                                          int r0, int len, bool rev) {
-  constexpr int CH = D / 8;
-#pragma unroll
-  for (int i = 0; i < kTC * CH / kTT; ++i) {
-    const int e = threadIdx.x + i * kTT, row = e / CH, ch = e % CH, r = r0 + row;
-    const bool ok = r < len;
-    const long long t = ok ? (rev ? len - 1 - r : r) : 0;
-    zfill16(dst + blk_at(row, ch), src + t * stride + ch * 8, ok);
-  }
-}
-
-template <int DK>
+// ---------------------------------------------------------------- states --
+template <int DK_>
 struct StCfg {
-  static constexpr int DKB = DK < 128 ? DK : 128;   // state rows (dk) per CTA
+  static constexpr int DK = DK_;
+  static constexpr int DKB = DK < 128 ? DK : 128;    // state rows (dk) per CTA
   static constexpr int MB = DK / DKB;
-  static constexpr uint32_t A = (DKB / 64) * kBlkBytes;
-  static constexpr int NA = 3;                      // buffers of a: two chunks ahead
-  // sets of c's three terms.  With two, a chunk's terms are made while the one before is
-  // multiplied; with 64 state rows one set, so that two CTAs fit on an SM.
-  static constexpr int NT = DKB == 128 ? 2 : 1;
+  static constexpr int NCW = DKB == 128 ? 16 : 8;    // compute warps
+  static constexpr int THREADS = 32 * (NCW + 1);
   static constexpr int OCC = DKB == 128 ? 1 : 2;
+  static constexpr int NC = 64 / (NCW / 4);          // state columns of a thread
+  static constexpr uint32_t A = (DKB / 64) * kBlkBytes;
+  // sets of c's three terms (and buffers of c).  With two, a chunk's terms are made while the one
+  // before is multiplied; with 64 state rows one set, so that two CTAs fit on an SM.
+  static constexpr int NT = DKB == 128 ? 2 : 1;
+  static constexpr uint32_t sA = 0, sC = 2 * A, sT = sC + NT * kBlkBytes;
   // (with 64 state rows the MMA's other 64 rows read the tile behind a, and are not used)
-  static constexpr uint32_t SMEM = NA * A + NT * 3 * kBlkBytes + 1024;
+  static constexpr uint32_t sS = sT + NT * 3 * kBlkBytes;
+  static constexpr uint32_t SMEM = sS + DKB * 128 + 1024;
   static constexpr int TILE = DKB * 64;
 };
 
-// workspace order of a state tile: quad by quad, the active threads' float4 side by side
+// workspace order of a state tile: quad by quad, the owning threads' float4 side by side
 template <int DK>
 struct TcOrder {
-  static constexpr int TILE = StCfg<DK>::TILE;
-  static __device__ __forceinline__ int tiles(const LinAttnParams& p) {
-    return StCfg<DK>::MB * (p.DV / 64);
-  }
+  using C = StCfg<DK>;
+  static constexpr int TILE = C::TILE;
+  static constexpr int OWN = C::DKB * (64 / C::NC);
+  static __device__ __forceinline__ int tiles(const LinAttnParams& p) { return C::MB * (p.DV / 64); }
   static __device__ __forceinline__ void at(const LinAttnParams& p, int tile, int e, int& dk, int& v) {
-    constexpr int DKB = StCfg<DK>::DKB;
-    const int vts = p.DV / 64, th = (e / 4) % (2 * DKB);
-    dk = (tile / vts) * DKB + th % DKB;
-    v = (tile % vts) * 64 + 32 * (th / DKB) + 4 * (e / (8 * DKB)) + (e & 3);
+    const int vts = p.DV / 64, th = (e / 4) % OWN;
+    dk = (tile / vts) * C::DKB + th % C::DKB;
+    v = (tile % vts) * 64 + C::NC * (th / C::DKB) + 4 * (e / (4 * OWN)) + (e & 3);
   }
 };
 
 // STATE_ONLY: a segment's own contribution to the state, from zero, into the workspace.
 template <int DK, bool STATE_ONLY>
-__global__ void __launch_bounds__(kTT, StCfg<DK>::OCC)
-    linattn_states_kernel(const __grid_constant__ LinAttnParams p) {
+__global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
+    linattn_states_kernel(const __grid_constant__ LinAttnParams p, const __grid_constant__ TcMaps m) {
   using C = StCfg<DK>;
-  constexpr int DKB = C::DKB;
+  constexpr int DKB = C::DKB, NC = C::NC, NCW = C::NCW, OWN = TcOrder<DK>::OWN;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int abort_flag_s;
   __shared__ uint32_t tslot_s;
-  __shared__ __align__(8) uint64_t bar_s;
+  __shared__ __align__(8) uint64_t bars_s[10];
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sC = sm + C::NA * C::A;
-  const uint32_t bar = smem_u32(&bar_s);
+  // copies of a, of c; terms ready; MMAs done; state published; its copy out read
+  const uint32_t bar = smem_u32(bars_s);
+  const uint32_t aF = bar, cF = bar + 16, tR = bar + 32, mD = bar + 48, sP = bar + 64, sF = bar + 72;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int vts = p.DV / 64;
   const Where w = where_of(p, C::MB * vts, STATE_ONLY ? p.nseg - 1 : p.nseg);
@@ -139,222 +187,297 @@ __global__ void __launch_bounds__(kTT, StCfg<DK>::OCC)
   const int cend = c1 < lch ? c1 : lch;
   if (STATE_ONLY && (long long)c1 * kTC >= len) return;
   if (!STATE_ONLY && c0 >= cend && w.seg != 0) return;  // nothing to add, nothing to leave
-  const float lg = p.log_decay[w.h] * 1.4426950408889634f;
+  const int cnt = cend > c0 ? cend - c0 : 0;
   const bool rev = ps.reverse != 0;
-  const TcWait tw{p.status, p.timeout_ns, &abort_flag_s};
+  const TcWait wait{p.status, p.timeout_ns, &abort_flag_s};
 
   if (tid == 0) {
-    mbar_init(bar, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(bar + 8 * i, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tR + 8 * i, NCW);
+      mbar_init(mD + 8 * i, 1);
+    }
+    mbar_init(sP, NCW);
+    mbar_init(sF, 1);
     abort_flag_s = 0;
     fence_mbar_init();
     fence_async_smem();
   }
-  if (warp == 0) {
-    tmem_alloc(smem_u32(&tslot_s), 64);
+  if (warp == NCW) {
+    tmem_alloc(smem_u32(&tslot_s), 128);
     tmem_relinquish();
-  }
-  const __nv_bfloat16* ga =
-      static_cast<const __nv_bfloat16*>(ps.a) + w.b * ps.as[1] + w.h * ps.as[2] + mb * DKB;
-  const __nv_bfloat16* gc =
-      static_cast<const __nv_bfloat16*>(ps.c) + w.b * ps.cs[1] + w.h * ps.cs[2] + vt * 64;
-
-  // c of a chunk: rows tid / 8 + 32 i, 16-byte chunk tid % 8
-  uint4 cr[4];
-  auto load_c = [&](int c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = c * kTC + tid / 8 + 32 * i;
-      const long long t = rev ? len - 1 - r : r;
-      cr[i] = r < len ? *reinterpret_cast<const uint4*>(gc + t * ps.cs[0] + (tid % 8) * 8)
-                      : make_uint4(0u, 0u, 0u, 0u);
-    }
-  };
-  auto load_a = [&](int c) {
-    if (c < cend) load_rows<DKB>(sm + ((c - c0) % C::NA) * C::A, ga, ps.as[0], c * kTC, len, rev);
-    cp_async_commit();
-  };
-  if (c0 < cend) load_c(c0);
-  load_a(c0);
-  load_a(c0 + 1);
-
-  // ---- the state at the segment's start: row dk = 32 q + lane, 32 columns --
-  const int q = warp & 3, half = warp >> 2;
-  const bool owner = 32 * q < DKB;
-  const int dk = 32 * q + lane, th = half * DKB + dk;
-  float S[32];
-#pragma unroll
-  for (int j = 0; j < 32; ++j) S[j] = 0.f;
-  if (!STATE_ONLY && owner) {
-    if (p.nseg > 1) {
-      const float4* src = reinterpret_cast<const float4*>(seg_state(p, w, w.seg, C::MB * vts, C::TILE));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 f = src[i * 2 * DKB + th];
-        S[4 * i] = f.x, S[4 * i + 1] = f.y, S[4 * i + 2] = f.z, S[4 * i + 3] = f.w;
-      }
-    } else if (ps.init != nullptr) {
-      const int gk = mb * DKB + dk, gv = vt * 64 + 32 * half;
-      const float* in = ps.init + (long long)w.bh * DK * p.DV;
-      if (ps.init_t) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) S[j] = in[(long long)(gv + j) * DK + gk];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(in + (long long)gk * p.DV + gv + j);
-          S[j] = f.x, S[j + 1] = f.y, S[j + 2] = f.z, S[j + 3] = f.w;
-        }
-      }
-    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tslot_s;
 
-  constexpr uint32_t idesc = idesc_bf16_f32(128, 64, true, true);
-  float wj[4];
-  int wn = -1;
-  // weighted c of chunk c (in cr) in three bf16 terms; then the next chunk's c on its way
-  auto make_terms = [&](int c) {
-    const int n = len - c * kTC < kTC ? len - c * kTC : kTC;
-    if (wn != n) {
-      wn = n;
+  if (warp == NCW) {
+    // ---------------------------------------------------------- control --
+    if (lane == 0 && cnt > 0) {
+      const int hA = w.h * m.ah[w.job], bA = w.b * m.ab[w.job];
+      const int hC = w.h * m.ch[w.job], bC = w.b * m.cb[w.job];
+      auto token = [&](int it) { return rev ? len - (c0 + it + 1) * kTC : (c0 + it) * kTC; };
+      int na = 0, nc = 0;  // copies issued
+      auto load_a = [&](int it) {
+        if (it >= cnt) return;
+        const uint32_t d = sm + C::sA + (it & 1) * C::A, f = aF + 8 * (it & 1);
+        mbar_arrive_expect_tx(f, C::A);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = tid / 8 + 32 * i;
-        wj[i] = j < n ? ps.upd * pw(lg, n - 1 - j + ps.shift) : 0.f;
+        for (int k = 0; k < DKB / 64; ++k)
+          tma_load_4d(d + k * kBlkBytes, &m.a[w.job], mb * DKB + 64 * k, hA, bA, token(it), f);
+        ++na;
+      };
+      auto load_c = [&](int it) {
+        if (it >= cnt) return;
+        const uint32_t f = cF + 8 * (it % C::NT);
+        mbar_arrive_expect_tx(f, kBlkBytes);
+        tma_load_4d(sm + C::sC + (it % C::NT) * kBlkBytes, &m.c[w.job], vt * 64, hC, bC, token(it), f);
+        ++nc;
+      };
+      load_c(0);
+      load_a(0);
+      if (C::NT == 2) load_c(1);
+      load_a(1);
+      constexpr uint32_t idesc = idesc_bf16_f32(128, 64, true, true);
+      int it = 0;
+      for (; it < cnt; ++it) {
+        if (!wait(tR + 8 * (it & 1), (it >> 1) & 1)) break;
+        load_c(it + C::NT);  // its buffer's terms have been made
+        if (!wait(aF + 8 * (it & 1), (it >> 1) & 1)) break;
+        tc_fence_after();
+        const uint32_t a = sm + C::sA + (it & 1) * C::A, t = sm + C::sT + (it % C::NT) * (3 * kBlkBytes);
+        const uint32_t d = tmem + (it & 1) * 64;
+#pragma unroll
+        for (int term = 2; term >= 0; --term)
+#pragma unroll
+          for (int ks = 0; ks < kTC / 16; ++ks)
+            umma_bf16(d, sdesc_sw128(a + ks * 2048, kBlkBytes, 1024),
+                      sdesc_sw128(t + term * kBlkBytes + ks * 2048, kBlkBytes, 1024), idesc,
+                      (term != 2 || ks != 0) ? 1u : 0u);
+        umma_commit(mD + 8 * (it & 1));
+        if (it >= 1) {  // the next a goes where the previous chunk's MMAs have read
+          if (!wait(mD + 8 * ((it - 1) & 1), ((it - 1) >> 1) & 1)) break;
+          load_a(it + 1);
+        }
+        // the state at this chunk's start is in shared memory (and the sum before it was read)
+        if (!wait(sP, it & 1)) break;
+        tc_fence_after();
+        if (!STATE_ONLY) {
+          tma_store_2d(&m.s_store, vt * 64,
+                       ((w.job * p.B * p.NH + w.bh) * nch + c0 + it) * DK + mb * DKB, sm + C::sS);
+          bulk_commit();
+          bulk_wait_read_all();
+        }
+        mbar_arrive(sF);
+      }
+      if (it < cnt) {
+        for (int k = na - 2 < 0 ? 0 : na - 2; k < na; ++k) drain(aF + 8 * (k & 1), (k >> 1) & 1);
+        for (int k = nc - C::NT < 0 ? 0 : nc - C::NT; k < nc; ++k)
+          drain(cF + 8 * (k % C::NT), (k / C::NT) & 1);
+      }
+      if (!STATE_ONLY) bulk_wait_all();
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- compute --
+    const float lg = p.log_decay[w.h] * 1.4426950408889634f;
+    const int q = warp & 3, g = warp >> 2;
+    const bool owner = 32 * q < DKB;  // of row dk = 32 q + lane, columns NC g ..
+    const int dk = 32 * q + lane, th = g * DKB + dk;
+    const int gk = mb * DKB + dk, gv = vt * 64 + NC * g;
+    float S[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) S[j] = 0.f;
+    if (!STATE_ONLY && owner) {
+      if (p.nseg > 1) {
+        const float4* src = reinterpret_cast<const float4*>(seg_state(p, w, w.seg, C::MB * vts, C::TILE));
+#pragma unroll
+        for (int i = 0; i < NC / 4; ++i) {
+          const float4 f = src[i * OWN + th];
+          S[4 * i] = f.x, S[4 * i + 1] = f.y, S[4 * i + 2] = f.z, S[4 * i + 3] = f.w;
+        }
+      } else if (ps.init != nullptr) {
+        const float* in = ps.init + (long long)w.bh * DK * p.DV;
+        if (ps.init_t) {
+#pragma unroll
+          for (int j = 0; j < NC; ++j) S[j] = in[(long long)(gv + j) * DK + gk];
+        } else {
+#pragma unroll
+          for (int j = 0; j < NC; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(in + (long long)gk * p.DV + gv + j);
+            S[j] = f.x, S[j + 1] = f.y, S[j + 2] = f.z, S[j + 3] = f.w;
+          }
+        }
       }
     }
-    const uint32_t set = sC + ((c - c0) % C::NT) * (3 * kBlkBytes);
+    auto publish = [&]() {
+      if (!STATE_ONLY && owner) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t in[4] = {cr[i].x, cr[i].y, cr[i].z, cr[i].w};
-      uint32_t t[3][4];
+        for (int j = 0; j < NC; j += 8) {
+          uint32_t pk[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float x0 = bf16_lo(in[k]) * wj[i], x1 = bf16_hi(in[k]) * wj[i];
-        t[0][k] = pack_bf16x2(x0, x1);
-        x0 -= bf16_lo(t[0][k]);
-        x1 -= bf16_hi(t[0][k]);
-        t[1][k] = pack_bf16x2(x0, x1);
-        x0 -= bf16_lo(t[1][k]);
-        x1 -= bf16_hi(t[1][k]);
-        t[2][k] = pack_bf16x2(x0, x1);
+          for (int k = 0; k < 4; ++k) pk[k] = pack_bf16x2(S[j + 2 * k], S[j + 2 * k + 1]);
+          sts128(sm + C::sS + blk_at(dk, (NC * g + j) / 8), pk);
+        }
+        fence_async_smem();
       }
-      const uint32_t at = set + blk_at(tid / 8 + 32 * i, tid % 8);
+      tc_fence_before();
+      warp_arrive(sP);
+    };
+    // c of chunk `it`, weighted, in three bf16 terms: rows tid / 8 + .., 16-byte chunk tid % 8
+    constexpr int ROWS = 1024 / (32 * NCW), STEP = 4 * NCW;
+    float wj[ROWS];
+    int wn = -1;
+    auto make_terms = [&](int it) {
+      const int c = c0 + it, n = len - c * kTC < kTC ? len - c * kTC : kTC;
+      if (wn != n) {
+        wn = n;
 #pragma unroll
-      for (int m = 0; m < 3; ++m)
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + m * kBlkBytes), "r"(t[m][0]),
-                     "r"(t[m][1]), "r"(t[m][2]), "r"(t[m][3])
-                     : "memory");
+        for (int i = 0; i < ROWS; ++i) {
+          const int row = tid / 8 + STEP * i, j = rev ? kTC - 1 - row : row;
+          wj[i] = j < n ? ps.upd * pw(lg, n - 1 - j + ps.shift) : 0.f;
+        }
+      }
+      if (!wait(cF + 8 * (it % C::NT), (it / C::NT) & 1)) return false;
+      const uint32_t src = sm + C::sC + (it % C::NT) * kBlkBytes;
+      const uint32_t set = sm + C::sT + (it % C::NT) * (3 * kBlkBytes);
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        const int row = tid / 8 + STEP * i;
+        const uint32_t at = blk_at(row, tid % 8);
+        uint32_t in[4], t[3][4];
+        lds128(in, src + at);
+        if ((rev ? kTC - 1 - row : row) >= n) in[0] = in[1] = in[2] = in[3] = 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float x0 = bf16_lo(in[k]) * wj[i], x1 = bf16_hi(in[k]) * wj[i];
+          t[0][k] = pack_bf16x2(x0, x1);
+          x0 -= bf16_lo(t[0][k]);
+          x1 -= bf16_hi(t[0][k]);
+          t[1][k] = pack_bf16x2(x0, x1);
+          x0 -= bf16_lo(t[1][k]);
+          x1 -= bf16_hi(t[1][k]);
+          t[2][k] = pack_bf16x2(x0, x1);
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) sts128(set + k * kBlkBytes + at, t[k]);
+      }
+      if (!rev && n < kTC && len < p.T) {
+        // a's rows behind the row's last token hold values that do not count: zeros
+        if (!wait(aF + 8 * (it & 1), (it >> 1) & 1)) return false;
+        const uint32_t z[4] = {0u, 0u, 0u, 0u};
+        for (int e = tid; e < kTC * (DKB / 8); e += 32 * NCW) {
+          const int row = e / (DKB / 8), ch = e % (DKB / 8);
+          if (row >= n) sts128(sm + C::sA + (it & 1) * C::A + (ch / 8) * kBlkBytes + blk_at(row, ch % 8), z);
+        }
+      }
+      fence_async_smem();
+      warp_arrive(tR + 8 * (it & 1));
+      return true;
+    };
+    bool ok = true;
+    if (cnt > 0) {
+      publish();
+      ok = make_terms(0);
     }
-    if (c + 1 < cend) load_c(c + 1);
-  };
-  if (c0 < cend) make_terms(c0);
-  for (int c = c0; c < cend; ++c) {
-    const int it = c - c0, n = len - c * kTC < kTC ? len - c * kTC : kTC;
-    cp_async_wait<1>();   // this chunk's a (the next one's may be on its way)
-    fence_async_smem();
-    tc_fence_before();    // (this CTA's reads of the previous sum)
-    __syncthreads();
-    if (tid == 0) {
+    for (int it = 0; ok && it < cnt; ++it) {
+      if (C::NT == 2 && it + 1 < cnt && !make_terms(it + 1)) break;
+      if (!wait(mD + 8 * (it & 1), (it >> 1) & 1)) break;
       tc_fence_after();
-      const uint32_t sA = sm + (it % C::NA) * C::A, set = sC + (it % C::NT) * (3 * kBlkBytes);
+      if (C::NT == 1 && it + 1 < cnt && !make_terms(it + 1)) break;
+      const int c = c0 + it, n = len - c * kTC < kTC ? len - c * kTC : kTC;
+      if (owner) {
+        const float wS = pw(lg, n);
+        uint32_t r[NC];
+        tmem_ld(tmem + ((uint32_t)(q * 32) << 16) + (it & 1) * 64 + NC * g, r);
+        tmem_wait_ld();
+        reg_fence(r);
 #pragma unroll
-      for (int term = 2; term >= 0; --term)
-#pragma unroll
-        for (int ks = 0; ks < kTC / 16; ++ks)
-          umma_bf16(tmem, sdesc_sw128(sA + ks * 2048, kBlkBytes, 1024),
-                    sdesc_sw128(set + term * kBlkBytes + ks * 2048, kBlkBytes, 1024), idesc,
-                    (term != 2 || ks != 0) ? 1u : 0u);
-      umma_commit(bar);
+        for (int j = 0; j < NC; ++j) S[j] = fmaf(wS, S[j], __uint_as_float(r[j]));
+      }
+      if (it + 1 < cnt) {
+        if (!wait(sF, it & 1)) break;
+        publish();
+      }
     }
-    load_a(c + 2);  // into the buffer that the previous chunk's MMAs have read
-    if (!STATE_ONLY && owner) {  // the state at this chunk's start
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.chunk_states) +
-                           ((((long long)w.job * p.B * p.NH + w.bh) * nch + c) * DK + mb * DKB + dk) * p.DV +
-                           vt * 64 + 32 * half;
-#pragma unroll
-      for (int j = 0; j < 32; j += 8)
-        *reinterpret_cast<uint4*>(dst + j) =
-            make_uint4(pack_bf16x2(S[j], S[j + 1]), pack_bf16x2(S[j + 2], S[j + 3]),
-                       pack_bf16x2(S[j + 4], S[j + 5]), pack_bf16x2(S[j + 6], S[j + 7]));
-    }
-    if (C::NT == 2 && c + 1 < cend) make_terms(c + 1);
-    const float wS = pw(lg, n);
-    if (!tc_wait(bar, it & 1, tw)) break;
-    tc_fence_after();
     if (owner) {
-      uint32_t r[32];
-      tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + 32 * half, r);
-      tmem_wait_ld();
-      tmem_reg_fence(r);
+      if (STATE_ONLY) {
+        float4* dst = reinterpret_cast<float4*>(seg_state(p, w, w.seg + 1, C::MB * vts, C::TILE));
 #pragma unroll
-      for (int j = 0; j < 32; ++j) S[j] = fmaf(wS, S[j], __uint_as_float(r[j]));
-    }
-    if (C::NT == 1 && c + 1 < cend) make_terms(c + 1);
-  }
-  cp_async_wait<0>();
-
-  if (owner) {
-    if (STATE_ONLY) {
-      float4* dst = reinterpret_cast<float4*>(seg_state(p, w, w.seg + 1, C::MB * vts, C::TILE));
+        for (int i = 0; i < NC / 4; ++i)
+          dst[i * OWN + th] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+      } else if (ps.fin != nullptr && ((len > c0 * kTC && (long long)len <= (long long)c1 * kTC) ||
+                                       (len == 0 && w.seg == 0))) {
+        float* f = ps.fin + ((long long)w.bh * DK + gk) * p.DV + gv;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        dst[i * 2 * DKB + th] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
-    } else if (ps.fin != nullptr &&
-               ((len > c0 * kTC && (long long)len <= (long long)c1 * kTC) || (len == 0 && w.seg == 0))) {
-      float* f = ps.fin + ((long long)w.bh * DK + mb * DKB + dk) * p.DV + vt * 64 + 32 * half;
-#pragma unroll
-      for (int j = 0; j < 32; j += 4)
-        *reinterpret_cast<float4*>(f + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+        for (int j = 0; j < NC; j += 4)
+          *reinterpret_cast<float4*>(f + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == NCW) {
     tc_fence_after();
-    tmem_dealloc(tmem, 64);
+    tmem_dealloc(tmem, 128);
   }
 }
 
+// --------------------------------------------------------------- outputs --
 template <int DK>
 struct OutCfg {
+  static constexpr int NCW = DK == 64 ? 8 : 16;        // compute warps
+  static constexpr int THREADS = 32 * (NCW + 1);
+  static constexpr int OCC = DK == 64 ? 2 : 1;
+  static constexpr int NG = NCW / 4, NC = 64 / NG;     // a thread: one row, NC of 64 output columns
   static constexpr uint32_t X = (DK / 64) * kBlkBytes;
   // x and a of one tile.  Scores in bf16 (32 KB) take the place of a once it has been multiplied
   // (with 64 columns of a, its 16 KB and 16 KB more).
-  static constexpr int NXA = DK <= 128 ? 2 : 1;        // tiles of x and a: the next one is loaded early
+  static constexpr int NXA = DK <= 128 ? 2 : 1;        // tiles of x and a
   static constexpr uint32_t XTRA = X < 2 * kBlkBytes ? kBlkBytes : 0;
   static constexpr uint32_t S = DK * 128;              // DK rows x 64 columns of the state
   static constexpr int NCS = DK >= 128 ? 2 : 1;        // c and state tiles of 64 columns
   // with 256 columns the second state tile lies in a's upper half, free after the scores
+  static constexpr uint32_t sXtra = NXA * 2 * X, sCS = sXtra + XTRA;
   static constexpr uint32_t CS = DK == 256 ? 2 * kBlkBytes + S : NCS * (kBlkBytes + S);
-  static constexpr uint32_t SMEM = NXA * 2 * X + XTRA + CS + 1024;
-  static constexpr int OCC = DK == 64 ? 2 : 1;
+  // outputs on their way: 32 rows x NC columns per warp; with 64 columns in x's place
+  static constexpr uint32_t sO = sCS + CS;
+  static constexpr uint32_t STG = 32 * NC * 2;
+  static constexpr uint32_t SMEM = sO + (DK == 64 ? 0 : NCW * STG) + 1024;
   static constexpr int NO = OCC == 1 ? 2 : 1;          // sums (P c and x S) in TMEM
   static constexpr uint32_t TMEM = OCC == 1 ? 512 : 256;
+  static __device__ __forceinline__ uint32_t s_at(int buf) {
+    return DK == 256 && buf == 1 ? X + 2 * kBlkBytes : sCS + buf * (kBlkBytes + S);
+  }
+  static __device__ __forceinline__ uint32_t c_at(int buf) {
+    return buf == 0 ? sCS + S : (DK == 256 ? sCS + S + kBlkBytes : sCS + 2 * S + kBlkBytes);
+  }
 };
 
 // A persistent CTA walks (row, head, chunk, pass) tiles, the passes of a chunk side by
 // side on the grid, since they read the same tokens.
 template <int DK>
-__global__ void __launch_bounds__(kTT, OutCfg<DK>::OCC)
-    linattn_outputs_kernel(const __grid_constant__ LinAttnParams p, int tiles) {
+__global__ void __launch_bounds__(OutCfg<DK>::THREADS, OutCfg<DK>::OCC)
+    linattn_outputs_kernel(const __grid_constant__ LinAttnParams p, const __grid_constant__ TcMaps m,
+                           int tiles) {
   using C = OutCfg<DK>;
+  constexpr int NCW = C::NCW, NG = C::NG, NC = C::NC;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int abort_flag_s;
   __shared__ uint32_t tslot_s;
-  __shared__ __align__(8) uint64_t bar_s;
-  __shared__ float pows[kTC];  // intra lambda^m
+  __shared__ __align__(8) uint64_t bars_s[14];
+  __shared__ float pows[2][kTC];  // intra lambda^m, of this tile and of the one before
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sXtra = sm + C::NXA * 2 * C::X, sCS = sXtra + C::XTRA;
-  const uint32_t bar = smem_u32(&bar_s);
+  const uint32_t bar = smem_u32(bars_s);
+  // x and a loaded; c and state loaded; scores done; scores written (and read from TMEM);
+  // sums done; sums read; staging in x read; c's rows behind the last token zeroed
+  const uint32_t xF = bar, cF = bar + 16, sc = bar + 32, pW = bar + 40, oD = bar + 48, oR = bar + 64,
+                 xR = bar + 80, cZ = bar + 88;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int q = warp & 3, half = warp >> 2, row = 32 * q + lane;
   const int nch = (p.T + kTC - 1) / kTC;
   const int vts = p.DV / 64;
-  const TcWait tw{p.status, p.timeout_ns, &abort_flag_s};
+  const TcWait wait{p.status, p.timeout_ns, &abort_flag_s};
 
   struct Tile {
     int job, b, h, bh, c, len;
@@ -370,60 +493,26 @@ __global__ void __launch_bounds__(kTT, OutCfg<DK>::OCC)
     t.len = row_len(p, t.b);
     return t;
   };
-  auto load_xa = [&](const Tile& t, int buf) {
-    const LinAttnPass& ps = p.pass[t.job];
-    const uint32_t d = sm + buf * (2 * C::X);
-    const __nv_bfloat16* gx = static_cast<const __nv_bfloat16*>(ps.x) + t.b * ps.xs[1] + t.h * ps.xs[2];
-    const __nv_bfloat16* ga = static_cast<const __nv_bfloat16*>(ps.a) + t.b * ps.as[1] + t.h * ps.as[2];
-    load_rows<DK>(d, gx, ps.xs[0], t.c * kTC, t.len, ps.reverse != 0);
-    load_rows<DK>(d + C::X, ga, ps.as[0], t.c * kTC, t.len, ps.reverse != 0);
-  };
-  auto s_at = [&](int buf) {  // state tile, and c tile behind the first one
-    return DK == 256 && buf == 1 ? sm + C::X + 2 * kBlkBytes : sCS + buf * (kBlkBytes + C::S);
-  };
-  auto c_at = [&](int buf) { return buf == 0 ? sCS + C::S : (DK == 256 ? sCS + C::S + kBlkBytes : sCS + 2 * C::S + kBlkBytes); };
-  auto load_cs = [&](const Tile& t, int v, int buf) {
-    const LinAttnPass& ps = p.pass[t.job];
-    const __nv_bfloat16* gc = static_cast<const __nv_bfloat16*>(ps.c) + t.b * ps.cs[1] + t.h * ps.cs[2];
-    const __nv_bfloat16* gs = static_cast<const __nv_bfloat16*>(p.chunk_states) +
-                              (((long long)t.job * p.B * p.NH + t.bh) * nch + t.c) * DK * p.DV;
-    const uint32_t sS = s_at(buf);
-    load_rows<64>(c_at(buf), gc + 64 * v, ps.cs[0], t.c * kTC, t.len, ps.reverse != 0);
-#pragma unroll
-    for (int i = 0; i < DK * 8 / kTT; ++i) {
-      const int e = tid + i * kTT, k = e / 8, ch = e % 8;
-      zfill16(sS + (uint32_t)(k * 128 + ((ch ^ (k & 7)) << 4)), gs + (long long)k * p.DV + 64 * v + ch * 8, true);
-    }
-  };
-  // the first tile at or after idx that holds tokens; the others get their zeros here
-  auto next_tile = [&](int idx, Tile& t) {
-    for (; idx < tiles; idx += gridDim.x) {
-      t = tile_of(idx);
-      if (t.len > t.c * kTC) break;
-      const LinAttnPass& ps = p.pass[t.job];
-      const int r = t.c * kTC + row;
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(ps.out) + t.b * ps.os[1] + t.h * ps.os[2] +
-                         (long long)r * ps.os[0] + 32 * half;
-      if (r < p.T)
-        for (int v = 0; v < vts; ++v)
-#pragma unroll
-          for (int j = 0; j < 32; j += 8)
-            *reinterpret_cast<uint4*>(o + 64 * v + j) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    return idx;
+  // first token of a tile's rows; whether rows of c have to be zeroed
+  auto token_of = [&](const Tile& t) { return p.pass[t.job].reverse ? t.len - (t.c + 1) * kTC : t.c * kTC; };
+  auto ragged = [&](const Tile& t) {
+    return !p.pass[t.job].reverse && t.len < p.T && t.len < (t.c + 1) * kTC;
   };
 
-  Tile t, tn;
-  int idx = next_tile(blockIdx.x, t);
-  if (idx >= tiles) return;
-  load_xa(t, 0);
-  cp_async_commit();
   if (tid == 0) {
-    mbar_init(bar, 1);
+    for (int i = 0; i < 5; ++i) mbar_init(bar + 8 * i, 1);
+    mbar_init(pW, NCW);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(oD + 8 * i, 1);
+      mbar_init(oR + 8 * i, NCW);
+    }
+    mbar_init(xR, NCW);
+    mbar_init(cZ, NCW);
     abort_flag_s = 0;
     fence_mbar_init();
+    fence_async_smem();
   }
-  if (warp == 0) {
+  if (warp == NCW) {
     tmem_alloc(smem_u32(&tslot_s), C::TMEM);
     tmem_relinquish();
   }
@@ -431,202 +520,379 @@ __global__ void __launch_bounds__(kTT, OutCfg<DK>::OCC)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tslot_s;
-  const uint32_t mylanes = (uint32_t)(q * 32) << 16;
-  uint32_t phase = 0;
-  constexpr int kNext = C::NXA == 2 ? 1 : 0, kPre = C::NCS == 2 ? 1 : 0;  // copy groups behind the one awaited
-  bool ok = true;
-  for (int k = 0; ok && idx < tiles; ++k) {
-    const int buf = C::NXA == 2 ? (k & 1) : 0;
-    const uint32_t sX = sm + buf * (2 * C::X), sA = sX + C::X;
-    const LinAttnPass& ps = p.pass[t.job];
-    const int r0 = t.c * kTC, n = t.len - r0 < kTC ? t.len - r0 : kTC;
-    const float lg = p.log_decay[t.h] * 1.4426950408889634f;
-    load_cs(t, 0, 0);
-    cp_async_commit();
-    const int nidx = next_tile(idx + gridDim.x, tn);
-    if (C::NXA == 2) {
-      if (nidx < tiles) load_xa(tn, buf ^ 1);
-      cp_async_commit();
-    }
-    if (tid < kTC) pows[tid] = ps.intra * pw(lg, tid);
-    const float fr = ps.inter * pw(lg, row + 1 - ps.shift);
-    cp_async_wait<1 + kNext>();
-    fence_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    if (tid == 0) {  // scores
-      tc_fence_after();
-      constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
-#pragma unroll
-      for (int ks = 0; ks < DK / 16; ++ks) {
-        const uint32_t o = (uint32_t)(ks / 4) * kBlkBytes + (ks % 4) * 32;
-        umma_bf16(tmem, sdesc_sw128(sX + o, 16, 1024), sdesc_sw128(sA + o, 16, 1024), idesc, ks != 0);
-      }
-      umma_commit(bar);
-    }
-    if (!tc_wait(bar, phase, tw)) break;
-    phase ^= 1;
-    tc_fence_after();
-    // decay and mask; 32-column blocks `half` and `half + 2` of this thread's row
-#pragma unroll
-    for (int jb = 0; jb < 2; ++jb) {
-      const int blk = half + 2 * jb;  // columns 32 blk ..
-      uint32_t pk[16];
-      if (blk <= q) {
-        uint32_t s[32];
-        tmem_ld32(tmem + mylanes + 32 * blk, s);
-        tmem_wait_ld();
-        tmem_reg_fence(s);
-        const float* pm = pows + (row - 32 * blk);
-        float v[32];
-        if (blk < q) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(s[j]) * pm[-j];
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = j <= lane ? __uint_as_float(s[j]) * pm[-min(j, lane)] : 0.f;
+
+  if (warp == NCW) {
+    // ---------------------------------------------------------- control --
+    if (lane == 0) {
+      auto next_tile = [&](int idx, Tile& t) {
+        for (; idx < tiles; idx += gridDim.x) {
+          t = tile_of(idx);
+          if (t.len > t.c * kTC) break;
         }
+        return idx;
+      };
+      uint32_t nx[2] = {0, 0}, ncs[2] = {0, 0};  // copies issued per buffer
+      uint32_t ux[2] = {0, 0}, ucs[2] = {0, 0};  // and waited for
+      auto load_xa = [&](const Tile& t, int buf) {
+        const uint32_t d = sm + buf * (2 * C::X), f = xF + 8 * buf;
+        const int j = t.job, tok = token_of(t);
+        mbar_arrive_expect_tx(f, 2 * C::X);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) pk[j] = 0u;
-      }
-      // block 0 (columns 0 .. 63) in a's place, block 1 behind it or in the extra space
-      const uint32_t d = jb == 0 || C::XTRA == 0 ? sA + blk_at(row, 4 * blk) : sXtra + blk_at(row, 4 * (blk - 2));
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
-                         (d & ~127u) | (((d & 127u) ^ (uint32_t)(i << 4)))),
-                     "r"(pk[4 * i]), "r"(pk[4 * i + 1]), "r"(pk[4 * i + 2]), "r"(pk[4 * i + 3])
-                     : "memory");
-    }
-    __nv_bfloat16* orow =
-        static_cast<__nv_bfloat16*>(ps.out) + t.b * ps.os[1] + t.h * ps.os[2] +
-        (long long)(row < n && ps.reverse ? t.len - 1 - r0 - row : r0 + row) * ps.os[0] + 32 * half;
-    // 64 columns at a time: the MMAs of one tile run during the epilogue of the one before
-    for (int v = 0; v <= vts; ++v) {
-      if (v > 0) {
-        if (!tc_wait(bar, phase, tw)) {
-          ok = false;
-          break;
+        for (int k = 0; k < DK / 64; ++k) {
+          tma_load_4d(d + k * kBlkBytes, &m.x[j], 64 * k, t.h * m.xh[j], t.b * m.xb[j], tok, f);
+          tma_load_4d(d + C::X + k * kBlkBytes, &m.a[j], 64 * k, t.h * m.ah[j], t.b * m.ab[j], tok, f);
         }
-        phase ^= 1;
-        tc_fence_after();
+        ++nx[buf];
+      };
+      auto load_cs = [&](const Tile& t, int v, int buf) {
+        const uint32_t f = cF + 8 * buf;
+        const int j = t.job;
+        mbar_arrive_expect_tx(f, kBlkBytes + C::S);
+        tma_load_4d(sm + C::c_at(buf), &m.c[j], 64 * v, t.h * m.ch[j], t.b * m.cb[j], token_of(t), f);
+        tma_load_2d(sm + C::s_at(buf), &m.s_load, 64 * v, ((j * p.B * p.NH + t.bh) * nch + t.c) * DK, f);
+        ++ncs[buf];
+      };
+      auto scores = [&](int buf) {
+        constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
+        const uint32_t x = sm + buf * (2 * C::X), a = x + C::X;
+#pragma unroll
+        for (int ks = 0; ks < DK / 16; ++ks) {
+          const uint32_t o = (uint32_t)(ks / 4) * kBlkBytes + (ks % 4) * 32;
+          umma_bf16(tmem, sdesc_sw128(x + o, 16, 1024), sdesc_sw128(a + o, 16, 1024), idesc, ks != 0);
+        }
+        umma_commit(sc);
+      };
+      uint32_t used[2] = {0, 0}, ret[2] = {0, 0};  // sums per TMEM set: issued, waited for
+      uint32_t nz = 0;                             // c tiles with rows zeroed
+      Tile t, tn, tnn;
+      int idx = next_tile(blockIdx.x, t), nidx = tiles;
+      bool ok = true;
+      if (idx < tiles) {
+        load_xa(t, 0);
+        load_cs(t, 0, 0);
+        nidx = next_tile(idx + gridDim.x, tn);
+        if (C::NXA == 2 && nidx < tiles) load_xa(tn, 1);
+        ok = wait(xF, 0);
+        if (ok) {
+          ++ux[0];
+          tc_fence_after();
+          scores(0);
+        }
       }
-      if (v < vts) {
-        if (C::NCS == 2) {
-          if (v + 1 < vts) load_cs(t, v + 1, (v + 1) & 1);
-          cp_async_commit();
-          if (v == 0) cp_async_wait<kNext + kPre>();
-          else cp_async_wait<kPre>();
-        } else {
-          if (v > 0) {
-            load_cs(t, v, 0);
-            cp_async_commit();
-            cp_async_wait<0>();
-          } else {
-            cp_async_wait<kNext>();
+      for (int k = 0; ok && idx < tiles; ++k) {
+        const int buf = C::NXA == 2 ? (k & 1) : 0;
+        const uint32_t x = sm + buf * (2 * C::X), a = x + C::X;
+        const bool zeroed = ragged(t);
+        for (int v = 0; ok && v < vts; ++v) {
+          const int cb = C::NCS == 2 ? (v & 1) : 0, o = C::NO == 2 ? (v & 1) : 0;
+          if (C::NCS == 2 && v + 1 < vts) {
+            // its buffers: read by the MMAs of v - 1; with 256 columns a's upper half (scores done)
+            if (v > 0) {
+              if (!(ok = wait(oD + 8 * (o ^ 1), ret[o ^ 1] & 1))) break;
+              ++ret[o ^ 1];
+            } else if (DK == 256) {
+              if (!(ok = wait(sc, k & 1))) break;
+            }
+            load_cs(t, v + 1, cb ^ 1);
           }
-        }
-        fence_async_smem();
-        tc_fence_before();  // (reads of the sums that these MMAs overwrite)
-        __syncthreads();
-        if (tid == 0) {
+          if (!(ok = wait(cF + 8 * cb, ucs[cb] & 1))) break;
+          ++ucs[cb];
+          if (used[o] > 0 && !(ok = wait(oR + 8 * o, (used[o] - 1) & 1))) break;
           tc_fence_after();
           constexpr uint32_t idesc = idesc_bf16_f32(128, 64, false, true);
-          const uint32_t tO = tmem + 128 + (v % C::NO) * 128, cb = C::NCS == 2 ? (v & 1) : 0;
-          const uint32_t sS = s_at(cb), sC = c_at(cb);
+          const uint32_t tO = tmem + 128 + o * 128, s = sm + C::s_at(cb), cc = sm + C::c_at(cb);
 #pragma unroll
           for (int ks = 0; ks < DK / 16; ++ks)
-            umma_bf16(tO + 64, sdesc_sw128(sX + (uint32_t)(ks / 4) * kBlkBytes + (ks % 4) * 32, 16, 1024),
-                      sdesc_sw128(sS + ks * 2048, kBlkBytes, 1024), idesc, ks != 0);
+            umma_bf16(tO + 64, sdesc_sw128(x + (uint32_t)(ks / 4) * kBlkBytes + (ks % 4) * 32, 16, 1024),
+                      sdesc_sw128(s + ks * 2048, kBlkBytes, 1024), idesc, ks != 0);
+          if (v == 0 && !(ok = wait(pW, k & 1))) break;
+          if (zeroed && !(ok = wait(cZ, nz++ & 1))) break;
+          tc_fence_after();
 #pragma unroll
           for (int ks = 0; ks < kTC / 16; ++ks)
-            umma_bf16(tO, sdesc_sw128((ks < 4 ? sA : (C::XTRA ? sXtra : sA + kBlkBytes)) + (ks % 4) * 32, 16, 1024),
-                      sdesc_sw128(sC + ks * 2048, kBlkBytes, 1024), idesc, ks != 0);
-          umma_commit(bar);
-        }
-      } else if (C::NXA == 1) {  // x and a have been multiplied for the last time
-        if (nidx < tiles) load_xa(tn, 0);
-        cp_async_commit();
-      }
-      const int e = v - (C::NO == 2 ? 1 : 0);  // columns whose sums are complete
-      if (C::NO == 1 && v < vts) {
-        if (!tc_wait(bar, phase, tw)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-      }
-      if (e < 0 || e >= vts) continue;
-      const uint32_t tO = tmem + 128 + (e % C::NO) * 128 + mylanes + 32 * half;
-      uint32_t o[32], s[32];
-      tmem_ld32(tO, o);
-      tmem_ld32(tO + 64, s);
-      tmem_wait_ld();
-      tmem_reg_fence(o);
-      tmem_reg_fence(s);
-      if (r0 + row < p.T) {
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          uint32_t pk[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int x = j + 2 * i;
-            pk[i] = row < n ? pack_bf16x2(fmaf(fr, __uint_as_float(s[x]), __uint_as_float(o[x])),
-                                          fmaf(fr, __uint_as_float(s[x + 1]), __uint_as_float(o[x + 1])))
-                            : 0u;
+            umma_bf16(tO,
+                      sdesc_sw128((ks < 4 ? a : (C::XTRA ? sm + C::sXtra : a + kBlkBytes)) + (ks % 4) * 32, 16, 1024),
+                      sdesc_sw128(cc + ks * 2048, kBlkBytes, 1024), idesc, ks != 0);
+          umma_commit(oD + 8 * o);
+          ++used[o];
+          if (C::NCS == 1 && v + 1 < vts) {  // the one buffer, once these MMAs have read it
+            if (!(ok = wait(oD, ret[0] & 1))) break;
+            ++ret[0];
+            load_cs(t, v + 1, 0);
           }
-          *reinterpret_cast<uint4*>(orow + 64 * e + j) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+        if (!ok) break;
+        if (C::NXA == 2 && nidx < tiles) {  // the next scores, behind these MMAs
+          const int nb = buf ^ 1;
+          if (!(ok = wait(xF + 8 * nb, ux[nb] & 1))) break;
+          ++ux[nb];
+          tc_fence_after();
+          scores(nb);
+        }
+        // every buffer of this tile has been read
+        for (int o = 0; ok && o < C::NO; ++o)
+          while (ok && ret[o] < used[o]) {
+            ok = wait(oD + 8 * o, ret[o] & 1);
+            ++ret[o];
+          }
+        if (!ok) break;
+        if (nidx < tiles) {
+          load_cs(tn, 0, 0);
+          const int nn = next_tile(nidx + gridDim.x, tnn);
+          if (C::NXA == 2) {
+            if (DK == 64 && !(ok = wait(xR, k & 1))) break;  // outputs in x's place have left
+            if (nn < tiles) load_xa(tnn, buf);
+          } else {
+            load_xa(tn, 0);
+            if (!(ok = wait(xF, ux[0] & 1))) break;
+            ++ux[0];
+            tc_fence_after();
+            scores(0);
+          }
+          t = tn;
+          tn = tnn;
+          idx = nidx;
+          nidx = nn;
+        } else {
+          idx = tiles;
         }
       }
+      if (!ok)
+        for (int i = 0; i < 2; ++i) {
+          if (nx[i]) drain(xF + 8 * i, (nx[i] - 1) & 1);
+          if (ncs[i]) drain(cF + 8 * i, (ncs[i] - 1) & 1);
+        }
     }
-    t = tn;
-    idx = nidx;
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- compute --
+    const int q = warp & 3, g = warp >> 2, row = 32 * q + lane;
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    uint32_t used[2] = {0, 0};
+    bool ok = true;
+    int k = 0;
+    for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
+      const Tile t = tile_of(idx);
+      const LinAttnPass& ps = p.pass[t.job];
+      const int r0 = t.c * kTC, n = t.len - r0 < kTC ? t.len - r0 : kTC;
+      const bool rev = ps.reverse != 0;
+      __nv_bfloat16* go = static_cast<__nv_bfloat16*>(ps.out) + t.b * ps.os[1] + t.h * ps.os[2] + NC * g;
+      // tokens of this chunk that do not count (reversed, the chunk's own rows are others)
+      if (row >= n && r0 + row < p.T && (rev || n <= 0)) {
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        for (int v = 0; v < vts; ++v)
+#pragma unroll
+          for (int j = 0; j < NC; j += 8)
+            *reinterpret_cast<uint4*>(go + (long long)(r0 + row) * ps.os[0] + 64 * v + j) = z;
+      }
+      if (n <= 0) continue;
+      const int buf = C::NXA == 2 ? (k & 1) : 0;
+      const uint32_t sX = sm + buf * (2 * C::X), sP = sX + C::X;
+      const float lg = p.log_decay[t.h] * 1.4426950408889634f;
+      float* pow_t = pows[k & 1];
+      if (tid < kTC) pow_t[tid] = ps.intra * pw(lg, tid);
+      bar_sync(1, 32 * NCW);
+      const float fr = ps.inter * pw(lg, (rev ? kTC - 1 - row : row) + 1 - ps.shift);
+      if (!wait(sc, k & 1)) break;
+      tc_fence_after();
+      // decay and mask of this thread's row of scores, 32 columns at a time
+#pragma unroll
+      for (int blk = g; blk < 4; blk += NG) {
+        uint32_t pk[16];
+        if (rev ? blk >= q : blk <= q) {
+          uint32_t s[32];
+          tmem_ld32(tmem + lanes + 32 * blk, s);
+          tmem_wait_ld();
+          tmem_reg_fence(s);
+          const int d = row - 32 * blk;  // row - column 0 of the block
+          float v[32];
+          if (blk != q) {
+            if (!rev) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(s[j]) * pow_t[d - j];
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(s[j]) * pow_t[j - d];
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int e = rev ? j - lane : lane - j;
+              v[j] = e >= 0 ? __uint_as_float(s[j]) * pow_t[e >= 0 ? e : 0] : 0.f;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk[j] = 0u;
+        }
+        // columns 0 .. 63 in a's place, the others behind them or in the extra space
+        const uint32_t b = blk < 2 ? sP : (C::XTRA ? sm + C::sXtra : sP + kBlkBytes);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sts128(b + blk_at(row, 4 * (blk & 1) + i), pk + 4 * i);
+      }
+      fence_async_smem();
+      tc_fence_before();
+      warp_arrive(pW);
+      const int tok = token_of(t) + 32 * q;  // of this warp's first row
+      const bool zero_c = ragged(t);
+      for (int v = 0; v < vts; ++v) {
+        const int cb = C::NCS == 2 ? (v & 1) : 0, o = C::NO == 2 ? (v & 1) : 0;
+        if (zero_c) {
+          // the buffer's uses so far: all tiles before this one, and this one's
+          const uint32_t uses = C::NCS == 2 ? (uint32_t)k * ((vts + 1 - cb) / 2) + v / 2 : (uint32_t)k * vts + v;
+          if (!(ok = wait(cF + 8 * cb, uses & 1))) break;
+          const uint32_t z[4] = {0u, 0u, 0u, 0u};
+          for (int e = tid; e < kTC * 8; e += 32 * NCW)
+            if (e / 8 >= n) sts128(sm + C::c_at(cb) + blk_at(e / 8, e % 8), z);
+          fence_async_smem();
+          warp_arrive(cZ);
+        }
+        if (!(ok = wait(oD + 8 * o, used[o] & 1))) break;
+        ++used[o];
+        tc_fence_after();
+        uint32_t u[NC], s[NC];
+        const uint32_t tO = tmem + 128 + o * 128 + lanes + NC * g;
+        tmem_ld(tO, u);
+        tmem_ld(tO + 64, s);
+        tmem_wait_ld();
+        reg_fence(u);
+        reg_fence(s);
+        tc_fence_before();
+        warp_arrive(oR + 8 * o);
+        uint32_t pk[NC / 2];
+        const bool counts = rev ? row >= kTC - n : row < n;
+#pragma unroll
+        for (int j = 0; j < NC / 2; ++j)
+          pk[j] = counts ? pack_bf16x2(fmaf(fr, __uint_as_float(s[2 * j]), __uint_as_float(u[2 * j])),
+                                       fmaf(fr, __uint_as_float(s[2 * j + 1]), __uint_as_float(u[2 * j + 1])))
+                         : 0u;
+        // with 64 columns x's place is free behind the last columns' MMAs only
+        if (tok >= 0 && (DK != 64 || v == vts - 1)) {
+          const uint32_t stg = (DK == 64 ? sX : sm + C::sO) + warp * C::STG;
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+          // 32 rows of 64 (32) bytes, 64- (32-) byte swizzle
+#pragma unroll
+          for (int j = 0; j < NC / 8; ++j)
+            sts128(stg + lane * (NC * 2) + ((j ^ (NC == 32 ? (lane >> 1) & 3 : (lane >> 2) & 1)) << 4), pk + 4 * j);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_4d(&m.out[t.job], 64 * v + NC * g, t.h, t.b, tok, stg);
+            bulk_commit();
+          }
+        } else if (tok + lane >= 0 && tok + lane < p.T) {
+#pragma unroll
+          for (int j = 0; j < NC; j += 8)
+            *reinterpret_cast<uint4*>(go + (long long)(tok + lane) * ps.os[0] + 64 * v + j) =
+                make_uint4(pk[j / 2], pk[j / 2 + 1], pk[j / 2 + 2], pk[j / 2 + 3]);
+        }
+      }
+      if (!ok) break;
+      if (DK == 64) {
+        if (lane == 0) bulk_wait_read_all();
+        warp_arrive(xR);
+      }
+      ++k;
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
-  cp_async_wait<0>();
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == NCW) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM);
   }
 }
 
+}  // namespace
+
+// ------------------------------------------------------------- host side --
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();  // tc_gemm.cu
+
+namespace {
+
+bool encode(CUtensorMap* map, const void* ptr, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return fn != nullptr &&
+         fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides,
+            box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [T, B, NH, D] with strides s (token, row, head; elements): box of 64 (cols) x rows tokens.
+// An operand shared by all heads or rows (stride 0) has one in its map; *uh, *ub
+// then are 0, the factor of the head's and row's coordinate.
+bool encode_operand(CUtensorMap* map, const void* ptr, const long long (&s)[3], const LinAttnParams& p,
+                    int D, uint32_t cols, uint32_t rows, CUtensorMapSwizzle swizzle, int* uh, int* ub) {
+  const int nh = s[2] == 0 ? 1 : p.NH, nb = s[1] == 0 ? 1 : p.B;
+  if (uh) *uh = s[2] != 0, *ub = s[1] != 0;
+  if (s[0] == 0 && p.T > 1) return false;
+  auto bytes = [&](long long e) { return (cuuint64_t)(e == 0 ? D * 2 : e * 2); };
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)nh, (cuuint64_t)nb, (cuuint64_t)p.T};
+  const cuuint64_t strides[3] = {bytes(s[2]), bytes(s[1]), bytes(s[0])};
+  const cuuint32_t box[4] = {cols, 1, 1, rows};
+  return encode(map, ptr, 4, dims, strides, box, swizzle);
+}
+
 template <int DK>
 int launch_dk(const LinAttnParams& p, cudaStream_t s) {
   using C = StCfg<DK>;
+  using O = OutCfg<DK>;
   static int prep_main[64][5], prep_state[64][5], prep_out[64][5];
-  int e = prepare_launch(prep_main, linattn_states_kernel<DK, false>, C::SMEM, kTT, 1);
+  int e = prepare_launch(prep_main, linattn_states_kernel<DK, false>, C::SMEM, C::THREADS, 1);
   if (e != 0) return e;
-  e = prepare_launch(prep_out, linattn_outputs_kernel<DK>, OutCfg<DK>::SMEM, kTT, 1);
+  e = prepare_launch(prep_out, linattn_outputs_kernel<DK>, O::SMEM, O::THREADS, 1);
   if (e != 0) return e;
   const long long nch = ((long long)p.T + kTC - 1) / kTC;
   const long long base = (long long)p.npass * p.B * p.NH * C::MB * (p.DV / 64);
   const long long outs = (long long)p.npass * p.B * p.NH * nch;
-  if (base * p.nseg * (C::TILE / 256) > 0x7fffffffLL || outs > 0x3fffffffLL)
-    return (int)cudaErrorInvalidValue;
+  if (base * p.nseg * (C::TILE / 256) > 0x7fffffffLL || outs * DK > 0x3fffffffLL) return kLinAttnTooWide;
+  TcMaps m;
+  bool ok = true;
+  for (int j = 0; j < p.npass; ++j) {
+    const LinAttnPass& ps = p.pass[j];
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    ok = ok && encode_operand(&m.x[j], ps.x, ps.xs, p, DK, 64, kTC, sw, &m.xh[j], &m.xb[j]);
+    ok = ok && encode_operand(&m.a[j], ps.a, ps.as, p, DK, 64, kTC, sw, &m.ah[j], &m.ab[j]);
+    ok = ok && encode_operand(&m.c[j], ps.c, ps.cs, p, p.DV, 64, kTC, sw, &m.ch[j], &m.cb[j]);
+    ok = ok && encode_operand(&m.out[j], ps.out, ps.os, p, p.DV, O::NC, 32,
+                              O::NC == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B, nullptr,
+                              nullptr);
+  }
+  const cuuint64_t dims[2] = {(cuuint64_t)p.DV, (cuuint64_t)(outs * DK)};
+  const cuuint64_t strides[1] = {(cuuint64_t)p.DV * 2};
+  const cuuint32_t in[2] = {64, (cuuint32_t)DK}, out[2] = {64, (cuuint32_t)C::DKB};
+  ok = ok && encode(&m.s_load, p.chunk_states, 2, dims, strides, in, CU_TENSOR_MAP_SWIZZLE_128B);
+  ok = ok && encode(&m.s_store, p.chunk_states, 2, dims, strides, out, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!ok) return kLinAttnTooWide;
+  if (cudaMemsetAsync(p.status, 0, sizeof(int), s) != cudaSuccess) return (int)cudaErrorUnknown;
   if (p.nseg > 1) {
-    e = prepare_launch(prep_state, linattn_states_kernel<DK, true>, C::SMEM, kTT, 1);
+    e = prepare_launch(prep_state, linattn_states_kernel<DK, true>, C::SMEM, C::THREADS, 1);
     if (e != 0) return e;
-    linattn_states_kernel<DK, true><<<(unsigned)(base * (p.nseg - 1)), kTT, C::SMEM, s>>>(p);
+    linattn_states_kernel<DK, true><<<(unsigned)(base * (p.nseg - 1)), C::THREADS, C::SMEM, s>>>(p, m);
     linattn_scan_kernel<TcOrder<DK>>
         <<<(unsigned)(base * (C::TILE / 256)), 256, 0, s>>>(p, p.seg_chunks * kTC);
   }
-  linattn_states_kernel<DK, false><<<(unsigned)(base * p.nseg), kTT, C::SMEM, s>>>(p);
-  if (outs > 0) {
-    const long long cap = (long long)sm_count() * OutCfg<DK>::OCC;
-    linattn_outputs_kernel<DK>
-        <<<(unsigned)(outs < cap ? outs : cap), kTT, OutCfg<DK>::SMEM, s>>>(p, (int)outs);
-  }
+  linattn_states_kernel<DK, false><<<(unsigned)(base * p.nseg), C::THREADS, C::SMEM, s>>>(p, m);
+  const long long cap = (long long)sm_count() * O::OCC;
+  linattn_outputs_kernel<DK>
+      <<<(unsigned)(outs < cap ? outs : cap), O::THREADS, O::SMEM, s>>>(p, m, (int)outs);
   return (int)cudaGetLastError();
 }
 
 }  // namespace
 
 int launch_linattn_tc(const LinAttnParams& p, cudaStream_t s) {
-  if (cudaMemsetAsync(p.status, 0, sizeof(int), s) != cudaSuccess) return (int)cudaErrorUnknown;
   switch (p.DK) {
     case 64: return launch_dk<64>(p, s);
     case 128: return launch_dk<128>(p, s);

@@ -97,6 +97,8 @@ struct LinAttnPlan {
 };
 LinAttnPlan linattn_plan(bool bf16, int npass, int T, int B, int NH, int DK, int DV);
 int launch_linattn_mma(const LinAttnParams& p, cudaStream_t s);
+// kLinAttnTooWide: the operands' strides or the sizes have no tensor map
+constexpr int kLinAttnTooWide = -2;
 int launch_linattn_tc(const LinAttnParams& p, cudaStream_t s);
 int launch_linattn_f32(const LinAttnParams& p, cudaStream_t s);
 

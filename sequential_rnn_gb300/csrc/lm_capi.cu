@@ -75,7 +75,13 @@ int run_passes(LinAttnParams& p, bool bf16, int DK, int DV, void* workspace, cud
   p.chunk_states = ws + align_up(pl.seg_bytes, 256);
   p.status = static_cast<int*>(workspace);
   p.timeout_ns = kTimeoutNs;
-  if (pl.path == kLinAttnTc) return launch_linattn_tc(p, s);
+  if (pl.path == kLinAttnTc) {
+    const int e = launch_linattn_tc(p, s);
+    if (e != kLinAttnTooWide) return e;
+    p.nseg = 1;  // the other kernels, with the token axis in one piece: no workspace
+    p.seg_chunks = p.T / 64 + 1;
+    return launch_linattn_mma(p, s);
+  }
   return pl.path == kLinAttnMma ? launch_linattn_mma(p, s) : launch_linattn_f32(p, s);
 }
 
