@@ -12,8 +12,8 @@
 //
 // The states' CTA holds 128 (or 64) x 64 of S in fp32 registers.  c times its weight is split into
 // three bf16 terms (24 bits), so that the state does not lose to operand rounding what fp32
-// keeps; the three products of a chunk accumulate from zero, smallest first, in TMEM, and the
-// sum joins the decayed state in round-to-nearest.
+// keeps; a chunk's products with the three accumulate from zero in TMEM, and their
+// sum, smallest first, joins the decayed state in round-to-nearest.
 //
 // Both kernels have one control warp (one lane: TMA loads, MMA issue, buffer bookkeeping)
 // and 8 or 16 compute warps (terms of c, decay and mask of the scores, state and
@@ -80,14 +80,6 @@ __device__ __forceinline__ void sts128(uint32_t at, const uint32_t* v) {
 __device__ __forceinline__ uint32_t blk_at(int r, int ch) {
   return (uint32_t)(r * 128 + ((ch ^ (r & 7)) << 4));
 }
-// N consecutive TMEM columns of this warp's lanes
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[N]) {
-  if constexpr (N == 32)
-    tmem_ld32(at, r);
-  else
-    tmem_ld16(at, r);
-}
 template <int N>
 __device__ __forceinline__ void reg_fence(uint32_t (&r)[N]) {
 #pragma unroll
@@ -141,8 +133,13 @@ struct StCfg {
   static constexpr int NT = DKB == 128 ? 2 : 1;
   static constexpr uint32_t sA = 0, sC = 2 * A, sT = sC + NT * kBlkBytes;
   // (with 64 state rows the MMA's other 64 rows read the tile behind a, and are not used)
-  static constexpr uint32_t sS = sT + NT * 3 * kBlkBytes;
+  static constexpr uint32_t sS = sT + NT * 3 * kBlkBytes;  // states on their way: 32 rows x NC per warp
+  static constexpr uint32_t STG = 32 * NC * 2;
   static constexpr uint32_t SMEM = sS + DKB * 128 + 1024;
+  // the sums of the three terms, side by side (one MMA of N = 192 reads a once for all three:
+  // with three of N = 64 a chunk's MMAs took 2,000 cycles, bound by a's shared-memory reads)
+  static constexpr int ND = DKB == 128 ? 2 : 1;            // TMEM buffers
+  static constexpr uint32_t TMEM = ND == 2 ? 512 : 256;
   static constexpr int TILE = DKB * 64;
 };
 
@@ -171,9 +168,9 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
   __shared__ uint32_t tslot_s;
   __shared__ __align__(8) uint64_t bars_s[10];
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  // copies of a, of c; terms ready; MMAs done; state published; its copy out read
+  // copies of a, of c; terms ready; MMAs done; sums read
   const uint32_t bar = smem_u32(bars_s);
-  const uint32_t aF = bar, cF = bar + 16, tR = bar + 32, mD = bar + 48, sP = bar + 64, sF = bar + 72;
+  const uint32_t aF = bar, cF = bar + 16, tR = bar + 32, mD = bar + 48, sR = bar + 64;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int vts = p.DV / 64;
   const Where w = where_of(p, C::MB * vts, STATE_ONLY ? p.nseg - 1 : p.nseg);
@@ -196,15 +193,14 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
     for (int i = 0; i < 2; ++i) {
       mbar_init(tR + 8 * i, NCW);
       mbar_init(mD + 8 * i, 1);
+      mbar_init(sR + 8 * i, NCW);
     }
-    mbar_init(sP, NCW);
-    mbar_init(sF, 1);
     abort_flag_s = 0;
     fence_mbar_init();
     fence_async_smem();
   }
   if (warp == NCW) {
-    tmem_alloc(smem_u32(&tslot_s), 128);
+    tmem_alloc(smem_u32(&tslot_s), C::TMEM);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -239,44 +235,31 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
       load_a(0);
       if (C::NT == 2) load_c(1);
       load_a(1);
-      constexpr uint32_t idesc = idesc_bf16_f32(128, 64, true, true);
+      constexpr uint32_t idesc = idesc_bf16_f32(128, 192, true, true);
       int it = 0;
       for (; it < cnt; ++it) {
+        const int d = it % C::ND;
         if (!wait(tR + 8 * (it & 1), (it >> 1) & 1)) break;
         load_c(it + C::NT);  // its buffer's terms have been made
         if (!wait(aF + 8 * (it & 1), (it >> 1) & 1)) break;
+        if (it >= C::ND && !wait(sR + 8 * d, ((it - C::ND) / C::ND) & 1)) break;
         tc_fence_after();
         const uint32_t a = sm + C::sA + (it & 1) * C::A, t = sm + C::sT + (it % C::NT) * (3 * kBlkBytes);
-        const uint32_t d = tmem + (it & 1) * 64;
 #pragma unroll
-        for (int term = 2; term >= 0; --term)
-#pragma unroll
-          for (int ks = 0; ks < kTC / 16; ++ks)
-            umma_bf16(d, sdesc_sw128(a + ks * 2048, kBlkBytes, 1024),
-                      sdesc_sw128(t + term * kBlkBytes + ks * 2048, kBlkBytes, 1024), idesc,
-                      (term != 2 || ks != 0) ? 1u : 0u);
+        for (int ks = 0; ks < kTC / 16; ++ks)
+          umma_bf16(tmem + d * 192, sdesc_sw128(a + ks * 2048, kBlkBytes, 1024),
+                    sdesc_sw128(t + ks * 2048, kBlkBytes, 1024), idesc, ks != 0 ? 1u : 0u);
         umma_commit(mD + 8 * (it & 1));
         if (it >= 1) {  // the next a goes where the previous chunk's MMAs have read
           if (!wait(mD + 8 * ((it - 1) & 1), ((it - 1) >> 1) & 1)) break;
           load_a(it + 1);
         }
-        // the state at this chunk's start is in shared memory (and the sum before it was read)
-        if (!wait(sP, it & 1)) break;
-        tc_fence_after();
-        if (!STATE_ONLY) {
-          tma_store_2d(&m.s_store, vt * 64,
-                       ((w.job * p.B * p.NH + w.bh) * nch + c0 + it) * DK + mb * DKB, sm + C::sS);
-          bulk_commit();
-          bulk_wait_read_all();
-        }
-        mbar_arrive(sF);
       }
       if (it < cnt) {
         for (int k = na - 2 < 0 ? 0 : na - 2; k < na; ++k) drain(aF + 8 * (k & 1), (k >> 1) & 1);
         for (int k = nc - C::NT < 0 ? 0 : nc - C::NT; k < nc; ++k)
           drain(cF + 8 * (k % C::NT), (k / C::NT) & 1);
       }
-      if (!STATE_ONLY) bulk_wait_all();
     }
     __syncwarp();
   } else {
@@ -311,19 +294,26 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
         }
       }
     }
-    auto publish = [&]() {
-      if (!STATE_ONLY && owner) {
+    // the state at the start of chunk `it` on its way to the chunk states
+    auto publish = [&](int it) {
+      if (STATE_ONLY || !owner) return;
+      const uint32_t stg = sm + C::sS + (g * (DKB / 32) + q) * C::STG;
+      if (lane == 0) bulk_wait_read_all();
+      __syncwarp();
 #pragma unroll
-        for (int j = 0; j < NC; j += 8) {
-          uint32_t pk[4];
+      for (int j = 0; j < NC / 8; ++j) {
+        uint32_t pk[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) pk[k] = pack_bf16x2(S[j + 2 * k], S[j + 2 * k + 1]);
-          sts128(sm + C::sS + blk_at(dk, (NC * g + j) / 8), pk);
-        }
-        fence_async_smem();
+        for (int k = 0; k < 4; ++k) pk[k] = pack_bf16x2(S[8 * j + 2 * k], S[8 * j + 2 * k + 1]);
+        // 32 rows of 64 (32) bytes, 64- (32-) byte swizzle
+        sts128(stg + lane * (NC * 2) + ((j ^ (NC == 32 ? (lane >> 1) & 3 : (lane >> 2) & 1)) << 4), pk);
       }
-      tc_fence_before();
-      warp_arrive(sP);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(&m.s_store, gv, ((w.job * p.B * p.NH + w.bh) * nch + c0 + it) * DK + mb * DKB + 32 * q, stg);
+        bulk_commit();
+      }
     };
     // c of chunk `it`, weighted, in three bf16 terms: rows tid / 8 + .., 16-byte chunk tid % 8
     constexpr int ROWS = 1024 / (32 * NCW), STEP = 4 * NCW;
@@ -376,31 +366,41 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
       warp_arrive(tR + 8 * (it & 1));
       return true;
     };
-    bool ok = true;
-    if (cnt > 0) {
-      publish();
-      ok = make_terms(0);
-    }
+    bool ok = cnt == 0 || make_terms(0);
+    if (cnt > 0) publish(0);
     for (int it = 0; ok && it < cnt; ++it) {
       if (C::NT == 2 && it + 1 < cnt && !make_terms(it + 1)) break;
       if (!wait(mD + 8 * (it & 1), (it >> 1) & 1)) break;
       tc_fence_after();
-      if (C::NT == 1 && it + 1 < cnt && !make_terms(it + 1)) break;
       const int c = c0 + it, n = len - c * kTC < kTC ? len - c * kTC : kTC;
       if (owner) {
         const float wS = pw(lg, n);
-        uint32_t r[NC];
-        tmem_ld(tmem + ((uint32_t)(q * 32) << 16) + (it & 1) * 64 + NC * g, r);
-        tmem_wait_ld();
-        reg_fence(r);
+        const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (it % C::ND) * 192 + NC * g;
 #pragma unroll
-        for (int j = 0; j < NC; ++j) S[j] = fmaf(wS, S[j], __uint_as_float(r[j]));
+        for (int h = 0; h < NC; h += 16) {
+          uint32_t r0[16], r1[16], r2[16];
+          tmem_ld16(t + 128 + h, r2);
+          tmem_ld16(t + 64 + h, r1);
+          tmem_ld16(t + h, r0);
+          tmem_wait_ld();
+          reg_fence(r0);
+          reg_fence(r1);
+          reg_fence(r2);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)  // smallest first
+            S[h + j] = fmaf(wS, S[h + j],
+                            (__uint_as_float(r2[j]) + __uint_as_float(r1[j])) + __uint_as_float(r0[j]));
+        }
       }
+      tc_fence_before();
+      warp_arrive(sR + 8 * (it % C::ND));
       if (it + 1 < cnt) {
-        if (!wait(sF, it & 1)) break;
-        publish();
+        if (C::NT == 1 && !make_terms(it + 1)) break;
+        publish(it + 1);
       }
     }
+    if (!STATE_ONLY && lane == 0) bulk_wait_all();
+    __syncwarp();
     if (owner) {
       if (STATE_ONLY) {
         float4* dst = reinterpret_cast<float4*>(seg_state(p, w, w.seg + 1, C::MB * vts, C::TILE));
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
   __syncthreads();
   if (warp == NCW) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, C::TMEM);
   }
 }
 
@@ -467,7 +467,6 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, OutCfg<DK>::OCC)
   __shared__ int abort_flag_s;
   __shared__ uint32_t tslot_s;
   __shared__ __align__(8) uint64_t bars_s[14];
-  __shared__ float pows[2][kTC];  // intra lambda^m, of this tile and of the one before
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bar = smem_u32(bars_s);
   // x and a loaded; c and state loaded; scores done; scores written (and read from TMEM);
@@ -671,8 +670,15 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, OutCfg<DK>::OCC)
     uint32_t used[2] = {0, 0};
     bool ok = true;
     int k = 0;
+    Tile tn = tile_of(blockIdx.x);
+    float dn = p.log_decay[tn.h];
     for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
-      const Tile t = tile_of(idx);
+      const Tile t = tn;
+      const float lg = dn * 1.4426950408889634f;
+      if (idx + (int)gridDim.x < tiles) {  // its loads are on their way meanwhile
+        tn = tile_of(idx + gridDim.x);
+        dn = p.log_decay[tn.h];
+      }
       const LinAttnPass& ps = p.pass[t.job];
       const int r0 = t.c * kTC, n = t.len - r0 < kTC ? t.len - r0 : kTC;
       const bool rev = ps.reverse != 0;
@@ -688,49 +694,47 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, OutCfg<DK>::OCC)
       if (n <= 0) continue;
       const int buf = C::NXA == 2 ? (k & 1) : 0;
       const uint32_t sX = sm + buf * (2 * C::X), sP = sX + C::X;
-      const float lg = p.log_decay[t.h] * 1.4426950408889634f;
-      float* pow_t = pows[k & 1];
-      if (tid < kTC) pow_t[tid] = ps.intra * pw(lg, tid);
-      bar_sync(1, 32 * NCW);
+      const float lam = pw(lg, 1);
       const float fr = ps.inter * pw(lg, (rev ? kTC - 1 - row : row) + 1 - ps.shift);
       if (!wait(sc, k & 1)) break;
       tc_fence_after();
       // decay and mask of this thread's row of scores, 32 columns at a time
-#pragma unroll
       for (int blk = g; blk < 4; blk += NG) {
+        // columns 0 .. 63 in a's place, the others behind them or in the extra space
+        const uint32_t dst = blk < 2 ? sP : (C::XTRA ? sm + C::sXtra : sP + kBlkBytes);
+        const int ch = 4 * (blk & 1);
         uint32_t pk[16];
         if (rev ? blk >= q : blk <= q) {
           uint32_t s[32];
           tmem_ld32(tmem + lanes + 32 * blk, s);
+          // powers from the column nearest to the diagonal on, each lambda times the one before
+          float f = blk == q ? ps.intra : ps.intra * pw(lg, rev ? 32 * blk - row : row - 32 * blk - 31);
           tmem_wait_ld();
           tmem_reg_fence(s);
-          const int d = row - 32 * blk;  // row - column 0 of the block
-          float v[32];
-          if (blk != q) {
-            if (!rev) {
+          const int live = blk == q ? lane : (rev ? 0 : 31);  // last (reversed: first) column that counts
+          if (rev) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(s[j]) * pow_t[d - j];
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(s[j]) * pow_t[j - d];
+            for (int j = 0; j < 32; ++j) {
+              const bool on = j >= live;
+              s[j] = on ? __float_as_uint(__uint_as_float(s[j]) * f) : 0u;
+              f = on ? f * lam : f;
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int e = rev ? j - lane : lane - j;
-              v[j] = e >= 0 ? __uint_as_float(s[j]) * pow_t[e >= 0 ? e : 0] : 0.f;
+            for (int j = 31; j >= 0; --j) {
+              const bool on = j <= live;
+              s[j] = on ? __float_as_uint(__uint_as_float(s[j]) * f) : 0u;
+              f = on ? f * lam : f;
             }
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+          for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) pk[j] = 0u;
         }
-        // columns 0 .. 63 in a's place, the others behind them or in the extra space
-        const uint32_t b = blk < 2 ? sP : (C::XTRA ? sm + C::sXtra : sP + kBlkBytes);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sts128(b + blk_at(row, 4 * (blk & 1) + i), pk + 4 * i);
+        for (int i = 0; i < 4; ++i) sts128(dst + blk_at(row, ch + i), pk + 4 * i);
       }
       fence_async_smem();
       tc_fence_before();
@@ -752,22 +756,26 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, OutCfg<DK>::OCC)
         if (!(ok = wait(oD + 8 * o, used[o] & 1))) break;
         ++used[o];
         tc_fence_after();
-        uint32_t u[NC], s[NC];
-        const uint32_t tO = tmem + 128 + o * 128 + lanes + NC * g;
-        tmem_ld(tO, u);
-        tmem_ld(tO + 64, s);
-        tmem_wait_ld();
-        reg_fence(u);
-        reg_fence(s);
-        tc_fence_before();
-        warp_arrive(oR + 8 * o);
         uint32_t pk[NC / 2];
         const bool counts = rev ? row >= kTC - n : row < n;
 #pragma unroll
-        for (int j = 0; j < NC / 2; ++j)
-          pk[j] = counts ? pack_bf16x2(fmaf(fr, __uint_as_float(s[2 * j]), __uint_as_float(u[2 * j])),
-                                       fmaf(fr, __uint_as_float(s[2 * j + 1]), __uint_as_float(u[2 * j + 1])))
-                         : 0u;
+        for (int h = 0; h < NC; h += 16) {
+          uint32_t u[16], s[16];
+          const uint32_t tO = tmem + 128 + o * 128 + lanes + NC * g + h;
+          tmem_ld16(tO, u);
+          tmem_ld16(tO + 64, s);
+          tmem_wait_ld();
+          reg_fence(u);
+          reg_fence(s);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            pk[h / 2 + j] =
+                counts ? pack_bf16x2(fmaf(fr, __uint_as_float(s[2 * j]), __uint_as_float(u[2 * j])),
+                                     fmaf(fr, __uint_as_float(s[2 * j + 1]), __uint_as_float(u[2 * j + 1])))
+                       : 0u;
+        }
+        tc_fence_before();
+        warp_arrive(oR + 8 * o);
         // with 64 columns x's place is free behind the last columns' MMAs only
         if (tok >= 0 && (DK != 64 || v == vts - 1)) {
           const uint32_t stg = (DK == 64 ? sX : sm + C::sO) + warp * C::STG;
@@ -871,9 +879,10 @@ int launch_dk(const LinAttnParams& p, cudaStream_t s) {
   }
   const cuuint64_t dims[2] = {(cuuint64_t)p.DV, (cuuint64_t)(outs * DK)};
   const cuuint64_t strides[1] = {(cuuint64_t)p.DV * 2};
-  const cuuint32_t in[2] = {64, (cuuint32_t)DK}, out[2] = {64, (cuuint32_t)C::DKB};
+  const cuuint32_t in[2] = {64, (cuuint32_t)DK}, out[2] = {(cuuint32_t)C::NC, 32};
   ok = ok && encode(&m.s_load, p.chunk_states, 2, dims, strides, in, CU_TENSOR_MAP_SWIZZLE_128B);
-  ok = ok && encode(&m.s_store, p.chunk_states, 2, dims, strides, out, CU_TENSOR_MAP_SWIZZLE_128B);
+  ok = ok && encode(&m.s_store, p.chunk_states, 2, dims, strides, out,
+                    C::NC == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
   if (!ok) return kLinAttnTooWide;
   if (cudaMemsetAsync(p.status, 0, sizeof(int), s) != cudaSuccess) return (int)cudaErrorUnknown;
   if (p.nseg > 1) {
