@@ -11,7 +11,7 @@
 // bytes per 128 tokens and head, written and read once, mostly inside L2.
 //
 // The states' CTA holds 128 (or 64) x 64 of S in fp32 registers.  c times its weight is split into
-// three bf16 terms (24 bits), so that the state does not lose to operand rounding what fp32
+// three bf16 terms (by truncation: exact, all 24 bits), so that the state does not lose to operand rounding what fp32
 // keeps; a chunk's products with the three accumulate from zero in TMEM, and their
 // sum, smallest first, joins the decayed state in round-to-nearest.
 //
@@ -42,6 +42,7 @@ namespace {
 
 constexpr int kTC = 128;                  // tokens per chunk
 constexpr uint32_t kBlkBytes = kTC * 128; // 128 rows x 64 columns
+constexpr int kAhead = 4;                 // chunks fetched into L2 ahead of their use (states)
 
 // tensor maps: x, a, c, out of each pass [T, B, NH, D]; chunk states as rows of DV
 struct TcMaps {
@@ -59,6 +60,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
+}
+// the same box into L2 only
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
 }
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3,
                                              uint32_t src) {
@@ -231,10 +239,21 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
         tma_load_4d(sm + C::sC + (it % C::NT) * kBlkBytes, &m.c[w.job], vt * 64, hC, bC, token(it), f);
         ++nc;
       };
+      // shared memory holds little more than a chunk ahead: the ones after it are fetched into L2
+      // (a by the CTA of the first columns, c by the one of the first state rows)
+      auto prefetch = [&](int it) {
+        if (it >= cnt || token(it) < 0) return;
+        if (vt == 0)
+#pragma unroll
+          for (int k = 0; k < DKB / 64; ++k)
+            tma_prefetch_4d(&m.a[w.job], mb * DKB + 64 * k, hA, bA, token(it));
+        if (mb == 0) tma_prefetch_4d(&m.c[w.job], vt * 64, hC, bC, token(it));
+      };
       load_c(0);
       load_a(0);
       if (C::NT == 2) load_c(1);
       load_a(1);
+      for (int k = 2; k < kAhead; ++k) prefetch(k);
       constexpr uint32_t idesc = idesc_bf16_f32(128, 192, true, true);
       int it = 0;
       for (; it < cnt; ++it) {
@@ -250,6 +269,7 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
           umma_bf16(tmem + d * 192, sdesc_sw128(a + ks * 2048, kBlkBytes, 1024),
                     sdesc_sw128(t + ks * 2048, kBlkBytes, 1024), idesc, ks != 0 ? 1u : 0u);
         umma_commit(mD + 8 * (it & 1));
+        prefetch(it + kAhead);
         if (it >= 1) {  // the next a goes where the previous chunk's MMAs have read
           if (!wait(mD + 8 * ((it - 1) & 1), ((it - 1) >> 1) & 1)) break;
           load_a(it + 1);
@@ -342,13 +362,12 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float x0 = bf16_lo(in[k]) * wj[i], x1 = bf16_hi(in[k]) * wj[i];
-          t[0][k] = pack_bf16x2(x0, x1);
-          x0 -= bf16_lo(t[0][k]);
-          x1 -= bf16_hi(t[0][k]);
-          t[1][k] = pack_bf16x2(x0, x1);
-          x0 -= bf16_lo(t[1][k]);
-          x1 -= bf16_hi(t[1][k]);
-          t[2][k] = pack_bf16x2(x0, x1);
+#pragma unroll
+          for (int e = 0; e < 3; ++e) {  // the leading 8 bits of the significand, three times
+            t[e][k] = __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632);
+            x0 -= __uint_as_float(__float_as_uint(x0) & 0xffff0000u);
+            x1 -= __uint_as_float(__float_as_uint(x1) & 0xffff0000u);
+          }
         }
 #pragma unroll
         for (int k = 0; k < 3; ++k) sts128(set + k * kBlkBytes + at, t[k]);
@@ -478,19 +497,30 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, OutCfg<DK>::OCC)
   const int vts = p.DV / 64;
   const TcWait wait{p.status, p.timeout_ns, &abort_flag_s};
 
+  // tiles in the order pass, chunk, head, row (fastest first); a step of the grid is added digit by
+  // digit (the divisions of a place cost 700 cycles a tile)
   struct Tile {
-    int job, b, h, bh, c, len;
+    int job, c, h, b, len;
   };
-  auto tile_of = [&](int idx) {
+  auto digits = [&](int idx) {
     Tile t;
     t.job = idx % p.npass;
     idx /= p.npass;
     t.c = idx % nch;
-    t.bh = idx / nch;
-    t.b = t.bh / p.NH;
-    t.h = t.bh % p.NH;
-    t.len = row_len(p, t.b);
+    idx /= nch;
+    t.h = idx % p.NH;
+    t.b = idx / p.NH;
     return t;
+  };
+  const Tile stride = digits((int)gridDim.x);
+  auto advance = [&](Tile& t) {  // (past the last tile b is past the last row: not to be read)
+    t.job += stride.job;
+    t.c += stride.c;
+    t.h += stride.h;
+    t.b += stride.b;
+    if (t.job >= p.npass) t.job -= p.npass, ++t.c;
+    if (t.c >= nch) t.c -= nch, ++t.h;
+    if (t.h >= p.NH) t.h -= p.NH, ++t.b;
   };
   // first token of a tile's rows; whether rows of c have to be zeroed
   auto token_of = [&](const Tile& t) { return p.pass[t.job].reverse ? t.len - (t.c + 1) * kTC : t.c * kTC; };
@@ -523,12 +553,18 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, OutCfg<DK>::OCC)
   if (warp == NCW) {
     // ---------------------------------------------------------- control --
     if (lane == 0) {
-      auto next_tile = [&](int idx, Tile& t) {
-        for (; idx < tiles; idx += gridDim.x) {
-          t = tile_of(idx);
+      Tile at = digits(blockIdx.x);
+      int at_idx = blockIdx.x;
+      auto next_tile = [&](Tile& t) {  // the next one that holds tokens
+        for (; at_idx < tiles; at_idx += gridDim.x, advance(at)) {
+          t = at;
+          t.len = row_len(p, t.b);
           if (t.len > t.c * kTC) break;
         }
-        return idx;
+        const int idx = at_idx;
+        at_idx += gridDim.x;
+        advance(at);
+        return idx < tiles ? idx : tiles;
       };
       uint32_t nx[2] = {0, 0}, ncs[2] = {0, 0};  // copies issued per buffer
       uint32_t ux[2] = {0, 0}, ucs[2] = {0, 0};  // and waited for
@@ -543,12 +579,20 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, OutCfg<DK>::OCC)
         }
         ++nx[buf];
       };
+      auto prefetch_xa = [&](const Tile& t) {
+        const int j = t.job, tok = token_of(t);
+        if (tok < 0) return;
+        for (int k = 0; k < DK / 64; ++k) {
+          tma_prefetch_4d(&m.x[j], 64 * k, t.h * m.xh[j], t.b * m.xb[j], tok);
+          tma_prefetch_4d(&m.a[j], 64 * k, t.h * m.ah[j], t.b * m.ab[j], tok);
+        }
+      };
       auto load_cs = [&](const Tile& t, int v, int buf) {
         const uint32_t f = cF + 8 * buf;
         const int j = t.job;
         mbar_arrive_expect_tx(f, kBlkBytes + C::S);
         tma_load_4d(sm + C::c_at(buf), &m.c[j], 64 * v, t.h * m.ch[j], t.b * m.cb[j], token_of(t), f);
-        tma_load_2d(sm + C::s_at(buf), &m.s_load, 64 * v, ((j * p.B * p.NH + t.bh) * nch + t.c) * DK, f);
+        tma_load_2d(sm + C::s_at(buf), &m.s_load, 64 * v, (((j * p.B + t.b) * p.NH + t.h) * nch + t.c) * DK, f);
         ++ncs[buf];
       };
       auto scores = [&](int buf) {
@@ -564,12 +608,12 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, OutCfg<DK>::OCC)
       uint32_t used[2] = {0, 0}, ret[2] = {0, 0};  // sums per TMEM set: issued, waited for
       uint32_t nz = 0;                             // c tiles with rows zeroed
       Tile t, tn, tnn;
-      int idx = next_tile(blockIdx.x, t), nidx = tiles;
+      int idx = next_tile(t), nidx = tiles;
       bool ok = true;
       if (idx < tiles) {
         load_xa(t, 0);
         load_cs(t, 0, 0);
-        nidx = next_tile(idx + gridDim.x, tn);
+        nidx = next_tile(tn);
         if (C::NXA == 2 && nidx < tiles) load_xa(tn, 1);
         ok = wait(xF, 0);
         if (ok) {
@@ -637,7 +681,8 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, OutCfg<DK>::OCC)
         if (!ok) break;
         if (nidx < tiles) {
           load_cs(tn, 0, 0);
-          const int nn = next_tile(nidx + gridDim.x, tnn);
+          const int nn = next_tile(tnn);
+          if (C::NXA == 1 && nn < tiles) prefetch_xa(tnn);
           if (C::NXA == 2) {
             if (DK == 64 && !(ok = wait(xR, k & 1))) break;  // outputs in x's place have left
             if (nn < tiles) load_xa(tnn, buf);
@@ -670,13 +715,15 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, OutCfg<DK>::OCC)
     uint32_t used[2] = {0, 0};
     bool ok = true;
     int k = 0;
-    Tile tn = tile_of(blockIdx.x);
+    Tile tn = digits(blockIdx.x);
+    tn.len = row_len(p, tn.b);
     float dn = p.log_decay[tn.h];
     for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
       const Tile t = tn;
       const float lg = dn * 1.4426950408889634f;
       if (idx + (int)gridDim.x < tiles) {  // its loads are on their way meanwhile
-        tn = tile_of(idx + gridDim.x);
+        advance(tn);
+        tn.len = row_len(p, tn.b);
         dn = p.log_decay[tn.h];
       }
       const LinAttnPass& ps = p.pass[t.job];
@@ -738,6 +785,10 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, OutCfg<DK>::OCC)
       }
       fence_async_smem();
       tc_fence_before();
+      if (DK == 64 && k > 0) {  // the tile before has left x's place
+        if (lane == 0) bulk_wait_read_all();
+        warp_arrive(xR);
+      }
       warp_arrive(pW);
       const int tok = token_of(t) + 32 * q;  // of this warp's first row
       const bool zero_c = ragged(t);
@@ -799,10 +850,6 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, OutCfg<DK>::OCC)
         }
       }
       if (!ok) break;
-      if (DK == 64) {
-        if (lane == 0) bulk_wait_read_all();
-        warp_arrive(xR);
-      }
       ++k;
     }
     if (lane == 0) bulk_wait_all();
