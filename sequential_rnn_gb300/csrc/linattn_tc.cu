@@ -15,9 +15,9 @@
 // keeps; a chunk's products with the three accumulate from zero in TMEM, and their
 // sum, smallest first, joins the decayed state in round-to-nearest.
 //
-// Both kernels have one control warp (one lane: TMA loads, MMA issue, buffer bookkeeping)
-// and 8 or 16 compute warps (terms of c, decay and mask of the scores, state and
-// output epilogues); mbarriers order them.  Tiles are rows of 64 values (128 bytes, 128-byte
+// In both kernels one warp loads (TMA, one lane), one issues the MMAs (one lane), and
+// the others compute (terms of c, decay and mask of the scores, state and output
+// epilogues); mbarriers order them.  Tiles are rows of 64 values (128 bytes, 128-byte
 // swizzle): the same tile is a K-major operand (scores) and an MN-major one (state
 // update, P c, x S).  Loading through the copy engine matters: with cp.async from all threads
 // the copies of a tile took longer to issue (2,000-2,600 cycles) than its MMAs to run.
@@ -42,7 +42,6 @@ namespace {
 
 constexpr int kTC = 128;                  // tokens per chunk
 constexpr uint32_t kBlkBytes = kTC * 128; // 128 rows x 64 columns
-constexpr int kAhead = 4;                 // chunks fetched into L2 ahead of their use (states)
 
 // tensor maps: x, a, c, out of each pass [T, B, NH, D]; chunk states as rows of DV
 struct TcMaps {
@@ -60,13 +59,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
-}
-// the same box into L2 only
-__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
-  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-               : "memory");
 }
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3,
                                              uint32_t src) {
@@ -126,27 +118,30 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 }
 
 // ---------------------------------------------------------------- states --
+// Warps: state (8; with 64 state rows the four whose TMEM lanes hold them), terms
+// (8; with 64 state rows the other four of the first eight), one that loads a, one that issues the MMAs.
 template <int DK_>
 struct StCfg {
   static constexpr int DK = DK_;
   static constexpr int DKB = DK < 128 ? DK : 128;    // state rows (dk) per CTA
   static constexpr int MB = DK / DKB;
-  static constexpr int NCW = DKB == 128 ? 16 : 8;    // compute warps
-  static constexpr int THREADS = 32 * (NCW + 1);
-  static constexpr int OCC = DKB == 128 ? 1 : 2;
-  static constexpr int NC = 64 / (NCW / 4);          // state columns of a thread
+  static constexpr bool WIDE = DKB == 128;
+  static constexpr int NSW = WIDE ? 8 : 4, NTW = WIDE ? 8 : 4;
+  static constexpr int WLOAD = WIDE ? 16 : 8, WMMA = WLOAD + 1;
+  static constexpr int THREADS = 32 * (WMMA + 1);
+  static constexpr int OCC = WIDE ? 1 : 2;
   static constexpr uint32_t A = (DKB / 64) * kBlkBytes;
-  // sets of c's three terms (and buffers of c).  With two, a chunk's terms are made while the one
-  // before is multiplied; with 64 state rows one set, so that two CTAs fit on an SM.
-  static constexpr int NT = DKB == 128 ? 2 : 1;
-  static constexpr uint32_t sA = 0, sC = 2 * A, sT = sC + NT * kBlkBytes;
+  static constexpr int NA = 3;                       // buffers of a
+  // sets of c's three terms.  With two, a chunk's terms are made while the one before is
+  // multiplied; with 64 state rows one set, so that two CTAs fit on an SM.
+  static constexpr int NT = WIDE ? 2 : 1;
+  static constexpr uint32_t sT = NA * A;
   // (with 64 state rows the MMA's other 64 rows read the tile behind a, and are not used)
-  static constexpr uint32_t sS = sT + NT * 3 * kBlkBytes;  // states on their way: 32 rows x NC per warp
-  static constexpr uint32_t STG = 32 * NC * 2;
+  static constexpr uint32_t sS = sT + NT * 3 * kBlkBytes;  // states on their way: 32 rows x 64 columns each
   static constexpr uint32_t SMEM = sS + DKB * 128 + 1024;
   // the sums of the three terms, side by side (one MMA of N = 192 reads a once for all three:
   // with three of N = 64 a chunk's MMAs took 2,000 cycles, bound by a's shared-memory reads)
-  static constexpr int ND = DKB == 128 ? 2 : 1;            // TMEM buffers
+  static constexpr int ND = WIDE ? 2 : 1;            // TMEM buffers
   static constexpr uint32_t TMEM = ND == 2 ? 512 : 256;
   static constexpr int TILE = DKB * 64;
 };
@@ -156,12 +151,12 @@ template <int DK>
 struct TcOrder {
   using C = StCfg<DK>;
   static constexpr int TILE = C::TILE;
-  static constexpr int OWN = C::DKB * (64 / C::NC);
+  static constexpr int OWN = C::DKB * 2;
   static __device__ __forceinline__ int tiles(const LinAttnParams& p) { return C::MB * (p.DV / 64); }
   static __device__ __forceinline__ void at(const LinAttnParams& p, int tile, int e, int& dk, int& v) {
     const int vts = p.DV / 64, th = (e / 4) % OWN;
     dk = (tile / vts) * C::DKB + th % C::DKB;
-    v = (tile % vts) * 64 + C::NC * (th / C::DKB) + 4 * (e / (4 * OWN)) + (e & 3);
+    v = (tile % vts) * 64 + 32 * (th / C::DKB) + 4 * (e / (4 * OWN)) + (e & 3);
   }
 };
 
@@ -170,15 +165,15 @@ template <int DK, bool STATE_ONLY>
 __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
     linattn_states_kernel(const __grid_constant__ LinAttnParams p, const __grid_constant__ TcMaps m) {
   using C = StCfg<DK>;
-  constexpr int DKB = C::DKB, NC = C::NC, NCW = C::NCW, OWN = TcOrder<DK>::OWN;
+  constexpr int DKB = C::DKB, OWN = TcOrder<DK>::OWN, NA = C::NA;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int abort_flag_s;
   __shared__ uint32_t tslot_s;
-  __shared__ __align__(8) uint64_t bars_s[10];
+  __shared__ __align__(8) uint64_t bars_s[16];
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  // copies of a, of c; terms ready; MMAs done; sums read
+  // copies of a landed; terms ready; MMAs done; sums read; a's rows zeroed
   const uint32_t bar = smem_u32(bars_s);
-  const uint32_t aF = bar, cF = bar + 16, tR = bar + 32, mD = bar + 48, sR = bar + 64;
+  const uint32_t aF = bar, aE = bar + 24, tR = bar + 48, mD = bar + 64, sR = bar + 80;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int vts = p.DV / 64;
   const Where w = where_of(p, C::MB * vts, STATE_ONLY ? p.nseg - 1 : p.nseg);
@@ -195,19 +190,21 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
   const int cnt = cend > c0 ? cend - c0 : 0;
   const bool rev = ps.reverse != 0;
   const TcWait wait{p.status, p.timeout_ns, &abort_flag_s};
+  // first token of chunk `it`'s rows (reversed: possibly below 0)
+  auto token = [&](int it) { return rev ? len - (c0 + it + 1) * kTC : (c0 + it) * kTC; };
 
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(bar + 8 * i, 1);
+    for (int i = 0; i < 6; ++i) mbar_init(bar + 8 * i, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(tR + 8 * i, NCW);
+      mbar_init(tR + 8 * i, C::NTW);
       mbar_init(mD + 8 * i, 1);
-      mbar_init(sR + 8 * i, NCW);
+      mbar_init(sR + 8 * i, C::NSW);
     }
     abort_flag_s = 0;
     fence_mbar_init();
     fence_async_smem();
   }
-  if (warp == NCW) {
+  if (warp == C::WMMA) {
     tmem_alloc(smem_u32(&tslot_s), C::TMEM);
     tmem_relinquish();
   }
@@ -216,87 +213,58 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
   tc_fence_after();
   const uint32_t tmem = tslot_s;
 
-  if (warp == NCW) {
-    // ---------------------------------------------------------- control --
-    if (lane == 0 && cnt > 0) {
+  if (warp == C::WLOAD) {
+    // ------------------------------------------------------------- loads --
+    if (lane == 0) {
       const int hA = w.h * m.ah[w.job], bA = w.b * m.ab[w.job];
-      const int hC = w.h * m.ch[w.job], bC = w.b * m.cb[w.job];
-      auto token = [&](int it) { return rev ? len - (c0 + it + 1) * kTC : (c0 + it) * kTC; };
-      int na = 0, nc = 0;  // copies issued
-      auto load_a = [&](int it) {
-        if (it >= cnt) return;
-        const uint32_t d = sm + C::sA + (it & 1) * C::A, f = aF + 8 * (it & 1);
+      int it = 0;
+      for (; it < cnt; ++it) {
+        const int s = it % NA;
+        if (it >= NA && !wait(aE + 8 * s, ((it - NA) / NA) & 1)) break;
+        const uint32_t d = sm + s * C::A, f = aF + 8 * s;
         mbar_arrive_expect_tx(f, C::A);
 #pragma unroll
         for (int k = 0; k < DKB / 64; ++k)
           tma_load_4d(d + k * kBlkBytes, &m.a[w.job], mb * DKB + 64 * k, hA, bA, token(it), f);
-        ++na;
-      };
-      auto load_c = [&](int it) {
-        if (it >= cnt) return;
-        const uint32_t f = cF + 8 * (it % C::NT);
-        mbar_arrive_expect_tx(f, kBlkBytes);
-        tma_load_4d(sm + C::sC + (it % C::NT) * kBlkBytes, &m.c[w.job], vt * 64, hC, bC, token(it), f);
-        ++nc;
-      };
-      // shared memory holds little more than a chunk ahead: the ones after it are fetched into L2
-      // (a by the CTA of the first columns, c by the one of the first state rows)
-      auto prefetch = [&](int it) {
-        if (it >= cnt || token(it) < 0) return;
-        if (vt == 0)
-#pragma unroll
-          for (int k = 0; k < DKB / 64; ++k)
-            tma_prefetch_4d(&m.a[w.job], mb * DKB + 64 * k, hA, bA, token(it));
-        if (mb == 0) tma_prefetch_4d(&m.c[w.job], vt * 64, hC, bC, token(it));
-      };
-      load_c(0);
-      load_a(0);
-      if (C::NT == 2) load_c(1);
-      load_a(1);
-      for (int k = 2; k < kAhead; ++k) prefetch(k);
+      }
+      if (it < cnt)
+        for (int k = it - NA < 0 ? 0 : it - NA; k < it; ++k) drain(aF + 8 * (k % NA), (k / NA) & 1);
+    }
+    __syncwarp();
+  } else if (warp == C::WMMA) {
+    // -------------------------------------------------------------- MMAs --
+    if (lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(128, 192, true, true);
-      int it = 0;
-      for (; it < cnt; ++it) {
-        const int d = it % C::ND;
-        if (!wait(tR + 8 * (it & 1), (it >> 1) & 1)) break;
-        load_c(it + C::NT);  // its buffer's terms have been made
-        if (!wait(aF + 8 * (it & 1), (it >> 1) & 1)) break;
+      for (int it = 0; it < cnt; ++it) {
+        const int s = it % NA, d = it % C::ND, ts = it % C::NT;
+        if (!wait(aF + 8 * s, (it / NA) & 1)) break;
+        if (!wait(tR + 8 * ts, (it / C::NT) & 1)) break;
         if (it >= C::ND && !wait(sR + 8 * d, ((it - C::ND) / C::ND) & 1)) break;
         tc_fence_after();
-        const uint32_t a = sm + C::sA + (it & 1) * C::A, t = sm + C::sT + (it % C::NT) * (3 * kBlkBytes);
+        const uint32_t a = sm + s * C::A, t = sm + C::sT + ts * (3 * kBlkBytes);
 #pragma unroll
         for (int ks = 0; ks < kTC / 16; ++ks)
           umma_bf16(tmem + d * 192, sdesc_sw128(a + ks * 2048, kBlkBytes, 1024),
                     sdesc_sw128(t + ks * 2048, kBlkBytes, 1024), idesc, ks != 0 ? 1u : 0u);
+        umma_commit(aE + 8 * s);
         umma_commit(mD + 8 * (it & 1));
-        prefetch(it + kAhead);
-        if (it >= 1) {  // the next a goes where the previous chunk's MMAs have read
-          if (!wait(mD + 8 * ((it - 1) & 1), ((it - 1) >> 1) & 1)) break;
-          load_a(it + 1);
-        }
-      }
-      if (it < cnt) {
-        for (int k = na - 2 < 0 ? 0 : na - 2; k < na; ++k) drain(aF + 8 * (k & 1), (k >> 1) & 1);
-        for (int k = nc - C::NT < 0 ? 0 : nc - C::NT; k < nc; ++k)
-          drain(cF + 8 * (k % C::NT), (k / C::NT) & 1);
       }
     }
     __syncwarp();
-  } else {
-    // ---------------------------------------------------------- compute --
+  } else if (C::WIDE ? warp < 8 : (warp & 3) < 2) {
+    // ------------------------------------------------------------- state --
     const float lg = p.log_decay[w.h] * 1.4426950408889634f;
-    const int q = warp & 3, g = warp >> 2;
-    const bool owner = 32 * q < DKB;  // of row dk = 32 q + lane, columns NC g ..
+    const int q = warp & 3, g = warp >> 2;   // rows dk = 32 q + lane, columns 32 g ..
     const int dk = 32 * q + lane, th = g * DKB + dk;
-    const int gk = mb * DKB + dk, gv = vt * 64 + NC * g;
-    float S[NC];
+    const int gk = mb * DKB + dk, gv = vt * 64 + 32 * g;
+    float S[32];
 #pragma unroll
-    for (int j = 0; j < NC; ++j) S[j] = 0.f;
-    if (!STATE_ONLY && owner) {
+    for (int j = 0; j < 32; ++j) S[j] = 0.f;
+    if (!STATE_ONLY) {
       if (p.nseg > 1) {
         const float4* src = reinterpret_cast<const float4*>(seg_state(p, w, w.seg, C::MB * vts, C::TILE));
 #pragma unroll
-        for (int i = 0; i < NC / 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
           const float4 f = src[i * OWN + th];
           S[4 * i] = f.x, S[4 * i + 1] = f.y, S[4 * i + 2] = f.z, S[4 * i + 3] = f.w;
         }
@@ -304,201 +272,216 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
         const float* in = ps.init + (long long)w.bh * DK * p.DV;
         if (ps.init_t) {
 #pragma unroll
-          for (int j = 0; j < NC; ++j) S[j] = in[(long long)(gv + j) * DK + gk];
+          for (int j = 0; j < 32; ++j) S[j] = in[(long long)(gv + j) * DK + gk];
         } else {
 #pragma unroll
-          for (int j = 0; j < NC; j += 4) {
+          for (int j = 0; j < 32; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(in + (long long)gk * p.DV + gv + j);
             S[j] = f.x, S[j + 1] = f.y, S[j + 2] = f.z, S[j + 3] = f.w;
           }
         }
       }
     }
-    // the state at the start of chunk `it` on its way to the chunk states
+    // The state at the start of chunk `it` on its way to the chunk states: the two warps of 32 rows
+    // fill a 64-column box (boxes of 32-byte rows, one per warp, took 700 cycles a chunk).
+    const uint32_t stg = sm + C::sS + q * 4096;
     auto publish = [&](int it) {
-      if (STATE_ONLY || !owner) return;
-      const uint32_t stg = sm + C::sS + (g * (DKB / 32) + q) * C::STG;
-      if (lane == 0) bulk_wait_read_all();
-      __syncwarp();
+      if (STATE_ONLY) return;
+      if (g == 0 && lane == 0) bulk_wait_read_all();
+      bar_sync(1 + q, 64);
 #pragma unroll
-      for (int j = 0; j < NC / 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
         uint32_t pk[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) pk[k] = pack_bf16x2(S[8 * j + 2 * k], S[8 * j + 2 * k + 1]);
-        // 32 rows of 64 (32) bytes, 64- (32-) byte swizzle
-        sts128(stg + lane * (NC * 2) + ((j ^ (NC == 32 ? (lane >> 1) & 3 : (lane >> 2) & 1)) << 4), pk);
+        sts128(stg + blk_at(lane, 4 * g + j), pk);
       }
       fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_2d(&m.s_store, gv, ((w.job * p.B * p.NH + w.bh) * nch + c0 + it) * DK + mb * DKB + 32 * q, stg);
+      bar_sync(1 + q, 64);
+      if (g == 0 && lane == 0) {
+        tma_store_2d(&m.s_store, vt * 64, ((w.job * p.B * p.NH + w.bh) * nch + c0 + it) * DK + mb * DKB + 32 * q,
+                     stg);
         bulk_commit();
       }
     };
-    // c of chunk `it`, weighted, in three bf16 terms: rows tid / 8 + .., 16-byte chunk tid % 8
-    constexpr int ROWS = 1024 / (32 * NCW), STEP = 4 * NCW;
+    if (cnt > 0) publish(0);
+    for (int it = 0; it < cnt; ++it) {
+      const int n = len - (c0 + it) * kTC < kTC ? len - (c0 + it) * kTC : kTC;
+      const float wS = pw(lg, n);
+      wait(mD + 8 * (it & 1), (it >> 1) & 1);  // (after an abort the loop runs out without waiting)
+      tc_fence_after();
+      const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (it % C::ND) * 192 + 32 * g;
+#pragma unroll
+      for (int h = 0; h < 32; h += 16) {
+        uint32_t r0[16], r1[16], r2[16];
+        tmem_ld16(t + 128 + h, r2);
+        tmem_ld16(t + 64 + h, r1);
+        tmem_ld16(t + h, r0);
+        tmem_wait_ld();
+        reg_fence(r0);
+        reg_fence(r1);
+        reg_fence(r2);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)  // smallest first
+          S[h + j] = fmaf(wS, S[h + j],
+                          (__uint_as_float(r2[j]) + __uint_as_float(r1[j])) + __uint_as_float(r0[j]));
+      }
+      tc_fence_before();
+      warp_arrive(sR + 8 * (it % C::ND));
+      if (it + 1 < cnt) publish(it + 1);
+    }
+    if (STATE_ONLY) {
+      float4* dst = reinterpret_cast<float4*>(seg_state(p, w, w.seg + 1, C::MB * vts, C::TILE));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        dst[i * OWN + th] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+    } else if (ps.fin != nullptr && ((len > c0 * kTC && (long long)len <= (long long)c1 * kTC) ||
+                                     (len == 0 && w.seg == 0))) {
+      float* f = ps.fin + ((long long)w.bh * DK + gk) * p.DV + gv;
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        *reinterpret_cast<float4*>(f + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+    }
+    if (!STATE_ONLY && g == 0 && lane == 0) bulk_wait_all();
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- terms --
+    // c of a chunk, weighted, in three bf16 terms.  c comes straight from global memory, a chunk
+    // ahead in registers: rows e / 8 + .., 16-byte chunk e % 8 for thread e.
+    const float lg = p.log_decay[w.h] * 1.4426950408889634f;
+    const int e = C::WIDE ? tid - 256 : (warp >> 2) * 64 + (warp & 1) * 32 + lane;
+    constexpr int ROWS = 1024 / (32 * C::NTW), STEP = 4 * C::NTW;
+    const __nv_bfloat16* gc = static_cast<const __nv_bfloat16*>(ps.c) + w.b * ps.cs[1] + w.h * ps.cs[2] +
+                              vt * 64 + (e % 8) * 8;
+    uint4 cr[ROWS];
+    auto fetch = [&](int it) {
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        const int t = token(it) + e / 8 + STEP * i;
+        cr[i] = t >= 0 && t < len ? *reinterpret_cast<const uint4*>(gc + (long long)t * ps.cs[0])
+                                  : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
     float wj[ROWS];
     int wn = -1;
-    auto make_terms = [&](int it) {
-      const int c = c0 + it, n = len - c * kTC < kTC ? len - c * kTC : kTC;
+    if (cnt > 0) fetch(0);
+    for (int it = 0; it < cnt; ++it) {
+      const int n = len - (c0 + it) * kTC < kTC ? len - (c0 + it) * kTC : kTC, ts = it % C::NT;
       if (wn != n) {
         wn = n;
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-          const int row = tid / 8 + STEP * i, j = rev ? kTC - 1 - row : row;
+          const int row = e / 8 + STEP * i, j = rev ? kTC - 1 - row : row;
           wj[i] = j < n ? ps.upd * pw(lg, n - 1 - j + ps.shift) : 0.f;
         }
       }
-      if (!wait(cF + 8 * (it % C::NT), (it / C::NT) & 1)) return false;
-      const uint32_t src = sm + C::sC + (it % C::NT) * kBlkBytes;
-      const uint32_t set = sm + C::sT + (it % C::NT) * (3 * kBlkBytes);
+      // the MMAs that read this set before are done
+      if (it >= C::NT && !wait(mD + 8 * ((it - C::NT) & 1), ((it - C::NT) >> 1) & 1)) break;
+      const uint32_t set = sm + C::sT + ts * (3 * kBlkBytes);
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
-        const int row = tid / 8 + STEP * i;
-        const uint32_t at = blk_at(row, tid % 8);
-        uint32_t in[4], t[3][4];
-        lds128(in, src + at);
-        if ((rev ? kTC - 1 - row : row) >= n) in[0] = in[1] = in[2] = in[3] = 0u;
+        const uint32_t in[4] = {cr[i].x, cr[i].y, cr[i].z, cr[i].w};
+        uint32_t t[3][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float x0 = bf16_lo(in[k]) * wj[i], x1 = bf16_hi(in[k]) * wj[i];
 #pragma unroll
-          for (int e = 0; e < 3; ++e) {  // the leading 8 bits of the significand, three times
-            t[e][k] = __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632);
+          for (int f = 0; f < 3; ++f) {  // the leading 8 bits of the significand, three times
+            t[f][k] = __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632);
             x0 -= __uint_as_float(__float_as_uint(x0) & 0xffff0000u);
             x1 -= __uint_as_float(__float_as_uint(x1) & 0xffff0000u);
           }
         }
 #pragma unroll
-        for (int k = 0; k < 3; ++k) sts128(set + k * kBlkBytes + at, t[k]);
+        for (int f = 0; f < 3; ++f) sts128(set + f * kBlkBytes + blk_at(e / 8 + STEP * i, e % 8), t[f]);
       }
+      if (it + 1 < cnt) fetch(it + 1);
       if (!rev && n < kTC && len < p.T) {
         // a's rows behind the row's last token hold values that do not count: zeros
-        if (!wait(aF + 8 * (it & 1), (it >> 1) & 1)) return false;
+        if (!wait(aF + 8 * (it % NA), (it / NA) & 1)) break;
         const uint32_t z[4] = {0u, 0u, 0u, 0u};
-        for (int e = tid; e < kTC * (DKB / 8); e += 32 * NCW) {
-          const int row = e / (DKB / 8), ch = e % (DKB / 8);
-          if (row >= n) sts128(sm + C::sA + (it & 1) * C::A + (ch / 8) * kBlkBytes + blk_at(row, ch % 8), z);
+        for (int k = e; k < kTC * (DKB / 8); k += 32 * C::NTW) {
+          const int row = k / (DKB / 8), ch = k % (DKB / 8);
+          if (row >= n) sts128(sm + (it % NA) * C::A + (ch / 8) * kBlkBytes + blk_at(row, ch % 8), z);
         }
       }
       fence_async_smem();
-      warp_arrive(tR + 8 * (it & 1));
-      return true;
-    };
-    bool ok = cnt == 0 || make_terms(0);
-    if (cnt > 0) publish(0);
-    for (int it = 0; ok && it < cnt; ++it) {
-      if (C::NT == 2 && it + 1 < cnt && !make_terms(it + 1)) break;
-      if (!wait(mD + 8 * (it & 1), (it >> 1) & 1)) break;
-      tc_fence_after();
-      const int c = c0 + it, n = len - c * kTC < kTC ? len - c * kTC : kTC;
-      if (owner) {
-        const float wS = pw(lg, n);
-        const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (it % C::ND) * 192 + NC * g;
-#pragma unroll
-        for (int h = 0; h < NC; h += 16) {
-          uint32_t r0[16], r1[16], r2[16];
-          tmem_ld16(t + 128 + h, r2);
-          tmem_ld16(t + 64 + h, r1);
-          tmem_ld16(t + h, r0);
-          tmem_wait_ld();
-          reg_fence(r0);
-          reg_fence(r1);
-          reg_fence(r2);
-#pragma unroll
-          for (int j = 0; j < 16; ++j)  // smallest first
-            S[h + j] = fmaf(wS, S[h + j],
-                            (__uint_as_float(r2[j]) + __uint_as_float(r1[j])) + __uint_as_float(r0[j]));
-        }
-      }
-      tc_fence_before();
-      warp_arrive(sR + 8 * (it % C::ND));
-      if (it + 1 < cnt) {
-        if (C::NT == 1 && !make_terms(it + 1)) break;
-        publish(it + 1);
-      }
+      warp_arrive(tR + 8 * ts);
     }
-    if (!STATE_ONLY && lane == 0) bulk_wait_all();
     __syncwarp();
-    if (owner) {
-      if (STATE_ONLY) {
-        float4* dst = reinterpret_cast<float4*>(seg_state(p, w, w.seg + 1, C::MB * vts, C::TILE));
-#pragma unroll
-        for (int i = 0; i < NC / 4; ++i)
-          dst[i * OWN + th] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
-      } else if (ps.fin != nullptr && ((len > c0 * kTC && (long long)len <= (long long)c1 * kTC) ||
-                                       (len == 0 && w.seg == 0))) {
-        float* f = ps.fin + ((long long)w.bh * DK + gk) * p.DV + gv;
-#pragma unroll
-        for (int j = 0; j < NC; j += 4)
-          *reinterpret_cast<float4*>(f + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
-      }
-    }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == NCW) {
+  if (warp == C::WMMA) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM);
   }
 }
 
 // --------------------------------------------------------------- outputs --
+// One CTA per SM walks tiles of 128 tokens; two groups of eight compute warps take every
+// other tile, so that one tile's scores are masked or its sums stored while the other's MMAs
+// run.  The scores stay in TMEM: fp32 in, bf16 out over the same columns, from where
+// P c takes them as its A operand.
 template <int DK>
 struct OutCfg {
-  static constexpr int NCW = DK == 64 ? 8 : 16;        // compute warps
-  static constexpr int THREADS = 32 * (NCW + 1);
-  static constexpr int OCC = DK == 64 ? 2 : 1;
-  static constexpr int NG = NCW / 4, NC = 64 / NG;     // a thread: one row, NC of 64 output columns
+  static constexpr int NGW = 8;                          // warps of a group
+  static constexpr int WLOAD = 16, WMMA = 17, THREADS = 32 * 18;
   static constexpr uint32_t X = (DK / 64) * kBlkBytes;
-  // x and a of one tile.  Scores in bf16 (32 KB) take the place of a once it has been multiplied
-  // (with 64 columns of a, its 16 KB and 16 KB more).
-  static constexpr int NXA = DK <= 128 ? 2 : 1;        // tiles of x and a
-  static constexpr uint32_t XTRA = X < 2 * kBlkBytes ? kBlkBytes : 0;
-  static constexpr uint32_t S = DK * 128;              // DK rows x 64 columns of the state
-  static constexpr int NCS = DK >= 128 ? 2 : 1;        // c and state tiles of 64 columns
-  // with 256 columns the second state tile lies in a's upper half, free after the scores
-  static constexpr uint32_t sXtra = NXA * 2 * X, sCS = sXtra + XTRA;
-  static constexpr uint32_t CS = DK == 256 ? 2 * kBlkBytes + S : NCS * (kBlkBytes + S);
-  // outputs on their way: 32 rows x NC columns per warp; with 64 columns in x's place
-  static constexpr uint32_t sO = sCS + CS;
-  static constexpr uint32_t STG = 32 * NC * 2;
-  static constexpr uint32_t SMEM = sO + (DK == 64 ? 0 : NCW * STG) + 1024;
-  static constexpr int NO = OCC == 1 ? 2 : 1;          // sums (P c and x S) in TMEM
-  static constexpr uint32_t TMEM = OCC == 1 ? 512 : 256;
-  static __device__ __forceinline__ uint32_t s_at(int buf) {
-    return DK == 256 && buf == 1 ? X + 2 * kBlkBytes : sCS + buf * (kBlkBytes + S);
-  }
-  static __device__ __forceinline__ uint32_t c_at(int buf) {
-    return buf == 0 ? sCS + S : (DK == 256 ? sCS + S + kBlkBytes : sCS + 2 * S + kBlkBytes);
-  }
+  static constexpr int NX = DK == 64 ? 3 : (DK == 128 ? 2 : 1);  // tiles of x and a
+  static constexpr uint32_t S = DK * 128;                // DK rows x 64 columns of the state
+  static constexpr int NCS = DK == 64 ? 3 : 2;           // c and state tiles of 64 columns
+  static constexpr uint32_t CS = kBlkBytes + S;
+  // with 256 columns the second of them lies in a's place, free after the scores
+  static constexpr uint32_t sCS = NX * 2 * X, sO = sCS + (DK == 256 ? 1 : NCS) * CS;
+  static constexpr uint32_t SMEM = sO + 8 * 4096 + 1024;  // (outputs on their way: 32 rows x 64 columns each)
+  static __device__ __forceinline__ uint32_t cs_at(int buf) { return DK == 256 && buf == 1 ? X : sCS + buf * CS; }
 };
 
-// A persistent CTA walks (row, head, chunk, pass) tiles, the passes of a chunk side by
-// side on the grid, since they read the same tokens.
+// D[tmem] (+)= A[tmem, bf16 pairs] * B[smem]^T
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 16 consecutive 32-bit TMEM columns of this warp's lanes
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 template <int DK>
-__global__ void __launch_bounds__(OutCfg<DK>::THREADS, OutCfg<DK>::OCC)
+__global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
     linattn_outputs_kernel(const __grid_constant__ LinAttnParams p, const __grid_constant__ TcMaps m,
                            int tiles) {
   using C = OutCfg<DK>;
-  constexpr int NCW = C::NCW, NG = C::NG, NC = C::NC;
+  constexpr int NX = C::NX, NCS = C::NCS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int abort_flag_s;
   __shared__ uint32_t tslot_s;
-  __shared__ __align__(8) uint64_t bars_s[14];
+  __shared__ __align__(8) uint64_t bars_s[24];
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bar = smem_u32(bars_s);
-  // x and a loaded; c and state loaded; scores done; scores written (and read from TMEM);
-  // sums done; sums read; staging in x read; c's rows behind the last token zeroed
-  const uint32_t xF = bar, cF = bar + 16, sc = bar + 32, pW = bar + 40, oD = bar + 48, oR = bar + 64,
-                 xR = bar + 80, cZ = bar + 88;
+  // x, a landed / read; c, state landed / read; scores done; sums done; scores in bf16; sums
+  // read; c's rows behind the last token zeroed
+  const uint32_t xF = bar, xE = bar + 24, cF = bar + 48, cE = bar + 72, sc = bar + 96, oD = bar + 112,
+                 pW = bar + 128, oR = bar + 144, cZ = bar + 160;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nch = (p.T + kTC - 1) / kTC;
   const int vts = p.DV / 64;
   const TcWait wait{p.status, p.timeout_ns, &abort_flag_s};
 
-  // tiles in the order pass, chunk, head, row (fastest first); a step of the grid is added digit by
-  // digit (the divisions of a place cost 700 cycles a tile)
+  // tiles in the order pass, chunk, head, row (fastest first: the passes of a chunk read the same
+  // tokens); a step of the grid is added digit by digit (the divisions of a place cost 700
+  // cycles a tile)
   struct Tile {
     int job, c, h, b, len;
   };
@@ -527,339 +510,296 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, OutCfg<DK>::OCC)
   auto ragged = [&](const Tile& t) {
     return !p.pass[t.job].reverse && t.len < p.T && t.len < (t.c + 1) * kTC;
   };
+  Tile at = digits(blockIdx.x);
+  int at_idx = blockIdx.x;
+  // the next tile that holds tokens; false: there is none.  Every role walks the same tiles.
+  auto next_tile = [&](Tile& t) {
+    for (; at_idx < tiles;) {
+      t = at;
+      t.len = row_len(p, t.b);
+      at_idx += gridDim.x;
+      advance(at);
+      if (t.len > t.c * kTC) return true;
+    }
+    return false;
+  };
+  // buffer of the f-th tile of c and state (the v-th of its tile), and how often it was used before
+  auto cs_buf = [&](int f, int v) { return DK == 256 ? (v & 1) : f % NCS; };
+  auto cs_use = [&](int f, int k) { return DK == 256 ? (vts == 1 ? k : f / 2) : f / NCS; };
 
   if (tid == 0) {
-    for (int i = 0; i < 5; ++i) mbar_init(bar + 8 * i, 1);
-    mbar_init(pW, NCW);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(oD + 8 * i, 1);
-      mbar_init(oR + 8 * i, NCW);
-    }
-    mbar_init(xR, NCW);
-    mbar_init(cZ, NCW);
+    for (int i = 0; i < 16; ++i) mbar_init(bar + 8 * i, 1);
+    for (int i = 16; i < 22; ++i) mbar_init(bar + 8 * i, C::NGW);
     abort_flag_s = 0;
     fence_mbar_init();
     fence_async_smem();
   }
-  if (warp == NCW) {
-    tmem_alloc(smem_u32(&tslot_s), C::TMEM);
+  if (warp == C::WMMA) {
+    tmem_alloc(smem_u32(&tslot_s), 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tslot_s;
+  const uint32_t tmem = tslot_s;  // two sets of scores (128 columns), then two of sums (P c, x S)
 
-  if (warp == NCW) {
-    // ---------------------------------------------------------- control --
+  if (warp == C::WLOAD) {
+    // ------------------------------------------------------------- loads --
     if (lane == 0) {
-      Tile at = digits(blockIdx.x);
-      int at_idx = blockIdx.x;
-      auto next_tile = [&](Tile& t) {  // the next one that holds tokens
-        for (; at_idx < tiles; at_idx += gridDim.x, advance(at)) {
-          t = at;
-          t.len = row_len(p, t.b);
-          if (t.len > t.c * kTC) break;
-        }
-        const int idx = at_idx;
-        at_idx += gridDim.x;
-        advance(at);
-        return idx < tiles ? idx : tiles;
-      };
-      uint32_t nx[2] = {0, 0}, ncs[2] = {0, 0};  // copies issued per buffer
-      uint32_t ux[2] = {0, 0}, ucs[2] = {0, 0};  // and waited for
-      auto load_xa = [&](const Tile& t, int buf) {
-        const uint32_t d = sm + buf * (2 * C::X), f = xF + 8 * buf;
-        const int j = t.job, tok = token_of(t);
-        mbar_arrive_expect_tx(f, 2 * C::X);
+      Tile t;
+      int k = 0, f = 0;
+      bool ok = true;
+      for (; ok && next_tile(t); ++k) {
+        const int j = t.job, tok = token_of(t), s = k % NX;
+        if (k >= NX && !(ok = wait(xE + 8 * s, ((k - NX) / NX) & 1))) break;
+        const uint32_t d = sm + s * (2 * C::X);
+        mbar_arrive_expect_tx(xF + 8 * s, 2 * C::X);
 #pragma unroll
-        for (int k = 0; k < DK / 64; ++k) {
-          tma_load_4d(d + k * kBlkBytes, &m.x[j], 64 * k, t.h * m.xh[j], t.b * m.xb[j], tok, f);
-          tma_load_4d(d + C::X + k * kBlkBytes, &m.a[j], 64 * k, t.h * m.ah[j], t.b * m.ab[j], tok, f);
+        for (int i = 0; i < DK / 64; ++i) {
+          tma_load_4d(d + i * kBlkBytes, &m.x[j], 64 * i, t.h * m.xh[j], t.b * m.xb[j], tok, xF + 8 * s);
+          tma_load_4d(d + C::X + i * kBlkBytes, &m.a[j], 64 * i, t.h * m.ah[j], t.b * m.ab[j], tok, xF + 8 * s);
         }
-        ++nx[buf];
-      };
-      auto prefetch_xa = [&](const Tile& t) {
-        const int j = t.job, tok = token_of(t);
-        if (tok < 0) return;
-        for (int k = 0; k < DK / 64; ++k) {
-          tma_prefetch_4d(&m.x[j], 64 * k, t.h * m.xh[j], t.b * m.xb[j], tok);
-          tma_prefetch_4d(&m.a[j], 64 * k, t.h * m.ah[j], t.b * m.ab[j], tok);
+        const int srow = (((j * p.B + t.b) * p.NH + t.h) * nch + t.c) * DK;
+        for (int v = 0; v < vts; ++v, ++f) {
+          const int cb = cs_buf(f, v), use = cs_use(f, k);
+          if (DK == 256 && cb == 1) {  // in a's place: its scores are done
+            if (!(ok = wait(sc + 8 * (k & 1), (k >> 1) & 1))) break;
+          }
+          if (use > 0 && !(ok = wait(cE + 8 * cb, (use - 1) & 1))) break;
+          mbar_arrive_expect_tx(cF + 8 * cb, C::CS);
+          tma_load_2d(sm + C::cs_at(cb), &m.s_load, 64 * v, srow, cF + 8 * cb);
+          tma_load_4d(sm + C::cs_at(cb) + C::S, &m.c[j], 64 * v, t.h * m.ch[j], t.b * m.cb[j], tok, cF + 8 * cb);
         }
-      };
-      auto load_cs = [&](const Tile& t, int v, int buf) {
-        const uint32_t f = cF + 8 * buf;
-        const int j = t.job;
-        mbar_arrive_expect_tx(f, kBlkBytes + C::S);
-        tma_load_4d(sm + C::c_at(buf), &m.c[j], 64 * v, t.h * m.ch[j], t.b * m.cb[j], token_of(t), f);
-        tma_load_2d(sm + C::s_at(buf), &m.s_load, 64 * v, (((j * p.B + t.b) * p.NH + t.h) * nch + t.c) * DK, f);
-        ++ncs[buf];
-      };
-      auto scores = [&](int buf) {
+      }
+      if (!ok) {  // copies in flight land first (a barrier without one is waited for in vain, 10 ms)
+        for (int i = 0; i < NX; ++i) drain(xF + 8 * i, ((k > i ? (k - 1 - i) / NX : 0)) & 1);
+        for (int i = 0; i < NCS; ++i) drain(cF + 8 * i, 0), drain(cF + 8 * i, 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == C::WMMA) {
+    // -------------------------------------------------------------- MMAs --
+    if (lane == 0) {
+      uint32_t nz[2] = {0, 0};  // c tiles with rows zeroed, by group
+      auto scores = [&](int k) {
         constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
-        const uint32_t x = sm + buf * (2 * C::X), a = x + C::X;
+        const uint32_t x = sm + (k % NX) * (2 * C::X), a = x + C::X;
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks) {
           const uint32_t o = (uint32_t)(ks / 4) * kBlkBytes + (ks % 4) * 32;
-          umma_bf16(tmem, sdesc_sw128(x + o, 16, 1024), sdesc_sw128(a + o, 16, 1024), idesc, ks != 0);
+          umma_bf16(tmem + (k & 1) * 128, sdesc_sw128(x + o, 16, 1024), sdesc_sw128(a + o, 16, 1024), idesc,
+                    ks != 0);
         }
-        umma_commit(sc);
+        umma_commit(sc + 8 * (k & 1));
       };
-      uint32_t used[2] = {0, 0}, ret[2] = {0, 0};  // sums per TMEM set: issued, waited for
-      uint32_t nz = 0;                             // c tiles with rows zeroed
-      Tile t, tn, tnn;
-      int idx = next_tile(t), nidx = tiles;
-      bool ok = true;
-      if (idx < tiles) {
-        load_xa(t, 0);
-        load_cs(t, 0, 0);
-        nidx = next_tile(tn);
-        if (C::NXA == 2 && nidx < tiles) load_xa(tn, 1);
+      Tile t, tn;
+      bool more = next_tile(t), ok = true;
+      if (more) {
         ok = wait(xF, 0);
-        if (ok) {
-          ++ux[0];
-          tc_fence_after();
-          scores(0);
-        }
+        tc_fence_after();
+        if (ok) scores(0);
       }
-      for (int k = 0; ok && idx < tiles; ++k) {
-        const int buf = C::NXA == 2 ? (k & 1) : 0;
-        const uint32_t x = sm + buf * (2 * C::X), a = x + C::X;
+      int f = 0;
+      for (int k = 0; ok && more; ++k) {
+        more = next_tile(tn);
+        const uint32_t x = sm + (k % NX) * (2 * C::X);
         const bool zeroed = ragged(t);
-        for (int v = 0; ok && v < vts; ++v) {
-          const int cb = C::NCS == 2 ? (v & 1) : 0, o = C::NO == 2 ? (v & 1) : 0;
-          if (C::NCS == 2 && v + 1 < vts) {
-            // its buffers: read by the MMAs of v - 1; with 256 columns a's upper half (scores done)
-            if (v > 0) {
-              if (!(ok = wait(oD + 8 * (o ^ 1), ret[o ^ 1] & 1))) break;
-              ++ret[o ^ 1];
-            } else if (DK == 256) {
-              if (!(ok = wait(sc, k & 1))) break;
-            }
-            load_cs(t, v + 1, cb ^ 1);
-          }
-          if (!(ok = wait(cF + 8 * cb, ucs[cb] & 1))) break;
-          ++ucs[cb];
-          if (used[o] > 0 && !(ok = wait(oR + 8 * o, (used[o] - 1) & 1))) break;
+        for (int v = 0; ok && v < vts; ++v, ++f) {
+          const int cb = cs_buf(f, v), o = f & 1;
+          if (!(ok = wait(cF + 8 * cb, cs_use(f, k) & 1))) break;
+          if (f >= 2 && !(ok = wait(oR + 8 * o, ((f - 2) >> 1) & 1))) break;
           tc_fence_after();
           constexpr uint32_t idesc = idesc_bf16_f32(128, 64, false, true);
-          const uint32_t tO = tmem + 128 + o * 128, s = sm + C::s_at(cb), cc = sm + C::c_at(cb);
+          const uint32_t tO = tmem + 256 + o * 128, st = sm + C::cs_at(cb), cc = st + C::S;
 #pragma unroll
           for (int ks = 0; ks < DK / 16; ++ks)
             umma_bf16(tO + 64, sdesc_sw128(x + (uint32_t)(ks / 4) * kBlkBytes + (ks % 4) * 32, 16, 1024),
-                      sdesc_sw128(s + ks * 2048, kBlkBytes, 1024), idesc, ks != 0);
-          if (v == 0 && !(ok = wait(pW, k & 1))) break;
-          if (zeroed && !(ok = wait(cZ, nz++ & 1))) break;
+                      sdesc_sw128(st + ks * 2048, kBlkBytes, 1024), idesc, ks != 0);
+          if (v == 0) {
+            if (NX > 1 && more) {
+              // the next tile's scores, over those that the previous tile's MMAs have read
+              if (!(ok = wait(xF + 8 * ((k + 1) % NX), ((k + 1) / NX) & 1))) break;
+              if (k >= 1 && !(ok = wait(oD + 8 * ((f - 1) & 1), ((f - 1) >> 1) & 1))) break;
+              tc_fence_after();
+              scores(k + 1);
+            }
+            if (!(ok = wait(pW + 8 * (k & 1), (k >> 1) & 1))) break;
+          }
+          if (zeroed && !(ok = wait(cZ + 8 * (k & 1), nz[k & 1]++ & 1))) break;
           tc_fence_after();
 #pragma unroll
           for (int ks = 0; ks < kTC / 16; ++ks)
-            umma_bf16(tO,
-                      sdesc_sw128((ks < 4 ? a : (C::XTRA ? sm + C::sXtra : a + kBlkBytes)) + (ks % 4) * 32, 16, 1024),
-                      sdesc_sw128(cc + ks * 2048, kBlkBytes, 1024), idesc, ks != 0);
+            umma_bf16_ts(tO, tmem + (k & 1) * 128 + ks * 8, sdesc_sw128(cc + ks * 2048, kBlkBytes, 1024), idesc,
+                         ks != 0);
           umma_commit(oD + 8 * o);
-          ++used[o];
-          if (C::NCS == 1 && v + 1 < vts) {  // the one buffer, once these MMAs have read it
-            if (!(ok = wait(oD, ret[0] & 1))) break;
-            ++ret[0];
-            load_cs(t, v + 1, 0);
-          }
+          umma_commit(cE + 8 * cb);
+          if (v == vts - 1) umma_commit(xE + 8 * (k % NX));
         }
-        if (!ok) break;
-        if (C::NXA == 2 && nidx < tiles) {  // the next scores, behind these MMAs
-          const int nb = buf ^ 1;
-          if (!(ok = wait(xF + 8 * nb, ux[nb] & 1))) break;
-          ++ux[nb];
+        if (NX == 1 && ok && more) {
+          if (!(ok = wait(xF, (k + 1) & 1))) break;
           tc_fence_after();
-          scores(nb);
+          scores(k + 1);
         }
-        // every buffer of this tile has been read
-        for (int o = 0; ok && o < C::NO; ++o)
-          while (ok && ret[o] < used[o]) {
-            ok = wait(oD + 8 * o, ret[o] & 1);
-            ++ret[o];
-          }
-        if (!ok) break;
-        if (nidx < tiles) {
-          load_cs(tn, 0, 0);
-          const int nn = next_tile(tnn);
-          if (C::NXA == 1 && nn < tiles) prefetch_xa(tnn);
-          if (C::NXA == 2) {
-            if (DK == 64 && !(ok = wait(xR, k & 1))) break;  // outputs in x's place have left
-            if (nn < tiles) load_xa(tnn, buf);
-          } else {
-            load_xa(tn, 0);
-            if (!(ok = wait(xF, ux[0] & 1))) break;
-            ++ux[0];
-            tc_fence_after();
-            scores(0);
-          }
-          t = tn;
-          tn = tnn;
-          idx = nidx;
-          nidx = nn;
-        } else {
-          idx = tiles;
-        }
+        t = tn;
       }
-      if (!ok)
-        for (int i = 0; i < 2; ++i) {
-          if (nx[i]) drain(xF + 8 * i, (nx[i] - 1) & 1);
-          if (ncs[i]) drain(cF + 8 * i, (ncs[i] - 1) & 1);
-        }
     }
     __syncwarp();
   } else {
     // ---------------------------------------------------------- compute --
-    const int q = warp & 3, g = warp >> 2, row = 32 * q + lane;
+    const int grp = warp >> 3, q = warp & 3, g = (warp >> 2) & 1;
+    const int row = 32 * q + lane, gt = tid & 255;  // thread of the group
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    uint32_t used[2] = {0, 0};
-    bool ok = true;
+    const uint32_t stg = sm + C::sO + (grp * 4 + q) * 4096;
+    const int id = 1 + grp * 4 + q;  // named barrier of the two warps of these rows
+    const uint32_t tS = tmem + lanes + grp * 128;
+    // (After an abort the waits return at once and the loop runs out: no warp leaves it before the other
+    // one of its named barrier.)
+    // zeros for a tile's tokens that do not count, 64 v + 32 g .. of token r0 + row
+    auto zeros = [&](const Tile& t, int n) {
+      const LinAttnPass& ps = p.pass[t.job];
+      const int r = t.c * kTC + row;
+      if (row < n || r >= p.T) return;
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(ps.out) + (long long)r * ps.os[0] + t.b * ps.os[1] +
+                         t.h * ps.os[2] + 32 * g;
+      for (int v = 0; v < vts; ++v)
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) *reinterpret_cast<uint4*>(o + 64 * v + j) = make_uint4(0u, 0u, 0u, 0u);
+    };
     int k = 0;
-    Tile tn = digits(blockIdx.x);
-    tn.len = row_len(p, tn.b);
-    float dn = p.log_decay[tn.h];
-    for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
-      const Tile t = tn;
-      const float lg = dn * 1.4426950408889634f;
-      if (idx + (int)gridDim.x < tiles) {  // its loads are on their way meanwhile
-        advance(tn);
-        tn.len = row_len(p, tn.b);
-        dn = p.log_decay[tn.h];
+    Tile t;
+    while (at_idx < tiles) {
+      t = at;
+      t.len = row_len(p, t.b);
+      at_idx += gridDim.x;
+      advance(at);
+      const int n = t.len - t.c * kTC < kTC ? t.len - t.c * kTC : kTC;
+      if (n <= 0) {
+        if (grp == 0) zeros(t, 0);
+        continue;
+      }
+      if ((k & 1) != grp) {
+        ++k;
+        continue;
       }
       const LinAttnPass& ps = p.pass[t.job];
-      const int r0 = t.c * kTC, n = t.len - r0 < kTC ? t.len - r0 : kTC;
       const bool rev = ps.reverse != 0;
-      __nv_bfloat16* go = static_cast<__nv_bfloat16*>(ps.out) + t.b * ps.os[1] + t.h * ps.os[2] + NC * g;
-      // tokens of this chunk that do not count (reversed, the chunk's own rows are others)
-      if (row >= n && r0 + row < p.T && (rev || n <= 0)) {
-        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-        for (int v = 0; v < vts; ++v)
-#pragma unroll
-          for (int j = 0; j < NC; j += 8)
-            *reinterpret_cast<uint4*>(go + (long long)(r0 + row) * ps.os[0] + 64 * v + j) = z;
-      }
-      if (n <= 0) continue;
-      const int buf = C::NXA == 2 ? (k & 1) : 0;
-      const uint32_t sX = sm + buf * (2 * C::X), sP = sX + C::X;
-      const float lam = pw(lg, 1);
+      const float lg = p.log_decay[t.h] * 1.4426950408889634f, lam = pw(lg, 1);
       const float fr = ps.inter * pw(lg, (rev ? kTC - 1 - row : row) + 1 - ps.shift);
-      if (!wait(sc, k & 1)) break;
+      // blocks of 32 columns g and g + 2; powers from the column nearest to the diagonal on, each lambda
+      // times the one before
+      float f0[2];
+      int live[2];  // last (reversed: first) column that counts; 32 (-1): none
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int blk = g + 2 * i, d = rev ? 32 * (blk - q) - lane : lane + 32 * (q - blk) - 31;
+        f0[i] = ps.intra * (blk == q ? 1.f : pw(lg, d > 0 ? d : 0));
+        live[i] = blk == q ? lane : ((rev ? blk > q : blk < q) ? (rev ? 0 : 31) : (rev ? 32 : -1));
+      }
+      if (rev) zeros(t, n);
+      wait(sc + 8 * grp, (k >> 1) & 1);
       tc_fence_after();
-      // decay and mask of this thread's row of scores, 32 columns at a time
-      for (int blk = g; blk < 4; blk += NG) {
-        // columns 0 .. 63 in a's place, the others behind them or in the extra space
-        const uint32_t dst = blk < 2 ? sP : (C::XTRA ? sm + C::sXtra : sP + kBlkBytes);
-        const int ch = 4 * (blk & 1);
-        uint32_t pk[16];
+      uint32_t pk[2][16];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int blk = g + 2 * i;
         if (rev ? blk >= q : blk <= q) {
           uint32_t s[32];
-          tmem_ld32(tmem + lanes + 32 * blk, s);
-          // powers from the column nearest to the diagonal on, each lambda times the one before
-          float f = blk == q ? ps.intra : ps.intra * pw(lg, rev ? 32 * blk - row : row - 32 * blk - 31);
+          tmem_ld32(tS + 32 * blk, s);
           tmem_wait_ld();
           tmem_reg_fence(s);
-          const int live = blk == q ? lane : (rev ? 0 : 31);  // last (reversed: first) column that counts
+          float fac = f0[i];
           if (rev) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const bool on = j >= live;
-              s[j] = on ? __float_as_uint(__uint_as_float(s[j]) * f) : 0u;
-              f = on ? f * lam : f;
+              const bool on = j >= live[i];
+              s[j] = on ? __float_as_uint(__uint_as_float(s[j]) * fac) : 0u;
+              fac = on ? fac * lam : fac;
             }
           } else {
 #pragma unroll
             for (int j = 31; j >= 0; --j) {
-              const bool on = j <= live;
-              s[j] = on ? __float_as_uint(__uint_as_float(s[j]) * f) : 0u;
-              f = on ? f * lam : f;
+              const bool on = j <= live[i];
+              s[j] = on ? __float_as_uint(__uint_as_float(s[j]) * fac) : 0u;
+              fac = on ? fac * lam : fac;
             }
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+          for (int j = 0; j < 16; ++j)
+            pk[i][j] = pack_bf16x2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
         } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) pk[j] = 0u;
+          for (int j = 0; j < 16; ++j) pk[i][j] = 0u;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sts128(dst + blk_at(row, ch + i), pk + 4 * i);
       }
-      fence_async_smem();
+      bar_sync(id, 64);  // both warps of these rows have read their scores
+      tmem_st16(tS + 16 * g, pk[0]);
+      tmem_st16(tS + 16 * (g + 2), pk[1]);
+      tmem_wait_st();
       tc_fence_before();
-      if (DK == 64 && k > 0) {  // the tile before has left x's place
-        if (lane == 0) bulk_wait_read_all();
-        warp_arrive(xR);
-      }
-      warp_arrive(pW);
+      warp_arrive(pW + 8 * grp);
       const int tok = token_of(t) + 32 * q;  // of this warp's first row
-      const bool zero_c = ragged(t);
+      const bool zero_c = ragged(t), counts = rev ? row >= kTC - n : row < n;
       for (int v = 0; v < vts; ++v) {
-        const int cb = C::NCS == 2 ? (v & 1) : 0, o = C::NO == 2 ? (v & 1) : 0;
+        const int f = k * vts + v, o = f & 1;
         if (zero_c) {
-          // the buffer's uses so far: all tiles before this one, and this one's
-          const uint32_t uses = C::NCS == 2 ? (uint32_t)k * ((vts + 1 - cb) / 2) + v / 2 : (uint32_t)k * vts + v;
-          if (!(ok = wait(cF + 8 * cb, uses & 1))) break;
+          const int cb = cs_buf(f, v);
+          wait(cF + 8 * cb, cs_use(f, k) & 1);
           const uint32_t z[4] = {0u, 0u, 0u, 0u};
-          for (int e = tid; e < kTC * 8; e += 32 * NCW)
-            if (e / 8 >= n) sts128(sm + C::c_at(cb) + blk_at(e / 8, e % 8), z);
+          for (int e = gt; e < kTC * 8; e += 256)
+            if (e / 8 >= n) sts128(sm + C::cs_at(cb) + C::S + blk_at(e / 8, e % 8), z);
           fence_async_smem();
-          warp_arrive(cZ);
+          warp_arrive(cZ + 8 * grp);
         }
-        if (!(ok = wait(oD + 8 * o, used[o] & 1))) break;
-        ++used[o];
+        wait(oD + 8 * o, (f >> 1) & 1);
         tc_fence_after();
-        uint32_t pk[NC / 2];
-        const bool counts = rev ? row >= kTC - n : row < n;
+        uint32_t w[16];
+        const uint32_t tO = tmem + 256 + o * 128 + lanes + 32 * g;
 #pragma unroll
-        for (int h = 0; h < NC; h += 16) {
+        for (int h = 0; h < 32; h += 16) {
           uint32_t u[16], s[16];
-          const uint32_t tO = tmem + 128 + o * 128 + lanes + NC * g + h;
-          tmem_ld16(tO, u);
-          tmem_ld16(tO + 64, s);
+          tmem_ld16(tO + h, u);
+          tmem_ld16(tO + 64 + h, s);
           tmem_wait_ld();
           reg_fence(u);
           reg_fence(s);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            pk[h / 2 + j] =
+            w[h / 2 + j] =
                 counts ? pack_bf16x2(fmaf(fr, __uint_as_float(s[2 * j]), __uint_as_float(u[2 * j])),
                                      fmaf(fr, __uint_as_float(s[2 * j + 1]), __uint_as_float(u[2 * j + 1])))
                        : 0u;
         }
         tc_fence_before();
         warp_arrive(oR + 8 * o);
-        // with 64 columns x's place is free behind the last columns' MMAs only
-        if (tok >= 0 && (DK != 64 || v == vts - 1)) {
-          const uint32_t stg = (DK == 64 ? sX : sm + C::sO) + warp * C::STG;
-          if (lane == 0) bulk_wait_read_all();
-          __syncwarp();
-          // 32 rows of 64 (32) bytes, 64- (32-) byte swizzle
+        if (tok >= 0) {
+          if (g == 0 && lane == 0) bulk_wait_read_all();
+          bar_sync(id, 64);
 #pragma unroll
-          for (int j = 0; j < NC / 8; ++j)
-            sts128(stg + lane * (NC * 2) + ((j ^ (NC == 32 ? (lane >> 1) & 3 : (lane >> 2) & 1)) << 4), pk + 4 * j);
+          for (int j = 0; j < 4; ++j) sts128(stg + blk_at(lane, 4 * g + j), w + 4 * j);
           fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_4d(&m.out[t.job], 64 * v + NC * g, t.h, t.b, tok, stg);
+          bar_sync(id, 64);
+          if (g == 0 && lane == 0) {
+            tma_store_4d(&m.out[t.job], 64 * v, t.h, t.b, tok, stg);
             bulk_commit();
           }
-        } else if (tok + lane >= 0 && tok + lane < p.T) {
+        } else if (tok + lane >= 0) {  // a store may not begin before token 0
+          __nv_bfloat16* go = static_cast<__nv_bfloat16*>(ps.out) + (long long)(tok + lane) * ps.os[0] +
+                              t.b * ps.os[1] + t.h * ps.os[2] + 64 * v + 32 * g;
 #pragma unroll
-          for (int j = 0; j < NC; j += 8)
-            *reinterpret_cast<uint4*>(go + (long long)(tok + lane) * ps.os[0] + 64 * v + j) =
-                make_uint4(pk[j / 2], pk[j / 2 + 1], pk[j / 2 + 2], pk[j / 2 + 3]);
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(go + 8 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         }
       }
-      if (!ok) break;
       ++k;
     }
-    if (lane == 0) bulk_wait_all();
+    if (g == 0 && lane == 0) bulk_wait_all();
     __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == NCW) {
+  if (warp == C::WMMA) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::TMEM);
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -920,16 +860,13 @@ int launch_dk(const LinAttnParams& p, cudaStream_t s) {
     ok = ok && encode_operand(&m.x[j], ps.x, ps.xs, p, DK, 64, kTC, sw, &m.xh[j], &m.xb[j]);
     ok = ok && encode_operand(&m.a[j], ps.a, ps.as, p, DK, 64, kTC, sw, &m.ah[j], &m.ab[j]);
     ok = ok && encode_operand(&m.c[j], ps.c, ps.cs, p, p.DV, 64, kTC, sw, &m.ch[j], &m.cb[j]);
-    ok = ok && encode_operand(&m.out[j], ps.out, ps.os, p, p.DV, O::NC, 32,
-                              O::NC == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B, nullptr,
-                              nullptr);
+    ok = ok && encode_operand(&m.out[j], ps.out, ps.os, p, p.DV, 64, 32, sw, nullptr, nullptr);
   }
   const cuuint64_t dims[2] = {(cuuint64_t)p.DV, (cuuint64_t)(outs * DK)};
   const cuuint64_t strides[1] = {(cuuint64_t)p.DV * 2};
-  const cuuint32_t in[2] = {64, (cuuint32_t)DK}, out[2] = {(cuuint32_t)C::NC, 32};
+  const cuuint32_t in[2] = {64, (cuuint32_t)DK}, out[2] = {64, 32};
   ok = ok && encode(&m.s_load, p.chunk_states, 2, dims, strides, in, CU_TENSOR_MAP_SWIZZLE_128B);
-  ok = ok && encode(&m.s_store, p.chunk_states, 2, dims, strides, out,
-                    C::NC == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+  ok = ok && encode(&m.s_store, p.chunk_states, 2, dims, strides, out, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return kLinAttnTooWide;
   if (cudaMemsetAsync(p.status, 0, sizeof(int), s) != cudaSuccess) return (int)cudaErrorUnknown;
   if (p.nseg > 1) {
@@ -940,7 +877,7 @@ int launch_dk(const LinAttnParams& p, cudaStream_t s) {
         <<<(unsigned)(base * (C::TILE / 256)), 256, 0, s>>>(p, p.seg_chunks * kTC);
   }
   linattn_states_kernel<DK, false><<<(unsigned)(base * p.nseg), C::THREADS, C::SMEM, s>>>(p, m);
-  const long long cap = (long long)sm_count() * O::OCC;
+  const long long cap = sm_count();
   linattn_outputs_kernel<DK>
       <<<(unsigned)(outs < cap ? outs : cap), O::THREADS, O::SMEM, s>>>(p, m, (int)outs);
   return (int)cudaGetLastError();
