@@ -43,13 +43,14 @@ namespace {
 constexpr int kTC = 128;                  // tokens per chunk
 constexpr uint32_t kBlkBytes = kTC * 128; // 128 rows x 64 columns
 
-// tensor maps: x, a, c, out of each pass [T, B, NH, D]; chunk states as rows of DV
+// tensor maps: x, a, c of each pass [T, B, NH, D]; chunk states as rows of DV
 struct TcMaps {
-  CUtensorMap x[kLinAttnPasses], a[kLinAttnPasses], c[kLinAttnPasses], out[kLinAttnPasses];
-  CUtensorMap s_load, s_store;
+  CUtensorMap x[kLinAttnPasses], a[kLinAttnPasses], c[kLinAttnPasses];
+  CUtensorMap s_load;
   // 0 where the operand is shared by all heads / rows (its map has one)
   int xh[kLinAttnPasses], xb[kLinAttnPasses], ah[kLinAttnPasses], ab[kLinAttnPasses];
   int ch[kLinAttnPasses], cb[kLinAttnPasses];
+  int v8;  // the outputs' rows begin at 32-byte boundaries
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
@@ -60,13 +61,16 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3,
-                                             uint32_t src) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
-          reinterpret_cast<uint64_t>(map)),
-      "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
-      : "memory");
+// 32 bytes to global memory (v8: at a 32-byte boundary, one access)
+__device__ __forceinline__ void store32(void* at, const uint32_t* v, bool v8) {
+  if (v8)
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  else
+#pragma unroll
+    for (int i = 0; i < 8; i += 4)
+      reinterpret_cast<uint4*>(at)[i / 4] = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -118,16 +122,17 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 }
 
 // ---------------------------------------------------------------- states --
-// Warps: state (8; with 64 state rows the four whose TMEM lanes hold them), terms
-// (8; with 64 state rows the other four of the first eight), one that loads a, one that issues the MMAs.
+// Warps: 16 (with 64 state rows 8) that make the terms of c and hold the state, one that
+// loads a, one that issues the MMAs.
 template <int DK_>
 struct StCfg {
   static constexpr int DK = DK_;
   static constexpr int DKB = DK < 128 ? DK : 128;    // state rows (dk) per CTA
   static constexpr int MB = DK / DKB;
   static constexpr bool WIDE = DKB == 128;
-  static constexpr int NSW = WIDE ? 8 : 4, NTW = WIDE ? 8 : 4;
-  static constexpr int WLOAD = WIDE ? 16 : 8, WMMA = WLOAD + 1;
+  static constexpr int NCW = WIDE ? 16 : 8;
+  static constexpr int WLOAD = NCW, WMMA = NCW + 1;
+  static constexpr int NC = 64 / (NCW / 4);          // state columns of a thread
   static constexpr int THREADS = 32 * (WMMA + 1);
   static constexpr int OCC = WIDE ? 1 : 2;
   static constexpr uint32_t A = (DKB / 64) * kBlkBytes;
@@ -137,8 +142,7 @@ struct StCfg {
   static constexpr int NT = WIDE ? 2 : 1;
   static constexpr uint32_t sT = NA * A;
   // (with 64 state rows the MMA's other 64 rows read the tile behind a, and are not used)
-  static constexpr uint32_t sS = sT + NT * 3 * kBlkBytes;  // states on their way: 32 rows x 64 columns each
-  static constexpr uint32_t SMEM = sS + DKB * 128 + 1024;
+  static constexpr uint32_t SMEM = sT + NT * 3 * kBlkBytes + 1024;
   // the sums of the three terms, side by side (one MMA of N = 192 reads a once for all three:
   // with three of N = 64 a chunk's MMAs took 2,000 cycles, bound by a's shared-memory reads)
   static constexpr int ND = WIDE ? 2 : 1;            // TMEM buffers
@@ -151,12 +155,12 @@ template <int DK>
 struct TcOrder {
   using C = StCfg<DK>;
   static constexpr int TILE = C::TILE;
-  static constexpr int OWN = C::DKB * 2;
+  static constexpr int OWN = C::DKB * (64 / C::NC);
   static __device__ __forceinline__ int tiles(const LinAttnParams& p) { return C::MB * (p.DV / 64); }
   static __device__ __forceinline__ void at(const LinAttnParams& p, int tile, int e, int& dk, int& v) {
     const int vts = p.DV / 64, th = (e / 4) % OWN;
     dk = (tile / vts) * C::DKB + th % C::DKB;
-    v = (tile % vts) * 64 + 32 * (th / C::DKB) + 4 * (e / (4 * OWN)) + (e & 3);
+    v = (tile % vts) * 64 + C::NC * (th / C::DKB) + 4 * (e / (4 * OWN)) + (e & 3);
   }
 };
 
@@ -165,7 +169,7 @@ template <int DK, bool STATE_ONLY>
 __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
     linattn_states_kernel(const __grid_constant__ LinAttnParams p, const __grid_constant__ TcMaps m) {
   using C = StCfg<DK>;
-  constexpr int DKB = C::DKB, OWN = TcOrder<DK>::OWN, NA = C::NA;
+  constexpr int DKB = C::DKB, NC = C::NC, NCW = C::NCW, OWN = TcOrder<DK>::OWN, NA = C::NA;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int abort_flag_s;
   __shared__ uint32_t tslot_s;
@@ -196,9 +200,9 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
   if (tid == 0) {
     for (int i = 0; i < 6; ++i) mbar_init(bar + 8 * i, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(tR + 8 * i, C::NTW);
+      mbar_init(tR + 8 * i, NCW);
       mbar_init(mD + 8 * i, 1);
-      mbar_init(sR + 8 * i, C::NSW);
+      mbar_init(sR + 8 * i, NCW);
     }
     abort_flag_s = 0;
     fence_mbar_init();
@@ -251,20 +255,38 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
       }
     }
     __syncwarp();
-  } else if (C::WIDE ? warp < 8 : (warp & 3) < 2) {
-    // ------------------------------------------------------------- state --
+  } else {
+    // ---------------------------------------------------------- compute --
     const float lg = p.log_decay[w.h] * 1.4426950408889634f;
-    const int q = warp & 3, g = warp >> 2;   // rows dk = 32 q + lane, columns 32 g ..
-    const int dk = 32 * q + lane, th = g * DKB + dk;
-    const int gk = mb * DKB + dk, gv = vt * 64 + 32 * g;
-    float S[32];
+    // c comes straight from global memory, two chunks ahead in registers (with 64 state rows, where the state takes more
+    // of them, one): rows tid / 8 + .., 16-byte chunk tid % 8
+    const __nv_bfloat16* gc = static_cast<const __nv_bfloat16*>(ps.c) + w.b * ps.cs[1] + w.h * ps.cs[2] +
+                              vt * 64 + (tid % 8) * 8;
+    constexpr int ROWS = 1024 / (32 * NCW), STEP = 4 * NCW;
+    uint4 cr[ROWS], cn[ROWS];
+    auto fetch = [&](int it, uint4 (&d)[ROWS]) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) S[j] = 0.f;
-    if (!STATE_ONLY) {
+      for (int i = 0; i < ROWS; ++i) {
+        const int t = token(it) + tid / 8 + STEP * i;
+        d[i] = it < cnt && t >= 0 && t < len ? *reinterpret_cast<const uint4*>(gc + (long long)t * ps.cs[0])
+                                             : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    fetch(0, cr);
+    if (C::WIDE) fetch(1, cn);
+
+    const int q = warp & 3, g = warp >> 2;   // rows dk = 32 q + lane, columns NC g ..
+    const bool owner = 32 * q < DKB;
+    const int dk = 32 * q + lane, th = g * DKB + dk;
+    const int gk = mb * DKB + dk, gv = vt * 64 + NC * g;
+    float S[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) S[j] = 0.f;
+    if (!STATE_ONLY && owner) {
       if (p.nseg > 1) {
         const float4* src = reinterpret_cast<const float4*>(seg_state(p, w, w.seg, C::MB * vts, C::TILE));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < NC / 4; ++i) {
           const float4 f = src[i * OWN + th];
           S[4 * i] = f.x, S[4 * i + 1] = f.y, S[4 * i + 2] = f.z, S[4 * i + 3] = f.w;
         }
@@ -272,112 +294,30 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
         const float* in = ps.init + (long long)w.bh * DK * p.DV;
         if (ps.init_t) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) S[j] = in[(long long)(gv + j) * DK + gk];
+          for (int j = 0; j < NC; ++j) S[j] = in[(long long)(gv + j) * DK + gk];
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
+          for (int j = 0; j < NC; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(in + (long long)gk * p.DV + gv + j);
             S[j] = f.x, S[j + 1] = f.y, S[j + 2] = f.z, S[j + 3] = f.w;
           }
         }
       }
     }
-    // The state at the start of chunk `it` on its way to the chunk states: the two warps of 32 rows
-    // fill a 64-column box (boxes of 32-byte rows, one per warp, took 700 cycles a chunk).
-    const uint32_t stg = sm + C::sS + q * 4096;
-    auto publish = [&](int it) {
-      if (STATE_ONLY) return;
-      if (g == 0 && lane == 0) bulk_wait_read_all();
-      bar_sync(1 + q, 64);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t pk[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) pk[k] = pack_bf16x2(S[8 * j + 2 * k], S[8 * j + 2 * k + 1]);
-        sts128(stg + blk_at(lane, 4 * g + j), pk);
-      }
-      fence_async_smem();
-      bar_sync(1 + q, 64);
-      if (g == 0 && lane == 0) {
-        tma_store_2d(&m.s_store, vt * 64, ((w.job * p.B * p.NH + w.bh) * nch + c0 + it) * DK + mb * DKB + 32 * q,
-                     stg);
-        bulk_commit();
-      }
-    };
-    if (cnt > 0) publish(0);
-    for (int it = 0; it < cnt; ++it) {
-      const int n = len - (c0 + it) * kTC < kTC ? len - (c0 + it) * kTC : kTC;
-      const float wS = pw(lg, n);
-      wait(mD + 8 * (it & 1), (it >> 1) & 1);  // (after an abort the loop runs out without waiting)
-      tc_fence_after();
-      const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (it % C::ND) * 192 + 32 * g;
-#pragma unroll
-      for (int h = 0; h < 32; h += 16) {
-        uint32_t r0[16], r1[16], r2[16];
-        tmem_ld16(t + 128 + h, r2);
-        tmem_ld16(t + 64 + h, r1);
-        tmem_ld16(t + h, r0);
-        tmem_wait_ld();
-        reg_fence(r0);
-        reg_fence(r1);
-        reg_fence(r2);
-#pragma unroll
-        for (int j = 0; j < 16; ++j)  // smallest first
-          S[h + j] = fmaf(wS, S[h + j],
-                          (__uint_as_float(r2[j]) + __uint_as_float(r1[j])) + __uint_as_float(r0[j]));
-      }
-      tc_fence_before();
-      warp_arrive(sR + 8 * (it % C::ND));
-      if (it + 1 < cnt) publish(it + 1);
-    }
-    if (STATE_ONLY) {
-      float4* dst = reinterpret_cast<float4*>(seg_state(p, w, w.seg + 1, C::MB * vts, C::TILE));
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        dst[i * OWN + th] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
-    } else if (ps.fin != nullptr && ((len > c0 * kTC && (long long)len <= (long long)c1 * kTC) ||
-                                     (len == 0 && w.seg == 0))) {
-      float* f = ps.fin + ((long long)w.bh * DK + gk) * p.DV + gv;
-#pragma unroll
-      for (int j = 0; j < 32; j += 4)
-        *reinterpret_cast<float4*>(f + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
-    }
-    if (!STATE_ONLY && g == 0 && lane == 0) bulk_wait_all();
-    __syncwarp();
-  } else {
-    // ------------------------------------------------------------- terms --
-    // c of a chunk, weighted, in three bf16 terms.  c comes straight from global memory, a chunk
-    // ahead in registers: rows e / 8 + .., 16-byte chunk e % 8 for thread e.
-    const float lg = p.log_decay[w.h] * 1.4426950408889634f;
-    const int e = C::WIDE ? tid - 256 : (warp >> 2) * 64 + (warp & 1) * 32 + lane;
-    constexpr int ROWS = 1024 / (32 * C::NTW), STEP = 4 * C::NTW;
-    const __nv_bfloat16* gc = static_cast<const __nv_bfloat16*>(ps.c) + w.b * ps.cs[1] + w.h * ps.cs[2] +
-                              vt * 64 + (e % 8) * 8;
-    uint4 cr[ROWS];
-    auto fetch = [&](int it) {
-#pragma unroll
-      for (int i = 0; i < ROWS; ++i) {
-        const int t = token(it) + e / 8 + STEP * i;
-        cr[i] = t >= 0 && t < len ? *reinterpret_cast<const uint4*>(gc + (long long)t * ps.cs[0])
-                                  : make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
     float wj[ROWS];
     int wn = -1;
-    if (cnt > 0) fetch(0);
-    for (int it = 0; it < cnt; ++it) {
-      const int n = len - (c0 + it) * kTC < kTC ? len - (c0 + it) * kTC : kTC, ts = it % C::NT;
+    // c of chunk `it` (in cr), weighted, in three bf16 terms
+    auto make_terms = [&](int it) {
+      const int n = len - (c0 + it) * kTC < kTC ? len - (c0 + it) * kTC : kTC;
       if (wn != n) {
         wn = n;
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-          const int row = e / 8 + STEP * i, j = rev ? kTC - 1 - row : row;
+          const int row = tid / 8 + STEP * i, j = rev ? kTC - 1 - row : row;
           wj[i] = j < n ? ps.upd * pw(lg, n - 1 - j + ps.shift) : 0.f;
         }
       }
-      // the MMAs that read this set before are done
-      if (it >= C::NT && !wait(mD + 8 * ((it - C::NT) & 1), ((it - C::NT) >> 1) & 1)) break;
-      const uint32_t set = sm + C::sT + ts * (3 * kBlkBytes);
+      const uint32_t set = sm + C::sT + (it % C::NT) * (3 * kBlkBytes);
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
         const uint32_t in[4] = {cr[i].x, cr[i].y, cr[i].z, cr[i].w};
@@ -393,22 +333,89 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
           }
         }
 #pragma unroll
-        for (int f = 0; f < 3; ++f) sts128(set + f * kBlkBytes + blk_at(e / 8 + STEP * i, e % 8), t[f]);
+        for (int f = 0; f < 3; ++f) sts128(set + f * kBlkBytes + blk_at(tid / 8 + STEP * i, tid % 8), t[f]);
+        if (C::WIDE) cr[i] = cn[i];
       }
-      if (it + 1 < cnt) fetch(it + 1);
       if (!rev && n < kTC && len < p.T) {
         // a's rows behind the row's last token hold values that do not count: zeros
-        if (!wait(aF + 8 * (it % NA), (it / NA) & 1)) break;
+        wait(aF + 8 * (it % NA), (it / NA) & 1);
         const uint32_t z[4] = {0u, 0u, 0u, 0u};
-        for (int k = e; k < kTC * (DKB / 8); k += 32 * C::NTW) {
+        for (int k = tid; k < kTC * (DKB / 8); k += 32 * NCW) {
           const int row = k / (DKB / 8), ch = k % (DKB / 8);
           if (row >= n) sts128(sm + (it % NA) * C::A + (ch / 8) * kBlkBytes + blk_at(row, ch % 8), z);
         }
       }
       fence_async_smem();
-      warp_arrive(tR + 8 * ts);
+      warp_arrive(tR + 8 * (it % C::NT));
+      if (C::WIDE)
+        fetch(it + 2, cn);
+      else
+        fetch(it + 1, cr);
+    };
+    // the state at the start of chunk `it`, straight to the chunk states (by way of
+    // shared memory and TMA stores the fence and barriers took 700 cycles a chunk)
+    __nv_bfloat16* cs = static_cast<__nv_bfloat16*>(p.chunk_states) +
+                        ((((long long)w.job * p.B * p.NH + w.bh) * nch + c0) * DK + gk) * p.DV + gv;
+    auto publish = [&](int it) {
+      if (STATE_ONLY || !owner) return;
+#pragma unroll
+      for (int j = 0; j < NC; j += 16) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) pk[k] = pack_bf16x2(S[j + 2 * k], S[j + 2 * k + 1]);
+        store32(cs + (long long)it * DK * p.DV + j, pk, true);
+      }
+    };
+    // (after an abort the waits return at once and the loop runs out)
+    if (cnt > 0) {
+      make_terms(0);
+      publish(0);
     }
-    __syncwarp();
+    for (int it = 0; it < cnt; ++it) {
+      if (C::NT == 2 && it + 1 < cnt) make_terms(it + 1);
+      const int n = len - (c0 + it) * kTC < kTC ? len - (c0 + it) * kTC : kTC;
+      const float wS = pw(lg, n);
+      wait(mD + 8 * (it & 1), (it >> 1) & 1);
+      tc_fence_after();
+      if (owner) {
+        const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (it % C::ND) * 192 + NC * g;
+#pragma unroll
+        for (int h = 0; h < NC; h += 16) {
+          uint32_t r0[16], r1[16], r2[16];
+          tmem_ld16(t + 128 + h, r2);
+          tmem_ld16(t + 64 + h, r1);
+          tmem_ld16(t + h, r0);
+          tmem_wait_ld();
+          reg_fence(r0);
+          reg_fence(r1);
+          reg_fence(r2);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)  // smallest first
+            S[h + j] = fmaf(wS, S[h + j],
+                            (__uint_as_float(r2[j]) + __uint_as_float(r1[j])) + __uint_as_float(r0[j]));
+        }
+      }
+      tc_fence_before();
+      warp_arrive(sR + 8 * (it % C::ND));
+      if (it + 1 < cnt) {
+        if (C::NT == 1) make_terms(it + 1);
+        publish(it + 1);
+      }
+    }
+    if (owner) {
+      if (STATE_ONLY) {
+        float4* dst = reinterpret_cast<float4*>(seg_state(p, w, w.seg + 1, C::MB * vts, C::TILE));
+#pragma unroll
+        for (int i = 0; i < NC / 4; ++i)
+          dst[i * OWN + th] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+      } else if (ps.fin != nullptr && ((len > c0 * kTC && (long long)len <= (long long)c1 * kTC) ||
+                                       (len == 0 && w.seg == 0))) {
+        float* f = ps.fin + ((long long)w.bh * DK + gk) * p.DV + gv;
+#pragma unroll
+        for (int j = 0; j < NC; j += 4)
+          *reinterpret_cast<float4*>(f + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -430,11 +437,11 @@ struct OutCfg {
   static constexpr uint32_t X = (DK / 64) * kBlkBytes;
   static constexpr int NX = DK == 64 ? 3 : (DK == 128 ? 2 : 1);  // tiles of x and a
   static constexpr uint32_t S = DK * 128;                // DK rows x 64 columns of the state
-  static constexpr int NCS = DK == 64 ? 3 : 2;           // c and state tiles of 64 columns
+  static constexpr int NCS = DK == 256 ? 2 : 3;          // c and state tiles of 64 columns
   static constexpr uint32_t CS = kBlkBytes + S;
   // with 256 columns the second of them lies in a's place, free after the scores
-  static constexpr uint32_t sCS = NX * 2 * X, sO = sCS + (DK == 256 ? 1 : NCS) * CS;
-  static constexpr uint32_t SMEM = sO + 8 * 4096 + 1024;  // (outputs on their way: 32 rows x 64 columns each)
+  static constexpr uint32_t sCS = NX * 2 * X;
+  static constexpr uint32_t SMEM = sCS + (DK == 256 ? 1 : NCS) * CS + 1024;
   static __device__ __forceinline__ uint32_t cs_at(int buf) { return DK == 256 && buf == 1 ? X : sCS + buf * CS; }
 };
 
@@ -458,6 +465,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// a tile as the loading warp tells of it
+struct OutTile {
+  int job, c, h, b, len;
+  float lg;               // log2 of the head's decay
+};
+
 template <int DK>
 __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
     linattn_outputs_kernel(const __grid_constant__ LinAttnParams p, const __grid_constant__ TcMaps m,
@@ -467,26 +480,30 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int abort_flag_s;
   __shared__ uint32_t tslot_s;
-  __shared__ __align__(8) uint64_t bars_s[24];
+  __shared__ __align__(8) uint64_t bars_s[17];
+  __shared__ OutTile info_s[4];  // what the loading warp tells the others of its tiles, the last four
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bar = smem_u32(bars_s);
-  // x, a landed / read; c, state landed / read; scores done; sums done; scores in bf16; sums
-  // read; c's rows behind the last token zeroed
-  const uint32_t xF = bar, xE = bar + 24, cF = bar + 48, cE = bar + 72, sc = bar + 96, oD = bar + 112,
-                 pW = bar + 128, oR = bar + 144, cZ = bar + 160;
+  // x, a landed; c, state landed; MMAs done, by buffer of c and state; scores done; scores in
+  // bf16; sums read; c's rows behind the last token zeroed
+  const uint32_t xF = bar, cF = bar + 24, dn = bar + 48, sc = bar + 72, pW = bar + 88, oR = bar + 104, cZ = bar + 120;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nch = (p.T + kTC - 1) / kTC;
   const int vts = p.DV / 64;
   const TcWait wait{p.status, p.timeout_ns, &abort_flag_s};
 
-  // tiles in the order pass, chunk, head, row (fastest first: the passes of a chunk read the same
-  // tokens); a step of the grid is added digit by digit (the divisions of a place cost 700
-  // cycles a tile)
-  struct Tile {
-    int job, c, h, b, len;
+  int revs = 0;  // passes with reversed time
+  for (int j = 0; j < p.npass; ++j) revs |= (p.pass[j].reverse != 0) << j;
+  // first token of a tile's rows; whether rows of c have to be zeroed
+  auto token_of = [&](const OutTile& t) { return (revs >> t.job) & 1 ? t.len - (t.c + 1) * kTC : t.c * kTC; };
+  auto ragged = [&](const OutTile& t) {
+    return t.len < p.T && t.len < (t.c + 1) * kTC && !((revs >> t.job) & 1);
   };
+  // Tiles in the order pass, chunk, head, row (fastest first: the passes of a chunk read the same
+  // tokens).  A step of the grid is added digit by digit, and by the loading warp alone: the
+  // divisions of a place cost every role 700 cycles a tile, the digits' walk still 1,400 the MMAs' warp.
   auto digits = [&](int idx) {
-    Tile t;
+    OutTile t;
     t.job = idx % p.npass;
     idx /= p.npass;
     t.c = idx % nch;
@@ -495,8 +512,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
     t.b = idx / p.NH;
     return t;
   };
-  const Tile stride = digits((int)gridDim.x);
-  auto advance = [&](Tile& t) {  // (past the last tile b is past the last row: not to be read)
+  auto advance = [&](OutTile& t, const OutTile& stride) {  // (past the last tile b is past the last row)
     t.job += stride.job;
     t.c += stride.c;
     t.h += stride.h;
@@ -505,31 +521,19 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
     if (t.c >= nch) t.c -= nch, ++t.h;
     if (t.h >= p.NH) t.h -= p.NH, ++t.b;
   };
-  // first token of a tile's rows; whether rows of c have to be zeroed
-  auto token_of = [&](const Tile& t) { return p.pass[t.job].reverse ? t.len - (t.c + 1) * kTC : t.c * kTC; };
-  auto ragged = [&](const Tile& t) {
-    return !p.pass[t.job].reverse && t.len < p.T && t.len < (t.c + 1) * kTC;
-  };
-  Tile at = digits(blockIdx.x);
-  int at_idx = blockIdx.x;
-  // the next tile that holds tokens; false: there is none.  Every role walks the same tiles.
-  auto next_tile = [&](Tile& t) {
-    for (; at_idx < tiles;) {
-      t = at;
-      t.len = row_len(p, t.b);
-      at_idx += gridDim.x;
-      advance(at);
-      if (t.len > t.c * kTC) return true;
-    }
-    return false;
-  };
-  // buffer of the f-th tile of c and state (the v-th of its tile), and how often it was used before
-  auto cs_buf = [&](int f, int v) { return DK == 256 ? (v & 1) : f % NCS; };
-  auto cs_use = [&](int f, int k) { return DK == 256 ? (vts == 1 ? k : f / 2) : f / NCS; };
+  // this CTA's tiles that hold tokens
+  int count = ((int)blockIdx.x < tiles ? (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0);
+  if (p.lens != nullptr) {
+    const OutTile stride = digits((int)gridDim.x);
+    OutTile t = digits(blockIdx.x);
+    count = 0;
+    for (int idx = blockIdx.x; idx < tiles; idx += gridDim.x, advance(t, stride))
+      count += row_len(p, t.b) > t.c * kTC;
+  }
 
   if (tid == 0) {
-    for (int i = 0; i < 16; ++i) mbar_init(bar + 8 * i, 1);
-    for (int i = 16; i < 22; ++i) mbar_init(bar + 8 * i, C::NGW);
+    for (int i = 0; i < 11; ++i) mbar_init(bar + 8 * i, 1);
+    for (int i = 11; i < 17; ++i) mbar_init(bar + 8 * i, C::NGW);
     abort_flag_s = 0;
     fence_mbar_init();
     fence_async_smem();
@@ -546,12 +550,22 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
   if (warp == C::WLOAD) {
     // ------------------------------------------------------------- loads --
     if (lane == 0) {
-      Tile t;
-      int k = 0, f = 0;
+      const OutTile stride = digits((int)gridDim.x);
+      OutTile t = digits(blockIdx.x);
+      int k = 0, f = 0, done = 0;  // tiles, c and state tiles; of these, known to be multiplied
       bool ok = true;
-      for (; ok && next_tile(t); ++k) {
+      auto multiplied = [&](int upto) {  // one after the other: no barrier is left two phases behind
+        for (; ok && done < upto; ++done) ok = wait(dn + 8 * (done % NCS), (done / NCS) & 1);
+        return ok;
+      };
+      for (; ok && k < count; advance(t, stride)) {
+        t.len = row_len(p, t.b);
+        if (t.len <= t.c * kTC) continue;  // no tokens: the other roles do not hear of it
+        t.lg = p.log_decay[t.h] * 1.4426950408889634f;
         const int j = t.job, tok = token_of(t), s = k % NX;
-        if (k >= NX && !(ok = wait(xE + 8 * s, ((k - NX) / NX) & 1))) break;
+        // (the roles have read the description of a tile before its last MMAs are issued)
+        if (!multiplied((k - NX + 1) * vts)) break;
+        info_s[k & 3] = t;
         const uint32_t d = sm + s * (2 * C::X);
         mbar_arrive_expect_tx(xF + 8 * s, 2 * C::X);
 #pragma unroll
@@ -561,19 +575,20 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
         }
         const int srow = (((j * p.B + t.b) * p.NH + t.h) * nch + t.c) * DK;
         for (int v = 0; v < vts; ++v, ++f) {
-          const int cb = cs_buf(f, v), use = cs_use(f, k);
+          const int cb = f % NCS;
+          if (!multiplied(f - NCS + 1)) break;
           if (DK == 256 && cb == 1) {  // in a's place: its scores are done
             if (!(ok = wait(sc + 8 * (k & 1), (k >> 1) & 1))) break;
           }
-          if (use > 0 && !(ok = wait(cE + 8 * cb, (use - 1) & 1))) break;
           mbar_arrive_expect_tx(cF + 8 * cb, C::CS);
           tma_load_2d(sm + C::cs_at(cb), &m.s_load, 64 * v, srow, cF + 8 * cb);
           tma_load_4d(sm + C::cs_at(cb) + C::S, &m.c[j], 64 * v, t.h * m.ch[j], t.b * m.cb[j], tok, cF + 8 * cb);
         }
+        ++k;
       }
       if (!ok) {  // copies in flight land first (a barrier without one is waited for in vain, 10 ms)
-        for (int i = 0; i < NX; ++i) drain(xF + 8 * i, ((k > i ? (k - 1 - i) / NX : 0)) & 1);
-        for (int i = 0; i < NCS; ++i) drain(cF + 8 * i, 0), drain(cF + 8 * i, 1);
+        for (int i = 0; i < 3; ++i) drain(xF + 8 * i, 0), drain(xF + 8 * i, 1);
+        for (int i = 0; i < 3; ++i) drain(cF + 8 * i, 0), drain(cF + 8 * i, 1);
       }
     }
     __syncwarp();
@@ -592,21 +607,21 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
         }
         umma_commit(sc + 8 * (k & 1));
       };
-      Tile t, tn;
-      bool more = next_tile(t), ok = true;
-      if (more) {
-        ok = wait(xF, 0);
+      auto landed = [&](int k) {  // x, a and the description of tile k
+        const bool l = wait(xF + 8 * (k % NX), (k / NX) & 1);
         tc_fence_after();
-        if (ok) scores(0);
-      }
+        return l;
+      };
+      bool ok = count > 0 && landed(0);
+      if (ok) scores(0);
       int f = 0;
-      for (int k = 0; ok && more; ++k) {
-        more = next_tile(tn);
+      for (int k = 0; ok && k < count; ++k) {
+        const OutTile t = info_s[k & 3];
         const uint32_t x = sm + (k % NX) * (2 * C::X);
         const bool zeroed = ragged(t);
         for (int v = 0; ok && v < vts; ++v, ++f) {
-          const int cb = cs_buf(f, v), o = f & 1;
-          if (!(ok = wait(cF + 8 * cb, cs_use(f, k) & 1))) break;
+          const int cb = f % NCS, o = f & 1;
+          if (!(ok = wait(cF + 8 * cb, (f / NCS) & 1))) break;
           if (f >= 2 && !(ok = wait(oR + 8 * o, ((f - 2) >> 1) & 1))) break;
           tc_fence_after();
           constexpr uint32_t idesc = idesc_bf16_f32(128, 64, false, true);
@@ -616,10 +631,10 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
             umma_bf16(tO + 64, sdesc_sw128(x + (uint32_t)(ks / 4) * kBlkBytes + (ks % 4) * 32, 16, 1024),
                       sdesc_sw128(st + ks * 2048, kBlkBytes, 1024), idesc, ks != 0);
           if (v == 0) {
-            if (NX > 1 && more) {
+            if (NX > 1 && k + 1 < count) {
               // the next tile's scores, over those that the previous tile's MMAs have read
-              if (!(ok = wait(xF + 8 * ((k + 1) % NX), ((k + 1) / NX) & 1))) break;
-              if (k >= 1 && !(ok = wait(oD + 8 * ((f - 1) & 1), ((f - 1) >> 1) & 1))) break;
+              if (!(ok = landed(k + 1))) break;
+              if (k >= 1 && !(ok = wait(dn + 8 * ((f - 1) % NCS), ((f - 1) / NCS) & 1))) break;
               tc_fence_after();
               scores(k + 1);
             }
@@ -631,16 +646,12 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
           for (int ks = 0; ks < kTC / 16; ++ks)
             umma_bf16_ts(tO, tmem + (k & 1) * 128 + ks * 8, sdesc_sw128(cc + ks * 2048, kBlkBytes, 1024), idesc,
                          ks != 0);
-          umma_commit(oD + 8 * o);
-          umma_commit(cE + 8 * cb);
-          if (v == vts - 1) umma_commit(xE + 8 * (k % NX));
+          umma_commit(dn + 8 * cb);
         }
-        if (NX == 1 && ok && more) {
-          if (!(ok = wait(xF, (k + 1) & 1))) break;
-          tc_fence_after();
+        if (NX == 1 && ok && k + 1 < count) {
+          if (!(ok = landed(k + 1))) break;
           scores(k + 1);
         }
-        t = tn;
       }
     }
     __syncwarp();
@@ -649,41 +660,35 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
     const int grp = warp >> 3, q = warp & 3, g = (warp >> 2) & 1;
     const int row = 32 * q + lane, gt = tid & 255;  // thread of the group
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    const uint32_t stg = sm + C::sO + (grp * 4 + q) * 4096;
     const int id = 1 + grp * 4 + q;  // named barrier of the two warps of these rows
     const uint32_t tS = tmem + lanes + grp * 128;
-    // (After an abort the waits return at once and the loop runs out: no warp leaves it before the other
-    // one of its named barrier.)
-    // zeros for a tile's tokens that do not count, 64 v + 32 g .. of token r0 + row
-    auto zeros = [&](const Tile& t, int n) {
-      const LinAttnPass& ps = p.pass[t.job];
-      const int r = t.c * kTC + row;
-      if (row < n || r >= p.T) return;
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(ps.out) + (long long)r * ps.os[0] + t.b * ps.os[1] +
-                         t.h * ps.os[2] + 32 * g;
-      for (int v = 0; v < vts; ++v)
+    if (p.lens != nullptr) {
+      // Zeros for tokens that do not count, of tiles without tokens and of reversed ones (whose rows
+      // are other tokens): row r0 + row, 64 v + 32 g ..
+      const OutTile stride = digits((int)gridDim.x);
+      OutTile t = digits(blockIdx.x);
+      for (int idx = blockIdx.x; idx < tiles; idx += gridDim.x, advance(t, stride)) {
+        t.len = row_len(p, t.b);
+        const int r = t.c * kTC + row;
+        if (grp != 0 || r < t.len || r >= p.T || (t.len > t.c * kTC && !((revs >> t.job) & 1))) continue;
+        const LinAttnPass& ps = p.pass[t.job];
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(ps.out) + (long long)r * ps.os[0] + t.b * ps.os[1] +
+                           t.h * ps.os[2] + 32 * g;
+        for (int v = 0; v < vts; ++v)
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) *reinterpret_cast<uint4*>(o + 64 * v + j) = make_uint4(0u, 0u, 0u, 0u);
-    };
-    int k = 0;
-    Tile t;
-    while (at_idx < tiles) {
-      t = at;
-      t.len = row_len(p, t.b);
-      at_idx += gridDim.x;
-      advance(at);
+          for (int j = 0; j < 32; j += 8) *reinterpret_cast<uint4*>(o + 64 * v + j) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    for (int k = grp; k < count; k += 2) {
+      // After an abort the waits of a tile return at once, and the two warps of a named barrier leave
+      // the loop together.
+      const bool landed = wait(xF + 8 * (k % NX), (k / NX) & 1);
+      if (bar_red_or(id, 64, !landed)) break;
+      const OutTile t = info_s[k & 3];
       const int n = t.len - t.c * kTC < kTC ? t.len - t.c * kTC : kTC;
-      if (n <= 0) {
-        if (grp == 0) zeros(t, 0);
-        continue;
-      }
-      if ((k & 1) != grp) {
-        ++k;
-        continue;
-      }
       const LinAttnPass& ps = p.pass[t.job];
-      const bool rev = ps.reverse != 0;
-      const float lg = p.log_decay[t.h] * 1.4426950408889634f, lam = pw(lg, 1);
+      const bool rev = (revs >> t.job) & 1;
+      const float lg = t.lg, lam = pw(lg, 1);
       const float fr = ps.inter * pw(lg, (rev ? kTC - 1 - row : row) + 1 - ps.shift);
       // blocks of 32 columns g and g + 2; powers from the column nearest to the diagonal on, each lambda
       // times the one before
@@ -695,7 +700,6 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
         f0[i] = ps.intra * (blk == q ? 1.f : pw(lg, d > 0 ? d : 0));
         live[i] = blk == q ? lane : ((rev ? blk > q : blk < q) ? (rev ? 0 : 31) : (rev ? 32 : -1));
       }
-      if (rev) zeros(t, n);
       wait(sc + 8 * grp, (k >> 1) & 1);
       tc_fence_after();
       uint32_t pk[2][16];
@@ -737,20 +741,22 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(pW + 8 * grp);
-      const int tok = token_of(t) + 32 * q;  // of this warp's first row
+      const int tok = token_of(t) + row;  // (reversed: possibly below 0)
+      __nv_bfloat16* go = static_cast<__nv_bfloat16*>(ps.out) + (long long)tok * ps.os[0] + t.b * ps.os[1] +
+                          t.h * ps.os[2] + 32 * g;
       const bool zero_c = ragged(t), counts = rev ? row >= kTC - n : row < n;
       for (int v = 0; v < vts; ++v) {
         const int f = k * vts + v, o = f & 1;
         if (zero_c) {
-          const int cb = cs_buf(f, v);
-          wait(cF + 8 * cb, cs_use(f, k) & 1);
+          const int cb = f % NCS;
+          wait(cF + 8 * cb, (f / NCS) & 1);
           const uint32_t z[4] = {0u, 0u, 0u, 0u};
           for (int e = gt; e < kTC * 8; e += 256)
             if (e / 8 >= n) sts128(sm + C::cs_at(cb) + C::S + blk_at(e / 8, e % 8), z);
           fence_async_smem();
           warp_arrive(cZ + 8 * grp);
         }
-        wait(oD + 8 * o, (f >> 1) & 1);
+        wait(dn + 8 * (f % NCS), (f / NCS) & 1);
         tc_fence_after();
         uint32_t w[16];
         const uint32_t tO = tmem + 256 + o * 128 + lanes + 32 * g;
@@ -771,29 +777,14 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
         }
         tc_fence_before();
         warp_arrive(oR + 8 * o);
-        if (tok >= 0) {
-          if (g == 0 && lane == 0) bulk_wait_read_all();
-          bar_sync(id, 64);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sts128(stg + blk_at(lane, 4 * g + j), w + 4 * j);
-          fence_async_smem();
-          bar_sync(id, 64);
-          if (g == 0 && lane == 0) {
-            tma_store_4d(&m.out[t.job], 64 * v, t.h, t.b, tok, stg);
-            bulk_commit();
-          }
-        } else if (tok + lane >= 0) {  // a store may not begin before token 0
-          __nv_bfloat16* go = static_cast<__nv_bfloat16*>(ps.out) + (long long)(tok + lane) * ps.os[0] +
-                              t.b * ps.os[1] + t.h * ps.os[2] + 64 * v + 32 * g;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(go + 8 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        // 64 bytes of a row per thread (by way of shared memory and TMA stores, with their fence and barriers, an
+        // epilogue took 2,000 cycles)
+        if (tok >= 0 && tok < p.T) {
+          store32(go + 64 * v, w, m.v8);
+          store32(go + 64 * v + 16, w + 8, m.v8);
         }
       }
-      ++k;
     }
-    if (g == 0 && lane == 0) bulk_wait_all();
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -830,7 +821,8 @@ bool encode(CUtensorMap* map, const void* ptr, int rank, const cuuint64_t* dims,
 bool encode_operand(CUtensorMap* map, const void* ptr, const long long (&s)[3], const LinAttnParams& p,
                     int D, uint32_t cols, uint32_t rows, CUtensorMapSwizzle swizzle, int* uh, int* ub) {
   const int nh = s[2] == 0 ? 1 : p.NH, nb = s[1] == 0 ? 1 : p.B;
-  if (uh) *uh = s[2] != 0, *ub = s[1] != 0;
+  *uh = s[2] != 0;
+  *ub = s[1] != 0;
   if (s[0] == 0 && p.T > 1) return false;
   auto bytes = [&](long long e) { return (cuuint64_t)(e == 0 ? D * 2 : e * 2); };
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)nh, (cuuint64_t)nb, (cuuint64_t)p.T};
@@ -853,20 +845,21 @@ int launch_dk(const LinAttnParams& p, cudaStream_t s) {
   const long long outs = (long long)p.npass * p.B * p.NH * nch;
   if (base * p.nseg * (C::TILE / 256) > 0x7fffffffLL || outs * DK > 0x3fffffffLL) return kLinAttnTooWide;
   TcMaps m;
-  bool ok = true;
+  bool ok = true, v8 = true;
   for (int j = 0; j < p.npass; ++j) {
     const LinAttnPass& ps = p.pass[j];
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     ok = ok && encode_operand(&m.x[j], ps.x, ps.xs, p, DK, 64, kTC, sw, &m.xh[j], &m.xb[j]);
     ok = ok && encode_operand(&m.a[j], ps.a, ps.as, p, DK, 64, kTC, sw, &m.ah[j], &m.ab[j]);
     ok = ok && encode_operand(&m.c[j], ps.c, ps.cs, p, p.DV, 64, kTC, sw, &m.ch[j], &m.cb[j]);
-    ok = ok && encode_operand(&m.out[j], ps.out, ps.os, p, p.DV, 64, 32, sw, nullptr, nullptr);
+    const long long a32 = (long long)(reinterpret_cast<uintptr_t>(ps.out) | (uintptr_t)((ps.os[0] | ps.os[1] | ps.os[2]) * 2));
+    v8 = v8 && a32 % 32 == 0;
   }
   const cuuint64_t dims[2] = {(cuuint64_t)p.DV, (cuuint64_t)(outs * DK)};
   const cuuint64_t strides[1] = {(cuuint64_t)p.DV * 2};
-  const cuuint32_t in[2] = {64, (cuuint32_t)DK}, out[2] = {64, 32};
+  const cuuint32_t in[2] = {64, (cuuint32_t)DK};
   ok = ok && encode(&m.s_load, p.chunk_states, 2, dims, strides, in, CU_TENSOR_MAP_SWIZZLE_128B);
-  ok = ok && encode(&m.s_store, p.chunk_states, 2, dims, strides, out, CU_TENSOR_MAP_SWIZZLE_128B);
+  m.v8 = v8;
   if (!ok) return kLinAttnTooWide;
   if (cudaMemsetAsync(p.status, 0, sizeof(int), s) != cudaSuccess) return (int)cudaErrorUnknown;
   if (p.nseg > 1) {
