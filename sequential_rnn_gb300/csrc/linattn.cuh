@@ -72,12 +72,12 @@ __global__ void __launch_bounds__(256)
   *ws = s;
   const long long step = (long long)p.npass * p.B * p.NH * VT * TILE;
   ws += step;
-  for (int k = 0; k < n; k += 8) {  // eight loads in flight
-    float x[8];
+  for (int k = 0; k < n; k += 32) {  // the loads of 32 segments in flight
+    float x[32];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = k + j < n ? ws[(k + j) * step] : 0.f;
+    for (int j = 0; j < 32; ++j) x[j] = k + j < n ? ws[(k + j) * step] : 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 32; ++j) {
       s = fmaf(lam, s, x[j]);
       if (k + j < n) ws[(k + j) * step] = s;
     }

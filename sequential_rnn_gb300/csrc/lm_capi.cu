@@ -157,7 +157,6 @@ int rnn_input_proj_fp8(int32_t M, int32_t N, int32_t K, const void* xq, const fl
   if (!aligned(xq, 16) || !aligned(Wq, 16) || !aligned(y, 16) || !aligned(xs, 4) ||
       !aligned(Ws, 4) || !aligned(bias, 4))
     return RNN_ERR_MISALIGNED;
-  if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return RNN_ERR_LAUNCH;
   ProjFp8Params p{xq, xs, Wq, Ws, bias, y, M, N, K, static_cast<int*>(workspace), kTimeoutNs};
   return map_launch_error(launch_proj_fp8(p, s));
 }

@@ -3,7 +3,7 @@
 //
 //   h = round(x + residual);  r = 1 / sqrt(mean_n h^2 + eps);  y = h r w
 //   8-bit output: per row and block of 128 columns s = max|y| / 448 (1 where
-//   the block is all zero), q = e4m3(y / s)
+//   the block is all zero), q = e4m3(y (1/s))
 //   gradient, xh = h r:  dx = r (w dy - xh mean_n(w dy xh)) + dh,
 //                        dw = sum over rows of dy xh
 //
@@ -93,14 +93,14 @@ __global__ void __launch_bounds__(256) norm_any_kernel(const NormParams p) {
         for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float s = block_scale(top);
         if (lane == 0) p.scale[row * nblk + b] = s;
-        inv = s;
+        inv = 1.f / s;
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int n = b * kBlk + 32 * j + lane;
         if (n >= N) continue;
         if (p.scale)
-          static_cast<uint8_t*>(p.y)[row * N + n] = to_e4m3(y[j] / inv);
+          static_cast<uint8_t*>(p.y)[row * N + n] = to_e4m3(y[j] * inv);
         else
           store1(static_cast<T*>(p.y) + row * N + n, y[j]);
         if (h) store1(h + n, hv[j]);
@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_vec_kernel(const NormP
 #pragma unroll
     for (int o = kBlk / E / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float s = block_scale(top);
+    const float inv = 1.f / s;  // (one division for the block: with one for each value they were half of the time)
     if (v >= nv) continue;
     if (v % (kBlk / E) == 0) p.scale[row * ((p.N + kBlk - 1) / kBlk) + v / (kBlk / E)] = s;
     uint32_t q[E / 4];
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_vec_kernel(const NormP
 #pragma unroll
       for (int k = 0; k < 4; k += 2) {
         const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(
-            make_float2(y[j + k] / s, y[j + k + 1] / s), __NV_SATFINITE, __NV_E4M3);
+            make_float2(y[j + k] * inv, y[j + k + 1] * inv), __NV_SATFINITE, __NV_E4M3);
         u |= (uint32_t)two << (8 * k);
       }
       q[j / 4] = u;
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_vec_kernel(const NormP
 // Gradient: a persistent grid; every thread keeps its columns' share of dw in
 // registers over all of its rows.
 template <class T, int NV, bool WARP>
-__global__ void __launch_bounds__(256) norm_bwd_vec_kernel(const NormBwdParams p) {
+__global__ void __launch_bounds__(256, NV <= 4 ? 2 : 1) norm_bwd_vec_kernel(const NormBwdParams p) {
   constexpr int E = Vec<T>::E;
   __shared__ float red[32];
   const int TPR = WARP ? 32 : blockDim.x;
@@ -369,21 +370,19 @@ __global__ void __launch_bounds__(256) norm_bwd_vec_kernel(const NormBwdParams p
   }
 }
 
-// dw[n] = sum over the partial rows: 32 columns per CTA, eight threads of a column
-// take every eighth row, then meet in a fixed order
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* part, float* dw, int parts, int N) {
-  __shared__ float red[8][32];
+// dw[n] = sum over the partial rows: 32 columns per CTA, the 32 threads of a column take every
+// 32nd row (all their loads in flight at once), then meet in a fixed order
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, float* dw, int parts, int N) {
+  __shared__ float red[32][33];
   const int c = threadIdx.x & 31, k = threadIdx.x >> 5, n = blockIdx.x * 32 + c;
   float s = 0.f;
   if (n < N)
-#pragma unroll 8
-    for (int i = k; i < parts; i += 8) s += part[(long long)i * N + n];
-  red[k][c] = s;
+#pragma unroll 20
+    for (int i = k; i < parts; i += 32) s += part[(long long)i * N + n];
+  red[c][k] = s;
   __syncthreads();
-  if (k != 0 || n >= N) return;
-#pragma unroll
-  for (int i = 1; i < 8; ++i) s += red[i][c];
-  dw[n] = s;
+  s = warp_sum(red[k][c]);
+  if (c == 0 && blockIdx.x * 32 + k < N) dw[blockIdx.x * 32 + k] = s;
 }
 
 // One CTA per 128 x 128 block of W [N, K]; thread t holds column t of the block.
@@ -464,7 +463,7 @@ int norm_bwd_typed(const NormBwdParams& p, cudaStream_t s) {
     else
       norm_bwd_vec_kernel<T, 8, false><<<parts, 256, 0, s>>>(p);
   }
-  if (p.dw) norm_dw_kernel<<<(p.N + 31) / 32, 256, 0, s>>>(p.part, p.dw, parts, p.N);
+  if (p.dw) norm_dw_kernel<<<(p.N + 31) / 32, 1024, 0, s>>>(p.part, p.dw, parts, p.N);
   return (int)cudaGetLastError();
 }
 

@@ -8,13 +8,19 @@
 //
 // A scale changes every 128 of K, so a tile's accumulator cannot stay in tensor
 // memory over the whole sum: each 128-deep block gets a fresh TMEM buffer
-// (four tcgen05.mma of K = 32), which the epilogue warps read, scale and add to
+// (four tcgen05.mma of K = 32), which the promotion warps read, scale and add to
 // the registers that hold the tile, while the MMAs of the next blocks run into
 // the other buffers:
-//   warp 0    TMA producer (one lane) and TMEM owner,
-//   warp 1    MMA issuer (one lane),
-//   warps 2-9 promotion and epilogue, two per 32-lane TMEM quarter, each half
-//             of the tile's columns (one row per thread).
+//   warp 0      TMA producer (one lane) and TMEM owner,
+//   warp 1      MMA issuer (one lane),
+//   warps 2 ..  promotion and epilogue, 64 columns of one row per thread: 16 warps for
+//               128 x 256 tiles, 8 for 128 x 128 ones.
+// A 128 x 256 tile's MMAs read 96 bytes a clock of operands (a 128 x 128 one's the 128 that
+// shared memory gives), and a block's 512 cycles of MMAs cover its promotion; the first two
+// blocks of a tile run during the epilogue of the one before.
+//
+// A few rows (kFewRows at most) are bound by the weights' bytes instead: a kernel of its own reads each
+// weight once, straight into the registers of mma.sync.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -30,18 +36,16 @@ namespace srnn {
 namespace {
 
 constexpr int FBM = 128, FBK = 128;
-constexpr int F_NEPI = 8;
-constexpr int F_THREADS = 32 * (2 + F_NEPI);
 
 template <int BN>
 struct F8Cfg {
   static constexpr uint32_t TILE_A = FBM * FBK, TILE_B = BN * FBK;
   static constexpr uint32_t STAGE = TILE_A + TILE_B;
   static constexpr int NSTG = BN == 256 ? 4 : 6;
-  static constexpr int NACC = 512 / BN;                 // TMEM buffers
-  static constexpr int WCOLS = BN / 2;                  // columns of an epilogue warp
-  static constexpr uint32_t OUT = F_NEPI * 32 * 128;    // 32 rows x 64 bf16 per warp
-  static constexpr uint32_t SMEM = NSTG * STAGE + OUT + 1024 + (2 * NSTG + 2 * NACC) * 8 + 16;
+  static constexpr int NACC = 512 / BN;    // TMEM buffers
+  static constexpr int NPW = BN / 16;      // promotion warps
+  static constexpr int THREADS = 32 * (2 + NPW);
+  static constexpr uint32_t SMEM = NSTG * STAGE + 1024 + (2 * NSTG + 2 * NACC) * 8 + 16;
 };
 
 struct F8Args {
@@ -51,6 +55,8 @@ struct F8Args {
   const float* bias;
   int* status;
   unsigned long long timeout_ns;
+  __nv_bfloat16* y;
+  int v8;  // the output's rows begin at 32-byte boundaries
 };
 
 // Instruction descriptor, kind::f8f6f4: fp32 accumulator, e4m3 A and B, both K-major.
@@ -82,18 +88,17 @@ __device__ __forceinline__ bool wait_f8(uint32_t bar, uint32_t parity, volatile 
 }
 
 template <int BN>
-__global__ void __launch_bounds__(F_THREADS, 1)
+__global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
     proj_fp8_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
-                    const __grid_constant__ CUtensorMap mC, const F8Args g) {
+                    const F8Args g) {
   using C = F8Cfg<BN>;
-  constexpr int NSTG = C::NSTG, NACC = C::NACC, WC = C::WCOLS;
+  constexpr int NSTG = C::NSTG, NACC = C::NACC, WC = 64;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int abort_flag_s, issued_s, consumed_s;
   volatile int* abort_flag = &abort_flag_s;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
-  const uint32_t out_stage = ring + NSTG * C::STAGE;
-  const uint32_t bar_full = out_stage + C::OUT, bar_empty = bar_full + 8 * NSTG;
+  const uint32_t bar_full = ring + NSTG * C::STAGE, bar_empty = bar_full + 8 * NSTG;
   const uint32_t bar_tfull = bar_empty + 8 * NSTG, bar_tempty = bar_tfull + 8 * NACC;
   const uint32_t tslot = bar_tempty + 8 * NACC;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -107,7 +112,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     }
     for (int a = 0; a < NACC; ++a) {
       mbar_init(bar_tfull + 8 * a, 1);
-      mbar_init(bar_tempty + 8 * a, F_NEPI);
+      mbar_init(bar_tempty + 8 * a, C::NPW);
     }
     abort_flag_s = 0;
     issued_s = 0;
@@ -180,22 +185,23 @@ __global__ void __launch_bounds__(F_THREADS, 1)
   } else {
     // --------------------------------------------- promotion and epilogue --
     const int q = warp & 3;          // TMEM lane quarter this warp may access
-    const int hc = (warp - 2) >> 2;  // column half of the tile
-    const uint32_t stg = out_stage + (uint32_t)(warp - 2) * 4096;
+    const int hc = (warp - 2) >> 2;  // columns 64 hc .. of the tile
     int it = 0;
     bool stop = false;
     for (int u = blockIdx.x; u < ntiles && !stop; u += gridDim.x) {
       const int m0 = (u / g.tiles_n) * FBM + q * 32, n0 = (u % g.tiles_n) * BN + hc * WC;
-      const int row = m0 + lane < g.M ? m0 + lane : g.M - 1;
-      const float* xs = g.xs + (long long)row * g.nkb;
-      const int nb = (n0 < g.N ? n0 : g.N - 1) / 128;
-      const float* ws = g.Ws + (long long)nb * g.nkb;
+      const bool row_ok = m0 + lane < g.M;
+      const long long row = row_ok ? m0 + lane : g.M - 1;
+      const float* xs = g.xs + row * g.nkb;
+      const float* ws = g.Ws + (long long)((n0 < g.N ? n0 : g.N - 1) / 128) * g.nkb;
       float acc[WC];
 #pragma unroll
       for (int j = 0; j < WC; ++j) acc[j] = 0.f;
+      float sc = __ldg(xs) * __ldg(ws);
       for (int kb = 0; kb < g.nkb; ++kb, ++it) {
         const int a = it % NACC, pa = it / NACC;
-        const float sc = __ldg(xs + kb) * __ldg(ws + kb);
+        const int kn = kb + 1 < g.nkb ? kb + 1 : kb;
+        const float x1 = __ldg(xs + kn), w1 = __ldg(ws + kn);  // the next block's scales on their way
         if (!wait_f8(bar_tfull + 8 * a, pa & 1, abort_flag, g.status, tlim)) {
           stop = true;
           break;
@@ -203,52 +209,49 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         tc_fence_after();
         const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * BN + hc * WC);
 #pragma unroll
-        for (int c = 0; c < WC / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld32(t + 32 * c, r);
+        for (int c = 0; c < WC; c += 16) {
+          uint32_t r[16];
+          tmem_ld16(t + c, r);
           tmem_wait_ld();
-          tmem_reg_fence(r);
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            acc[32 * c + j] = fmaf(sc, __uint_as_float(r[j]), acc[32 * c + j]);
+          for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(r[j]));
+          if (c + 16 == WC) {  // the buffer has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_tempty + 8 * a);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(sc, __uint_as_float(r[j]), acc[c + j]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_tempty + 8 * a);
+        sc = x1 * w1;
       }
       if (stop) break;
-      // 64 columns at a time: bf16 (+ bias) into the warp's 128-byte swizzled box, TMA store
+      // bf16 (+ bias), 128 bytes of a row per thread
+      __nv_bfloat16* y = g.y + row * g.N + n0;
 #pragma unroll
-      for (int b = 0; b < WC / 64; ++b) {
-        if (lane == 0) bulk_wait_read_all();
-        __syncwarp();
+      for (int c = 0; c < WC; c += 16) {
+        uint32_t pk[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint32_t pk[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int c = 64 * b + 8 * k + 2 * j, n = n0 + c;
-            float b0 = 0.f, b1 = 0.f;
-            if (g.bias) {
-              b0 = n < g.N ? __ldg(g.bias + n) : 0.f;
-              b1 = n + 1 < g.N ? __ldg(g.bias + n + 1) : 0.f;
-            }
-            pk[j] = pack_bf16x2(acc[c] + b0, acc[c + 1] + b1);
+        for (int j = 0; j < 16; j += 4) {
+          float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (g.bias && n0 + c + j < g.N) {  // (N is a multiple of 8, the pointer of 4 bytes)
+            b.x = __ldg(g.bias + n0 + c + j), b.y = __ldg(g.bias + n0 + c + j + 1);
+            b.z = __ldg(g.bias + n0 + c + j + 2), b.w = __ldg(g.bias + n0 + c + j + 3);
           }
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
-                           stg + (uint32_t)lane * 128 + (uint32_t)((k ^ (lane & 7)) * 16)),
-                       "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
-                       : "memory");
+          pk[j / 2] = pack_bf16x2(acc[c + j] + b.x, acc[c + j + 1] + b.y);
+          pk[j / 2 + 1] = pack_bf16x2(acc[c + j + 2] + b.z, acc[c + j + 3] + b.w);
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          if (n0 + 64 * b < g.N && m0 < g.M) tma_store_2d(&mC, n0 + 64 * b, m0, stg);
-          bulk_commit();
+        if (!row_ok) continue;
+        if (g.v8 && n0 + c + 16 <= g.N) {
+          asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(y + c), "r"(pk[0]),
+                       "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]), "r"(pk[7])
+                       : "memory");
+        } else {
+          if (n0 + c < g.N) *reinterpret_cast<uint4*>(y + c) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          if (n0 + c + 8 < g.N) *reinterpret_cast<uint4*>(y + c + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
         }
       }
     }
-    if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -268,6 +271,94 @@ __global__ void __launch_bounds__(F_THREADS, 1)
   }
 }
 
+// ------------------------------------------------------------- few rows --
+constexpr int kFewRows = 64;
+constexpr int kFewWarps = 8;
+
+__device__ __forceinline__ void mma_e4m3_16832(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 16 weight rows (the MMA's M) x up to 8 NT tokens (its N) per CTA; the blocks of 128 go round
+// the CTA's warps, whose sums meet in shared memory in a fixed order.  A thread's 16-byte loads
+// take 32 consecutive k of a row: which k an MMA's operand slots stand for is free, as long as A's and
+// B's agree, so the four MMAs of a block take them in the order in which they were loaded.
+template <int NT>
+__global__ void __launch_bounds__(32 * kFewWarps)
+    proj_fp8_few_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ xs,
+                        const uint8_t* __restrict__ Wq, const float* __restrict__ Ws,
+                        const float* __restrict__ bias, __nv_bfloat16* __restrict__ y, int M, int N, int K,
+                        int* status) {
+  __shared__ float part[kFewWarps][8 * NT][17];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * 16, nkb = (K + FBK - 1) / FBK;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;  // no waits here: nothing to report
+  const uint8_t* w0 = Wq + (long long)(n0 + g) * K + t * 32;
+  const uint8_t* w1 = w0 + 8LL * K;
+  const bool has0 = n0 + g < N, has1 = n0 + g + 8 < N;
+  const float* ws = Ws + (long long)(n0 / 128) * nkb;
+  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+  float acc[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 2
+  for (int kb = warp; kb < nkb; kb += kFewWarps) {
+    const int k = kb * FBK;
+    uint4 a[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = k + t * 32 + 16 * h < K;
+      a[0][h] = in && has0 ? __ldg(reinterpret_cast<const uint4*>(w0 + k) + h) : z;
+      a[1][h] = in && has1 ? __ldg(reinterpret_cast<const uint4*>(w1 + k) + h) : z;
+    }
+    const float w = __ldg(ws + kb);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int m = 8 * i + g;
+      uint4 b[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        b[h] = m < M && k + t * 32 + 16 * h < K
+                   ? __ldg(reinterpret_cast<const uint4*>(xq + (long long)m * K + t * 32 + k) + h)
+                   : z;
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t a0[4] = {a[0][h].x, a[1][h].x, a[0][h].y, a[1][h].y};
+        const uint32_t a1[4] = {a[0][h].z, a[1][h].z, a[0][h].w, a[1][h].w};
+        mma_e4m3_16832(d, a0, b[h].x, b[h].y);
+        mma_e4m3_16832(d, a1, b[h].z, b[h].w);
+      }
+      const int c = 8 * i + 2 * t;  // this thread's two tokens
+      const float s0 = c < M ? w * __ldg(xs + (long long)c * nkb + kb) : 0.f;
+      const float s1 = c + 1 < M ? w * __ldg(xs + (long long)(c + 1) * nkb + kb) : 0.f;
+      acc[i][0] = fmaf(s0, d[0], acc[i][0]);
+      acc[i][1] = fmaf(s1, d[1], acc[i][1]);
+      acc[i][2] = fmaf(s0, d[2], acc[i][2]);
+      acc[i][3] = fmaf(s1, d[3], acc[i][3]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[warp][8 * i + 2 * t + (j & 1)][g + 8 * (j >> 1)] = acc[i][j];
+  __syncthreads();
+  for (int e = threadIdx.x; e < 8 * NT * 16; e += 32 * kFewWarps) {
+    const int m = e / 16, n = e % 16;
+    if (m >= M || n0 + n >= N) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < kFewWarps; ++k) s += part[k][m][n];
+    y[(long long)m * N + n0 + n] = __float2bfloat16_rn(s + (bias ? __ldg(bias + n0 + n) : 0.f));
+  }
+}
+
 }  // namespace
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -275,8 +366,6 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn encode_fn();  // tc_gemm.cu
-int make_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t pitch,
-             uint32_t bx, uint32_t by);
 
 namespace {
 
@@ -299,7 +388,7 @@ int launch_bn(const ProjFp8Params& p, cudaStream_t s) {
   using C = F8Cfg<BN>;
   auto kern = proj_fp8_kernel<BN>;
   static int prepared[64][5];
-  int e = prepare_launch(prepared, kern, C::SMEM, F_THREADS, 1);
+  int e = prepare_launch(prepared, kern, C::SMEM, C::THREADS, 1);
   if (e != 0) return e;
   F8Args g{};
   g.M = p.M;
@@ -315,18 +404,36 @@ int launch_bn(const ProjFp8Params& p, cudaStream_t s) {
   const long long tiles = (long long)g.tiles_m * g.tiles_n;
   // ring positions are counted in 32 bits
   if (tiles * g.nkb > 0x3fffffffLL) return (int)cudaErrorInvalidValue;
-  CUtensorMap a, b, c;
+  g.y = static_cast<__nv_bfloat16*>(p.y);
+  g.v8 = p.N % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 32 == 0;
+  CUtensorMap a, b;
   if ((e = make_map8(&a, p.xq, (uint64_t)p.M, (uint64_t)p.K, FBM))) return e;
   if ((e = make_map8(&b, p.Wq, (uint64_t)p.N, (uint64_t)p.K, BN))) return e;
-  if ((e = make_map(&c, p.y, (uint64_t)p.M, (uint64_t)p.N, (uint64_t)p.N, 64, 32))) return e;
   const int cap = sm_count();
   const int grid = (int)(tiles < cap ? tiles : cap);
-  kern<<<grid, F_THREADS, C::SMEM, s>>>(a, b, c, g);
+  if (cudaMemsetAsync(p.status, 0, sizeof(int), s) != cudaSuccess) return (int)cudaErrorUnknown;
+  kern<<<grid, C::THREADS, C::SMEM, s>>>(a, b, g);
   return (int)cudaGetLastError();
 }
 
 }  // namespace
 
-int launch_proj_fp8(const ProjFp8Params& p, cudaStream_t s) { return launch_bn<128>(p, s); }
+template <int NT>
+static int launch_few(const ProjFp8Params& p, cudaStream_t s) {
+  proj_fp8_few_kernel<NT><<<(unsigned)((p.N + 15) / 16), 32 * kFewWarps, 0, s>>>(
+      static_cast<const uint8_t*>(p.xq), p.xs, static_cast<const uint8_t*>(p.Wq), p.Ws, p.bias,
+      static_cast<__nv_bfloat16*>(p.y), p.M, p.N, p.K, p.status);
+  return (int)cudaGetLastError();
+}
+
+int launch_proj_fp8(const ProjFp8Params& p, cudaStream_t s) {
+  if (p.M <= 8) return launch_few<1>(p, s);
+  if (p.M <= 16) return launch_few<2>(p, s);
+  if (p.M <= 32) return launch_few<4>(p, s);
+  if (p.M <= kFewRows) return launch_few<8>(p, s);
+  // the larger tiles where they are enough for every SM
+  const long long wide = (long long)((p.M + FBM - 1) / FBM) * ((p.N + 255) / 256);
+  return wide >= sm_count() ? launch_bn<256>(p, s) : launch_bn<128>(p, s);
+}
 
 }  // namespace srnn
