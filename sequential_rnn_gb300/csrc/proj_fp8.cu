@@ -11,13 +11,15 @@
 // (four tcgen05.mma of K = 32), which the promotion warps read, scale and add to
 // the registers that hold the tile, while the MMAs of the next blocks run into
 // the other buffers:
-//   warp 0      TMA producer (one lane) and TMEM owner,
-//   warp 1      MMA issuer (one lane),
-//   warps 2 ..  promotion and epilogue, 64 columns of one row per thread: 16 warps for
-//               128 x 256 tiles, 8 for 128 x 128 ones.
+//   warp 0       TMA producer (one lane) and TMEM owner,
+//   warps 1, 2   MMA issuers (one lane each), every other block: what one of them spends on its
+//                waits and commits (600 cycles a block) passes while the other's MMAs run,
+//   warps 4-19   promotion and epilogue, a row and a quarter of the tile's columns per
+//                thread; setmaxnreg moves registers to them from the first four.
 // A 128 x 256 tile's MMAs read 96 bytes a clock of operands (a 128 x 128 one's the 128 that
-// shared memory gives), and a block's 512 cycles of MMAs cover its promotion; the first two
-// blocks of a tile run during the epilogue of the one before.
+// shared memory gives), and a block's 512 cycles of MMAs cover its promotion; the first
+// blocks of a tile run during the epilogue of the one before.  The outputs leave by way of shared memory and
+// TMA stores (stored straight from registers, an epilogue took 6,200 cycles).
 //
 // A few rows (kFewRows at most) are bound by the weights' bytes instead: a kernel of its own reads each
 // weight once, straight into the registers of mma.sync.
@@ -41,11 +43,13 @@ template <int BN>
 struct F8Cfg {
   static constexpr uint32_t TILE_A = FBM * FBK, TILE_B = BN * FBK;
   static constexpr uint32_t STAGE = TILE_A + TILE_B;
-  static constexpr int NSTG = BN == 256 ? 4 : 6;
-  static constexpr int NACC = 512 / BN;    // TMEM buffers
-  static constexpr int NPW = BN / 16;      // promotion warps
-  static constexpr int THREADS = 32 * (2 + NPW);
-  static constexpr uint32_t SMEM = NSTG * STAGE + 1024 + (2 * NSTG + 2 * NACC) * 8 + 16;
+  static constexpr int NSTG = BN == 256 ? 3 : 4;
+  static constexpr int NACC = BN == 256 ? 2 : 4;  // TMEM buffers (at most NSTG, see `done`)
+  static constexpr int WC = BN / 4;               // columns of a promotion warp
+  static constexpr int NPW = 16;                  // promotion warps
+  static constexpr int THREADS = 32 * (4 + NPW);
+  static constexpr uint32_t STG = 32 * WC * 2;    // outputs on their way, per warp
+  static constexpr uint32_t SMEM = NSTG * STAGE + NPW * STG + 1024 + (2 * NSTG + NACC) * 8 + 16;
 };
 
 struct F8Args {
@@ -55,8 +59,6 @@ struct F8Args {
   const float* bias;
   int* status;
   unsigned long long timeout_ns;
-  __nv_bfloat16* y;
-  int v8;  // the output's rows begin at 32-byte boundaries
 };
 
 // Instruction descriptor, kind::f8f6f4: fp32 accumulator, e4m3 A and B, both K-major.
@@ -90,17 +92,18 @@ __device__ __forceinline__ bool wait_f8(uint32_t bar, uint32_t parity, volatile 
 template <int BN>
 __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
     proj_fp8_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
-                    const F8Args g) {
+                    const __grid_constant__ CUtensorMap mC, const F8Args g) {
   using C = F8Cfg<BN>;
-  constexpr int NSTG = C::NSTG, NACC = C::NACC, WC = 64;
+  constexpr int NSTG = C::NSTG, NACC = C::NACC, WC = C::WC;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ int abort_flag_s, issued_s, consumed_s;
+  __shared__ int abort_flag_s, issued_s;
   volatile int* abort_flag = &abort_flag_s;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
-  const uint32_t bar_full = ring + NSTG * C::STAGE, bar_empty = bar_full + 8 * NSTG;
-  const uint32_t bar_tfull = bar_empty + 8 * NSTG, bar_tempty = bar_tfull + 8 * NACC;
-  const uint32_t tslot = bar_tempty + 8 * NACC;
+  const uint32_t out_stage = ring + NSTG * C::STAGE;
+  // `done`: a block's MMAs are complete, so its stage is free and its sums can be promoted
+  const uint32_t bar_full = out_stage + C::NPW * C::STG, bar_done = bar_full + 8 * NSTG;
+  const uint32_t bar_read = bar_done + 8 * NSTG, tslot = bar_read + 8 * NACC;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ntiles = g.tiles_m * g.tiles_n;
   const unsigned long long tlim = g.timeout_ns;
@@ -108,15 +111,11 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
   if (threadIdx.x == 32) {
     for (int s = 0; s < NSTG; ++s) {
       mbar_init(bar_full + 8 * s, 1);
-      mbar_init(bar_empty + 8 * s, 1);
+      mbar_init(bar_done + 8 * s, 1);
     }
-    for (int a = 0; a < NACC; ++a) {
-      mbar_init(bar_tfull + 8 * a, 1);
-      mbar_init(bar_tempty + 8 * a, C::NPW);
-    }
+    for (int a = 0; a < NACC; ++a) mbar_init(bar_read + 8 * a, C::NPW);
     abort_flag_s = 0;
     issued_s = 0;
-    consumed_s = 0;
     fence_mbar_init();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -129,46 +128,43 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
   tc_fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tslot) : "memory");
+  const int mine = (ntiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // this CTA's tiles
+  const int blocks = mine * g.nkb;
 
-  if (warp == 0) {
-    // ------------------------------------------------------ TMA producer --
-    if (lane == 0) {
-      tma_prefetch_map(&mA);
-      tma_prefetch_map(&mB);
-      int it = 0;
-      bool stop = false;
-      for (int u = blockIdx.x; u < ntiles && !stop; u += gridDim.x) {
-        const int m0 = (u / g.tiles_n) * FBM, n0 = (u % g.tiles_n) * BN;
-        for (int kb = 0; kb < g.nkb; ++kb, ++it) {
-          const int s = it % NSTG, ph = it / NSTG;
-          if (it >= NSTG &&
-              !wait_f8(bar_empty + 8 * s, (ph - 1) & 1, abort_flag, g.status, tlim)) {
-            stop = true;
-            break;
+  // 640 threads x 96 registers at the launch: 128 x 24 + 512 x 112 are less
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
+    if (warp == 0) {
+      // ---------------------------------------------------- TMA producer --
+      if (lane == 0) {
+        tma_prefetch_map(&mA);
+        tma_prefetch_map(&mB);
+        int it = 0;
+        bool stop = false;
+        for (int u = blockIdx.x; u < ntiles && !stop; u += gridDim.x) {
+          const int m0 = (u / g.tiles_n) * FBM, n0 = (u % g.tiles_n) * BN;
+          for (int kb = 0; kb < g.nkb; ++kb, ++it) {
+            const int s = it % NSTG, ph = it / NSTG;
+            if (it >= NSTG && !wait_f8(bar_done + 8 * s, (ph - 1) & 1, abort_flag, g.status, tlim)) {
+              stop = true;
+              break;
+            }
+            const uint32_t sA = ring + s * C::STAGE, sB = sA + C::TILE_A, fb = bar_full + 8 * s;
+            mbar_arrive_expect_tx(fb, C::STAGE);
+            tma_load_2d(sA, &mA, kb * FBK, m0, fb);
+            tma_load_2d(sB, &mB, kb * FBK, n0, fb);
           }
-          const uint32_t sA = ring + s * C::STAGE, sB = sA + C::TILE_A, fb = bar_full + 8 * s;
-          mbar_arrive_expect_tx(fb, C::STAGE);
-          tma_load_2d(sA, &mA, kb * FBK, m0, fb);
-          tma_load_2d(sB, &mB, kb * FBK, n0, fb);
         }
+        issued_s = it;
       }
-      issued_s = it;
-    }
-  } else if (warp == 1) {
-    // -------------------------------------------------------- MMA issuer --
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3_f32(FBM, BN);
-      int it = 0;
-      bool stop = false;
-      for (int u = blockIdx.x; u < ntiles && !stop; u += gridDim.x) {
-        for (int kb = 0; kb < g.nkb; ++kb, ++it) {
-          const int s = it % NSTG, ph = it / NSTG, a = it % NACC, pa = it / NACC;
-          if (!wait_f8(bar_full + 8 * s, ph & 1, abort_flag, g.status, tlim) ||
-              (it >= NACC &&
-               !wait_f8(bar_tempty + 8 * a, (pa - 1) & 1, abort_flag, g.status, tlim))) {
-            stop = true;
-            break;
-          }
+    } else if (warp < 3) {
+      // ------------------------------------------------------ MMA issuers --
+      if (lane == 0) {
+        constexpr uint32_t idesc = idesc_e4m3_f32(FBM, BN);
+        for (int it = warp - 1; it < blocks; it += 2) {
+          const int s = it % NSTG, a = it % NACC;
+          if (!wait_f8(bar_full + 8 * s, (it / NSTG) & 1, abort_flag, g.status, tlim)) break;
+          if (it >= NACC && !wait_f8(bar_read + 8 * a, ((it - NACC) / NACC) & 1, abort_flag, g.status, tlim)) break;
           tc_fence_after();
           const uint32_t sA = ring + s * C::STAGE, sB = sA + C::TILE_A;
           const uint32_t dacc = tmem + (uint32_t)(a * BN);
@@ -176,22 +172,22 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
           for (int k4 = 0; k4 < FBK / 32; ++k4)  // 32 bytes along the K-major rows
             umma_f8(dacc, sdesc_sw128(sA + k4 * 32, 16, 1024), sdesc_sw128(sB + k4 * 32, 16, 1024),
                     idesc, k4 != 0 ? 1u : 0u);
-          umma_commit(bar_empty + 8 * s);
-          umma_commit(bar_tfull + 8 * a);
+          umma_commit(bar_done + 8 * s);
         }
       }
-      consumed_s = it;
     }
+    __syncwarp();
   } else {
     // --------------------------------------------- promotion and epilogue --
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
     const int q = warp & 3;          // TMEM lane quarter this warp may access
-    const int hc = (warp - 2) >> 2;  // columns 64 hc .. of the tile
+    const int hc = (warp - 4) >> 2;  // columns WC hc .. of the tile
+    const uint32_t stg = out_stage + (uint32_t)(warp - 4) * C::STG;
     int it = 0;
     bool stop = false;
     for (int u = blockIdx.x; u < ntiles && !stop; u += gridDim.x) {
       const int m0 = (u / g.tiles_n) * FBM + q * 32, n0 = (u % g.tiles_n) * BN + hc * WC;
-      const bool row_ok = m0 + lane < g.M;
-      const long long row = row_ok ? m0 + lane : g.M - 1;
+      const long long row = m0 + lane < g.M ? m0 + lane : g.M - 1;
       const float* xs = g.xs + row * g.nkb;
       const float* ws = g.Ws + (long long)((n0 < g.N ? n0 : g.N - 1) / 128) * g.nkb;
       float acc[WC];
@@ -199,67 +195,67 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
       for (int j = 0; j < WC; ++j) acc[j] = 0.f;
       float sc = __ldg(xs) * __ldg(ws);
       for (int kb = 0; kb < g.nkb; ++kb, ++it) {
-        const int a = it % NACC, pa = it / NACC;
+        const int a = it % NACC;
         const int kn = kb + 1 < g.nkb ? kb + 1 : kb;
         const float x1 = __ldg(xs + kn), w1 = __ldg(ws + kn);  // the next block's scales on their way
-        if (!wait_f8(bar_tfull + 8 * a, pa & 1, abort_flag, g.status, tlim)) {
+        if (!wait_f8(bar_done + 8 * (it % NSTG), (it / NSTG) & 1, abort_flag, g.status, tlim)) {
           stop = true;
           break;
         }
         tc_fence_after();
         const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * BN + hc * WC);
 #pragma unroll
-        for (int c = 0; c < WC; c += 16) {
-          uint32_t r[16];
-          tmem_ld16(t + c, r);
+        for (int c = 0; c < WC; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(t + c, r);
           tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(r[j]));
-          if (c + 16 == WC) {  // the buffer has been read
+          tmem_reg_fence(r);
+          if (c + 32 == WC) {  // the buffer has been read
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_tempty + 8 * a);
+            if (lane == 0) mbar_arrive(bar_read + 8 * a);
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(sc, __uint_as_float(r[j]), acc[c + j]);
+          for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(sc, __uint_as_float(r[j]), acc[c + j]);
         }
         sc = x1 * w1;
       }
       if (stop) break;
-      // bf16 (+ bias), 128 bytes of a row per thread
-      __nv_bfloat16* y = g.y + row * g.N + n0;
+      // bf16 (+ bias) into the warp's swizzled box of 32 rows, TMA store
+      if (lane == 0) bulk_wait_read_all();
+      __syncwarp();
 #pragma unroll
-      for (int c = 0; c < WC; c += 16) {
-        uint32_t pk[8];
+      for (int k = 0; k < WC / 8; ++k) {
+        uint32_t pk[4];
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (g.bias && n0 + c + j < g.N) {  // (N is a multiple of 8, the pointer of 4 bytes)
-            b.x = __ldg(g.bias + n0 + c + j), b.y = __ldg(g.bias + n0 + c + j + 1);
-            b.z = __ldg(g.bias + n0 + c + j + 2), b.w = __ldg(g.bias + n0 + c + j + 3);
-          }
-          pk[j / 2] = pack_bf16x2(acc[c + j] + b.x, acc[c + j + 1] + b.y);
-          pk[j / 2 + 1] = pack_bf16x2(acc[c + j + 2] + b.z, acc[c + j + 3] + b.w);
+        for (int j = 0; j < 4; ++j) {
+          const int c = 8 * k + 2 * j, n = n0 + c;
+          float b0 = 0.f, b1 = 0.f;
+          if (g.bias && n < g.N) b0 = __ldg(g.bias + n), b1 = __ldg(g.bias + n + 1);  // (N is even)
+          pk[j] = pack_bf16x2(acc[c] + b0, acc[c + 1] + b1);
         }
-        if (!row_ok) continue;
-        if (g.v8 && n0 + c + 16 <= g.N) {
-          asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(y + c), "r"(pk[0]),
-                       "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]), "r"(pk[7])
-                       : "memory");
-        } else {
-          if (n0 + c < g.N) *reinterpret_cast<uint4*>(y + c) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          if (n0 + c + 8 < g.N) *reinterpret_cast<uint4*>(y + c + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-        }
+        const int ch = k ^ (WC == 64 ? lane & 7 : (lane >> 1) & 3);
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(stg + (uint32_t)(lane * WC * 2 + ch * 16)),
+                     "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
+                     : "memory");
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        if (n0 < g.N && m0 < g.M) tma_store_2d(&mC, n0, m0, stg);
+        bulk_commit();
       }
     }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
 
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     if (lane == 0 && *abort_flag) {
-      // let TMA copies that were issued but never consumed land before exit
-      for (int k = consumed_s; k < issued_s; ++k) {
+      // let TMA copies that were issued land before exit
+      for (int k = issued_s - NSTG < 0 ? 0 : issued_s - NSTG; k < issued_s; ++k) {
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(bar_full + 8 * (k % NSTG), (k / NSTG) & 1))
           if (globaltimer_ns() - t0 > 10000000ull) break;
@@ -369,17 +365,18 @@ EncodeTiledFn encode_fn();  // tc_gemm.cu
 
 namespace {
 
-// 8-bit row-major [rows, cols]; box of 128 columns x by rows, 128-byte swizzle
-int make_map8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t by) {
+// row-major [rows, cols] of `bytes`-byte values; box of bx columns x by rows
+int make_map2(CUtensorMap* m, CUtensorMapDataType type, int bytes, const void* ptr, uint64_t rows, uint64_t cols,
+              uint32_t bx, uint32_t by, CUtensorMapSwizzle swizzle) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return (int)cudaErrorNotSupported;
   const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols};
-  const cuuint32_t box[2] = {FBK, by};
+  const cuuint64_t strides[1] = {cols * bytes};
+  const cuuint32_t box[2] = {bx, by};
   const cuuint32_t es[2] = {1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides,
-                        box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = fn(m, type, 2, const_cast<void*>(ptr), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? 0 : (int)cudaErrorInvalidValue;
 }
 
@@ -404,15 +401,20 @@ int launch_bn(const ProjFp8Params& p, cudaStream_t s) {
   const long long tiles = (long long)g.tiles_m * g.tiles_n;
   // ring positions are counted in 32 bits
   if (tiles * g.nkb > 0x3fffffffLL) return (int)cudaErrorInvalidValue;
-  g.y = static_cast<__nv_bfloat16*>(p.y);
-  g.v8 = p.N % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 32 == 0;
-  CUtensorMap a, b;
-  if ((e = make_map8(&a, p.xq, (uint64_t)p.M, (uint64_t)p.K, FBM))) return e;
-  if ((e = make_map8(&b, p.Wq, (uint64_t)p.N, (uint64_t)p.K, BN))) return e;
+  CUtensorMap a, b, c;
+  if ((e = make_map2(&a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.xq, (uint64_t)p.M, (uint64_t)p.K, FBK, FBM,
+                     CU_TENSOR_MAP_SWIZZLE_128B)))
+    return e;
+  if ((e = make_map2(&b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.Wq, (uint64_t)p.N, (uint64_t)p.K, FBK, BN,
+                     CU_TENSOR_MAP_SWIZZLE_128B)))
+    return e;
+  if ((e = make_map2(&c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.y, (uint64_t)p.M, (uint64_t)p.N, C::WC, 32,
+                     C::WC == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)))
+    return e;
   const int cap = sm_count();
   const int grid = (int)(tiles < cap ? tiles : cap);
   if (cudaMemsetAsync(p.status, 0, sizeof(int), s) != cudaSuccess) return (int)cudaErrorUnknown;
-  kern<<<grid, C::THREADS, C::SMEM, s>>>(a, b, g);
+  kern<<<grid, C::THREADS, C::SMEM, s>>>(a, b, c, g);
   return (int)cudaGetLastError();
 }
 
