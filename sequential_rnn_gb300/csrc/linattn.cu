@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
   if (STATE_ONLY && (long long)c1 * kC >= len) return;  // no later segment starts from it
   const float lg = p.log_decay[w.h] * 1.4426950408889634f;
   const bool rev = ps.reverse != 0;
-  if (!STATE_ONLY && blockIdx.x == 0 && tid == 0 && p.status) *p.status = 0;
+  if (!STATE_ONLY && blockIdx.x == 0 && tid == 0 && p.clear) *p.status = 0;
 
   const __nv_bfloat16* gx = static_cast<const __nv_bfloat16*>(ps.x) + w.b * ps.xs[1] + w.h * ps.xs[2];
   const __nv_bfloat16* ga = static_cast<const __nv_bfloat16*>(ps.a) + w.b * ps.as[1] + w.h * ps.as[2];

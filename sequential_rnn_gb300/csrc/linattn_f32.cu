@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kT32)
   if (STATE_ONLY && (long long)c1 * kC32 >= len) return;
   const float lg = p.log_decay[w.h] * 1.4426950408889634f;
   const bool rev = ps.reverse != 0;
-  if (!STATE_ONLY && blockIdx.x == 0 && tid == 0 && p.status) *p.status = 0;
+  if (!STATE_ONLY && blockIdx.x == 0 && tid == 0 && p.clear) *p.status = 0;
   const float* gx = static_cast<const float*>(ps.x) + w.b * ps.xs[1] + w.h * ps.xs[2];
   const float* ga = static_cast<const float*>(ps.a) + w.b * ps.as[1] + w.h * ps.as[2];
   const float* gc = static_cast<const float*>(ps.c) + w.b * ps.cs[1] + w.h * ps.cs[2] + w.vt * kV32;

@@ -6,8 +6,12 @@ namespace srnn {
 
 LinAttnPlan linattn_plan(bool bf16, int npass, int T, int B, int NH, int DK, int DV) {
   LinAttnPlan pl{};
-  pl.path = !bf16 ? kLinAttnF32
-                  : (DK % 64 == 0 && DV % 64 == 0 && T > 128 ? kLinAttnTc : kLinAttnMma);
+  // tcgen05 from the lengths on where it is the faster (us, 8 rows unless said; mma.sync / tcgen05): 6 x 128,
+  // T = 128 13.5 / 17.0, T = 256 21.5 / 18.8, 16 rows of 1024 108 / 63; 4 x 256, T = 256 29.9 / 29.3, 4 rows of 4096 370 /
+  // 98.  With 64 columns of x and a, whose products are small, the gradient's passes gain on long rows only
+  // (16 rows of 1024 104 / 113, 4 rows of 4096 154 / 123), the forward's does not (1 row of 4096 24.8 / 34.1).
+  const bool tc = DK % 64 == 0 && DV % 64 == 0 && (DK == 64 ? npass > 1 && T >= 2048 : T >= 256);
+  pl.path = !bf16 ? kLinAttnF32 : (tc ? kLinAttnTc : kLinAttnMma);
   int chunk, tiles, occ;  // tokens per chunk, state tiles per head, CTAs per SM
   if (pl.path == kLinAttnTc) {
     chunk = 128;

@@ -43,14 +43,13 @@ namespace {
 constexpr int kTC = 128;                  // tokens per chunk
 constexpr uint32_t kBlkBytes = kTC * 128; // 128 rows x 64 columns
 
-// tensor maps: x, a, c of each pass [T, B, NH, D]; chunk states as rows of DV
+// tensor maps: x, a, c, out of each pass [T, B, NH, D]; chunk states as rows of DV
 struct TcMaps {
-  CUtensorMap x[kLinAttnPasses], a[kLinAttnPasses], c[kLinAttnPasses];
+  CUtensorMap x[kLinAttnPasses], a[kLinAttnPasses], c[kLinAttnPasses], out[kLinAttnPasses];
   CUtensorMap s_load;
   // 0 where the operand is shared by all heads / rows (its map has one)
   int xh[kLinAttnPasses], xb[kLinAttnPasses], ah[kLinAttnPasses], ab[kLinAttnPasses];
   int ch[kLinAttnPasses], cb[kLinAttnPasses];
-  int v8;  // the outputs' rows begin at 32-byte boundaries
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
@@ -59,6 +58,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                             uint32_t src) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
       : "memory");
 }
 // 32 bytes to global memory (v8: at a 32-byte boundary, one access)
@@ -437,11 +444,11 @@ struct OutCfg {
   static constexpr uint32_t X = (DK / 64) * kBlkBytes;
   static constexpr int NX = DK == 64 ? 3 : (DK == 128 ? 2 : 1);  // tiles of x and a
   static constexpr uint32_t S = DK * 128;                // DK rows x 64 columns of the state
-  static constexpr int NCS = DK == 256 ? 2 : 3;          // c and state tiles of 64 columns
+  static constexpr int NCS = DK == 64 ? 3 : 2;           // c and state tiles of 64 columns
   static constexpr uint32_t CS = kBlkBytes + S;
   // with 256 columns the second of them lies in a's place, free after the scores
-  static constexpr uint32_t sCS = NX * 2 * X;
-  static constexpr uint32_t SMEM = sCS + (DK == 256 ? 1 : NCS) * CS + 1024;
+  static constexpr uint32_t sCS = NX * 2 * X, sO = sCS + (DK == 256 ? 1 : NCS) * CS;
+  static constexpr uint32_t SMEM = sO + 8 * 4096 + 1024;  // outputs on their way: 32 rows x 64 columns for two warps
   static __device__ __forceinline__ uint32_t cs_at(int buf) { return DK == 256 && buf == 1 ? X : sCS + buf * CS; }
 };
 
@@ -480,13 +487,17 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int abort_flag_s;
   __shared__ uint32_t tslot_s;
-  __shared__ __align__(8) uint64_t bars_s[17];
+  __shared__ __align__(8) uint64_t bars_s[27];
   __shared__ OutTile info_s[4];  // what the loading warp tells the others of its tiles, the last four
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bar = smem_u32(bars_s);
   // x, a landed; c, state landed; MMAs done, by buffer of c and state; scores done; scores in
-  // bf16; sums read; c's rows behind the last token zeroed
-  const uint32_t xF = bar, cF = bar + 24, dn = bar + 48, sc = bar + 72, pW = bar + 88, oR = bar + 104, cZ = bar + 120;
+  // bf16; sums read; c's rows behind the last token zeroed; info_s written; sums done, by group and parity of v; c landed
+  // whose rows a group has to zero.  A barrier's waiter waits for every one of its phases in turn (of one that it saw only
+  // every other time it would take the phase before for the one that it wants: their parity is all it
+  // sees), so what a group waits for has a barrier for each group.
+  const uint32_t xF = bar, cF = bar + 24, dn = bar + 48, sc = bar + 72, pW = bar + 88, oR = bar + 104, cZ = bar + 120,
+                 iF = bar + 136, oD = bar + 168, zF = bar + 200;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nch = (p.T + kTC - 1) / kTC;
   const int vts = p.DV / 64;
@@ -534,6 +545,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < 11; ++i) mbar_init(bar + 8 * i, 1);
     for (int i = 11; i < 17; ++i) mbar_init(bar + 8 * i, C::NGW);
+    for (int i = 17; i < 27; ++i) mbar_init(bar + 8 * i, 1);
     abort_flag_s = 0;
     fence_mbar_init();
     fence_async_smem();
@@ -551,21 +563,29 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
     // ------------------------------------------------------------- loads --
     if (lane == 0) {
       const OutTile stride = digits((int)gridDim.x);
-      OutTile t = digits(blockIdx.x);
-      int k = 0, f = 0, done = 0;  // tiles, c and state tiles; of these, known to be multiplied
+      OutTile at = digits(blockIdx.x);
+      int f = 0, done = 0;  // c and state tiles; of these, known to be multiplied
       bool ok = true;
       auto multiplied = [&](int upto) {  // one after the other: no barrier is left two phases behind
         for (; ok && done < upto; ++done) ok = wait(dn + 8 * (done % NCS), (done / NCS) & 1);
         return ok;
       };
-      for (; ok && k < count; advance(t, stride)) {
-        t.len = row_len(p, t.b);
-        if (t.len <= t.c * kTC) continue;  // no tokens: the other roles do not hear of it
+      auto next = [&]() {  // the next tile that holds tokens (there is one)
+        for (;; advance(at, stride)) {
+          at.len = row_len(p, at.b);
+          if (at.len > at.c * kTC) break;
+        }
+        OutTile t = at;
         t.lg = p.log_decay[t.h] * 1.4426950408889634f;
+        advance(at, stride);
+        return t;
+      };
+      auto load_xa = [&](const OutTile& t, int k) {
         const int j = t.job, tok = token_of(t), s = k % NX;
         // (the roles have read the description of a tile before its last MMAs are issued)
-        if (!multiplied((k - NX + 1) * vts)) break;
+        if (!multiplied((k - NX + 1) * vts)) return;
         info_s[k & 3] = t;
+        mbar_arrive(iF + 8 * (k & 3));
         const uint32_t d = sm + s * (2 * C::X);
         mbar_arrive_expect_tx(xF + 8 * s, 2 * C::X);
 #pragma unroll
@@ -573,8 +593,17 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
           tma_load_4d(d + i * kBlkBytes, &m.x[j], 64 * i, t.h * m.xh[j], t.b * m.xb[j], tok, xF + 8 * s);
           tma_load_4d(d + C::X + i * kBlkBytes, &m.a[j], 64 * i, t.h * m.ah[j], t.b * m.ab[j], tok, xF + 8 * s);
         }
-        const int srow = (((j * p.B + t.b) * p.NH + t.h) * nch + t.c) * DK;
-        for (int v = 0; v < vts; ++v, ++f) {
+      };
+      // in the order in which the MMAs take them (the next tile's scores follow this one's first product
+      // with the state): a copy whose buffer a later MMA has to free must not stand before one that this MMA needs
+      OutTile t, tn;
+      if (count > 0) {
+        t = next();
+        load_xa(t, 0);
+      }
+      for (int k = 0; ok && k < count; ++k) {
+        const int j = t.job, tok = token_of(t), srow = (((j * p.B + t.b) * p.NH + t.h) * nch + t.c) * DK;
+        for (int v = 0; ok && v < vts; ++v, ++f) {
           const int cb = f % NCS;
           if (!multiplied(f - NCS + 1)) break;
           if (DK == 256 && cb == 1) {  // in a's place: its scores are done
@@ -583,8 +612,13 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
           mbar_arrive_expect_tx(cF + 8 * cb, C::CS);
           tma_load_2d(sm + C::cs_at(cb), &m.s_load, 64 * v, srow, cF + 8 * cb);
           tma_load_4d(sm + C::cs_at(cb) + C::S, &m.c[j], 64 * v, t.h * m.ch[j], t.b * m.cb[j], tok, cF + 8 * cb);
+          if (v == 0 && k + 1 < count) {
+            tn = next();
+            if (NX > 1) load_xa(tn, k + 1);
+          }
         }
-        ++k;
+        if (NX == 1 && ok && k + 1 < count) load_xa(tn, k + 1);
+        t = tn;
       }
       if (!ok) {  // copies in flight land first (a barrier without one is waited for in vain, 10 ms)
         for (int i = 0; i < 3; ++i) drain(xF + 8 * i, 0), drain(xF + 8 * i, 1);
@@ -622,6 +656,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
         for (int v = 0; ok && v < vts; ++v, ++f) {
           const int cb = f % NCS, o = f & 1;
           if (!(ok = wait(cF + 8 * cb, (f / NCS) & 1))) break;
+          if (zeroed) mbar_arrive(zF + 8 * (k & 1));
           if (f >= 2 && !(ok = wait(oR + 8 * o, ((f - 2) >> 1) & 1))) break;
           tc_fence_after();
           constexpr uint32_t idesc = idesc_bf16_f32(128, 64, false, true);
@@ -646,6 +681,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
           for (int ks = 0; ks < kTC / 16; ++ks)
             umma_bf16_ts(tO, tmem + (k & 1) * 128 + ks * 8, sdesc_sw128(cc + ks * 2048, kBlkBytes, 1024), idesc,
                          ks != 0);
+          umma_commit(oD + 8 * (2 * (k & 1) + (v & 1)));
           umma_commit(dn + 8 * cb);
         }
         if (NX == 1 && ok && k + 1 < count) {
@@ -662,6 +698,8 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     const int id = 1 + grp * 4 + q;  // named barrier of the two warps of these rows
     const uint32_t tS = tmem + lanes + grp * 128;
+    const uint32_t stg = sm + C::sO + (grp * 4 + q) * 4096;
+    uint32_t nz = 0;  // c tiles with rows zeroed
     if (p.lens != nullptr) {
       // Zeros for tokens that do not count, of tiles without tokens and of reversed ones (whose rows
       // are other tokens): row r0 + row, 64 v + 32 g ..
@@ -682,8 +720,8 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
     for (int k = grp; k < count; k += 2) {
       // After an abort the waits of a tile return at once, and the two warps of a named barrier leave
       // the loop together.
-      const bool landed = wait(xF + 8 * (k % NX), (k / NX) & 1);
-      if (bar_red_or(id, 64, !landed)) break;
+      const bool told = wait(iF + 8 * (k & 3), (k >> 2) & 1);
+      if (bar_red_or(id, 64, !told)) break;
       const OutTile t = info_s[k & 3];
       const int n = t.len - t.c * kTC < kTC ? t.len - t.c * kTC : kTC;
       const LinAttnPass& ps = p.pass[t.job];
@@ -741,22 +779,21 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(pW + 8 * grp);
-      const int tok = token_of(t) + row;  // (reversed: possibly below 0)
-      __nv_bfloat16* go = static_cast<__nv_bfloat16*>(ps.out) + (long long)tok * ps.os[0] + t.b * ps.os[1] +
-                          t.h * ps.os[2] + 32 * g;
+      const int tok0 = token_of(t) + 32 * q;  // of this warp's first row (reversed: possibly below 0)
       const bool zero_c = ragged(t), counts = rev ? row >= kTC - n : row < n;
       for (int v = 0; v < vts; ++v) {
         const int f = k * vts + v, o = f & 1;
         if (zero_c) {
           const int cb = f % NCS;
-          wait(cF + 8 * cb, (f / NCS) & 1);
+          wait(zF + 8 * grp, nz++ & 1);
           const uint32_t z[4] = {0u, 0u, 0u, 0u};
           for (int e = gt; e < kTC * 8; e += 256)
             if (e / 8 >= n) sts128(sm + C::cs_at(cb) + C::S + blk_at(e / 8, e % 8), z);
           fence_async_smem();
           warp_arrive(cZ + 8 * grp);
         }
-        wait(dn + 8 * (f % NCS), (f / NCS) & 1);
+        const int vp = v & 1;  // (k >> 1) tiles of this group before, (vts + 1 - vp) / 2 sums of v's parity in each
+        wait(oD + 8 * (2 * grp + vp), ((k >> 1) * ((vts + 1 - vp) / 2) + (v >> 1)) & 1);
         tc_fence_after();
         uint32_t w[16];
         const uint32_t tO = tmem + 256 + o * 128 + lanes + 32 * g;
@@ -777,14 +814,27 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
         }
         tc_fence_before();
         warp_arrive(oR + 8 * o);
-        // 64 bytes of a row per thread (by way of shared memory and TMA stores, with their fence and barriers, an
-        // epilogue took 2,000 cycles)
-        if (tok >= 0 && tok < p.T) {
-          store32(go + 64 * v, w, m.v8);
-          store32(go + 64 * v + 16, w + 8, m.v8);
+        if (tok0 >= 0) {
+          if (g == 0 && lane == 0) bulk_wait_read_all();
+          bar_sync(id, 64);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sts128(stg + blk_at(lane, 4 * g + j), w + 4 * j);
+          fence_async_smem();
+          bar_sync(id, 64);
+          if (g == 0 && lane == 0) {
+            tma_store_4d(&m.out[t.job], 64 * v, t.h, t.b, tok0, stg);
+            bulk_commit();
+          }
+        } else if (tok0 + lane >= 0) {  // a store may not begin before token 0
+          __nv_bfloat16* go = static_cast<__nv_bfloat16*>(ps.out) + (long long)(tok0 + lane) * ps.os[0] +
+                              t.b * ps.os[1] + t.h * ps.os[2] + 64 * v + 32 * g;
+          store32(go, w, false);
+          store32(go + 16, w + 8, false);
         }
       }
     }
+    if (g == 0 && lane == 0) bulk_wait_all();
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -845,23 +895,22 @@ int launch_dk(const LinAttnParams& p, cudaStream_t s) {
   const long long outs = (long long)p.npass * p.B * p.NH * nch;
   if (base * p.nseg * (C::TILE / 256) > 0x7fffffffLL || outs * DK > 0x3fffffffLL) return kLinAttnTooWide;
   TcMaps m;
-  bool ok = true, v8 = true;
+  bool ok = true;
+  int one;
   for (int j = 0; j < p.npass; ++j) {
     const LinAttnPass& ps = p.pass[j];
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     ok = ok && encode_operand(&m.x[j], ps.x, ps.xs, p, DK, 64, kTC, sw, &m.xh[j], &m.xb[j]);
     ok = ok && encode_operand(&m.a[j], ps.a, ps.as, p, DK, 64, kTC, sw, &m.ah[j], &m.ab[j]);
     ok = ok && encode_operand(&m.c[j], ps.c, ps.cs, p, p.DV, 64, kTC, sw, &m.ch[j], &m.cb[j]);
-    const long long a32 = (long long)(reinterpret_cast<uintptr_t>(ps.out) | (uintptr_t)((ps.os[0] | ps.os[1] | ps.os[2]) * 2));
-    v8 = v8 && a32 % 32 == 0;
+    ok = ok && encode_operand(&m.out[j], ps.out, ps.os, p, p.DV, 64, 32, sw, &one, &one);
   }
   const cuuint64_t dims[2] = {(cuuint64_t)p.DV, (cuuint64_t)(outs * DK)};
   const cuuint64_t strides[1] = {(cuuint64_t)p.DV * 2};
   const cuuint32_t in[2] = {64, (cuuint32_t)DK};
   ok = ok && encode(&m.s_load, p.chunk_states, 2, dims, strides, in, CU_TENSOR_MAP_SWIZZLE_128B);
-  m.v8 = v8;
   if (!ok) return kLinAttnTooWide;
-  if (cudaMemsetAsync(p.status, 0, sizeof(int), s) != cudaSuccess) return (int)cudaErrorUnknown;
+  if (p.clear && cudaMemsetAsync(p.status, 0, sizeof(int), s) != cudaSuccess) return (int)cudaErrorUnknown;
   if (p.nseg > 1) {
     e = prepare_launch(prep_state, linattn_states_kernel<DK, true>, C::SMEM, C::THREADS, 1);
     if (e != 0) return e;

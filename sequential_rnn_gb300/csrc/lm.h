@@ -86,6 +86,7 @@ struct LinAttnParams {
   int nseg, seg_chunks;    // segments of the token axis, chunks in each
   void* chunk_states;      // bf16 [pass][head of a row][chunk][DK][DV] (kLinAttnTc)
   int* status;
+  int clear;               // clear the status word (the first launch of a call)
   unsigned long long timeout_ns;
 };
 enum : int { kLinAttnF32 = 0, kLinAttnMma = 1, kLinAttnTc = 2 };

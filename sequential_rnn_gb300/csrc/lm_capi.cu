@@ -190,6 +190,7 @@ int rnn_linattn_fwd(const rnn_linattn_desc_t* d, const rnn_linattn_strides_t* st
     return RNN_ERR_MISALIGNED;
   LinAttnParams p{};
   p.npass = 1;
+  p.clear = 1;
   p.log_decay = log_decay;
   p.lens = lens;
   p.T = d->T;
@@ -240,6 +241,7 @@ int rnn_linattn_bwd(const rnn_linattn_desc_t* d, const rnn_linattn_strides_t* st
       !strides_aligned(sv, es) || !strides_aligned(so, es))
     return RNN_ERR_MISALIGNED;
   LinAttnParams p{};
+  p.clear = 1;
   p.log_decay = log_decay;
   p.lens = lens;
   p.T = d->T;
@@ -284,6 +286,7 @@ int rnn_linattn_bwd(const rnn_linattn_desc_t* d, const rnn_linattn_strides_t* st
   if (e != 0) return map_launch_error(e);
   p.pass[0] = gvp;
   p.npass = 1;
+  p.clear = 0;  // what the first two passes reported stays
   return map_launch_error(run_passes(p, bf16, d->Dk, d->Dv, workspace, s));
 }
 

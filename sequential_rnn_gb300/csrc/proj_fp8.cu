@@ -49,7 +49,7 @@ struct F8Cfg {
   static constexpr int NPW = 16;                  // promotion warps
   static constexpr int THREADS = 32 * (4 + NPW);
   static constexpr uint32_t STG = 32 * WC * 2;    // outputs on their way, per warp
-  static constexpr uint32_t SMEM = NSTG * STAGE + NPW * STG + 1024 + (2 * NSTG + NACC) * 8 + 16;
+  static constexpr uint32_t SMEM = NSTG * STAGE + NPW * STG + 1024 + (3 * NSTG + NACC) * 8 + 16;
 };
 
 struct F8Args {
@@ -101,18 +101,18 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
   const uint32_t out_stage = ring + NSTG * C::STAGE;
+  // `full`: a block has landed; for each stage one barrier for the blocks of either issuer, so that each issuer
+  // waits for every phase of its own (seeing every other one it would take the phase before for it).
   // `done`: a block's MMAs are complete, so its stage is free and its sums can be promoted
-  const uint32_t bar_full = out_stage + C::NPW * C::STG, bar_done = bar_full + 8 * NSTG;
+  const uint32_t bar_full = out_stage + C::NPW * C::STG, bar_done = bar_full + 16 * NSTG;
   const uint32_t bar_read = bar_done + 8 * NSTG, tslot = bar_read + 8 * NACC;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ntiles = g.tiles_m * g.tiles_n;
   const unsigned long long tlim = g.timeout_ns;
 
   if (threadIdx.x == 32) {
-    for (int s = 0; s < NSTG; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
-      mbar_init(bar_done + 8 * s, 1);
-    }
+    for (int s = 0; s < 2 * NSTG; ++s) mbar_init(bar_full + 8 * s, 1);
+    for (int s = 0; s < NSTG; ++s) mbar_init(bar_done + 8 * s, 1);
     for (int a = 0; a < NACC; ++a) mbar_init(bar_read + 8 * a, C::NPW);
     abort_flag_s = 0;
     issued_s = 0;
@@ -130,10 +130,13 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tslot) : "memory");
   const int mine = (ntiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // this CTA's tiles
   const int blocks = mine * g.nkb;
+  // an even number of stages gives a stage's blocks to one issuer anyway
+  constexpr int NFULL = NSTG % 2 ? 2 * NSTG : NSTG;
+  auto full_of = [](int it) { return it % NFULL; };
 
-  // 640 threads x 96 registers at the launch: 128 x 24 + 512 x 112 are less
+  // 640 threads x 96 registers at the launch = 128 x 32 + 512 x 112
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
     if (warp == 0) {
       // ---------------------------------------------------- TMA producer --
       if (lane == 0) {
@@ -149,7 +152,8 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
               stop = true;
               break;
             }
-            const uint32_t sA = ring + s * C::STAGE, sB = sA + C::TILE_A, fb = bar_full + 8 * s;
+            const uint32_t sA = ring + s * C::STAGE, sB = sA + C::TILE_A;
+            const uint32_t fb = bar_full + 8 * full_of(it);
             mbar_arrive_expect_tx(fb, C::STAGE);
             tma_load_2d(sA, &mA, kb * FBK, m0, fb);
             tma_load_2d(sB, &mB, kb * FBK, n0, fb);
@@ -163,7 +167,7 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
         constexpr uint32_t idesc = idesc_e4m3_f32(FBM, BN);
         for (int it = warp - 1; it < blocks; it += 2) {
           const int s = it % NSTG, a = it % NACC;
-          if (!wait_f8(bar_full + 8 * s, (it / NSTG) & 1, abort_flag, g.status, tlim)) break;
+          if (!wait_f8(bar_full + 8 * full_of(it), (it / NFULL) & 1, abort_flag, g.status, tlim)) break;
           if (it >= NACC && !wait_f8(bar_read + 8 * a, ((it - NACC) / NACC) & 1, abort_flag, g.status, tlim)) break;
           tc_fence_after();
           const uint32_t sA = ring + s * C::STAGE, sB = sA + C::TILE_A;
@@ -257,7 +261,7 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
       // let TMA copies that were issued land before exit
       for (int k = issued_s - NSTG < 0 ? 0 : issued_s - NSTG; k < issued_s; ++k) {
         const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(bar_full + 8 * (k % NSTG), (k / NSTG) & 1))
+        while (!mbar_try_wait(bar_full + 8 * full_of(k), (k / NFULL) & 1))
           if (globaltimer_ns() - t0 > 10000000ull) break;
       }
     }

@@ -146,6 +146,29 @@ def test_long_rows_in_segments(S, dtype, T, B, NH, Dk, Dv):
     check_backward(S, d, dtype)
 
 
+@pytest.mark.parametrize("T,B,NH,Dk,Dv,ragged", [(3001, 8, 4, 256, 256, False), (3001, 8, 4, 256, 256, True),
+                                                  (2000, 8, 2, 256, 64, True), (4000, 8, 6, 128, 128, True),
+                                                  (4000, 8, 6, 128, 64, False), (4096, 8, 12, 64, 64, True),
+                                                  (3000, 8, 4, 128, 256, True), (4000, 8, 4, 64, 256, False),
+                                                  (4100, 8, 6, 64, 128, False)])
+def test_many_tiles_per_cta(S, T, B, NH, Dk, Dv, ragged):
+    """Enough rows and chunks that every CTA of a persistent grid takes several: against the fp32 path (itself
+    tested against the oracle) on the same inputs.  Two roundings of operands or result, each uniform within 2^-8 of
+    the value (2^-8 / sqrt 3 root mean square): together below 2^-8 of the norm."""
+    lens = [T - (T * b) // (B - 1) for b in range(B)] if ragged else None
+    d = draw(T + Dk, T, B, NH, Dk, Dv, "bf16", lens=lens)
+    f = {n: x.float() if n in ("q", "k", "v", "do") else x for n, x in d.items()}
+    got, want = ({**S.linear_attention(x["q"], x["k"], x["v"], x["g"], state=x["s0"], lens=x["lens"]),
+                  **{n: t for n, t in S.linear_attention_backward(
+                      x["q"], x["k"], x["v"], x["g"], x["do"], state=x["s0"], dstate=x["ds"],
+                      lens=x["lens"]).items() if n != "workspace"}} for x in (d, f))
+    for n, tol in (("o", H), ("dq", H), ("dk", H), ("dv", H), ("state", 4 * U), ("dstate", 4 * U)):
+        a, b = got[n].double(), want[n].double()
+        for row in range(B):   # a wrong tile shows in its row
+            i = (slice(None), row) if n in ("o", "dq", "dk", "dv") else row
+            assert (a[i] - b[i]).norm() <= tol * b[i].norm(), (n, row)
+
+
 def test_state_in_place_across_segments(S):
     """The final state may be written over the initial one."""
     for T in (64, 3000):
