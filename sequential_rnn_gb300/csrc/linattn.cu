@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
   const int c1 = c0 + p.seg_chunks < nch ? c0 + p.seg_chunks : nch;
   const int lch = (len + kC - 1) / kC;
   const int cend = c1 < lch ? c1 : lch;  // chunks c0 .. cend - 1 hold tokens
+  if (STATE_ONLY) depend_launch();
   if (STATE_ONLY && (long long)c1 * kC >= len) return;  // no later segment starts from it
   const float lg = p.log_decay[w.h] * 1.4426950408889634f;
   const bool rev = ps.reverse != 0;
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[i][r] = 0.f;
   } else if (p.nseg > 1 && (w.seg == 0 || c0 < cend)) {
+    depend_wait();  // for the scan
     const float4* src = reinterpret_cast<const float4*>(seg_state(p, w, w.seg, VT, DK * DVT));
 #pragma unroll
     for (int i = 0; i < NTS; ++i) {
@@ -398,9 +400,14 @@ int launch_cfg(const LinAttnParams& p, cudaStream_t s) {
     e = prepare_launch(prep_state, linattn_kernel<C, true>, C::SMEM_STATE, C::NT, 1);
     if (e != 0) return e;
     linattn_kernel<C, true><<<(unsigned)(base * (p.nseg - 1)), C::NT, C::SMEM_STATE, s>>>(p);
-    linattn_scan_kernel<QuadOrder<C>><<<(unsigned)(base * (DK * DVT / 256)), 256, 0, s>>>(p, p.seg_chunks * kC);
+    e = launch_dependent(linattn_scan_kernel<QuadOrder<C>>, (unsigned)(base * (DK * DVT / 256)), 256, 0, s, p,
+                         p.seg_chunks * kC);
+    if (e != 0) return e;
+    e = launch_dependent(linattn_kernel<C, false>, (unsigned)(base * p.nseg), C::NT, C::SMEM, s, p);
+    if (e != 0) return e;
+  } else {
+    linattn_kernel<C, false><<<(unsigned)base, C::NT, C::SMEM, s>>>(p);
   }
-  linattn_kernel<C, false><<<(unsigned)(base * p.nseg), C::NT, C::SMEM, s>>>(p);
   return (int)cudaGetLastError();
 }
 

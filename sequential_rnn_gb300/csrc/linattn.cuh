@@ -49,6 +49,7 @@ template <class Order>
 __global__ void __launch_bounds__(256)
     linattn_scan_kernel(const __grid_constant__ LinAttnParams p, int seg_tokens) {
   constexpr int TILE = Order::TILE, PER = TILE / 256;  // blocks of 256 per tile
+  depend_launch();
   const int VT = Order::tiles(p);
   const int e = (blockIdx.x % PER) * 256 + threadIdx.x;
   int i = blockIdx.x / PER;
@@ -69,6 +70,7 @@ __global__ void __launch_bounds__(256)
   const float* in = ps.init ? ps.init + (long long)w.bh * p.DK * p.DV : nullptr;
   float s = in ? in[ps.init_t ? (long long)v * p.DK + dk : (long long)dk * p.DV + v] : 0.f;
   float* ws = seg_state(p, w, 0, VT, TILE) + e;
+  depend_wait();  // for the segments' contributions
   *ws = s;
   const long long step = (long long)p.npass * p.B * p.NH * VT * TILE;
   ws += step;

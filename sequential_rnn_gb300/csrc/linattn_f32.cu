@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(kT32)
   const int c1 = c0 + p.seg_chunks < nch ? c0 + p.seg_chunks : nch;
   const int lch = (len + kC32 - 1) / kC32;
   const int cend = c1 < lch ? c1 : lch;
+  if (STATE_ONLY) depend_launch();
   if (STATE_ONLY && (long long)c1 * kC32 >= len) return;
   const float lg = p.log_decay[w.h] * 1.4426950408889634f;
   const bool rev = ps.reverse != 0;
@@ -69,6 +70,7 @@ __global__ void __launch_bounds__(kT32)
   if (STATE_ONLY) {
     for (int e = tid; e < DK * kV32; e += kT32) S[e] = 0.f;
   } else if (p.nseg > 1) {
+    depend_wait();  // for the scan
     const float* src = seg_state(p, w, w.seg, VT, DK * kV32);
     if (w.seg == 0 || c0 < cend)
       for (int e = tid; e < DK * kV32; e += kT32) S[e] = src[e];
@@ -207,10 +209,14 @@ int launch_dk(const LinAttnParams& p, cudaStream_t s) {
     e = prepare_launch(prep_state, linattn_f32_kernel<DK, true>, C::SMEM, kT32, 1);
     if (e != 0) return e;
     linattn_f32_kernel<DK, true><<<(unsigned)(base * (p.nseg - 1)), kT32, C::SMEM, s>>>(p);
-    linattn_scan_kernel<RowOrder<DK>>
-        <<<(unsigned)(base * (DK * kV32 / 256)), 256, 0, s>>>(p, p.seg_chunks * kC32);
+    e = launch_dependent(linattn_scan_kernel<RowOrder<DK>>, (unsigned)(base * (DK * kV32 / 256)), 256, 0, s, p,
+                         p.seg_chunks * kC32);
+    if (e != 0) return e;
+    e = launch_dependent(linattn_f32_kernel<DK, false>, (unsigned)(base * p.nseg), kT32, C::SMEM, s, p);
+    if (e != 0) return e;
+  } else {
+    linattn_f32_kernel<DK, false><<<(unsigned)base, kT32, C::SMEM, s>>>(p);
   }
-  linattn_f32_kernel<DK, false><<<(unsigned)(base * p.nseg), kT32, C::SMEM, s>>>(p);
   return (int)cudaGetLastError();
 }
 

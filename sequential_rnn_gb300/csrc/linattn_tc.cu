@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tslot_s;
+  depend_launch();  // (with its TMEM in hand: the next kernel's CTAs ask for theirs)
 
   if (warp == C::WLOAD) {
     // ------------------------------------------------------------- loads --
@@ -291,6 +292,7 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
     for (int j = 0; j < NC; ++j) S[j] = 0.f;
     if (!STATE_ONLY && owner) {
       if (p.nseg > 1) {
+        depend_wait();  // for the scan
         const float4* src = reinterpret_cast<const float4*>(seg_state(p, w, w.seg, C::MB * vts, C::TILE));
 #pragma unroll
         for (int i = 0; i < NC / 4; ++i) {
@@ -600,6 +602,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
       if (count > 0) {
         t = next();
         load_xa(t, 0);
+        depend_wait();  // for the chunk states
       }
       for (int k = 0; ok && k < count; ++k) {
         const int j = t.job, tok = token_of(t), srow = (((j * p.B + t.b) * p.NH + t.h) * nch + t.c) * DK;
@@ -915,14 +918,18 @@ int launch_dk(const LinAttnParams& p, cudaStream_t s) {
     e = prepare_launch(prep_state, linattn_states_kernel<DK, true>, C::SMEM, C::THREADS, 1);
     if (e != 0) return e;
     linattn_states_kernel<DK, true><<<(unsigned)(base * (p.nseg - 1)), C::THREADS, C::SMEM, s>>>(p, m);
-    linattn_scan_kernel<TcOrder<DK>>
-        <<<(unsigned)(base * (C::TILE / 256)), 256, 0, s>>>(p, p.seg_chunks * kTC);
+    e = launch_dependent(linattn_scan_kernel<TcOrder<DK>>, (unsigned)(base * (C::TILE / 256)), 256, 0, s, p,
+                         p.seg_chunks * kTC);
+    if (e != 0) return e;
+    e = launch_dependent(linattn_states_kernel<DK, false>, (unsigned)(base * p.nseg), C::THREADS, C::SMEM, s, p, m);
+    if (e != 0) return e;
+  } else {
+    linattn_states_kernel<DK, false><<<(unsigned)base, C::THREADS, C::SMEM, s>>>(p, m);
   }
-  linattn_states_kernel<DK, false><<<(unsigned)(base * p.nseg), C::THREADS, C::SMEM, s>>>(p, m);
   const long long cap = sm_count();
-  linattn_outputs_kernel<DK>
-      <<<(unsigned)(outs < cap ? outs : cap), O::THREADS, O::SMEM, s>>>(p, m, (int)outs);
-  return (int)cudaGetLastError();
+  e = launch_dependent(linattn_outputs_kernel<DK>, (unsigned)(outs < cap ? outs : cap), O::THREADS, O::SMEM, s, p,
+                       m, (int)outs);
+  return e != 0 ? e : (int)cudaGetLastError();
 }
 
 }  // namespace

@@ -8,6 +8,28 @@
 
 namespace srnn {
 
+// Launch of a kernel that follows another one of the same call on the stream: it may begin
+// while that one's last CTAs run, and waits for the whole of it at depend_wait(), before it touches what that one
+// writes.  (The kernel in front, itself launched after everything earlier had ended, says depend_launch().)
+template <class... P, class... A>
+int launch_dependent(void (*kern)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return (int)cudaLaunchKernelEx(&cfg, kern, args...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void depend_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
+
 // ------------------------------------------------------------------ norm --
 struct NormParams {
   const void* x;

@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_vec_kernel(const NormP
 // Gradient: a persistent grid; every thread keeps its columns' share of dw in
 // registers over all of its rows.
 template <class T, int NV, bool WARP>
-__global__ void __launch_bounds__(256, NV <= 4 ? 2 : 1) norm_bwd_vec_kernel(const NormBwdParams p) {
+__global__ void __launch_bounds__(256) norm_bwd_vec_kernel(const NormBwdParams p) {
   constexpr int E = Vec<T>::E;
   __shared__ float red[32];
   const int TPR = WARP ? 32 : blockDim.x;
@@ -297,11 +297,12 @@ __global__ void __launch_bounds__(256, NV <= 4 ? 2 : 1) norm_bwd_vec_kernel(cons
     for (int j = 0; j < E; ++j) dw[i][j] = 0.f;
   const long long first = WARP ? (long long)blockIdx.x * kRowsPerCta + wp : blockIdx.x;
   const long long step = WARP ? (long long)gridDim.x * kRowsPerCta : gridDim.x;
-  for (long long row = first; row < p.rows; row += step) {
+  uint4 gv[NV], hv[NV], ev[NV];
+  float r = 0.f;
+  auto load = [&](long long row) {
     const uint4* dy = reinterpret_cast<const uint4*>(p.dy) + row * nv;
     const uint4* h = reinterpret_cast<const uint4*>(p.h) + row * nv;
     const uint4* dh = reinterpret_cast<const uint4*>(p.dh) + row * nv;
-    uint4 gv[NV], hv[NV], ev[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = t + i * TPR;
@@ -309,7 +310,14 @@ __global__ void __launch_bounds__(256, NV <= 4 ? 2 : 1) norm_bwd_vec_kernel(cons
       hv[i] = v < nv ? h[v] : zero;
       ev[i] = p.dh && v < nv ? dh[v] : zero;
     }
-    const float r = p.rstd[row];
+    r = p.rstd[row];
+  };
+  constexpr bool AHEAD = NV <= 4;  // registers for the next row
+  if (AHEAD && first < p.rows) load(first);
+  for (long long row = first; row < p.rows; row += step) {
+    if (!AHEAD) load(row);
+    uint4 g0[NV], h0[NV], e0[NV];
+    const float rs = r;
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -320,26 +328,32 @@ __global__ void __launch_bounds__(256, NV <= 4 ? 2 : 1) norm_bwd_vec_kernel(cons
       load_weight<E>(p.weight, (v < nv ? v : 0) * E, w);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        const float xh = a[j] * r;
+        const float xh = a[j] * rs;
         dw[i][j] = fmaf(g[j], xh, dw[i][j]);
         dot = fmaf(g[j] * w[j], xh, dot);
       }
+      g0[i] = gv[i];
+      h0[i] = hv[i];
+      e0[i] = ev[i];
     }
+    // the next row is on its way while this one's sum is taken and its dx written
+    if (AHEAD && row + step < p.rows) load(row + step);
     dot = (WARP ? warp_sum(dot) : block_sum(dot, red)) / (float)p.N;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = t + i * TPR;
       if (v >= nv) break;
       float g[E], a[E], e[E], w[E];
-      Vec<T>::unpack(gv[i], g);
-      Vec<T>::unpack(hv[i], a);
-      Vec<T>::unpack(ev[i], e);
+      Vec<T>::unpack(g0[i], g);
+      Vec<T>::unpack(h0[i], a);
+      Vec<T>::unpack(e0[i], e);
       load_weight<E>(p.weight, v * E, w);
 #pragma unroll
-      for (int j = 0; j < E; ++j) e[j] += r * (w[j] * g[j] - a[j] * r * dot);
+      for (int j = 0; j < E; ++j) e[j] += rs * (w[j] * g[j] - a[j] * rs * dot);
       reinterpret_cast<uint4*>(p.dx)[row * nv + v] = Vec<T>::pack(e);
     }
   }
+  depend_launch();
   if (p.dw == nullptr) return;
   float* part = p.part + (long long)blockIdx.x * p.N;
   if (WARP) {  // the CTA's warps one after the other, in shared memory
@@ -376,6 +390,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, float*
   __shared__ float red[32][33];
   const int c = threadIdx.x & 31, k = threadIdx.x >> 5, n = blockIdx.x * 32 + c;
   float s = 0.f;
+  depend_wait();
   if (n < N)
 #pragma unroll 20
     for (int i = k; i < parts; i += 32) s += part[(long long)i * N + n];
@@ -449,7 +464,7 @@ int norm_bwd_typed(const NormBwdParams& p, cudaStream_t s) {
   if (!vec || nv > 8 * 256) {
     norm_bwd_any_kernel<T><<<parts, 256, 0, s>>>(p);
   } else if (nv <= 128) {
-    const long long ctas = (p.rows + kRowsPerCta - 1) / kRowsPerCta, cap = 2LL * sm_count();
+    const long long ctas = (p.rows + kRowsPerCta - 1) / kRowsPerCta, cap = (nv <= 64 ? 2LL : 1LL) * sm_count();
     if (ctas < parts) parts = (int)ctas;
     if (cap < parts) parts = (int)cap;
     if (nv <= 64)
@@ -463,7 +478,11 @@ int norm_bwd_typed(const NormBwdParams& p, cudaStream_t s) {
     else
       norm_bwd_vec_kernel<T, 8, false><<<parts, 256, 0, s>>>(p);
   }
-  if (p.dw) norm_dw_kernel<<<(p.N + 31) / 32, 1024, 0, s>>>(p.part, p.dw, parts, p.N);
+  if (p.dw) {
+    const int e = launch_dependent(norm_dw_kernel, (unsigned)((p.N + 31) / 32), 1024, 0, s, (const float*)p.part, p.dw,
+                                   parts, p.N);
+    if (e != 0) return e;
+  }
   return (int)cudaGetLastError();
 }
 
