@@ -50,8 +50,8 @@ struct LaCfg {
   static constexpr uint32_t XB = kC * DK * 2, CB = kC * DVT * 2;
   static constexpr uint32_t STAGE = 2 * XB + CB;
   static constexpr uint32_t SB = DVT * DK * 2;   // bf16 copy of the state, [v][dk]
-  static constexpr uint32_t SMEM = 2 * STAGE + 2 * SB;
-  static constexpr uint32_t SMEM_STATE = 2 * (XB + CB);
+  static constexpr uint32_t SMEM = 2 * STAGE + 2 * SB + 1024;  // (1024: for aligning the tiles)
+  static constexpr uint32_t SMEM_STATE = 2 * (XB + CB) + 1024;
   static constexpr int OCC = DK <= 64 ? 3 : (DK == 128 ? 2 : 1);
 };
 
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
   constexpr int DK = C::DK, DVT = C::DVT, NT = C::NT, NTS = C::NTS, NTO = C::NTO;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ float pow8[8];  // lambda^(8 m)
-  const uint32_t sm = smem_u32(smem_raw);
+  const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t stage_bytes = STATE_ONLY ? C::XB + C::CB : C::STAGE;
   const uint32_t sS = sm + 2 * C::STAGE;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -175,13 +175,13 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
   }
   // bf16 copy of the state into buffer `buf`, [v][dk]
   auto publish = [&](int buf) {
-    const uint32_t d = sS + buf * C::SB;
+    const uint32_t d = sS + buf * C::SB + tile_at<DK>(16 * vg + g0, (kg * C::DKW) / 8) + t0 * 2;
 #pragma unroll
     for (int i = 0; i < NTS; ++i) {
-      const int ch = (kg * C::DKW) / 8 + i;
+      const uint32_t at = d ^ (uint32_t)(i << 4);
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh)
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(d + tile_at<DK>(16 * vg + g0 + 8 * hh, ch) + t0 * 2),
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 8 * hh * (DK * 2)),
                      "r"(pack_bf16x2(S[i][2 * hh], S[i][2 * hh + 1]))
                      : "memory");
     }
@@ -208,6 +208,16 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
 
   const int rb = warp & 3, cg = warp >> 2;  // output rows 16 rb .., columns OVC cg ..
   const int mg = lane >> 3, l7 = lane & 7;
+  // Where a thread's fragments begin in each tile.  A swizzled tile's 16-byte chunk numbers enter an address by
+  // exclusive or, and its rows 8 apart swizzle alike: chunk 2 ks + m is (base ^ ks << 5), a row 8 i on is
+  // + 8 i row bytes, an immediate (computed place by place, addresses were a third of the instructions).
+  constexpr int RX = DK * 2, RC = DVT * 2;  // row bytes
+  const uint32_t oX = tile_at<DK>(16 * rb + (lane & 15), lane >> 4);            // x, rows as A operand
+  const uint32_t oA = tile_at<DK>(8 * (mg >> 1) + l7, mg & 1);                  // a, rows as B operand
+  const uint32_t oS = tile_at<DK>(cg * C::OVC + 8 * (mg >> 1) + l7, mg & 1);    // state
+  const uint32_t oCp = tile_at<DVT>(8 * (mg & 1) + l7, (cg * C::OVC) / 8 + (mg >> 1));   // c, columns as B operand
+  const uint32_t oCu = tile_at<DVT>(8 * (mg >> 1) + l7, 2 * vg + (mg & 1));              // c, columns as A operand
+  const uint32_t oAu = tile_at<DK>(8 * (mg & 1) + l7, (kg * C::DKW) / 8 + (mg >> 1));    // a, columns as B operand
   for (int c = c0; c < cend; ++c) {
     const int st = (c - c0) & 1;
     const uint32_t bA = sm + st * stage_bytes, bC = bA + C::XB, bX = bC + C::CB;
@@ -231,11 +241,12 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
 #pragma unroll 4
       for (int ks = 0; ks < DK / 16; ++ks) {
         uint32_t qa[4];
-        ldmatrix_x4(qa, bX + tile_at<DK>(16 * rb + (lane & 15), 2 * ks + (lane >> 4)));
+        ldmatrix_x4(qa, (bX + oX) ^ (uint32_t)(ks << 5));
+        const uint32_t sk = (bS + oS) ^ (uint32_t)(ks << 5), ak = (bA + oA) ^ (uint32_t)(ks << 5);
 #pragma unroll
         for (int i = 0; i < NTO; i += 2) {
           uint32_t sb[4];
-          ldmatrix_x4(sb, bS + tile_at<DK>(cg * C::OVC + 8 * (i + (mg >> 1)) + l7, 2 * ks + (mg & 1)));
+          ldmatrix_x4(sb, sk + 8 * i * RX);
           mma_bf16_16816(O[i], qa, sb[0], sb[1]);
           mma_bf16_16816(O[i + 1], qa, sb[2], sb[3]);
         }
@@ -243,7 +254,7 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
         for (int i = 0; i < 8; i += 2) {
           if (i <= 2 * rb) {
             uint32_t kb[4];
-            ldmatrix_x4(kb, bA + tile_at<DK>(8 * (i + (mg >> 1)) + l7, 2 * ks + (mg & 1)));
+            ldmatrix_x4(kb, ak + 8 * i * RX);
             mma_bf16_16816(P[i], qa, kb[0], kb[1]);
             mma_bf16_16816(P[i + 1], qa, kb[2], kb[3]);
           }
@@ -286,8 +297,7 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
 #pragma unroll
         for (int i = 0; i < NTO; i += 2) {
           uint32_t vb[4];
-          ldmatrix_x4_trans(vb, bC + tile_at<DVT>(16 * ks + 8 * (mg & 1) + l7,
-                                                  (cg * C::OVC) / 8 + i + (mg >> 1)));
+          ldmatrix_x4_trans(vb, ((bC + oCp) ^ (uint32_t)(i << 4)) + 16 * ks * RC);
           mma_bf16_16816(O[i], pa, vb[0], vb[1]);
           mma_bf16_16816(O[i + 1], pa, vb[2], vb[3]);
         }
@@ -321,7 +331,7 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       uint32_t vt[4];
-      ldmatrix_x4_trans(vt, bC + tile_at<DVT>(16 * ks + 8 * (mg >> 1) + l7, 2 * vg + (mg & 1)));
+      ldmatrix_x4_trans(vt, bC + oCu + 16 * ks * RC);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         float x0 = bf16_lo(vt[r]) * wj[ks][2 * (r >> 1)];
@@ -341,8 +351,7 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
         uint32_t kb[4];
-        ldmatrix_x4_trans(kb, bA + tile_at<DK>(16 * ks + 8 * (mg & 1) + l7,
-                                               (kg * C::DKW) / 8 + i + (mg >> 1)));
+        ldmatrix_x4_trans(kb, ((bA + oAu) ^ (uint32_t)(i << 4)) + 16 * ks * RX);
         mma_bf16_16816(d[0], al[ks], kb[0], kb[1]);
         mma_bf16_16816(d[1], al[ks], kb[2], kb[3]);
         mma_bf16_16816(d[0], am[ks], kb[0], kb[1]);
