@@ -3,7 +3,7 @@
 //
 //   h = round(x + residual);  r = 1 / sqrt(mean_n h^2 + eps);  y = h r w
 //   8-bit output: per row and block of 128 columns s = max|y| / 448 (1 where
-//   the block is all zero), q = e4m3(y (1/s))
+//   the block is all zero), q = e4m3(y / s)
 //   gradient, xh = h r:  dx = r (w dy - xh mean_n(w dy xh)) + dh,
 //                        dw = sum over rows of dy xh
 //
@@ -38,6 +38,11 @@ template <>
 __device__ __forceinline__ float rounded<__nv_bfloat16>(float v) { return bf16_round(v); }
 __device__ __forceinline__ uint8_t to_e4m3(float v) {
   return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
+         (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3) << 16;
 }
 
 // scale of a block whose largest magnitude is `top` (NaN values do not count towards it);
@@ -87,20 +92,19 @@ __global__ void __launch_bounds__(256) norm_any_kernel(const NormParams p) {
         y[j] = n < N ? hv[j] * r * p.weight[n] : 0.f;
         top = fmaxf(top, fabsf(y[j]));
       }
-      float inv = 1.f;
+      float s = 1.f;
       if (p.scale) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float s = block_scale(top);
+        s = block_scale(top);
         if (lane == 0) p.scale[row * nblk + b] = s;
-        inv = 1.f / s;
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int n = b * kBlk + 32 * j + lane;
         if (n >= N) continue;
         if (p.scale)
-          static_cast<uint8_t*>(p.y)[row * N + n] = to_e4m3(y[j] * inv);
+          static_cast<uint8_t*>(p.y)[row * N + n] = to_e4m3(y[j] / s);
         else
           store1(static_cast<T*>(p.y) + row * N + n, y[j]);
         if (h) store1(h + n, hv[j]);
@@ -257,20 +261,21 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_vec_kernel(const NormP
 #pragma unroll
     for (int o = kBlk / E / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float s = block_scale(top);
-    const float inv = 1.f / s;  // (one division for the block: with one for each value they were half of the time)
+    // q = e4m3(y / s) with one division for the block (one for each value took half of the time): y times
+    // the ends of an interval of 1/s that is wider than the three roundings between them and y / s (3 2^-24).
+    // Where both products give the same code so does the quotient; about one warp in 500 has to divide.
+    const float inv = 1.f / s, lo = inv * (1.f - 0x1p-22f), hi = inv * (1.f + 0x1p-22f);
     if (v >= nv) continue;
     if (v % (kBlk / E) == 0) p.scale[row * ((p.N + kBlk - 1) / kBlk) + v / (kBlk / E)] = s;
-    uint32_t q[E / 4];
+    uint32_t q[E / 4], differ = s < 0x1p-126f;  // (1/s of a subnormal s may be infinite)
 #pragma unroll
     for (int j = 0; j < E; j += 4) {
-      uint32_t u = 0;
+      q[j / 4] = pack_e4m3(y[j] * lo, y[j + 1] * lo, y[j + 2] * lo, y[j + 3] * lo);
+      differ |= q[j / 4] ^ pack_e4m3(y[j] * hi, y[j + 1] * hi, y[j + 2] * hi, y[j + 3] * hi);
+    }
+    if (differ) {
 #pragma unroll
-      for (int k = 0; k < 4; k += 2) {
-        const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(
-            make_float2(y[j + k] * inv, y[j + k + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-        u |= (uint32_t)two << (8 * k);
-      }
-      q[j / 4] = u;
+      for (int j = 0; j < E; j += 4) q[j / 4] = pack_e4m3(y[j] / s, y[j + 1] / s, y[j + 2] / s, y[j + 3] / s);
     }
     uint8_t* dst = static_cast<uint8_t*>(p.y) + row * p.N + v * E;
     if constexpr (E == 8)

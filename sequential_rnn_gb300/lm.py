@@ -332,7 +332,7 @@ def _linattn(q, k, v, log_decay, scale, lead, do=None):
             and (do is None or do.is_contiguous())):
         st = _strides(_stride_of("q", q), _stride_of("k", k), _stride_of("v", v),
                       _stride_of("do", do) if do is not None else (B * NH * Dv, NH * Dv, Dv))
-    return *_desc(_DT[dt], T, B, NH, Dk, Dv, Dk ** -0.5 if scale is None else scale), st, dev, dt
+    return *_desc(_DT[dt], T, B, NH, Dk, Dv, max(Dk, 1) ** -0.5 if scale is None else scale), st, dev, dt
 
 
 @_for_stream

@@ -76,6 +76,19 @@ def test_rms_norm_8bit(S, rows, N, dtype):
     assert out["scale"][0, 0] == 1 and not np64(out["y"])[0, :min(N, 128)].any()
 
 
+@pytest.mark.parametrize("small", [1.0, 2.0 ** -114, 2.0 ** -128, 2.0 ** -135])
+@pytest.mark.parametrize("rows,N", [(2000, 768), (700, 1001), (40, 8192), (5, 16512)])
+def test_rms_norm_8bit_codes_are_those_of_the_quotient(S, rows, N, small):
+    """y / scale as fp32 divides, rounded once: equal codes, at every magnitude a scale can have."""
+    x, w = rand(60, rows, N), rand(61, N, scale=small)
+    out = S.rms_norm(x, w, quantize=True, train=True)
+    y = x.cpu().numpy() * out["rstd"].cpu().numpy()[:, None] * w.cpu().numpy()
+    s = np.repeat(out["scale"].cpu().numpy(), 128, 1)[:, :N]
+    q = torch.from_numpy(y / s).to(torch.float8_e4m3fn)
+    assert (s < 2.0 ** -126).any() == (small < 2.0 ** -120)
+    assert torch.equal(out["y"].cpu().view(torch.uint8), q.view(torch.uint8))
+
+
 def test_rms_norm_leading_dimensions_in_place_and_empty(S):
     x, res, w = rand(7, 3, 5, 256, dtype="bf16"), rand(8, 3, 5, 256, dtype="bf16"), rand(9, 256)
     want = S.rms_norm(x, w, res, quantize=True, train=True)
