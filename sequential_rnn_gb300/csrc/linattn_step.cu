@@ -29,11 +29,23 @@ __global__ void __launch_bounds__(128) linattn_step_kernel(const LinAttnStepPara
   const int vt = blockIdx.x % VT, bh = blockIdx.x / VT, b = bh / p.NH, h = bh % p.NH;
   const int tid = threadIdx.x, g = tid % G, r0 = tid / G;
   T* o = static_cast<T*>(p.o) + ((long long)b * p.NH + h) * p.DV + vt * VC;
+  depend_launch();
+  depend_wait();
   const int slot = p.slots ? p.slots[b] : b;
   if (slot < 0 || slot >= p.nslots) {  // a row without a state
     if (tid < VC) out1(o + tid, 0.f);
     return;
   }
+  float4* S = reinterpret_cast<float4*>(p.state + (((long long)slot * p.NH + h) * DK) * p.DV + vt * VC) + g;
+  const int pitch = p.DV / 4;
+  // the thread's rows of S in batches, each loaded whole before its first store
+  constexpr int ROWS = DK / R, BATCH = ROWS < 8 ? ROWS : 8;
+  float4 s[BATCH];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) s[i] = S[(long long)(r0 + (i0 + i) * R) * pitch];
+  };
+  load(0);
   const T* q = static_cast<const T*>(p.q) + b * p.qs[0] + h * p.qs[1];
   const T* k = static_cast<const T*>(p.k) + b * p.ks[0] + h * p.ks[1];
   const T* v = static_cast<const T*>(p.v) + b * p.vs[0] + h * p.vs[1] + vt * VC;
@@ -41,26 +53,28 @@ __global__ void __launch_bounds__(128) linattn_step_kernel(const LinAttnStepPara
     qk[0][i] = in1(q + i) * p.scale;
     qk[1][i] = in1(k + i);
   }
-  float4* S = reinterpret_cast<float4*>(p.state + (((long long)slot * p.NH + h) * DK) * p.DV + vt * VC) + g;
-  const int pitch = p.DV / 4;
   const float lam = expf(p.log_decay[h]);
   float4 v4;
   v4.x = in1(v + 4 * g), v4.y = in1(v + 4 * g + 1), v4.z = in1(v + 4 * g + 2), v4.w = in1(v + 4 * g + 3);
   __syncthreads();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int d = r0; d < DK; d += R) {
-    float4 s = S[(long long)d * pitch];
-    const float kd = qk[1][d], qd = qk[0][d];
-    s.x = fmaf(lam, s.x, kd * v4.x);
-    s.y = fmaf(lam, s.y, kd * v4.y);
-    s.z = fmaf(lam, s.z, kd * v4.z);
-    s.w = fmaf(lam, s.w, kd * v4.w);
-    S[(long long)d * pitch] = s;
-    acc.x = fmaf(qd, s.x, acc.x);
-    acc.y = fmaf(qd, s.y, acc.y);
-    acc.z = fmaf(qd, s.z, acc.z);
-    acc.w = fmaf(qd, s.w, acc.w);
+  for (int i0 = 0; i0 < ROWS; i0 += BATCH) {
+    if (i0) load(i0);
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int d = r0 + (i0 + i) * R;
+      const float kd = qk[1][d], qd = qk[0][d];
+      float4 x = s[i];
+      x.x = fmaf(lam, x.x, kd * v4.x);
+      x.y = fmaf(lam, x.y, kd * v4.y);
+      x.z = fmaf(lam, x.z, kd * v4.z);
+      x.w = fmaf(lam, x.w, kd * v4.w);
+      S[(long long)d * pitch] = x;
+      acc.x = fmaf(qd, x.x, acc.x);
+      acc.y = fmaf(qd, x.y, acc.y);
+      acc.z = fmaf(qd, x.z, acc.z);
+      acc.w = fmaf(qd, x.w, acc.w);
+    }
   }
   part[r0][g] = acc;
   __syncthreads();
@@ -75,10 +89,8 @@ template <class T, int DK>
 int launch_t(const LinAttnStepParams& p, cudaStream_t s) {
   const long long rows = (long long)p.B * p.NH;
   if (p.DV % 64 == 0)
-    linattn_step_kernel<T, DK, 64><<<(unsigned)(rows * (p.DV / 64)), 128, 0, s>>>(p);
-  else
-    linattn_step_kernel<T, DK, 32><<<(unsigned)(rows * (p.DV / 32)), 128, 0, s>>>(p);
-  return (int)cudaGetLastError();
+    return launch_dependent(linattn_step_kernel<T, DK, 64>, (unsigned)(rows * (p.DV / 64)), 128, 0, s, p);
+  return launch_dependent(linattn_step_kernel<T, DK, 32>, (unsigned)(rows * (p.DV / 32)), 128, 0, s, p);
 }
 template <class T>
 int launch_dk(const LinAttnStepParams& p, cudaStream_t s) {

@@ -70,6 +70,8 @@ template <class T>
 __global__ void __launch_bounds__(256) norm_any_kernel(const NormParams p) {
   __shared__ float red[8];
   const int N = p.N;
+  depend_launch();
+  depend_wait();
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(p.x) + row * N;
     const T* res = p.residual ? static_cast<const T*>(p.residual) + row * N : nullptr;
@@ -185,7 +187,7 @@ template <int E>
 __device__ __forceinline__ void load_weight(const float* w, int col, float (&f)[E]) {
 #pragma unroll
   for (int j = 0; j < E; j += 4) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(w + col + j));
+    const float4 v = *reinterpret_cast<const float4*>(w + col + j);
     f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
   }
 }
@@ -195,93 +197,107 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 constexpr int kRowsPerCta = 8;  // warp-per-row kernels: 256 threads
+constexpr int kNormCtas = 2;    // their CTAs per SM
 
 template <class T, int NV, bool WARP, bool QUANT>
-__global__ void __launch_bounds__(WARP ? 256 : 1024) norm_vec_kernel(const NormParams p) {
+__global__ void __launch_bounds__(WARP ? 256 : 1024, WARP ? kNormCtas : 1) norm_vec_kernel(const NormParams p) {
   constexpr int E = Vec<T>::E;
   __shared__ float red[32];
   const int TPR = WARP ? 32 : blockDim.x;
   const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const long long row = WARP ? (long long)blockIdx.x * kRowsPerCta + (threadIdx.x >> 5) : blockIdx.x;
-  if (WARP && row >= p.rows) return;
   const int nv = p.N / E;
-  const uint4* x = reinterpret_cast<const uint4*>(p.x) + row * nv;
-  const uint4* res = reinterpret_cast<const uint4*>(p.residual) + row * nv;
-  uint4* h = reinterpret_cast<uint4*>(p.h) + row * nv;
-  uint4 hv[NV], rv[NV];
+  depend_launch();
+  depend_wait();
+  // a warp keeps its columns' weights for all of its rows
+  float w[WARP ? NV : 1][E];
+  if (WARP)
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = t + i * TPR;
-    hv[i] = v < nv ? x[v] : make_uint4(0u, 0u, 0u, 0u);
-  }
-  if (p.residual) {
+    for (int i = 0; i < NV; ++i) load_weight<E>(p.weight, (t + i * TPR < nv ? t + i * TPR : 0) * E, w[i]);
+  const long long stride = WARP ? (long long)gridDim.x * kRowsPerCta : gridDim.x;
+  long long row = WARP ? (long long)blockIdx.x * kRowsPerCta + (threadIdx.x >> 5) : blockIdx.x;
+  uint4 hv[NV], rv[NV];
+  auto load_row = [&](long long at) {
+    const uint4* x = reinterpret_cast<const uint4*>(p.x) + at * nv;
+    const uint4* res = reinterpret_cast<const uint4*>(p.residual) + at * nv;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = t + i * TPR;
-      rv[i] = v < nv ? res[v] : make_uint4(0u, 0u, 0u, 0u);
+      const bool in = at < p.rows && v < nv;
+      hv[i] = in ? x[v] : make_uint4(0u, 0u, 0u, 0u);
+      rv[i] = in && p.residual ? res[v] : make_uint4(0u, 0u, 0u, 0u);
     }
-  }
-  float ss = 0.f;
+  };
+  load_row(row);
+  for (; row < p.rows; row += stride) {
+    uint4* h = reinterpret_cast<uint4*>(p.h) + row * nv;
+    uint4 cur[NV];
+    float ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float a[E];
-    Vec<T>::unpack(hv[i], a);
-    if (p.residual) {
-      float b[E];
-      Vec<T>::unpack(rv[i], b);
+    for (int i = 0; i < NV; ++i) {
+      float a[E];
+      cur[i] = hv[i];
+      Vec<T>::unpack(cur[i], a);
+      if (p.residual) {
+        float b[E];
+        Vec<T>::unpack(rv[i], b);
 #pragma unroll
-      for (int j = 0; j < E; ++j) a[j] += b[j];
-      hv[i] = Vec<T>::pack(a);  // the rounding of h
-      Vec<T>::unpack(hv[i], a);
+        for (int j = 0; j < E; ++j) a[j] += b[j];
+        cur[i] = Vec<T>::pack(a);  // the rounding of h
+        Vec<T>::unpack(cur[i], a);
+      }
+#pragma unroll
+      for (int j = 0; j < E; ++j) ss += a[j] * a[j];
     }
-    const int v = t + i * TPR;
-    if (p.h && v < nv) h[v] = hv[i];
+    if (WARP) load_row(row + stride);
 #pragma unroll
-    for (int j = 0; j < E; ++j) ss += a[j] * a[j];
-  }
-  const float sum = WARP ? warp_sum(ss) : block_sum(ss, red);
-  const float r = rsqrtf(sum / (float)p.N + p.eps);
-  if (p.rstd && t == 0) p.rstd[row] = r;
+    for (int i = 0; i < NV; ++i)
+      if (p.h && t + i * TPR < nv) h[t + i * TPR] = cur[i];
+    const float sum = WARP ? warp_sum(ss) : block_sum(ss, red);
+    const float r = rsqrtf(sum / (float)p.N + p.eps);
+    if (p.rstd && t == 0) p.rstd[row] = r;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = t + i * TPR;
-    if (!QUANT && v >= nv) break;
-    float y[E], w[E];
-    Vec<T>::unpack(hv[i], y);
-    load_weight<E>(p.weight, (v < nv ? v : 0) * E, w);  // (past the row y is zero)
+    for (int i = 0; i < NV; ++i) {
+      const int v = t + i * TPR;
+      if (!QUANT && v >= nv) break;
+      float y[E];
+      if (!WARP) load_weight<E>(p.weight, (v < nv ? v : 0) * E, w[0]);
+      Vec<T>::unpack(cur[i], y);
+      // (past the row h is zero)
 #pragma unroll
-    for (int j = 0; j < E; ++j) y[j] = v < nv ? y[j] * r * w[j] : 0.f;
-    if (!QUANT) {
-      reinterpret_cast<uint4*>(p.y)[row * nv + v] = Vec<T>::pack(y);
-      continue;
+      for (int j = 0; j < E; ++j) y[j] = v < nv ? y[j] * r * w[WARP ? i : 0][j] : 0.f;
+      if (!QUANT) {
+        reinterpret_cast<uint4*>(p.y)[row * nv + v] = Vec<T>::pack(y);
+        continue;
+      }
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < E; ++j) top = fmaxf(top, fabsf(y[j]));
+#pragma unroll
+      for (int o = kBlk / E / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float s = block_scale(top);
+      // q = e4m3(y / s) with one division for the block (one for each value took half of the time): y times
+      // the ends of an interval of 1/s that is wider than the three roundings between them and y / s (3 2^-24).
+      // Where both products give the same code so does the quotient; about one warp in 500 has to divide.
+      const float inv = 1.f / s, lo = inv * (1.f - 0x1p-22f), hi = inv * (1.f + 0x1p-22f);
+      if (v >= nv) continue;
+      if (v % (kBlk / E) == 0) p.scale[row * ((p.N + kBlk - 1) / kBlk) + v / (kBlk / E)] = s;
+      uint32_t q[E / 4], differ = s < 0x1p-126f;  // (1/s of a subnormal s may be infinite)
+#pragma unroll
+      for (int j = 0; j < E; j += 4) {
+        q[j / 4] = pack_e4m3(y[j] * lo, y[j + 1] * lo, y[j + 2] * lo, y[j + 3] * lo);
+        differ |= q[j / 4] ^ pack_e4m3(y[j] * hi, y[j + 1] * hi, y[j + 2] * hi, y[j + 3] * hi);
+      }
+      if (differ) {
+#pragma unroll
+        for (int j = 0; j < E; j += 4) q[j / 4] = pack_e4m3(y[j] / s, y[j + 1] / s, y[j + 2] / s, y[j + 3] / s);
+      }
+      uint8_t* dst = static_cast<uint8_t*>(p.y) + row * p.N + v * E;
+      if constexpr (E == 8)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+      else
+        *reinterpret_cast<uint32_t*>(dst) = q[0];
     }
-    float top = 0.f;
-#pragma unroll
-    for (int j = 0; j < E; ++j) top = fmaxf(top, fabsf(y[j]));
-#pragma unroll
-    for (int o = kBlk / E / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float s = block_scale(top);
-    // q = e4m3(y / s) with one division for the block (one for each value took half of the time): y times
-    // the ends of an interval of 1/s that is wider than the three roundings between them and y / s (3 2^-24).
-    // Where both products give the same code so does the quotient; about one warp in 500 has to divide.
-    const float inv = 1.f / s, lo = inv * (1.f - 0x1p-22f), hi = inv * (1.f + 0x1p-22f);
-    if (v >= nv) continue;
-    if (v % (kBlk / E) == 0) p.scale[row * ((p.N + kBlk - 1) / kBlk) + v / (kBlk / E)] = s;
-    uint32_t q[E / 4], differ = s < 0x1p-126f;  // (1/s of a subnormal s may be infinite)
-#pragma unroll
-    for (int j = 0; j < E; j += 4) {
-      q[j / 4] = pack_e4m3(y[j] * lo, y[j + 1] * lo, y[j + 2] * lo, y[j + 3] * lo);
-      differ |= q[j / 4] ^ pack_e4m3(y[j] * hi, y[j + 1] * hi, y[j + 2] * hi, y[j + 3] * hi);
-    }
-    if (differ) {
-#pragma unroll
-      for (int j = 0; j < E; j += 4) q[j / 4] = pack_e4m3(y[j] / s, y[j + 1] / s, y[j + 2] / s, y[j + 3] / s);
-    }
-    uint8_t* dst = static_cast<uint8_t*>(p.y) + row * p.N + v * E;
-    if constexpr (E == 8)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
-    else
-      *reinterpret_cast<uint32_t*>(dst) = q[0];
+    if (!WARP) break;  // (a CTA has one row)
   }
 }
 
@@ -446,17 +462,16 @@ int norm_typed(const NormParams& p, cudaStream_t s) {
                    vec_ok(p.weight) && vec_ok(p.y);
   const int nv = p.N / E, th = vec_threads(nv);
   if (!vec || th == 0) {
-    norm_any_kernel<T><<<(unsigned)(p.rows < 65536 ? p.rows : 65536), 256, 0, s>>>(p);
+    return launch_dependent(norm_any_kernel<T>, (unsigned)(p.rows < 65536 ? p.rows : 65536), 256, 0, s, p);
   } else if (nv <= 128) {
-    const unsigned grid = (unsigned)((p.rows + kRowsPerCta - 1) / kRowsPerCta);
+    const long long ctas = (p.rows + kRowsPerCta - 1) / kRowsPerCta, most = (long long)kNormCtas * sm_count();
+    const unsigned grid = (unsigned)(ctas < most ? ctas : most);
     if (nv <= 64)
-      norm_vec_kernel<T, 2, true, QUANT><<<grid, 256, 0, s>>>(p);
-    else
-      norm_vec_kernel<T, 4, true, QUANT><<<grid, 256, 0, s>>>(p);
-  } else {
-    norm_vec_kernel<T, 4, false, QUANT><<<(unsigned)p.rows, th, 0, s>>>(p);
+      return launch_dependent(norm_vec_kernel<T, 2, true, QUANT>, grid, 256, 0, s, p);
+    if (nv <= 96) return launch_dependent(norm_vec_kernel<T, 3, true, QUANT>, grid, 256, 0, s, p);
+    return launch_dependent(norm_vec_kernel<T, 4, true, QUANT>, grid, 256, 0, s, p);
   }
-  return (int)cudaGetLastError();
+  return launch_dependent(norm_vec_kernel<T, 4, false, QUANT>, (unsigned)p.rows, th, 0, s, p);
 }
 
 template <class T>

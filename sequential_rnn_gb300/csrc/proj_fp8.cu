@@ -289,19 +289,25 @@ __device__ __forceinline__ void mma_e4m3_16832(float (&d)[4], const uint32_t (&a
 // B's agree, so the four MMAs of a block take them in the order in which they were loaded.
 template <int NT>
 __global__ void __launch_bounds__(32 * kFewWarps)
-    proj_fp8_few_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ xs,
-                        const uint8_t* __restrict__ Wq, const float* __restrict__ Ws,
-                        const float* __restrict__ bias, __nv_bfloat16* __restrict__ y, int M, int N, int K,
-                        int* status) {
+    proj_fp8_few_kernel(const uint8_t* xq, const float* xs, const uint8_t* Wq, const float* Ws, const float* bias,
+                        __nv_bfloat16* y, int M, int N, int K, int* status) {
   __shared__ float part[kFewWarps][8 * NT][17];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int n0 = blockIdx.x * 16, nkb = (K + FBK - 1) / FBK;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;  // no waits here: nothing to report
   const uint8_t* w0 = Wq + (long long)(n0 + g) * K + t * 32;
   const uint8_t* w1 = w0 + 8LL * K;
   const bool has0 = n0 + g < N, has1 = n0 + g + 8 < N;
   const float* ws = Ws + (long long)(n0 / 128) * nkb;
   const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+  depend_launch();
+  // (a kernel that begins while another one writes its inputs takes them by coherent loads alone)
+  // the weights on their way to L2 (where alone they may still be written) while the kernel in front ends
+  for (int kb = warp + kFewWarps * t; kb < nkb; kb += 4 * kFewWarps) {
+    if (has0) asm volatile("prefetch.global.L2 [%0];" ::"l"(w0 - t * 32 + kb * FBK));
+    if (has1) asm volatile("prefetch.global.L2 [%0];" ::"l"(w1 - t * 32 + kb * FBK));
+  }
+  depend_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;  // no waits here: nothing to report
   float acc[NT][4];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
@@ -314,10 +320,10 @@ __global__ void __launch_bounds__(32 * kFewWarps)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const bool in = k + t * 32 + 16 * h < K;
-      a[0][h] = in && has0 ? __ldg(reinterpret_cast<const uint4*>(w0 + k) + h) : z;
-      a[1][h] = in && has1 ? __ldg(reinterpret_cast<const uint4*>(w1 + k) + h) : z;
+      a[0][h] = in && has0 ? *(reinterpret_cast<const uint4*>(w0 + k) + h) : z;
+      a[1][h] = in && has1 ? *(reinterpret_cast<const uint4*>(w1 + k) + h) : z;
     }
-    const float w = __ldg(ws + kb);
+    const float w = ws[kb];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int m = 8 * i + g;
@@ -325,7 +331,7 @@ __global__ void __launch_bounds__(32 * kFewWarps)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         b[h] = m < M && k + t * 32 + 16 * h < K
-                   ? __ldg(reinterpret_cast<const uint4*>(xq + (long long)m * K + t * 32 + k) + h)
+                   ? *(reinterpret_cast<const uint4*>(xq + (long long)m * K + t * 32 + k) + h)
                    : z;
       float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -336,8 +342,8 @@ __global__ void __launch_bounds__(32 * kFewWarps)
         mma_e4m3_16832(d, a1, b[h].z, b[h].w);
       }
       const int c = 8 * i + 2 * t;  // this thread's two tokens
-      const float s0 = c < M ? w * __ldg(xs + (long long)c * nkb + kb) : 0.f;
-      const float s1 = c + 1 < M ? w * __ldg(xs + (long long)(c + 1) * nkb + kb) : 0.f;
+      const float s0 = c < M ? w * xs[(long long)c * nkb + kb] : 0.f;
+      const float s1 = c + 1 < M ? w * xs[(long long)(c + 1) * nkb + kb] : 0.f;
       acc[i][0] = fmaf(s0, d[0], acc[i][0]);
       acc[i][1] = fmaf(s1, d[1], acc[i][1]);
       acc[i][2] = fmaf(s0, d[2], acc[i][2]);
@@ -355,7 +361,7 @@ __global__ void __launch_bounds__(32 * kFewWarps)
     float s = 0.f;
 #pragma unroll
     for (int k = 0; k < kFewWarps; ++k) s += part[k][m][n];
-    y[(long long)m * N + n0 + n] = __float2bfloat16_rn(s + (bias ? __ldg(bias + n0 + n) : 0.f));
+    y[(long long)m * N + n0 + n] = __float2bfloat16_rn(s + (bias ? bias[n0 + n] : 0.f));
   }
 }
 
@@ -426,10 +432,9 @@ int launch_bn(const ProjFp8Params& p, cudaStream_t s) {
 
 template <int NT>
 static int launch_few(const ProjFp8Params& p, cudaStream_t s) {
-  proj_fp8_few_kernel<NT><<<(unsigned)((p.N + 15) / 16), 32 * kFewWarps, 0, s>>>(
-      static_cast<const uint8_t*>(p.xq), p.xs, static_cast<const uint8_t*>(p.Wq), p.Ws, p.bias,
-      static_cast<__nv_bfloat16*>(p.y), p.M, p.N, p.K, p.status);
-  return (int)cudaGetLastError();
+  return launch_dependent(proj_fp8_few_kernel<NT>, (unsigned)((p.N + 15) / 16), 32 * kFewWarps, 0, s,
+                          static_cast<const uint8_t*>(p.xq), p.xs, static_cast<const uint8_t*>(p.Wq), p.Ws, p.bias,
+                          static_cast<__nv_bfloat16*>(p.y), p.M, p.N, p.K, p.status);
 }
 
 int launch_proj_fp8(const ProjFp8Params& p, cudaStream_t s) {
