@@ -2,8 +2,9 @@
 
 Each CUDA translation unit is compiled in parallel with nvcc
 (-gencode arch=compute_103a,code=sm_103a), then linked with the static CUDA
-runtime into sequential_rnn_gb300/libsrnn.so.  Objects go to
-sequential_rnn_gb300/_build/.  Usage:  python -m sequential_rnn_gb300.build
+runtime into sequential_rnn_gb300/libsrnn.so.  Beside it g++ builds _binding.so, the
+language-model operators' Python calls, against the installed PyTorch's headers.
+Objects go to sequential_rnn_gb300/_build/.  Usage:  python -m sequential_rnn_gb300.build
 
 The bounds-check variant (-DRNN_BOUNDS_CHECK: every computed index checked,
 violations reported as RNN_ERR_BOUNDS) goes to libsrnn_bc.so via
@@ -21,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsrnn.so")
+BINDING = os.path.join(PKG, "_binding.so")
 LIB_BC = os.path.join(PKG, "libsrnn_bc.so")
 
 SOURCES = ["capi.cu", "plan.cu", "runtime.cu", "fwd_f32.cu", "fwd_bf16_lstm.cu", "fwd_bf16_gru.cu", "fwd_bf16_slstm.cu",
@@ -39,6 +41,38 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def binding(verbose: bool = False, force: bool = False):
+    """Start the compilation of _binding.so; returns (process or None, the step that finishes it)."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    src, stamp = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, "binding.stamp")
+    header = os.path.join(ROOT, "include", "rnn.h")
+    made_for = f"{torch.__version__} {sys.version}"
+    if not force and os.path.exists(BINDING) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == made_for and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, (src, header))):
+                return None, lambda: None
+    os.makedirs(BUILD, exist_ok=True)
+    inc = os.path.join(base, "include")
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.dirname(header),
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+           src, "-o", BINDING + ".tmp", "-L", os.path.join(base, "lib"),
+           "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+
+    def finish():
+        os.replace(BINDING + ".tmp", BINDING)
+        with open(stamp, "w") as f:
+            f.write(made_for)
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), finish
+
+
 def build(verbose: bool = False, force: bool = False, bounds_check: bool = False) -> str:
     bdir = BUILD + "_bc" if bounds_check else BUILD
     lib = LIB_BC if bounds_check else LIB
@@ -46,10 +80,13 @@ def build(verbose: bool = False, force: bool = False, bounds_check: bool = False
     os.makedirs(bdir, exist_ok=True)
     cc = nvcc()
     srcs = [s for s in SOURCES if os.path.exists(os.path.join(CSRC, s))]
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "rnn.h")]
+    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".cpp")] + [os.path.join(ROOT, "include", "rnn.h")]
     newest_dep = max(os.path.getmtime(f) for f in deps)
     procs = []
     objs = []
+    bind, finish = binding(verbose, force)
+    if bind:
+        procs.append(("binding.cpp", bind))
     for s in srcs:
         obj = os.path.join(bdir, s.replace(".cu", ".o"))
         objs.append(obj)
@@ -68,7 +105,8 @@ def build(verbose: bool = False, force: bool = False, bounds_check: bool = False
             print(out.decode(errors="replace"))
     if failed:
         msg = "\n".join(f"--- {s}\n{o}" for s, o in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
+        raise RuntimeError(f"compilation failed:\n{msg}")
+    finish()
     if force or not os.path.exists(lib) or any(os.path.getmtime(o) > os.path.getmtime(lib) for o in objs):
         cmd = [cc, *ARCH, "-shared", "-o", lib + ".tmp", *objs, "-cudart", "static"]
         r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
