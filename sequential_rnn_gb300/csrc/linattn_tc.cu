@@ -68,6 +68,18 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int c0, int
       "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
       : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
 // 32 bytes to global memory (v8: at a 32-byte boundary, one access)
 __device__ __forceinline__ void store32(void* at, const uint32_t* v, bool v8) {
   if (v8)
@@ -442,7 +454,7 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
 template <int DK>
 struct OutCfg {
   static constexpr int NGW = 8;                          // warps of a group
-  static constexpr int WLOAD = 16, WMMA = 17, THREADS = 32 * 18;
+  static constexpr int WLOAD = 16, WMMA = 17, THREADS = 32 * 20;
   static constexpr uint32_t X = (DK / 64) * kBlkBytes;
   static constexpr int NX = DK == 64 ? 3 : (DK == 128 ? 2 : 1);  // tiles of x and a
   static constexpr uint32_t S = DK * 128;                // DK rows x 64 columns of the state
@@ -489,17 +501,17 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int abort_flag_s;
   __shared__ uint32_t tslot_s;
-  __shared__ __align__(8) uint64_t bars_s[27];
+  __shared__ __align__(8) uint64_t bars_s[29];
   __shared__ OutTile info_s[4];  // what the loading warp tells the others of its tiles, the last four
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bar = smem_u32(bars_s);
   // x, a landed; c, state landed; MMAs done, by buffer of c and state; scores done; scores in
   // bf16; sums read; c's rows behind the last token zeroed; info_s written; sums done, by group and parity of v; c landed
-  // whose rows a group has to zero.  A barrier's waiter waits for every one of its phases in turn (of one that it saw only
+  // whose rows a group has to zero; scores multiplied.  A barrier's waiter waits for every one of its phases in turn (of one that it saw only
   // every other time it would take the phase before for the one that it wants: their parity is all it
   // sees), so what a group waits for has a barrier for each group.
   const uint32_t xF = bar, cF = bar + 24, dn = bar + 48, sc = bar + 72, pW = bar + 88, oR = bar + 104, cZ = bar + 120,
-                 iF = bar + 136, oD = bar + 168, zF = bar + 200;
+                 iF = bar + 136, oD = bar + 168, zF = bar + 200, sF = bar + 216;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nch = (p.T + kTC - 1) / kTC;
   const int vts = p.DV / 64;
@@ -512,27 +524,27 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
   auto ragged = [&](const OutTile& t) {
     return t.len < p.T && t.len < (t.c + 1) * kTC && !((revs >> t.job) & 1);
   };
-  // Tiles in the order pass, chunk, head, row (fastest first: the passes of a chunk read the same
-  // tokens).  A step of the grid is added digit by digit, and by the loading warp alone: the
+  // Tiles in the order pass, head, row, chunk (fastest first), the last chunk first: what the states' kernel touched
+  // last is still in L2.  A step of the grid is added digit by digit, and by the loading warp alone: the
   // divisions of a place cost every role 700 cycles a tile, the digits' walk still 1,400 the MMAs' warp.
   auto digits = [&](int idx) {
     OutTile t;
     t.job = idx % p.npass;
     idx /= p.npass;
-    t.c = idx % nch;
-    idx /= nch;
     t.h = idx % p.NH;
-    t.b = idx / p.NH;
+    idx /= p.NH;
+    t.b = idx % p.B;
+    t.c = nch - 1 - idx / p.B;
     return t;
   };
-  auto advance = [&](OutTile& t, const OutTile& stride) {  // (past the last tile b is past the last row)
+  auto advance = [&](OutTile& t, const OutTile& stride) {  // (past the last tile c is below 0)
     t.job += stride.job;
-    t.c += stride.c;
     t.h += stride.h;
     t.b += stride.b;
-    if (t.job >= p.npass) t.job -= p.npass, ++t.c;
-    if (t.c >= nch) t.c -= nch, ++t.h;
+    t.c -= nch - 1 - stride.c;
+    if (t.job >= p.npass) t.job -= p.npass, ++t.h;
     if (t.h >= p.NH) t.h -= p.NH, ++t.b;
+    if (t.b >= p.B) t.b -= p.B, --t.c;
   };
   // this CTA's tiles that hold tokens
   int count = ((int)blockIdx.x < tiles ? (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0);
@@ -547,7 +559,9 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < 11; ++i) mbar_init(bar + 8 * i, 1);
     for (int i = 11; i < 17; ++i) mbar_init(bar + 8 * i, C::NGW);
-    for (int i = 17; i < 27; ++i) mbar_init(bar + 8 * i, 1);
+    for (int i = 17; i < 29; ++i) mbar_init(bar + 8 * i, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(dn + 8 * i, 2);  // (P c's and x S's)
+    for (int i = 0; i < 4; ++i) mbar_init(oD + 8 * i, 2);
     abort_flag_s = 0;
     fence_mbar_init();
     fence_async_smem();
@@ -596,6 +610,20 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
           tma_load_4d(d + C::X + i * kBlkBytes, &m.a[j], 64 * i, t.h * m.ah[j], t.b * m.ab[j], tok, xF + 8 * s);
         }
       };
+      // With one buffer of x and a, the next tile's operands on their way to L2 while this one's are multiplied (from
+      // DRAM, its x and a took 7,000 cycles in which nothing else ran).
+      auto prefetch = [&](const OutTile& t, int v) {
+        const int j = t.job, tok = token_of(t);
+        if (tok < 0) return;
+        if (v == 0)
+#pragma unroll
+          for (int i = 0; i < DK / 64; ++i) {
+            tma_prefetch_4d(&m.x[j], 64 * i, t.h * m.xh[j], t.b * m.xb[j], tok);
+            tma_prefetch_4d(&m.a[j], 64 * i, t.h * m.ah[j], t.b * m.ab[j], tok);
+          }
+        tma_prefetch_2d(&m.s_load, 64 * v, (((j * p.B + t.b) * p.NH + t.h) * nch + t.c) * DK);
+        tma_prefetch_4d(&m.c[j], 64 * v, t.h * m.ch[j], t.b * m.cb[j], tok);
+      };
       // in the order in which the MMAs take them (the next tile's scores follow this one's first product
       // with the state): a copy whose buffer a later MMA has to free must not stand before one that this MMA needs
       OutTile t, tn;
@@ -619,6 +647,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
             tn = next();
             if (NX > 1) load_xa(tn, k + 1);
           }
+          if (NX == 1 && k + 1 < count) prefetch(tn, v);
         }
         if (NX == 1 && ok && k + 1 < count) load_xa(tn, k + 1);
         t = tn;
@@ -629,13 +658,18 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (warp == C::WMMA) {
+  } else if (warp >= C::WMMA) {
     // -------------------------------------------------------------- MMAs --
-    if (lane == 0) {
-      uint32_t nz[2] = {0, 0};  // c tiles with rows zeroed, by group
-      auto scores = [&](int k) {
-        constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
+    // Three warps issue, a product each, as soon as its own operands are there: one that issued all three held this
+    // tile's P c back until the next tile's x and a had landed, 4,500 cycles of a tile's 7,000, and stood still
+    // for the waits (100 cycles even when a phase is over) and commits (120).
+    if (lane == 0 && warp == C::WMMA) {  // scores
+      constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
+      for (int k = 0; k < count; ++k) {
         const uint32_t x = sm + (k % NX) * (2 * C::X), a = x + C::X;
+        if (!wait(xF + 8 * (k % NX), (k / NX) & 1)) break;
+        if (k >= 2 && !wait(sF + 8 * (k & 1), ((k - 2) >> 1) & 1)) break;
+        tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks) {
           const uint32_t o = (uint32_t)(ks / 4) * kBlkBytes + (ks % 4) * 32;
@@ -643,53 +677,54 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
                     ks != 0);
         }
         umma_commit(sc + 8 * (k & 1));
-      };
-      auto landed = [&](int k) {  // x, a and the description of tile k
-        const bool l = wait(xF + 8 * (k % NX), (k / NX) & 1);
-        tc_fence_after();
-        return l;
-      };
-      bool ok = count > 0 && landed(0);
-      if (ok) scores(0);
+      }
+    } else if (lane == 0 && warp == C::WMMA + 1) {  // P c
+      constexpr uint32_t idesc = idesc_bf16_f32(128, 64, false, true);
+      uint32_t nz[2] = {0, 0};  // c tiles with rows zeroed, by group
+      bool ok = true;
       int f = 0;
       for (int k = 0; ok && k < count; ++k) {
-        const OutTile t = info_s[k & 3];
-        const uint32_t x = sm + (k % NX) * (2 * C::X);
-        const bool zeroed = ragged(t);
-        for (int v = 0; ok && v < vts; ++v, ++f) {
+        if (!(ok = wait(pW + 8 * (k & 1), (k >> 1) & 1))) break;
+        const bool zeroed = ragged(info_s[k & 3]);
+        for (int v = 0; v < vts; ++v, ++f) {
           const int cb = f % NCS, o = f & 1;
           if (!(ok = wait(cF + 8 * cb, (f / NCS) & 1))) break;
-          if (zeroed) mbar_arrive(zF + 8 * (k & 1));
+          if (zeroed) {
+            mbar_arrive(zF + 8 * (k & 1));
+            if (!(ok = wait(cZ + 8 * (k & 1), nz[k & 1]++ & 1))) break;
+          }
           if (f >= 2 && !(ok = wait(oR + 8 * o, ((f - 2) >> 1) & 1))) break;
           tc_fence_after();
-          constexpr uint32_t idesc = idesc_bf16_f32(128, 64, false, true);
-          const uint32_t tO = tmem + 256 + o * 128, st = sm + C::cs_at(cb), cc = st + C::S;
-#pragma unroll
-          for (int ks = 0; ks < DK / 16; ++ks)
-            umma_bf16(tO + 64, sdesc_sw128(x + (uint32_t)(ks / 4) * kBlkBytes + (ks % 4) * 32, 16, 1024),
-                      sdesc_sw128(st + ks * 2048, kBlkBytes, 1024), idesc, ks != 0);
-          if (v == 0) {
-            if (NX > 1 && k + 1 < count) {
-              // the next tile's scores, over those that the previous tile's MMAs have read
-              if (!(ok = landed(k + 1))) break;
-              if (k >= 1 && !(ok = wait(dn + 8 * ((f - 1) % NCS), ((f - 1) / NCS) & 1))) break;
-              tc_fence_after();
-              scores(k + 1);
-            }
-            if (!(ok = wait(pW + 8 * (k & 1), (k >> 1) & 1))) break;
-          }
-          if (zeroed && !(ok = wait(cZ + 8 * (k & 1), nz[k & 1]++ & 1))) break;
-          tc_fence_after();
+          const uint32_t cc = sm + C::cs_at(cb) + C::S;
 #pragma unroll
           for (int ks = 0; ks < kTC / 16; ++ks)
-            umma_bf16_ts(tO, tmem + (k & 1) * 128 + ks * 8, sdesc_sw128(cc + ks * 2048, kBlkBytes, 1024), idesc,
-                         ks != 0);
+            umma_bf16_ts(tmem + 256 + o * 128, tmem + (k & 1) * 128 + ks * 8,
+                         sdesc_sw128(cc + ks * 2048, kBlkBytes, 1024), idesc, ks != 0);
           umma_commit(oD + 8 * (2 * (k & 1) + (v & 1)));
           umma_commit(dn + 8 * cb);
         }
-        if (NX == 1 && ok && k + 1 < count) {
-          if (!(ok = landed(k + 1))) break;
-          scores(k + 1);
+        if (ok) umma_commit(sF + 8 * (k & 1));
+      }
+    } else if (lane == 0) {  // x S
+      constexpr uint32_t idesc = idesc_bf16_f32(128, 64, false, true);
+      bool ok = true;
+      int f = 0;
+      for (int k = 0; ok && k < count; ++k) {
+        if (!(ok = wait(xF + 8 * (k % NX), (k / NX) & 1))) break;
+        const uint32_t x = sm + (k % NX) * (2 * C::X);
+        for (int v = 0; v < vts; ++v, ++f) {
+          const int cb = f % NCS, o = f & 1;
+          if (!(ok = wait(cF + 8 * cb, (f / NCS) & 1))) break;
+          if (f >= 2 && !(ok = wait(oR + 8 * o, ((f - 2) >> 1) & 1))) break;
+          tc_fence_after();
+          const uint32_t st = sm + C::cs_at(cb);
+#pragma unroll
+          for (int ks = 0; ks < DK / 16; ++ks)
+            umma_bf16(tmem + 256 + o * 128 + 64,
+                      sdesc_sw128(x + (uint32_t)(ks / 4) * kBlkBytes + (ks % 4) * 32, 16, 1024),
+                      sdesc_sw128(st + ks * 2048, kBlkBytes, 1024), idesc, ks != 0);
+          umma_commit(oD + 8 * (2 * (k & 1) + (v & 1)));
+          umma_commit(dn + 8 * cb);
         }
       }
     }
