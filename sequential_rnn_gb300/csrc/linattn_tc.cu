@@ -68,18 +68,6 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int c0, int
       "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
       : "memory");
 }
-__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
-  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-               : "memory");
-}
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(c0), "r"(c1)
-               : "memory");
-}
 // 32 bytes to global memory (v8: at a 32-byte boundary, one access)
 __device__ __forceinline__ void store32(void* at, const uint32_t* v, bool v8) {
   if (v8)
@@ -610,20 +598,6 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
           tma_load_4d(d + C::X + i * kBlkBytes, &m.a[j], 64 * i, t.h * m.ah[j], t.b * m.ab[j], tok, xF + 8 * s);
         }
       };
-      // With one buffer of x and a, the next tile's operands on their way to L2 while this one's are multiplied (from
-      // DRAM, its x and a took 7,000 cycles in which nothing else ran).
-      auto prefetch = [&](const OutTile& t, int v) {
-        const int j = t.job, tok = token_of(t);
-        if (tok < 0) return;
-        if (v == 0)
-#pragma unroll
-          for (int i = 0; i < DK / 64; ++i) {
-            tma_prefetch_4d(&m.x[j], 64 * i, t.h * m.xh[j], t.b * m.xb[j], tok);
-            tma_prefetch_4d(&m.a[j], 64 * i, t.h * m.ah[j], t.b * m.ab[j], tok);
-          }
-        tma_prefetch_2d(&m.s_load, 64 * v, (((j * p.B + t.b) * p.NH + t.h) * nch + t.c) * DK);
-        tma_prefetch_4d(&m.c[j], 64 * v, t.h * m.ch[j], t.b * m.cb[j], tok);
-      };
       // in the order in which the MMAs take them (the next tile's scores follow this one's first product
       // with the state): a copy whose buffer a later MMA has to free must not stand before one that this MMA needs
       OutTile t, tn;
@@ -647,7 +621,6 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
             tn = next();
             if (NX > 1) load_xa(tn, k + 1);
           }
-          if (NX == 1 && k + 1 < count) prefetch(tn, v);
         }
         if (NX == 1 && ok && k + 1 < count) load_xa(tn, k + 1);
         t = tn;
