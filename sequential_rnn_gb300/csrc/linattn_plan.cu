@@ -6,11 +6,21 @@ namespace srnn {
 
 LinAttnPlan linattn_plan(bool bf16, int npass, int T, int B, int NH, int DK, int DV) {
   LinAttnPlan pl{};
-  // tcgen05 from the lengths on where it is the faster (us, 8 rows unless said; mma.sync / tcgen05): 6 x 128,
-  // T = 128 13.5 / 17.0, T = 256 21.5 / 18.8, 16 rows of 1024 108 / 63; 4 x 256, T = 256 29.9 / 29.3, 4 rows of 4096 370 /
-  // 98.  With 64 columns of x and a, whose products are small, the gradient's passes gain on long rows only
-  // (16 rows of 1024 104 / 113, 4 rows of 4096 154 / 123), the forward's does not (1 row of 4096 24.8 / 34.1).
-  const bool tc = DK % 64 == 0 && DV % 64 == 0 && (DK == 64 ? npass > 1 && T >= 2048 : T >= 256);
+  // tcgen05 where it is the faster (us, mma.sync / tcgen05, T x rows x heads x Dk x Dv unless said).  Both sizes 128
+  // or more: from 256 tokens on (256x8x6x128x128 20.6 / 16.7, its gradient 39 / 25; 256x8x4x256x256 27.8 / 25.1; the
+  // same at 128 tokens 17.2 / 20.9).  Dk = 64, whose products with a are small, against wider values: the gradient from
+  // 256 tokens on (256x8x8x64x128 32.4 / 31.2, 1024x16 187 / 115), the forward pass with enough work (1024x16x8 52.9 /
+  // 46.1, 16384x1x8 70.9 / 62.7; 512x16x8 28.7 / 29.0, 2048x1x8 20.1 / 25.2).  64 x 64: the gradient's passes on long rows
+  // (4096x4x12 147 / 124; 2048x8x12 100 / 109), the forward pass with many long rows (2048x8x12 66.4 / 55.3,
+  // 1024x16x12 53.2 / 48.4; 4096x4x12 64.5 / 66.9, 16384x1x12 54.8 / 61.2).
+  const long long heads = (long long)B * NH;
+  bool tc = DK % 64 == 0 && DV % 64 == 0;
+  if (DK > 64)
+    tc = tc && T >= 256;
+  else if (DV > 64)
+    tc = tc && (npass > 1 ? T >= 256 : T >= 1024 && T * heads >= 65536);
+  else
+    tc = tc && (npass > 1 ? T >= 4096 : T >= 1024 && heads >= 96);
   pl.path = !bf16 ? kLinAttnF32 : (tc ? kLinAttnTc : kLinAttnMma);
   int chunk, tiles, occ;  // tokens per chunk, state tiles per head, CTAs per SM
   if (pl.path == kLinAttnTc) {

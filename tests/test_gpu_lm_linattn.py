@@ -169,6 +169,16 @@ def test_many_tiles_per_cta(S, T, B, NH, Dk, Dv, ragged):
             assert (a[i] - b[i]).norm() <= tol * b[i].norm(), (n, row)
 
 
+@pytest.mark.parametrize("T,B,NH,Dk,Dv", [(300, 3, 2, 64, 128), (300, 3, 2, 64, 256), (300, 3, 2, 128, 64),
+                                          (300, 3, 2, 256, 64), (1030, 8, 12, 64, 64), (1025, 13, 5, 64, 128)])
+def test_unequal_head_sizes_and_many_heads(S, T, B, NH, Dk, Dv):
+    """The lengths and numbers of heads from which on other kernels take 64 columns, with ragged rows."""
+    d = draw(T + Dk + Dv, T, B, NH, Dk, Dv, "bf16", lens=[T, 129, 0] + [T - 7 * b for b in range(B - 3)])
+    check_forward(S, d, "bf16")
+    if T < 1000:
+        check_backward(S, d, "bf16")
+
+
 def test_state_in_place_across_segments(S):
     """The final state may be written over the initial one."""
     for T in (64, 3000):
