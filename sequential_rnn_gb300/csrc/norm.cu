@@ -3,7 +3,8 @@
 //
 //   h = round(x + residual);  r = 1 / sqrt(mean_n h^2 + eps);  y = h r w
 //   8-bit output: per row and block of 128 columns s = max|y| / 448 (1 where
-//   the block is all zero), q = e4m3(y / s)
+//   the block is all zero), q = e4m3(y / s), the code nearest to the exact quotient:
+//   r cancels, y / s = 448 h w / max|h w|
 //   gradient, xh = h r:  dx = r (w dy - xh mean_n(w dy xh)) + dh,
 //                        dw = sum over rows of dy xh
 //
@@ -52,6 +53,96 @@ __device__ __forceinline__ float block_scale(float top) {
   return s > 0.f ? s : 1.f;
 }
 
+// The codes of E of a block's 128 columns, together with the LANES neighbouring threads of its other columns: t = h w in
+// fp32, its products with the ends of an interval of 448 / max|t| that is wider than the five roundings between
+// them and the exact quotient (5 2^-24).  Where both give the same code (lo, hi) the quotient does, too.
+template <int E, int LANES>
+__device__ __forceinline__ void quantize_ends(const float (&h)[E], const float (&w)[E], uint32_t (&lo)[E / 4],
+                                              uint32_t (&hi)[E / 4], float& top) {
+  float t[E];
+  top = 0.f;
+#pragma unroll
+  for (int j = 0; j < E; ++j) {
+    t[j] = h[j] * w[j];
+    top = fmaxf(top, fabsf(t[j]));
+  }
+#pragma unroll
+  for (int o = LANES / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float inv = kE4m3Max / top, a = inv * (1.f - 0x1p-21f), b = inv * (1.f + 0x1p-21f);
+#pragma unroll
+  for (int j = 0; j < E; j += 4) {
+    lo[j / 4] = pack_e4m3(t[j] * a, t[j + 1] * a, t[j + 2] * a, t[j + 3] * a);
+    hi[j / 4] = pack_e4m3(t[j] * b, t[j + 1] * b, t[j + 2] * b, t[j + 3] * b);
+  }
+}
+__device__ __forceinline__ bool in_range(float v) { return v >= 0x1p-60f && v <= 0x1p60f; }
+// Codes and scale where the ends agree; false where they do not or the numbers leave the range.  (A division in fp32
+// for each value instead took half of the kernel's time, and, with y and s rounded before it, put every
+// millionth value on the other side of a tie.)
+template <int E, int LANES>
+__device__ __forceinline__ bool quantize_fast(const float (&h)[E], const float (&w)[E], float r, uint32_t (&q)[E / 4],
+                                              float& s) {
+  float top;
+  uint32_t hi[E / 4];
+  quantize_ends<E, LANES>(h, w, q, hi, top);
+  s = top * r * (1.f / kE4m3Max);
+  bool ok = in_range(top) && in_range(r);
+  if (top == 0.f && r <= 0x1p60f) {  // (r is not a number where h has one)
+    s = 1.f, ok = true;
+#pragma unroll
+    for (int j = 0; j < E / 4; ++j) q[j] = hi[j] = 0u;
+  }
+#pragma unroll
+  for (int j = 0; j < E / 4; ++j) ok &= q[j] == hi[j];
+  return ok;
+}
+// The same where they do not, by the whole warp (one row in 170 of 768 columns): the quotient in 64 bits.
+template <int E, int LANES>
+__device__ __forceinline__ void quantize_exact(const float (&h)[E], const float (&w)[E], float r, uint32_t (&q)[E / 4],
+                                               float& s) {
+  float top;
+  uint32_t hi[E / 4];
+  quantize_ends<E, LANES>(h, w, q, hi, top);
+  // what rounding took from the largest product
+  float rest = -1.f;
+#pragma unroll
+  for (int j = 0; j < E; ++j) {
+    const float t = h[j] * w[j], e = fmaf(h[j], w[j], -t);
+    if (fabsf(t) == top) rest = fmaxf(rest, (t < 0.f ? -e : e) / top);
+  }
+#pragma unroll
+  for (int o = LANES / 2; o; o >>= 1) rest = fmaxf(rest, __shfl_xor_sync(0xffffffffu, rest, o));
+  s = top * r * (1.f / kE4m3Max);
+  if (__all_sync(0xffffffffu, in_range(top) && in_range(r))) {
+    const double f = kE4m3Max / ((double)top + (double)rest * top);
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const int at = 8 * (j % 4);
+      if (((q[j / 4] ^ hi[j / 4]) >> at & 0xffu) == 0) continue;
+      const uint32_t c = to_e4m3((float)((double)h[j] * w[j] * f));
+      q[j / 4] = (q[j / 4] & ~(0xffu << at)) | c << at;
+    }
+    return;
+  }
+  // zeros, products or scales near the ends of fp32's range, values that are not finite
+  double top64 = 0.0;
+#pragma unroll
+  for (int j = 0; j < E; ++j) top64 = fmax(top64, fabs((double)h[j] * w[j]));
+#pragma unroll
+  for (int o = LANES / 2; o; o >>= 1) top64 = fmax(top64, __shfl_xor_sync(0xffffffffu, top64, o));
+  s = (float)(top64 * r / kE4m3Max);
+  double f = kE4m3Max / top64;
+  if (!(s >= 0x1p-126f)) f = s > 0.f ? (double)r / s : r;  // (a subnormal scale is coarse: the quotient by what is stored)
+  if (!(s > 0.f)) s = 1.f;  // zeros, values that underflow, a row whose r is zero or not a number
+#pragma unroll
+  for (int j = 0; j < E; j += 4) {
+    float c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] = (float)((double)h[j + k] * w[j + k] * f);
+    q[j / 4] = pack_e4m3(c[0], c[1], c[2], c[3]);
+  }
+}
+
 // sum over the block's threads (a multiple of 32), the same value in each
 __device__ __forceinline__ float block_sum(float v, float* red) {
 #pragma unroll
@@ -86,19 +177,17 @@ __global__ void __launch_bounds__(256) norm_any_kernel(const NormParams p) {
     const int nblk = (N + kBlk - 1) / kBlk, lane = threadIdx.x & 31;
     // a warp takes whole blocks of 128 columns; h is written last, since it may be x or residual
     for (int b = threadIdx.x >> 5; b < nblk; b += 8) {
-      float hv[4], y[4], top = 0.f;
+      float hv[4], w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int n = b * kBlk + 32 * j + lane;
         hv[j] = n < N ? rounded<T>(load1(x + n) + (res ? load1(res + n) : 0.f)) : 0.f;
-        y[j] = n < N ? hv[j] * r * p.weight[n] : 0.f;
-        top = fmaxf(top, fabsf(y[j]));
+        w[j] = n < N ? p.weight[n] : 0.f;
       }
-      float s = 1.f;
+      uint32_t q[1];
       if (p.scale) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        s = block_scale(top);
+        float s;
+        if (__any_sync(0xffffffffu, !quantize_fast<4, 32>(hv, w, r, q, s))) quantize_exact<4, 32>(hv, w, r, q, s);
         if (lane == 0) p.scale[row * nblk + b] = s;
       }
 #pragma unroll
@@ -106,9 +195,9 @@ __global__ void __launch_bounds__(256) norm_any_kernel(const NormParams p) {
         const int n = b * kBlk + 32 * j + lane;
         if (n >= N) continue;
         if (p.scale)
-          static_cast<uint8_t*>(p.y)[row * N + n] = to_e4m3(y[j] / s);
+          static_cast<uint8_t*>(p.y)[row * N + n] = (uint8_t)(q[0] >> (8 * j));
         else
-          store1(static_cast<T*>(p.y) + row * N + n, y[j]);
+          store1(static_cast<T*>(p.y) + row * N + n, hv[j] * r * w[j]);
         if (h) store1(h + n, hv[j]);
       }
     }
@@ -196,6 +285,23 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+// quantize_exact() for a vector of h and its weights: out of line, so that the rows which need it fetch little code
+struct Codes {
+  uint32_t q[2];
+  float s;
+};
+template <class T>
+__device__ __noinline__ Codes exact_codes(uint4 h, const float* weight, float r) {
+  constexpr int E = Vec<T>::E;
+  float y[E], w[E];
+  uint32_t q[E / 4];
+  Codes c;
+  load_weight<E>(weight, 0, w);
+  Vec<T>::unpack(h, y);
+  quantize_exact<E, kBlk / E>(y, w, r, q, c.s);
+  c.q[0] = q[0], c.q[1] = q[E / 4 - 1];
+  return c;
+}
 constexpr int kRowsPerCta = 8;  // warp-per-row kernels: 256 threads
 constexpr int kNormCtas = 2;    // their CTAs per SM
 
@@ -255,6 +361,16 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024, WARP ? kNormCtas : 1) norm_
     const float sum = WARP ? warp_sum(ss) : block_sum(ss, red);
     const float r = rsqrtf(sum / (float)p.N + p.eps);
     if (p.rstd && t == 0) p.rstd[row] = r;
+    uint32_t bad = 0;  // vectors to be done again
+    auto store_block = [&](int v, const uint32_t* q, float s) {
+      if (v >= nv) return;
+      if (v % (kBlk / E) == 0) p.scale[row * ((p.N + kBlk - 1) / kBlk) + v / (kBlk / E)] = s;
+      uint8_t* dst = static_cast<uint8_t*>(p.y) + row * p.N + v * E;
+      if constexpr (E == 8)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+      else
+        *reinterpret_cast<uint32_t*>(dst) = q[0];
+    };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = t + i * TPR;
@@ -262,40 +378,28 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024, WARP ? kNormCtas : 1) norm_
       float y[E];
       if (!WARP) load_weight<E>(p.weight, (v < nv ? v : 0) * E, w[0]);
       Vec<T>::unpack(cur[i], y);
-      // (past the row h is zero)
+      if constexpr (QUANT) {  // (past the row h is zero)
+        uint32_t q[E / 4];
+        float s;
+        bad |= (quantize_fast<E, kBlk / E>(y, w[WARP ? i : 0], r, q, s) ? 0u : 1u) << i;
+        store_block(v, q, s);
+      } else {
 #pragma unroll
-      for (int j = 0; j < E; ++j) y[j] = v < nv ? y[j] * r * w[WARP ? i : 0][j] : 0.f;
-      if (!QUANT) {
+        for (int j = 0; j < E; ++j) y[j] = y[j] * r * w[WARP ? i : 0][j];
         reinterpret_cast<uint4*>(p.y)[row * nv + v] = Vec<T>::pack(y);
-        continue;
       }
-      float top = 0.f;
+    }
+    if constexpr (QUANT) {
+      if (__any_sync(0xffffffffu, bad)) {
+        bad = __reduce_or_sync(0xffffffffu, bad);
 #pragma unroll
-      for (int j = 0; j < E; ++j) top = fmaxf(top, fabsf(y[j]));
-#pragma unroll
-      for (int o = kBlk / E / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float s = block_scale(top);
-      // q = e4m3(y / s) with one division for the block (one for each value took half of the time): y times
-      // the ends of an interval of 1/s that is wider than the three roundings between them and y / s (3 2^-24).
-      // Where both products give the same code so does the quotient; about one warp in 500 has to divide.
-      const float inv = 1.f / s, lo = inv * (1.f - 0x1p-22f), hi = inv * (1.f + 0x1p-22f);
-      if (v >= nv) continue;
-      if (v % (kBlk / E) == 0) p.scale[row * ((p.N + kBlk - 1) / kBlk) + v / (kBlk / E)] = s;
-      uint32_t q[E / 4], differ = s < 0x1p-126f;  // (1/s of a subnormal s may be infinite)
-#pragma unroll
-      for (int j = 0; j < E; j += 4) {
-        q[j / 4] = pack_e4m3(y[j] * lo, y[j + 1] * lo, y[j + 2] * lo, y[j + 3] * lo);
-        differ |= q[j / 4] ^ pack_e4m3(y[j] * hi, y[j + 1] * hi, y[j + 2] * hi, y[j + 3] * hi);
+        for (int i = 0; i < NV; ++i) {
+          if (!(bad >> i & 1)) continue;
+          const int v = t + i * TPR;
+          const Codes c = exact_codes<T>(cur[i], p.weight + (v < nv ? v : 0) * E, r);
+          store_block(v, c.q, c.s);
+        }
       }
-      if (differ) {
-#pragma unroll
-        for (int j = 0; j < E; j += 4) q[j / 4] = pack_e4m3(y[j] / s, y[j + 1] / s, y[j + 2] / s, y[j + 3] / s);
-      }
-      uint8_t* dst = static_cast<uint8_t*>(p.y) + row * p.N + v * E;
-      if constexpr (E == 8)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
-      else
-        *reinterpret_cast<uint32_t*>(dst) = q[0];
     }
     if (!WARP) break;  // (a CTA has one row)
   }

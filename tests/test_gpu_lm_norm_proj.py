@@ -76,17 +76,20 @@ def test_rms_norm_8bit(S, rows, N, dtype):
     assert out["scale"][0, 0] == 1 and not np64(out["y"])[0, :min(N, 128)].any()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("small", [1.0, 2.0 ** -114, 2.0 ** -128, 2.0 ** -135])
 @pytest.mark.parametrize("rows,N", [(2000, 768), (700, 1001), (40, 8192), (5, 16512)])
-def test_rms_norm_8bit_codes_are_those_of_the_quotient(S, rows, N, small):
-    """y / scale as fp32 divides, rounded once: equal codes, at every magnitude a scale can have."""
-    x, w = rand(60, rows, N), rand(61, N, scale=small)
+def test_rms_norm_8bit_codes_are_the_nearest(S, rows, N, small, dtype):
+    """y / scale = 448 h w / max|h w|, of which 64 bits hold the products exactly, rounded to fp32 and then to 8
+    bits: equal codes, at every magnitude a scale can have (by a subnormal one, which is coarse, the quotient is that of
+    what is stored)."""
+    x, w = rand(60, rows, N, dtype=dtype), rand(61, N, scale=small)
     out = S.rms_norm(x, w, quantize=True, train=True)
-    y = x.cpu().numpy() * out["rstd"].cpu().numpy()[:, None] * w.cpu().numpy()
-    s = np.repeat(out["scale"].cpu().numpy(), 128, 1)[:, :N]
-    q = torch.from_numpy(y / s).to(torch.float8_e4m3fn)
+    hw, s = np64(x) * np64(w), np.repeat(np64(out["scale"]), 128, 1)[:, :N]
+    pad = np.pad(np.abs(hw), ((0, 0), (0, -N % 128))).reshape(rows, -1, 128).max(2)
+    q = np.where(s >= 2.0 ** -126, 448 * hw / np.repeat(pad, 128, 1)[:, :N], hw * (np64(out["rstd"])[:, None] / s))
     assert (s < 2.0 ** -126).any() == (small < 2.0 ** -120)
-    assert torch.equal(out["y"].cpu().view(torch.uint8), q.view(torch.uint8))
+    assert np.array_equal(np64(out["y"]), O.e4m3(q.astype(np.float32)))
 
 
 def test_rms_norm_leading_dimensions_in_place_and_empty(S):
