@@ -287,8 +287,8 @@ int rnn_fwd_noalloc(const rnn_desc_t* desc, const void* Wx, const void* R, const
  * norm is taken of h as stored.  rstd [rows] fp32 (NULL = not written) is r, for the
  * gradient.  scale NULL: y has dtype.  Otherwise y is 8-bit floating point (e4m3)
  * and scale [rows, ceil(N/128)] fp32 holds, for each row and block of 128
- * columns, max|y| / 448 (1 where that is zero); y holds y / scale, rounded
- * to nearest even.  N == 0 is refused, rows == 0 a no-op.  Any N; widths that are
+ * columns, max|y| / 448 (1 where that is zero); y holds the exact quotient y / scale,
+ * rounded to fp32 and then to e4m3 (to nearest even).  N == 0 is refused, rows == 0 a no-op.  Any N; widths that are
  * a multiple of 16 bytes (of 8 values for e4m3) with 16-byte aligned pointers
  * run the vector kernels.  Alignment: the element's.  No workspace, no device status. */
 int rnn_rms_norm(int32_t dtype, int32_t rows, int32_t N, float eps, const void* x,
@@ -329,11 +329,11 @@ int rnn_input_proj_fp8(int32_t M, int32_t N, int32_t K, const void* xq, const fl
  * log_decay [NH] fp32, <= 0 (a constant of the layer: no gradient; -inf forgets all);
  * state0, stateT [B, NH, Dk, Dv] fp32 (NULL = zero / not written; stateT may be state0).
  * lens [B] int32 (NULL = T for every row): tokens of a row that count, taken as at
- * least 0 and at most T; the others are not read, their outputs are zero, and
+ * least 0 and at most T; what the others hold does not matter, their outputs are zero, and
  * stateT is the state after the last one that counts.
  * Operands may be strided views (of one fused projection, say): strides in elements
  * for (token, row, head), the innermost dimension contiguous; st NULL = contiguous.
- * RNN_BF16: tokens are taken in chunks of 64 on the tensor cores, scores and the
+ * RNN_BF16: tokens are taken in chunks of 64 or 128 on the tensor cores, scores and the
  * state as an operand rounded to bf16 once, all sums and the state fp32.  A v that is not finite can reach
  * the outputs of earlier tokens of its chunk.  RNN_F32: fp32 throughout.
  * Alignment: 16 bytes for tensors and strides, 4 for log_decay and lens, workspace 256

@@ -15,12 +15,18 @@
 // keeps; a chunk's products with the three accumulate from zero in TMEM, and their
 // sum, smallest first, joins the decayed state in round-to-nearest.
 //
-// In both kernels one warp loads (TMA, one lane), one issues the MMAs (one lane), and
+// In both kernels one warp loads (TMA, one lane), one (outputs: three) issues the MMAs (one lane), and
 // the others compute (terms of c, decay and mask of the scores, state and output
 // epilogues); mbarriers order them.  Tiles are rows of 64 values (128 bytes, 128-byte
 // swizzle): the same tile is a K-major operand (scores) and an MN-major one (state
 // update, P c, x S).  Loading through the copy engine matters: with cp.async from all threads
 // the copies of a tile took longer to issue (2,000-2,600 cycles) than its MMAs to run.
+//
+// Measured: 4 x 256, 4 rows of 4096 89-91 us (states 50, outputs 46 alone); gradient 6 x 128, 4 rows of 2001 57
+// us (28 and 32).  The states are bound by what a chunk makes the compute warps do one after the other (terms of c, 3 x 128
+// columns of sums out of TMEM, the state's stores: issue slots 55%, load and store unit 63%), the outputs by
+// the copies (320 KB a tile with 256 columns, half of it from DRAM: inputs, outputs and chunk states are 200 MB
+// beside 129 of L2) and the chain from a tile's scores to its stores.
 //
 // A pass with reversed time loads the same ascending token rows (a box that begins before
 // token 0 reads zeros there): row i of a chunk is then its token 127 - i, and the mask

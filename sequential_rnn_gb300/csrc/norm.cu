@@ -11,6 +11,11 @@
 // The norm is taken of h as it is stored (rounded to the input type), so that
 // the gradient, which reads the stored h, differentiates the very function that
 // was computed.  All sums are fp32.
+//
+// Both are bound by their bytes.  Rows of up to 128 vectors take a warp each, persistent, with the weights (gradient:
+// the columns' share of dw) in registers and the next row's loads in flight: 16384 x 768 to 8 bits 18.2 us,
+// 4.9 TB/s of the copy's 6.8 (a row a launch's warp, without the next row's loads: 19.4 on the device against 17.2);
+// gradient, 16384 x 1000, 30.9 us, 4.2 TB/s.  Wider rows take a CTA, which registers hold as well.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>

@@ -200,6 +200,14 @@ def test_input_proj_fp8(S, M, N, K):
     assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + U * mag).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(16, 4872, 272), (17, 4864, 144), (17, 4872, 144), (40, 4872, 272), (64, 6000, 128)])
+def test_input_proj_fp8_few_rows_of_many_columns(S, M, N, K):
+    """Both sides of the places where another kernel takes over."""
+    (xq, xs, wq, ws, b), (want, mag) = operands(M, N, K, M + N + K)
+    got = np64(S.input_proj_fp8(xq, xs, wq, ws, b))
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + U * mag).all()
+
+
 def test_input_proj_fp8_row_isolation_and_no_rows(S):
     """A row of NaN stays in its row; nothing is done for no rows."""
     (xq, xs, wq, ws, b), _ = operands(130, 200, 384, 5)
