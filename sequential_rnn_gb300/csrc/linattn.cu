@@ -18,8 +18,8 @@
 // A CTA takes a head of a row (of up to 64 columns of c) and walks its chunks, warps side by side over 16 rows of
 // the output and 16 of the state.  Bound by latency: a chunk is a chain of copies, three products that depend on one
 // another and a barrier, with 12 warps an SM (168 registers each) to fill it; the tensor cores run at 42% of
-// mma.sync's rate, DRAM at 26% of its.  Measured, 12 heads of 64: 1 x 16384 tokens 57.4 us (in 37 segments), 16 x
-// 1024 gradient 104.6, five ragged rows of up to 333 18.4.
+// mma.sync's rate, DRAM at 26% of its.  Measured, 12 heads of 64: 1 x 16384 tokens 55.5 us (in 37 segments), 16 x
+// 1024 gradient 104.6, five ragged rows of up to 333 14.3.
 //
 // Rounding: the scores times their decay, and the state as an operand of q S,
 // are rounded to bf16, once each (as bf16 results are); every sum is fp32.  The
@@ -104,6 +104,10 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
   const uint32_t sS = sm + 2 * C::STAGE;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g0 = lane >> 2, t0 = 2 * (lane & 3);
+  if (STATE_ONLY || p.nseg == 1) {  // the call's first kernel
+    depend_wait();
+    depend_launch();
+  }
   const int VT = p.DV / DVT;
   const Where w = where_of(p, VT, STATE_ONLY ? p.nseg - 1 : p.nseg);
   const LinAttnPass& ps = p.pass[w.job];
@@ -113,7 +117,6 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
   const int c1 = c0 + p.seg_chunks < nch ? c0 + p.seg_chunks : nch;
   const int lch = (len + kC - 1) / kC;
   const int cend = c1 < lch ? c1 : lch;  // chunks c0 .. cend - 1 hold tokens
-  if (STATE_ONLY) depend_launch();
   if (STATE_ONLY && (long long)c1 * kC >= len) return;  // no later segment starts from it
   const float lg = p.log_decay[w.h] * 1.4426950408889634f;
   const bool rev = ps.reverse != 0;
@@ -414,21 +417,21 @@ int launch_cfg(const LinAttnParams& p, cudaStream_t s) {
   if (p.nseg > 1) {
     e = prepare_launch(prep_state, linattn_kernel<C, true>, C::SMEM_STATE, C::NT, 1);
     if (e != 0) return e;
-    linattn_kernel<C, true><<<(unsigned)(base * (p.nseg - 1)), C::NT, C::SMEM_STATE, s>>>(p);
+    e = launch_dependent(linattn_kernel<C, true>, (unsigned)(base * (p.nseg - 1)), C::NT, C::SMEM_STATE, s, p);
+    if (e != 0) return e;
     e = launch_dependent(linattn_scan_kernel<QuadOrder<C>>, (unsigned)(base * (DK * DVT / 256)), 256, 0, s, p,
                          p.seg_chunks * kC);
     if (e != 0) return e;
-    e = launch_dependent(linattn_kernel<C, false>, (unsigned)(base * p.nseg), C::NT, C::SMEM, s, p);
-    if (e != 0) return e;
-  } else {
-    linattn_kernel<C, false><<<(unsigned)base, C::NT, C::SMEM, s>>>(p);
   }
-  return (int)cudaGetLastError();
+  return launch_dependent(linattn_kernel<C, false>, (unsigned)(base * p.nseg), C::NT, C::SMEM, s, p);
 }
 
 template <int DK>
 int launch_dk(const LinAttnParams& p, cudaStream_t s) {
-  return p.DV % 64 == 0 ? launch_cfg<DK, 64>(p, s) : launch_cfg<DK, 32>(p, s);
+  // 32 columns of c a CTA also where twice the CTAs still have an SM each: a chunk's chain is shorter (5 ragged rows of
+  // up to 333, 12 x 64: 18.4 -> 14.3 us)
+  const bool narrow = p.nseg == 1 && (long long)p.npass * p.B * p.NH * (p.DV / 32) <= sm_count();
+  return p.DV % 64 == 0 && !narrow ? launch_cfg<DK, 64>(p, s) : launch_cfg<DK, 32>(p, s);
 }
 
 }  // namespace

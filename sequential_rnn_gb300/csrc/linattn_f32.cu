@@ -48,6 +48,10 @@ __global__ void __launch_bounds__(kT32)
   float* pws = S + DK * kV32;  // lambda^m, m = 0 .. 32
   float* wj = pws + kC32 + 1;  // weight of token j in the state's update
   const int tid = threadIdx.x;
+  if (STATE_ONLY || p.nseg == 1) {  // the call's first kernel
+    depend_wait();
+    depend_launch();
+  }
   const int VT = p.DV / kV32;
   const Where w = where_of(p, VT, STATE_ONLY ? p.nseg - 1 : p.nseg);
   const LinAttnPass& ps = p.pass[w.job];
@@ -57,7 +61,6 @@ __global__ void __launch_bounds__(kT32)
   const int c1 = c0 + p.seg_chunks < nch ? c0 + p.seg_chunks : nch;
   const int lch = (len + kC32 - 1) / kC32;
   const int cend = c1 < lch ? c1 : lch;
-  if (STATE_ONLY) depend_launch();
   if (STATE_ONLY && (long long)c1 * kC32 >= len) return;
   const float lg = p.log_decay[w.h] * 1.4426950408889634f;
   const bool rev = ps.reverse != 0;
@@ -208,16 +211,13 @@ int launch_dk(const LinAttnParams& p, cudaStream_t s) {
   if (p.nseg > 1) {
     e = prepare_launch(prep_state, linattn_f32_kernel<DK, true>, C::SMEM, kT32, 1);
     if (e != 0) return e;
-    linattn_f32_kernel<DK, true><<<(unsigned)(base * (p.nseg - 1)), kT32, C::SMEM, s>>>(p);
+    e = launch_dependent(linattn_f32_kernel<DK, true>, (unsigned)(base * (p.nseg - 1)), kT32, C::SMEM, s, p);
+    if (e != 0) return e;
     e = launch_dependent(linattn_scan_kernel<RowOrder<DK>>, (unsigned)(base * (DK * kV32 / 256)), 256, 0, s, p,
                          p.seg_chunks * kC32);
     if (e != 0) return e;
-    e = launch_dependent(linattn_f32_kernel<DK, false>, (unsigned)(base * p.nseg), kT32, C::SMEM, s, p);
-    if (e != 0) return e;
-  } else {
-    linattn_f32_kernel<DK, false><<<(unsigned)base, kT32, C::SMEM, s>>>(p);
   }
-  return (int)cudaGetLastError();
+  return launch_dependent(linattn_f32_kernel<DK, false>, (unsigned)(base * p.nseg), kT32, C::SMEM, s, p);
 }
 
 }  // namespace

@@ -10,9 +10,9 @@ namespace srnn {
 
 // Launch of a kernel that may begin while the one in front of it on the stream still runs (its start-up then
 // overlaps that one's end) and that waits for the whole of it at depend_wait().  Two uses:
-// - inside a call, before it touches what the call's kernel in front writes; that one, itself launched after
-//   everything earlier had ended, says depend_launch();
-// - as a call's only kernel, whatever is in front: every one of its CTAs waits before its first access, so that
+// - inside a call, before it touches what the call's kernel in front writes; that one says depend_launch() once
+//   everything before the call has ended (where it was itself launched so, after its own depend_wait());
+// - as a call's first kernel, whatever is in front: every one of its CTAs waits before its first access, so that
 //   "the kernel in front has ended" goes on meaning that everything before that one has.
 // No non-coherent load (__ldg, const __restrict__) in such a kernel: its inputs may be written after it began.
 template <class... P, class... A>
