@@ -429,8 +429,10 @@ int launch_cfg(const LinAttnParams& p, cudaStream_t s) {
 template <int DK>
 int launch_dk(const LinAttnParams& p, cudaStream_t s) {
   // 32 columns of c a CTA also where twice the CTAs still have an SM each: a chunk's chain is shorter (5 ragged rows of
-  // up to 333, 12 x 64: 18.4 -> 14.3 us)
-  const bool narrow = p.nseg == 1 && (long long)p.npass * p.B * p.NH * (p.DV / 32) <= sm_count();
+  // up to 333, 12 x 64: 18.4 -> 14.3 us); forward with 64 x 64, up to three an SM (16 rows of 200 16.3 -> 14.5, of 512
+  // 28.8 -> 25.4; a gradient's passes lose by it, 8 rows of 200 19.7 / 23.2, as do 64 x 128, 12.8 / 14.0)
+  const long long ctas = (long long)p.npass * p.B * p.NH * (p.DV / 32);
+  const bool narrow = p.nseg == 1 && ctas <= (DK == 64 && p.DV == 64 && p.npass == 1 ? 3 : 1) * sm_count();
   return p.DV % 64 == 0 && !narrow ? launch_cfg<DK, 64>(p, s) : launch_cfg<DK, 32>(p, s);
 }
 

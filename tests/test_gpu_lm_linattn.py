@@ -179,6 +179,15 @@ def test_unequal_head_sizes_and_many_heads(S, T, B, NH, Dk, Dv):
         check_backward(S, d, "bf16")
 
 
+@pytest.mark.parametrize("T,B,NH,Dk,Dv", [(150, 19, 12, 64, 64), (150, 20, 12, 64, 64), (150, 38, 2, 64, 64),
+                                          (150, 39, 2, 128, 64), (70, 19, 4, 128, 128), (70, 10, 4, 256, 64)])
+def test_numbers_of_heads(S, T, B, NH, Dk, Dv):
+    """Both sides of the numbers of heads at which a CTA takes more columns."""
+    d = draw(B, T, B, NH, Dk, Dv, "bf16", lens=[T - b for b in range(B)])
+    check_forward(S, d, "bf16")
+    check_backward(S, d, "bf16")
+
+
 def test_state_in_place_across_segments(S):
     """The final state may be written over the initial one."""
     for T in (64, 3000):
