@@ -17,6 +17,7 @@
 // 4.9 TB/s of the copy's 6.8 (a row a launch's warp, without the next row's loads: 19.4 on the device against 17.2);
 // gradient, 16384 x 1000, 30.9 us, 4.2 TB/s.  Wider rows take a CTA, which registers hold as well.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -58,14 +59,24 @@ __device__ __forceinline__ float block_scale(float top) {
   return s > 0.f ? s : 1.f;
 }
 
-// The codes of E of a block's 128 columns, together with the LANES neighbouring threads of its other columns: t = h w in
-// fp32, its products with the ends of an interval of 448 / max|t| that is wider than the five roundings between
-// them and the exact quotient (5 2^-24).  Where both give the same code (lo, hi) the quotient does, too.
+__device__ __forceinline__ bool in_range(float v) { return v >= 0x1p-60f && v <= 0x1p60f; }
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
+}
+
+// The codes of E of a block's 128 columns and the block's scale, together with the LANES neighbouring threads of its
+// other columns and all of the warp.  t = h w in fp32, its products with the ends of an interval of 448 / max|t| that
+// is wider than the five roundings between them and the exact quotient (5 2^-24): where both give the same code
+// the quotient does, too.  Where they give neighbours (values near a tie between them; with weights of one, whose
+// products are short numbers, many are ties) 448 h w and the tie times max|h w| are compared as sums of two fp32 numbers,
+// exact to 2^-46; what rounds to the tie in fp32 goes to the even code.  (A division in fp32 for each value instead took
+// half of the kernel's time, and, with y and s rounded before it, put every millionth value on the other side of
+// a tie; in 64 bits rows with many ties took four times as long.)
+// False where the numbers leave the range of this (zeros stay in it): then quantize_wide() has to do it.
 template <int E, int LANES>
-__device__ __forceinline__ void quantize_ends(const float (&h)[E], const float (&w)[E], uint32_t (&lo)[E / 4],
-                                              uint32_t (&hi)[E / 4], float& top) {
-  float t[E];
-  top = 0.f;
+__device__ __forceinline__ bool quantize_block(const float (&h)[E], const float (&w)[E], float r, uint32_t (&q)[E / 4],
+                                               float& s) {
+  float t[E], top = 0.f;
 #pragma unroll
   for (int j = 0; j < E; ++j) {
     t[j] = h[j] * w[j];
@@ -74,69 +85,57 @@ __device__ __forceinline__ void quantize_ends(const float (&h)[E], const float (
 #pragma unroll
   for (int o = LANES / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float inv = kE4m3Max / top, a = inv * (1.f - 0x1p-21f), b = inv * (1.f + 0x1p-21f);
+  uint32_t hi[E / 4], differ = 0;
 #pragma unroll
   for (int j = 0; j < E; j += 4) {
-    lo[j / 4] = pack_e4m3(t[j] * a, t[j + 1] * a, t[j + 2] * a, t[j + 3] * a);
+    q[j / 4] = pack_e4m3(t[j] * a, t[j + 1] * a, t[j + 2] * a, t[j + 3] * a);
     hi[j / 4] = pack_e4m3(t[j] * b, t[j + 1] * b, t[j + 2] * b, t[j + 3] * b);
+    differ |= q[j / 4] ^ hi[j / 4];
   }
-}
-__device__ __forceinline__ bool in_range(float v) { return v >= 0x1p-60f && v <= 0x1p60f; }
-// Codes and scale where the ends agree; false where they do not or the numbers leave the range.  (A division in fp32
-// for each value instead took half of the kernel's time, and, with y and s rounded before it, put every
-// millionth value on the other side of a tie.)
-template <int E, int LANES>
-__device__ __forceinline__ bool quantize_fast(const float (&h)[E], const float (&w)[E], float r, uint32_t (&q)[E / 4],
-                                              float& s) {
-  float top;
-  uint32_t hi[E / 4];
-  quantize_ends<E, LANES>(h, w, q, hi, top);
   s = top * r * (1.f / kE4m3Max);
-  bool ok = in_range(top) && in_range(r);
-  if (top == 0.f && r <= 0x1p60f) {  // (r is not a number where h has one)
-    s = 1.f, ok = true;
+  if (__any_sync(0xffffffffu, differ)) {
+    float rest = -INFINITY;  // what rounding took from the largest product
 #pragma unroll
-    for (int j = 0; j < E / 4; ++j) q[j] = hi[j] = 0u;
-  }
+    for (int j = 0; j < E; ++j) {
+      const float e = fmaf(h[j], w[j], -t[j]);
+      if (fabsf(t[j]) == top) rest = fmaxf(rest, t[j] < 0.f ? -e : e);
+    }
 #pragma unroll
-  for (int j = 0; j < E / 4; ++j) ok &= q[j] == hi[j];
-  return ok;
-}
-// The same where they do not, by the whole warp (one row in 170 of 768 columns): the quotient in 64 bits.
-template <int E, int LANES>
-__device__ __forceinline__ void quantize_exact(const float (&h)[E], const float (&w)[E], float r, uint32_t (&q)[E / 4],
-                                               float& s) {
-  float top;
-  uint32_t hi[E / 4];
-  quantize_ends<E, LANES>(h, w, q, hi, top);
-  // what rounding took from the largest product
-  float rest = -1.f;
-#pragma unroll
-  for (int j = 0; j < E; ++j) {
-    const float t = h[j] * w[j], e = fmaf(h[j], w[j], -t);
-    if (fabsf(t) == top) rest = fmaxf(rest, (t < 0.f ? -e : e) / top);
-  }
-#pragma unroll
-  for (int o = LANES / 2; o; o >>= 1) rest = fmaxf(rest, __shfl_xor_sync(0xffffffffu, rest, o));
-  s = top * r * (1.f / kE4m3Max);
-  if (__all_sync(0xffffffffu, in_range(top) && in_range(r))) {
-    const double f = kE4m3Max / ((double)top + (double)rest * top);
+    for (int o = LANES / 2; o; o >>= 1) rest = fmaxf(rest, __shfl_xor_sync(0xffffffffu, rest, o));
 #pragma unroll
     for (int j = 0; j < E; ++j) {
       const int at = 8 * (j % 4);
-      if (((q[j / 4] ^ hi[j / 4]) >> at & 0xffu) == 0) continue;
-      const uint32_t c = to_e4m3((float)((double)h[j] * w[j] * f));
-      q[j / 4] = (q[j / 4] & ~(0xffu << at)) | c << at;
+      const uint32_t lo = q[j / 4] >> at & 0xffu, up = hi[j / 4] >> at & 0xffu;
+      if (lo == up) continue;
+      const float tie = 0.5f * fabsf(e4m3_value(lo) + e4m3_value(up)), e = fmaf(h[j], w[j], -t[j]);
+      const float x = kE4m3Max * fabsf(t[j]), y = tie * top;
+      const float d = (x - y) + ((fmaf(kE4m3Max, fabsf(t[j]), -x) + kE4m3Max * (t[j] < 0.f ? -e : e)) -
+                                 (fmaf(tie, top, -y) + tie * rest));
+      // half of the tie's last place, times max|t|
+      const float near = top * __uint_as_float((__float_as_uint(tie) & 0x7f800000u) - (24u << 23));
+      const bool take = fabsf(d) <= near ? (lo & 1u) != 0 : d > 0.f;
+      if (take) q[j / 4] ^= (lo ^ up) << at;
     }
-    return;
   }
-  // zeros, products or scales near the ends of fp32's range, values that are not finite
-  double top64 = 0.0;
+  if (top == 0.f && r <= 0x1p60f) {  // (r is not a number where h has one)
+    s = 1.f;
 #pragma unroll
-  for (int j = 0; j < E; ++j) top64 = fmax(top64, fabs((double)h[j] * w[j]));
+    for (int j = 0; j < E / 4; ++j) q[j] = 0u;
+    return true;
+  }
+  return in_range(top) && in_range(r);
+}
+// The same in 64 bits, by the whole warp: products or scales near the ends of fp32's range, values that are not finite.
+template <int E, int LANES>
+__device__ __forceinline__ void quantize_wide(const float (&h)[E], const float (&w)[E], float r, uint32_t (&q)[E / 4],
+                                              float& s) {
+  double top = 0.0;
 #pragma unroll
-  for (int o = LANES / 2; o; o >>= 1) top64 = fmax(top64, __shfl_xor_sync(0xffffffffu, top64, o));
-  s = (float)(top64 * r / kE4m3Max);
-  double f = kE4m3Max / top64;
+  for (int j = 0; j < E; ++j) top = fmax(top, fabs((double)h[j] * w[j]));
+#pragma unroll
+  for (int o = LANES / 2; o; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+  s = (float)(top * r / kE4m3Max);
+  double f = kE4m3Max / top;
   if (!(s >= 0x1p-126f)) f = s > 0.f ? (double)r / s : r;  // (a subnormal scale is coarse: the quotient by what is stored)
   if (!(s > 0.f)) s = 1.f;  // zeros, values that underflow, a row whose r is zero or not a number
 #pragma unroll
@@ -192,7 +191,7 @@ __global__ void __launch_bounds__(256) norm_any_kernel(const NormParams p) {
       uint32_t q[1];
       if (p.scale) {
         float s;
-        if (__any_sync(0xffffffffu, !quantize_fast<4, 32>(hv, w, r, q, s))) quantize_exact<4, 32>(hv, w, r, q, s);
+        if (__any_sync(0xffffffffu, !quantize_block<4, 32>(hv, w, r, q, s))) quantize_wide<4, 32>(hv, w, r, q, s);
         if (lane == 0) p.scale[row * nblk + b] = s;
       }
 #pragma unroll
@@ -291,20 +290,20 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// quantize_exact() for a vector of h and its weights: out of line, so that the rows which need it fetch little code
+// quantize_wide() for a vector of h and its weights: out of line, it is rare
 struct Codes {
   uint32_t q[2];
   float s;
 };
 template <class T>
-__device__ __noinline__ Codes exact_codes(uint4 h, const float* weight, float r) {
+__device__ __noinline__ Codes wide_codes(uint4 h, const float* weight, float r) {
   constexpr int E = Vec<T>::E;
   float y[E], w[E];
   uint32_t q[E / 4];
   Codes c;
   load_weight<E>(weight, 0, w);
   Vec<T>::unpack(h, y);
-  quantize_exact<E, kBlk / E>(y, w, r, q, c.s);
+  quantize_wide<E, kBlk / E>(y, w, r, q, c.s);
   c.q[0] = q[0], c.q[1] = q[E / 4 - 1];
   return c;
 }
@@ -387,7 +386,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024, WARP ? kNormCtas : 1) norm_
       if constexpr (QUANT) {  // (past the row h is zero)
         uint32_t q[E / 4];
         float s;
-        bad |= (quantize_fast<E, kBlk / E>(y, w[WARP ? i : 0], r, q, s) ? 0u : 1u) << i;
+        bad |= (quantize_block<E, kBlk / E>(y, w[WARP ? i : 0], r, q, s) ? 0u : 1u) << i;
         store_block(v, q, s);
       } else {
 #pragma unroll
@@ -402,7 +401,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024, WARP ? kNormCtas : 1) norm_
         for (int i = 0; i < NV; ++i) {
           if (!(bad >> i & 1)) continue;
           const int v = t + i * TPR;
-          const Codes c = exact_codes<T>(cur[i], p.weight + (v < nv ? v : 0) * E, r);
+          const Codes c = wide_codes<T>(cur[i], p.weight + (v < nv ? v : 0) * E, r);
           store_block(v, c.q, c.s);
         }
       }

@@ -77,13 +77,18 @@ def test_rms_norm_8bit(S, rows, N, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("small", [1.0, 2.0 ** -114, 2.0 ** -128, 2.0 ** -135])
+@pytest.mark.parametrize("small", [1.0, 2.0 ** -114, 2.0 ** -128, 2.0 ** -135, "ones", "short"])
 @pytest.mark.parametrize("rows,N", [(2000, 768), (700, 1001), (40, 8192), (5, 16512)])
 def test_rms_norm_8bit_codes_are_the_nearest(S, rows, N, small, dtype):
     """y / scale = 448 h w / max|h w|, of which 64 bits hold the products exactly, rounded to fp32 and then to 8
     bits: equal codes, at every magnitude a scale can have (by a subnormal one, which is coarse, the quotient is that of
     what is stored)."""
-    x, w = rand(60, rows, N, dtype=dtype), rand(61, N, scale=small)
+    x, w = rand(60, rows, N, dtype=dtype), rand(61, N, scale=small if isinstance(small, float) else 1.0)
+    if small == "ones":                           # products of 8 bits: many exact ties
+        w = torch.ones_like(w)
+    if small == "short":
+        x, w, small = x.bfloat16().to(x.dtype), w.bfloat16().float(), 1.0
+    small = 1.0 if small == "ones" else small
     out = S.rms_norm(x, w, quantize=True, train=True)
     hw, s = np64(x) * np64(w), np.repeat(np64(out["scale"]), 128, 1)[:, :N]
     pad = np.pad(np.abs(hw), ((0, 0), (0, -N % 128))).reshape(rows, -1, 128).max(2)
