@@ -68,12 +68,6 @@ __device__ __forceinline__ uint32_t tile_at(int r, int ch) {
   return (uint32_t)(r * (D * 2) + ((ch ^ x) << 4));
 }
 
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
-}
-
 // which state element register `reg` of quad i of thread t holds
 template <class C>
 __device__ __forceinline__ void state_of(int t, int i, int reg, int& dk, int& v) {

@@ -12,6 +12,12 @@
 
 namespace srnn {
 
+// 16 bytes to shared memory, zeros where not `valid`
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
 // lambda^n, n >= 0 (lg = log2 lambda, possibly -inf)
 __device__ __forceinline__ float pw(float lg, int n) { return n == 0 ? 1.f : exp2f(lg * (float)n); }
 

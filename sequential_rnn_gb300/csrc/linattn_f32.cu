@@ -1,10 +1,10 @@
 // Linear attention with a decay for each head, fp32: the precision path.  The
 // same passes as linattn.cu, with fp32 multiply-adds throughout.
 //
-// One CTA per (pass, row, head, 32 columns of the state, segment), chunks of 32
-// tokens staged in shared memory, the state [DK, 32] there too.  Each thread
-// owns a 2 x 2 piece of the scores and of the output, and DK / 8 elements of
-// the state.
+// One CTA per (pass, row, head, 64 or 32 columns of the state, segment), chunks of 32 tokens (the scores, which every
+// CTA of a head makes for itself, grow with the chunk) staged in shared memory, the state [DK, DVT] there too.
+// Bound by the multiply-adds: a thread owns up to 4 x 4 of each product, so that eight 16-byte loads feed
+// 64 of them (with 2 x 2, a load to each two, the loads took five times as long as the sums).  Measured: @f32@
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -17,42 +17,59 @@
 namespace srnn {
 namespace {
 
-constexpr int kC32 = 32, kV32 = 32, kT32 = 256;
+constexpr int kC32 = 32;  // tokens per chunk
 
-template <int DK>
+template <int DK_, int DVT_>
 struct La32Cfg {
-  static constexpr int LD = DK + 4;  // row pitch of x and a: 16-byte rows, banks shifted row by row
-  static constexpr uint32_t FLOATS = 2 * kC32 * LD + kC32 * kV32 + kC32 * (kC32 + 1) + DK * kV32 + 3 * kC32;
-  static constexpr uint32_t SMEM = FLOATS * 4;
+  static constexpr int DK = DK_, DVT = DVT_;
+  static constexpr int NT = DK <= 128 ? 128 : 256;
+  static constexpr int OCC = DK <= 64 ? 4 : (DK == 128 ? 2 : 1);
+  static constexpr int STAGES = DK <= 128 ? 1 : 2;  // with one CTA on an SM, the next chunk's copies run ahead
+  static constexpr int LD = DK + 4;   // row pitch of x and a: 16-byte rows, banks shifted row by row
+  static constexpr int LP = kC32 + 4;  // and of the scores
+  static constexpr int RS = kC32 / (NT / 16);  // scores: rows of a thread (beside two columns)
+  static constexpr int CT = DVT / 4, RT = NT / CT;  // threads side by side over the columns (4 each), and over rows
+  static constexpr int RO = kC32 / RT;          // output: rows of a thread
+  static constexpr int M = DK >= 4 * RT ? DK / (4 * RT) : 1;  // state: blocks of 4 rows of a thread
+  static constexpr int STAGE = 2 * kC32 * LD + kC32 * DVT;    // x, a, c
+  static constexpr uint32_t SMEM = (STAGES * STAGE + kC32 * LP + DK * DVT + 3 * kC32) * 4;
 };
-template <int DK>
+template <class C>
 struct RowOrder {
-  static constexpr int TILE = DK * kV32;
-  static __device__ __forceinline__ int tiles(const LinAttnParams& p) { return p.DV / kV32; }
+  static constexpr int TILE = C::DK * C::DVT;
+  static __device__ __forceinline__ int tiles(const LinAttnParams& p) { return p.DV / C::DVT; }
   static __device__ __forceinline__ void at(const LinAttnParams&, int tile, int e, int& dk, int& v) {
-    dk = e / kV32;
-    v = tile * kV32 + e % kV32;
+    dk = e / C::DVT;
+    v = tile * C::DVT + e % C::DVT;
   }
 };
 
-template <int DK, bool STATE_ONLY>
-__global__ void __launch_bounds__(kT32)
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ void fma4(float (&d)[4], float a, const float4& b) {
+  d[0] = fmaf(a, b.x, d[0]);
+  d[1] = fmaf(a, b.y, d[1]);
+  d[2] = fmaf(a, b.z, d[2]);
+  d[3] = fmaf(a, b.w, d[3]);
+}
+__device__ __forceinline__ float dot4(const float4& a, const float4& b, float c) {
+  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
+
+template <class C, bool STATE_ONLY>
+__global__ void __launch_bounds__(C::NT, C::OCC)
     linattn_f32_kernel(const __grid_constant__ LinAttnParams p) {
-  using C = La32Cfg<DK>;
+  constexpr int DK = C::DK, DVT = C::DVT, NT = C::NT, LD = C::LD, LP = C::LP, RS = C::RS, RO = C::RO, M = C::M;
   extern __shared__ __align__(16) float sm[];
-  float* X = sm;
-  float* A = X + kC32 * C::LD;
-  float* V = A + kC32 * C::LD;
-  float* P = V + kC32 * kV32;
-  float* S = P + kC32 * (kC32 + 1);
-  float* pws = S + DK * kV32;  // lambda^m, m = 0 .. 32
+  float* P = sm + C::STAGES * C::STAGE;
+  float* S = P + kC32 * LP;
+  float* pws = S + DK * DVT;   // lambda^m, m = 0 .. 32
   float* wj = pws + kC32 + 1;  // weight of token j in the state's update
   const int tid = threadIdx.x;
   if (STATE_ONLY || p.nseg == 1) {  // the call's first kernel
     depend_wait();
     depend_launch();
   }
-  const int VT = p.DV / kV32;
+  const int VT = p.DV / DVT;
   const Where w = where_of(p, VT, STATE_ONLY ? p.nseg - 1 : p.nseg);
   const LinAttnPass& ps = p.pass[w.job];
   const int len = row_len(p, w.b);
@@ -67,157 +84,212 @@ __global__ void __launch_bounds__(kT32)
   if (!STATE_ONLY && blockIdx.x == 0 && tid == 0 && p.clear) *p.status = 0;
   const float* gx = static_cast<const float*>(ps.x) + w.b * ps.xs[1] + w.h * ps.xs[2];
   const float* ga = static_cast<const float*>(ps.a) + w.b * ps.as[1] + w.h * ps.as[2];
-  const float* gc = static_cast<const float*>(ps.c) + w.b * ps.cs[1] + w.h * ps.cs[2] + w.vt * kV32;
-  float* gout = static_cast<float*>(ps.out) + w.b * ps.os[1] + w.h * ps.os[2] + w.vt * kV32;
+  const float* gc = static_cast<const float*>(ps.c) + w.b * ps.cs[1] + w.h * ps.cs[2] + w.vt * DVT;
+  float* gout = static_cast<float*>(ps.out) + w.b * ps.os[1] + w.h * ps.os[2] + w.vt * DVT;
+
+  auto load_rows = [&](float* dst, int pitch, int width, const float* src, long long stride, int c) {
+    const uint32_t to = smem_u32(dst);
+    for (int e = tid; e < kC32 * (width / 4); e += NT) {
+      const int row = e / (width / 4), col = 4 * (e % (width / 4)), r = c * kC32 + row;
+      const bool ok = r < len;
+      const long long t = ok ? (rev ? len - 1 - r : r) : 0;
+      cp_async16_zfill(to + (row * pitch + col) * 4, src + t * stride + col, ok);
+    }
+  };
+  auto load_chunk = [&](int c, int st) {
+    float* X = sm + st * C::STAGE;
+    if (!STATE_ONLY) load_rows(X, LD, DK, gx, ps.xs[0], c);
+    load_rows(X + kC32 * LD, LD, DK, ga, ps.as[0], c);
+    load_rows(X + 2 * kC32 * LD, DVT, DVT, gc, ps.cs[0], c);
+  };
+  if (C::STAGES == 2 && c0 < cend) {
+    load_chunk(c0, 0);
+    cp_async_commit();
+  }
 
   if (STATE_ONLY) {
-    for (int e = tid; e < DK * kV32; e += kT32) S[e] = 0.f;
+    for (int e = tid; e < DK * DVT; e += NT) S[e] = 0.f;
   } else if (p.nseg > 1) {
     depend_wait();  // for the scan
-    const float* src = seg_state(p, w, w.seg, VT, DK * kV32);
+    const float* src = seg_state(p, w, w.seg, VT, DK * DVT);
     if (w.seg == 0 || c0 < cend)
-      for (int e = tid; e < DK * kV32; e += kT32) S[e] = src[e];
+      for (int e = tid; e < DK * DVT; e += NT) S[e] = src[e];
   } else {
     const float* in = ps.init ? ps.init + (long long)w.bh * DK * p.DV : nullptr;
-    for (int e = tid; e < DK * kV32; e += kT32) {
-      const int dk = e / kV32, v = w.vt * kV32 + e % kV32;
+    for (int e = tid; e < DK * DVT; e += NT) {
+      const int dk = e / DVT, v = w.vt * DVT + e % DVT;
       S[e] = in ? in[ps.init_t ? (long long)v * DK + dk : (long long)dk * p.DV + v] : 0.f;
     }
   }
   if (tid <= kC32) pws[tid] = pw(lg, tid);
 
+  const int v0 = 4 * (tid % C::CT), rt = tid / C::CT;  // this thread's columns, and its place over the rows
   for (int c = c0; c < cend; ++c) {
     const int n = len - c * kC32 < kC32 ? len - c * kC32 : kC32;
-    __syncthreads();
-    for (int e = tid; e < kC32 * (DK / 4); e += kT32) {
-      const int row = e / (DK / 4), col = 4 * (e % (DK / 4));
-      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int r = c * kC32 + row;
-      const long long t = rev ? len - 1 - r : r;
-      const bool ok = row < n;
-      if (!STATE_ONLY)
-        *reinterpret_cast<float4*>(X + row * C::LD + col) =
-            ok ? *reinterpret_cast<const float4*>(gx + t * ps.xs[0] + col) : z;
-      *reinterpret_cast<float4*>(A + row * C::LD + col) =
-          ok ? *reinterpret_cast<const float4*>(ga + t * ps.as[0] + col) : z;
-    }
-    for (int e = tid; e < kC32 * (kV32 / 4); e += kT32) {
-      const int row = e / (kV32 / 4), col = 4 * (e % (kV32 / 4));
-      const int r = c * kC32 + row;
-      const long long t = rev ? len - 1 - r : r;
-      *reinterpret_cast<float4*>(V + row * kV32 + col) =
-          row < n ? *reinterpret_cast<const float4*>(gc + t * ps.cs[0] + col)
-                  : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+    const int st = C::STAGES == 2 ? (c - c0) & 1 : 0;
+    const float *X = sm + st * C::STAGE, *A = X + kC32 * LD, *V = A + kC32 * LD;
+    __syncthreads();  // the chunk before has been read
+    if (C::STAGES == 1)
+      load_chunk(c, 0);
+    else if (c + 1 < cend)
+      load_chunk(c + 1, st ^ 1);
+    cp_async_commit();
     if (tid < kC32) wj[tid] = tid < n ? ps.upd * pw(lg, n - 1 - tid + ps.shift) : 0.f;
+    cp_async_wait<C::STAGES - 1>();
     __syncthreads();
-    const int i0 = 2 * (tid / 16), j0 = 2 * (tid % 16);  // this thread's 2 x 2 pieces
     if (!STATE_ONLY) {
-      float s00 = 0.f, s01 = 0.f, s10 = 0.f, s11 = 0.f;
-      if (j0 <= i0 + 1)
+      {  // scores: rows i0 .., columns tid % 16 and 16 more
+        const int i0 = RS * (tid / 16), j0 = tid % 16;
+        float s[RS][2];
+#pragma unroll
+        for (int i = 0; i < RS; ++i) s[i][0] = s[i][1] = 0.f;
+        if (j0 < i0 + RS)
 #pragma unroll 4
-        for (int d = 0; d < DK; d += 4) {
-          const float4 x0 = *reinterpret_cast<const float4*>(X + i0 * C::LD + d);
-          const float4 x1 = *reinterpret_cast<const float4*>(X + (i0 + 1) * C::LD + d);
-          const float4 a0 = *reinterpret_cast<const float4*>(A + j0 * C::LD + d);
-          const float4 a1 = *reinterpret_cast<const float4*>(A + (j0 + 1) * C::LD + d);
-          s00 = fmaf(x0.x, a0.x, fmaf(x0.y, a0.y, fmaf(x0.z, a0.z, fmaf(x0.w, a0.w, s00))));
-          s01 = fmaf(x0.x, a1.x, fmaf(x0.y, a1.y, fmaf(x0.z, a1.z, fmaf(x0.w, a1.w, s01))));
-          s10 = fmaf(x1.x, a0.x, fmaf(x1.y, a0.y, fmaf(x1.z, a0.z, fmaf(x1.w, a0.w, s10))));
-          s11 = fmaf(x1.x, a1.x, fmaf(x1.y, a1.y, fmaf(x1.z, a1.z, fmaf(x1.w, a1.w, s11))));
-        }
-      auto put = [&](int i, int j, float v) {
-        P[i * (kC32 + 1) + j] = j <= i ? v * (ps.intra * pws[i - j]) : 0.f;
-      };
-      put(i0, j0, s00);
-      put(i0, j0 + 1, s01);
-      put(i0 + 1, j0, s10);
-      put(i0 + 1, j0 + 1, s11);
-      __syncthreads();
-      float o[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, u[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll 4
-      for (int d = 0; d < DK; ++d) {
-        const float x0 = X[i0 * C::LD + d], x1 = X[(i0 + 1) * C::LD + d];
-        const float2 s = *reinterpret_cast<const float2*>(S + d * kV32 + j0);
-        u[0][0] = fmaf(x0, s.x, u[0][0]);
-        u[0][1] = fmaf(x0, s.y, u[0][1]);
-        u[1][0] = fmaf(x1, s.x, u[1][0]);
-        u[1][1] = fmaf(x1, s.y, u[1][1]);
+          for (int d = 0; d < DK; d += 4) {
+            const float4 a0 = ld4(A + j0 * LD + d), a1 = ld4(A + (j0 + 16) * LD + d);
+#pragma unroll
+            for (int i = 0; i < RS; ++i) {
+              const float4 x = ld4(X + (i0 + i) * LD + d);
+              s[i][0] = dot4(x, a0, s[i][0]);
+              s[i][1] = dot4(x, a1, s[i][1]);
+            }
+          }
+#pragma unroll
+        for (int i = 0; i < RS; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int j = j0 + 16 * k, lag = i0 + i - j;
+            P[(i0 + i) * LP + j] = lag >= 0 ? s[i][k] * (ps.intra * pws[lag]) : 0.f;
+          }
       }
-      for (int j = 0; j <= i0 + 1; ++j) {
-        const float p0 = P[i0 * (kC32 + 1) + j], p1 = P[(i0 + 1) * (kC32 + 1) + j];
-        const float2 v = *reinterpret_cast<const float2*>(V + j * kV32 + j0);
-        if (j <= i0) {
-          o[0][0] = fmaf(p0, v.x, o[0][0]);
-          o[0][1] = fmaf(p0, v.y, o[0][1]);
+      __syncthreads();
+      const int i0 = RO * rt;
+      float o[RO][4];
+#pragma unroll
+      for (int i = 0; i < RO; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+#pragma unroll 2
+      for (int d = 0; d < DK; d += 4) {
+        const float4 s0 = ld4(S + d * DVT + v0), s1 = ld4(S + (d + 1) * DVT + v0), s2 = ld4(S + (d + 2) * DVT + v0),
+                     s3 = ld4(S + (d + 3) * DVT + v0);
+#pragma unroll
+        for (int i = 0; i < RO; ++i) {
+          const float4 x = ld4(X + (i0 + i) * LD + d);
+          fma4(o[i], x.x, s0);
+          fma4(o[i], x.y, s1);
+          fma4(o[i], x.z, s2);
+          fma4(o[i], x.w, s3);
         }
-        o[1][0] = fmaf(p1, v.x, o[1][0]);
-        o[1][1] = fmaf(p1, v.y, o[1][1]);
       }
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const int i = i0 + a;
-        if (i >= n) continue;
-        const float f = ps.inter * pws[i + 1 - ps.shift];
-        const int r = c * kC32 + i;
+      for (int i = 0; i < RO; ++i) {
+        const float f = ps.inter * pws[i0 + i + 1 - ps.shift];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][k] *= f;
+      }
+      int j = 0;
+      for (; j + 4 <= i0; j += 4) {
+        const float4 c_0 = ld4(V + j * DVT + v0), c_1 = ld4(V + (j + 1) * DVT + v0), c_2 = ld4(V + (j + 2) * DVT + v0),
+                     c_3 = ld4(V + (j + 3) * DVT + v0);
+#pragma unroll
+        for (int i = 0; i < RO; ++i) {
+          const float4 q = ld4(P + (i0 + i) * LP + j);
+          fma4(o[i], q.x, c_0);
+          fma4(o[i], q.y, c_1);
+          fma4(o[i], q.z, c_2);
+          fma4(o[i], q.w, c_3);
+        }
+      }
+      for (; j < i0 + RO; ++j) {  // (a token's own row must not meet later ones, which may not be finite)
+        const float4 cj = ld4(V + j * DVT + v0);
+#pragma unroll
+        for (int i = 0; i < RO; ++i)
+          if (j <= i0 + i) fma4(o[i], P[(i0 + i) * LP + j], cj);
+      }
+#pragma unroll
+      for (int i = 0; i < RO; ++i) {
+        if (i0 + i >= n) continue;
+        const int r = c * kC32 + i0 + i;
         const long long t = rev ? len - 1 - r : r;
-        *reinterpret_cast<float2*>(gout + t * ps.os[0] + j0) =
-            make_float2(fmaf(f, u[a][0], o[a][0]), fmaf(f, u[a][1], o[a][1]));
+        *reinterpret_cast<float4*>(gout + t * ps.os[0] + v0) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
       }
       __syncthreads();  // S was read
     }
-    // state: thread (dk group, v): rows dk = tid / 32 + 8 m, column tid % 32
-    const int v = tid & 31, d0 = tid >> 5;
-    const float wS = pws[n];
-    float add[DK / 8];
+    if (4 * rt < DK) {  // state: rows 4 rt .., and every 4 RT further
+      const float wS = pws[n];
+      float add[M][4][4];
 #pragma unroll
-    for (int m = 0; m < DK / 8; ++m) add[m] = 0.f;
-    for (int j = 0; j < n; ++j) {
-      const float cv = V[j * kV32 + v] * wj[j];
+      for (int m = 0; m < M; ++m)
 #pragma unroll
-      for (int m = 0; m < DK / 8; ++m) add[m] = fmaf(A[j * C::LD + d0 + 8 * m], cv, add[m]);
-    }
+        for (int i = 0; i < 4; ++i) add[m][i][0] = add[m][i][1] = add[m][i][2] = add[m][i][3] = 0.f;
+#pragma unroll 2
+      for (int j = 0; j < n; ++j) {
+        const float wt = wj[j];
+        float4 cj = ld4(V + j * DVT + v0);
+        cj.x *= wt, cj.y *= wt, cj.z *= wt, cj.w *= wt;
 #pragma unroll
-    for (int m = 0; m < DK / 8; ++m) {
-      float* s = S + (d0 + 8 * m) * kV32 + v;
-      *s = fmaf(wS, *s, add[m]);
+        for (int m = 0; m < M; ++m) {
+          const float4 a = ld4(A + j * LD + 4 * rt + 4 * C::RT * m);
+          fma4(add[m][0], a.x, cj);
+          fma4(add[m][1], a.y, cj);
+          fma4(add[m][2], a.z, cj);
+          fma4(add[m][3], a.w, cj);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float* at = S + (4 * rt + 4 * C::RT * m + i) * DVT + v0;
+          float4 s = ld4(at);
+          s.x = fmaf(wS, s.x, add[m][i][0]);
+          s.y = fmaf(wS, s.y, add[m][i][1]);
+          s.z = fmaf(wS, s.z, add[m][i][2]);
+          s.w = fmaf(wS, s.w, add[m][i][3]);
+          *reinterpret_cast<float4*>(at) = s;
+        }
     }
   }
+  cp_async_wait<0>();
   __syncthreads();
 
   if (STATE_ONLY) {
-    float* dst = seg_state(p, w, w.seg + 1, VT, DK * kV32);
-    for (int e = tid; e < DK * kV32; e += kT32) dst[e] = S[e];
+    float* dst = seg_state(p, w, w.seg + 1, VT, DK * DVT);
+    for (int e = tid; e < DK * DVT; e += NT) dst[e] = S[e];
     return;
   }
   if (ps.fin != nullptr &&
       ((len > c0 * kC32 && (long long)len <= (long long)c1 * kC32) || (len == 0 && w.seg == 0))) {
-    float* f = ps.fin + (long long)w.bh * DK * p.DV + w.vt * kV32;
-    for (int e = tid; e < DK * kV32; e += kT32) f[(long long)(e / kV32) * p.DV + e % kV32] = S[e];
+    float* f = ps.fin + (long long)w.bh * DK * p.DV + w.vt * DVT;
+    for (int e = tid; e < DK * DVT; e += NT) f[(long long)(e / DVT) * p.DV + e % DVT] = S[e];
   }
   const int rlo = len > c0 * kC32 ? len : c0 * kC32, rhi = c1 * kC32 < p.T ? c1 * kC32 : p.T;
-  for (int e = tid; e < (rhi - rlo) * kV32; e += kT32)
-    gout[(long long)(rlo + e / kV32) * ps.os[0] + e % kV32] = 0.f;
+  for (int e = tid; e < (rhi - rlo) * C::CT; e += NT)
+    *reinterpret_cast<float4*>(gout + (long long)(rlo + e / C::CT) * ps.os[0] + 4 * (e % C::CT)) =
+        make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
-template <int DK>
-int launch_dk(const LinAttnParams& p, cudaStream_t s) {
-  using C = La32Cfg<DK>;
+template <int DK, int DVT>
+int launch_cfg(const LinAttnParams& p, cudaStream_t s) {
+  using C = La32Cfg<DK, DVT>;
   static int prep_main[64][5], prep_state[64][5];
-  int e = prepare_launch(prep_main, linattn_f32_kernel<DK, false>, C::SMEM, kT32, 1);
+  int e = prepare_launch(prep_main, linattn_f32_kernel<C, false>, C::SMEM, C::NT, 1);
   if (e != 0) return e;
-  const long long base = (long long)p.npass * p.B * p.NH * (p.DV / kV32);
-  if (base * p.nseg * (DK * kV32 / 256) > 0x7fffffffLL) return (int)cudaErrorInvalidValue;
+  const long long base = (long long)p.npass * p.B * p.NH * (p.DV / DVT);
+  if (base * p.nseg * (DK * DVT / 256) > 0x7fffffffLL) return (int)cudaErrorInvalidValue;
   if (p.nseg > 1) {
-    e = prepare_launch(prep_state, linattn_f32_kernel<DK, true>, C::SMEM, kT32, 1);
+    e = prepare_launch(prep_state, linattn_f32_kernel<C, true>, C::SMEM, C::NT, 1);
     if (e != 0) return e;
-    e = launch_dependent(linattn_f32_kernel<DK, true>, (unsigned)(base * (p.nseg - 1)), kT32, C::SMEM, s, p);
+    e = launch_dependent(linattn_f32_kernel<C, true>, (unsigned)(base * (p.nseg - 1)), C::NT, C::SMEM, s, p);
     if (e != 0) return e;
-    e = launch_dependent(linattn_scan_kernel<RowOrder<DK>>, (unsigned)(base * (DK * kV32 / 256)), 256, 0, s, p,
+    e = launch_dependent(linattn_scan_kernel<RowOrder<C>>, (unsigned)(base * (DK * DVT / 256)), 256, 0, s, p,
                          p.seg_chunks * kC32);
     if (e != 0) return e;
   }
-  return launch_dependent(linattn_f32_kernel<DK, false>, (unsigned)(base * p.nseg), kT32, C::SMEM, s, p);
+  return launch_dependent(linattn_f32_kernel<C, false>, (unsigned)(base * p.nseg), C::NT, C::SMEM, s, p);
+}
+template <int DK>
+int launch_dk(const LinAttnParams& p, cudaStream_t s) {
+  return p.DV % 64 == 0 ? launch_cfg<DK, 64>(p, s) : launch_cfg<DK, 32>(p, s);
 }
 
 }  // namespace

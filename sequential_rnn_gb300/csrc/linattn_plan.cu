@@ -33,8 +33,8 @@ LinAttnPlan linattn_plan(bool bf16, int npass, int T, int B, int NH, int DK, int
     occ = DK <= 64 ? 3 : (DK == 128 ? 2 : 1);
   } else {
     chunk = 32;
-    tiles = DV / 32;
-    occ = DK <= 64 ? 4 : (DK == 128 ? 3 : 2);
+    tiles = DV % 64 == 0 ? DV / 64 : DV / 32;
+    occ = DK <= 64 ? 4 : (DK == 128 ? 2 : 1);
   }
   const long long nch = ((long long)T + chunk - 1) / chunk;
   const long long base = (long long)npass * B * NH * tiles;
