@@ -45,7 +45,8 @@ LinAttnPlan linattn_plan(bool bf16, int npass, int T, int B, int NH, int DK, int
   long long nseg = 1, best = ((base + cap - 1) / cap) * nch;
   for (long long n = 2; base > 0 && n <= nch / 2 && base * (n - 1) < cap; ++n) {
     const long long per = (nch + n - 1) / n, waves = (base * n + cap - 1) / cap;
-    const long long cost = (waves + 1) * per + 8;
+    // (fp32: the contributions are a product of three, at most)
+    const long long cost = pl.path == kLinAttnF32 ? waves * per + (per + 1) / 2 + 4 : (waves + 1) * per + 8;
     if (cost < best) best = cost, nseg = n;
   }
   const long long per = nch > 0 ? (nch + nseg - 1) / nseg : 1;
