@@ -4,7 +4,7 @@
 // One CTA per (pass, row, head, 64 or 32 columns of the state, segment), chunks of 32 tokens (the scores, which every
 // CTA of a head makes for itself, grow with the chunk) staged in shared memory, the state [DK, DVT] there too.
 // Bound by the multiply-adds: a thread owns up to 4 x 4 of each product, so that eight 16-byte loads feed
-// 64 of (with 2 x 2, a load to each two, the kernel took 2.6 times as long).  Measured: 16 x 1024 tokens, 12 x 64,
+// 64 of them (with 2 x 2, a load to each two, the kernel took 2.6 times as long).  Measured: 16 x 1024 tokens, 12 x 64,
 // 217 us, gradient 393; 4 x 2001, 6 x 128 205 and 526; 4 x 4096, 4 x 256 1109 (19 TFLOP/s of fp32's 75) and 3112.
 #include <cuda_runtime.h>
 

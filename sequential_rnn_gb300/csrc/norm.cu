@@ -13,9 +13,9 @@
 // was computed.  All sums are fp32.
 //
 // Both are bound by their bytes.  Rows of up to 128 vectors take a warp each, persistent, with the weights (gradient:
-// the columns' share of dw) in registers and the next row's loads in flight: 16384 x 768 to 8 bits 18.2 us,
-// 4.9 TB/s of the copy's 6.8 (a row a launch's warp, without the next row's loads: 19.4 on the device against 17.2);
-// gradient, 16384 x 1000, 30.9 us, 4.2 TB/s.  Wider rows take a CTA, which registers hold as well.
+// the columns' share of dw) in registers and the next row's loads in flight: 16384 x 768 to 8 bits 16.4 us,
+// 5.4 TB/s of the copy's 6.8 (a row to each warp of a launch, without the next row's loads: 2 us more);
+// gradient, 16384 x 1000, 29.3 us, 4.5 TB/s.  Wider rows take a CTA, which registers hold as well.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -158,6 +158,129 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   float t = 0.f;
   for (int i = 0; i < nw; ++i) t += red[i];
   return t;
+}
+
+// Any width and alignment up to 4096 columns: a CTA per row of as many warps as the row has blocks of 128 columns, up to
+// eight; a thread's values, four of each block of its warp, stay in registers between the sum and the output.
+// Values are loaded one by one, since a row may begin at any of them; 16384 x 1001 bf16 in 41.5 us.
+template <class T, int NB>
+__global__ void __launch_bounds__(256) norm_rows_kernel(const NormParams p) {
+  __shared__ float red[8];
+  depend_launch();
+  depend_wait();
+  const int N = p.N, nblk = (N + kBlk - 1) / kBlk, W = blockDim.x >> 5, wp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const T* x = static_cast<const T*>(p.x) + row * N;
+    const T* res = p.residual ? static_cast<const T*>(p.residual) + row * N : nullptr;
+    T* h = p.h ? static_cast<T*>(p.h) + row * N : nullptr;
+    float hv[NB][4], ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = (wp + W * i) * kBlk + 32 * j + lane;
+        hv[i][j] = n < N ? load1(x + n) : 0.f;
+      }
+    if (res)
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int n = (wp + W * i) * kBlk + 32 * j + lane;
+          if (n < N) hv[i][j] = rounded<T>(hv[i][j] + load1(res + n));
+        }
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ss += hv[i][j] * hv[i][j];
+    const float r = rsqrtf(block_sum(ss, red) / (float)N + p.eps);
+    if (p.rstd && threadIdx.x == 0) p.rstd[row] = r;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int b = wp + W * i;
+      if (b >= nblk) break;
+      float w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = b * kBlk + 32 * j + lane;
+        w[j] = n < N ? p.weight[n] : 0.f;
+      }
+      uint32_t q[1];
+      if (p.scale) {
+        float s;
+        if (__any_sync(0xffffffffu, !quantize_block<4, 32>(hv[i], w, r, q, s))) quantize_wide<4, 32>(hv[i], w, r, q, s);
+        if (lane == 0) p.scale[row * nblk + b] = s;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = b * kBlk + 32 * j + lane;
+        if (n >= N) continue;
+        if (p.scale)
+          static_cast<uint8_t*>(p.y)[row * N + n] = (uint8_t)(q[0] >> (8 * j));
+        else
+          store1(static_cast<T*>(p.y) + row * N + n, hv[i][j] * r * w[j]);
+        if (h) store1(h + n, hv[i][j]);
+      }
+    }
+  }
+}
+// Its gradient, in the same places: a persistent grid, a thread keeps its columns' weights and share of dw.
+template <class T, int NB>
+__global__ void __launch_bounds__(256) norm_bwd_rows_kernel(const NormBwdParams p) {
+  __shared__ float red[8];
+  depend_wait();
+  const int N = p.N, W = blockDim.x >> 5, n0 = (threadIdx.x >> 5) * kBlk + (threadIdx.x & 31);
+  float w[NB][4], dw[NB][4];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = n0 + W * i * kBlk + 32 * j;
+      w[i][j] = n < N ? p.weight[n] : 0.f;
+      dw[i][j] = 0.f;
+    }
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const T* dy = static_cast<const T*>(p.dy) + row * N;
+    const T* h = static_cast<const T*>(p.h) + row * N;
+    const float r = p.rstd[row];
+    float g[NB][4], xh[NB][4], e[NB][4], dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = n0 + W * i * kBlk + 32 * j;
+        g[i][j] = n < N ? load1(dy + n) : 0.f;
+        xh[i][j] = n < N ? load1(h + n) : 0.f;
+        e[i][j] = n < N && p.dh ? load1(static_cast<const T*>(p.dh) + row * N + n) : 0.f;
+      }
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        xh[i][j] *= r;
+        dw[i][j] = fmaf(g[i][j], xh[i][j], dw[i][j]);
+        g[i][j] *= w[i][j];
+        dot = fmaf(g[i][j], xh[i][j], dot);
+      }
+    dot = block_sum(dot, red) / (float)N;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = n0 + W * i * kBlk + 32 * j;
+        if (n < N)
+          store1(static_cast<T*>(p.dx) + row * N + n, e[i][j] + r * (g[i][j] - xh[i][j] * dot));
+      }
+  }
+  depend_launch();
+  if (p.dw)
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = n0 + W * i * kBlk + 32 * j;
+        if (n < N) p.part[(long long)blockIdx.x * N + n] = dw[i][j];
+      }
 }
 
 // One CTA per row, any width and alignment.
@@ -573,6 +696,13 @@ int norm_typed(const NormParams& p, cudaStream_t s) {
   const bool vec = p.N % (QUANT ? 8 : E) == 0 && vec_ok(p.x) && vec_ok(p.residual) && vec_ok(p.h) &&
                    vec_ok(p.weight) && vec_ok(p.y);
   const int nv = p.N / E, th = vec_threads(nv);
+  if (!vec && p.N <= 4096) {
+    const int nblk = (p.N + kBlk - 1) / kBlk, threads = 32 * (nblk < 8 ? nblk : 8);
+    const unsigned grid = (unsigned)(p.rows < 1000000 ? p.rows : 1000000);
+    return nblk <= 8    ? launch_dependent(norm_rows_kernel<T, 1>, grid, threads, 0, s, p)
+           : nblk <= 16 ? launch_dependent(norm_rows_kernel<T, 2>, grid, threads, 0, s, p)
+                        : launch_dependent(norm_rows_kernel<T, 4>, grid, threads, 0, s, p);
+  }
   if (!vec || th == 0) {
     return launch_dependent(norm_any_kernel<T>, (unsigned)(p.rows < 65536 ? p.rows : 65536), 256, 0, s, p);
   } else if (nv <= 128) {
@@ -594,7 +724,12 @@ int norm_bwd_typed(const NormBwdParams& p, cudaStream_t s) {
   const int nv = p.N / E;
   int parts = norm_bwd_parts(p.rows, p.N);
   int e;
-  if (!vec || nv > 8 * 256) {
+  if (!vec && p.N <= 4096) {
+    const int nblk = (p.N + kBlk - 1) / kBlk, threads = 32 * (nblk < 8 ? nblk : 8);
+    e = nblk <= 8    ? launch_dependent(norm_bwd_rows_kernel<T, 1>, parts, threads, 0, s, p)
+        : nblk <= 16 ? launch_dependent(norm_bwd_rows_kernel<T, 2>, parts, threads, 0, s, p)
+                     : launch_dependent(norm_bwd_rows_kernel<T, 4>, parts, threads, 0, s, p);
+  } else if (!vec || nv > 8 * 256) {
     e = launch_dependent(norm_bwd_any_kernel<T>, parts, 256, 0, s, p);
   } else if (nv <= 128) {
     // (eight warps an SM with four vectors a thread: twelve, of 168 registers, took 31 us for 16384 x 1000, eight 25)
