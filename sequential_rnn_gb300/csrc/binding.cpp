@@ -113,6 +113,12 @@ double number(PyObject* o) {
   return v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v == 1;
+}
+
 Tensor make(IntArrayRef shape, ScalarType type, at::Device dev) {
   return Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));
 }
@@ -152,7 +158,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor &x = tensor("x", a[0]), &weight = tensor("weight", a[1]);
   const Tensor* residual = optional("residual", a[2]);
   const float eps = (float)number(a[3]);
-  const bool quantize = PyObject_IsTrue(a[4]) == 1, train = PyObject_IsTrue(a[5]) == 1;
+  const bool quantize = truth(a[4]), train = truth(a[5]);
   const at::Device dev = device_of("x", x);
   const int dt = dtype_of("x", x);
   if (x.dim() == 0) fail(PyExc_ValueError, "x: expected at least one dimension");

@@ -610,8 +610,8 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
       if (count > 0) {
         t = next();
         load_xa(t, 0);
-        depend_wait();  // for the chunk states
       }
+      depend_wait();  // for the chunk states (without a tile, too: a kernel that ends stands for those before it)
       for (int k = 0; ok && k < count; ++k) {
         const int j = t.job, tok = token_of(t), srow = (((j * p.B + t.b) * p.NH + t.h) * nch + t.c) * DK;
         for (int v = 0; ok && v < vts; ++v, ++f) {

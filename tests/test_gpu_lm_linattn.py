@@ -188,6 +188,19 @@ def test_numbers_of_heads(S, T, B, NH, Dk, Dv):
     check_backward(S, d, "bf16")
 
 
+@pytest.mark.parametrize("dtype,T,B,Dk", [("bf16", 300, 4, 128), ("bf16", 3000, 1, 256), ("bf16", 3000, 1, 64),
+                                          ("bf16", 40, 4, 64), ("f32", 3000, 1, 64)])
+def test_no_row_has_a_token(S, dtype, T, B, Dk):
+    """Every kernel of the call finds nothing to do: zeros, and the states as they came in."""
+    d = draw(11, T, B, 2, Dk, Dk, dtype, lens=[0] * B)
+    for _ in range(20):
+        out = S.linear_attention(d["q"], d["k"], d["v"], d["g"], state=d["s0"], lens=d["lens"], check=False)
+        g = S.linear_attention_backward(d["q"], d["k"], d["v"], d["g"], d["do"], state=d["s0"], dstate=d["ds"],
+                                        lens=d["lens"], check=False)
+        assert torch.equal(out["state"], d["s0"]) and torch.equal(g["dstate"], d["ds"])
+        assert not any(t.any() for t in (out["o"], g["dq"], g["dk"], g["dv"]))
+
+
 def test_state_in_place_across_segments(S):
     """The final state may be written over the initial one."""
     for T in (64, 3000):
