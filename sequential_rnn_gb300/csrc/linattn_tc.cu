@@ -22,7 +22,7 @@
 // update, P c, x S).  Loading through the copy engine matters: with cp.async from all threads
 // the copies of a tile took longer to issue (2,000-2,600 cycles) than its MMAs to run.
 //
-// Measured: 4 x 256, 4 rows of 4096 89-91 us (states 50, outputs 46 alone); gradient 6 x 128, 4 rows of 2001 57
+// Measured: 4 x 256, 4 rows of 4096 86 us (states 50, outputs 43 alone); gradient 6 x 128, 4 rows of 2001 53.7
 // us (28 and 32).  The states are bound by what a chunk makes the compute warps do one after the other (terms of c, 3 x 128
 // columns of sums out of TMEM, the state's stores: issue slots 55%, load and store unit 63%), the outputs by
 // the copies (320 KB a tile with 256 columns, half of it from DRAM: inputs, outputs and chunk states are 200 MB
@@ -193,6 +193,11 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
   const uint32_t aF = bar, aE = bar + 24, tR = bar + 48, mD = bar + 64, sR = bar + 80;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int vts = p.DV / 64;
+  if (STATE_ONLY || p.nseg == 1) {  // the call's first kernel
+    depend_wait();
+    // (a wait that runs out is told two seconds after its CTA began at the earliest, and this one is the first)
+    if (p.clear && blockIdx.x == 0 && tid == 0) *p.status = 0;
+  }
   const Where w = where_of(p, C::MB * vts, STATE_ONLY ? p.nseg - 1 : p.nseg);
   const LinAttnPass& ps = p.pass[w.job];
   const int mb = w.vt / vts, vt = w.vt % vts;
@@ -927,23 +932,23 @@ int launch_dk(const LinAttnParams& p, cudaStream_t s) {
   const cuuint32_t in[2] = {64, (cuuint32_t)DK};
   ok = ok && encode(&m.s_load, p.chunk_states, 2, dims, strides, in, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return kLinAttnTooWide;
-  if (p.clear && cudaMemsetAsync(p.status, 0, sizeof(int), s) != cudaSuccess) return (int)cudaErrorUnknown;
   if (p.nseg > 1) {
     e = prepare_launch(prep_state, linattn_states_kernel<DK, true>, C::SMEM, C::THREADS, 1);
     if (e != 0) return e;
-    linattn_states_kernel<DK, true><<<(unsigned)(base * (p.nseg - 1)), C::THREADS, C::SMEM, s>>>(p, m);
+    e = launch_dependent(linattn_states_kernel<DK, true>, (unsigned)(base * (p.nseg - 1)), C::THREADS, C::SMEM, s, p, m);
+    if (e != 0) return e;
     e = launch_dependent(linattn_scan_kernel<TcOrder<DK>>, (unsigned)(base * (C::TILE / 256)), 256, 0, s, p,
                          p.seg_chunks * kTC);
     if (e != 0) return e;
     e = launch_dependent(linattn_states_kernel<DK, false>, (unsigned)(base * p.nseg), C::THREADS, C::SMEM, s, p, m);
-    if (e != 0) return e;
   } else {
-    linattn_states_kernel<DK, false><<<(unsigned)base, C::THREADS, C::SMEM, s>>>(p, m);
+    e = launch_dependent(linattn_states_kernel<DK, false>, (unsigned)base, C::THREADS, C::SMEM, s, p, m);
   }
+  if (e != 0) return e;
   const long long cap = sm_count();
   e = launch_dependent(linattn_outputs_kernel<DK>, (unsigned)(outs < cap ? outs : cap), O::THREADS, O::SMEM, s, p,
                        m, (int)outs);
-  return e != 0 ? e : (int)cudaGetLastError();
+  return e;
 }
 
 }  // namespace

@@ -21,7 +21,7 @@
 // blocks of a tile run during the epilogue of the one before.  The outputs leave by way of shared memory and
 // TMA stores (stored straight from registers, an epilogue took 6,200 cycles).
 //
-// Measured at 16384 x 4096 x 1024: 84.5 us, 1.63 PFLOP/s (the bf16 matrix product's rate is 1.91), 23 us of bytes.
+// Measured at 16384 x 4096 x 1024: 84 us, 1.64 PFLOP/s (the bf16 matrix product's rate is 1.91), 23 us of bytes.
 // What bounds it is the promotion: every fp32 sum of a block of 128 leaves TMEM, at about 125 bytes a clock
 // and SM, which with nothing else would be 57 us, and a tile's epilogue between.
 //
@@ -132,6 +132,10 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
   tc_fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tslot) : "memory");
+  depend_launch();
+  depend_wait();
+  // (a wait that runs out is told two seconds after its CTA began at the earliest; the grid fits on the GPU at once)
+  if (blockIdx.x == 0 && threadIdx.x == 0) *g.status = 0;
   const int mine = (ntiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // this CTA's tiles
   const int blocks = mine * g.nkb;
   // an even number of stages gives a stage's blocks to one issuer anyway
@@ -201,11 +205,11 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
       float acc[WC];
 #pragma unroll
       for (int j = 0; j < WC; ++j) acc[j] = 0.f;
-      float sc = __ldg(xs) * __ldg(ws);
+      float sc = *xs * *ws;
       for (int kb = 0; kb < g.nkb; ++kb, ++it) {
         const int a = it % NACC;
         const int kn = kb + 1 < g.nkb ? kb + 1 : kb;
-        const float x1 = __ldg(xs + kn), w1 = __ldg(ws + kn);  // the next block's scales on their way
+        const float x1 = xs[kn], w1 = ws[kn];  // the next block's scales on their way
         if (!wait_f8(bar_done + 8 * (it % NSTG), (it / NSTG) & 1, abort_flag, g.status, tlim)) {
           stop = true;
           break;
@@ -239,7 +243,7 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
         for (int j = 0; j < 4; ++j) {
           const int c = 8 * k + 2 * j, n = n0 + c;
           float b0 = 0.f, b1 = 0.f;
-          if (g.bias && n < g.N) b0 = __ldg(g.bias + n), b1 = __ldg(g.bias + n + 1);  // (N is even)
+          if (g.bias && n < g.N) b0 = g.bias[n], b1 = g.bias[n + 1];  // (N is even)
           pk[j] = pack_bf16x2(acc[c] + b0, acc[c + 1] + b1);
         }
         const int ch = k ^ (WC == 64 ? lane & 7 : (lane >> 1) & 3);
@@ -427,9 +431,7 @@ int launch_bn(const ProjFp8Params& p, cudaStream_t s) {
     return e;
   const int cap = sm_count();
   const int grid = (int)(tiles < cap ? tiles : cap);
-  if (cudaMemsetAsync(p.status, 0, sizeof(int), s) != cudaSuccess) return (int)cudaErrorUnknown;
-  kern<<<grid, C::THREADS, C::SMEM, s>>>(a, b, c, g);
-  return (int)cudaGetLastError();
+  return launch_dependent(kern, (unsigned)grid, C::THREADS, C::SMEM, s, a, b, c, g);
 }
 
 }  // namespace
@@ -442,12 +444,13 @@ static int launch_few(const ProjFp8Params& p, cudaStream_t s) {
 }
 
 int launch_proj_fp8(const ProjFp8Params& p, cudaStream_t s) {
-  // Few rows: the kernel that reads each weight once, whose CTAs of 16 columns take longer with more rows; over
-  // 16 rows while two rounds of them hold all columns (us, it / tiles: K = 768, N = 4096, 33 rows 6.4 / 8.5, K = 4096 16.5 /
-  // 16.6; N = 8192 11.6 / 8.9 and 30.6 / 16.6; 32 rows 7.4 / 8.9 and 21.4 / 16.6; 16 rows 9.6 / 16.6 at 8192 x 4096).
-  if (p.M <= 8) return launch_few<1>(p, s);
-  if (p.M <= 16) return launch_few<2>(p, s);
-  if (p.M <= kFewRows && p.N <= 32 * sm_count()) return p.M <= 32 ? launch_few<4>(p, s) : launch_few<8>(p, s);
+  // Few rows: the kernel that reads each weight once, whose CTAs of 16 columns take longer with more rows, up to so many
+  // rounds of them (us on the device, it / tiles; K = 768 and 4096: 16 rows, N = 8192 3.8 / 5.4, 9.6 / 13.5; 32 rows, N =
+  // 4096 4.1 / 5.4, 12.4 / 13.2; 33 rows, N = 2304 3.6 / 5.3, 8.9 / 13.4, N = 4096 6.4 / 5.4, 16.5 / 13.2).
+  const int rounds = (p.N + 16 * sm_count() - 1) / (16 * sm_count());
+  if (p.M <= 16 && rounds <= 4) return p.M <= 8 ? launch_few<1>(p, s) : launch_few<2>(p, s);
+  if (p.M <= 32 && rounds <= 2) return launch_few<4>(p, s);
+  if (p.M <= kFewRows && rounds == 1) return launch_few<8>(p, s);
   // the larger tiles where they are enough for every SM
   const long long wide = (long long)((p.M + FBM - 1) / FBM) * ((p.N + 255) / 256);
   return wide >= sm_count() ? launch_bn<256>(p, s) : launch_bn<128>(p, s);

@@ -205,7 +205,8 @@ def test_input_proj_fp8(S, M, N, K):
     assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + U * mag).all()
 
 
-@pytest.mark.parametrize("M,N,K", [(16, 4872, 272), (17, 4864, 144), (17, 4872, 144), (40, 4872, 272), (64, 6000, 128)])
+@pytest.mark.parametrize("M,N,K", [(16, 4872, 272), (17, 4864, 144), (17, 4872, 144), (40, 4872, 272), (64, 6000, 128),
+                                   (33, 2432, 144), (33, 2440, 400), (16, 9728, 144), (1, 9736, 144), (9, 9736, 272)])
 def test_input_proj_fp8_few_rows_of_many_columns(S, M, N, K):
     """Both sides of the places where another kernel takes over."""
     (xq, xs, wq, ws, b), (want, mag) = operands(M, N, K, M + N + K)
