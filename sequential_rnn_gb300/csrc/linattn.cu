@@ -19,7 +19,7 @@
 // the output and 16 of the state.  Bound by latency: a chunk is a chain of copies, three products that depend on one
 // another and a barrier, with 12 warps an SM (168 registers each) to fill it; the tensor cores run at 42% of
 // mma.sync's rate, DRAM at 26% of its.  Measured, 12 heads of 64: 1 x 16384 tokens 55.5 us (in 37 segments), 16 x
-// 1024 gradient 104.6, five ragged rows of up to 333 14.3.
+// 1024 gradient 104.6, five ragged rows of up to 333 13.1.
 //
 // Rounding: the scores times their decay, and the state as an operand of q S,
 // are rounded to bf16, once each (as bf16 results are); every sum is fp32.  The
@@ -98,10 +98,8 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
   const uint32_t sS = sm + 2 * C::STAGE;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g0 = lane >> 2, t0 = 2 * (lane & 3);
-  if (STATE_ONLY || p.nseg == 1) {  // the call's first kernel
-    depend_wait();
-    depend_launch();
-  }
+  if (STATE_ONLY || p.nseg == 1) depend_wait();  // the call's first kernel
+  if (STATE_ONLY) depend_launch();
   const int VT = p.DV / DVT;
   const Where w = where_of(p, VT, STATE_ONLY ? p.nseg - 1 : p.nseg);
   const LinAttnPass& ps = p.pass[w.job];
@@ -389,6 +387,9 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
         f[(long long)dk * p.DV + w.vt * DVT + v] = S[i][r];
       }
   }
+  // (not before: the next kernel's CTAs would take the places that this one's leave free, three on some SMs, and keep
+  // them: 8 x 2048 gradients one after the other 133 us each instead of 100)
+  depend_launch();
   // tokens that do not count: zeros
   const int rlo = len > c0 * kC ? len : c0 * kC, rhi = c1 * kC < p.T ? c1 * kC : p.T;
   constexpr int CH = DVT / 8;

@@ -66,10 +66,8 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
   float* pws = S + DK * DVT;   // lambda^m, m = 0 .. 32
   float* wj = pws + kC32 + 1;  // weight of token j in the state's update
   const int tid = threadIdx.x;
-  if (STATE_ONLY || p.nseg == 1) {  // the call's first kernel
-    depend_wait();
-    depend_launch();
-  }
+  if (STATE_ONLY || p.nseg == 1) depend_wait();  // the call's first kernel
+  if (STATE_ONLY) depend_launch();
   const int VT = p.DV / DVT;
   const Where w = where_of(p, VT, STATE_ONLY ? p.nseg - 1 : p.nseg);
   const LinAttnPass& ps = p.pass[w.job];
@@ -263,6 +261,9 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
     float* f = ps.fin + (long long)w.bh * DK * p.DV + w.vt * DVT;
     for (int e = tid; e < DK * DVT; e += NT) f[(long long)(e / DVT) * p.DV + e % DVT] = S[e];
   }
+  // (not before: the next kernel's CTAs would take the places that this one's leave free, three on some SMs, and keep
+  // them: 8 x 2048 gradients one after the other 133 us each instead of 100)
+  depend_launch();
   const int rlo = len > c0 * kC32 ? len : c0 * kC32, rhi = c1 * kC32 < p.T ? c1 * kC32 : p.T;
   for (int e = tid; e < (rhi - rlo) * C::CT; e += NT)
     *reinterpret_cast<float4*>(gout + (long long)(rlo + e / C::CT) * ps.os[0] + 4 * (e % C::CT)) =

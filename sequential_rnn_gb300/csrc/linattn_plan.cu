@@ -6,21 +6,21 @@ namespace srnn {
 
 LinAttnPlan linattn_plan(bool bf16, int npass, int T, int B, int NH, int DK, int DV) {
   LinAttnPlan pl{};
-  // tcgen05 where it is the faster (us, mma.sync / tcgen05, T x rows x heads x Dk x Dv unless said).  Both sizes 128
-  // or more: from 256 tokens on (256x8x6x128x128 20.6 / 16.7, its gradient 39 / 25; 256x8x4x256x256 27.8 / 25.1; the
-  // same at 128 tokens 17.2 / 20.9).  Dk = 64, whose products with a are small, against wider values: the gradient from
-  // 256 tokens on (256x8x8x64x128 32.4 / 31.2, 1024x16 187 / 115), the forward pass with enough work (1024x16x8 52.9 /
-  // 46.1, 16384x1x8 70.9 / 62.7; 512x16x8 28.7 / 29.0, 2048x1x8 20.1 / 25.2).  64 x 64: the gradient's passes on long rows
-  // (4096x4x12 147 / 124; 2048x8x12 100 / 109), the forward pass with many long rows (2048x8x12 66.4 / 55.3,
-  // 1024x16x12 53.2 / 48.4; 4096x4x12 64.5 / 66.9, 16384x1x12 54.8 / 61.2).
+  // tcgen05 where it is the faster (us, mma.sync / tcgen05, T x rows x heads x Dk x Dv).  Dk of 128 or more: from 128
+  // tokens on (128x8x6x128x128 12.1 / 9.5, its gradient 23.0 / 16.4; 128x8x4x256x256 16.8 / 16.7, 44.8 / 32.2; 64 tokens
+  // 8.2 / 9.3 and 11.4 / 16.5).  Dk = 64, whose products with a are small, against wider values: the gradient from 192
+  // tokens on (200x16x8x64x128 58 / 40; 128x2x8 14.4 / 16.5), the forward pass from 512 (512x2x8 15.4 / 13.3, 1024x16x8 69 /
+  // 42; 256x8x8 12.8 / 13.5).  64 x 64: the gradient's passes on long rows (4096x4x12 148 / 119; 1024x16x12 101 / 108,
+  // 2048x8x12 100 / 105), the forward pass with enough long rows (1024x4x12 27.8 / 22.6, 2048x8x12 66.9 / 51.1;
+  // 16384x1x12 55.3 / 57.1, 512x16x12 25.3 / 26.3).
   const long long heads = (long long)B * NH;
   bool tc = DK % 64 == 0 && DV % 64 == 0;
   if (DK > 64)
-    tc = tc && T >= 256;
+    tc = tc && T >= 128;
   else if (DV > 64)
-    tc = tc && (npass > 1 ? T >= 256 : T >= 1024 && T * heads >= 65536);
+    tc = tc && T >= (npass > 1 ? 192 : 512);
   else
-    tc = tc && (npass > 1 ? T >= 4096 : T >= 1024 && heads >= 96);
+    tc = tc && (npass > 1 ? T >= 4096 : T >= 1024 && heads >= 48);
   pl.path = !bf16 ? kLinAttnF32 : (tc ? kLinAttnTc : kLinAttnMma);
   int chunk, tiles, occ;  // tokens per chunk, state tiles per head, CTAs per SM
   if (pl.path == kLinAttnTc) {
