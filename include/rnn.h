@@ -288,7 +288,8 @@ int rnn_fwd_noalloc(const rnn_desc_t* desc, const void* Wx, const void* R, const
  * gradient.  scale NULL: y has dtype.  Otherwise y is 8-bit floating point (e4m3)
  * and scale [rows, ceil(N/128)] fp32 holds, for each row and block of 128
  * columns, max|y| / 448 (1 where that is zero); y holds the exact quotient y / scale,
- * rounded to fp32 and then to e4m3 (to nearest even).  N == 0 is refused, rows == 0 a no-op.  Any N; widths that are
+ * rounded to fp32 and then to e4m3 (to nearest even).  A y that is not a number has a NaN code and does not count
+ * towards its block's scale; an infinite one has a NaN code and makes the scale infinite.  N == 0 is refused, rows == 0 a no-op.  Any N; widths that are
  * a multiple of 16 bytes (of 8 values for e4m3) with 16-byte aligned pointers
  * run the vector kernels.  Alignment: the element's.  No workspace, no device status. */
 int rnn_rms_norm(int32_t dtype, int32_t rows, int32_t N, float eps, const void* x,

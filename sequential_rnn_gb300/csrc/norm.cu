@@ -118,6 +118,10 @@ __device__ __forceinline__ bool quantize_block(const float (&h)[E], const float 
     }
   }
   if (top == 0.f && r <= 0x1p60f) {  // (r is not a number where h has one)
+    bool zero = true;  // (fmaxf passes over products that are not numbers)
+#pragma unroll
+    for (int j = 0; j < E; ++j) zero = zero && t[j] == 0.f;
+    if (!zero) return false;
     s = 1.f;
 #pragma unroll
     for (int j = 0; j < E / 4; ++j) q[j] = 0u;

@@ -1,0 +1,67 @@
+"""GPU tests of the 8-bit norm where its values are not ordinary numbers, against the definition in 64 bits.
+
+The codes are those of 448 h w / max|h w|, rounded to fp32 and then to e4m3: compared exactly.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import lm_oracle as O
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+# a row in a warp's vectors, in a CTA's, value by value in registers, and past what they hold
+WIDTHS = [256, 1000, 8192, 301, 5001]
+
+
+@pytest.fixture(scope="module")
+def S():
+    from sequential_rnn_gb300 import build
+    build.build()
+    import sequential_rnn_gb300 as S
+    return S
+
+
+def rand(seed, *shape, dtype="f32", scale=1.0):
+    x = np.random.default_rng(seed).normal(size=shape).astype(np.float32) * scale
+    return torch.from_numpy(np.asarray(x, np.float32)).to("cuda", DT[dtype])
+
+
+def np64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def blocks(a):
+    """[rows, N] -> [rows, blocks, 128], zeros behind the row's end."""
+    return np.pad(a, ((0, 0), (0, -a.shape[1] % 128))).reshape(a.shape[0], -1, 128)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", WIDTHS)
+@pytest.mark.parametrize("where", ["column", "among zeros", "block", "all"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_weights_that_are_not_finite(S, N, where, value, dtype):
+    """A product that is not a number has a NaN code and does not count towards its block's scale; an infinite one has
+    a NaN code and an infinite scale.  The other blocks do not notice."""
+    rows = 5
+    x, w = rand(1, rows, N, dtype=dtype), rand(2, N)
+    lo = 128
+    hit = {"column": slice(lo + 3, lo + 4), "among zeros": slice(lo + 3, lo + 4), "block": slice(lo, lo + 128),
+           "all": slice(0, N)}[where]
+    if where == "among zeros":
+        x[:, lo:lo + 128] = 0
+        x[:, lo + 3] = 1
+    w[hit] = value
+    out = S.rms_norm(x, w, quantize=True)
+    y, scale = np64(out["y"]), np64(out["scale"])
+    with np.errstate(invalid="ignore"):
+        hw = np64(x) * np64(w)
+    mag = blocks(np.where(np.isnan(hw), 0, np.abs(hw)))
+    top = mag.max(2)
+    assert np.array_equal(np.isnan(y), ~np.isfinite(hw))
+    assert np.array_equal(np.isinf(scale), np.isinf(top)) and (scale[top == 0] == 1).all()
+    ok = np.isfinite(top) & (top > 0)
+    full = np.repeat(np.where(ok, top, 1), 128, 1)[:, :N]
+    fine = np.isfinite(hw) & np.repeat(np.isfinite(top), 128, 1)[:, :N]
+    want = O.e4m3((448 * np.where(fine, hw, 0) / full).astype(np.float32))
+    assert np.array_equal(y[fine], want[fine])
