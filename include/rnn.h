@@ -335,8 +335,9 @@ int rnn_input_proj_fp8(int32_t M, int32_t N, int32_t K, const void* xq, const fl
  * Operands may be strided views (of one fused projection, say): strides in elements
  * for (token, row, head), the innermost dimension contiguous; st NULL = contiguous.
  * RNN_BF16: tokens are taken in chunks of 64 or 128 on the tensor cores, scores and the
- * state as an operand rounded to bf16 once, all sums and the state fp32.  A v that is not finite can reach
- * the outputs of earlier tokens of its chunk.  RNN_F32: fp32 throughout.
+ * state as an operand rounded to bf16 once, all sums and the state fp32.  RNN_F32: fp32 throughout.
+ * A value that is not finite reaches the outputs of its own and later tokens of its row and head and the
+ * state, as the recurrence has it (in the gradient: the tokens before it, too); never an output that does not depend on it.
  * Alignment: 16 bytes for tensors and strides, 4 for log_decay and lens, workspace 256
  * and >= rnn_linattn_workspace_size(desc, 0) bytes (status word at offset 0). */
 typedef struct {

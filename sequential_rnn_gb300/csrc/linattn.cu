@@ -271,11 +271,11 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
         O[i][3] *= r1;
       }
       // ---- decay and mask, then times c ----------------------------------
+      uint32_t pd[4];  // of the tiles on the diagonal, which come last
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
         if (ks > rb) continue;
-        uint32_t pa[4];
-        if (ks == rb) {  // tiles on the diagonal: (2 ks: d0 and d0 + 8), (2 ks + 1: d0 - 8 and d0)
+        if (ks == rb) {  // (2 ks: d0 and d0 + 8), (2 ks + 1: d0 - 8 and d0)
           float d[2][2], f[2], m[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -284,23 +284,63 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
             f[e] = P[2 * ks][2 + e] * fe[0][e];
             m[e] = low ? P[2 * ks + 1][2 + e] * ge[e] : 0.f;
           }
-          pa[0] = pack_bf16x2(d[0][0], d[0][1]);
-          pa[1] = pack_bf16x2(f[0], f[1]);
-          pa[2] = 0u;
-          pa[3] = pack_bf16x2(m[0], m[1]);
+          pd[0] = pack_bf16x2(d[0][0], d[0][1]);
+          pd[1] = pack_bf16x2(f[0], f[1]);
+          pd[2] = 0u;
+          pd[3] = pack_bf16x2(m[0], m[1]);
         } else {
+          uint32_t pa[4];
           const float m0 = pow8[2 * (rb - ks) - 1], m1 = pow8[2 * (rb - ks) - 2];
           pa[0] = pack_bf16x2(P[2 * ks][0] * (m0 * fe[0][0]), P[2 * ks][1] * (m0 * fe[0][1]));
           pa[1] = pack_bf16x2(P[2 * ks][2] * (m0 * fe[1][0]), P[2 * ks][3] * (m0 * fe[1][1]));
           pa[2] = pack_bf16x2(P[2 * ks + 1][0] * (m1 * fe[0][0]), P[2 * ks + 1][1] * (m1 * fe[0][1]));
           pa[3] = pack_bf16x2(P[2 * ks + 1][2] * (m1 * fe[1][0]), P[2 * ks + 1][3] * (m1 * fe[1][1]));
+#pragma unroll
+          for (int i = 0; i < NTO; i += 2) {
+            uint32_t vb[4];
+            ldmatrix_x4_trans(vb, ((bC + oCp) ^ (uint32_t)(i << 4)) + 16 * ks * RC);
+            mma_bf16_16816(O[i], pa, vb[0], vb[1]);
+            mma_bf16_16816(O[i + 1], pa, vb[2], vb[3]);
+          }
         }
+      }
+      // On the diagonal zero scores stand for later tokens, and zero times a c that is not finite is NaN: those 16
+      // rows of c are looked at first, and where one is found the tokens are taken one by one.
+      uint32_t vd[NTO / 2][4], seen = 0u;
+#pragma unroll
+      for (int i = 0; i < NTO; i += 2) {
+        ldmatrix_x4_trans(vd[i / 2], ((bC + oCp) ^ (uint32_t)(i << 4)) + 16 * rb * RC);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) seen = seen_finite(seen, vd[i / 2][r]);
+      }
+      if (!__any_sync(0xffffffffu, seen != 0u)) {
 #pragma unroll
         for (int i = 0; i < NTO; i += 2) {
-          uint32_t vb[4];
-          ldmatrix_x4_trans(vb, ((bC + oCp) ^ (uint32_t)(i << 4)) + 16 * ks * RC);
-          mma_bf16_16816(O[i], pa, vb[0], vb[1]);
-          mma_bf16_16816(O[i + 1], pa, vb[2], vb[3]);
+          mma_bf16_16816(O[i], pd, vd[i / 2][0], vd[i / 2][1]);
+          mma_bf16_16816(O[i + 1], pd, vd[i / 2][2], vd[i / 2][3]);
+        }
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < 16; ++j) {
+          const int from = (lane & 28) | ((j & 7) >> 1);  // its scores' lane; this thread's rows are g0 and g0 + 8
+          const uint32_t s0 = __shfl_sync(0xffffffffu, j < 8 ? pd[0] : pd[2], from);
+          const uint32_t s1 = __shfl_sync(0xffffffffu, j < 8 ? pd[1] : pd[3], from);
+          const float p0 = j & 1 ? bf16_hi(s0) : bf16_lo(s0), p1 = j & 1 ? bf16_hi(s1) : bf16_lo(s1);
+#pragma unroll
+          for (int i = 0; i < NTO; ++i) {
+            uint32_t cj;
+            asm volatile("ld.shared.b32 %0, [%1];"
+                         : "=r"(cj)
+                         : "r"(bC + tile_at<DVT>(16 * rb + j, (cg * C::OVC) / 8 + i) + t0 * 2));
+            if (j <= g0) {
+              O[i][0] = fmaf(p0, bf16_lo(cj), O[i][0]);
+              O[i][1] = fmaf(p0, bf16_hi(cj), O[i][1]);
+            }
+            if (j <= g0 + 8) {
+              O[i][2] = fmaf(p1, bf16_lo(cj), O[i][2]);
+              O[i][3] = fmaf(p1, bf16_hi(cj), O[i][3]);
+            }
+          }
         }
       }
 #pragma unroll

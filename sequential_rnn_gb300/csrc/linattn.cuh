@@ -18,6 +18,17 @@ __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, 
                "r"(valid ? 16 : 0)
                : "memory");
 }
+// 0 as long as every value of the packed pairs seen is finite (0 times an infinity or NaN is NaN, and NaN stays)
+__device__ __forceinline__ uint32_t seen_finite(uint32_t seen, uint32_t pair) {
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(seen) : "r"(pair), "r"(0u));
+  return seen;
+}
+// largest magnitude of three, NaN if one is
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // lambda^n, n >= 0 (lg = log2 lambda, possibly -inf)
 __device__ __forceinline__ float pw(float lg, int n) { return n == 0 ? 1.f : exp2f(lg * (float)n); }
 

@@ -491,6 +491,107 @@ struct OutTile {
   float lg;               // log2 of the head's decay
 };
 
+// Tiles in the order pass, head, row, chunk (fastest first), the last chunk first: what the states' kernel touched
+// last is still in L2.  A step of the grid is added digit by digit, and by the loading warp alone: the
+// divisions of a place cost every role 700 cycles a tile, the digits' walk still 1,400 the MMAs' warp.
+__device__ __forceinline__ OutTile digits(const LinAttnParams& p, int nch, int idx) {
+  OutTile t;
+  t.job = idx % p.npass;
+  idx /= p.npass;
+  t.h = idx % p.NH;
+  idx /= p.NH;
+  t.b = idx % p.B;
+  t.c = nch - 1 - idx / p.B;
+  return t;
+}
+__device__ __forceinline__ void advance(const LinAttnParams& p, int nch, OutTile& t, const OutTile& stride) {
+  t.job += stride.job;  // (past the last tile c is below 0)
+  t.h += stride.h;
+  t.b += stride.b;
+  t.c -= nch - 1 - stride.c;
+  if (t.job >= p.npass) t.job -= p.npass, ++t.h;
+  if (t.h >= p.NH) t.h -= p.NH, ++t.b;
+  if (t.b >= p.B) t.b -= p.B, --t.c;
+}
+
+// Zero scores stand for a chunk's later tokens, and zero times a c that is not finite is NaN.  Where a P c came out so, the
+// warp takes the outputs of its rows (32 q + lane, columns 64 v + 32 g ..) that are not finite again, token by token, each
+// with the tokens up to it alone; once its tiles are done, since in their loop the registers for it cost 10-20%.
+template <int DK>
+__device__ __noinline__ void repair_rows(const LinAttnParams& p, int tiles, int grp, int q, int g) {
+  const int nch = (p.T + kTC - 1) / kTC, lane = threadIdx.x & 31;
+  const OutTile stride = digits(p, nch, (int)gridDim.x);
+  OutTile at = digits(p, nch, blockIdx.x);
+  depend_wait();  // (read here straight from memory: the chunk states)
+  int k = 0;
+  for (int idx = blockIdx.x; idx < tiles; idx += gridDim.x, advance(p, nch, at, stride)) {
+    const int len = row_len(p, at.b), first = at.c * kTC;
+    if (len <= first || (k++ & 1) != grp) continue;
+    const LinAttnPass& ps = p.pass[at.job];
+    // i: the row's place in its chunk, in the pass's time
+    const int i = ps.reverse ? kTC - 1 - (32 * q + lane) : 32 * q + lane;
+    if (first + i >= len) continue;
+    auto token = [&](int j) { return (long long)(ps.reverse ? len - 1 - (first + j) : first + j); };
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(ps.x) + token(i) * ps.xs[0] + at.b * ps.xs[1] + at.h * ps.xs[2];
+    const __nv_bfloat16* a = static_cast<const __nv_bfloat16*>(ps.a) + at.b * ps.as[1] + at.h * ps.as[2];
+    const __nv_bfloat16* c = static_cast<const __nv_bfloat16*>(ps.c) + at.b * ps.cs[1] + at.h * ps.cs[2];
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(ps.out) + token(i) * ps.os[0] + at.b * ps.os[1] + at.h * ps.os[2];
+    const __nv_bfloat16* S = static_cast<const __nv_bfloat16*>(p.chunk_states) +
+                             ((((long long)at.job * p.B + at.b) * p.NH + at.h) * nch + at.c) * DK * p.DV;
+    const float lg = p.log_decay[at.h] * 1.4426950408889634f;
+    const float fr = ps.inter * pw(lg, i + 1 - ps.shift);
+    auto fma8 = [](float (&o)[8], float f, const __nv_bfloat16* r) {
+      const uint4 v = *reinterpret_cast<const uint4*>(r);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[2 * e] = fmaf(f, bf16_lo(w[e]), o[2 * e]);
+        o[2 * e + 1] = fmaf(f, bf16_hi(w[e]), o[2 * e + 1]);
+      }
+    };
+    // eights of columns: 4 of every 64
+    const int eights = p.DV / 16;
+    auto col_of = [&](int e) { return 64 * (e >> 2) + 32 * g + 8 * (e & 3); };
+    uint32_t need = 0u;
+    for (int e = 0; e < eights; ++e) {
+      const uint4 v = *reinterpret_cast<const uint4*>(out + col_of(e));
+      need |= (seen_finite(seen_finite(seen_finite(seen_finite(0u, v.x), v.y), v.z), v.w) != 0u ? 1u : 0u) << e;
+    }
+    if (need == 0u) continue;
+    float o[16][8];
+#pragma unroll 1
+    for (int e = 0; e < eights; ++e) {
+      if (!(need >> e & 1u)) continue;
+      float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int d = 0; d < DK; ++d) fma8(y, __bfloat162float(x[d]), S + (long long)d * p.DV + col_of(e));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[e][k] = y[k] * fr;
+    }
+#pragma unroll 1
+    for (int j = 0; j <= i; ++j) {
+      float s = 0.f;
+#pragma unroll 1
+      for (int d = 0; d < DK; d += 8) {
+        float xf[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, af[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        fma8(xf, 1.f, x + d);
+        fma8(af, 1.f, a + token(j) * ps.as[0] + d);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s = fmaf(xf[k], af[k], s);
+      }
+      s = bf16_round(s * (ps.intra * pw(lg, i - j)));
+#pragma unroll 1
+      for (int e = 0; e < eights; ++e)
+        if (need >> e & 1u) fma8(o[e], s, c + token(j) * ps.cs[0] + col_of(e));
+    }
+#pragma unroll 1
+    for (int e = 0; e < eights; ++e)
+      if (need >> e & 1u)
+        *reinterpret_cast<uint4*>(out + col_of(e)) = make_uint4(pack_bf16x2(o[e][0], o[e][1]), pack_bf16x2(o[e][2], o[e][3]),
+                                                                pack_bf16x2(o[e][4], o[e][5]), pack_bf16x2(o[e][6], o[e][7]));
+  }
+}
+
 template <int DK>
 __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
     linattn_outputs_kernel(const __grid_constant__ LinAttnParams p, const __grid_constant__ TcMaps m,
@@ -523,35 +624,13 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
   auto ragged = [&](const OutTile& t) {
     return t.len < p.T && t.len < (t.c + 1) * kTC && !((revs >> t.job) & 1);
   };
-  // Tiles in the order pass, head, row, chunk (fastest first), the last chunk first: what the states' kernel touched
-  // last is still in L2.  A step of the grid is added digit by digit, and by the loading warp alone: the
-  // divisions of a place cost every role 700 cycles a tile, the digits' walk still 1,400 the MMAs' warp.
-  auto digits = [&](int idx) {
-    OutTile t;
-    t.job = idx % p.npass;
-    idx /= p.npass;
-    t.h = idx % p.NH;
-    idx /= p.NH;
-    t.b = idx % p.B;
-    t.c = nch - 1 - idx / p.B;
-    return t;
-  };
-  auto advance = [&](OutTile& t, const OutTile& stride) {  // (past the last tile c is below 0)
-    t.job += stride.job;
-    t.h += stride.h;
-    t.b += stride.b;
-    t.c -= nch - 1 - stride.c;
-    if (t.job >= p.npass) t.job -= p.npass, ++t.h;
-    if (t.h >= p.NH) t.h -= p.NH, ++t.b;
-    if (t.b >= p.B) t.b -= p.B, --t.c;
-  };
   // this CTA's tiles that hold tokens
   int count = ((int)blockIdx.x < tiles ? (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0);
   if (p.lens != nullptr) {
-    const OutTile stride = digits((int)gridDim.x);
-    OutTile t = digits(blockIdx.x);
+    const OutTile stride = digits(p, nch, (int)gridDim.x);
+    OutTile t = digits(p, nch, blockIdx.x);
     count = 0;
-    for (int idx = blockIdx.x; idx < tiles; idx += gridDim.x, advance(t, stride))
+    for (int idx = blockIdx.x; idx < tiles; idx += gridDim.x, advance(p, nch, t, stride))
       count += row_len(p, t.b) > t.c * kTC;
   }
 
@@ -577,8 +656,8 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
   if (warp == C::WLOAD) {
     // ------------------------------------------------------------- loads --
     if (lane == 0) {
-      const OutTile stride = digits((int)gridDim.x);
-      OutTile at = digits(blockIdx.x);
+      const OutTile stride = digits(p, nch, (int)gridDim.x);
+      OutTile at = digits(p, nch, blockIdx.x);
       int f = 0, done = 0;  // c and state tiles; of these, known to be multiplied
       bool ok = true;
       auto multiplied = [&](int upto) {  // one after the other: no barrier is left two phases behind
@@ -586,13 +665,13 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
         return ok;
       };
       auto next = [&]() {  // the next tile that holds tokens (there is one)
-        for (;; advance(at, stride)) {
+        for (;; advance(p, nch, at, stride)) {
           at.len = row_len(p, at.b);
           if (at.len > at.c * kTC) break;
         }
         OutTile t = at;
         t.lg = p.log_decay[t.h] * 1.4426950408889634f;
-        advance(at, stride);
+        advance(p, nch, at, stride);
         return t;
       };
       auto load_xa = [&](const OutTile& t, int k) {
@@ -725,9 +804,9 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
     if (p.lens != nullptr) {
       // Zeros for tokens that do not count, of tiles without tokens and of reversed ones (whose rows
       // are other tokens): row r0 + row, 64 v + 32 g ..
-      const OutTile stride = digits((int)gridDim.x);
-      OutTile t = digits(blockIdx.x);
-      for (int idx = blockIdx.x; idx < tiles; idx += gridDim.x, advance(t, stride)) {
+      const OutTile stride = digits(p, nch, (int)gridDim.x);
+      OutTile t = digits(p, nch, blockIdx.x);
+      for (int idx = blockIdx.x; idx < tiles; idx += gridDim.x, advance(p, nch, t, stride)) {
         t.len = row_len(p, t.b);
         const int r = t.c * kTC + row;
         if (grp != 0 || r < t.len || r >= p.T || (t.len > t.c * kTC && !((revs >> t.job) & 1))) continue;
@@ -739,6 +818,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
           for (int j = 0; j < 32; j += 8) *reinterpret_cast<uint4*>(o + 64 * v + j) = make_uint4(0u, 0u, 0u, 0u);
       }
     }
+    bool spoilt = false;  // a row of P c that is not finite
     for (int k = grp; k < count; k += 2) {
       // After an abort the waits of a tile return at once, and the two warps of a named barrier leave
       // the loop together.
@@ -818,6 +898,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
         wait(oD + 8 * (2 * grp + vp), ((k >> 1) * ((vts + 1 - vp) / 2) + (v >> 1)) & 1);
         tc_fence_after();
         uint32_t w[16];
+        float top = 0.f;  // of P c
         const uint32_t tO = tmem + 256 + o * 128 + lanes + 32 * g;
 #pragma unroll
         for (int h = 0; h < 32; h += 16) {
@@ -828,12 +909,15 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
           reg_fence(u);
           reg_fence(s);
 #pragma unroll
+          for (int j = 0; j < 16; j += 2) top = max_abs3(top, __uint_as_float(u[j]), __uint_as_float(u[j + 1]));
+#pragma unroll
           for (int j = 0; j < 8; ++j)
             w[h / 2 + j] =
                 counts ? pack_bf16x2(fmaf(fr, __uint_as_float(s[2 * j]), __uint_as_float(u[2 * j])),
                                      fmaf(fr, __uint_as_float(s[2 * j + 1]), __uint_as_float(u[2 * j + 1])))
                        : 0u;
         }
+        spoilt |= counts && !(top < INFINITY);
         tc_fence_before();
         warp_arrive(oR + 8 * o);
         if (tok0 >= 0) {
@@ -857,6 +941,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
     }
     if (g == 0 && lane == 0) bulk_wait_all();
     __syncwarp();
+    if (bar_red_or(id, 64, spoilt)) repair_rows<DK>(p, tiles, grp, q, g);  // (behind the stores of both warps' columns)
   }
   tc_fence_before();
   __syncthreads();
