@@ -59,6 +59,7 @@ struct LaCfg {
   static constexpr uint32_t SMEM = 2 * STAGE + 2 * SB + 1024;  // (1024: for aligning the tiles)
   static constexpr uint32_t SMEM_STATE = 2 * (XB + CB) + 1024;
   static constexpr int OCC = DK <= 64 ? 3 : (DK == 128 ? 2 : 1);
+  static constexpr int GT = NTS < 8 ? NTS : 8;  // state tiles whose update is looked at together
 };
 
 // byte offset of 16-byte chunk ch of row r in a swizzled tile of D bf16 columns
@@ -66,6 +67,38 @@ template <int D>
 __device__ __forceinline__ uint32_t tile_at(int r, int ch) {
   const int x = D >= 64 ? (r & 7) : ((r >> 1) & 3);
   return (uint32_t)(r * (D * 2) + ((ch ^ x) << 4));
+}
+
+// A chunk's update of the state in fp32 multiply-adds, where d[m][r] (rows v, v + 8 (r >> 1), columns dk + 8 m + (r & 1)) is
+// not finite
+template <int DK, int DVT, int GT>
+__device__ __forceinline__ void add_tokens(float (&d)[GT][4], uint32_t bA, uint32_t bC, int dk, int v, int n, float lg,
+                                           float upd, int shift) {
+  uint32_t on = 0u;
+#pragma unroll
+  for (int m = 0; m < GT; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (!(fabsf(d[m][r]) < INFINITY)) on |= 1u << (4 * m + r), d[m][r] = 0.f;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const float w = upd * pw(lg, n - 1 - j + shift);
+    float c[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint16_t x;
+      asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(bC + tile_at<DVT>(j, v / 8 + k) + (v & 7) * 2));
+      c[k] = bf16_to_f32(x) * w;
+    }
+#pragma unroll
+    for (int m = 0; m < GT; ++m) {
+      uint32_t a;
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a) : "r"(bA + tile_at<DK>(j, dk / 8 + m) + (dk & 7) * 2));
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (on >> (4 * m + r) & 1u) d[m][r] = fmaf(r & 1 ? bf16_hi(a) : bf16_lo(a), c[r >> 1], d[m][r]);
+    }
+  }
 }
 
 // which state element register `reg` of quad i of thread t holds
@@ -386,25 +419,35 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
         al[ks][r] = pack_bf16x2(x0, x1);
       }
     }
+    constexpr int GT = C::GT;
 #pragma unroll
-    for (int i = 0; i < NTS; i += 2) {
-      float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    for (int i0 = 0; i0 < NTS; i0 += GT) {
+      float d[GT][4], top = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        uint32_t kb[4];
-        ldmatrix_x4_trans(kb, ((bA + oAu) ^ (uint32_t)(i << 4)) + 16 * ks * RX);
-        mma_bf16_16816(d[0], al[ks], kb[0], kb[1]);
-        mma_bf16_16816(d[1], al[ks], kb[2], kb[3]);
-        mma_bf16_16816(d[0], am[ks], kb[0], kb[1]);
-        mma_bf16_16816(d[1], am[ks], kb[2], kb[3]);
-        mma_bf16_16816(d[0], ah[ks], kb[0], kb[1]);
-        mma_bf16_16816(d[1], ah[ks], kb[2], kb[3]);
+      for (int i = 0; i < GT; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < GT; i += 2) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          uint32_t kb[4];
+          ldmatrix_x4_trans(kb, ((bA + oAu) ^ (uint32_t)((i0 + i) << 4)) + 16 * ks * RX);
+          mma_bf16_16816(d[i], al[ks], kb[0], kb[1]);
+          mma_bf16_16816(d[i + 1], al[ks], kb[2], kb[3]);
+          mma_bf16_16816(d[i], am[ks], kb[0], kb[1]);
+          mma_bf16_16816(d[i + 1], am[ks], kb[2], kb[3]);
+          mma_bf16_16816(d[i], ah[ks], kb[0], kb[1]);
+          mma_bf16_16816(d[i + 1], ah[ks], kb[2], kb[3]);
+        }
       }
+      // an infinite c or a: its terms' rests are NaN, or zeros that meet it; token by token it stays what it is
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        S[i][r] = fmaf(wS, S[i][r], d[0][r]);
-        S[i + 1][r] = fmaf(wS, S[i + 1][r], d[1][r]);
-      }
+      for (int i = 0; i < GT; ++i) top = max_abs3(max_abs3(top, d[i][0], d[i][1]), d[i][2], d[i][3]);
+      if (__any_sync(0xffffffffu, !(top < INFINITY)))
+        add_tokens<DK, DVT>(d, bA, bC, kg * C::DKW + 8 * i0 + t0, 16 * vg + g0, n, lg, ps.upd, ps.shift);
+#pragma unroll
+      for (int i = 0; i < GT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[i0 + i][r] = fmaf(wS, S[i0 + i][r], d[i][r]);
     }
     if (!STATE_ONLY && c + 1 < cend) publish(st ^ 1);
   }

@@ -410,9 +410,11 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
           reg_fence(r1);
           reg_fence(r2);
 #pragma unroll
-          for (int j = 0; j < 16; ++j)  // smallest first
-            S[h + j] = fmaf(wS, S[h + j],
-                            (__uint_as_float(r2[j]) + __uint_as_float(r1[j])) + __uint_as_float(r0[j]));
+          for (int j = 0; j < 16; ++j) {  // smallest first
+            const float hi = __uint_as_float(r0[j]), sum = (__uint_as_float(r2[j]) + __uint_as_float(r1[j])) + hi;
+            // an infinite c or a: what it leaves to the lower terms is NaN, or zeros that meet it
+            S[h + j] = fmaf(wS, S[h + j], sum == sum ? sum : hi);
+          }
         }
       }
       tc_fence_before();

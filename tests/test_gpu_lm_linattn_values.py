@@ -109,3 +109,26 @@ def test_what_a_value_that_is_not_finite_reaches(S, dtype, T, Dk, Dv, value):
                     rest = torch.where(hit, 0, out.float() - plain[n].float())
                     tol = 0 if n in ("state", "dstate") else 6 * 2.0 ** -8 * (1 + 2.0 ** -7) * size[n]
                     assert (rest.abs() <= tol).all(), (name, n, t, b)
+
+
+@pytest.mark.parametrize("dtype,T,Dk,Dv", SHAPES)
+def test_an_infinity_stays_one_in_the_state(S, dtype, T, Dk, Dv):
+    """k_t v_t^T of an infinite k or v is an infinity of the product's sign, and stays one in the state; two of
+    opposite sign are NaN.  The same holds for q and do in the initial state's gradient."""
+    d = draw(T, Dk, Dv, dtype)
+    inf, t0, t1 = float("inf"), T // 2, T // 2 + 2
+    for a, c, n in (("k", "v", "state"), ("q", "do", "dstate")):
+        if n == "dstate" and T > 600 and Dk != 128:
+            continue
+        # column 3 of c, row 5 of a: one infinity; column 7 of c, row 9 of a: one of either sign
+        x, y = d[a].clone(), d[c].clone()
+        y[t0, 0, 0, 3], y[t0, 0, 0, 7], y[t1, 0, 0, 7] = inf, inf, -inf
+        x[t0, 0, 1, 5], x[t0, 0, 1, 9], x[t1, 0, 1, 9] = -inf, inf, -inf
+        got = (forward if n == "state" else backward)(S, dict(d, **{a: x, c: y}))[n]
+        outer = lambda t, h: x[t, 0, h].double()[:, None] * y[t, 0, h].double()[None]  # noqa: E731
+        for h, hit in ((0, (slice(None), [3, 7])), (1, ([5, 9], slice(None)))):
+            want = (outer(t0, h) + outer(t1, h))[hit]
+            assert not want.isfinite().any() and torch.equal(got[0, h][hit].double().nan_to_num(2.0, 1.0, -1.0),
+                                                             want.nan_to_num(2.0, 1.0, -1.0)), n
+            got[0, h][hit] = 0.0
+        assert got.isfinite().all()
