@@ -344,7 +344,8 @@ typedef struct {
   int32_t dtype; /* rnn_dtype_t of q, k, v, o */
   int32_t T, B, NH, Dk, Dv;
   float scale;
-  int32_t flags; /* 0 */
+  int32_t flags; /* 0, or RNN_FLAG_TEST_TIMEOUT: rnn_linattn_fwd and _bwd at sizes whose kernels wait on the device
+                    (tcgen05), else RNN_ERR_UNSUPPORTED */
 } rnn_linattn_desc_t;
 
 typedef struct {

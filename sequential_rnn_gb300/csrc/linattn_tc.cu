@@ -113,8 +113,8 @@ struct TcWait {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
-      if (mbar_try_wait(bar, parity)) return true;
       if (*abort_flag) return false;
+      if (mbar_try_wait(bar, parity)) return true;
       if (globaltimer_ns() - t0 > limit_ns) {
         *abort_flag = 1;
         atomicOr(status, kStatusTimeout);
@@ -123,7 +123,7 @@ struct TcWait {
     }
   }
 };
-// after an abort: a copy that was issued on `bar` lands before the CTA leaves
+// After an abort, whoever gave up: what was issued on `bar` (a copy, the MMAs before a commit) ends before the CTA leaves.
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity))
@@ -184,13 +184,13 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
   using C = StCfg<DK>;
   constexpr int DKB = C::DKB, NC = C::NC, NCW = C::NCW, OWN = TcOrder<DK>::OWN, NA = C::NA;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ int abort_flag_s;
+  __shared__ int abort_flag_s, issued_s;
   __shared__ uint32_t tslot_s;
-  __shared__ __align__(8) uint64_t bars_s[16];
+  __shared__ __align__(8) uint64_t bars_s[13];
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  // copies of a landed; terms ready; MMAs done; sums read; a's rows zeroed
+  // copies of a landed; a multiplied; terms ready; MMAs done; sums read; the last MMAs of all done
   const uint32_t bar = smem_u32(bars_s);
-  const uint32_t aF = bar, aE = bar + 24, tR = bar + 48, mD = bar + 64, sR = bar + 80;
+  const uint32_t aF = bar, aE = bar + 24, tR = bar + 48, mD = bar + 64, sR = bar + 80, xD = bar + 96;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int vts = p.DV / 64;
   if (STATE_ONLY || p.nseg == 1) {  // the call's first kernel
@@ -222,7 +222,9 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
       mbar_init(mD + 8 * i, 1);
       mbar_init(sR + 8 * i, NCW);
     }
+    mbar_init(xD, 1);
     abort_flag_s = 0;
+    issued_s = 0;
     fence_mbar_init();
     fence_async_smem();
   }
@@ -250,8 +252,7 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
         for (int k = 0; k < DKB / 64; ++k)
           tma_load_4d(d + k * kBlkBytes, &m.a[w.job], mb * DKB + 64 * k, hA, bA, token(it), f);
       }
-      if (it < cnt)
-        for (int k = it - NA < 0 ? 0 : it - NA; k < it; ++k) drain(aF + 8 * (k % NA), (k / NA) & 1);
+      issued_s = it;
     }
     __syncwarp();
   } else if (warp == C::WMMA) {
@@ -272,6 +273,7 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
         umma_commit(aE + 8 * s);
         umma_commit(mD + 8 * (it & 1));
       }
+      umma_commit(xD);
     }
     __syncwarp();
   } else {
@@ -366,7 +368,7 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
         }
       }
       fence_async_smem();
-      warp_arrive(tR + 8 * (it % C::NT));
+      if (!(p.withhold && it == 0 && warp == 0)) warp_arrive(tR + 8 * (it % C::NT));
       if (C::WIDE)
         fetch(it + 2, cn);
       else
@@ -442,6 +444,11 @@ __global__ void __launch_bounds__(StCfg<DK>::THREADS, StCfg<DK>::OCC)
   tc_fence_before();
   __syncthreads();
   if (warp == C::WMMA) {
+    if (lane == 0 && abort_flag_s) {
+      drain(xD, 0);
+      for (int k = issued_s - NA < 0 ? 0 : issued_s - NA; k < issued_s; ++k) drain(aF + 8 * (k % NA), (k / NA) & 1);
+    }
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM);
   }
@@ -601,19 +608,19 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
   using C = OutCfg<DK>;
   constexpr int NX = C::NX, NCS = C::NCS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ int abort_flag_s;
+  __shared__ int abort_flag_s, issued_s[2];  // copies of x and a, of c and the state
   __shared__ uint32_t tslot_s;
-  __shared__ __align__(8) uint64_t bars_s[29];
+  __shared__ __align__(8) uint64_t bars_s[30];
   __shared__ OutTile info_s[4];  // what the loading warp tells the others of its tiles, the last four
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bar = smem_u32(bars_s);
   // x, a landed; c, state landed; MMAs done, by buffer of c and state; scores done; scores in
   // bf16; sums read; c's rows behind the last token zeroed; info_s written; sums done, by group and parity of v; c landed
-  // whose rows a group has to zero; scores multiplied.  A barrier's waiter waits for every one of its phases in turn (of one that it saw only
+  // whose rows a group has to zero; scores multiplied; the last MMAs of all done.  A barrier's waiter waits for every one of its phases in turn (of one that it saw only
   // every other time it would take the phase before for the one that it wants: their parity is all it
   // sees), so what a group waits for has a barrier for each group.
   const uint32_t xF = bar, cF = bar + 24, dn = bar + 48, sc = bar + 72, pW = bar + 88, oR = bar + 104, cZ = bar + 120,
-                 iF = bar + 136, oD = bar + 168, zF = bar + 200, sF = bar + 216;
+                 iF = bar + 136, oD = bar + 168, zF = bar + 200, sF = bar + 216, xD = bar + 232;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nch = (p.T + kTC - 1) / kTC;
   const int vts = p.DV / 64;
@@ -642,7 +649,8 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
     for (int i = 17; i < 29; ++i) mbar_init(bar + 8 * i, 1);
     for (int i = 0; i < 3; ++i) mbar_init(dn + 8 * i, 2);  // (P c's and x S's)
     for (int i = 0; i < 4; ++i) mbar_init(oD + 8 * i, 2);
-    abort_flag_s = 0;
+    mbar_init(xD, 3);
+    abort_flag_s = issued_s[0] = issued_s[1] = 0;
     fence_mbar_init();
     fence_async_smem();
   }
@@ -660,7 +668,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
     if (lane == 0) {
       const OutTile stride = digits(p, nch, (int)gridDim.x);
       OutTile at = digits(p, nch, blockIdx.x);
-      int f = 0, done = 0;  // c and state tiles; of these, known to be multiplied
+      int f = 0, done = 0, xa = 0;  // c and state tiles; of these, known to be multiplied; tiles of x and a
       bool ok = true;
       auto multiplied = [&](int upto) {  // one after the other: no barrier is left two phases behind
         for (; ok && done < upto; ++done) ok = wait(dn + 8 * (done % NCS), (done / NCS) & 1);
@@ -689,6 +697,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
           tma_load_4d(d + i * kBlkBytes, &m.x[j], 64 * i, t.h * m.xh[j], t.b * m.xb[j], tok, xF + 8 * s);
           tma_load_4d(d + C::X + i * kBlkBytes, &m.a[j], 64 * i, t.h * m.ah[j], t.b * m.ab[j], tok, xF + 8 * s);
         }
+        xa = k + 1;
       };
       // in the order in which the MMAs take them (the next tile's scores follow this one's first product
       // with the state): a copy whose buffer a later MMA has to free must not stand before one that this MMA needs
@@ -717,10 +726,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
         if (NX == 1 && ok && k + 1 < count) load_xa(tn, k + 1);
         t = tn;
       }
-      if (!ok) {  // copies in flight land first (a barrier without one is waited for in vain, 10 ms)
-        for (int i = 0; i < 3; ++i) drain(xF + 8 * i, 0), drain(xF + 8 * i, 1);
-        for (int i = 0; i < 3; ++i) drain(cF + 8 * i, 0), drain(cF + 8 * i, 1);
-      }
+      issued_s[0] = xa, issued_s[1] = f;
     }
     __syncwarp();
   } else if (warp >= C::WMMA) {
@@ -743,6 +749,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
         }
         umma_commit(sc + 8 * (k & 1));
       }
+      umma_commit(xD);
     } else if (lane == 0 && warp == C::WMMA + 1) {  // P c
       constexpr uint32_t idesc = idesc_bf16_f32(128, 64, false, true);
       uint32_t nz[2] = {0, 0};  // c tiles with rows zeroed, by group
@@ -770,6 +777,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
         }
         if (ok) umma_commit(sF + 8 * (k & 1));
       }
+      umma_commit(xD);
     } else if (lane == 0) {  // x S
       constexpr uint32_t idesc = idesc_bf16_f32(128, 64, false, true);
       bool ok = true;
@@ -792,6 +800,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
           umma_commit(dn + 8 * cb);
         }
       }
+      umma_commit(xD);
     }
     __syncwarp();
   } else {
@@ -882,7 +891,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
       tmem_st16(tS + 16 * (g + 2), pk[1]);
       tmem_wait_st();
       tc_fence_before();
-      warp_arrive(pW + 8 * grp);
+      if (!(p.withhold && k == 0 && warp == 0)) warp_arrive(pW + 8 * grp);
       const int tok0 = token_of(t) + 32 * q;  // of this warp's first row (reversed: possibly below 0)
       const bool zero_c = ragged(t), counts = rev ? row >= kTC - n : row < n;
       for (int v = 0; v < vts; ++v) {
@@ -948,6 +957,13 @@ __global__ void __launch_bounds__(OutCfg<DK>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == C::WMMA) {
+    if (lane == 0 && abort_flag_s) {
+      drain(xD, 0);
+      for (int k = issued_s[0] - NX < 0 ? 0 : issued_s[0] - NX; k < issued_s[0]; ++k) drain(xF + 8 * (k % NX), (k / NX) & 1);
+      for (int k = issued_s[1] - NCS < 0 ? 0 : issued_s[1] - NCS; k < issued_s[1]; ++k)
+        drain(cF + 8 * (k % NCS), (k / NCS) & 1);
+    }
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -113,6 +113,7 @@ struct LinAttnParams {
   void* chunk_states;      // bf16 [pass][head of a row][chunk][DK][DV] (kLinAttnTc)
   int* status;
   int clear;               // clear the status word (the first launch of a call)
+  int withhold;            // test: an arrival of each kernel's first wait for compute warps is left out (kLinAttnTc)
   unsigned long long timeout_ns;
 };
 enum : int { kLinAttnF32 = 0, kLinAttnMma = 1, kLinAttnTc = 2 };

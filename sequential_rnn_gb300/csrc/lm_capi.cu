@@ -18,7 +18,8 @@ bool head_dim_ok(int32_t d) { return d == 32 || d == 64 || d == 128 || d == 256;
 
 int check_linattn(const rnn_linattn_desc_t* d) {
   if (d == nullptr || !valid_dtype(d->dtype)) return RNN_ERR_INVALID_ARG;
-  if (d->T < 0 || d->B < 0 || d->NH < 0 || d->Dk <= 0 || d->Dv <= 0 || d->flags != 0)
+  if (d->T < 0 || d->B < 0 || d->NH < 0 || d->Dk <= 0 || d->Dv <= 0 ||
+      (d->flags & ~RNN_FLAG_TEST_TIMEOUT) != 0)
     return RNN_ERR_INVALID_ARG;
   if (!head_dim_ok(d->Dk) || !head_dim_ok(d->Dv) || d->T > (1 << 30)) return RNN_ERR_UNSUPPORTED;
   // one CTA per row, head, column tile and segment: the largest grid
@@ -64,6 +65,16 @@ size_t linattn_ws(const rnn_linattn_desc_t* d, int pass) {
   return a > b ? a : b;  // the two launches follow one another on the stream
 }
 
+// RNN_FLAG_TEST_TIMEOUT is for the kernels that wait on the device
+bool waits(const rnn_linattn_desc_t* d, int pass) {
+  const bool bf16 = d->dtype == RNN_BF16;
+  auto tc = [&](int npass, int DK, int DV) {
+    return linattn_plan(bf16, npass, d->T, d->B, d->NH, DK, DV).path == kLinAttnTc;
+  };
+  if (pass == 0) return tc(1, d->Dk, d->Dv);
+  return d->Dk == d->Dv ? tc(3, d->Dk, d->Dv) : tc(2, d->Dv, d->Dk) && tc(1, d->Dk, d->Dv);
+}
+
 int run_passes(LinAttnParams& p, bool bf16, int DK, int DV, void* workspace, cudaStream_t s) {
   p.DK = DK;
   p.DV = DV;
@@ -74,7 +85,7 @@ int run_passes(LinAttnParams& p, bool bf16, int DK, int DV, void* workspace, cud
   p.ws = reinterpret_cast<float*>(ws);
   p.chunk_states = ws + align_up(pl.seg_bytes, 256);
   p.status = static_cast<int*>(workspace);
-  p.timeout_ns = kTimeoutNs;
+  p.timeout_ns = p.withhold ? kTestTimeoutNs : kTimeoutNs;
   if (pl.path == kLinAttnTc) {
     const int e = launch_linattn_tc(p, s);
     if (e != kLinAttnTooWide) return e;
@@ -177,6 +188,7 @@ int rnn_linattn_fwd(const rnn_linattn_desc_t* d, const rnn_linattn_strides_t* st
   if (!aligned(workspace, 256)) return RNN_ERR_MISALIGNED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d->B == 0 || d->NH == 0) return clear_status(workspace, workspace_bytes, s);
+  if (d->flags != 0 && !waits(d, 0)) return RNN_ERR_UNSUPPORTED;
   if (log_decay == nullptr) return RNN_ERR_INVALID_ARG;
   if (d->T > 0 && (q == nullptr || k == nullptr || v == nullptr || o == nullptr))
     return RNN_ERR_INVALID_ARG;
@@ -191,6 +203,7 @@ int rnn_linattn_fwd(const rnn_linattn_desc_t* d, const rnn_linattn_strides_t* st
   LinAttnParams p{};
   p.npass = 1;
   p.clear = 1;
+  p.withhold = d->flags != 0;
   p.log_decay = log_decay;
   p.lens = lens;
   p.T = d->T;
@@ -224,6 +237,7 @@ int rnn_linattn_bwd(const rnn_linattn_desc_t* d, const rnn_linattn_strides_t* st
   if (!aligned(workspace, 256)) return RNN_ERR_MISALIGNED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d->B == 0 || d->NH == 0) return clear_status(workspace, workspace_bytes, s);
+  if (d->flags != 0 && !waits(d, 1)) return RNN_ERR_UNSUPPORTED;
   if (log_decay == nullptr) return RNN_ERR_INVALID_ARG;
   if (d->T > 0 && (q == nullptr || k == nullptr || v == nullptr || dout == nullptr ||
                    dq == nullptr || dk == nullptr || dv == nullptr))
@@ -242,6 +256,7 @@ int rnn_linattn_bwd(const rnn_linattn_desc_t* d, const rnn_linattn_strides_t* st
     return RNN_ERR_MISALIGNED;
   LinAttnParams p{};
   p.clear = 1;
+  p.withhold = d->flags != 0;
   p.log_decay = log_decay;
   p.lens = lens;
   p.T = d->T;
@@ -295,7 +310,7 @@ int rnn_linattn_step(const rnn_linattn_desc_t* d, const rnn_linattn_strides_t* s
                      int32_t n_slots, float* state, void* o, void* stream) {
   int e = check_linattn(d);
   if (e != RNN_OK) return e;
-  if (n_slots < 0 || d->T != 1) return RNN_ERR_INVALID_ARG;
+  if (n_slots < 0 || d->T != 1 || d->flags != 0) return RNN_ERR_INVALID_ARG;
   if (d->B == 0 || d->NH == 0) return RNN_OK;
   if (slots == nullptr && n_slots < d->B) return RNN_ERR_INVALID_ARG;
   if (q == nullptr || k == nullptr || v == nullptr || log_decay == nullptr || o == nullptr ||

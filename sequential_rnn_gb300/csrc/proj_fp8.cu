@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
   constexpr int NSTG = C::NSTG, NACC = C::NACC, WC = C::WC;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int abort_flag_s, issued_s;
+  __shared__ __align__(8) uint64_t last_s;  // the last MMAs of both issuers done
   volatile int* abort_flag = &abort_flag_s;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
@@ -118,6 +119,7 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
     for (int s = 0; s < 2 * NSTG; ++s) mbar_init(bar_full + 8 * s, 1);
     for (int s = 0; s < NSTG; ++s) mbar_init(bar_done + 8 * s, 1);
     for (int a = 0; a < NACC; ++a) mbar_init(bar_read + 8 * a, C::NPW);
+    mbar_init(smem_u32(&last_s), 2);
     abort_flag_s = 0;
     issued_s = 0;
     fence_mbar_init();
@@ -186,6 +188,7 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
                     idesc, k4 != 0 ? 1u : 0u);
           umma_commit(bar_done + 8 * s);
         }
+        umma_commit(smem_u32(&last_s));
       }
     }
     __syncwarp();
@@ -266,12 +269,15 @@ __global__ void __launch_bounds__(F8Cfg<BN>::THREADS, 1)
   __syncthreads();
   if (warp == 0) {
     if (lane == 0 && *abort_flag) {
-      // let TMA copies that were issued land before exit
-      for (int k = issued_s - NSTG < 0 ? 0 : issued_s - NSTG; k < issued_s; ++k) {
+      // let the MMAs and TMA copies that were issued end before exit
+      auto drain = [](uint32_t bar, uint32_t parity) {
         const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(bar_full + 8 * full_of(k), (k / NFULL) & 1))
+        while (!mbar_try_wait(bar, parity))
           if (globaltimer_ns() - t0 > 10000000ull) break;
-      }
+      };
+      drain(smem_u32(&last_s), 0);
+      for (int k = issued_s - NSTG < 0 ? 0 : issued_s - NSTG; k < issued_s; ++k)
+        drain(bar_full + 8 * full_of(k), (k / NFULL) & 1);
     }
     __syncwarp();
     tc_fence_after();
