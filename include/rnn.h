@@ -363,8 +363,8 @@ int rnn_linattn_fwd(const rnn_linattn_desc_t* desc, const rnn_linattn_strides_t*
 
 /* Gradients of L = sum(o * dout) + sum(stateT * dstateT) from the forward's inputs (nothing
  * is stashed): dq, dk [T, B, NH, Dk], dv [T, B, NH, Dv] contiguous in dtype, zero for
- * tokens that do not count; dstate0 [B, NH, Dk, Dv] fp32 (NULL = not written; must not be
- * dstateT).  dout has the strides st->o; dstateT NULL = zero.  Workspace as above (pass 1). */
+ * tokens that do not count; dstate0 [B, NH, Dk, Dv] fp32 (NULL = not written; must be neither
+ * state0 nor dstateT).  dout has the strides st->o; dstateT NULL = zero.  Workspace as above (pass 1). */
 int rnn_linattn_bwd(const rnn_linattn_desc_t* desc, const rnn_linattn_strides_t* st, const void* q,
                     const void* k, const void* v, const float* log_decay, const int32_t* lens,
                     const float* state0, const void* dout, const float* dstateT, void* dq, void* dk,

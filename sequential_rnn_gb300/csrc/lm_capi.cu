@@ -242,8 +242,8 @@ int rnn_linattn_bwd(const rnn_linattn_desc_t* d, const rnn_linattn_strides_t* st
   if (d->T > 0 && (q == nullptr || k == nullptr || v == nullptr || dout == nullptr ||
                    dq == nullptr || dk == nullptr || dv == nullptr))
     return RNN_ERR_INVALID_ARG;
-  // the passes run at once: one of them reads dstateT while another writes dstate0
-  if (dstateT != nullptr && dstateT == dstate0) return RNN_ERR_INVALID_ARG;
+  // the passes run at once: some read state0 and dstateT while another writes dstate0
+  if (dstate0 != nullptr && (dstateT == dstate0 || state0 == dstate0)) return RNN_ERR_INVALID_ARG;
   const size_t es = dtype_bytes(d->dtype);
   const St sq = strides_or(st ? st->q : nullptr, d, d->Dk), sk = strides_or(st ? st->k : nullptr, d, d->Dk);
   const St sv = strides_or(st ? st->v : nullptr, d, d->Dv), so = strides_or(st ? st->o : nullptr, d, d->Dv);
