@@ -13,6 +13,8 @@ using namespace srnn::api;
 namespace {
 
 bool valid_dtype(int32_t d) { return d == RNN_F32 || d == RNN_BF16; }
+// the widest row: the kernels count its columns, rounded up to tiles or strided over by a grid's share, in 32 bits
+constexpr int32_t kMaxCols = INT32_MAX - 4095;
 size_t dtype_bytes(int32_t d) { return d == RNN_F32 ? 4 : 2; }
 bool head_dim_ok(int32_t d) { return d == 32 || d == 64 || d == 128 || d == 256; }
 
@@ -104,6 +106,7 @@ int rnn_rms_norm(int32_t dtype, int32_t rows, int32_t N, float eps, const void* 
                  const void* residual, const float* weight, void* h, void* y, float* scale,
                  float* rstd, void* stream) {
   if (!valid_dtype(dtype) || rows < 0 || N <= 0 || !(eps >= 0.f)) return RNN_ERR_INVALID_ARG;
+  if (N > kMaxCols) return RNN_ERR_UNSUPPORTED;
   if (rows == 0) return RNN_OK;
   if (x == nullptr || weight == nullptr || y == nullptr) return RNN_ERR_INVALID_ARG;
   const size_t es = dtype_bytes(dtype);
@@ -123,6 +126,7 @@ int rnn_rms_norm_bwd(int32_t dtype, int32_t rows, int32_t N, const void* dy, con
                      const float* weight, const float* rstd, const void* dh, void* dx, float* dw,
                      void* workspace, size_t workspace_bytes, void* stream) {
   if (!valid_dtype(dtype) || rows < 0 || N <= 0) return RNN_ERR_INVALID_ARG;
+  if (N > kMaxCols) return RNN_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (rows == 0) {
     if (dw == nullptr) return RNN_OK;
@@ -147,7 +151,7 @@ int rnn_rms_norm_bwd(int32_t dtype, int32_t rows, int32_t N, const void* dy, con
 int rnn_quantize_weight(int32_t dtype, int32_t N, int32_t K, const void* W, void* Wq, float* Ws,
                         void* stream) {
   if (!valid_dtype(dtype) || N <= 0 || K <= 0) return RNN_ERR_INVALID_ARG;
-  if (N > 65535 * 128) return RNN_ERR_UNSUPPORTED;
+  if (N > 65535 * 128 || K > kMaxCols) return RNN_ERR_UNSUPPORTED;
   if (W == nullptr || Wq == nullptr || Ws == nullptr) return RNN_ERR_INVALID_ARG;
   if (!aligned(W, dtype_bytes(dtype)) || !aligned(Ws, 4)) return RNN_ERR_MISALIGNED;
   return map_launch_error(
@@ -160,7 +164,8 @@ int rnn_input_proj_fp8(int32_t M, int32_t N, int32_t K, const void* xq, const fl
   if (M < 0 || N <= 0 || K <= 0) return RNN_ERR_INVALID_ARG;
   if (workspace == nullptr || workspace_bytes < kStatusBytes) return RNN_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return RNN_ERR_MISALIGNED;
-  if (K % 16 != 0 || N % 8 != 0 || M > 65535 * 128) return RNN_ERR_UNSUPPORTED;
+  if (K % 16 != 0 || N % 8 != 0 || M > 65535 * 128 || N > kMaxCols || K > kMaxCols)
+    return RNN_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (M == 0) return clear_status(workspace, workspace_bytes, s);
   if (xq == nullptr || xs == nullptr || Wq == nullptr || Ws == nullptr || y == nullptr)
