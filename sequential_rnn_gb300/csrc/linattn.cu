@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
   // tokens that do not count: zeros
   const int rlo = len > c0 * kC ? len : c0 * kC, rhi = c1 * kC < p.T ? c1 * kC : p.T;
   constexpr int CH = DVT / 8;
-  for (int e = tid; e < (rhi - rlo) * CH; e += NT) {
+  for (long long e = tid; e < (long long)(rhi - rlo) * CH; e += NT) {
     const long long t = rlo + e / CH;
     __nv_bfloat16* go = static_cast<__nv_bfloat16*>(ps.out) + t * ps.os[0] + w.b * ps.os[1] +
                         w.h * ps.os[2] + w.vt * DVT + (e % CH) * 8;

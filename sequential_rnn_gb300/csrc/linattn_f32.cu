@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(C::NT, C::OCC)
   // them: 8 x 2048 gradients one after the other 133 us each instead of 100)
   depend_launch();
   const int rlo = len > c0 * kC32 ? len : c0 * kC32, rhi = c1 * kC32 < p.T ? c1 * kC32 : p.T;
-  for (int e = tid; e < (rhi - rlo) * C::CT; e += NT)
+  for (long long e = tid; e < (long long)(rhi - rlo) * C::CT; e += NT)
     *reinterpret_cast<float4*>(gout + (long long)(rlo + e / C::CT) * ps.os[0] + 4 * (e % C::CT)) =
         make_float4(0.f, 0.f, 0.f, 0.f);
 }
