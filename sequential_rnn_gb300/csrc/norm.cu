@@ -59,7 +59,8 @@ __device__ __forceinline__ float block_scale(float top) {
   return s > 0.f ? s : 1.f;
 }
 
-__device__ __forceinline__ bool in_range(float v) { return v >= 0x1p-60f && v <= 0x1p60f; }
+// a block's largest product and r: between them the scale, their product / 448, is no subnormal number
+__device__ __forceinline__ bool in_range(float v) { return v >= 0x1p-58f && v <= 0x1p60f; }
 __device__ __forceinline__ float e4m3_value(uint32_t code) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
 }

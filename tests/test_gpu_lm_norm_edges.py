@@ -65,3 +65,23 @@ def test_weights_that_are_not_finite(S, N, where, value, dtype):
     fine = np.isfinite(hw) & np.repeat(np.isfinite(top), 128, 1)[:, :N]
     want = O.e4m3((448 * np.where(fine, hw, 0) / full).astype(np.float32))
     assert np.array_equal(y[fine], want[fine])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [256, 1000, 301])
+def test_a_subnormal_scale_between_factors_that_are_not(S, N, dtype):
+    """A column of some 2^64 makes rstd 2^-59, a block's largest product is 2^-59, and its scale, 2^-127, is subnormal: coarse.
+    The codes are of the quotient by what is stored.  The products are ties of the quotient by the scale
+    before it was rounded, which fall to either side as the rounding goes."""
+    rows = 40
+    x = torch.zeros(rows, N)
+    x[:, 0] = 2.0 ** 63 * (1.5 + torch.arange(rows) / 128)
+    x[:, 128:256] = torch.tensor([448, 272, -304, 336, 368, -400, 432, 136] * 16)
+    w = torch.ones(N)
+    w[128:256] = 2.0 ** -68
+    x, w = x.to(DT[dtype]).cuda(), w.cuda()
+    out = S.rms_norm(x, w, quantize=True, train=True)
+    s = np64(out["scale"])[:, 1:2]
+    assert (s < 2.0 ** -126).all() and (s > 2.0 ** -129).all() and (np64(out["rstd"]) > 2.0 ** -60).all()
+    q = np64(x)[:, 128:256] * np64(w)[128:256] * (np64(out["rstd"])[:, None] / s)
+    assert np.array_equal(np64(out["y"])[:, 128:256], O.e4m3(q.astype(np.float32)))
