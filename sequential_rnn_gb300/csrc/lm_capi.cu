@@ -44,9 +44,9 @@ St strides_or(const int64_t* given, const rnn_linattn_desc_t* d, int D) {
   }
   return r;
 }
-bool strides_aligned(const St& s, size_t esize) {
-  for (long long v : s.s)
-    if (v < 0 || (v * (long long)esize) % 16 != 0) return false;
+bool strides_aligned(const St& s, size_t esize, int first = 0) {  // (1: without the token's)
+  for (int i = first; i < 3; ++i)
+    if (s.s[i] < 0 || s.s[i] % (long long)(16 / esize) != 0) return false;
   return true;
 }
 void set3(long long (&dst)[3], const St& s) {
@@ -326,7 +326,7 @@ int rnn_linattn_step(const rnn_linattn_desc_t* d, const rnn_linattn_strides_t* s
   const St sv = strides_or(st ? st->v : nullptr, d, d->Dv);
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) ||
       !aligned(state, 16) || !aligned(log_decay, 4) || !aligned(slots, 4) ||
-      !strides_aligned(sq, es) || !strides_aligned(sk, es) || !strides_aligned(sv, es))
+      !strides_aligned(sq, es, 1) || !strides_aligned(sk, es, 1) || !strides_aligned(sv, es, 1))
     return RNN_ERR_MISALIGNED;
   LinAttnStepParams p{};
   p.q = q, p.k = k, p.v = v, p.o = o;

@@ -36,3 +36,20 @@ def test_zeros_behind_more_than_2_to_the_31_vectors(S):
     assert not any(o[lo:lo + (1 << 24)].any().item() for lo in range(n, T, 1 << 24))
     del o, ws
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("token", [4, -64])
+def test_a_step_does_not_use_token_strides(S, token):
+    """A single token has no token stride: any value stands there."""
+    from sequential_rnn_gb300._lib import rnn_linattn_desc_t, rnn_linattn_strides_t
+    B, NH, D = 3, 2, 64
+    q, k, v = (torch.randn(B, NH, D, device="cuda").bfloat16() for _ in range(3))
+    g, state = torch.tensor([-0.1, -0.2], device="cuda"), torch.randn(B, NH, D, D, device="cuda")
+    st = rnn_linattn_strides_t()
+    for n in ("q", "k", "v"):
+        getattr(st, n)[:] = (token, NH * D, D)
+    st.o[:] = (token, 3, 5)
+    o, s = torch.empty_like(v), state.clone()
+    assert S.rnn_linattn_step(rnn_linattn_desc_t(1, 1, B, NH, D, D, 0.5, 0), st, q, k, v, g, None, B, s, o) == 0
+    want = S.linear_attention_step(q, k, v, g, state, scale=0.5)
+    assert torch.equal(o, want) and torch.equal(s, state)
