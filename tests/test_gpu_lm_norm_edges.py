@@ -85,3 +85,42 @@ def test_a_subnormal_scale_between_factors_that_are_not(S, N, dtype):
     assert (s < 2.0 ** -126).all() and (s > 2.0 ** -129).all() and (np64(out["rstd"]) > 2.0 ** -60).all()
     q = np64(x)[:, 128:256] * np64(w)[128:256] * (np64(out["rstd"])[:, None] / s)
     assert np.array_equal(np64(out["y"])[:, 128:256], O.e4m3(q.astype(np.float32)))
+
+
+def codes(h, w):
+    """e4m3 of the quotient by the block's scale, as rnn_rms_norm defines it."""
+    hw = np64(h) * np64(w)
+    top = blocks(np.abs(hw)).max(2)
+    top = np.repeat(np.where(top > 0, top, 1), 128, 1)[:, :hw.shape[1]]
+    return O.e4m3((448 * hw / top).astype(np.float32))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("weights", ["drawn", "ones"])
+@pytest.mark.parametrize("rows,N", [(1, 1), (5, 1), (3, 2), (3, 7), (2, 8), (300, 8), (40, 9), (33, 100), (20, 120), (21, 127),
+                                    (19, 128), (17, 129), (16, 136), (9, 255), (9, 257)])
+def test_codes_of_narrow_rows(S, rows, N, weights, dtype):
+    """A block that ends early, blocks of a few columns, rows narrower than a vector: equal codes."""
+    x, res, w = rand(70, rows, N, dtype=dtype), rand(71, rows, N, dtype=dtype), rand(72, N)
+    if weights == "ones":                          # products of 8 bits: many exact ties
+        w = torch.ones_like(w)
+    out = S.rms_norm(x, w, res, quantize=True)
+    assert np.array_equal(np64(out["y"]), codes(out["h"], w))
+    y, _ = O.rms_norm(np64(out["h"]), np64(w), 1e-6)
+    np.testing.assert_allclose(np64(out["scale"]), O.quantize(y)[1], rtol=2.0 ** -20)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,K", [(1, 1), (1, 7), (7, 1), (2, 129), (129, 2), (128, 128), (130, 300), (5, 1000)])
+def test_weight_codes(S, N, K, dtype):
+    """A code is that of W over the stored scale, unless the quotient lies within fp32's error (2^-23 of it) of a tie."""
+    W = rand(73, N, K, dtype=dtype)
+    W[:, ::5] = W[:, ::5].bfloat16().to(W.dtype)
+    Wq, Ws = S.quantize_weight(W)
+    s = np.repeat(np.repeat(np64(Ws), 128, 0)[:N], 128, 1)[:, :K]
+    top = O.quantize(np64(W), 128)[1]
+    np.testing.assert_allclose(np64(Ws), top, rtol=2.0 ** -23)
+    q = np64(W) / s
+    lo, hi = O.e4m3(q * (1 - 2.0 ** -23)), O.e4m3(q * (1 + 2.0 ** -23))
+    got = np64(Wq)
+    assert ((got == lo) | (got == hi)).all()
