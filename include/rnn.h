@@ -288,9 +288,11 @@ int rnn_fwd_noalloc(const rnn_desc_t* desc, const void* Wx, const void* R, const
  * gradient.  scale NULL: y has dtype.  Otherwise y is 8-bit floating point (e4m3)
  * and scale [rows, ceil(N/128)] fp32 holds, for each row and block of 128
  * columns, max|y| / 448 (1 where that is zero); y holds the exact quotient y / scale,
- * rounded to fp32 and then to e4m3 (to nearest even).  A y that is not a number has a NaN code and does not count
- * towards its block's scale; an infinite one has a NaN code and makes the scale infinite.  N == 0 is refused, rows == 0 a no-op.  Any N up to 2^31 - 4096; widths that are
- * a multiple of 16 bytes (of 8 values for e4m3) with 16-byte aligned pointers
+ * rounded to fp32 and then to e4m3 (to nearest even).  A y that is not a number has a
+ * NaN code and does not count towards its block's scale; an infinite one has a NaN code
+ * and makes the scale infinite.  Squares are summed in fp32: a row with values past 2^63
+ * can have r = 0.  N == 0 is refused, rows == 0 a no-op.  Any N up to 2^31 - 4096; widths
+ * that are a multiple of 16 bytes (of 8 values for e4m3) with 16-byte aligned pointers
  * run the vector kernels.  Alignment: the element's.  No workspace, no device status. */
 int rnn_rms_norm(int32_t dtype, int32_t rows, int32_t N, float eps, const void* x,
                  const void* residual, const float* weight, void* h, void* y, float* scale,
@@ -309,7 +311,8 @@ int rnn_rms_norm_bwd(int32_t dtype, int32_t rows, int32_t N, const void* dy, con
                      void* workspace, size_t workspace_bytes, void* stream);
 
 /* A weight W [N, K] (dtype) in 8 bits: Wq [N, K] e4m3, Ws [ceil(N/128), ceil(K/128)]
- * fp32, one scale (max|W| / 448, 1 where that is zero) for each 128 x 128 block.  N at most 8388480, K 2^31 - 4096. */
+ * fp32, one scale (max|W| / 448, 1 where that is zero) for each 128 x 128 block;
+ * values that are not finite as above.  N at most 8388480, K at most 2^31 - 4096. */
 int rnn_quantize_weight(int32_t dtype, int32_t N, int32_t K, const void* W, void* Wq, float* Ws,
                         void* stream);
 
@@ -318,8 +321,8 @@ int rnn_quantize_weight(int32_t dtype, int32_t N, int32_t K, const void* W, void
  * xq [M, K], Wq [N, K] e4m3; xs [M, ceil(K/128)] and Ws [ceil(N/128), ceil(K/128)] fp32
  * (rnn_rms_norm's and rnn_quantize_weight's outputs); bias [N] fp32 (NULL =
  * none); y [M, N] bf16, rounded once from the fp32 sum.  Requires K % 16 == 0,
- * N % 8 == 0, M <= 8388480, N and K at most 2^31 - 4096.  Alignment: xq, Wq, y 16 bytes, fp32 pointers 4, workspace
- * 256 bytes and >= 256 bytes (status word at offset 0).  M == 0 is a no-op. */
+ * N % 8 == 0, M <= 8388480, N and K at most 2^31 - 4096.  Alignment: xq, Wq, y 16
+ * bytes, fp32 pointers 4, workspace 256 bytes and >= 256 bytes (status word at offset 0).  M == 0 is a no-op. */
 int rnn_input_proj_fp8(int32_t M, int32_t N, int32_t K, const void* xq, const float* xs,
                        const void* Wq, const float* Ws, const float* bias, void* y,
                        void* workspace, size_t workspace_bytes, void* stream);
@@ -337,7 +340,8 @@ int rnn_input_proj_fp8(int32_t M, int32_t N, int32_t K, const void* xq, const fl
  * RNN_BF16: tokens are taken in chunks of 64 or 128 on the tensor cores, scores and the
  * state as an operand rounded to bf16 once, all sums and the state fp32.  RNN_F32: fp32 throughout.
  * A value that is not finite reaches the outputs of its own and later tokens of its row and head and the
- * state, as the recurrence has it (in the gradient: the tokens before it, too); never an output that does not depend on it.
+ * state, as the recurrence has it (in the gradient: the tokens before it, too); never an
+ * output that does not depend on it.
  * Alignment: 16 bytes for tensors and strides, 4 for log_decay and lens, workspace 256
  * and >= rnn_linattn_workspace_size(desc, 0) bytes (status word at offset 0). */
 typedef struct {

@@ -18,8 +18,8 @@
 // A CTA takes a head of a row (of up to 64 columns of c) and walks its chunks, warps side by side over 16 rows of
 // the output and 16 of the state.  Bound by latency: a chunk is a chain of copies, three products that depend on one
 // another and a barrier, with 12 warps an SM (168 registers each) to fill it; the tensor cores run at 42% of
-// mma.sync's rate, DRAM at 26% of its.  Measured, 12 heads of 64: 1 x 16384 tokens 55.5 us (in 37 segments), 16 x
-// 1024 gradient 104.6, five ragged rows of up to 333 13.1.
+// mma.sync's rate, DRAM at 26% of its.  Measured, 12 heads of 64: 1 x 16384 tokens 56.4 us (in 37 segments), 16 x
+// 1024 gradient 104.3, five ragged rows of up to 333 13.4.
 //
 // Rounding: the scores times their decay, and the state as an operand of q S,
 // are rounded to bf16, once each (as bf16 results are); every sum is fp32.  The

@@ -7,12 +7,13 @@ namespace srnn {
 LinAttnPlan linattn_plan(bool bf16, int npass, int T, int B, int NH, int DK, int DV) {
   LinAttnPlan pl{};
   // tcgen05 where it is the faster (us, mma.sync / tcgen05, T x rows x heads x Dk x Dv).  Dk of 128 or more: from 128
-  // tokens on (128x8x6x128x128 12.1 / 9.5, its gradient 23.0 / 16.4; 128x8x4x256x256 16.8 / 16.7, 44.8 / 32.2; 64 tokens
-  // 8.2 / 9.3 and 11.4 / 16.5).  Dk = 64, whose products with a are small, against wider values: the gradient from 192
-  // tokens on (200x16x8x64x128 58 / 40; 128x2x8 14.4 / 16.5), the forward pass from 512 (512x2x8 15.4 / 13.3, 1024x16x8 69 /
-  // 42; 256x8x8 12.8 / 13.5).  64 x 64: the gradient's passes on long rows (4096x4x12 148 / 119; 1024x16x12 101 / 108,
-  // 2048x8x12 100 / 105), the forward pass with enough long rows (1024x4x12 27.8 / 22.6, 2048x8x12 66.9 / 51.1;
-  // 16384x1x12 55.3 / 57.1, 512x16x12 25.3 / 26.3).
+  // tokens on (128x8x6x128x128 12.7 / 10.1, its gradient 24.1 / 17.3; 128x8x4x256x256 16.8 / 17.4, 45.7 / 32.9; 64 tokens
+  // 8.3 / 9.9 and 15.7 / 17.0; few heads: 128x1x1x128x128 9.0 / 9.9, 9.0 / 12.0, 256x1x2x128x128 14.4 / 10.9, 14.4 / 12.1,
+  // 128x1x1x256x256 12.4 / 11.8, 12.3 / 12.7; 128x1x2x256x64 12.3 / 9.8).  Dk = 64, whose products with a are small, against
+  // wider values: the gradient from 192 tokens on (200x16x8x64x128 59 / 40; 128x2x8 15.6 / 18.1), the forward pass from 512
+  // (512x2x8 16.0 / 14.1, 1024x16x8 53 / 43; 256x8x8 12.6 / 13.9).  64 x 64: the gradient's passes on long rows (4096x4x12
+  // 150 / 119; 1024x16x12 101 / 105, 2048x8x12 101.7 / 101.8), the forward pass with enough long rows (1024x4x12 28.4 /
+  // 23.6, 2048x8x12 67.5 / 52.0; 16384x1x12 55.7 / 58.1, 512x16x12 25.8 / 26.5).
   const long long heads = (long long)B * NH;
   bool tc = DK % 64 == 0 && DV % 64 == 0;
   if (DK > 64)

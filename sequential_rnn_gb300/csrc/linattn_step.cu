@@ -3,7 +3,7 @@
 // Bound by the state's bytes (8 DK DV a row and head, read and written once).
 // One CTA per (row, head, 64 or 32 columns): a thread owns four neighbouring
 // columns of every (256 / column groups)-th row of S; the partial sums of q S meet in
-// shared memory.  64 rows of 12 heads, 64 x 64: 4.6 us with the call, 5.5 TB/s; a thread's rows of S are loaded in batches
+// shared memory.  64 rows of 12 heads, 64 x 64: 4.7 us with the call, 5.5 TB/s; a thread's rows of S are loaded in batches
 // (one after the other, each load waited for the store before it).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -22,8 +22,8 @@
 // update, P c, x S).  Loading through the copy engine matters: with cp.async from all threads
 // the copies of a tile took longer to issue (2,000-2,600 cycles) than its MMAs to run.
 //
-// Measured: 4 x 256, 4 rows of 4096 86 us (states 50, outputs 43 alone); gradient 6 x 128, 4 rows of 2001 53.7
-// us (28 and 32).  The states are bound by what a chunk makes the compute warps do one after the other (terms of c, 3 x 128
+// Measured: 4 x 256, 4 rows of 4096 87 us (states 52, outputs 42 alone); gradient 6 x 128, 4 rows of 2001 54.7
+// us (30 and 32).  The states are bound by what a chunk makes the compute warps do one after the other (terms of c, 3 x 128
 // columns of sums out of TMEM, the state's stores: issue slots 55%, load and store unit 63%), the outputs by
 // the copies (320 KB a tile with 256 columns, half of it from DRAM: inputs, outputs and chunk states are 200 MB
 // beside 129 of L2) and the chain from a tile's scores to its stores.

@@ -22,11 +22,11 @@
 // TMA stores (stored straight from registers, an epilogue took 6,200 cycles).
 //
 // Measured at 16384 x 4096 x 1024: 84 us, 1.64 PFLOP/s (the bf16 matrix product's rate is 1.91), 23 us of bytes.
-// What bounds it is the promotion: every fp32 sum of a block of 128 leaves TMEM, at about 125 bytes a clock
-// and SM, which with nothing else would be 57 us, and a tile's epilogue between.
+// What bounds it is the promotion: every fp32 sum of a block of 128 leaves TMEM, 32 columns a load, a wait and the multiply-adds
+// one after the other (the tensor pipe is 34% busy), and a tile's epilogue between.
 //
 // A few rows (kFewRows at most) are bound by the weights' bytes instead: a kernel of its own reads each
-// weight once, straight into the registers of mma.sync (16 x 2304 x 768: 2.3 us on the device, 4.4 with its call).
+// weight once, straight into the registers of mma.sync (16 x 2304 x 768: 2.3 us on the device, 4.7 with its call).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

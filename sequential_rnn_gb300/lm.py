@@ -14,7 +14,7 @@ marshal arguments, and the others check them, allocate the outputs (both in
 csrc/binding.cpp) and raise ``RnnError`` on a non-OK status.  Everything runs on ``stream`` (a
 ``torch.cuda.Stream`` or a raw handle; None: the current stream), outputs and
 workspace are allocated for that stream, and inputs made on another one have to
-be ordered before it by the caller.
+be ordered before it, and kept until it is done with them, by the caller.
 """
 from __future__ import annotations
 
@@ -144,8 +144,8 @@ def rms_norm(x, weight, residual=None, *, eps=1e-6, quantize=False, train=False,
     """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight over the last dimension.
 
     x, residual [..., N] bf16 or fp32, weight [N] fp32.  Returns ``h`` (x itself
-    without a residual), ``y`` (x's type; with ``quantize`` e4m3, and ``scale``
-    [..., ceil(N/128)] fp32) and with ``train`` the ``rstd`` [...] fp32 that
+    without a residual), ``y`` (x's type; with ``quantize`` e4m3, NaN where y is not finite, and
+    ``scale`` [..., ceil(N/128)] fp32) and with ``train`` the ``rstd`` [...] fp32 that
     ``rms_norm_backward`` takes.
     """
     if stream is not None:
@@ -207,7 +207,9 @@ def linear_attention(q, k, v, log_decay, *, state=None, lens=None, scale=None, c
     contiguous last dimension are taken as they are), log_decay [NH] fp32,
     state [B, NH, Dk, Dv] fp32 or None, lens [B] int32 or None (tokens of each row
     that count), scale Dk^-0.5 unless given.  Returns ``o`` [T, B, NH, Dv], ``state``
-    (after the last token) and the ``workspace``.
+    (after the last token) and the ``workspace``.  A value that is not finite reaches its
+    own and later tokens of its row and head and the state, never an output that does not
+    depend on it.
     """
     if stream is not None:
         with _on(stream):

@@ -124,3 +124,23 @@ def test_weight_codes(S, N, K, dtype):
     lo, hi = O.e4m3(q * (1 - 2.0 ** -23)), O.e4m3(q * (1 + 2.0 ** -23))
     got = np64(Wq)
     assert ((got == lo) | (got == hi)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_weights_to_quantise_that_are_not_finite(S, dtype):
+    """As in the norm: NaN codes; a NaN leaves its block's scale to the others, an infinity makes it infinite."""
+    W = rand(74, 300, 400, dtype=dtype)
+    clean = S.quantize_weight(W)
+    W[5, 7], W[140, 390], W[130, 150] = float("nan"), float("inf"), -float("inf")
+    W[256:300, 256:384] = float("nan")             # a whole block
+    q, s = S.quantize_weight(W)
+    bad = ~torch.isfinite(W)
+    assert torch.equal(q.float().isnan(), bad)
+    want = clean[1].clone()
+    want[0, 0] = W[:128, :128][~bad[:128, :128]].float().abs().max() / 448
+    want[1, 3], want[1, 1], want[2, 2] = float("inf"), float("inf"), 1.0
+    assert torch.allclose(s, want, rtol=2.0 ** -22, atol=0)
+    other = torch.ones_like(bad)
+    for i, j in ((0, 0), (1, 3), (1, 1), (2, 2)):
+        other[128 * i:128 * i + 128, 128 * j:128 * j + 128] = False
+    assert torch.equal(q.float()[other], clean[0].float()[other])
