@@ -384,6 +384,96 @@ int rnn_linattn_step(const rnn_linattn_desc_t* desc, const rnn_linattn_strides_t
                      const void* k, const void* v, const float* log_decay, const int32_t* slots,
                      int32_t n_slots, float* state, void* o, void* stream);
 
+/* Gated linear recurrence: the cells without a recurrent matrix, so that a sequence is a scan.  For
+ * each row, head and channel, with the gates of Wx [T, B, NH, G*D] (gate-major, as for rnn_fwd):
+ *   RNN_GATES_FZ    c_t = sigm(f) c_{t-1} + sigm(-f) z           y_t = c_t
+ *   RNN_GATES_FZO   the same                                     y_t = sigm(o) c_t
+ *   RNN_GATES_IFZO  c_t = sigm(f) c_{t-1} + sigm(i) z            y_t = sigm(o) c_t
+ * y [T, B, NH, D] in dtype; state0, stateT [B, NH, D] fp32 (NULL = zero / not written; stateT may be
+ * state0).  lens [B] int32 (NULL = T for every row): tokens of a row that count, taken as at least
+ * 0 and at most T; what the others hold does not matter, their y is zero, and stateT is the state
+ * after the last one that counts.  stash (NULL = not written): what rnn_gated_bwd needs,
+ * rnn_gated_stash_size bytes.  Gates, states and sums are fp32, y is rounded once.  A value that is not
+ * finite reaches its own and later tokens of its row and channel (in the gradient: earlier ones, too) and
+ * nothing else; where a product of forget gates underflows, an infinity before it may turn to NaN.
+ * Wx, y contiguous; aligned as their element is (4 bytes for bf16 and 8 for fp32, with an even D, are faster).
+ * No workspace, no device status. */
+typedef enum { RNN_GATES_FZ = 2, RNN_GATES_FZO = 3, RNN_GATES_IFZO = 4 } rnn_gates_t;
+
+typedef struct {
+  int32_t dtype; /* rnn_dtype_t of Wx, y, dy, dWx */
+  int32_t T, B, NH, D;
+  int32_t gates; /* rnn_gates_t: the gates' number G */
+} rnn_gated_desc_t;
+
+/* Bytes of the stash: the fp32 state before every eighth token, [ceil(T/8), B, NH, D].  0 on an invalid desc. */
+size_t rnn_gated_stash_size(const rnn_gated_desc_t* desc);
+
+int rnn_gated_fwd(const rnn_gated_desc_t* desc, const void* Wx, const int32_t* lens, const float* state0, void* y,
+                  float* stateT, float* stash, void* stream);
+
+/* Gradients of L = sum(y * dy) + sum(stateT * dstateT) from the forward's Wx, lens and stash: dWx like Wx (zero for
+ * tokens that do not count), dstate0 [B, NH, D] fp32 (NULL = not written; may be dstateT).  dstateT NULL = zero. */
+int rnn_gated_bwd(const rnn_gated_desc_t* desc, const void* Wx, const int32_t* lens, const float* stash, const void* dy,
+                  const float* dstateT, void* dWx, float* dstate0, void* stream);
+
+/* One token (desc->T == 1, Wx [B, NH, G*D]) for each of B rows out of a cache of n_slots states [n_slots, NH, D] fp32,
+ * updated in place: row b uses state slots[b] (slots NULL: state b).  A row whose slot is not in [0, n_slots) has no
+ * state: its y is zero.  Two rows must not name the same slot. */
+int rnn_gated_step(const rnn_gated_desc_t* desc, const void* Wx, const int32_t* slots, int32_t n_slots, float* state,
+                   void* y, void* stream);
+
+/* Norm of each query's and key's head with the rotation by its token's position, in one pass: for x = a head [D] of q
+ * or k at position pos, w its weight,
+ *   y = x w / sqrt(mean x^2 + eps);  for j < rot/2 the pair (y1, y2) becomes
+ *   (y1 cos - y2 sin, y2 cos + y1 sin) of the angle pos freqs[j]
+ * with the pair's columns j and j + rot/2, or 2j and 2j + 1 with RNN_ROTARY_INTERLEAVED; columns from rot on are not
+ * turned.  q [T, B, NQ, D], k [T, B, NK, D] in dtype (strided views as for the attention: strides of q and k for
+ * (token, row, head), st NULL = contiguous), outputs contiguous in dtype, rounded once.  q_weight, k_weight [D] fp32; both
+ * NULL = no norm.  freqs [rot/2] fp64, finite, radians a position (NULL with rot == 0: no rotation).  positions int32:
+ * [B], where each row's first token stands, the following ones after it; [T, B] with RNN_ROTARY_PER_TOKEN; NULL = 0 for
+ * every row.  Any position: angles are formed modulo a turn in 64 bits of fraction.  Squares are summed in fp32: a
+ * head with values past 2^63 comes out as zero.
+ * D and rot even, rot <= D <= 4096, T*B at most 2^31 - 1.  Alignment: the element's.  D that is a multiple of 8 up to
+ * 256 (and, unless interleaved, rot too) with strides and addresses that are multiples of four values runs the vector
+ * kernels. */
+enum { RNN_ROTARY_INTERLEAVED = 1, RNN_ROTARY_PER_TOKEN = 2 };
+
+typedef struct {
+  int32_t dtype; /* rnn_dtype_t of q, k and what comes of them */
+  int32_t T, B, NQ, NK, D, rot;
+  float eps;
+  int32_t flags; /* RNN_ROTARY_* */
+} rnn_rotary_desc_t;
+
+typedef struct {
+  int64_t q[3], k[3], dq[3], dk[3]; /* (token, row, head), elements; dq, dk: the gradient's inputs */
+} rnn_rotary_strides_t;
+
+int rnn_head_norm_rotary(const rnn_rotary_desc_t* desc, const rnn_rotary_strides_t* st, const void* q, const void* k,
+                         const float* q_weight, const float* k_weight, const double* freqs, const int32_t* positions,
+                         void* q_out, void* k_out, void* stream);
+
+/* Its gradient from q and k as the forward took them and dq_out, dk_out (strides st->dq, st->dk), the gradients of its
+ * outputs: dq, dk contiguous in dtype, dq_weight, dk_weight [D] fp32 (both needed where the weights are given), summed in
+ * fp32 in a fixed order.  Workspace: 256-byte aligned, size below (none without weights). */
+size_t rnn_head_norm_rotary_bwd_workspace_size(const rnn_rotary_desc_t* desc);
+int rnn_head_norm_rotary_bwd(const rnn_rotary_desc_t* desc, const rnn_rotary_strides_t* st, const void* q,
+                             const void* k, const float* q_weight, const float* k_weight, const double* freqs,
+                             const int32_t* positions, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                             float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* The common norm of n tensors, sqrt(sum of all x^2), to *norm (fp32, NULL = not written), and their scaling to it: where
+ * it is finite and above max_norm every value becomes x (max_norm / norm) in place, rounded once; else nothing is written to
+ * them.  max_norm >= 0; INFINITY = the norm alone.  dtypes (rnn_dtype_t), sizes (elements; 0 is allowed) and
+ * tensors (device memory, aligned as the element is) are host arrays, read before the call returns.  Unless max_norm is
+ * INFINITY no two tensors may overlap (RNN_ERR_INVALID_ARG).  Sums are taken in fixed order, with fp64 above
+ * 64 bytes; no square overflows (a norm that fp32 cannot hold is told as infinity, and clipped to max_norm all the same).  A tensor's size is at most 2^40.  Workspace: 256-byte aligned, size below. */
+size_t rnn_clip_grad_norm_workspace_size(int32_t n);
+int rnn_clip_grad_norm(int32_t n, const int32_t* dtypes, const int64_t* sizes, void* const* tensors, float max_norm,
+                       float* norm, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

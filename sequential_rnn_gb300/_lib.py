@@ -19,7 +19,9 @@ RNN_F32, RNN_BF16 = 0, 1
 RNN_FLAG_TRAIN = 1
 RNN_FLAG_H_BF16 = 2
 RNN_FLAG_TEST_TIMEOUT = 1 << 30
+RNN_ROTARY_INTERLEAVED, RNN_ROTARY_PER_TOKEN = 1, 2
 RNN_HOST_DIRECT = -1  # rnn_fwd_host chunk: the kernel reads / writes the mapped host buffers
+GATE_COUNTS = {"fz": 2, "fzo": 3, "ifzo": 4}  # rnn_gates_t
 STATUS = {0: "RNN_OK", 1: "RNN_ERR_INVALID_ARG", 2: "RNN_ERR_UNSUPPORTED",
           3: "RNN_ERR_MISALIGNED", 4: "RNN_ERR_LAUNCH", 5: "RNN_ERR_TIMEOUT",
           6: "RNN_ERR_NO_CLUSTER", 7: "RNN_ERR_SCRATCH_LIMIT", 8: "RNN_ERR_BOUNDS"}
@@ -33,7 +35,10 @@ EXPORTS = ("rnn_workspace_size", "rnn_stash_size", "rnn_fwd", "rnn_bwd", "rnn_re
            "rnn_fwd_host_workspace_size", "rnn_fwd_host", "rnn_rms_norm",
            "rnn_rms_norm_bwd_workspace_size", "rnn_rms_norm_bwd", "rnn_quantize_weight",
            "rnn_input_proj_fp8", "rnn_linattn_workspace_size", "rnn_linattn_fwd",
-           "rnn_linattn_bwd", "rnn_linattn_step")
+           "rnn_linattn_bwd", "rnn_linattn_step", "rnn_gated_stash_size", "rnn_gated_fwd",
+           "rnn_gated_bwd", "rnn_gated_step", "rnn_head_norm_rotary",
+           "rnn_head_norm_rotary_bwd_workspace_size", "rnn_head_norm_rotary_bwd",
+           "rnn_clip_grad_norm_workspace_size", "rnn_clip_grad_norm")
 
 
 class rnn_desc_t(ctypes.Structure):
@@ -52,12 +57,28 @@ class rnn_linattn_strides_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64 * 3) for n in ("q", "k", "v", "o")]
 
 
+class rnn_gated_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "T", "B", "NH", "D", "gates")]
+
+
+class rnn_rotary_desc_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("dtype", "T", "B", "NQ", "NK", "D", "rot")]
+                + [("eps", ctypes.c_float), ("flags", ctypes.c_int32)])
+
+
+class rnn_rotary_strides_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64 * 3) for n in ("q", "k", "dq", "dk")]
+
+
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _I = ctypes.c_int
 _I32 = ctypes.c_int32
 _DESC = ctypes.POINTER(rnn_desc_t)
 _LDESC = ctypes.POINTER(rnn_linattn_desc_t)
+_GDESC = ctypes.POINTER(rnn_gated_desc_t)
+_RDESC = ctypes.POINTER(rnn_rotary_desc_t)
+_RST = ctypes.POINTER(rnn_rotary_strides_t)
 _LST = ctypes.POINTER(rnn_linattn_strides_t)
 
 _SIGS = {
@@ -85,6 +106,15 @@ _SIGS = {
     "rnn_linattn_fwd": (_I, [_LDESC, _LST] + [_P] * 9 + [_SZ, _P]),
     "rnn_linattn_bwd": (_I, [_LDESC, _LST] + [_P] * 13 + [_SZ, _P]),
     "rnn_linattn_step": (_I, [_LDESC, _LST] + [_P] * 5 + [_I32] + [_P] * 3),
+    "rnn_gated_stash_size": (_SZ, [_GDESC]),
+    "rnn_gated_fwd": (_I, [_GDESC] + [_P] * 7),
+    "rnn_gated_bwd": (_I, [_GDESC] + [_P] * 8),
+    "rnn_gated_step": (_I, [_GDESC] + [_P] * 2 + [_I32] + [_P] * 3),
+    "rnn_head_norm_rotary": (_I, [_RDESC, _RST] + [_P] * 9),
+    "rnn_head_norm_rotary_bwd_workspace_size": (_SZ, [_RDESC]),
+    "rnn_head_norm_rotary_bwd": (_I, [_RDESC, _RST] + [_P] * 13 + [_SZ, _P]),
+    "rnn_clip_grad_norm_workspace_size": (_SZ, [_I32]),
+    "rnn_clip_grad_norm": (_I, [_I32] + [_P] * 3 + [ctypes.c_float, _P, _P, _SZ, _P]),
 }
 
 _lib = None

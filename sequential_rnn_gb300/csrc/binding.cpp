@@ -39,6 +39,15 @@ struct {
   decltype(&rnn_linattn_fwd) la_fwd;
   decltype(&rnn_linattn_bwd) la_bwd;
   decltype(&rnn_linattn_step) la_step;
+  decltype(&rnn_gated_stash_size) gated_stash;
+  decltype(&rnn_gated_fwd) gated_fwd;
+  decltype(&rnn_gated_bwd) gated_bwd;
+  decltype(&rnn_gated_step) gated_step;
+  decltype(&rnn_head_norm_rotary) rotary;
+  decltype(&rnn_head_norm_rotary_bwd_workspace_size) rotary_bwd_ws;
+  decltype(&rnn_head_norm_rotary_bwd) rotary_bwd;
+  decltype(&rnn_clip_grad_norm_workspace_size) clip_ws;
+  decltype(&rnn_clip_grad_norm) clip;
 } api;
 
 constexpr int64_t kBlock = 128;  // columns (and weight rows) that share a scale
@@ -435,6 +444,268 @@ PyObject* linear_attention_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------- gated linear recurrence --
+struct Gated {
+  rnn_gated_desc_t desc;
+  at::Device dev;
+  ScalarType type;
+  int64_t T, B, NH, D;
+
+  // lead: dimensions before the heads' (2: [T, B, NH, G D], 1: [B, NH, G D])
+  Gated(const Tensor& Wx, PyObject* gates, int lead) : dev(device_of("Wx", Wx)), type(Wx.scalar_type()) {
+    const int dt = dtype_of("Wx", Wx);
+    if (!PyUnicode_Check(gates)) fail(PyExc_TypeError, "gates: expected \"fz\", \"fzo\" or \"ifzo\"");
+    desc = {};
+    if (PyUnicode_CompareWithASCIIString(gates, "fz") == 0)
+      desc.gates = RNN_GATES_FZ;
+    else if (PyUnicode_CompareWithASCIIString(gates, "fzo") == 0)
+      desc.gates = RNN_GATES_FZO;
+    else if (PyUnicode_CompareWithASCIIString(gates, "ifzo") == 0)
+      desc.gates = RNN_GATES_IFZO;
+    else
+      fail(PyExc_ValueError, "gates: expected \"fz\", \"fzo\" or \"ifzo\", got %R", gates);
+    if (Wx.dim() != lead + 2) fail(PyExc_ValueError, "Wx: expected shape %s", lead == 2 ? "[T, B, NH, G*D]" : "[B, NH, G*D]");
+    T = lead == 2 ? Wx.size(0) : 1, B = Wx.size(lead - 1), NH = Wx.size(lead), D = Wx.size(lead + 1) / desc.gates;
+    if (D == 0 || D * desc.gates != Wx.size(lead + 1))
+      fail(PyExc_ValueError, "Wx: its last dimension has to be a positive multiple of the %d gates", (int)desc.gates);
+    want("Wx", Wx, Wx.sizes(), type, dev);
+    desc.dtype = dt;
+    desc.T = count("Wx", T), desc.B = count("Wx", B), desc.NH = count("Wx", NH), desc.D = count("Wx", D);
+  }
+  Tensor states() const { return make({B, NH, D}, at::kFloat, dev); }
+  void want_state(const char* name, const Tensor* t) const { want(name, t, {B, NH, D}, at::kFloat, dev); }
+};
+
+// Wx, gates, state or None, lens or None, train
+PyObject* gated_recurrence(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity("gated_recurrence", n, 5);
+  const Tensor& Wx = tensor("Wx", a[0]);
+  const Tensor *state = optional("state", a[2]), *lens = optional("lens", a[3]);
+  const bool train = truth(a[4]);
+  const Gated g(Wx, a[1], 2);
+  g.want_state("state", state);
+  want("lens", lens, {g.B}, at::kInt, g.dev);
+  Tensor y, fin, stash;
+  int st;
+  {
+    NoGil free;
+    y = make({g.T, g.B, g.NH, g.D}, g.type, g.dev), fin = g.states();
+    if (train) stash = make({(int64_t)(api.gated_stash(&g.desc) / sizeof(float))}, at::kFloat, g.dev);
+    st = api.gated_fwd(&g.desc, Wx.data_ptr(), at_of<const int32_t>(lens), at_of<const float>(state), y.data_ptr(),
+                       at_of<float>(&fin), train ? at_of<float>(&stash) : nullptr, current_stream());
+  }
+  if (st) return status(st);
+  PyObject* out = PyDict_New();
+  put(out, "y", y);
+  put(out, "state", fin);
+  if (train) put(out, "stash", stash);
+  return out;
+  END_HANDLE_TH_ERRORS
+}
+
+// Wx, stash, dy, gates, dstate or None, lens or None
+PyObject* gated_recurrence_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity("gated_recurrence_backward", n, 6);
+  const Tensor &Wx = tensor("Wx", a[0]), &stash = tensor("stash", a[1]), &dy = tensor("dy", a[2]);
+  const Tensor *dstate = optional("dstate", a[4]), *lens = optional("lens", a[5]);
+  const Gated g(Wx, a[3], 2);
+  want("stash", stash, {(int64_t)(api.gated_stash(&g.desc) / sizeof(float))}, at::kFloat, g.dev);
+  want("dy", dy, {g.T, g.B, g.NH, g.D}, g.type, g.dev);
+  g.want_state("dstate", dstate);
+  want("lens", lens, {g.B}, at::kInt, g.dev);
+  Tensor dWx, ds;
+  int st;
+  {
+    NoGil free;
+    dWx = make(Wx.sizes(), g.type, g.dev), ds = g.states();
+    st = api.gated_bwd(&g.desc, Wx.data_ptr(), at_of<const int32_t>(lens), at_of<const float>(&stash), dy.data_ptr(),
+                       at_of<const float>(dstate), dWx.data_ptr(), at_of<float>(&ds), current_stream());
+  }
+  if (st) return status(st);
+  PyObject* out = PyDict_New();
+  put(out, "dWx", dWx);
+  put(out, "dstate", ds);
+  return out;
+  END_HANDLE_TH_ERRORS
+}
+
+// Wx, state, gates, slots or None
+PyObject* gated_recurrence_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity("gated_recurrence_step", n, 4);
+  const Tensor &Wx = tensor("Wx", a[0]), &state = tensor("state", a[1]);
+  const Tensor* slots = optional("slots", a[3]);
+  const Gated g(Wx, a[2], 1);
+  if (state.dim() != 3) fail(PyExc_ValueError, "state: expected [n_slots, NH, D]");
+  want("state", state, {state.size(0), g.NH, g.D}, at::kFloat, g.dev);
+  want("slots", slots, {g.B}, at::kInt, g.dev);
+  const int32_t n_slots = count("state", state.size(0));
+  Tensor y;
+  int st;
+  {
+    NoGil free;
+    y = make({g.B, g.NH, g.D}, g.type, g.dev);
+    st = api.gated_step(&g.desc, Wx.data_ptr(), at_of<const int32_t>(slots), n_slots, at_of<float>(&state), y.data_ptr(),
+                        current_stream());
+  }
+  return st ? status(st) : THPVariable_Wrap(y);
+  END_HANDLE_TH_ERRORS
+}
+
+// ------------------------------------------ norm and rotation of heads --
+struct Rotary {
+  rnn_rotary_desc_t desc;
+  rnn_rotary_strides_t strides;
+  at::Device dev;
+  ScalarType type;
+  const Tensor *qw, *kw, *freqs, *positions;
+  Shape sq, sk;
+
+  // a: q, k, q_weight, k_weight, freqs, positions (the last four or None); eps, interleaved
+  Rotary(PyObject* const* a, PyObject* eps, PyObject* interleaved) : dev(device_of("q", tensor("q", a[0]))) {
+    const Tensor &q = tensor("q", a[0]), &k = tensor("k", a[1]);
+    qw = optional("q_weight", a[2]), kw = optional("k_weight", a[3]), freqs = optional("freqs", a[4]);
+    positions = optional("positions", a[5]);
+    type = q.scalar_type();
+    const int dt = dtype_of("q", q);
+    const int64_t nd = q.dim();
+    if ((nd != 3 && nd != 4) || k.dim() != nd) fail(PyExc_ValueError, "expected q, k of shape [T, B, NH, D] or [B, NH, D]");
+    sq.assign(q.sizes().begin(), q.sizes().end());
+    sk = sq;
+    sk[nd - 2] = k.size(nd - 2);
+    const int64_t T = nd == 4 ? q.size(0) : 1, B = q.size(nd - 3), D = q.size(nd - 1);
+    want("k", k, sk, type, dev, false);
+    if ((qw == nullptr) != (kw == nullptr)) fail(PyExc_ValueError, "q_weight and k_weight: both or neither");
+    want("q_weight", qw, {D}, at::kFloat, dev);
+    want("k_weight", kw, {D}, at::kFloat, dev);
+    desc = {};
+    if (freqs) {
+      if (freqs->dim() != 1 || 2 * freqs->size(0) > D) fail(PyExc_ValueError, "freqs: expected at most D / 2 of them");
+      want("freqs", *freqs, freqs->sizes(), at::kDouble, dev);
+      desc.rot = 2 * (int32_t)count("freqs", freqs->size(0));
+    }
+    if (truth(interleaved)) desc.flags |= RNN_ROTARY_INTERLEAVED;
+    if (positions) {
+      const bool per_token = positions->dim() == 2;
+      if (per_token)
+        want("positions", *positions, {T, B}, at::kInt, dev);
+      else
+        want("positions", *positions, {B}, at::kInt, dev);
+      if (per_token) desc.flags |= RNN_ROTARY_PER_TOKEN;
+    }
+    desc.dtype = dt;
+    desc.T = count("q", T), desc.B = count("q", B), desc.NQ = count("q", q.size(nd - 2)), desc.NK = count("k", k.size(nd - 2));
+    desc.D = count("q", D);
+    desc.eps = (float)number(eps);
+    strides = {};
+    Attention::strides_of("q", q, strides.q);
+    Attention::strides_of("k", k, strides.k);
+  }
+};
+
+// q, k, q_weight, k_weight, freqs, positions (each of the last four or None), eps, interleaved -> (q, k)
+PyObject* head_norm_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity("head_norm_rotary", n, 8);
+  const Rotary r(a, a[6], a[7]);
+  const Tensor &q = tensor("q", a[0]), &k = tensor("k", a[1]);
+  Tensor qo, ko;
+  int st;
+  {
+    NoGil free;
+    qo = make(r.sq, r.type, r.dev), ko = make(r.sk, r.type, r.dev);
+    st = api.rotary(&r.desc, &r.strides, q.data_ptr(), k.data_ptr(), at_of<const float>(r.qw), at_of<const float>(r.kw),
+                    at_of<const double>(r.freqs), at_of<const int32_t>(r.positions), qo.data_ptr(), ko.data_ptr(),
+                    current_stream());
+  }
+  return st ? status(st) : pair(qo, ko);
+  END_HANDLE_TH_ERRORS
+}
+
+// the same, dq, dk, eps, interleaved
+PyObject* head_norm_rotary_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity("head_norm_rotary_backward", n, 10);
+  Rotary r(a, a[8], a[9]);
+  const Tensor &q = tensor("q", a[0]), &k = tensor("k", a[1]), &dqo = tensor("dq", a[6]), &dko = tensor("dk", a[7]);
+  want("dq", dqo, r.sq, r.type, r.dev, false);
+  want("dk", dko, r.sk, r.type, r.dev, false);
+  Attention::strides_of("dq", dqo, r.strides.dq);
+  Attention::strides_of("dk", dko, r.strides.dk);
+  Tensor dq, dk, dqw, dkw, ws;
+  int st;
+  {
+    NoGil free;
+    dq = make(r.sq, r.type, r.dev), dk = make(r.sk, r.type, r.dev);
+    size_t bytes = 0;
+    if (r.qw) {
+      bytes = api.rotary_bwd_ws(&r.desc);
+      dqw = make({r.desc.D}, at::kFloat, r.dev), dkw = make({r.desc.D}, at::kFloat, r.dev);
+      ws = make({(int64_t)bytes}, at::kByte, r.dev);
+    }
+    st = api.rotary_bwd(&r.desc, &r.strides, q.data_ptr(), k.data_ptr(), at_of<const float>(r.qw),
+                        at_of<const float>(r.kw), at_of<const double>(r.freqs), at_of<const int32_t>(r.positions),
+                        dqo.data_ptr(), dko.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                        r.qw ? at_of<float>(&dqw) : nullptr, r.qw ? at_of<float>(&dkw) : nullptr,
+                        r.qw ? ws.data_ptr() : nullptr, bytes, current_stream());
+  }
+  if (st) return status(st);
+  PyObject* out = PyDict_New();
+  put(out, "dq", dq);
+  put(out, "dk", dk);
+  if (r.qw) {
+    put(out, "dwq", dqw);
+    put(out, "dwk", dkw);
+  }
+  return out;
+  END_HANDLE_TH_ERRORS
+}
+
+// ------------------------------------------------------------ clipping --
+struct Ref {  // a reference held while the GIL is not
+  PyObject* o;
+  ~Ref() { Py_XDECREF(o); }
+};
+// tensors (a sequence, None among them passed over), max_norm -> norm
+PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity("clip_grad_norm", n, 2);
+  const Ref list{PySequence_Fast(a[0], "grads: expected a sequence of tensors")};
+  if (!list.o) throw python_error();
+  const float max_norm = (float)number(a[1]);
+  const Py_ssize_t items = PySequence_Fast_GET_SIZE(list.o);
+  c10::SmallVector<int32_t, 64> types;
+  c10::SmallVector<int64_t, 64> sizes;
+  c10::SmallVector<void*, 64> at;
+  c10::SmallVector<Tensor, 64> held;  // (the list may change in another thread meanwhile)
+  for (Py_ssize_t i = 0; i < items; ++i) {
+    PyObject* o = PySequence_Fast_GET_ITEM(list.o, i);
+    if (o == Py_None) continue;
+    const Tensor& t = tensor("grads", o);
+    device_of("grads", t);
+    types.push_back(dtype_of("grads", t));
+    if (!t.is_non_overlapping_and_dense()) fail(PyExc_ValueError, "grads: a tensor must be dense, without gaps or overlaps");
+    sizes.push_back(t.numel());
+    at.push_back(t.data_ptr());
+    held.push_back(t);
+  }
+  const at::Device dev(at::kCUDA, c10::cuda::current_device());
+  const int32_t count32 = count("grads", (int64_t)types.size());
+  Tensor norm, ws;
+  int st;
+  {
+    NoGil free;
+    const size_t bytes = api.clip_ws(count32);
+    norm = make({}, at::kFloat, dev), ws = make({(int64_t)bytes}, at::kByte, dev);
+    st = api.clip(count32, types.data(), sizes.data(), at.data(), max_norm, at_of<float>(&norm), ws.data_ptr(), bytes,
+                  current_stream());
+  }
+  return st ? status(st) : THPVariable_Wrap(norm);
+  END_HANDLE_TH_ERRORS
+}
+
 // the entry points' addresses, in the order of `api`
 PyObject* connect(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -452,6 +723,8 @@ PyObject* connect(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define CALL(name) {#name, (PyCFunction)(void (*)())name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CALL(rms_norm), CALL(rms_norm_backward), CALL(quantize_weight), CALL(input_proj_fp8),
                          CALL(linear_attention), CALL(linear_attention_backward), CALL(linear_attention_step),
+                         CALL(gated_recurrence), CALL(gated_recurrence_backward), CALL(gated_recurrence_step),
+                         CALL(head_norm_rotary), CALL(head_norm_rotary_backward), CALL(clip_grad_norm),
                          CALL(connect), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods};
 

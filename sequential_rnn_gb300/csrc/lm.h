@@ -1,6 +1,7 @@
 // Internal interface of the language-model operators: the root-mean-square
 // norm, the 8-bit projection and the linear attention with a decay per head
-// (entry points and argument checks in lm_capi.cu).
+// (entry points and argument checks in lm_capi.cu); the gated linear recurrence, the
+// norm and rotation of heads and the clipping of gradients (mix_capi.cu).
 #pragma once
 #include <cstddef>
 #include <cstdint>
@@ -143,5 +144,68 @@ struct LinAttnStepParams {
   float scale;
 };
 int launch_linattn_step(const LinAttnStepParams& p, bool bf16, cudaStream_t s);
+
+// ------------------------------------------- gated linear recurrence --
+constexpr int kGatedRun = 8;  // tokens that share a state of the stash
+struct GatedParams {
+  const void* wx;       // [T, B, NH, gates D]
+  const int* lens;      // [B] or null
+  const float* state0;  // [B, N] or null
+  void* y;              // [T, B, N]
+  float* stateT;        // or null
+  float* stash;         // [ceil(T / kGatedRun), B, N] states before every run of tokens (forward: or null)
+  const void* dy;       // gradient alone: [T, B, N]
+  const float* dstateT; // or null
+  void* dwx;
+  float* dstate0;       // or null
+  int T, B, N, D;       // N = NH D
+  int tiles, cs;        // (launch) channel tiles of a row, CTAs of a cluster along time
+};
+int launch_gated(GatedParams p, int gates, bool bf16, bool bwd, cudaStream_t s);
+struct GatedStepParams {
+  const void* wx;    // [B, NH, gates D]
+  const int* slots;  // [B] or null
+  float* state;      // [nslots, N]
+  void* y;           // [B, N]
+  int B, N, D, nslots;
+};
+int launch_gated_step(const GatedStepParams& p, int gates, bool bf16, cudaStream_t s);
+
+// ------------------------------------------ norm and rotation of heads --
+constexpr int kRotaryParts = 608;  // partial sums of the weights' gradients: 4 x 152 SMs
+struct RotaryParams {
+  const void* q;
+  const void* k;
+  const float* qw;       // [D]; null (both): no norm
+  const float* kw;
+  const double* freqs;   // [rot / 2]
+  const int* positions;  // [B] (of the first token) or, per_token, [T, B]; null: 0
+  void* qo;              // [T, B, NQ, D] (gradient: of q)
+  void* ko;
+  const void* dq;        // gradient alone: of the outputs
+  const void* dk;
+  float* dqw;
+  float* dkw;
+  float* part;           // [kRotaryParts, 2, D]
+  long long qs[3], ks[3], dqs[3], dks[3];  // strides in elements: token, row, head
+  int T, B, NQ, NK, D, rot, interleaved, per_token, split;
+  float eps;
+};
+int launch_rotary(RotaryParams p, bool bf16, bool bwd, cudaStream_t s);
+
+// ------------------------------------------------------------ clipping --
+constexpr int kClipTensors = 256;  // of a launch: their table is a kernel parameter
+constexpr int kClipUnit = 16384;   // bytes
+struct ClipParams {
+  void* const* at;
+  const int64_t* sizes;
+  const int32_t* dtypes;  // 1: bf16
+  int n;
+  float limit;   // infinite: the norm alone
+  float* norm;   // or null
+  double* part;  // clip_parts(n) partial sums
+};
+int clip_parts(int n);
+int launch_clip(const ClipParams& p, cudaStream_t s);
 
 }  // namespace srnn

@@ -8,6 +8,14 @@
 ``linear_attention`` (``_backward``, ``_step``)
                                        matrix-memory recurrence with a decay for
                                        each head: prompts, gradient, single tokens
+``gated_recurrence`` (``_backward``, ``_step``)
+                                       the cells without a recurrent matrix: a scan over
+                                       the sequence, its gradient, single tokens
+``head_norm_rotary`` / ``head_norm_rotary_backward``, ``rotary_frequencies``
+                                       norm of each query's and key's head and the
+                                       rotation by its position, in front of the attention
+``grad_norm`` / ``clip_grad_norm``     the common norm of all gradients, and their
+                                       scaling to a limit
 
 As in the package's top level, the functions named like the C entry points only
 marshal arguments, and the others check them, allocate the outputs (both in
@@ -28,12 +36,19 @@ __all__ = ["rnn_rms_norm", "rnn_rms_norm_bwd_workspace_size", "rnn_rms_norm_bwd"
            "rnn_quantize_weight", "rnn_input_proj_fp8", "rnn_linattn_workspace_size",
            "rnn_linattn_fwd", "rnn_linattn_bwd", "rnn_linattn_step", "rms_norm",
            "rms_norm_backward", "quantize_weight", "input_proj_fp8", "linear_attention",
-           "linear_attention_backward", "linear_attention_step"]
+           "linear_attention_backward", "linear_attention_step",
+           "rnn_gated_stash_size", "rnn_gated_fwd", "rnn_gated_bwd", "rnn_gated_step",
+           "rnn_head_norm_rotary", "rnn_head_norm_rotary_bwd_workspace_size", "rnn_head_norm_rotary_bwd",
+           "rnn_clip_grad_norm_workspace_size", "rnn_clip_grad_norm", "gated_recurrence",
+           "gated_recurrence_backward", "gated_recurrence_step", "rotary_frequencies", "head_norm_rotary",
+           "head_norm_rotary_backward", "grad_norm", "clip_grad_norm"]
 
 _native = None  # the compiled calls (csrc/binding.cpp), loaded with the library
 _ENTRIES = ("rnn_rms_norm", "rnn_rms_norm_bwd_workspace_size", "rnn_rms_norm_bwd", "rnn_quantize_weight",
             "rnn_input_proj_fp8", "rnn_linattn_workspace_size", "rnn_linattn_fwd", "rnn_linattn_bwd",
-            "rnn_linattn_step")
+            "rnn_linattn_step", "rnn_gated_stash_size", "rnn_gated_fwd", "rnn_gated_bwd", "rnn_gated_step",
+            "rnn_head_norm_rotary", "rnn_head_norm_rotary_bwd_workspace_size", "rnn_head_norm_rotary_bwd",
+            "rnn_clip_grad_norm_workspace_size", "rnn_clip_grad_norm")
 
 
 def _load():
@@ -137,6 +152,57 @@ def rnn_linattn_step(desc, strides, q, k, v, log_decay, slots, n_slots, state, o
     return _lib.load().rnn_linattn_step(ctypes.byref(desc), _sref(strides), _at(q), _at(k), _at(v),
                                         _at(log_decay), _at(slots), n_slots, _at(state), _at(o),
                                         _handle(stream))
+
+
+def rnn_gated_stash_size(desc) -> int:
+    return int(_lib.load().rnn_gated_stash_size(ctypes.byref(desc)))
+
+
+def rnn_gated_fwd(desc, Wx, lens, state0, y, stateT, stash, stream=None) -> int:
+    return _lib.load().rnn_gated_fwd(ctypes.byref(desc), _at(Wx), _at(lens), _at(state0), _at(y),
+                                     _at(stateT), _at(stash), _handle(stream))
+
+
+def rnn_gated_bwd(desc, Wx, lens, stash, dy, dstateT, dWx, dstate0, stream=None) -> int:
+    return _lib.load().rnn_gated_bwd(ctypes.byref(desc), _at(Wx), _at(lens), _at(stash), _at(dy),
+                                     _at(dstateT), _at(dWx), _at(dstate0), _handle(stream))
+
+
+def rnn_gated_step(desc, Wx, slots, n_slots, state, y, stream=None) -> int:
+    return _lib.load().rnn_gated_step(ctypes.byref(desc), _at(Wx), _at(slots), n_slots, _at(state),
+                                      _at(y), _handle(stream))
+
+
+def rnn_head_norm_rotary(desc, strides, q, k, q_weight, k_weight, freqs, positions, q_out, k_out,
+                         stream=None) -> int:
+    return _lib.load().rnn_head_norm_rotary(ctypes.byref(desc), _sref(strides), _at(q), _at(k),
+                                            _at(q_weight), _at(k_weight), _at(freqs), _at(positions),
+                                            _at(q_out), _at(k_out), _handle(stream))
+
+
+def rnn_head_norm_rotary_bwd_workspace_size(desc) -> int:
+    return int(_lib.load().rnn_head_norm_rotary_bwd_workspace_size(ctypes.byref(desc)))
+
+
+def rnn_head_norm_rotary_bwd(desc, strides, q, k, q_weight, k_weight, freqs, positions, dq_out, dk_out,
+                             dq, dk, dq_weight, dk_weight, workspace, stream=None) -> int:
+    return _lib.load().rnn_head_norm_rotary_bwd(
+        ctypes.byref(desc), _sref(strides), _at(q), _at(k), _at(q_weight), _at(k_weight), _at(freqs),
+        _at(positions), _at(dq_out), _at(dk_out), _at(dq), _at(dk), _at(dq_weight), _at(dk_weight),
+        _at(workspace), workspace.nbytes if workspace is not None else 0, _handle(stream))
+
+
+def rnn_clip_grad_norm_workspace_size(n) -> int:
+    return int(_lib.load().rnn_clip_grad_norm_workspace_size(n))
+
+
+def rnn_clip_grad_norm(tensors, max_norm, norm, workspace, stream=None) -> int:
+    n = len(tensors)
+    dtypes = (ctypes.c_int32 * n)(*[_lib.RNN_BF16 if t.dtype == torch.bfloat16 else _lib.RNN_F32 for t in tensors])
+    sizes = (ctypes.c_int64 * n)(*[t.numel() for t in tensors])
+    at = (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors])
+    return _lib.load().rnn_clip_grad_norm(n, dtypes, sizes, at, max_norm, _at(norm), _at(workspace),
+                                          workspace.nbytes if workspace is not None else 0, _handle(stream))
 
 
 # ------------------------------------------------------------------ norm --
@@ -251,3 +317,116 @@ def linear_attention_step(q, k, v, log_decay, state, *, slots=None, scale=None, 
     if type(out) is int:
         _raise(out, "rnn_linattn_step")
     return out
+
+
+# ---------------------------------------------- gated linear recurrence --
+def gated_recurrence(Wx, *, gates="fz", state=None, lens=None, train=False, stream=None):
+    """The cells without a recurrent matrix through rnn_gated_fwd, a scan over the sequence:
+
+        "fz"    c_t = sigm(f) c_{t-1} + sigm(-f) z     y_t = c_t
+        "fzo"   the same                               y_t = sigm(o) c_t
+        "ifzo"  c_t = sigm(f) c_{t-1} + sigm(i) z      y_t = sigm(o) c_t
+
+    Wx [T, B, NH, G*D] bf16 or fp32, gate-major in the order of ``gates`` (as ``forward``'s,
+    contiguous), state [B, NH, D] fp32 or None, lens [B] int32 or None (tokens of each row that
+    count).  Returns ``y`` [T, B, NH, D], ``state`` (after the last token) and with ``train`` the
+    ``stash`` that ``gated_recurrence_backward`` takes.
+    """
+    if stream is not None:
+        with _on(stream):
+            return gated_recurrence(Wx, gates=gates, state=state, lens=lens, train=train)
+    out = (_native or _load()).gated_recurrence(Wx, gates, state, lens, train)
+    if type(out) is int:
+        _raise(out, "rnn_gated_fwd")
+    return out
+
+
+def gated_recurrence_backward(Wx, stash, dy, *, gates="fz", dstate=None, lens=None, stream=None):
+    """Gradients of ``gated_recurrence`` from its Wx, gates, lens and ``stash``, dy [T, B, NH, D] and
+    ``dstate`` (of the final state, or None): ``dWx`` and ``dstate`` (of the initial state)."""
+    if stream is not None:
+        with _on(stream):
+            return gated_recurrence_backward(Wx, stash, dy, gates=gates, dstate=dstate, lens=lens)
+    out = (_native or _load()).gated_recurrence_backward(Wx, stash, dy, gates, dstate, lens)
+    if type(out) is int:
+        _raise(out, "rnn_gated_bwd")
+    return out
+
+
+def gated_recurrence_step(Wx, state, *, gates="fz", slots=None, stream=None):
+    """One token for each row: Wx [B, NH, G*D] against the cache ``state`` [n_slots, NH, D] fp32,
+    updated in place; row b uses state slots[b] (int32; None: state b).  A slot outside the
+    cache gives zeros; no two rows may name the same one.  Returns y [B, NH, D]."""
+    if stream is not None:
+        with _on(stream):
+            return gated_recurrence_step(Wx, state, gates=gates, slots=slots)
+    out = (_native or _load()).gated_recurrence_step(Wx, state, gates, slots)
+    if type(out) is int:
+        _raise(out, "rnn_gated_step")
+    return out
+
+
+# --------------------------------------------- norm and rotation of heads --
+def rotary_frequencies(dims, base=10000.0, device="cuda"):
+    """base^(-2j/dims) for j < dims/2 (fp64): the usual ``freqs`` of ``head_norm_rotary``, which turn the
+    first ``dims`` columns of a head."""
+    if dims < 0 or dims % 2:
+        raise ValueError("dims: expected an even number")
+    j = torch.arange(dims // 2, dtype=torch.float64)
+    return (float(base) ** (-2.0 * j / max(dims, 1))).to(device)
+
+
+def head_norm_rotary(q, k, q_weight, k_weight, freqs, positions=None, *, eps=1e-6, interleaved=False,
+                     stream=None):
+    """Norm of each head of q [T, B, NQ, D] and k [T, B, NK, D] (or [B, NQ, D], [B, NK, D]: one token a
+    row) over its D values, then the rotation of its first 2 len(freqs) columns by the angle
+    position * freqs[j], in one pass; the arguments are ``linear_attention``'s strided views.
+
+    q_weight, k_weight [D] fp32, both None: no norm.  freqs [<= D/2] fp64 (``rotary_frequencies``), None: no
+    rotation.  positions int32: [B] where each row's first token stands (the others follow), or [T, B];
+    None: 0.  The pairs are columns j and j + len(freqs), ``interleaved``: 2j and 2j + 1.  Returns (q, k),
+    contiguous.
+    """
+    if stream is not None:
+        with _on(stream):
+            return head_norm_rotary(q, k, q_weight, k_weight, freqs, positions, eps=eps, interleaved=interleaved)
+    out = (_native or _load()).head_norm_rotary(q, k, q_weight, k_weight, freqs, positions, eps, interleaved)
+    if type(out) is int:
+        _raise(out, "rnn_head_norm_rotary")
+    return out
+
+
+def head_norm_rotary_backward(q, k, q_weight, k_weight, freqs, positions, dq, dk, *, eps=1e-6,
+                              interleaved=False, stream=None):
+    """Gradient of ``head_norm_rotary`` from its inputs and dq, dk (of its outputs; may be strided as q and k
+    may): ``dq``, ``dk`` and, with weights, ``dwq``, ``dwk`` [D] fp32."""
+    if stream is not None:
+        with _on(stream):
+            return head_norm_rotary_backward(q, k, q_weight, k_weight, freqs, positions, dq, dk, eps=eps,
+                                             interleaved=interleaved)
+    out = (_native or _load()).head_norm_rotary_backward(q, k, q_weight, k_weight, freqs, positions, dq, dk, eps,
+                                                         interleaved)
+    if type(out) is int:
+        _raise(out, "rnn_head_norm_rotary_bwd")
+    return out
+
+
+# --------------------------------------------------------------- clipping --
+def clip_grad_norm(grads, max_norm, *, stream=None):
+    """Scales the tensors ``grads`` (bf16 or fp32, dense; None among them is passed over) in place to a common
+    norm of at most ``max_norm``: each value times max_norm / norm where the norm is above it and finite,
+    untouched otherwise.  Returns the norm before, a tensor of no dimensions (fp32) on the device; nothing
+    waits for it."""
+    if stream is not None:
+        with _on(stream):
+            return clip_grad_norm(grads, max_norm)
+    out = (_native or _load()).clip_grad_norm(grads, max_norm)
+    if type(out) is int:
+        _raise(out, "rnn_clip_grad_norm")
+    return out
+
+
+def grad_norm(grads, *, stream=None):
+    """The common norm of the tensors ``grads``, sqrt(sum of all x^2), as ``clip_grad_norm`` takes and
+    returns it; they are left as they are."""
+    return clip_grad_norm(grads, float("inf"), stream=stream)
