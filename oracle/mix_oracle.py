@@ -25,13 +25,16 @@ def _split(Wx, gates):
     return {n: x[..., i, :] for i, n in enumerate(gates)}
 
 
-def gated(Wx, gates, state=None, lens=None):
+def gated(Wx, gates, state=None, lens=None, fast=False):
     """Wx [T,B,NH,G*D] -> dict of y, state (the last), c [T+1,B,NH,D] (all states) and the bounds y_err, state_err,
     c_err of fp32 arithmetic.
 
     A step c = a c + u: a's error is at most 8 E of sigm(-f) (exponential, quotient) and E of itself, u's 10 E; the step's
-    sum is rounded once and the products of a that carry a state over several tokens once and a half a token."""
+    sum is rounded once and the products of a that carry a state over several tokens once and a half a token.
+    fast (bf16 gates): e^-|x| as 2^t with t = |x| log2 e rounded to fp32, off by at most 2 |x| E more (the product's
+    rounding, 2^-24 of t, and the constant's, 2^-25, both times log 2)."""
     p = _split(Wx, gates)
+    more = {n: 2 * np.abs(p[n]) if fast and n != "z" else 0.0 * p[n] for n in p}
     T, B, NH, D = p["f"].shape
     (a, low), z = _sigmoids(p["f"]), p["z"]
     gain = _sigmoids(p["i"])[0] if "i" in p else low
@@ -44,19 +47,22 @@ def gated(Wx, gates, state=None, lens=None):
     for t in range(T):
         u = gain[t] * z[t]
         c[t + 1] = np.where(live[t], a[t] * c[t] + u, c[t])
-        new = a[t] * err[t] + E * (4 + 8 * low[t]) * a[t] * m + 10 * E * np.abs(u)
+        k = 10 + more["i" if "i" in p else "f"][t]
+        new = a[t] * err[t] + E * (4 + (8 + more["f"][t]) * low[t]) * a[t] * m + k * E * np.abs(u)
         err[t + 1] = np.where(live[t], new, err[t])
         m = np.where(live[t], a[t] * m + np.abs(u), m)
     y = np.where(live, o * c[1:], 0.0)
     return {"y": y, "state": c[T], "c": c, "state_err": err[T], "c_err": err,
-            "y_err": np.where(live, o * err[1:] + (12 * E if "o" in p else 0.0) * np.abs(y), 0.0)}
+            "y_err": np.where(live, o * err[1:] + ((12 + more["o"]) * E if "o" in p else 0.0) * np.abs(y), 0.0)}
 
 
-def gated_backward(Wx, gates, dy, state=None, dstate=None, lens=None):
+def gated_backward(Wx, gates, dy, state=None, dstate=None, lens=None, fast=False):
     """dWx and the initial state's gradient of sum(y dy) + sum(state dstate), with their bounds."""
     p = _split(Wx, gates)
     T, B, NH, D = p["f"].shape
-    f = gated(Wx, gates, state, lens)
+    f = gated(Wx, gates, state, lens, fast)
+    more = {n: 2 * np.abs(p[n]) if fast and n != "z" else 0.0 * p[n] for n in p}
+    mo, mg = more.get("o", np.zeros_like(p["f"])), more["i" if "i" in p else "f"]
     c, ec = f["c"], f["c_err"]
     (a, low), z = _sigmoids(p["f"]), p["z"]
     gain, gainc = _sigmoids(p["i"]) if "i" in p else (low, a)
@@ -69,24 +75,24 @@ def gated_backward(Wx, gates, dy, state=None, dstate=None, lens=None):
     ge = {n: np.zeros_like(a) for n in gates}
     for t in reversed(range(T)):
         e = dy[t] * o[t]
-        dc, edc = d + e, err + 12 * E * np.abs(e) + E * m
+        dc, edc = d + e, err + (12 + mo[t]) * E * np.abs(e) + E * m
         mc = m + np.abs(e)
         g["z"][t] = dc * gain[t]
-        ge["z"][t] = (edc + 12 * E * np.abs(dc)) * gain[t]
+        ge["z"][t] = (edc + (12 + mg[t]) * E * np.abs(dc)) * gain[t]
         x = c[t] if "i" in p else c[t] - z[t]
         ex = ec[t] + E * (np.abs(c[t]) + np.abs(z[t]))
         s = a[t] * low[t]
         g["f"][t] = dc * x * s
-        ge["f"][t] = s * (edc * np.abs(x) + np.abs(dc) * ex + 24 * E * np.abs(dc * x))
+        ge["f"][t] = s * (edc * np.abs(x) + np.abs(dc) * ex + (24 + 2 * more["f"][t]) * E * np.abs(dc * x))
         if "i" in p:
             g["i"][t] = dc * z[t] * gain[t] * gainc[t]
-            ge["i"][t] = gain[t] * gainc[t] * np.abs(z[t]) * (edc + 24 * E * np.abs(dc))
+            ge["i"][t] = gain[t] * gainc[t] * np.abs(z[t]) * (edc + (24 + 2 * more["i"][t]) * E * np.abs(dc))
         if "o" in p:
             # (the state after the token, formed once more from the one before it)
             g["o"][t] = dy[t] * c[t + 1] * o[t] * oc[t]
-            ge["o"][t] = o[t] * oc[t] * np.abs(dy[t]) * (ec[t + 1] + 24 * E * np.abs(c[t + 1]))
+            ge["o"][t] = o[t] * oc[t] * np.abs(dy[t]) * (ec[t + 1] + (24 + 2 * mo[t]) * E * np.abs(c[t + 1]))
         d = np.where(live[t], a[t] * dc, d)
-        err = np.where(live[t], a[t] * edc + E * (4 + 8 * low[t]) * a[t] * mc, err)
+        err = np.where(live[t], a[t] * edc + E * (4 + (8 + more["f"][t]) * low[t]) * a[t] * mc, err)
         m = np.where(live[t], a[t] * mc, m)
     stack = lambda q: np.where(live, np.stack([q[n] for n in gates], -2).reshape(T, B, NH, len(gates) * D), 0.0)  # noqa: E731
     return {"dWx": stack(g), "dWx_err": stack(ge), "dstate": d, "dstate_err": err}

@@ -30,87 +30,175 @@ constexpr int kWarps = 8;         // runs of a CTA side by side
 constexpr int kChunk = kS * kWarps;
 constexpr int kMaxCluster = 16;
 
+// V fp32 numbers; a pair is added and multiplied by one instruction
+template <int V>
+struct Num;
+template <>
+struct Num<1> {
+  float x;
+  __device__ Num() {}
+  __device__ explicit Num(float a) : x(a) {}
+  __device__ float get(int) const { return x; }
+  __device__ void set(int, float a) { x = a; }
+};
+template <>
+struct Num<2> {
+  float2 x;
+  __device__ Num() {}
+  __device__ explicit Num(float a) : x(make_float2(a, a)) {}
+  __device__ float get(int i) const { return i ? x.y : x.x; }
+  __device__ void set(int i, float a) { (i ? x.y : x.x) = a; }
+};
+__device__ __forceinline__ uint64_t bits(const Num<2>& a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x.x), "f"(a.x.y));
+  return r;
+}
+__device__ __forceinline__ Num<2> of_bits(uint64_t r) {
+  Num<2> a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x.x), "=f"(a.x.y) : "l"(r));
+  return a;
+}
+__device__ __forceinline__ Num<1> fma(const Num<1>& a, const Num<1>& b, const Num<1>& c) { return Num<1>(fmaf(a.x, b.x, c.x)); }
+__device__ __forceinline__ Num<1> operator*(const Num<1>& a, const Num<1>& b) { return Num<1>(a.x * b.x); }
+__device__ __forceinline__ Num<1> operator+(const Num<1>& a, const Num<1>& b) { return Num<1>(a.x + b.x); }
+__device__ __forceinline__ Num<2> fma(const Num<2>& a, const Num<2>& b, const Num<2>& c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return of_bits(r);
+}
+__device__ __forceinline__ Num<2> operator*(const Num<2>& a, const Num<2>& b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return of_bits(r);
+}
+__device__ __forceinline__ Num<2> operator+(const Num<2>& a, const Num<2>& b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return of_bits(r);
+}
+template <int V>
+__device__ __forceinline__ Num<V> minus(const Num<V>& a, const Num<V>& b) { return fma(b, Num<V>(-1.f), a); }
+
+template <class T>
+__device__ __forceinline__ float exp_of(float x);  // x <= 0
+template <>
+__device__ __forceinline__ float exp_of<float>(float x) { return expf(x); }
+// for bf16 gates: the product's rounding leaves a relative error of |x| 2^-24
+template <>
+__device__ __forceinline__ float exp_of<__nv_bfloat16>(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// s = sigmoid(x), c = sigmoid(-x): the smaller one from e^-|x|, the larger one as 1 less it, so that both are good to
+// a few units of their own last place (a memory of n tokens needs 1 - a to better than 1 / n); sl = s c
+template <class T, int V>
+__device__ __forceinline__ void sigmoids(const Num<V>& x, Num<V>& s, Num<V>& c, Num<V>* slope = nullptr) {
+  Num<V> e, r;
+#pragma unroll
+  for (int v = 0; v < V; ++v) e.set(v, exp_of<T>(-fabsf(x.get(v))));
+  const Num<V> d = e + Num<V>(1.f);
+#pragma unroll
+  for (int v = 0; v < V; ++v) r.set(v, reciprocal(d.get(v)));
+  const Num<V> low = e * r, high = minus(Num<V>(1.f), low);
+  if (slope) *slope = low * high;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const bool up = x.get(v) > 0.f;
+    s.set(v, up ? high.get(v) : low.get(v));
+    c.set(v, up ? low.get(v) : high.get(v));
+  }
+}
+template <class T, int V>
+__device__ __forceinline__ Num<V> sigmoid(const Num<V>& x) {
+  Num<V> s, c;
+  sigmoids<T>(x, s, c);
+  return s;
+}
+
 // V neighbouring channels of one token
 template <class T, int V>
 struct Raw;
 template <>
 struct Raw<__nv_bfloat16, 2> {
   uint32_t v;
-  __device__ void load(const void* p) { v = *static_cast<const uint32_t*>(p); }
+  __device__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint32_t*>(p); }
   __device__ void zero() { v = 0u; }
-  __device__ float get(int i) const { return i ? bf16_hi(v) : bf16_lo(v); }
-  static __device__ void store(void* p, const float (&x)[2]) { *static_cast<uint32_t*>(p) = pack_bf16x2(x[0], x[1]); }
+  __device__ Num<2> get() const {
+    Num<2> r;
+    r.x = make_float2(bf16_lo(v), bf16_hi(v));
+    return r;
+  }
+  static __device__ void store(__nv_bfloat16* p, const Num<2>& a) { *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(a.x.x, a.x.y); }
 };
 template <>
 struct Raw<__nv_bfloat16, 1> {
   uint16_t v;
-  __device__ void load(const void* p) { v = *static_cast<const uint16_t*>(p); }
+  __device__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint16_t*>(p); }
   __device__ void zero() { v = 0; }
-  __device__ float get(int) const { return bf16_to_f32(v); }
-  static __device__ void store(void* p, const float (&x)[1]) {
-    *static_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(x[0]);
-  }
+  __device__ Num<1> get() const { return Num<1>(bf16_to_f32(v)); }
+  static __device__ void store(__nv_bfloat16* p, const Num<1>& a) { *p = __float2bfloat16_rn(a.x); }
 };
 template <>
 struct Raw<float, 2> {
   float2 v;
-  __device__ void load(const void* p) { v = *static_cast<const float2*>(p); }
+  __device__ void load(const float* p) { v = *reinterpret_cast<const float2*>(p); }
   __device__ void zero() { v = make_float2(0.f, 0.f); }
-  __device__ float get(int i) const { return i ? v.y : v.x; }
-  static __device__ void store(void* p, const float (&x)[2]) { *static_cast<float2*>(p) = make_float2(x[0], x[1]); }
+  __device__ Num<2> get() const {
+    Num<2> r;
+    r.x = v;
+    return r;
+  }
+  static __device__ void store(float* p, const Num<2>& a) { *reinterpret_cast<float2*>(p) = a.x; }
 };
 template <>
 struct Raw<float, 1> {
   float v;
-  __device__ void load(const void* p) { v = *static_cast<const float*>(p); }
+  __device__ void load(const float* p) { v = *p; }
   __device__ void zero() { v = 0.f; }
-  __device__ float get(int) const { return v; }
-  static __device__ void store(void* p, const float (&x)[1]) { *static_cast<float*>(p) = x[0]; }
+  __device__ Num<1> get() const { return Num<1>(v); }
+  static __device__ void store(float* p, const Num<1>& a) { *p = a.x; }
 };
 
-// s = sigmoid(x) and c = sigmoid(-x): the smaller one from e^-|x|, the larger one as 1 less it, so that both are good to
-// a few units of their own last place (a memory of n tokens needs 1 - a to better than 1 / n)
-__device__ __forceinline__ void sigmoids(float x, float& s, float& c) {
-  const float e = expf(-fabsf(x));
-  const float low = __fdividef(e, 1.f + e), high = 1.f - low;
-  const bool up = x > 0.f;
-  s = up ? high : low;
-  c = up ? low : high;
-}
-__device__ __forceinline__ float sigmoid1(float x) {
-  float s, c;
-  sigmoids(x, s, c);
-  return s;
-}
-
-template <int V>
-struct Map {  // c -> a c + u
-  float a[V], u[V];
+// c -> a c + u of one channel
+struct Map {
+  float a, u;
 };
 template <int V>
 struct Shared {
-  Map<V> part[2][kWarps][32];
-  Map<V> all[2][kMaxCluster][32];
+  alignas(16) Map part[kWarps][32 * V];
+  alignas(16) Map all[2][kMaxCluster][32 * V];
+  alignas(16) float start[kWarps][32 * V];
 };
 
 // what a thread works on
 template <class T, int G, int V>
 struct Where {
-  int b, t0, rank, warp, lane, len, steps;
+  int b, rank, warp, lane, len, steps, first;  // first: its run's first token of the first round
   bool on;
   long long wx, wstep, ch, ystep;  // elements: token 0's first gate, tokens apart; the channel in [B, N], tokens apart
+  long long at;                    // [B, N]: the channel whose state this thread carries from round to round, or -1
 
   __device__ explicit Where(const GatedParams& p) {
     rank = (int)(blockIdx.x % p.cs);
     const unsigned id = blockIdx.x / p.cs;
     b = (int)(id / p.tiles);
     warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int c = (int)(id % p.tiles * 32 + lane) * V;
-    on = c < p.N;
+    const int c0 = (int)(id % p.tiles) * 32 * V, mine = c0 + lane * V, own = c0 + (int)threadIdx.x;
+    on = mine < p.N;
+    const int c = on ? mine : p.N - V;  // (a thread past the last channel reads another one's values and writes none)
     wstep = (long long)p.B * p.N * G, ystep = (long long)p.B * p.N;
     wx = ((long long)b * p.N + c / p.D * p.D) * G + c % p.D;
     ch = (long long)b * p.N + c;
+    at = threadIdx.x < 32 * V && own < p.N ? (long long)b * p.N + own : -1;
     steps = p.cs * kChunk;
+    first = rank * kChunk + warp * kS;
   }
   // (after what writes the lengths)
   __device__ void lengths(const GatedParams& p) {
@@ -123,128 +211,141 @@ struct Where {
   __device__ int rounds() const { return (int)((len + (long long)steps - 1) / steps); }
 };
 
-// Composes the maps of a CTA's warps, then those of the cluster's CTAs, in the order of time (REV: against it).  h: the
-// state the round begins with, replaced by the one it ends with; returns the state before this warp's run.
+// The state before this warp's run from the runs' maps m: the CTA's threads of one channel each compose the maps of its
+// warps, then those of the cluster's CTAs, in the order of time (REV: against it).  h: the state of thread's own channel
+// (Where::at), at the round's beginning; replaced by that at its end.
 template <int V, bool REV>
-__device__ __forceinline__ void carry(Shared<V>& sh, int buf, const Map<V>& mine, int warp, int lane, int rank, int cs,
-                                      float (&h)[V], float (&start)[V]) {
-  sh.part[buf][warp][lane] = mine;
+__device__ __forceinline__ Num<V> carry(Shared<V>& sh, int buf, const Num<V>& ma, const Num<V>& mu, int warp, int lane,
+                                        int rank, int cs, float& h) {
+  Map m[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) m[v].a = ma.get(v), m[v].u = mu.get(v);
+  if constexpr (V == 2)
+    *reinterpret_cast<float4*>(&sh.part[warp][2 * lane]) = make_float4(m[0].a, m[0].u, m[1].a, m[1].u);
+  else
+    sh.part[warp][lane] = m[0];
   __syncthreads();
-  Map<V> before, total;
+  const int c = threadIdx.x;
+  const bool fold = c < 32 * V;
+  float in = h;
+  if (cs > 1) {
+    if (fold) {
+      Map t{1.f, 0.f};
 #pragma unroll
-  for (int v = 0; v < V; ++v) total.a[v] = 1.f, total.u[v] = 0.f;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    const int w = REV ? kWarps - 1 - i : i;
-    if (w == warp) before = total;
-    const Map<V> m = sh.part[buf][w][lane];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      total.u[v] = fmaf(m.a[v], total.u[v], m.u[v]);
-      total.a[v] *= m.a[v];
-    }
-  }
-  float in[V];
-  if (cs == 1) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      in[v] = h[v];
-      h[v] = fmaf(total.a[v], h[v], total.u[v]);
-    }
-  } else {
-    // warp w hands the CTA's map to the CTAs w, w + 8; the buffer's last readers were done before the round between
-    const uint32_t at = smem_u32(&sh.all[buf][rank][lane]);
-    for (int r = warp; r < cs; r += kWarps) {
-      const uint32_t to = mapa(at, (uint32_t)r);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * v), "f"(total.a[v]) : "memory");
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * (V + v)), "f"(total.u[v]) : "memory");
+      for (int i = 0; i < kWarps; ++i) {
+        const Map x = sh.part[REV ? kWarps - 1 - i : i][c];
+        t.u = fmaf(x.a, t.u, x.u);
+        t.a *= x.a;
       }
+      const uint32_t to = smem_u32(&sh.all[buf][rank][c]);
+      for (int r = 0; r < cs; ++r)
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa(to, (uint32_t)r)), "f"(t.a), "f"(t.u) : "memory");
     }
+    // (the buffer's readers of two rounds ago were done before the round between)
+    __syncwarp();
     cluster_sync();
-    for (int i = 0; i < cs; ++i) {
-      const int r = REV ? cs - 1 - i : i;
-      const Map<V> m = sh.all[buf][r][lane];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (r == rank) in[v] = h[v];
-        h[v] = fmaf(m.a[v], h[v], m.u[v]);
+    if (fold)
+      for (int i = 0; i < cs; ++i) {
+        const int r = REV ? cs - 1 - i : i;
+        const Map x = sh.all[buf][r][c];
+        if (r == rank) in = h;
+        h = fmaf(x.a, h, x.u);
       }
-    }
   }
+  if (fold) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) start[v] = fmaf(before.a[v], in[v], before.u[v]);
+    for (int i = 0; i < kWarps; ++i) {
+      const int w = REV ? kWarps - 1 - i : i;
+      const Map x = sh.part[w][c];
+      sh.start[w][c] = in;
+      in = fmaf(x.a, in, x.u);
+    }
+    if (cs == 1) h = in;
+  }
+  __syncthreads();
+  Num<V> s;
+  if constexpr (V == 2)
+    s.x = *reinterpret_cast<const float2*>(&sh.start[warp][2 * lane]);
+  else
+    s.x = sh.start[warp][lane];
+  return s;
 }
 
 template <class T, int G, int V>
+struct Run {  // a run's raw values
+  Raw<T, V> x[G][kS];
+  // n: tokens of it that count
+  __device__ __forceinline__ void load(const T* wx, long long wstep, int D, int n) {
+    if (n >= kS) {
+#pragma unroll
+      for (int s = 0; s < kS; ++s)
+#pragma unroll
+        for (int g = 0; g < G; ++g) x[g][s].load(wx + s * wstep + (long long)g * D);
+    } else {
+#pragma unroll
+      for (int s = 0; s < kS; ++s)
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          x[g][s].zero();
+          if (s < n) x[g][s].load(wx + s * wstep + (long long)g * D);
+        }
+    }
+  }
+};
+
+template <class T, int G, int V>
 __global__ void __launch_bounds__(32 * kWarps) gated_fwd_kernel(const GatedParams p) {
-  constexpr int F = G == 4 ? 1 : 0, Z = F + 1, O = F + 2;  // the gates' places
+  constexpr int F = G == 4 ? 1 : 0, Z = F + 1, O = G == 2 ? 0 : F + 2;  // the gates' places
   __shared__ Shared<V> sh;
   depend_launch();
   Where<T, G, V> w(p);
-  const T* wx = static_cast<const T*>(p.wx) + w.wx;
-  T* y = static_cast<T*>(p.y) + w.ch;
+  const T* wx = static_cast<const T*>(p.wx) + w.wx + w.first * w.wstep;
+  T* y = static_cast<T*>(p.y) + w.ch + w.first * w.ystep;
   depend_wait();
   w.lengths(p);
-  float h[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = p.state0 && w.on ? p.state0[w.ch + v] : 0.f;
+  float h = p.state0 && w.at >= 0 ? p.state0[w.at] : 0.f;
   const int rounds = w.rounds();
   if (p.cs > 1) cluster_sync();  // every CTA has begun before another one writes to its shared memory
+  Run<T, G, V> raw;
+  if (rounds > 0) raw.load(wx, w.wstep, p.D, w.len - w.first);
+  int t0 = w.first;
   for (int k = 0; k < rounds; ++k) {
-    const int t0 = k * w.steps + w.rank * kChunk + w.warp * kS;
-    const int n = w.on ? min(kS, w.len - t0) : 0;  // tokens that count (none: 0 or less)
-    Raw<T, V> raw[G][kS];
+    const int n = w.len - t0;  // tokens from the run's first on that count (none: 0 or less)
+    Num<V> a[kS], u[kS], ma(1.f), mu(0.f);
+    Raw<T, V> o[kS];
 #pragma unroll
     for (int s = 0; s < kS; ++s) {
-      const T* at = wx + (t0 + s) * w.wstep;
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        raw[g][s].zero();
-        if (s < n) raw[g][s].load(at + (long long)g * p.D);
-      }
+      Num<V> gain;
+      sigmoids<T>(raw.x[F][s].get(), a[s], gain);
+      if (G == 4) gain = sigmoid<T>(raw.x[0][s].get());
+      u[s] = gain * raw.x[Z][s].get();
+      if (G != 2) o[s] = raw.x[O][s];
+      if (s >= n) a[s] = Num<V>(1.f), u[s] = Num<V>(0.f);
+      mu = fma(a[s], mu, u[s]);
+      ma = ma * a[s];
     }
-    float a[kS][V], u[kS][V];
-    Map<V> m;
-#pragma unroll
-    for (int v = 0; v < V; ++v) m.a[v] = 1.f, m.u[v] = 0.f;
-#pragma unroll
-    for (int s = 0; s < kS; ++s)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float gain;
-        sigmoids(raw[F][s].get(v), a[s][v], gain);
-        if (G == 4) gain = sigmoid1(raw[0][s].get(v));
-        u[s][v] = gain * raw[Z][s].get(v);
-        if (s >= n) a[s][v] = 1.f, u[s][v] = 0.f;
-        m.u[v] = fmaf(a[s][v], m.u[v], u[s][v]);
-        m.a[v] *= a[s][v];
-      }
-    float c[V];
-    carry<V, false>(sh, k & 1, m, w.warp, w.lane, w.rank, p.cs, h, c);
-    if (p.stash && n > 0)
-#pragma unroll
-      for (int v = 0; v < V; ++v) p.stash[t0 / kS * w.ystep + w.ch + v] = c[v];
+    wx += w.steps * w.wstep;
+    if (k + 1 < rounds) raw.load(wx, w.wstep, p.D, n - w.steps);  // the next round's
+    Num<V> c = carry<V, false>(sh, k & 1, ma, mu, w.warp, w.lane, w.rank, p.cs, h);
+    if (p.stash && w.on && n > 0)
+      Raw<float, 1>::store(p.stash + t0 / kS * w.ystep + w.ch, Num<1>(c.get(0))),
+          V == 2 ? Raw<float, 1>::store(p.stash + t0 / kS * w.ystep + w.ch + 1, Num<1>(c.get(V - 1))) : (void)0;
+    const int room = w.on ? p.T - t0 : 0;
 #pragma unroll
     for (int s = 0; s < kS; ++s) {
-      float out[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        c[v] = fmaf(a[s][v], c[v], u[s][v]);
-        out[v] = G == 2 ? c[v] : sigmoid1(raw[G == 2 ? 0 : O][s].get(v)) * c[v];
-        if (s >= n) out[v] = 0.f;
-      }
-      if (w.on && t0 + s < p.T) Raw<T, V>::store(y + (t0 + s) * w.ystep, out);
+      c = fma(a[s], c, u[s]);
+      Num<V> out = c;
+      if (G != 2) out = sigmoid<T>(o[s].get()) * c;
+      if (s >= n) out = Num<V>(0.f);
+      if (s < room) Raw<T, V>::store(y + s * w.ystep, out);
     }
+    y += w.steps * w.ystep;
+    t0 += w.steps;
   }
-  if (!w.on) return;
-  const float none[V] = {};
-  for (long long t = (long long)rounds * w.steps + w.rank * kChunk + w.warp * kS; t < p.T; t += w.steps)
-    for (int s = 0; s < kS && t + s < p.T; ++s) Raw<T, V>::store(y + (t + s) * w.ystep, none);
-  if (p.stateT && w.rank == 0 && w.warp == 0)
-#pragma unroll
-    for (int v = 0; v < V; ++v) p.stateT[w.ch + v] = h[v];
+  if (w.on)
+    for (long long t = t0; t < p.T; t += w.steps, y += w.steps * w.ystep)
+      for (int s = 0; s < kS && t + s < p.T; ++s) Raw<T, V>::store(y + s * w.ystep, Num<V>(0.f));
+  if (p.stateT && w.rank == 0 && w.at >= 0) p.stateT[w.at] = h;
 }
 
 template <class T, int G, int V>
@@ -253,91 +354,73 @@ __global__ void __launch_bounds__(32 * kWarps) gated_bwd_kernel(const GatedParam
   __shared__ Shared<V> sh;
   depend_launch();
   Where<T, G, V> w(p);
-  const T* wx = static_cast<const T*>(p.wx) + w.wx;
-  T* dwx = static_cast<T*>(p.dwx) + w.wx;
-  const T* dy = static_cast<const T*>(p.dy) + w.ch;
   depend_wait();
   w.lengths(p);
-  float d[V];  // gradient of the state after the round's last token
-#pragma unroll
-  for (int v = 0; v < V; ++v) d[v] = p.dstateT && w.on ? p.dstateT[w.ch + v] : 0.f;
+  float h = p.dstateT && w.at >= 0 ? p.dstateT[w.at] : 0.f;  // gradient of the state after the round's last token
   const int rounds = w.rounds();
   if (p.cs > 1) cluster_sync();
   for (int k = rounds - 1; k >= 0; --k) {
-    const int t0 = k * w.steps + w.rank * kChunk + w.warp * kS;
-    const int n = w.on ? min(kS, w.len - t0) : 0;
-    Raw<T, V> raw[G][kS], up[kS];
+    const int t0 = k * w.steps + w.first, n = w.len - t0;
+    const T* wx = static_cast<const T*>(p.wx) + w.wx + t0 * w.wstep;
+    const T* dy = static_cast<const T*>(p.dy) + w.ch + t0 * w.ystep;
+    Run<T, G, V> raw;
+    Run<T, 1, V> up;
+    raw.load(wx, w.wstep, p.D, n);
+    up.load(dy, w.ystep, 0, n);
+    Num<V> c[kS];  // states before each token
 #pragma unroll
-    for (int s = 0; s < kS; ++s) {
-      const T* at = wx + (t0 + s) * w.wstep;
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        raw[g][s].zero();
-        if (s < n) raw[g][s].load(at + (long long)g * p.D);
-      }
-      up[s].zero();
-      if (s < n) up[s].load(dy + (t0 + s) * w.ystep);
-    }
-    float c[kS][V];  // states before each token
-#pragma unroll
-    for (int v = 0; v < V; ++v) c[0][v] = n > 0 ? p.stash[t0 / kS * w.ystep + w.ch + v] : 0.f;
-    float a[kS][V], b[kS][V];  // sigmoid(f), sigmoid(-f)
-    Map<V> m;
-#pragma unroll
-    for (int v = 0; v < V; ++v) m.a[v] = 1.f, m.u[v] = 0.f;
-#pragma unroll
-    for (int s = kS - 1; s >= 0; --s)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        sigmoids(raw[F][s].get(v), a[s][v], b[s][v]);
-        float e = up[s].get(v);
-        if (G != 2) e *= sigmoid1(raw[O][s].get(v));
-        if (s >= n) a[s][v] = 1.f, e = 0.f;
-        m.u[v] = a[s][v] * (m.u[v] + e);
-        m.a[v] *= a[s][v];
-      }
-    float q[V];
-    carry<V, true>(sh, k & 1, m, w.warp, w.lane, w.rank, p.cs, d, q);
-#pragma unroll
-    for (int s = 0; s + 1 < kS; ++s)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float gain = G == 4 ? sigmoid1(raw[0][s].get(v)) : b[s][v];
-        c[s + 1][v] = fmaf(a[s][v], c[s][v], gain * raw[Z][s].get(v));
-      }
+    for (int v = 0; v < V; ++v) c[0].set(v, n > 0 ? p.stash[t0 / kS * w.ystep + w.ch + v] : 0.f);
+    Num<V> a[kS], b[kS], ma(1.f), mu(0.f);  // sigmoid(f), sigmoid(-f)
 #pragma unroll
     for (int s = kS - 1; s >= 0; --s) {
-      float g[G][V];
+      sigmoids<T>(raw.x[F][s].get(), a[s], b[s]);
+      Num<V> e = up.x[0][s].get();
+      if (G != 2) e = e * sigmoid<T>(raw.x[O][s].get());
+      if (s >= n) a[s] = Num<V>(1.f), e = Num<V>(0.f);
+      mu = a[s] * (mu + e);
+      ma = ma * a[s];
+    }
+    Num<V> q = carry<V, true>(sh, k & 1, ma, mu, w.warp, w.lane, w.rank, p.cs, h);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float z = raw[Z][s].get(v), slope = a[s][v] * b[s][v];
-        float e = up[s].get(v), os = 1.f, oc = 0.f, is = b[s][v], ic = 0.f;
-        if (G != 2) sigmoids(raw[O][s].get(v), os, oc);
-        if (G == 4) sigmoids(raw[0][s].get(v), is, ic);
-        const float dc = fmaf(e, os, q[v]);
-        g[Z][v] = dc * is;
-        g[F][v] = dc * (G == 4 ? c[s][v] : c[s][v] - z) * slope;
-        if (G == 4) g[0][v] = dc * z * (is * ic);
-        if (G != 2) g[O][v] = e * fmaf(a[s][v], c[s][v], is * z) * (os * oc);
-        if (s < n) q[v] = a[s][v] * dc;
-        if (s >= n)
+    for (int s = 0; s + 1 < kS; ++s) {
+      const Num<V> gain = G == 4 ? sigmoid<T>(raw.x[0][s].get()) : b[s];
+      c[s + 1] = fma(a[s], c[s], gain * raw.x[Z][s].get());
+    }
+    T* dwx = static_cast<T*>(p.dwx) + w.wx + t0 * w.wstep;
+    const int room = w.on ? p.T - t0 : 0;
 #pragma unroll
-          for (int j = 0; j < G; ++j) g[j][v] = 0.f;
+    for (int s = kS - 1; s >= 0; --s) {
+      Num<V> g[G];
+      const Num<V> z = raw.x[Z][s].get(), e = up.x[0][s].get();
+      Num<V> os, oc, is = b[s], ic, si, so;
+      Num<V> dc = e + q;
+      if (G != 2) {
+        sigmoids<T>(raw.x[O][s].get(), os, oc, &so);
+        dc = fma(e, os, q);
       }
-      if (w.on && t0 + s < p.T)
+      if (G == 4) sigmoids<T>(raw.x[0][s].get(), is, ic, &si);
+      g[Z] = dc * is;
+      g[F] = dc * (G == 4 ? c[s] : minus(c[s], z)) * (a[s] * b[s]);
+      if (G == 4) g[0] = dc * z * si;
+      if (G != 2) g[O] = e * fma(a[s], c[s], is * z) * so;
+      if (s < n) q = a[s] * dc;
+      if (s >= n)
 #pragma unroll
-        for (int j = 0; j < G; ++j) Raw<T, V>::store(dwx + (t0 + s) * w.wstep + (long long)j * p.D, g[j]);
+        for (int j = 0; j < G; ++j) g[j] = Num<V>(0.f);
+      if (s < room)
+#pragma unroll
+        for (int j = 0; j < G; ++j) Raw<T, V>::store(dwx + s * w.wstep + (long long)j * p.D, g[j]);
     }
   }
-  if (!w.on) return;
-  const float none[V] = {};
-  for (long long t = (long long)rounds * w.steps + w.rank * kChunk + w.warp * kS; t < p.T; t += w.steps)
-    for (int s = 0; s < kS && t + s < p.T; ++s)
+  if (w.on) {
+    long long t = (long long)rounds * w.steps + w.first;
+    T* dwx = static_cast<T*>(p.dwx) + w.wx + t * w.wstep;
+    for (; t < p.T; t += w.steps, dwx += w.steps * w.wstep)
+      for (int s = 0; s < kS && t + s < p.T; ++s)
 #pragma unroll
-      for (int j = 0; j < G; ++j) Raw<T, V>::store(dwx + (t + s) * w.wstep + (long long)j * p.D, none);
-  if (p.dstate0 && w.rank == 0 && w.warp == 0)
-#pragma unroll
-    for (int v = 0; v < V; ++v) p.dstate0[w.ch + v] = d[v];
+        for (int j = 0; j < G; ++j) Raw<T, V>::store(dwx + s * w.wstep + (long long)j * p.D, Num<V>(0.f));
+  }
+  if (p.dstate0 && w.rank == 0 && w.at >= 0) p.dstate0[w.at] = h;
 }
 
 // One token of each row against a cache of states: a thread for V channels of a row.
@@ -351,21 +434,22 @@ __global__ void __launch_bounds__(128) gated_step_kernel(const GatedStepParams p
   const T* wx = static_cast<const T*>(p.wx) + ((long long)b * p.N + c / p.D * p.D) * G + c % p.D;
   depend_wait();
   const int slot = p.slots ? p.slots[b] : b;
-  float out[V] = {};
+  Num<V> out(0.f);
   if (slot >= 0 && slot < p.nslots) {
     Raw<T, V> raw[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) raw[g].load(wx + (long long)g * p.D);
     float* state = p.state + (long long)slot * p.N + c;
+    Num<V> h, a, gain;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float a, gain;
-      sigmoids(raw[F].get(v), a, gain);
-      if (G == 4) gain = sigmoid1(raw[0].get(v));
-      const float h = fmaf(a, state[v], gain * raw[Z].get(v));
-      state[v] = h;
-      out[v] = G == 2 ? h : sigmoid1(raw[O].get(v)) * h;
-    }
+    for (int v = 0; v < V; ++v) h.set(v, state[v]);
+    sigmoids<T>(raw[F].get(), a, gain);
+    if (G == 4) gain = sigmoid<T>(raw[0].get());
+    h = fma(a, h, gain * raw[Z].get());
+#pragma unroll
+    for (int v = 0; v < V; ++v) state[v] = h.get(v);
+    out = h;
+    if (G != 2) out = sigmoid<T>(raw[O].get()) * h;
   }
   Raw<T, V>::store(static_cast<T*>(p.y) + (long long)b * p.N + c, out);
 }

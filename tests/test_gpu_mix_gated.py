@@ -54,8 +54,8 @@ def check(S, T, B, NH, D, gates, dtype, lens=None, state=True, seed=0):
     out = S.gated_recurrence(Wx, gates=gates, state=s0, lens=ln, train=True)
     g = S.gated_recurrence_backward(Wx, out["stash"], dy, gates=gates, dstate=ds, lens=ln)
     a = (None if s0 is None else np64(s0), None if ds is None else np64(ds))
-    f = O.gated(np64(Wx), gates, a[0], lens)
-    b = O.gated_backward(np64(Wx), gates, np64(dy), a[0], a[1], lens)
+    f = O.gated(np64(Wx), gates, a[0], lens, dtype == "bf16")
+    b = O.gated_backward(np64(Wx), gates, np64(dy), a[0], a[1], lens, dtype == "bf16")
     close(out["y"], f["y"], f["y_err"], HALF[dtype])
     close(out["state"], f["state"], f["state_err"])
     close(g["dWx"], b["dWx"], b["dWx_err"], HALF[dtype])
@@ -151,7 +151,7 @@ def test_step(S, B, NH, D, gates, dtype):
     y = S.gated_recurrence_step(Wx[0], cache, gates=gates, slots=slots)
     ok = [(b, int(s)) for b, s in enumerate(slots) if 0 <= s < B + 3]
     at = [s for _, s in ok]
-    f = O.gated(np64(Wx)[:, [b for b, _ in ok]], gates, np64(old)[at])
+    f = O.gated(np64(Wx)[:, [b for b, _ in ok]], gates, np64(old)[at], fast=dtype == "bf16")
     close(cache[at], f["state"], f["state_err"])
     close(y[[b for b, _ in ok]], f["y"][0], f["y_err"][0], HALF[dtype])
     rest = [s for s in range(B + 3) if s not in at]
@@ -161,7 +161,7 @@ def test_step(S, B, NH, D, gates, dtype):
     # without slots: row b's state is b
     cache2 = old[:B].clone()
     y2 = S.gated_recurrence_step(Wx[0], cache2, gates=gates)
-    f = O.gated(np64(Wx), gates, np64(old[:B]))
+    f = O.gated(np64(Wx), gates, np64(old[:B]), fast=dtype == "bf16")
     close(cache2, f["state"], f["state_err"])
     close(y2, f["y"][0], f["y_err"][0], HALF[dtype])
 
@@ -173,7 +173,7 @@ def test_steps_continue_a_prompt(S):
     state, ys = out["state"], [out["y"]]
     for t in range(25, 40):
         ys.append(S.gated_recurrence_step(Wx[t], state, gates="ifzo")[None])
-    f = O.gated(np64(Wx), "ifzo", np64(s0))
+    f = O.gated(np64(Wx), "ifzo", np64(s0), fast=True)
     close(torch.cat(ys), f["y"], f["y_err"], HALF["bf16"])
     close(state, f["state"], f["state_err"])
     close(want["state"], f["state"], f["state_err"])
@@ -187,10 +187,10 @@ def test_unaligned_views(S):
     odd = buf[1:].view(Wx.shape).copy_(Wx)
     a = S.gated_recurrence(Wx, state=s0, train=True)
     b = S.gated_recurrence(odd, state=s0, train=True)
-    f = O.gated(np64(Wx), "fz", np64(s0))
+    f = O.gated(np64(Wx), "fz", np64(s0), fast=True)
     for o in (a, b):
         close(o["y"], f["y"], f["y_err"], HALF["bf16"])
-    g = O.gated_backward(np64(Wx), "fz", np64(dy), np64(s0), np64(ds))
+    g = O.gated_backward(np64(Wx), "fz", np64(dy), np64(s0), np64(ds), fast=True)
     r = S.gated_recurrence_backward(odd, b["stash"], dy, dstate=ds)
     close(r["dWx"], g["dWx"], g["dWx_err"], HALF["bf16"])
 
