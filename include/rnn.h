@@ -396,30 +396,33 @@ int rnn_linattn_step(const rnn_linattn_desc_t* desc, const rnn_linattn_strides_t
  * rnn_gated_stash_size bytes.  Gates, states and sums are fp32, y is rounded once.  A value that is not
  * finite reaches its own and later tokens of its row and channel (in the gradient: earlier ones, too) and
  * nothing else; where a product of forget gates underflows, an infinity before it may turn to NaN.
- * Wx, y contiguous; aligned as their element is (4 bytes for bf16 and 8 for fp32, with an even D, are faster).
- * No workspace, no device status. */
+ * Wx, y contiguous; aligned as their element is.  From 32 tokens on, heads of a multiple of 16 bytes at addresses that
+ * are run on tiles that the kernels wait for.  workspace: 256-byte aligned, >= 256 bytes (status word at offset 0). */
 typedef enum { RNN_GATES_FZ = 2, RNN_GATES_FZO = 3, RNN_GATES_IFZO = 4 } rnn_gates_t;
 
 typedef struct {
   int32_t dtype; /* rnn_dtype_t of Wx, y, dy, dWx */
   int32_t T, B, NH, D;
   int32_t gates; /* rnn_gates_t: the gates' number G */
+  int32_t flags; /* 0, or RNN_FLAG_TEST_TIMEOUT: rnn_gated_fwd and _bwd at sizes that run on tiles, else
+                    RNN_ERR_UNSUPPORTED */
 } rnn_gated_desc_t;
 
 /* Bytes of the stash: the fp32 state before every eighth token, [ceil(T/8), B, NH, D].  0 on an invalid desc. */
 size_t rnn_gated_stash_size(const rnn_gated_desc_t* desc);
 
 int rnn_gated_fwd(const rnn_gated_desc_t* desc, const void* Wx, const int32_t* lens, const float* state0, void* y,
-                  float* stateT, float* stash, void* stream);
+                  float* stateT, float* stash, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Gradients of L = sum(y * dy) + sum(stateT * dstateT) from the forward's Wx, lens and stash: dWx like Wx (zero for
  * tokens that do not count), dstate0 [B, NH, D] fp32 (NULL = not written; may be dstateT).  dstateT NULL = zero. */
 int rnn_gated_bwd(const rnn_gated_desc_t* desc, const void* Wx, const int32_t* lens, const float* stash, const void* dy,
-                  const float* dstateT, void* dWx, float* dstate0, void* stream);
+                  const float* dstateT, void* dWx, float* dstate0, void* workspace, size_t workspace_bytes,
+                  void* stream);
 
 /* One token (desc->T == 1, Wx [B, NH, G*D]) for each of B rows out of a cache of n_slots states [n_slots, NH, D] fp32,
  * updated in place: row b uses state slots[b] (slots NULL: state b).  A row whose slot is not in [0, n_slots) has no
- * state: its y is zero.  Two rows must not name the same slot. */
+ * state: its y is zero.  Two rows must not name the same slot.  No workspace, no device status. */
 int rnn_gated_step(const rnn_gated_desc_t* desc, const void* Wx, const int32_t* slots, int32_t n_slots, float* state,
                    void* y, void* stream);
 

@@ -58,7 +58,7 @@ class rnn_linattn_strides_t(ctypes.Structure):
 
 
 class rnn_gated_desc_t(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "T", "B", "NH", "D", "gates")]
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "T", "B", "NH", "D", "gates", "flags")]
 
 
 class rnn_rotary_desc_t(ctypes.Structure):
@@ -107,8 +107,8 @@ _SIGS = {
     "rnn_linattn_bwd": (_I, [_LDESC, _LST] + [_P] * 13 + [_SZ, _P]),
     "rnn_linattn_step": (_I, [_LDESC, _LST] + [_P] * 5 + [_I32] + [_P] * 3),
     "rnn_gated_stash_size": (_SZ, [_GDESC]),
-    "rnn_gated_fwd": (_I, [_GDESC] + [_P] * 7),
-    "rnn_gated_bwd": (_I, [_GDESC] + [_P] * 8),
+    "rnn_gated_fwd": (_I, [_GDESC] + [_P] * 7 + [_SZ, _P]),
+    "rnn_gated_bwd": (_I, [_GDESC] + [_P] * 8 + [_SZ, _P]),
     "rnn_gated_step": (_I, [_GDESC] + [_P] * 2 + [_I32] + [_P] * 3),
     "rnn_head_norm_rotary": (_I, [_RDESC, _RST] + [_P] * 9),
     "rnn_head_norm_rotary_bwd_workspace_size": (_SZ, [_RDESC]),

@@ -486,19 +486,21 @@ PyObject* gated_recurrence(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Gated g(Wx, a[1], 2);
   g.want_state("state", state);
   want("lens", lens, {g.B}, at::kInt, g.dev);
-  Tensor y, fin, stash;
+  Tensor y, fin, stash, ws;
   int st;
   {
     NoGil free;
+    ws = make({256}, at::kByte, g.dev);
     y = make({g.T, g.B, g.NH, g.D}, g.type, g.dev), fin = g.states();
     if (train) stash = make({(int64_t)(api.gated_stash(&g.desc) / sizeof(float))}, at::kFloat, g.dev);
     st = api.gated_fwd(&g.desc, Wx.data_ptr(), at_of<const int32_t>(lens), at_of<const float>(state), y.data_ptr(),
-                       at_of<float>(&fin), train ? at_of<float>(&stash) : nullptr, current_stream());
+                       at_of<float>(&fin), train ? at_of<float>(&stash) : nullptr, ws.data_ptr(), 256, current_stream());
   }
   if (st) return status(st);
   PyObject* out = PyDict_New();
   put(out, "y", y);
   put(out, "state", fin);
+  put(out, "workspace", ws);
   if (train) put(out, "stash", stash);
   return out;
   END_HANDLE_TH_ERRORS
@@ -515,18 +517,20 @@ PyObject* gated_recurrence_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
   want("dy", dy, {g.T, g.B, g.NH, g.D}, g.type, g.dev);
   g.want_state("dstate", dstate);
   want("lens", lens, {g.B}, at::kInt, g.dev);
-  Tensor dWx, ds;
+  Tensor dWx, ds, ws;
   int st;
   {
     NoGil free;
+    ws = make({256}, at::kByte, g.dev);
     dWx = make(Wx.sizes(), g.type, g.dev), ds = g.states();
     st = api.gated_bwd(&g.desc, Wx.data_ptr(), at_of<const int32_t>(lens), at_of<const float>(&stash), dy.data_ptr(),
-                       at_of<const float>(dstate), dWx.data_ptr(), at_of<float>(&ds), current_stream());
+                       at_of<const float>(dstate), dWx.data_ptr(), at_of<float>(&ds), ws.data_ptr(), 256, current_stream());
   }
   if (st) return status(st);
   PyObject* out = PyDict_New();
   put(out, "dWx", dWx);
   put(out, "dstate", ds);
+  put(out, "workspace", ws);
   return out;
   END_HANDLE_TH_ERRORS
 }

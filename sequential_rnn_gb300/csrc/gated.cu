@@ -18,6 +18,7 @@
 
 #include <cstdint>
 
+#include "gated.cuh"
 #include "kernels.h"
 #include "lm.h"
 #include "ptx.cuh"
@@ -25,102 +26,7 @@
 namespace srnn {
 namespace {
 
-constexpr int kS = kGatedRun;     // tokens of a run
-constexpr int kWarps = 8;         // runs of a CTA side by side
-constexpr int kChunk = kS * kWarps;
-constexpr int kMaxCluster = 16;
-
-// V fp32 numbers; a pair is added and multiplied by one instruction
-template <int V>
-struct Num;
-template <>
-struct Num<1> {
-  float x;
-  __device__ Num() {}
-  __device__ explicit Num(float a) : x(a) {}
-  __device__ float get(int) const { return x; }
-  __device__ void set(int, float a) { x = a; }
-};
-template <>
-struct Num<2> {
-  float2 x;
-  __device__ Num() {}
-  __device__ explicit Num(float a) : x(make_float2(a, a)) {}
-  __device__ float get(int i) const { return i ? x.y : x.x; }
-  __device__ void set(int i, float a) { (i ? x.y : x.x) = a; }
-};
-__device__ __forceinline__ uint64_t bits(const Num<2>& a) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x.x), "f"(a.x.y));
-  return r;
-}
-__device__ __forceinline__ Num<2> of_bits(uint64_t r) {
-  Num<2> a;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x.x), "=f"(a.x.y) : "l"(r));
-  return a;
-}
-__device__ __forceinline__ Num<1> fma(const Num<1>& a, const Num<1>& b, const Num<1>& c) { return Num<1>(fmaf(a.x, b.x, c.x)); }
-__device__ __forceinline__ Num<1> operator*(const Num<1>& a, const Num<1>& b) { return Num<1>(a.x * b.x); }
-__device__ __forceinline__ Num<1> operator+(const Num<1>& a, const Num<1>& b) { return Num<1>(a.x + b.x); }
-__device__ __forceinline__ Num<2> fma(const Num<2>& a, const Num<2>& b, const Num<2>& c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-  return of_bits(r);
-}
-__device__ __forceinline__ Num<2> operator*(const Num<2>& a, const Num<2>& b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
-  return of_bits(r);
-}
-__device__ __forceinline__ Num<2> operator+(const Num<2>& a, const Num<2>& b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
-  return of_bits(r);
-}
-template <int V>
-__device__ __forceinline__ Num<V> minus(const Num<V>& a, const Num<V>& b) { return fma(b, Num<V>(-1.f), a); }
-
-template <class T>
-__device__ __forceinline__ float exp_of(float x);  // x <= 0
-template <>
-__device__ __forceinline__ float exp_of<float>(float x) { return expf(x); }
-// for bf16 gates: the product's rounding leaves a relative error of |x| 2^-24
-template <>
-__device__ __forceinline__ float exp_of<__nv_bfloat16>(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
-  return y;
-}
-__device__ __forceinline__ float reciprocal(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// s = sigmoid(x), c = sigmoid(-x): the smaller one from e^-|x|, the larger one as 1 less it, so that both are good to
-// a few units of their own last place (a memory of n tokens needs 1 - a to better than 1 / n); sl = s c
-template <class T, int V>
-__device__ __forceinline__ void sigmoids(const Num<V>& x, Num<V>& s, Num<V>& c, Num<V>* slope = nullptr) {
-  Num<V> e, r;
-#pragma unroll
-  for (int v = 0; v < V; ++v) e.set(v, exp_of<T>(-fabsf(x.get(v))));
-  const Num<V> d = e + Num<V>(1.f);
-#pragma unroll
-  for (int v = 0; v < V; ++v) r.set(v, reciprocal(d.get(v)));
-  const Num<V> low = e * r, high = minus(Num<V>(1.f), low);
-  if (slope) *slope = low * high;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const bool up = x.get(v) > 0.f;
-    s.set(v, up ? high.get(v) : low.get(v));
-    c.set(v, up ? low.get(v) : high.get(v));
-  }
-}
-template <class T, int V>
-__device__ __forceinline__ Num<V> sigmoid(const Num<V>& x) {
-  Num<V> s, c;
-  sigmoids<T>(x, s, c);
-  return s;
-}
+constexpr int kS = kRunTokens, kWarps = kRunWarps, kChunk = kRunChunk, kMaxCluster = 8;
 
 // V neighbouring channels of one token
 template <class T, int V>
@@ -166,10 +72,6 @@ struct Raw<float, 1> {
   static __device__ void store(float* p, const Num<1>& a) { *p = a.x; }
 };
 
-// c -> a c + u of one channel
-struct Map {
-  float a, u;
-};
 template <int V>
 struct Shared {
   alignas(16) Map part[kWarps][32 * V];
@@ -302,6 +204,7 @@ __global__ void __launch_bounds__(32 * kWarps) gated_fwd_kernel(const GatedParam
   const T* wx = static_cast<const T*>(p.wx) + w.wx + w.first * w.wstep;
   T* y = static_cast<T*>(p.y) + w.ch + w.first * w.ystep;
   depend_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   w.lengths(p);
   float h = p.state0 && w.at >= 0 ? p.state0[w.at] : 0.f;
   const int rounds = w.rounds();
@@ -355,6 +258,7 @@ __global__ void __launch_bounds__(32 * kWarps) gated_bwd_kernel(const GatedParam
   depend_launch();
   Where<T, G, V> w(p);
   depend_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   w.lengths(p);
   float h = p.dstateT && w.at >= 0 ? p.dstateT[w.at] : 0.f;  // gradient of the state after the round's last token
   const int rounds = w.rounds();
@@ -516,6 +420,10 @@ int step_t(const GatedStepParams& p, int gates, cudaStream_t s) {
 }  // namespace
 
 int launch_gated(GatedParams p, int gates, bool bf16, bool bwd, cudaStream_t s) {
+  if (gated_takes_tiles(p, bf16)) {
+    const int e = launch_gated_tile(p, gates, bf16, bwd, s);
+    if (e != kGatedNoTile) return e;
+  }
   return bf16 ? launch_t<__nv_bfloat16>(p, gates, bwd, s) : launch_t<float>(p, gates, bwd, s);
 }
 int launch_gated_step(const GatedStepParams& p, int gates, bool bf16, cudaStream_t s) {

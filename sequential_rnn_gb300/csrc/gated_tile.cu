@@ -1,0 +1,467 @@
+// Gated linear recurrence on tiles that TMA brings: head sizes that are multiples of 16 bytes, from a few tokens on (the
+// mathematics and the other sizes: gated.cu).
+//
+// A CTA takes 64 channels of a head of one row, and goes through time in rounds of 64 tokens; the CTAs of a cluster take
+// neighbouring rounds at once.  A control warp keeps a ring of tiles [64 tokens][gates][64 channels] filled.  Eight warps
+// take a run of 8 tokens each: gates and the run's map c -> A c + U in registers, the map handed to 64 threads of two
+// more warps, one for each channel, which compose the maps in the order of time -- those of the cluster's CTAs after
+// exchanging them by st.async -- and hand every run the state at its start; then the run once more, its results written into
+// the tile it came from, from where TMA stores them.  Nothing is read twice and no thread forms an address per token.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "gated.cuh"
+#include "kernels.h"
+#include "lm.h"
+#include "ptx.cuh"
+#include "tc.cuh"
+
+namespace srnn {
+namespace {
+
+constexpr int kS = kRunTokens, kW = kRunWarps, kC = kRunChunk, kX = 64;  // channels of a tile
+constexpr int kFold = 2;                        // warps that compose the maps
+constexpr int kThreads = 32 * (kW + kFold + 1);
+constexpr int kReady = 1, kStart = 2;           // named barriers: maps there, starts there
+constexpr uint32_t kMapBytes = kX * sizeof(Map);
+
+struct TileMaps {
+  CUtensorMap wx;                 // [T, B, NH G, D], box [64, 1, G, 64]
+  CUtensorMap out;                // y, or dWx by runs
+  CUtensorMap dy, stash;          // gradient alone: box [64, 1, 1, 64], [8 runs, 1, 1, 64]
+};
+
+template <class T, int G, bool BWD>
+struct Tile {
+  static constexpr uint32_t ROW = kX * sizeof(T), TOK = G * ROW;
+  static constexpr uint32_t WX = kC * TOK, DY = BWD ? kC * ROW : 0, ST = BWD ? kW * kX * 4 : 0;
+  static constexpr uint32_t STAGE = WX + DY + ST;
+  static constexpr int STAGES = STAGE <= 24 * 1024 ? 3 : STAGE <= 64 * 1024 ? 3 : 2;
+  static constexpr uint32_t PART = STAGES * STAGE, START = PART + kW * kMapBytes, BARS = START + kW * kX * 4,
+                            ALL = BARS + 256;
+  static constexpr uint32_t smem(int cs) { return ALL + (cs > 1 ? 2 * cs * kMapBytes : 0) + 128; }
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void bar_arrive(uint32_t id, uint32_t n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+// A bounded wait.  Nobody leaves its loop early (the named barriers count on everyone): after one wait has run out the
+// others do not wait any more, and what the call writes is not valid.
+struct Wait {
+  int* status;
+  unsigned long long limit_ns;
+  volatile int* gave_up;
+  template <bool CLUSTER = false>
+  __device__ __forceinline__ void on(uint32_t bar, uint32_t parity) const {
+    auto there = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+    if (there()) return;
+    const uint64_t t0 = globaltimer_ns();
+    while (!*gave_up && !there())
+      if (globaltimer_ns() - t0 > limit_ns) {
+        *gave_up = 1;
+        atomicOr(status, kStatusTimeout);
+      }
+  }
+};
+
+// two neighbouring channels in shared memory
+template <class T>
+__device__ __forceinline__ Num<2> get2(uint32_t at);
+template <>
+__device__ __forceinline__ Num<2> get2<__nv_bfloat16>(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
+  Num<2> r;
+  r.x = make_float2(bf16_lo(v), bf16_hi(v));
+  return r;
+}
+template <>
+__device__ __forceinline__ Num<2> get2<float>(uint32_t at) {
+  Num<2> r;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(r.x.x), "=f"(r.x.y) : "r"(at));
+  return r;
+}
+template <class T>
+__device__ __forceinline__ void put2(uint32_t at, const Num<2>& a);
+template <>
+__device__ __forceinline__ void put2<__nv_bfloat16>(uint32_t at, const Num<2>& a) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pack_bf16x2(a.x.x, a.x.y)) : "memory");
+}
+template <>
+__device__ __forceinline__ void put2<float>(uint32_t at, const Num<2>& a) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(a.x.x), "f"(a.x.y) : "memory");
+}
+__device__ __forceinline__ void st_async_map(uint32_t raddr, const Map& m, uint32_t rbar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(raddr),
+               "r"(__float_as_uint(m.a)), "r"(__float_as_uint(m.u)), "r"(rbar)
+               : "memory");
+}
+
+// One run of a round, forward: maps first, results second.  FULL: all its tokens count (else the first n do).
+template <class T, int G, bool FULL>
+struct Forward {
+  using C = Tile<T, G, false>;
+  static constexpr int F = G == 4 ? 1 : 0, Z = F + 1, O = G == 2 ? 0 : F + 2;
+  static __device__ __forceinline__ void maps(uint32_t x, int n, Num<2> (&a)[kS], Num<2> (&u)[kS], Num<2>& ma, Num<2>& mu) {
+    ma = Num<2>(1.f), mu = Num<2>(0.f);
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+      Num<2> gain;
+      sigmoids<T>(get2<T>(x + s * C::TOK + F * C::ROW), a[s], gain);
+      if (G == 4) gain = sigmoid<T>(get2<T>(x + s * C::TOK));
+      u[s] = gain * get2<T>(x + s * C::TOK + Z * C::ROW);
+      if (!FULL && s >= n) a[s] = Num<2>(1.f), u[s] = Num<2>(0.f);
+      mu = fma(a[s], mu, u[s]);
+      ma = ma * a[s];
+    }
+  }
+  // y of token s goes where value s G^0 of the run was: rows of one gate behind one another, each past what is still read
+  static __device__ __forceinline__ void results(uint32_t x, int n, const Num<2> (&a)[kS], const Num<2> (&u)[kS], Num<2> c) {
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+      c = fma(a[s], c, u[s]);
+      Num<2> y = c;
+      if (G != 2) y = sigmoid<T>(get2<T>(x + s * C::TOK + O * C::ROW)) * c;
+      if (!FULL && s >= n) y = Num<2>(0.f);
+      put2<T>(x + s * C::ROW, y);
+    }
+  }
+};
+
+template <class T, int G, bool FULL>
+struct Backward {
+  using C = Tile<T, G, true>;
+  static constexpr int F = G == 4 ? 1 : 0, Z = F + 1, O = G == 2 ? 0 : F + 2;
+  static __device__ __forceinline__ void maps(uint32_t x, uint32_t dy, int n, Num<2> (&a)[kS], Num<2> (&b)[kS], Num<2>& ma,
+                                              Num<2>& mu) {
+    ma = Num<2>(1.f), mu = Num<2>(0.f);
+#pragma unroll
+    for (int s = kS - 1; s >= 0; --s) {
+      sigmoids<T>(get2<T>(x + s * C::TOK + F * C::ROW), a[s], b[s]);
+      Num<2> e = get2<T>(dy + s * C::ROW);
+      if (G != 2) e = e * sigmoid<T>(get2<T>(x + s * C::TOK + O * C::ROW));
+      if (!FULL && s >= n) a[s] = Num<2>(1.f), e = Num<2>(0.f);
+      mu = a[s] * (mu + e);
+      ma = ma * a[s];
+    }
+  }
+  // c0: the state before the run; q: the gradient of the state after it
+  static __device__ __forceinline__ void results(uint32_t x, uint32_t dy, int n, const Num<2> (&a)[kS],
+                                                 const Num<2> (&b)[kS], const Num<2>& c0, Num<2> q) {
+    Num<2> c[kS];
+    c[0] = c0;
+#pragma unroll
+    for (int s = 0; s + 1 < kS; ++s) {
+      const Num<2> gain = G == 4 ? sigmoid<T>(get2<T>(x + s * C::TOK)) : b[s];
+      c[s + 1] = fma(a[s], c[s], gain * get2<T>(x + s * C::TOK + Z * C::ROW));
+    }
+#pragma unroll
+    for (int s = kS - 1; s >= 0; --s) {
+      const uint32_t at = x + s * C::TOK;
+      Num<2> g[G];
+      const Num<2> z = get2<T>(at + Z * C::ROW), e = get2<T>(dy + s * C::ROW);
+      Num<2> os, oc, is = b[s], ic, si, so;
+      Num<2> dc = e + q;
+      if (G != 2) {
+        sigmoids<T>(get2<T>(at + O * C::ROW), os, oc, &so);
+        dc = fma(e, os, q);
+      }
+      if (G == 4) sigmoids<T>(get2<T>(at), is, ic, &si);
+      g[Z] = dc * is;
+      g[F] = dc * (G == 4 ? c[s] : minus(c[s], z)) * (a[s] * b[s]);
+      if (G == 4) g[0] = dc * z * si;
+      if (G != 2) g[O] = e * fma(a[s], c[s], is * z) * so;
+      if (FULL || s < n) q = a[s] * dc;
+#pragma unroll
+      for (int j = 0; j < G; ++j) put2<T>(at + j * C::ROW, !FULL && s >= n ? Num<2>(0.f) : g[j]);
+    }
+  }
+};
+
+template <class T, int G, bool BWD>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && G == 2 ? 2 : 1)
+    gated_tile_kernel(const GatedParams p, const __grid_constant__ TileMaps maps) {
+  using C = Tile<T, G, BWD>;
+  extern __shared__ char dyn[];
+  __shared__ int gave_up_s;
+  const uint32_t sm = (smem_u32(dyn) + 127u) & ~127u;
+  char* const sp = dyn + (sm - smem_u32(dyn));
+  Map* const part = reinterpret_cast<Map*>(sp + C::PART);        // [kW][kX]
+  float* const start = reinterpret_cast<float*>(sp + C::START);  // [kW][kX]
+  Map* const all = reinterpret_cast<Map*>(sp + C::ALL);          // [2][cs][kX]
+  const uint32_t full = sm + C::BARS, empty = full + 8 * C::STAGES, swap = empty + 8 * C::STAGES;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, cs = p.cs;
+  const int rank = (int)(blockIdx.x % cs);
+  const unsigned id = blockIdx.x / cs;
+  const int b = (int)(id / p.tiles), tile = (int)(id % p.tiles), per = (p.D + kX - 1) / kX;
+  const int head = tile / per, c0 = tile % per * kX;
+  depend_launch();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, kW);
+    mbar_init(swap, 1), mbar_init(swap + 8, 1);
+    gave_up_s = 0;
+    fence_mbar_init();
+    fence_async_smem();
+  }
+  __syncthreads();
+  depend_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+  const Wait wait{p.status, p.timeout_ns, &gave_up_s};
+  int len = p.T;
+  if (p.lens) len = min(max(p.lens[b], 0), p.T);
+  const int step = cs * kC, rounds = (len + step - 1) / step;
+  __syncwarp();
+  if (cs > 1) cluster_sync();  // every CTA's barriers are there
+  auto round_of = [&](int i) { return BWD ? rounds - 1 - i : i; };
+
+  if (warp == kW + kFold) {  // ---- copies
+    if (lane == 0) {
+      tma_prefetch_map(&maps.wx);
+      tma_prefetch_map(&maps.out);
+      int i = 0;
+      for (; i < rounds && !p.withhold; ++i) {
+        const int st = i % C::STAGES;
+        if (i >= C::STAGES) wait.on(empty + 8 * st, (i / C::STAGES - 1) & 1);
+        if (gave_up_s) break;
+        const uint32_t at = sm + st * C::STAGE, bar = full + 8 * st;
+        const int t0 = round_of(i) * step + rank * kC;
+        mbar_arrive_expect_tx(bar, C::STAGE);
+        tma_load_4d(at, &maps.wx, c0, head * G, b, t0, bar);
+        if (BWD) {
+          tma_load_4d(at + C::WX, &maps.dy, c0, head, b, t0, bar);
+          tma_load_4d(at + C::WX + C::DY, &maps.stash, c0, head, b, t0 / kS, bar);
+        }
+      }
+      if (gave_up_s)  // what was asked for lands before the CTA leaves
+        for (int j = i < C::STAGES ? 0 : i - C::STAGES; j < i; ++j) {
+          const uint64_t since = globaltimer_ns();
+          while (!mbar_try_wait(full + 8 * (j % C::STAGES), (j / C::STAGES) & 1) && globaltimer_ns() - since < 10000000ull) {
+          }
+        }
+    }
+    __syncwarp();
+  } else if (warp >= kW) {  // ---- maps: a thread for each channel
+    const int c = threadIdx.x - 32 * kW;
+    const long long at = c0 + c < p.D ? (long long)b * p.N + (long long)head * p.D + c0 + c : -1;
+    const float* from = BWD ? p.dstateT : p.state0;
+    float h = from && at >= 0 ? from[at] : 0.f;
+    for (int i = 0; i < rounds; ++i) {
+      bar_sync(kReady, 32 * (kW + kFold));
+      Map m[kW];
+#pragma unroll
+      for (int w = 0; w < kW; ++w) m[w] = part[(BWD ? kW - 1 - w : w) * kX + c];
+      float in = h;
+      if (cs > 1) {
+        Map t = m[0];
+#pragma unroll
+        for (int w = 1; w < kW; ++w) {
+          t.u = fmaf(m[w].a, t.u, m[w].u);
+          t.a *= m[w].a;
+        }
+        const uint32_t bar = swap + 8 * (i & 1), to = smem_u32(&all[((i & 1) * cs + rank) * kX + c]);
+        if (!gave_up_s) {
+          if (c == 0) mbar_arrive_expect_tx(bar, cs * kMapBytes);
+          // (a CTA sends round i + 2 after it has round i + 1 from this one, which has then read round i)
+          for (int r = 0; r < cs; ++r) st_async_map(mapa(to, (uint32_t)r), t, mapa(bar, (uint32_t)r));
+          wait.on<true>(bar, (i >> 1) & 1);
+        }
+        const Map* x = all + (i & 1) * cs * kX + c;
+        for (int j = 0; j < cs; ++j) {
+          const int r = BWD ? cs - 1 - j : j;
+          if (r == rank) in = h;
+          h = fmaf(x[r * kX].a, h, x[r * kX].u);
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        start[(BWD ? kW - 1 - w : w) * kX + c] = in;
+        in = fmaf(m[w].a, in, m[w].u);
+      }
+      if (cs == 1) h = in;
+      bar_arrive(kStart, 32 * (kW + kFold));
+    }
+    float* const to = BWD ? p.dstate0 : p.stateT;
+    if (to && rank == 0 && at >= 0) to[at] = h;
+  } else {  // ---- runs
+    const uint32_t mine = sm + warp * kS * C::TOK + lane * 2 * sizeof(T);
+    const long long ystep = (long long)p.B * p.N;
+    const bool on = c0 + 2 * lane < p.D;
+    float* const stash = p.stash + (long long)b * p.N + (long long)head * p.D + c0 + 2 * lane;
+    int prev = -1;  // the stage whose results are on their way out
+    auto release = [&] {
+      if (prev >= 0 && lane == 0) {
+        bulk_wait_read_all();
+        mbar_arrive(empty + 8 * prev);
+      }
+    };
+    for (int i = 0; i < rounds; ++i) {
+      const int st = i % C::STAGES, t0 = round_of(i) * step + rank * kC + warp * kS, n = len - t0;
+      const uint32_t x = mine + st * C::STAGE, dy = sm + st * C::STAGE + C::WX + warp * kS * C::ROW + lane * 2 * sizeof(T);
+      wait.on(full + 8 * st, (i / C::STAGES) & 1);
+      Num<2> a[kS], u[kS], ma, mu;
+      if constexpr (BWD) {
+        if (n >= kS)
+          Backward<T, G, true>::maps(x, dy, n, a, u, ma, mu);
+        else
+          Backward<T, G, false>::maps(x, dy, n, a, u, ma, mu);
+      } else {
+        if (n >= kS)
+          Forward<T, G, true>::maps(x, n, a, u, ma, mu);
+        else
+          Forward<T, G, false>::maps(x, n, a, u, ma, mu);
+      }
+      *reinterpret_cast<float4*>(&part[warp * kX + 2 * lane]) = make_float4(ma.x.x, mu.x.x, ma.x.y, mu.x.y);
+      bar_arrive(kReady, 32 * (kW + kFold));
+      release();
+      bar_sync(kStart, 32 * (kW + kFold));
+      Num<2> c;
+      c.x = *reinterpret_cast<const float2*>(&start[warp * kX + 2 * lane]);
+      if constexpr (BWD) {
+        Num<2> before;
+        const uint32_t sa = sm + st * C::STAGE + C::WX + C::DY + (warp * kX + 2 * lane) * 4;
+        before = get2<float>(sa);
+        if (n >= kS)
+          Backward<T, G, true>::results(x, dy, n, a, u, before, c);
+        else
+          Backward<T, G, false>::results(x, dy, n, a, u, before, c);
+      } else {
+        if (p.stash && on && n > 0) *reinterpret_cast<float2*>(stash + t0 / kS * ystep) = c.x;
+        if (n >= kS)
+          Forward<T, G, true>::results(x, n, a, u, c);
+        else
+          Forward<T, G, false>::results(x, n, a, u, c);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (t0 < p.T) tma_store_4d(&maps.out, c0, BWD ? head * G : head, b, t0, sm + st * C::STAGE + warp * kS * C::TOK);
+        bulk_commit();
+      }
+      prev = st;
+    }
+    // rows of zeros behind the last round: from a run's place in the first stage, which nothing uses any more
+    long long t = (long long)rounds * step + rank * kC + warp * kS;
+    if (t < p.T) {
+      if (lane == 0) bulk_wait_read_all();
+      __syncwarp();
+#pragma unroll
+      for (int s = 0; s < kS; ++s)
+#pragma unroll
+        for (int j = 0; j < (BWD ? G : 1); ++j) put2<T>(mine + (BWD ? s * C::TOK + j * C::ROW : s * C::ROW), Num<2>(0.f));
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        for (; t < p.T; t += step) tma_store_4d(&maps.out, c0, BWD ? head * G : head, b, (int)t, sm + warp * kS * C::TOK);
+        bulk_commit();
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  if (cs > 1) {
+    __syncthreads();
+    cluster_sync();
+    if (gave_up_s) {  // (maps that other CTAs sent after this one had given up land)
+      const uint64_t since = globaltimer_ns();
+      while (globaltimer_ns() - since < 100000ull) __nanosleep(1000);
+    }
+  }
+}
+
+}  // namespace
+
+// ------------------------------------------------------------- host side --
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();  // tc_gemm.cu
+
+namespace {
+
+// [T, B, heads, D] contiguous, boxes of `rows` tokens, `h` heads and 64 channels
+bool encode(CUtensorMap* map, const void* ptr, bool bf16, long long D, long long heads, long long B, long long T, uint32_t h,
+            uint32_t rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr || reinterpret_cast<uintptr_t>(ptr) % 16 != 0) return false;
+  const cuuint64_t es = bf16 ? 2 : 4, d = (cuuint64_t)D * es;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)B, (cuuint64_t)T};
+  const cuuint64_t strides[3] = {d, d * heads, d * heads * B};
+  const cuuint32_t box[4] = {kX, h, 1, rows}, ones[4] = {1, 1, 1, 1};
+  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void*>(ptr), dims,
+            strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T, int G, bool BWD>
+int launch_tile(GatedParams p, cudaStream_t s) {
+  using C = Tile<T, G, BWD>;
+  const bool bf16 = sizeof(T) == 2;
+  const long long NH = p.N / p.D;
+  TileMaps m;
+  bool ok = encode(&m.wx, p.wx, bf16, p.D, NH * G, p.B, p.T, G, kC);
+  if (BWD)
+    ok = ok && encode(&m.out, p.dwx, bf16, p.D, NH * G, p.B, p.T, G, kS) && encode(&m.dy, p.dy, bf16, p.D, NH, p.B, p.T, 1, kC) &&
+         encode(&m.stash, p.stash, false, p.D, NH, p.B, (p.T + kS - 1) / kS, 1, kW);
+  else
+    ok = ok && encode(&m.out, p.y, bf16, p.D, NH, p.B, p.T, 1, kS) && reinterpret_cast<uintptr_t>(p.stash) % 8 == 0;
+  if (!ok) return kGatedNoTile;
+  p.tiles = (int)(NH * ((p.D + kX - 1) / kX));
+  const long long tiles = (long long)p.tiles * p.B, want = 2LL * sm_count();
+  p.cs = 1;
+  while (p.cs < kGatedCluster && tiles * p.cs < want && p.cs * kC < p.T) p.cs *= 2;
+  if (tiles * p.cs > 0x7fffffff) return (int)cudaErrorInvalidConfiguration;
+  static int prep[64][5];
+  const int e = prepare_launch(prep, gated_tile_kernel<T, G, BWD>, C::smem(kGatedCluster), kThreads, p.cs);
+  if (e != 0) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * p.cs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::smem(p.cs);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.cs;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cs > 1 ? 2 : 1;
+  return (int)cudaLaunchKernelEx(&cfg, gated_tile_kernel<T, G, BWD>, (const GatedParams)p, (const TileMaps)m);
+}
+template <class T, int G>
+int launch_dir(const GatedParams& p, bool bwd, cudaStream_t s) {
+  return bwd ? launch_tile<T, G, true>(p, s) : launch_tile<T, G, false>(p, s);
+}
+template <class T>
+int launch_t(const GatedParams& p, int gates, bool bwd, cudaStream_t s) {
+  switch (gates) {
+    case 2: return launch_dir<T, 2>(p, bwd, s);
+    case 3: return launch_dir<T, 3>(p, bwd, s);
+    default: return launch_dir<T, 4>(p, bwd, s);
+  }
+}
+
+}  // namespace
+
+bool gated_takes_tiles(const GatedParams& p, bool bf16) { return p.D % (bf16 ? 8 : 4) == 0 && p.T >= kGatedTileTokens; }
+
+int launch_gated_tile(const GatedParams& p, int gates, bool bf16, bool bwd, cudaStream_t s) {
+  return bf16 ? launch_t<__nv_bfloat16>(p, gates, bwd, s) : launch_t<float>(p, gates, bwd, s);
+}
+
+}  // namespace srnn

@@ -160,8 +160,16 @@ struct GatedParams {
   float* dstate0;       // or null
   int T, B, N, D;       // N = NH D
   int tiles, cs;        // (launch) channel tiles of a row, CTAs of a cluster along time
+  int* status;
+  int withhold;         // test: no tile is brought (tile kernels)
+  unsigned long long timeout_ns;
 };
 int launch_gated(GatedParams p, int gates, bool bf16, bool bwd, cudaStream_t s);
+// the kernels on tiles: whether the sizes suit them; kGatedNoTile: addresses or strides have no tensor map
+constexpr int kGatedTileTokens = 32;
+constexpr int kGatedNoTile = -2;
+bool gated_takes_tiles(const GatedParams& p, bool bf16);
+int launch_gated_tile(const GatedParams& p, int gates, bool bf16, bool bwd, cudaStream_t s);
 struct GatedStepParams {
   const void* wx;    // [B, NH, gates D]
   const int* slots;  // [B] or null

@@ -21,7 +21,8 @@ size_t dtype_bytes(int32_t d) { return d == RNN_F32 ? 4 : 2; }
 int check_gated(const rnn_gated_desc_t* d) {
   if (d == nullptr || !valid_dtype(d->dtype)) return RNN_ERR_INVALID_ARG;
   if (d->T < 0 || d->B < 0 || d->NH < 0 || d->D <= 0) return RNN_ERR_INVALID_ARG;
-  if (d->gates < RNN_GATES_FZ || d->gates > RNN_GATES_IFZO) return RNN_ERR_INVALID_ARG;
+  if (d->gates < RNN_GATES_FZ || d->gates > RNN_GATES_IFZO || (d->flags & ~RNN_FLAG_TEST_TIMEOUT) != 0)
+    return RNN_ERR_INVALID_ARG;
   // tokens and channels are counted in 32 bits, up to a cluster's share past the end; a CTA for 32 channels
   const long long n = (long long)d->NH * d->D;
   if (d->T > (1 << 30) || n > (1 << 30) || (n + 31) / 32 * d->B > (1 << 27)) return RNN_ERR_UNSUPPORTED;
@@ -30,8 +31,11 @@ int check_gated(const rnn_gated_desc_t* d) {
 size_t stash_bytes(const rnn_gated_desc_t* d) {
   return (size_t)((d->T + kGatedRun - 1) / kGatedRun) * d->B * d->NH * d->D * sizeof(float);
 }
-GatedParams gated_params(const rnn_gated_desc_t* d, const void* Wx, const int32_t* lens) {
+GatedParams gated_params(const rnn_gated_desc_t* d, const void* Wx, const int32_t* lens, void* workspace) {
   GatedParams p{};
+  p.status = static_cast<int*>(workspace);
+  p.withhold = d->flags != 0;
+  p.timeout_ns = d->flags != 0 ? kTestTimeoutNs : kTimeoutNs;
   p.wx = Wx;
   p.lens = lens;
   p.T = d->T, p.B = d->B, p.N = d->NH * d->D, p.D = d->D;
@@ -92,40 +96,49 @@ extern "C" {
 size_t rnn_gated_stash_size(const rnn_gated_desc_t* d) { return check_gated(d) == RNN_OK ? stash_bytes(d) : 0; }
 
 int rnn_gated_fwd(const rnn_gated_desc_t* d, const void* Wx, const int32_t* lens, const float* state0, void* y,
-                  float* stateT, float* stash, void* stream) {
+                  float* stateT, float* stash, void* workspace, size_t workspace_bytes, void* stream) {
   const int e = check_gated(d);
   if (e != RNN_OK) return e;
-  if (d->B == 0 || d->NH == 0) return RNN_OK;
+  if (workspace == nullptr || workspace_bytes < kStatusBytes) return RNN_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return RNN_ERR_MISALIGNED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d->B == 0 || d->NH == 0) return clear_status(workspace, workspace_bytes, s);
   if (d->T > 0 && (Wx == nullptr || y == nullptr)) return RNN_ERR_INVALID_ARG;
   const size_t es = dtype_bytes(d->dtype);
   if (!aligned(Wx, es) || !aligned(y, es) || !aligned(lens, 4) || !aligned(state0, 4) || !aligned(stateT, 4) ||
       !aligned(stash, 4))
     return RNN_ERR_MISALIGNED;
-  GatedParams p = gated_params(d, Wx, lens);
+  GatedParams p = gated_params(d, Wx, lens, workspace);
+  if (d->flags != 0 && !gated_takes_tiles(p, d->dtype == RNN_BF16)) return RNN_ERR_UNSUPPORTED;
   p.state0 = state0, p.y = y, p.stateT = stateT, p.stash = stash;
-  return map_launch_error(launch_gated(p, d->gates, d->dtype == RNN_BF16, false, static_cast<cudaStream_t>(stream)));
+  return map_launch_error(launch_gated(p, d->gates, d->dtype == RNN_BF16, false, s));
 }
 
 int rnn_gated_bwd(const rnn_gated_desc_t* d, const void* Wx, const int32_t* lens, const float* stash, const void* dy,
-                  const float* dstateT, void* dWx, float* dstate0, void* stream) {
+                  const float* dstateT, void* dWx, float* dstate0, void* workspace, size_t workspace_bytes,
+                  void* stream) {
   const int e = check_gated(d);
   if (e != RNN_OK) return e;
-  if (d->B == 0 || d->NH == 0) return RNN_OK;
+  if (workspace == nullptr || workspace_bytes < kStatusBytes) return RNN_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return RNN_ERR_MISALIGNED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d->B == 0 || d->NH == 0) return clear_status(workspace, workspace_bytes, s);
   if (d->T > 0 && (Wx == nullptr || stash == nullptr || dy == nullptr || dWx == nullptr)) return RNN_ERR_INVALID_ARG;
   const size_t es = dtype_bytes(d->dtype);
   if (!aligned(Wx, es) || !aligned(dy, es) || !aligned(dWx, es) || !aligned(lens, 4) || !aligned(stash, 4) ||
       !aligned(dstateT, 4) || !aligned(dstate0, 4))
     return RNN_ERR_MISALIGNED;
-  GatedParams p = gated_params(d, Wx, lens);
+  GatedParams p = gated_params(d, Wx, lens, workspace);
+  if (d->flags != 0 && !gated_takes_tiles(p, d->dtype == RNN_BF16)) return RNN_ERR_UNSUPPORTED;
   p.stash = const_cast<float*>(stash), p.dy = dy, p.dstateT = dstateT, p.dwx = dWx, p.dstate0 = dstate0;
-  return map_launch_error(launch_gated(p, d->gates, d->dtype == RNN_BF16, true, static_cast<cudaStream_t>(stream)));
+  return map_launch_error(launch_gated(p, d->gates, d->dtype == RNN_BF16, true, s));
 }
 
 int rnn_gated_step(const rnn_gated_desc_t* d, const void* Wx, const int32_t* slots, int32_t n_slots, float* state,
                    void* y, void* stream) {
   const int e = check_gated(d);
   if (e != RNN_OK) return e;
-  if (n_slots < 0 || d->T != 1) return RNN_ERR_INVALID_ARG;
+  if (n_slots < 0 || d->T != 1 || d->flags != 0) return RNN_ERR_INVALID_ARG;
   if (d->B == 0 || d->NH == 0) return RNN_OK;
   if (slots == nullptr && n_slots < d->B) return RNN_ERR_INVALID_ARG;
   if (Wx == nullptr || y == nullptr || (state == nullptr && n_slots > 0)) return RNN_ERR_INVALID_ARG;

@@ -158,14 +158,16 @@ def rnn_gated_stash_size(desc) -> int:
     return int(_lib.load().rnn_gated_stash_size(ctypes.byref(desc)))
 
 
-def rnn_gated_fwd(desc, Wx, lens, state0, y, stateT, stash, stream=None) -> int:
+def rnn_gated_fwd(desc, Wx, lens, state0, y, stateT, stash, workspace, stream=None) -> int:
     return _lib.load().rnn_gated_fwd(ctypes.byref(desc), _at(Wx), _at(lens), _at(state0), _at(y),
-                                     _at(stateT), _at(stash), _handle(stream))
+                                     _at(stateT), _at(stash), _at(workspace),
+                                     workspace.nbytes if workspace is not None else 0, _handle(stream))
 
 
-def rnn_gated_bwd(desc, Wx, lens, stash, dy, dstateT, dWx, dstate0, stream=None) -> int:
+def rnn_gated_bwd(desc, Wx, lens, stash, dy, dstateT, dWx, dstate0, workspace, stream=None) -> int:
     return _lib.load().rnn_gated_bwd(ctypes.byref(desc), _at(Wx), _at(lens), _at(stash), _at(dy),
-                                     _at(dstateT), _at(dWx), _at(dstate0), _handle(stream))
+                                     _at(dstateT), _at(dWx), _at(dstate0), _at(workspace),
+                                     workspace.nbytes if workspace is not None else 0, _handle(stream))
 
 
 def rnn_gated_step(desc, Wx, slots, n_slots, state, y, stream=None) -> int:
@@ -320,7 +322,7 @@ def linear_attention_step(q, k, v, log_decay, state, *, slots=None, scale=None, 
 
 
 # ---------------------------------------------- gated linear recurrence --
-def gated_recurrence(Wx, *, gates="fz", state=None, lens=None, train=False, stream=None):
+def gated_recurrence(Wx, *, gates="fz", state=None, lens=None, train=False, check=True, stream=None):
     """The cells without a recurrent matrix through rnn_gated_fwd, a scan over the sequence:
 
         "fz"    c_t = sigm(f) c_{t-1} + sigm(-f) z     y_t = c_t
@@ -329,27 +331,31 @@ def gated_recurrence(Wx, *, gates="fz", state=None, lens=None, train=False, stre
 
     Wx [T, B, NH, G*D] bf16 or fp32, gate-major in the order of ``gates`` (as ``forward``'s,
     contiguous), state [B, NH, D] fp32 or None, lens [B] int32 or None (tokens of each row that
-    count).  Returns ``y`` [T, B, NH, D], ``state`` (after the last token) and with ``train`` the
-    ``stash`` that ``gated_recurrence_backward`` takes.
+    count).  Returns ``y`` [T, B, NH, D], ``state`` (after the last token), the ``workspace`` and with
+    ``train`` the ``stash`` that ``gated_recurrence_backward`` takes.
     """
     if stream is not None:
         with _on(stream):
-            return gated_recurrence(Wx, gates=gates, state=state, lens=lens, train=train)
+            return gated_recurrence(Wx, gates=gates, state=state, lens=lens, train=train, check=check)
     out = (_native or _load()).gated_recurrence(Wx, gates, state, lens, train)
     if type(out) is int:
         _raise(out, "rnn_gated_fwd")
+    if check:
+        _read(out["workspace"], "rnn_gated_fwd")
     return out
 
 
-def gated_recurrence_backward(Wx, stash, dy, *, gates="fz", dstate=None, lens=None, stream=None):
+def gated_recurrence_backward(Wx, stash, dy, *, gates="fz", dstate=None, lens=None, check=True, stream=None):
     """Gradients of ``gated_recurrence`` from its Wx, gates, lens and ``stash``, dy [T, B, NH, D] and
     ``dstate`` (of the final state, or None): ``dWx`` and ``dstate`` (of the initial state)."""
     if stream is not None:
         with _on(stream):
-            return gated_recurrence_backward(Wx, stash, dy, gates=gates, dstate=dstate, lens=lens)
+            return gated_recurrence_backward(Wx, stash, dy, gates=gates, dstate=dstate, lens=lens, check=check)
     out = (_native or _load()).gated_recurrence_backward(Wx, stash, dy, gates, dstate, lens)
     if type(out) is int:
         _raise(out, "rnn_gated_bwd")
+    if check:
+        _read(out["workspace"], "rnn_gated_bwd")
     return out
 
 

@@ -68,7 +68,8 @@ def check(S, T, B, NH, D, gates, dtype, lens=None, state=True, seed=0):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("gates", ["fz", "fzo", "ifzo"])
 @pytest.mark.parametrize("T,B,NH,D", [(1, 1, 1, 1), (0, 2, 3, 8), (7, 2, 2, 33), (8, 3, 1, 64), (9, 1, 5, 40), (64, 2, 2, 32),
-                                      (65, 1, 1, 130), (200, 3, 2, 31), (1100, 2, 3, 64), (700, 1, 1, 6)])
+                                      (65, 1, 1, 130), (200, 3, 2, 31), (1100, 2, 3, 64), (700, 1, 1, 6),
+                                      (32, 2, 2, 8), (100, 4, 3, 136), (2500, 1, 1, 48), (257, 30, 8, 72)])
 def test_shapes(S, T, B, NH, D, gates, dtype):
     check(S, T, B, NH, D, gates, dtype, seed=T + D)
 
@@ -201,20 +202,21 @@ def test_in_place_states_and_streams(S):
     Wx, s0, dy, ds = inputs(T, B, NH, D, "fzo", "bf16")
     want = S.gated_recurrence(Wx, gates="fzo", state=s0, train=True)
     from sequential_rnn_gb300._lib import rnn_gated_desc_t
-    d = rnn_gated_desc_t(1, T, B, NH, D, 3)
+    d = rnn_gated_desc_t(1, T, B, NH, D, 3, 0)
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")  # (a call clears its status word)
     y, st = torch.empty_like(want["y"]), s0.clone()
-    assert S.rnn_gated_fwd(d, Wx, None, st, y, st, None) == 0
+    assert S.rnn_gated_fwd(d, Wx, None, st, y, st, None, ws) == 0 and S.rnn_read_status(ws) == 0
     assert torch.equal(y, want["y"]) and torch.equal(st, want["state"])
     g = S.gated_recurrence_backward(Wx, want["stash"], dy, gates="fzo", dstate=ds)
     dW, dst = torch.empty_like(Wx), ds.clone()
-    assert S.rnn_gated_bwd(d, Wx, None, want["stash"], dy, dst, dW, dst) == 0
+    assert S.rnn_gated_bwd(d, Wx, None, want["stash"], dy, dst, dW, dst, ws) == 0 and S.rnn_read_status(ws) == 0
     assert torch.equal(dW, g["dWx"]) and torch.equal(dst, g["dstate"])
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     out = S.gated_recurrence(Wx, gates="fzo", state=s0, stream=side)
     side.synchronize()
     assert torch.equal(out["y"], want["y"])
-    assert ctypes.sizeof(rnn_gated_desc_t) == 24
+    assert ctypes.sizeof(rnn_gated_desc_t) == 28
 
 
 def test_captured_calls(S):
@@ -224,8 +226,8 @@ def test_captured_calls(S):
     cache = s0.clone()
 
     def step():
-        o = S.gated_recurrence(Wx, gates="ifzo", state=s0, train=True)
-        g = S.gated_recurrence_backward(Wx, o["stash"], dy, gates="ifzo", dstate=ds)
+        o = S.gated_recurrence(Wx, gates="ifzo", state=s0, train=True, check=False)
+        g = S.gated_recurrence_backward(Wx, o["stash"], dy, gates="ifzo", dstate=ds, check=False)
         return o["y"], g["dWx"], g["dstate"], S.gated_recurrence_step(Wx[0], cache, gates="ifzo")
 
     side = torch.cuda.Stream()
@@ -247,6 +249,23 @@ def test_captured_calls(S):
     for a, b in zip(got, step()):
         assert torch.equal(a, b)
     assert torch.equal(first, cache)
+
+
+@pytest.mark.parametrize("B", [1, 40])  # a cluster for each tile, and a CTA
+def test_an_expired_wait_is_reported(S, B):
+    """RNN_FLAG_TEST_TIMEOUT: no tile is brought, every wait runs out after 50 ms; the next call is fine."""
+    from sequential_rnn_gb300._lib import RNN_FLAG_TEST_TIMEOUT, rnn_gated_desc_t
+    T, NH, D = 1000, 12, 64
+    Wx, s0, dy, ds = inputs(T, B, NH, D, "fz", "bf16")
+    want = S.gated_recurrence(Wx, state=s0, train=True)
+    d = rnn_gated_desc_t(1, T, B, NH, D, 2, RNN_FLAG_TEST_TIMEOUT)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    y, dW, st = torch.empty_like(want["y"]), torch.empty_like(Wx), torch.empty_like(s0)
+    assert S.rnn_gated_fwd(d, Wx, None, s0, y, st, None, ws) == 0 and S.rnn_read_status(ws) == 5
+    assert S.rnn_gated_bwd(d, Wx, None, want["stash"], dy, ds, dW, st, ws) == 0 and S.rnn_read_status(ws) == 5
+    again = S.gated_recurrence(Wx, state=s0, train=True)
+    for k in ("y", "state", "stash"):
+        assert torch.equal(again[k], want[k])
 
 
 def test_refusals(S):

@@ -19,12 +19,12 @@ def lib():
 
 def gdesc(**kw):
     from sequential_rnn_gb300._lib import rnn_gated_desc_t
-    d = dict(dtype=1, T=8, B=2, NH=2, D=64, gates=2)
+    d = dict(dtype=1, T=8, B=2, NH=2, D=64, gates=2, flags=0)
     d.update(kw)
     return rnn_gated_desc_t(**d)
 
 
-def gated(lib, call, desc=None, n_slots=2, **ptr):
+def gated(lib, call, desc=None, n_slots=2, nbytes=256, ws=W, **ptr):
     d = ctypes.byref(desc or gdesc(T=1 if call == "step" else 8))
     names = {"fwd": ("Wx", "lens", "s0", "y", "sT", "stash"),
              "bwd": ("Wx", "lens", "stash", "dy", "dsT", "dWx", "ds0"), "step": ("Wx", "slots", "state", "y")}[call]
@@ -33,12 +33,14 @@ def gated(lib, call, desc=None, n_slots=2, **ptr):
     a = [P(p[n]) for n in names]
     if call == "step":
         a.insert(2, n_slots)
+    else:
+        a += [P(ws), nbytes]
     return getattr(lib, "rnn_gated_" + call)(d, *a, None)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=2), 1), (dict(T=-1), 1), (dict(B=-1), 1), (dict(NH=-1), 1), (dict(D=0), 1), (dict(gates=1), 1),
-    (dict(gates=5), 1), (dict(T=(1 << 30) + 1), 2), (dict(NH=1 << 20, D=1 << 11), 2),
+    (dict(gates=5), 1), (dict(flags=1), 1), (dict(T=(1 << 30) + 1), 2), (dict(NH=1 << 20, D=1 << 11), 2),
     (dict(B=1 << 24, NH=16, D=64), 2),
 ])
 def test_gated_descriptors(lib, kw, status):
@@ -59,8 +61,13 @@ def test_gated_null_and_misaligned(lib):
     assert gated(lib, "fwd", gdesc(dtype=0), Wx=A + 2) == 3
     assert gated(lib, "step", slots=A + 2) == 3
     assert gated(lib, "step", gdesc(T=2)) == gated(lib, "step", n_slots=1) == gated(lib, "step", n_slots=-1) == 1
-    for call in ("fwd", "bwd"):  # nothing to do
-        assert gated(lib, call, gdesc(B=0), Wx=0, y=0) == gated(lib, call, gdesc(NH=0), Wx=0) == 0
+    assert gated(lib, "step", gdesc(T=1, flags=1 << 30)) == 1
+    for call in ("fwd", "bwd"):
+        assert gated(lib, call, ws=0) == gated(lib, call, nbytes=128) == 1 and gated(lib, call, ws=W + 16) == 3
+        assert gated(lib, call, gdesc(B=0), ws=W + 16, Wx=0) == 3  # the status word is still checked
+        for kw in (dict(T=31), dict(T=100, D=36), dict(T=100, D=6, dtype=0)):  # sizes whose kernels do not wait
+            assert gated(lib, call, gdesc(flags=1 << 30, **kw)) == 2
+    assert gated(lib, "step", gdesc(T=1, B=0), Wx=0, y=0) == gated(lib, "step", gdesc(T=1, NH=0), Wx=0) == 0
     assert lib.rnn_gated_stash_size(ctypes.byref(gdesc(T=17, B=3, NH=2, D=5))) == 3 * 3 * 2 * 5 * 4
     assert lib.rnn_gated_stash_size(ctypes.byref(gdesc(T=0))) == 0
 
