@@ -3,9 +3,9 @@
 //
 // A CTA takes 64 channels of a head of one row, and goes through time in rounds of 64 tokens; the CTAs of a cluster take
 // neighbouring rounds at once.  A control warp keeps a ring of tiles [64 tokens][gates][64 channels] filled.  Eight warps
-// take a run of 8 tokens each: gates and the run's map c -> A c + U in registers, the map handed to 64 threads of two
-// more warps, one for each channel, which compose the maps in the order of time -- those of the cluster's CTAs after
-// exchanging them by st.async -- and hand every run the state at its start; then the run once more, its results written into
+// take a run of 8 tokens each: gates and the run's map c -> A c + U in registers, the map handed to
+// one more warp, which composes the maps in the order of time -- those of the cluster's CTAs after
+// exchanging them by st.async -- and hands every run the state at its start; then the run once more, its results written into
 // the tile it came from, from where TMA stores them.  Nothing is read twice and no thread forms an address per token.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -23,10 +23,24 @@ namespace srnn {
 namespace {
 
 constexpr int kS = kRunTokens, kW = kRunWarps, kC = kRunChunk, kX = 64;  // channels of a tile
-constexpr int kFold = 2;                        // warps that compose the maps
-constexpr int kThreads = 32 * (kW + kFold + 1);
+constexpr int kThreads = 32 * (kW + 2);
+constexpr int kTalk = 32 * (kW + 1);            // threads of the runs and of the maps
 constexpr int kReady = 1, kStart = 2;           // named barriers: maps there, starts there
-constexpr uint32_t kMapBytes = kX * sizeof(Map);
+constexpr uint32_t kMapBytes = kX * 8;
+// c -> a c + u of two neighbouring channels, as 16 bytes of shared memory
+struct Map2 {
+  Num<2> a, u;
+};
+__device__ __forceinline__ void put(float4* at, const Num<2>& a, const Num<2>& u) {
+  *at = make_float4(a.x.x, a.x.y, u.x.x, u.x.y);
+}
+__device__ __forceinline__ Map2 get(const float4* at) {
+  const float4 v = *at;
+  Map2 m;
+  m.a.x = make_float2(v.x, v.y);
+  m.u.x = make_float2(v.z, v.w);
+  return m;
+}
 
 struct TileMaps {
   CUtensorMap wx;                 // [T, B, NH G, D], box [64, 1, G, 64]
@@ -39,7 +53,10 @@ struct Tile {
   static constexpr uint32_t ROW = kX * sizeof(T), TOK = G * ROW;
   static constexpr uint32_t WX = kC * TOK, DY = BWD ? kC * ROW : 0, ST = BWD ? kW * kX * 4 : 0;
   static constexpr uint32_t STAGE = WX + DY + ST;
-  static constexpr int STAGES = STAGE <= 24 * 1024 ? 3 : STAGE <= 64 * 1024 ? 3 : 2;
+  // CTAs of an SM, as registers (64 for three, 96 for two) and shared memory allow
+  static constexpr int CTAS = !BWD && sizeof(T) == 2 ? 3 : STAGE <= 50 * 1024 ? 2 : 1;
+  static constexpr uint32_t REST = kW * kMapBytes + kW * kX * 4 + 256 + 128 + 2048;
+  static constexpr int FIT = (int)((224 * 1024 / CTAS - REST) / STAGE), STAGES = FIT > 3 ? 3 : FIT;
   static constexpr uint32_t PART = STAGES * STAGE, START = PART + kW * kMapBytes, BARS = START + kW * kX * 4,
                             ALL = BARS + 256;
   static constexpr uint32_t smem(int cs) { return ALL + (cs > 1 ? 2 * cs * kMapBytes : 0) + 128; }
@@ -106,11 +123,6 @@ __device__ __forceinline__ void put2<__nv_bfloat16>(uint32_t at, const Num<2>& a
 template <>
 __device__ __forceinline__ void put2<float>(uint32_t at, const Num<2>& a) {
   asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(a.x.x), "f"(a.x.y) : "memory");
-}
-__device__ __forceinline__ void st_async_map(uint32_t raddr, const Map& m, uint32_t rbar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(raddr),
-               "r"(__float_as_uint(m.a)), "r"(__float_as_uint(m.u)), "r"(rbar)
-               : "memory");
 }
 
 // One run of a round, forward: maps first, results second.  FULL: all its tokens count (else the first n do).
@@ -195,16 +207,16 @@ struct Backward {
 };
 
 template <class T, int G, bool BWD>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && G == 2 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, Tile<T, G, BWD>::CTAS)
     gated_tile_kernel(const GatedParams p, const __grid_constant__ TileMaps maps) {
   using C = Tile<T, G, BWD>;
   extern __shared__ char dyn[];
   __shared__ int gave_up_s;
   const uint32_t sm = (smem_u32(dyn) + 127u) & ~127u;
   char* const sp = dyn + (sm - smem_u32(dyn));
-  Map* const part = reinterpret_cast<Map*>(sp + C::PART);        // [kW][kX]
-  float* const start = reinterpret_cast<float*>(sp + C::START);  // [kW][kX]
-  Map* const all = reinterpret_cast<Map*>(sp + C::ALL);          // [2][cs][kX]
+  float4* const part = reinterpret_cast<float4*>(sp + C::PART);    // maps of the runs: [kW][32 pairs of channels]
+  float2* const start = reinterpret_cast<float2*>(sp + C::START);  // states before them: the same
+  float4* const all = reinterpret_cast<float4*>(sp + C::ALL);      // maps of the CTAs: [2][cs][32]
   const uint32_t full = sm + C::BARS, empty = full + 8 * C::STAGES, swap = empty + 8 * C::STAGES;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, cs = p.cs;
   const int rank = (int)(blockIdx.x % cs);
@@ -230,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && G == 2 ? 2 : 1)
   if (cs > 1) cluster_sync();  // every CTA's barriers are there
   auto round_of = [&](int i) { return BWD ? rounds - 1 - i : i; };
 
-  if (warp == kW + kFold) {  // ---- copies
+  if (warp == kW + 1) {  // ---- copies
     if (lane == 0) {
       tma_prefetch_map(&maps.wx);
       tma_prefetch_map(&maps.out);
@@ -256,48 +268,53 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && G == 2 ? 2 : 1)
         }
     }
     __syncwarp();
-  } else if (warp >= kW) {  // ---- maps: a thread for each channel
-    const int c = threadIdx.x - 32 * kW;
-    const long long at = c0 + c < p.D ? (long long)b * p.N + (long long)head * p.D + c0 + c : -1;
+  } else if (warp == kW) {  // ---- maps: two channels a thread
     const float* from = BWD ? p.dstateT : p.state0;
-    float h = from && at >= 0 ? from[at] : 0.f;
+    float* const to = BWD ? p.dstate0 : p.stateT;
+    const int c = c0 + 2 * lane;  // (D is even)
+    const long long at = (long long)b * p.N + (long long)head * p.D + c;
+    Num<2> h(0.f);
+    if (from && c < p.D) h.x = make_float2(from[at], from[at + 1]);
     for (int i = 0; i < rounds; ++i) {
-      bar_sync(kReady, 32 * (kW + kFold));
-      Map m[kW];
+      bar_sync(kReady, kTalk);
+      Map2 m[kW];
 #pragma unroll
-      for (int w = 0; w < kW; ++w) m[w] = part[(BWD ? kW - 1 - w : w) * kX + c];
-      float in = h;
+      for (int w = 0; w < kW; ++w) m[w] = get(part + (BWD ? kW - 1 - w : w) * 32 + lane);
+      Num<2> in = h;
       if (cs > 1) {
-        Map t = m[0];
+        Map2 t = m[0];
 #pragma unroll
         for (int w = 1; w < kW; ++w) {
-          t.u = fmaf(m[w].a, t.u, m[w].u);
-          t.a *= m[w].a;
+          t.u = fma(m[w].a, t.u, m[w].u);
+          t.a = m[w].a * t.a;
         }
-        const uint32_t bar = swap + 8 * (i & 1), to = smem_u32(&all[((i & 1) * cs + rank) * kX + c]);
+        const uint32_t bar = swap + 8 * (i & 1), slot = smem_u32(&all[((i & 1) * cs + rank) * 32 + lane]);
+        const uint32_t v[4] = {__float_as_uint(t.a.x.x), __float_as_uint(t.a.x.y), __float_as_uint(t.u.x.x),
+                               __float_as_uint(t.u.x.y)};
         if (!gave_up_s) {
-          if (c == 0) mbar_arrive_expect_tx(bar, cs * kMapBytes);
+          if (lane == 0) mbar_arrive_expect_tx(bar, cs * kMapBytes);
           // (a CTA sends round i + 2 after it has round i + 1 from this one, which has then read round i)
-          for (int r = 0; r < cs; ++r) st_async_map(mapa(to, (uint32_t)r), t, mapa(bar, (uint32_t)r));
+          for (int r = 0; r < cs; ++r) st_async_v4(mapa(slot, (uint32_t)r), v, mapa(bar, (uint32_t)r));
           wait.on<true>(bar, (i >> 1) & 1);
         }
-        const Map* x = all + (i & 1) * cs * kX + c;
+        const float4* x = all + (i & 1) * cs * 32 + lane;
+#pragma unroll 4
         for (int j = 0; j < cs; ++j) {
           const int r = BWD ? cs - 1 - j : j;
+          const Map2 y = get(x + r * 32);
           if (r == rank) in = h;
-          h = fmaf(x[r * kX].a, h, x[r * kX].u);
+          h = fma(y.a, h, y.u);
         }
       }
 #pragma unroll
       for (int w = 0; w < kW; ++w) {
-        start[(BWD ? kW - 1 - w : w) * kX + c] = in;
-        in = fmaf(m[w].a, in, m[w].u);
+        start[(BWD ? kW - 1 - w : w) * 32 + lane] = in.x;
+        in = fma(m[w].a, in, m[w].u);
       }
       if (cs == 1) h = in;
-      bar_arrive(kStart, 32 * (kW + kFold));
+      bar_arrive(kStart, kTalk);
     }
-    float* const to = BWD ? p.dstate0 : p.stateT;
-    if (to && rank == 0 && at >= 0) to[at] = h;
+    if (to && rank == 0 && c < p.D) to[at] = h.x.x, to[at + 1] = h.x.y;
   } else {  // ---- runs
     const uint32_t mine = sm + warp * kS * C::TOK + lane * 2 * sizeof(T);
     const long long ystep = (long long)p.B * p.N;
@@ -326,12 +343,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && G == 2 ? 2 : 1)
         else
           Forward<T, G, false>::maps(x, n, a, u, ma, mu);
       }
-      *reinterpret_cast<float4*>(&part[warp * kX + 2 * lane]) = make_float4(ma.x.x, mu.x.x, ma.x.y, mu.x.y);
-      bar_arrive(kReady, 32 * (kW + kFold));
+      put(part + warp * 32 + lane, ma, mu);
+      bar_arrive(kReady, kTalk);
       release();
-      bar_sync(kStart, 32 * (kW + kFold));
+      bar_sync(kStart, kTalk);
       Num<2> c;
-      c.x = *reinterpret_cast<const float2*>(&start[warp * kX + 2 * lane]);
+      c.x = start[warp * 32 + lane];
       if constexpr (BWD) {
         Num<2> before;
         const uint32_t sa = sm + st * C::STAGE + C::WX + C::DY + (warp * kX + 2 * lane) * 4;
@@ -421,9 +438,9 @@ int launch_tile(GatedParams p, cudaStream_t s) {
     ok = ok && encode(&m.out, p.y, bf16, p.D, NH, p.B, p.T, 1, kS) && reinterpret_cast<uintptr_t>(p.stash) % 8 == 0;
   if (!ok) return kGatedNoTile;
   p.tiles = (int)(NH * ((p.D + kX - 1) / kX));
-  const long long tiles = (long long)p.tiles * p.B, want = 2LL * sm_count();
+  const long long tiles = (long long)p.tiles * p.B, room = (long long)C::CTAS * sm_count();
   p.cs = 1;
-  while (p.cs < kGatedCluster && tiles * p.cs < want && p.cs * kC < p.T) p.cs *= 2;
+  while (p.cs < kGatedCluster && 2 * tiles * p.cs <= room && p.cs * kC < p.T) p.cs *= 2;
   if (tiles * p.cs > 0x7fffffff) return (int)cudaErrorInvalidConfiguration;
   static int prep[64][5];
   const int e = prepare_launch(prep, gated_tile_kernel<T, G, BWD>, C::smem(kGatedCluster), kThreads, p.cs);
@@ -431,7 +448,10 @@ int launch_tile(GatedParams p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * p.cs));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::smem(p.cs);
+  // few CTAs: shared memory asked for so that the SMs share them out evenly (a cluster's would pack three to an SM)
+  const uint32_t each = (uint32_t)((tiles * p.cs + sm_count() - 1) / sm_count());
+  const uint32_t spread = each < (uint32_t)C::CTAS ? 226 * 1024 / (each + 1) + 1024 : 0;
+  cfg.dynamicSmemBytes = spread > C::smem(p.cs) ? spread : C::smem(p.cs);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
