@@ -19,6 +19,7 @@
 
 #include "kernels.h"
 #include "lm.h"
+#include "num.cuh"
 #include "ptx.cuh"
 
 namespace srnn {
@@ -27,7 +28,7 @@ namespace {
 // 2^64 turns of a frequency in radians: f / (2 pi) in two doubles, the whole turns dropped
 __device__ __forceinline__ unsigned long long turns(double f) {
   constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;  // 1 / (2 pi) and the rest of it
-  const double hi = f * kHi, lo = fma(f, kHi, -hi) + f * kLo;
+  const double hi = f * kHi, lo = ::fma(f, kHi, -hi) + f * kLo;
   const double frac = hi - rint(hi);  // exact, in [-1/2, 1/2]
   // (1/2 is 2^63, which wraps round to the same angle as -2^63)
   const long long a = frac == 0.5 ? (long long)(1ull << 63) : __double2ll_rn(frac * 0x1p64);
@@ -44,87 +45,206 @@ __device__ __forceinline__ float get1(const __nv_bfloat16* p) { return __bfloat1
 __device__ __forceinline__ void put1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// four neighbouring columns
-struct Bf4 {
-  uint2 v;
-  __device__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint2*>(p); }
-  __device__ void get(float* x) const { x[0] = bf16_lo(v.x), x[1] = bf16_hi(v.x), x[2] = bf16_lo(v.y), x[3] = bf16_hi(v.y); }
-  static __device__ void store(__nv_bfloat16* p, const float* x) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-  }
-};
-struct F4 {
-  float4 v;
-  __device__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
-  __device__ void get(float* x) const { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; }
-  static __device__ void store(float* p, const float* x) { *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]); }
-};
-template <class T>
-struct Vec;
-template <>
-struct Vec<__nv_bfloat16> { typedef Bf4 type; };
-template <>
-struct Vec<float> { typedef F4 type; };
-
 __device__ __forceinline__ long long position(const RotaryParams& p, unsigned t, unsigned b) {
   if (p.positions == nullptr) return t;
   return p.per_token ? p.positions[(long long)t * p.B + b] : (long long)p.positions[b] + t;
 }
 
-// A head's columns among LPH lanes: lane l of them holds two pieces of four columns at a0, a1 (l: valid where a0 >= 0)
-// whose values are pairs: (x[i], x[4 + i]) or, INTER, (x[2 i], x[2 i + 1]).
-template <int LPH, bool INTER>
+// A head among LPH lanes, four pairs of columns each: how a lane reaches them.
+//   kHalf   pairs (j, j + rot / 2): two pieces of four neighbouring columns (past rot, two of what is not turned)
+//   kNext   pairs (2 j, 2 j + 1): eight neighbouring columns
+//   kAny    either, pairs LPH apart, value by value: sizes and addresses that are no multiples of four values
+enum : int { kHalf = 0, kNext = 1, kAny = 2 };
+
+template <class T, int MODE>
+struct Head;  // a lane's raw values
+template <>
+struct Head<__nv_bfloat16, kHalf> {
+  uint2 a, b;
+};
+template <>
+struct Head<__nv_bfloat16, kNext> {
+  uint2 a, b;
+};
+template <>
+struct Head<float, kHalf> {
+  float4 a, b;
+};
+template <>
+struct Head<float, kNext> {
+  float4 a, b;
+};
+template <class T>
+struct Head<T, kAny> {
+  T a[4], b[4];
+};
+
+// two pairs' first values, and their second ones; twice
+struct Pairs {
+  Num<2> a[2], b[2];
+};
+
+template <int LPH, int MODE>
 struct Lanes {
-  int l, sub, a0, a1, j0;  // lane within the head, the warp's head of it, columns, first pair's frequency (-1: not turned)
+  int l, sub;    // lane of the head, the warp's head of it
+  int a0, gap;   // vector forms: first column, from the first piece to the second
+  int half, D;
+  bool inter, on;
   __device__ explicit Lanes(const RotaryParams& p) {
     const int lane = threadIdx.x % 32;
     l = lane % LPH, sub = lane / LPH;
-    const int c = 4 * l, half = p.rot / 2;
-    if (INTER) {
-      a0 = 2 * c, a1 = a0 + 4;
-      j0 = 2 * c < p.rot ? c : -1;  // (the last one may be turned in part)
-    } else if (c < half) {
-      a0 = c, a1 = c + half, j0 = c;
+    half = p.rot / 2, D = p.D, inter = p.interleaved;
+    a0 = 0, gap = 4;
+    on = 8 * l < D;
+    if (MODE == kNext) {
+      a0 = 8 * l;
+    } else if (MODE == kHalf) {
+      if (4 * l < half)
+        a0 = 4 * l, gap = half;
+      else
+        a0 = 4 * l + half, gap = (D - 2 * half) / 2;
     } else {
-      a0 = p.rot + c - half, a1 = a0 + (p.D - p.rot) / 2, j0 = -1;
+      on = l < D / 2;
     }
-    if (2 * c >= p.D) a0 = -1, j0 = -1;
+    if (!on && MODE != kAny) a0 = 0;
   }
-};
-// frequencies that this lane computes: its pairs are shared out among the lanes of the other heads
-template <int LPH>
-struct Freqs {
-  static constexpr int kHeads = 32 / LPH, kN = kHeads >= 4 ? 1 : 4 / kHeads;
-  unsigned long long f[kN];
-  template <class L>
-  __device__ void load(const RotaryParams& p, const L& w) {
+  // index of the lane's pair i; pairs below `half` turn
+  __device__ int pair(int i) const { return MODE == kAny ? l + LPH * i : 4 * l + i; }
+  __device__ void columns(int i, int& a, int& b) const {  // kAny
+    const int j = pair(i);
+    if (inter)
+      a = 2 * j, b = a + 1;
+    else if (j < half)
+      a = j, b = j + half;
+    else
+      a = j + half, b = a + D / 2 - half;
+  }
+  template <class T>
+  __device__ void load(Head<T, MODE>& h, const T* x) const {
+    if constexpr (MODE == kAny) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int j = w.j0 + (w.sub * kN + i) % 4;
-      f[i] = w.j0 >= 0 && j < p.rot / 2 ? turns(p.freqs[j]) : 0ull;
+      for (int i = 0; i < 4; ++i) {
+        int a, b;
+        columns(i, a, b);
+        const bool in = pair(i) < D / 2;
+        h.a[i] = in ? x[a] : T(0.f);
+        h.b[i] = in ? x[b] : T(0.f);
+      }
+    } else {
+      h.a = *reinterpret_cast<const decltype(h.a)*>(x + a0);
+      h.b = *reinterpret_cast<const decltype(h.b)*>(x + a0 + gap);
     }
   }
-  template <class L>
-  __device__ void at(const L& w, long long pos, float (&c)[4], float (&s)[4]) const {
-    float cc[kN], ss[kN];
+  template <class T>
+  __device__ Pairs get(const Head<T, MODE>& h) const {
+    Pairs r;
+    float v[8];
+    if constexpr (MODE == kAny) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) turn(f[i], pos, cc[i], ss[i]);
+      for (int i = 0; i < 4; ++i) v[i] = get1(&h.a[i]), v[4 + i] = get1(&h.b[i]);
+    } else {
+      float y[8];
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t w[4] = {h.a.x, h.a.y, h.b.x, h.b.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[2 * i] = bf16_lo(w[i]), y[2 * i + 1] = bf16_hi(w[i]);
+      } else {
+        y[0] = h.a.x, y[1] = h.a.y, y[2] = h.a.z, y[3] = h.a.w, y[4] = h.b.x, y[5] = h.b.y, y[6] = h.b.z, y[7] = h.b.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = y[MODE == kNext ? 2 * i : i], v[4 + i] = y[MODE == kNext ? 2 * i + 1 : 4 + i];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r.a[i].x = make_float2(v[2 * i], v[2 * i + 1]), r.b[i].x = make_float2(v[4 + 2 * i], v[5 + 2 * i]);
+    return r;
+  }
+  template <class T>
+  __device__ void store(T* x, const Pairs& r) const {
+    const float a[4] = {r.a[0].x.x, r.a[0].x.y, r.a[1].x.x, r.a[1].x.y};
+    const float b[4] = {r.b[0].x.x, r.b[0].x.y, r.b[1].x.x, r.b[1].x.y};
+    if constexpr (MODE == kAny) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int ia, ib;
+        columns(i, ia, ib);
+        if (pair(i) < D / 2) put1(x + ia, a[i]), put1(x + ib, b[i]);
+      }
+    } else {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[MODE == kNext ? 2 * i : i] = a[i], y[MODE == kNext ? 2 * i + 1 : 4 + i] = b[i];
+      if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint2*>(x + a0) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+        *reinterpret_cast<uint2*>(x + a0 + gap) = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+      } else {
+        *reinterpret_cast<float4*>(x + a0) = make_float4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<float4*>(x + a0 + gap) = make_float4(y[4], y[5], y[6], y[7]);
+      }
+    }
+  }
+  // the lane's values of a [D] vector of fp32 numbers (null, or no column: 1)
+  __device__ Pairs weights(const float* w) const {
+    Pairs r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      c[i] = __shfl_sync(0xffffffffu, cc[i % kN], w.l + LPH * (i / kN));
-      s[i] = __shfl_sync(0xffffffffu, ss[i % kN], w.l + LPH * (i / kN));
+      int a, b;
+      if (MODE == kAny)
+        columns(i, a, b);
+      else
+        a = MODE == kNext ? a0 + 2 * i : a0 + i, b = MODE == kNext ? a + 1 : a + gap;
+      const bool in = w && on && pair(i) < D / 2;
+      r.a[i / 2].set(i % 2, in ? w[a] : 1.f);
+      r.b[i / 2].set(i % 2, in ? w[b] : 1.f);
+    }
+    return r;
+  }
+  __device__ void add_to(float* sum, const Pairs& r) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int a, b;
+      if (MODE == kAny)
+        columns(i, a, b);
+      else
+        a = MODE == kNext ? a0 + 2 * i : a0 + i, b = MODE == kNext ? a + 1 : a + gap;
+      if (on && pair(i) < D / 2) sum[a] = r.a[i / 2].get(i % 2), sum[b] = r.b[i / 2].get(i % 2);
     }
   }
 };
 
-template <bool INTER>
-__device__ __forceinline__ void rotate(float (&x)[8], const float (&c)[4], const float (&s)[4], float sign) {
+struct Turn {
+  Num<2> c[2], s[2], n[2];  // cos, sin, -sin of the lane's four pairs
+};
+// a token's: the lanes that hold the same pairs of different heads share them out
+template <class L, int LPH>
+__device__ __forceinline__ Turn turn_of(const L& w, const unsigned long long* freqs, long long pos) {
+  constexpr int HEADS = 32 / LPH, N = HEADS >= 4 ? 1 : 4 / HEADS;
+  float cc[N], ss[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int j = w.pair((w.sub * N + i) % 4);
+    cc[i] = 1.f, ss[i] = 0.f;
+    if (j < w.half) turn(freqs[j], pos, cc[i], ss[i]);
+  }
+  Turn t;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float &a = x[INTER ? 2 * i : i], &b = x[INTER ? 2 * i + 1 : 4 + i];
-    const float sn = sign * s[i], y = fmaf(a, c[i], -b * sn), z = fmaf(b, c[i], a * sn);
-    a = y, b = z;
+    const float c = __shfl_sync(0xffffffffu, cc[i % N], w.l + LPH * (i / N));
+    const float s = __shfl_sync(0xffffffffu, ss[i % N], w.l + LPH * (i / N));
+    t.c[i / 2].set(i % 2, c), t.s[i / 2].set(i % 2, s), t.n[i / 2].set(i % 2, -s);
   }
+  return t;
+}
+__device__ __forceinline__ void rotate(Pairs& x, const Num<2> (&c)[2], const Num<2> (&s)[2], const Num<2> (&n)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const Num<2> a = x.a[i], b = x.b[i];
+    x.a[i] = fma(b, n[i], a * c[i]);
+    x.b[i] = fma(a, s[i], b * c[i]);
+  }
+}
+__device__ __forceinline__ float dot(const Pairs& x, const Pairs& y) {
+  const Num<2> s = fma(x.b[1], y.b[1], x.b[0] * y.b[0]) + fma(x.a[1], y.a[1], x.a[0] * y.a[0]);
+  return s.x.x + s.x.y;
 }
 template <int LPH>
 __device__ __forceinline__ float head_sum(float v) {
@@ -133,156 +253,160 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-constexpr int kBatch = 3;  // heads that a lane loads before it uses the first
+constexpr int kMaxPairs = 128;  // of a head that lanes hold: D up to 256
 
-template <class T, int LPH, bool INTER>
-__global__ void __launch_bounds__(256) rotary_kernel(const RotaryParams p) {
-  typedef typename Vec<T>::type V4;
-  constexpr int HPW = 32 / LPH;
-  depend_launch();
-  const Lanes<LPH, INTER> w(p);
-  depend_wait();
-  Freqs<LPH> fr;
-  fr.load(p, w);
-  float wq[8], wk[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int at = (i < 4 ? w.a0 : w.a1 - 4) + i;
-    wq[i] = p.qw && w.a0 >= 0 ? p.qw[at] : 1.f;
-    wk[i] = p.kw && w.a0 >= 0 ? p.kw[at] : 1.f;
+// the frequencies in turns, by a CTA (the double arithmetic once, not for each warp)
+__device__ __forceinline__ void load_freqs(unsigned long long* sh, const RotaryParams& p) {
+  if ((int)threadIdx.x < p.rot / 2) sh[threadIdx.x] = turns(p.freqs[threadIdx.x]);
+  __syncthreads();
+}
+// Items: whole tokens, or (p.split) the batches of heads of a token one by one
+struct Items {
+  long long n, at, step;
+  int groups, nbq;
+  template <int HEADS>
+  __device__ static Items of(const RotaryParams& p) {
+    Items r;
+    r.nbq = (p.NQ + HEADS - 1) / HEADS;
+    r.groups = r.nbq + (p.NK + HEADS - 1) / HEADS;
+    r.n = (long long)p.T * p.B * (p.split ? r.groups : 1);
+    r.at = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+    r.step = (long long)gridDim.x * (blockDim.x / 32);
+    return r;
   }
-  const int H = p.NQ + p.NK, groups = (H + HPW * kBatch - 1) / (HPW * kBatch);
-  const int parts = p.split ? groups : 1;  // work items of a token
-  const long long items = (long long)p.T * p.B * parts, stride = (long long)gridDim.x * (blockDim.x / 32);
-  for (long long it = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; it < items; it += stride) {
-    const unsigned tb = (unsigned)(it / parts), part = (unsigned)(it % parts), t = tb / p.B, b = tb % p.B;
-    const T* q = static_cast<const T*>(p.q) + t * p.qs[0] + b * p.qs[1];
-    const T* k = static_cast<const T*>(p.k) + t * p.ks[0] + b * p.ks[1];
-    T* qo = static_cast<T*>(p.qo) + (long long)tb * p.NQ * p.D;
-    T* ko = static_cast<T*>(p.ko) + (long long)tb * p.NK * p.D;
-    float c[4], s[4];
+};
+
+constexpr int kBatch = 3, kBatchBwd = 2;  // heads that a lane loads before it uses the first
+
+template <class T, int LPH, int MODE>
+__global__ void __launch_bounds__(256, 3) rotary_kernel(const RotaryParams p) {
+  constexpr int HPW = 32 / LPH;
+  __shared__ unsigned long long freqs[kMaxPairs];
+  depend_launch();
+  const Lanes<LPH, MODE> w(p);
+  depend_wait();
+  load_freqs(freqs, p);
+  const Pairs wq = w.weights(p.qw), wk = w.weights(p.kw);
+  const float inv = 1.f / p.D;
+  Items it = Items::of<HPW * kBatch>(p);
+  for (; it.at < it.n; it.at += it.step) {
+    const unsigned tb = p.split ? (unsigned)(it.at / it.groups) : (unsigned)it.at, t = tb / p.B, b = tb % p.B;
+    const int g0 = p.split ? (int)(it.at % it.groups) : 0, g1 = p.split ? g0 + 1 : it.groups;
+    Turn tn;
     bool have = false;
-    for (int h0 = (p.split ? part * kBatch : 0) * HPW, end = p.split ? h0 + kBatch * HPW : H; h0 < min(end, H);
-         h0 += kBatch * HPW) {
-      V4 raw[kBatch][2];
+    auto heads = [&](const T* x, long long hs, T* o, int h0, int n, const Pairs& wt) {
+      Head<T, MODE> raw[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int h = h0 + i * HPW + w.sub;
-        if (h < H && w.a0 >= 0) {
-          const T* x = h < p.NQ ? q + h * p.qs[2] : k + (h - p.NQ) * p.ks[2];
-          raw[i][0].load(x + w.a0);
-          raw[i][1].load(x + w.a1);
-        }
+        raw[i] = Head<T, MODE>{};
+        if (w.on && h < n) w.load(raw[i], x + h * hs);
       }
-      if (!have) fr.at(w, position(p, t, b), c, s), have = true;
+      if (!have) tn = turn_of<Lanes<LPH, MODE>, LPH>(w, freqs, position(p, t, b)), have = true;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
+        if (h0 + i * HPW >= n) break;
         const int h = h0 + i * HPW + w.sub;
-        const bool on = h < H && w.a0 >= 0, isq = h < p.NQ;
-        float x[8] = {};
-        if (on) raw[i][0].get(x), raw[i][1].get(x + 4);
+        Pairs y = w.get(raw[i]);
         if (p.qw) {
-          float sum = 0.f;
+          const Num<2> r(rsqrtf(fmaf(head_sum<LPH>(dot(y, y)), inv, p.eps)));
 #pragma unroll
-          for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
-          const float r = rsqrtf(head_sum<LPH>(sum) / p.D + p.eps);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] *= r * (isq ? wq[j] : wk[j]);
+          for (int j = 0; j < 2; ++j) y.a[j] = y.a[j] * (r * wt.a[j]), y.b[j] = y.b[j] * (r * wt.b[j]);
         }
-        rotate<INTER>(x, c, s, 1.f);
-        if (on) {
-          T* o = isq ? qo + h * p.D : ko + (h - p.NQ) * p.D;
-          V4::store(o + w.a0, x);
-          V4::store(o + w.a1, x + 4);
-        }
+        rotate(y, tn.c, tn.s, tn.n);
+        if (w.on && h < n) w.store(o + (long long)h * p.D, y);
       }
+    };
+    for (int g = g0; g < g1; ++g) {
+      if (g < it.nbq)
+        heads(static_cast<const T*>(p.q) + t * p.qs[0] + b * p.qs[1], p.qs[2], static_cast<T*>(p.qo) + (long long)tb * p.NQ * p.D,
+              g * HPW * kBatch, p.NQ, wq);
+      else
+        heads(static_cast<const T*>(p.k) + t * p.ks[0] + b * p.ks[1], p.ks[2], static_cast<T*>(p.ko) + (long long)tb * p.NK * p.D,
+              (g - it.nbq) * HPW * kBatch, p.NK, wk);
     }
   }
 }
 
 // dw's partial sums: a row of 2 D for each CTA (q's, then k's)
-template <class T, int LPH, bool INTER>
-__global__ void __launch_bounds__(256) rotary_bwd_kernel(const RotaryParams p) {
-  typedef typename Vec<T>::type V4;
+template <class T, int LPH, int MODE>
+__global__ void __launch_bounds__(256, 2) rotary_bwd_kernel(const RotaryParams p) {
   constexpr int HPW = 32 / LPH, W = 8;
+  __shared__ unsigned long long freqs[kMaxPairs];
   __shared__ float part[W][2][LPH * 8];
   depend_launch();
-  const Lanes<LPH, INTER> w(p);
+  const Lanes<LPH, MODE> w(p);
   depend_wait();
-  Freqs<LPH> fr;
-  fr.load(p, w);
-  float wq[8], wk[8], gq[8] = {}, gk[8] = {};
+  load_freqs(freqs, p);
+  const Pairs wq = w.weights(p.qw), wk = w.weights(p.kw);
+  const float inv = 1.f / p.D;
+  Pairs sq, sk;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int at = (i < 4 ? w.a0 : w.a1 - 4) + i;
-    wq[i] = p.qw && w.a0 >= 0 ? p.qw[at] : 1.f;
-    wk[i] = p.kw && w.a0 >= 0 ? p.kw[at] : 1.f;
-  }
-  const int H = p.NQ + p.NK, warp = threadIdx.x / 32;
-  const long long items = (long long)p.T * p.B, stride = (long long)gridDim.x * W;
-  for (long long tb = (long long)blockIdx.x * W + warp; tb < items; tb += stride) {
-    const unsigned t = (unsigned)tb / p.B, b = (unsigned)tb % p.B;
-    const T* q = static_cast<const T*>(p.q) + t * p.qs[0] + b * p.qs[1];
-    const T* k = static_cast<const T*>(p.k) + t * p.ks[0] + b * p.ks[1];
-    const T* dq = static_cast<const T*>(p.dq) + t * p.dqs[0] + b * p.dqs[1];
-    const T* dk = static_cast<const T*>(p.dk) + t * p.dks[0] + b * p.dks[1];
-    T* qo = static_cast<T*>(p.qo) + tb * p.NQ * p.D;
-    T* ko = static_cast<T*>(p.ko) + tb * p.NK * p.D;
-    float c[4], s[4];
-    fr.at(w, position(p, t, b), c, s);
-    for (int h0 = 0; h0 < H; h0 += HPW) {
-      const int h = h0 + w.sub;
-      const bool on = h < H && w.a0 >= 0, isq = h < p.NQ;
-      float x[8] = {}, g[8] = {};
-      if (on) {
-        V4 raw[4];
-        const T* xp = isq ? q + h * p.qs[2] : k + (h - p.NQ) * p.ks[2];
-        const T* gp = isq ? dq + h * p.dqs[2] : dk + (h - p.NQ) * p.dks[2];
-        raw[0].load(xp + w.a0), raw[1].load(xp + w.a1), raw[2].load(gp + w.a0), raw[3].load(gp + w.a1);
-        raw[0].get(x), raw[1].get(x + 4), raw[2].get(g), raw[3].get(g + 4);
+  for (int j = 0; j < 2; ++j) sq.a[j] = sq.b[j] = sk.a[j] = sk.b[j] = Num<2>(0.f);
+  Items it = Items::of<HPW * kBatchBwd>(p);
+  for (; it.at < it.n; it.at += it.step) {
+    const unsigned tb = p.split ? (unsigned)(it.at / it.groups) : (unsigned)it.at, t = tb / p.B, b = tb % p.B;
+    const int g0 = p.split ? (int)(it.at % it.groups) : 0, g1 = p.split ? g0 + 1 : it.groups;
+    Turn tn;
+    bool have = false;
+    auto heads = [&](const T* x, long long hs, const T* d, long long ds, T* o, int h0, int n, const Pairs& wt, Pairs& sum) {
+      Head<T, MODE> rx[kBatchBwd], rd[kBatchBwd];
+#pragma unroll
+      for (int i = 0; i < kBatchBwd; ++i) {
+        const int h = h0 + i * HPW + w.sub;
+        rx[i] = Head<T, MODE>{}, rd[i] = Head<T, MODE>{};
+        if (w.on && h < n) w.load(rx[i], x + h * hs), w.load(rd[i], d + h * ds);
       }
-      rotate<INTER>(g, c, s, -1.f);
-      if (p.qw) {
-        float sum = 0.f, along = 0.f;
+      if (!have) tn = turn_of<Lanes<LPH, MODE>, LPH>(w, freqs, position(p, t, b)), have = true;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          sum = fmaf(x[j], x[j], sum);
-          along = fmaf(g[j] * (isq ? wq[j] : wk[j]), x[j], along);
+      for (int i = 0; i < kBatchBwd; ++i) {
+        if (h0 + i * HPW >= n) break;
+        const int h = h0 + i * HPW + w.sub;
+        Pairs g = w.get(rd[i]);
+        rotate(g, tn.c, tn.n, tn.s);  // back
+        if (p.qw) {
+          const Pairs v = w.get(rx[i]);
+          Pairs gw;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) gw.a[j] = g.a[j] * wt.a[j], gw.b[j] = g.b[j] * wt.b[j];
+          const float r = rsqrtf(fmaf(head_sum<LPH>(dot(v, v)), inv, p.eps));
+          const Num<2> m(-(head_sum<LPH>(dot(gw, v)) * inv) * r * r), rr(r);  // - mean(w g xh) r
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            sum.a[j] = fma(g.a[j], v.a[j] * rr, sum.a[j]);
+            sum.b[j] = fma(g.b[j], v.b[j] * rr, sum.b[j]);
+            g.a[j] = rr * fma(m, v.a[j], gw.a[j]);
+            g.b[j] = rr * fma(m, v.b[j], gw.b[j]);
+          }
         }
-        const float r = rsqrtf(head_sum<LPH>(sum) / p.D + p.eps);
-        const float m = head_sum<LPH>(along) * r * r / p.D;  // mean(w g xh) r
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float gw = g[j] * (isq ? wq[j] : wk[j]);
-          if (isq)
-            gq[j] = fmaf(g[j], x[j] * r, gq[j]);
-          else
-            gk[j] = fmaf(g[j], x[j] * r, gk[j]);
-          g[j] = r * fmaf(-m, x[j], gw);
-        }
+        if (w.on && h < n) w.store(o + (long long)h * p.D, g);
       }
-      if (on) {
-        T* o = isq ? qo + h * p.D : ko + (h - p.NQ) * p.D;
-        V4::store(o + w.a0, g);
-        V4::store(o + w.a1, g + 4);
-      }
+    };
+    for (int g = g0; g < g1; ++g) {
+      if (g < it.nbq)
+        heads(static_cast<const T*>(p.q) + t * p.qs[0] + b * p.qs[1], p.qs[2],
+              static_cast<const T*>(p.dq) + t * p.dqs[0] + b * p.dqs[1], p.dqs[2],
+              static_cast<T*>(p.qo) + (long long)tb * p.NQ * p.D, g * HPW * kBatchBwd, p.NQ, wq, sq);
+      else
+        heads(static_cast<const T*>(p.k) + t * p.ks[0] + b * p.ks[1], p.ks[2],
+              static_cast<const T*>(p.dk) + t * p.dks[0] + b * p.dks[1], p.dks[2],
+              static_cast<T*>(p.ko) + (long long)tb * p.NK * p.D, (g - it.nbq) * HPW * kBatchBwd, p.NK, wk, sk);
     }
   }
   if (!p.qw) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int o = LPH; o < 32; o <<= 1)
 #pragma unroll
-    for (int o = LPH; o < 32; o <<= 1) {
-      gq[j] += __shfl_xor_sync(0xffffffffu, gq[j], o);
-      gk[j] += __shfl_xor_sync(0xffffffffu, gk[j], o);
-    }
-  if (w.sub == 0 && w.a0 >= 0)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int at = (j < 4 ? w.a0 : w.a1 - 4) + j;
-      part[warp][0][at] = gq[j];
-      part[warp][1][at] = gk[j];
-    }
+      for (int v = 0; v < 2; ++v) {
+        sq.a[j].set(v, sq.a[j].get(v) + __shfl_xor_sync(0xffffffffu, sq.a[j].get(v), o));
+        sq.b[j].set(v, sq.b[j].get(v) + __shfl_xor_sync(0xffffffffu, sq.b[j].get(v), o));
+        sk.a[j].set(v, sk.a[j].get(v) + __shfl_xor_sync(0xffffffffu, sk.a[j].get(v), o));
+        sk.b[j].set(v, sk.b[j].get(v) + __shfl_xor_sync(0xffffffffu, sk.b[j].get(v), o));
+      }
+  const int warp = threadIdx.x / 32;
+  if (w.sub == 0) w.add_to(part[warp][0], sq), w.add_to(part[warp][1], sk);
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * p.D; i += blockDim.x) {
     float v = 0.f;
@@ -292,7 +416,7 @@ __global__ void __launch_bounds__(256) rotary_bwd_kernel(const RotaryParams p) {
   }
 }
 
-// The same for any even head size, value by value: a CTA of one warp takes a head of a token at a time.
+// The same for larger heads, value by value: a CTA of one warp takes a head of a token at a time.
 // (Gradient: the CTA's dw stays in shared memory; its threads own the columns of their pairs.)
 template <class T, bool BWD>
 __global__ void __launch_bounds__(32) rotary_any_kernel(const RotaryParams p) {
@@ -365,77 +489,77 @@ __global__ void __launch_bounds__(32) rotary_any_kernel(const RotaryParams p) {
   }
 }
 
-// dw[i] = sum of the CTAs' parts, in their order: a warp for each column
-__global__ void __launch_bounds__(256) rotary_dw_kernel(const float* part, float* dqw, float* dkw, int parts, int D) {
+// dw[i] = sum of the CTAs' parts in a fixed order: 32 columns a CTA, 32 threads for each
+__global__ void __launch_bounds__(1024) rotary_dw_kernel(const float* part, float* dqw, float* dkw, int parts, int D) {
+  __shared__ float sh[32][33];
   depend_launch();
   depend_wait();
-  const int i = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (i >= 2 * D) return;
+  const int x = threadIdx.x % 32, y = threadIdx.x / 32, i = blockIdx.x * 32 + x;
   float v = 0.f;
-  for (int j = lane; j < parts; j += 32) v += part[(long long)j * 2 * D + i];
-  v = head_sum<32>(v);
-  if (lane == 0) (i < D ? dqw : dkw)[i % D] = v;
+  if (i < 2 * D) {
+#pragma unroll 8
+    for (int j = y; j < parts; j += 32) v += part[(long long)j * 2 * D + i];
+  }
+  sh[y][x] = v;
+  __syncthreads();
+  v = head_sum<32>(sh[x][y]);
+  const int c = blockIdx.x * 32 + y;
+  if (x == 0 && c < 2 * D) (c < D ? dqw : dkw)[c % D] = v;
 }
 
 bool at16(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 bool strides4(const long long (&s)[3]) { return s[0] % 4 == 0 && s[1] % 4 == 0 && s[2] % 4 == 0; }
 
-// two pieces of four columns a lane need sizes and addresses that are multiples of four values (half layout: of a turned
-// part that is, too)
+// pieces of four columns need sizes and addresses that are multiples of four values (kHalf: a turned part that is, too)
 template <class T>
 bool vector_form(const RotaryParams& p, bool bwd) {
   constexpr size_t A = 4 * sizeof(T);
-  bool ok = p.D % 8 == 0 && p.D <= 256 && (p.interleaved || p.rot % 8 == 0) && strides4(p.qs) && strides4(p.ks) &&
+  bool ok = p.D % 8 == 0 && (p.interleaved || p.rot % 8 == 0) && strides4(p.qs) && strides4(p.ks) &&
             at16(p.q, A) && at16(p.k, A) && at16(p.qo, A) && at16(p.ko, A);
   if (bwd) ok = ok && strides4(p.dqs) && strides4(p.dks) && at16(p.dq, A) && at16(p.dk, A);
   return ok;
 }
 
-int bwd_ctas(long long items, int per) {
-  const long long want = (items + per - 1) / per;
-  return (int)(want < kRotaryParts ? want : kRotaryParts);
+int reduce_dw(const RotaryParams& p, int parts, cudaStream_t s) {
+  return launch_dependent(rotary_dw_kernel, (unsigned)((2 * p.D + 31) / 32), 1024, 0, s, (const float*)p.part, p.dqw, p.dkw,
+                          parts, p.D);
 }
 
-template <class T, int LPH, bool INTER>
-int launch_vec(RotaryParams& p, bool bwd, cudaStream_t s) {
+template <class T, int LPH, int MODE>
+int launch_lanes(RotaryParams& p, bool bwd, cudaStream_t s) {
   const long long tokens = (long long)p.T * p.B;
-  if (bwd) {
-    const int grid = bwd_ctas(tokens, 8);
-    const int e = launch_dependent(rotary_bwd_kernel<T, LPH, INTER>, (unsigned)grid, 256, 0, s, (const RotaryParams)p);
-    if (e != 0 || !p.qw) return e;
-    return launch_dependent(rotary_dw_kernel, (unsigned)((2 * p.D + 7) / 8), 256, 0, s, (const float*)p.part, p.dqw,
-                            p.dkw, grid, p.D);
-  }
-  const int groups = (p.NQ + p.NK + 32 / LPH * kBatch - 1) / (32 / LPH * kBatch);
-  p.split = tokens < 8LL * sm_count();
-  const long long want = (tokens * (p.split ? groups : 1) + 7) / 8, most = 6LL * sm_count();
-  return launch_dependent(rotary_kernel<T, LPH, INTER>, (unsigned)(want < most ? want : most), 256, 0, s,
-                          (const RotaryParams)p);
+  const int heads = 32 / LPH * (bwd ? kBatchBwd : kBatch), per_sm = bwd ? 2 : 3;
+  const int groups = (p.NQ + heads - 1) / heads + (p.NK + heads - 1) / heads;
+  // few tokens: a warp for each batch of heads, so that the latency of one batch is that of all
+  p.split = tokens < 8LL * per_sm * sm_count();
+  const long long want = (tokens * (p.split ? groups : 1) + 7) / 8, most = (long long)per_sm * sm_count();
+  unsigned grid = (unsigned)(want < most ? want : most);
+  if (!bwd) return launch_dependent(rotary_kernel<T, LPH, MODE>, grid, 256, 0, s, (const RotaryParams)p);
+  if (grid > kRotaryParts) grid = kRotaryParts;
+  const int e = launch_dependent(rotary_bwd_kernel<T, LPH, MODE>, grid, 256, 0, s, (const RotaryParams)p);
+  return e != 0 || !p.qw ? e : reduce_dw(p, (int)grid, s);
 }
 template <class T, int LPH>
-int launch_l(RotaryParams& p, bool bwd, cudaStream_t s) {
-  return p.interleaved ? launch_vec<T, LPH, true>(p, bwd, s) : launch_vec<T, LPH, false>(p, bwd, s);
+int launch_mode(RotaryParams& p, bool bwd, cudaStream_t s) {
+  if (!vector_form<T>(p, bwd)) return launch_lanes<T, LPH, kAny>(p, bwd, s);
+  return p.interleaved ? launch_lanes<T, LPH, kNext>(p, bwd, s) : launch_lanes<T, LPH, kHalf>(p, bwd, s);
 }
 template <class T>
 int launch_t(RotaryParams& p, bool bwd, cudaStream_t s) {
-  if (vector_form<T>(p, bwd)) {
-    if (p.D <= 32) return launch_l<T, 4>(p, bwd, s);
-    if (p.D <= 64) return launch_l<T, 8>(p, bwd, s);
-    if (p.D <= 128) return launch_l<T, 16>(p, bwd, s);
-    return launch_l<T, 32>(p, bwd, s);
-  }
+  if (p.D <= 32) return launch_mode<T, 4>(p, bwd, s);
+  if (p.D <= 64) return launch_mode<T, 8>(p, bwd, s);
+  if (p.D <= 128) return launch_mode<T, 16>(p, bwd, s);
+  if (p.D <= 2 * kMaxPairs) return launch_mode<T, 32>(p, bwd, s);
   const long long items = (long long)p.T * p.B * (p.NQ + p.NK);
   if (!bwd) {
     const long long most = 32LL * sm_count();
     return launch_dependent(rotary_any_kernel<T, false>, (unsigned)(items < most ? items : most), 32, 0, s,
                             (const RotaryParams)p);
   }
-  const int grid = bwd_ctas(items, 1);
+  const int grid = (int)(items < kRotaryParts ? items : kRotaryParts);
   const int e = launch_dependent(rotary_any_kernel<T, true>, (unsigned)grid, 32, p.qw ? 8 * (size_t)p.D : 0, s,
                                  (const RotaryParams)p);
-  if (e != 0 || !p.qw) return e;
-  return launch_dependent(rotary_dw_kernel, (unsigned)((2 * p.D + 7) / 8), 256, 0, s, (const float*)p.part, p.dqw, p.dkw,
-                          grid, p.D);
+  return e != 0 || !p.qw ? e : reduce_dw(p, grid, s);
 }
 
 }  // namespace
