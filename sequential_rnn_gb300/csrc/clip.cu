@@ -24,19 +24,24 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kCtasPerSm = 4;
+constexpr long long kKeep = 80ll << 20;  // bytes that the L2 is asked to hold from one kernel to the next
 
+struct Entry {
+  void* at;
+  long long size;  // elements; negative: bf16
+  int first;       // its first unit
+  int pad;
+};
 struct Table {  // of one launch
-  void* at[kClipTensors];
-  long long size[kClipTensors];   // elements; negative: bf16
-  int first[kClipTensors + 1];    // its first unit; the last: units in all
-  int n;
+  int units, n, keep;  // keep: units at the end of a CTA's range that the L2 is to hold for the second kernel
+  Entry t[kClipTensors];
 };
 
-__device__ __forceinline__ int tensor_of(const Table& t, int unit) {  // the last with first <= unit
+__device__ __forceinline__ int tensor_of(const Table& t, int unit) {  // the last that begins at or before it
   int lo = 0, hi = t.n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
-    if (t.first[mid] <= unit)
+    if (t.t[mid].first <= unit)
       lo = mid;
     else
       hi = mid;
@@ -45,21 +50,8 @@ __device__ __forceinline__ int tensor_of(const Table& t, int unit) {  // the las
 }
 // a CTA's units
 __device__ __forceinline__ void range_of(const Table& t, int& u0, int& u1) {
-  const long long units = t.first[t.n];
-  u0 = (int)(units * blockIdx.x / gridDim.x);
-  u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
-}
-
-// sum over the CTA in a fixed order; every thread gets it
-__device__ double cta_sum(double v, double* sh) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
-  __syncthreads();
-  double s = 0.0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) s += sh[i];
-  return s;
+  u0 = (int)((long long)t.units * blockIdx.x / gridDim.x);
+  u1 = (int)((long long)t.units * (blockIdx.x + 1) / gridDim.x);
 }
 
 // the values of a 16-byte vector
@@ -77,8 +69,19 @@ __device__ __forceinline__ void values(const uint4& r, float (&x)[BF ? 8 : 4]) {
 
 constexpr int kVecs = kClipUnit / 16 / kThreads;  // vectors of a unit that a thread takes
 
+// a thread's sum: fp32 with the rounding errors beside it, and what that cannot hold
+struct Sum {
+  float s, c;
+  double d;
+  __device__ __forceinline__ void add(float x, float more) {
+    const float t = s + x, z = t - s;
+    c += (s - (t - z)) + (x - z) + more;
+    s = t;
+  }
+};
+
 template <bool BF>
-__device__ __forceinline__ double squares(const uint4 (&r)[kVecs]) {
+__device__ __forceinline__ void squares(Sum& sum, const uint4 (&r)[kVecs]) {
   constexpr int E = BF ? 8 : 4;
   float s[kVecs] = {};
 #pragma unroll
@@ -91,126 +94,163 @@ __device__ __forceinline__ double squares(const uint4 (&r)[kVecs]) {
   float all = 0.f;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) all += s[i];
-  if (all >= 0x1p-100f && all <= 0x1p127f) return all;
+  if (all >= 0x1p-100f && all <= 0x1p90f) {
+    sum.add(all, 0.f);
+    return;
+  }
   // (what is below 2^-100 in all may have lost squares below 2^-126; NaN comes here, too)
-  double d = 0.0;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     if (((r[i].x | r[i].y | r[i].z | r[i].w) & (BF ? 0x7fff7fffu : 0x7fffffffu)) == 0u) continue;
     float x[E];
     values<BF>(r[i], x);
 #pragma unroll
-    for (int j = 0; j < E; ++j) d = fma((double)x[j], (double)x[j], d);
+    for (int j = 0; j < E; ++j) sum.d = fma((double)x[j], (double)x[j], sum.d);
   }
-  return d;
 }
 
-template <bool BF>
-__device__ double unit_sum(const void* at, long long size, long long e0) {
-  constexpr int E = BF ? 8 : 4, UNIT = kClipUnit / (16 / E);
-  const char* p = static_cast<const char*>(at) + e0 * (16 / E);
-  const long long left = size - e0;
-  const int n = (int)(left < UNIT ? left : UNIT);
-  const bool aligned = reinterpret_cast<uintptr_t>(p) % 16 == 0;
-  const int whole = aligned ? n / E : 0;
-  uint4 r[kVecs];
+// a unit of a tensor: its address and how many values it has
+struct Unit {
+  char* p;
+  int n;
+  bool bf16, aligned;
+  __device__ Unit(const Entry& e, int u) {
+    bf16 = e.size < 0;
+    const int es = bf16 ? 2 : 4;
+    const long long size = bf16 ? -e.size : e.size, e0 = (long long)(u - e.first) * (kClipUnit / es);
+    p = static_cast<char*>(e.at) + e0 * es;
+    n = (int)(size - e0 < kClipUnit / es ? size - e0 : kClipUnit / es);
+    aligned = reinterpret_cast<uintptr_t>(e.at) % 16 == 0;
+  }
+  __device__ int whole() const { return aligned ? n / (bf16 ? 8 : 4) : 0; }  // vectors; the rest is taken value by value
+  __device__ int rest() const { return whole() * (bf16 ? 8 : 4); }
+  template <bool STREAM>
+  __device__ __forceinline__ void load(uint4 (&r)[kVecs]) const {
+    const uint4* v = reinterpret_cast<const uint4*>(p) + threadIdx.x;
+    const int left = whole() - (int)threadIdx.x;
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int v = threadIdx.x + i * kThreads;
-    r[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (v < whole) r[i] = reinterpret_cast<const uint4*>(p)[v];
+    for (int i = 0; i < kVecs; ++i) {
+      r[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (i * kThreads < left) r[i] = STREAM ? __ldcs(v + i * kThreads) : v[i * kThreads];
+    }
   }
-  double d = squares<BF>(r);
-  for (int i = whole * E + threadIdx.x; i < n; i += kThreads) {
-    const double x = BF ? (double)__bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i])
-                        : (double)reinterpret_cast<const float*>(p)[i];
-    d = fma(x, x, d);
-  }
-  return d;
-}
+};
 
-__global__ void __launch_bounds__(kThreads) clip_sum_kernel(const __grid_constant__ Table t, double* part) {
-  __shared__ double sh[kThreads / 32];
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) clip_sum_kernel(const __grid_constant__ Table t, double* part) {
+  __shared__ float2 sh[kThreads / 32];
+  __shared__ double wide[kThreads];
   depend_launch();
   int u0, u1;
   range_of(t, u0, u1);
   int i = tensor_of(t, u0);
   depend_wait();
-  double d = 0.0;
+  Sum sum{0.f, 0.f, 0.0};
   for (int u = u0; u < u1; ++u) {
-    while (u >= t.first[i + 1]) ++i;
-    const long long size = t.size[i], k = u - t.first[i];
-    d += size < 0 ? unit_sum<true>(t.at[i], -size, k * (kClipUnit / 2)) : unit_sum<false>(t.at[i], size, k * (kClipUnit / 4));
+    while (i + 1 < t.n && u >= t.t[i + 1].first) ++i;
+    const Unit x(t.t[i], u);
+    uint4 r[kVecs];
+    if (u < u1 - t.keep)
+      x.load<true>(r);
+    else
+      x.load<false>(r);
+    if (x.bf16)
+      squares<true>(sum, r);
+    else
+      squares<false>(sum, r);
+    for (int j = x.rest() + threadIdx.x; j < x.n; j += kThreads) {
+      const double v = x.bf16 ? (double)__bfloat162float(reinterpret_cast<const __nv_bfloat16*>(x.p)[j])
+                              : (double)reinterpret_cast<const float*>(x.p)[j];
+      sum.d = fma(v, v, sum.d);
+    }
   }
-  d = cta_sum(d, sh);
-  if (threadIdx.x == 0) part[blockIdx.x] = d;
+  const bool any = __syncthreads_or(sum.d != 0.0);  // (NaN is not 0)
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float s = __shfl_xor_sync(0xffffffffu, sum.s, o), c = __shfl_xor_sync(0xffffffffu, sum.c, o);
+    sum.add(s, c);
+  }
+  if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = make_float2(sum.s, sum.c);
+  if (any) wide[threadIdx.x] = sum.d;
+  __syncthreads();
+  if (threadIdx.x < 32) {  // (fp64 is slow: one warp's work)
+    double d = 0.0;
+    if (threadIdx.x < kThreads / 32) d = (double)sh[threadIdx.x].x + (double)sh[threadIdx.x].y;
+    if (any)
+      for (int j = threadIdx.x; j < kThreads; j += 32) d += wide[j];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if (threadIdx.x == 0) part[blockIdx.x] = d;
+  }
 }
 
 template <bool BF>
-__device__ void unit_scale(void* at, long long size, long long e0, float by, float again) {
-  constexpr int E = BF ? 8 : 4, UNIT = kClipUnit / (16 / E);
-  char* p = static_cast<char*>(at) + e0 * (16 / E);
-  const long long left = size - e0;
-  const int n = (int)(left < UNIT ? left : UNIT);
-  const bool aligned = reinterpret_cast<uintptr_t>(p) % 16 == 0;
-  const int whole = aligned ? n / E : 0;
-  uint4 r[kVecs];
+__device__ __forceinline__ void scale(uint4& r, float by, float again) {
+  constexpr int E = BF ? 8 : 4;
+  float x[E];
+  values<BF>(r, x);
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int v = threadIdx.x + i * kThreads;
-    if (v < whole) r[i] = reinterpret_cast<uint4*>(p)[v];
-  }
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int v = threadIdx.x + i * kThreads;
-    if (v >= whole) continue;
-    float x[E];
-    values<BF>(r[i], x);
-#pragma unroll
-    for (int j = 0; j < E; ++j) x[j] = x[j] * by * again;
-    if (BF)
-      r[i] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[E - 4], x[E - 3]),
-                        pack_bf16x2(x[E - 2], x[E - 1]));
-    else
-      r[i] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-    reinterpret_cast<uint4*>(p)[v] = r[i];
-  }
-  for (int i = whole * E + threadIdx.x; i < n; i += kThreads) {
-    if (BF) {
-      __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(p) + i;
-      *x = __float2bfloat16_rn(__bfloat162float(*x) * by * again);
-    } else {
-      float* x = reinterpret_cast<float*>(p) + i;
-      *x = *x * by * again;
-    }
-  }
+  for (int j = 0; j < E; ++j) x[j] = x[j] * by * again;
+  if (BF)
+    r = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[E - 4], x[E - 3]),
+                   pack_bf16x2(x[E - 2], x[E - 1]));
+  else
+    r = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
 }
 
-// parts: of all launches of clip_sum_kernel, which only the last of these kernels' launches may overwrite
-__global__ void __launch_bounds__(kThreads)
+// part: of all launches of clip_sum_kernel; read by every launch of this one
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     clip_scale_kernel(const __grid_constant__ Table t, const double* part, int parts, double limit, float* norm) {
-  __shared__ double sh[kThreads / 32];
+  __shared__ float factor[2];
   depend_launch();
   int u0, u1;
   range_of(t, u0, u1);
   int i = u1 > u0 ? tensor_of(t, u1 - 1) : 0;
   depend_wait();
-  double d = 0.0;
-  for (int j = threadIdx.x; j < parts; j += kThreads) d += part[j];
-  const double all = sqrt(cta_sum(d, sh));
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)all;
-  if (!(all > limit) || isinf(all)) return;
-  // a factor that is no normal fp32 number is applied in two steps
-  const double f = limit / all;
-  const bool tiny = f < 0x1p-100;
-  const float by = tiny ? 0x1p-64f : (float)f, again = tiny ? (float)(f * 0x1p64) : 1.f;
+  uint4 r[kVecs];
+  if (u1 > u0) Unit(t.t[i], u1 - 1).load<false>(r);  // on its way while the norm is formed
+  if (threadIdx.x < 32) {
+    double d = 0.0;
+#pragma unroll 4
+    for (int j = threadIdx.x; j < parts; j += 32) d += part[j];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if (threadIdx.x == 0) {
+      const double all = sqrt(d);
+      if (norm && blockIdx.x == 0) *norm = (float)all;
+      const bool clip = all > limit && !isinf(all);
+      // a factor that is no normal fp32 number is applied in two steps; 2: not at all
+      const double f = clip ? limit / all : 2.0;
+      const bool tiny = f < 0x1p-100;
+      factor[0] = tiny ? 0x1p-64f : (float)f;
+      factor[1] = tiny ? (float)(f * 0x1p64) : 1.f;
+    }
+  }
+  __syncthreads();
+  const float by = factor[0], again = factor[1];
+  if (by > 1.f) return;
   for (int u = u1 - 1; u >= u0; --u) {
-    while (u < t.first[i]) --i;
-    const long long size = t.size[i], k = u - t.first[i];
-    if (size < 0)
-      unit_scale<true>(t.at[i], -size, k * (kClipUnit / 2), by, again);
-    else
-      unit_scale<false>(t.at[i], size, k * (kClipUnit / 4), by, again);
+    while (u < t.t[i].first) --i;
+    const Unit x(t.t[i], u);
+    if (u < u1 - 1) x.load<false>(r);
+    uint4* const v = reinterpret_cast<uint4*>(x.p) + threadIdx.x;
+    const int left = x.whole() - (int)threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      if (x.bf16)
+        scale<true>(r[k], by, again);
+      else
+        scale<false>(r[k], by, again);
+      if (k * kThreads < left) __stcs(v + k * kThreads, r[k]);
+    }
+    for (int j = x.rest() + threadIdx.x; j < x.n; j += kThreads) {
+      if (x.bf16) {
+        __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(x.p) + j;
+        *y = __float2bfloat16_rn(__bfloat162float(*y) * by * again);
+      } else {
+        float* y = reinterpret_cast<float*>(x.p) + j;
+        *y = *y * by * again;
+      }
+    }
   }
 }
 
@@ -223,26 +263,25 @@ int launch_clip(const ClipParams& p, cudaStream_t s) {
   int parts = 0;
   // the tensors from i on that fit a launch; returns the next one
   auto fill = [&](int i) {
-    t.n = 0;
+    t.n = 0, t.keep = 0;
     long long units = 0;
     for (; i < p.n && t.n < kClipTensors; ++i) {
       const long long size = p.sizes[i];
       if (size == 0) continue;
       const long long per = kClipUnit / (p.dtypes[i] == 1 ? 2 : 4), more = (size + per - 1) / per;
       if (units + more > 0x7fffffff) break;  // (of one tensor: refused before)
-      t.at[t.n] = p.at[i];
-      t.size[t.n] = p.dtypes[i] == 1 ? -size : size;
-      t.first[t.n++] = (int)units;
+      t.t[t.n++] = Entry{p.at[i], p.dtypes[i] == 1 ? -size : size, (int)units, 0};
       units += more;
     }
-    t.first[t.n] = (int)units;
+    t.units = (int)units;
     return i;
   };
   const long long most = (long long)kCtasPerSm * sm_count();
-  auto grid = [&] { return (unsigned)(t.first[t.n] < most ? t.first[t.n] : most); };
+  auto grid = [&] { return (unsigned)(t.units < most ? t.units : most); };
   for (int i = 0; i < p.n;) {
     i = fill(i);
     if (t.n == 0) continue;
+    t.keep = (int)(kKeep / kClipUnit / grid());
     const int e = launch_dependent(clip_sum_kernel, grid(), kThreads, 0, s, t, p.part + parts);
     if (e != 0) return e;
     parts += (int)grid();
@@ -253,7 +292,7 @@ int launch_clip(const ClipParams& p, cudaStream_t s) {
     if (t.n == 0 && told) continue;
     // (without a limit, or without tensors, one CTA for the norm)
     const bool scale = p.limit < INFINITY && t.n > 0;
-    if (!scale) t.n = 0, t.first[0] = 0;
+    if (!scale) t.n = 0, t.units = 0;
     const int e = launch_dependent(clip_scale_kernel, scale ? grid() : 1u, kThreads, 0, s, t, (const double*)p.part, parts,
                                    (double)p.limit, told ? (float*)nullptr : p.norm);
     if (e != 0) return e;
