@@ -24,7 +24,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kCtasPerSm = 4;
-constexpr long long kKeep = 80ll << 20;  // bytes that the L2 is asked to hold from one kernel to the next
 
 struct Entry {
   void* at;
@@ -32,12 +31,14 @@ struct Entry {
   int first;       // its first unit
   int pad;
 };
+template <int N>
 struct Table {  // of one launch
-  int units, n, keep;  // keep: units at the end of a CTA's range that the L2 is to hold for the second kernel
-  Entry t[kClipTensors];
+  int units, n;
+  Entry t[N];
 };
 
-__device__ __forceinline__ int tensor_of(const Table& t, int unit) {  // the last that begins at or before it
+template <int N>
+__device__ __forceinline__ int tensor_of(const Table<N>& t, int unit) {  // the last that begins at or before it
   int lo = 0, hi = t.n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -49,7 +50,8 @@ __device__ __forceinline__ int tensor_of(const Table& t, int unit) {  // the las
   return lo;
 }
 // a CTA's units
-__device__ __forceinline__ void range_of(const Table& t, int& u0, int& u1) {
+template <int N>
+__device__ __forceinline__ void range_of(const Table<N>& t, int& u0, int& u1) {
   u0 = (int)((long long)t.units * blockIdx.x / gridDim.x);
   u1 = (int)((long long)t.units * (blockIdx.x + 1) / gridDim.x);
 }
@@ -124,19 +126,19 @@ struct Unit {
   }
   __device__ int whole() const { return aligned ? n / (bf16 ? 8 : 4) : 0; }  // vectors; the rest is taken value by value
   __device__ int rest() const { return whole() * (bf16 ? 8 : 4); }
-  template <bool STREAM>
   __device__ __forceinline__ void load(uint4 (&r)[kVecs]) const {
     const uint4* v = reinterpret_cast<const uint4*>(p) + threadIdx.x;
     const int left = whole() - (int)threadIdx.x;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       r[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (i * kThreads < left) r[i] = STREAM ? __ldcs(v + i * kThreads) : v[i * kThreads];
+      if (i * kThreads < left) r[i] = v[i * kThreads];
     }
   }
 };
 
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) clip_sum_kernel(const __grid_constant__ Table t, double* part) {
+template <int N>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) clip_sum_kernel(const __grid_constant__ Table<N> t, double* part) {
   __shared__ float2 sh[kThreads / 32];
   __shared__ double wide[kThreads];
   depend_launch();
@@ -149,10 +151,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) clip_sum_kernel(const __
     while (i + 1 < t.n && u >= t.t[i + 1].first) ++i;
     const Unit x(t.t[i], u);
     uint4 r[kVecs];
-    if (u < u1 - t.keep)
-      x.load<true>(r);
-    else
-      x.load<false>(r);
+    x.load(r);
     if (x.bf16)
       squares<true>(sum, r);
     else
@@ -198,8 +197,9 @@ __device__ __forceinline__ void scale(uint4& r, float by, float again) {
 }
 
 // part: of all launches of clip_sum_kernel; read by every launch of this one
+template <int N>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
-    clip_scale_kernel(const __grid_constant__ Table t, const double* part, int parts, double limit, float* norm) {
+    clip_scale_kernel(const __grid_constant__ Table<N> t, const double* part, int parts, double limit, float* norm) {
   __shared__ float factor[2];
   depend_launch();
   int u0, u1;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   int i = u1 > u0 ? tensor_of(t, u1 - 1) : 0;
   depend_wait();
   uint4 r[kVecs];
-  if (u1 > u0) Unit(t.t[i], u1 - 1).load<false>(r);  // on its way while the norm is formed
+  if (u1 > u0) Unit(t.t[i], u1 - 1).load(r);  // on its way while the norm is formed
   if (threadIdx.x < 32) {
     double d = 0.0;
 #pragma unroll 4
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   for (int u = u1 - 1; u >= u0; --u) {
     while (u < t.t[i].first) --i;
     const Unit x(t.t[i], u);
-    if (u < u1 - 1) x.load<false>(r);
+    if (u < u1 - 1) x.load(r);
     uint4* const v = reinterpret_cast<uint4*>(x.p) + threadIdx.x;
     const int left = x.whole() - (int)threadIdx.x;
 #pragma unroll
@@ -254,18 +254,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
 }
 
-}  // namespace
-
-int clip_parts(int n) { return (n / kClipTensors + 1) * kCtasPerSm * sm_count(); }
-
-int launch_clip(const ClipParams& p, cudaStream_t s) {
-  Table t;
+// N: tensors of a launch at most
+template <int N>
+int launch_n(const ClipParams& p, cudaStream_t s) {
+  Table<N> t;
   int parts = 0;
   // the tensors from i on that fit a launch; returns the next one
   auto fill = [&](int i) {
-    t.n = 0, t.keep = 0;
+    t.n = 0;
     long long units = 0;
-    for (; i < p.n && t.n < kClipTensors; ++i) {
+    for (; i < p.n && t.n < N; ++i) {
       const long long size = p.sizes[i];
       if (size == 0) continue;
       const long long per = kClipUnit / (p.dtypes[i] == 1 ? 2 : 4), more = (size + per - 1) / per;
@@ -281,8 +279,7 @@ int launch_clip(const ClipParams& p, cudaStream_t s) {
   for (int i = 0; i < p.n;) {
     i = fill(i);
     if (t.n == 0) continue;
-    t.keep = (int)(kKeep / kClipUnit / grid());
-    const int e = launch_dependent(clip_sum_kernel, grid(), kThreads, 0, s, t, p.part + parts);
+    const int e = launch_dependent(clip_sum_kernel<N>, grid(), kThreads, 0, s, t, p.part + parts);
     if (e != 0) return e;
     parts += (int)grid();
   }
@@ -293,12 +290,21 @@ int launch_clip(const ClipParams& p, cudaStream_t s) {
     // (without a limit, or without tensors, one CTA for the norm)
     const bool scale = p.limit < INFINITY && t.n > 0;
     if (!scale) t.n = 0, t.units = 0;
-    const int e = launch_dependent(clip_scale_kernel, scale ? grid() : 1u, kThreads, 0, s, t, (const double*)p.part, parts,
-                                   (double)p.limit, told ? (float*)nullptr : p.norm);
+    const int e = launch_dependent(clip_scale_kernel<N>, scale ? grid() : 1u, kThreads, 0, s, t, (const double*)p.part,
+                                   parts, (double)p.limit, told ? (float*)nullptr : p.norm);
     if (e != 0) return e;
     told = true;
   }
   return 0;
+}
+
+}  // namespace
+
+int clip_parts(int n) { return (n / kClipTensors + 1) * kCtasPerSm * sm_count(); }
+
+int launch_clip(const ClipParams& p, cudaStream_t s) {
+  // (a table of 256 is 6 KB that every launch copies)
+  return p.n <= 16 ? launch_n<16>(p, s) : launch_n<kClipTensors>(p, s);
 }
 
 }  // namespace srnn
