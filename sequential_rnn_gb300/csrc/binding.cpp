@@ -604,8 +604,11 @@ struct Rotary {
     desc.D = count("q", D);
     desc.eps = (float)number(eps);
     strides = {};
-    Attention::strides_of("q", q, strides.q);
-    Attention::strides_of("k", k, strides.k);
+    strides_of("q", q, strides.q);
+    strides_of("k", k, strides.k);
+  }
+  static void strides_of(const char* name, const Tensor& t, int64_t (&s)[3]) {
+    if (t.numel() > 0) Attention::strides_of(name, t, s);  // (no values: any strides will do)
   }
 };
 
@@ -636,8 +639,8 @@ PyObject* head_norm_rotary_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
   const Tensor &q = tensor("q", a[0]), &k = tensor("k", a[1]), &dqo = tensor("dq", a[6]), &dko = tensor("dk", a[7]);
   want("dq", dqo, r.sq, r.type, r.dev, false);
   want("dk", dko, r.sk, r.type, r.dev, false);
-  Attention::strides_of("dq", dqo, r.strides.dq);
-  Attention::strides_of("dk", dko, r.strides.dk);
+  Rotary::strides_of("dq", dqo, r.strides.dq);
+  Rotary::strides_of("dk", dko, r.strides.dk);
   Tensor dq, dk, dqw, dkw, ws;
   int st;
   {

@@ -90,6 +90,7 @@ struct Lanes {
   int a0, gap;   // vector forms: first column, from the first piece to the second
   int half, D;
   bool inter, on;
+  bool swap;     // kHalf: the pair's second value first
   __device__ explicit Lanes(const RotaryParams& p) {
     const int lane = threadIdx.x % 32;
     l = lane % LPH, sub = lane / LPH;
@@ -107,7 +108,16 @@ struct Lanes {
       on = l < D / 2;
     }
     if (!on && MODE != kAny) a0 = 0;
+    swap = false;
   }
+  // The lanes of some heads read their pieces in the other order, so that those that shared memory serves at once
+  // (128 bytes) lie in different banks.  row: bytes of a head
+  __device__ void spread(int row) {
+    if (MODE != kHalf || ((sub * row) >> 7 & 1) == 0) return;
+    a0 += gap, gap = -gap;
+    swap = true;
+  }
+  __device__ int step() const { return MODE == kNext ? 4 : gap; }
   // index of the lane's pair i; pairs below `half` turn
   __device__ int pair(int i) const { return MODE == kAny ? l + LPH * i : 4 * l + i; }
   __device__ void columns(int i, int& a, int& b) const {  // kAny
@@ -132,7 +142,7 @@ struct Lanes {
       }
     } else {
       h.a = *reinterpret_cast<const decltype(h.a)*>(x + a0);
-      h.b = *reinterpret_cast<const decltype(h.b)*>(x + a0 + gap);
+      h.b = *reinterpret_cast<const decltype(h.b)*>(x + a0 + step());
     }
   }
   template <class T>
@@ -175,27 +185,33 @@ struct Lanes {
       for (int i = 0; i < 4; ++i) y[MODE == kNext ? 2 * i : i] = a[i], y[MODE == kNext ? 2 * i + 1 : 4 + i] = b[i];
       if constexpr (sizeof(T) == 2) {
         *reinterpret_cast<uint2*>(x + a0) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-        *reinterpret_cast<uint2*>(x + a0 + gap) = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        *reinterpret_cast<uint2*>(x + a0 + step()) = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
       } else {
         *reinterpret_cast<float4*>(x + a0) = make_float4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<float4*>(x + a0 + gap) = make_float4(y[4], y[5], y[6], y[7]);
+        *reinterpret_cast<float4*>(x + a0 + step()) = make_float4(y[4], y[5], y[6], y[7]);
       }
     }
   }
-  // the lane's values of a [D] vector of fp32 numbers (null, or no column: 1)
+  // the lane's weights, from shared memory (what lanes without columns get does not matter)
   __device__ Pairs weights(const float* w) const {
     Pairs r;
+    float a[4], b[4];
+    if constexpr (MODE == kAny) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      int a, b;
-      if (MODE == kAny)
-        columns(i, a, b);
-      else
-        a = MODE == kNext ? a0 + 2 * i : a0 + i, b = MODE == kNext ? a + 1 : a + gap;
-      const bool in = w && on && pair(i) < D / 2;
-      r.a[i / 2].set(i % 2, in ? w[a] : 1.f);
-      r.b[i / 2].set(i % 2, in ? w[b] : 1.f);
+      for (int i = 0; i < 4; ++i) {
+        int ia, ib;
+        columns(i, ia, ib);
+        const bool in = pair(i) < D / 2;
+        a[i] = in ? w[ia] : 0.f, b[i] = in ? w[ib] : 0.f;
+      }
+    } else {
+      const float4 x = *reinterpret_cast<const float4*>(w + a0), y = *reinterpret_cast<const float4*>(w + a0 + step());
+      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = v[MODE == kNext ? 2 * i : i], b[i] = v[MODE == kNext ? 2 * i + 1 : 4 + i];
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r.a[i].x = make_float2(a[2 * i], a[2 * i + 1]), r.b[i].x = make_float2(b[2 * i], b[2 * i + 1]);
     return r;
   }
   __device__ void add_to(float* sum, const Pairs& r) const {
@@ -230,7 +246,7 @@ __device__ __forceinline__ Turn turn_of(const L& w, const unsigned long long* fr
   for (int i = 0; i < 4; ++i) {
     const float c = __shfl_sync(0xffffffffu, cc[i % N], w.l + LPH * (i / N));
     const float s = __shfl_sync(0xffffffffu, ss[i % N], w.l + LPH * (i / N));
-    t.c[i / 2].set(i % 2, c), t.s[i / 2].set(i % 2, s), t.n[i / 2].set(i % 2, -s);
+    t.c[i / 2].set(i % 2, c), t.s[i / 2].set(i % 2, w.swap ? -s : s), t.n[i / 2].set(i % 2, w.swap ? s : -s);
   }
   return t;
 }
@@ -253,13 +269,33 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
+// over the lanes that hold the same pairs of different heads
+template <int LPH>
+__device__ __forceinline__ void sum_lanes(Pairs& x) {
+#pragma unroll
+  for (int o = LPH; o < 32; o <<= 1)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        x.a[j].set(v, x.a[j].get(v) + __shfl_xor_sync(0xffffffffu, x.a[j].get(v), o));
+        x.b[j].set(v, x.b[j].get(v) + __shfl_xor_sync(0xffffffffu, x.b[j].get(v), o));
+      }
+}
+
 constexpr int kMaxPairs = 128;  // of a head that lanes hold: D up to 256
 
-// the frequencies in turns, by a CTA (the double arithmetic once, not for each warp)
-__device__ __forceinline__ void load_freqs(unsigned long long* sh, const RotaryParams& p) {
-  if ((int)threadIdx.x < p.rot / 2) sh[threadIdx.x] = turns(p.freqs[threadIdx.x]);
-  __syncthreads();
-}
+// What a CTA keeps: the frequencies in turns (the double arithmetic once, not for each warp), the weights
+struct Consts {
+  unsigned long long freqs[kMaxPairs];
+  alignas(16) float w[2][2 * kMaxPairs];
+  __device__ void load(const RotaryParams& p) {
+    for (int i = threadIdx.x; i < p.rot / 2; i += blockDim.x) freqs[i] = turns(p.freqs[i]);
+    if (p.qw)
+      for (int i = threadIdx.x; i < p.D; i += blockDim.x) w[0][i] = p.qw[i], w[1][i] = p.kw[i];
+    __syncthreads();
+  }
+};
 // Items: whole tokens, or (p.split) the batches of heads of a token one by one
 struct Items {
   long long n, at, step;
@@ -276,17 +312,18 @@ struct Items {
   }
 };
 
+constexpr int kRingTokens = 16;  // for each SM
 constexpr int kBatch = 3, kBatchBwd = 2;  // heads that a lane loads before it uses the first
 
 template <class T, int LPH, int MODE>
 __global__ void __launch_bounds__(256, 3) rotary_kernel(const RotaryParams p) {
   constexpr int HPW = 32 / LPH;
-  __shared__ unsigned long long freqs[kMaxPairs];
+  __shared__ Consts sh;
   depend_launch();
   const Lanes<LPH, MODE> w(p);
   depend_wait();
-  load_freqs(freqs, p);
-  const Pairs wq = w.weights(p.qw), wk = w.weights(p.kw);
+  sh.load(p);
+  const Pairs wq = w.weights(sh.w[0]), wk = w.weights(sh.w[1]);
   const float inv = 1.f / p.D;
   Items it = Items::of<HPW * kBatch>(p);
   for (; it.at < it.n; it.at += it.step) {
@@ -302,7 +339,7 @@ __global__ void __launch_bounds__(256, 3) rotary_kernel(const RotaryParams p) {
         raw[i] = Head<T, MODE>{};
         if (w.on && h < n) w.load(raw[i], x + h * hs);
       }
-      if (!have) tn = turn_of<Lanes<LPH, MODE>, LPH>(w, freqs, position(p, t, b)), have = true;
+      if (!have) tn = turn_of<Lanes<LPH, MODE>, LPH>(w, sh.freqs, position(p, t, b)), have = true;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         if (h0 + i * HPW >= n) break;
@@ -332,13 +369,13 @@ __global__ void __launch_bounds__(256, 3) rotary_kernel(const RotaryParams p) {
 template <class T, int LPH, int MODE>
 __global__ void __launch_bounds__(256, 2) rotary_bwd_kernel(const RotaryParams p) {
   constexpr int HPW = 32 / LPH, W = 8;
-  __shared__ unsigned long long freqs[kMaxPairs];
+  __shared__ Consts sh;
   __shared__ float part[W][2][LPH * 8];
   depend_launch();
   const Lanes<LPH, MODE> w(p);
   depend_wait();
-  load_freqs(freqs, p);
-  const Pairs wq = w.weights(p.qw), wk = w.weights(p.kw);
+  sh.load(p);
+  const Pairs wq = w.weights(sh.w[0]), wk = w.weights(sh.w[1]);
   const float inv = 1.f / p.D;
   Pairs sq, sk;
 #pragma unroll
@@ -357,7 +394,7 @@ __global__ void __launch_bounds__(256, 2) rotary_bwd_kernel(const RotaryParams p
         rx[i] = Head<T, MODE>{}, rd[i] = Head<T, MODE>{};
         if (w.on && h < n) w.load(rx[i], x + h * hs), w.load(rd[i], d + h * ds);
       }
-      if (!have) tn = turn_of<Lanes<LPH, MODE>, LPH>(w, freqs, position(p, t, b)), have = true;
+      if (!have) tn = turn_of<Lanes<LPH, MODE>, LPH>(w, sh.freqs, position(p, t, b)), have = true;
 #pragma unroll
       for (int i = 0; i < kBatchBwd; ++i) {
         if (h0 + i * HPW >= n) break;
@@ -394,17 +431,8 @@ __global__ void __launch_bounds__(256, 2) rotary_bwd_kernel(const RotaryParams p
     }
   }
   if (!p.qw) return;
-#pragma unroll
-  for (int o = LPH; o < 32; o <<= 1)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        sq.a[j].set(v, sq.a[j].get(v) + __shfl_xor_sync(0xffffffffu, sq.a[j].get(v), o));
-        sq.b[j].set(v, sq.b[j].get(v) + __shfl_xor_sync(0xffffffffu, sq.b[j].get(v), o));
-        sk.a[j].set(v, sk.a[j].get(v) + __shfl_xor_sync(0xffffffffu, sk.a[j].get(v), o));
-        sk.b[j].set(v, sk.b[j].get(v) + __shfl_xor_sync(0xffffffffu, sk.b[j].get(v), o));
-      }
+  sum_lanes<LPH>(sq);
+  sum_lanes<LPH>(sk);
   const int warp = threadIdx.x / 32;
   if (w.sub == 0) w.add_to(part[warp][0], sq), w.add_to(part[warp][1], sk);
   __syncthreads();
@@ -413,6 +441,168 @@ __global__ void __launch_bounds__(256, 2) rotary_bwd_kernel(const RotaryParams p
 #pragma unroll
     for (int j = 0; j < W; ++j) v += part[j][i / p.D][i % p.D];
     p.part[(long long)blockIdx.x * 2 * p.D + i] = v;
+  }
+}
+
+// Many tokens, heads of 32, 64, 128 or 256 at 16-byte addresses: a warp takes whole tokens, a batch of heads at a time (512
+// bytes of bf16 three times), which asynchronous copies bring into a ring of its own in shared memory, so that up to three
+// batches are on their way while one is worked on and no register holds them.  (Loads into registers: 33 -> 23 us.)
+template <class T, int LPH, bool BWD>
+struct Ring {
+  static constexpr int HPW = 32 / LPH, D = 8 * LPH, BATCH = 3, STAGES = !BWD ? 4 : sizeof(T) == 4 ? 2 : 3;
+  static constexpr int SWEEP = 32 * 8 * sizeof(T);            // bytes of one head a lane group: HPW heads
+  static constexpr int PART = BATCH * SWEEP, STAGE = PART * (BWD ? 2 : 1);
+  static constexpr int COPIES = SWEEP / 512;                  // 16-byte copies of a sweep for each lane
+  static constexpr int SMEM = 8 * STAGES * STAGE, CTAS = BWD || sizeof(T) == 4 ? 2 : 3;
+};
+
+// a warp's batches of heads, token after token
+struct Item {
+  unsigned t, b;
+  int g;
+  __device__ bool there(const RotaryParams& p) const { return t < (unsigned)p.T; }
+  __device__ void next(const RotaryParams& p, int groups, unsigned dt, unsigned db) {
+    if (++g < groups) return;
+    g = 0, t += dt, b += db;
+    if (b >= (unsigned)p.B) b -= p.B, ++t;
+  }
+};
+
+template <class T, int LPH, int MODE, bool BWD>
+__global__ void __launch_bounds__(256, (Ring<T, LPH, BWD>::CTAS)) rotary_ring_kernel(const RotaryParams p) {
+  using C = Ring<T, LPH, BWD>;
+  constexpr int HPW = C::HPW, D = C::D;
+  extern __shared__ __align__(128) char dyn[];
+  __shared__ Consts sh;
+  __shared__ float part[BWD ? 8 : 1][2][BWD ? D : 1];
+  depend_launch();
+  Lanes<LPH, MODE> w(p);
+  w.spread(D * sizeof(T));
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  char* const ring = dyn + warp * C::STAGES * C::STAGE;
+  const int nbq = (p.NQ + HPW * C::BATCH - 1) / (HPW * C::BATCH), groups = nbq + (p.NK + HPW * C::BATCH - 1) / (HPW * C::BATCH);
+  const unsigned line = blockIdx.x * 8 + warp, lines = gridDim.x * 8, dt = lines / p.B, db = lines % p.B;
+  Item it{line / p.B, line % p.B, 0}, ahead = it;
+  depend_wait();
+  // the batch of `ahead` into a stage: lane's 16 bytes of each 512
+  auto bring = [&](int stage) {
+    if (ahead.there(p)) {
+      const bool isq = ahead.g < nbq;
+      const int h0 = (isq ? ahead.g : ahead.g - nbq) * HPW * C::BATCH, n = (isq ? p.NQ : p.NK) - h0;
+#pragma unroll
+      for (int k = 0; k < (BWD ? 2 : 1); ++k) {
+        const long long* st = k ? (isq ? p.dqs : p.dks) : (isq ? p.qs : p.ks);
+        const T* x = static_cast<const T*>(k ? (isq ? p.dq : p.dk) : (isq ? p.q : p.k)) + ahead.t * st[0] + ahead.b * st[1] + h0 * st[2];
+        const uint32_t to = smem_u32(ring + stage * C::STAGE + k * C::PART) + 16 * lane;
+#pragma unroll
+        for (int c = 0; c < C::COPIES; ++c) {
+          constexpr int E = 16 / sizeof(T);  // values of a copy
+          const int at = (c * 32 + lane) * E, h = at / D;
+          const T* from = x + h * st[2] + at % D;
+#pragma unroll
+          for (int i = 0; i < C::BATCH; ++i)
+            if (i * HPW + h < n) cp_async16(to + i * C::SWEEP + c * 512, from + i * HPW * st[2]);
+        }
+      }
+    }
+    cp_async_commit();
+    ahead.next(p, groups, dt, db);
+  };
+#pragma unroll
+  for (int k = 0; k < C::STAGES - 1; ++k) bring(k);
+  sh.load(p);
+  constexpr float inv = 1.f / D;
+  Pairs sq, sk;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) sq.a[j] = sq.b[j] = sk.a[j] = sk.b[j] = Num<2>(0.f);
+  Turn tn;
+  long long pos = it.there(p) ? position(p, it.t, it.b) : 0;
+  for (int stage = 0; it.there(p); stage = stage + 1 == C::STAGES ? 0 : stage + 1) {
+    bring(stage == 0 ? C::STAGES - 1 : stage - 1);
+    if (it.g == 0) {
+      tn = turn_of<Lanes<LPH, MODE>, LPH>(w, sh.freqs, pos);
+      Item next = it;  // the next token's position, a token ahead
+      next.g = groups - 1;
+      next.next(p, groups, dt, db);
+      if (next.there(p)) pos = position(p, next.t, next.b);
+    }
+    const bool isq = it.g < nbq;
+    const int h0 = (isq ? it.g : it.g - nbq) * HPW * C::BATCH, H = isq ? p.NQ : p.NK, n = H - h0 - w.sub;
+    T* o = static_cast<T*>(isq ? p.qo : p.ko) + (((long long)it.t * p.B + it.b) * H + h0 + w.sub) * D;
+    const Pairs wt = w.weights(sh.w[isq ? 0 : 1]);
+    cp_async_wait<C::STAGES - 1>();
+    __syncwarp();
+    const T* x = reinterpret_cast<const T*>(ring + stage * C::STAGE) + w.sub * D;
+    const T* d = reinterpret_cast<const T*>(ring + stage * C::STAGE + C::PART) + w.sub * D;
+#pragma unroll
+    for (int i = 0; i < C::BATCH; ++i) {
+      const bool on = i * HPW < n;  // (what the others compute stays in their own head)
+      Head<T, MODE> raw;
+      w.load(raw, x + i * HPW * D);
+      Pairs y = w.get(raw);
+      if constexpr (!BWD) {
+        if (p.qw) {
+          const Num<2> r(rsqrtf(fmaf(head_sum<LPH>(dot(y, y)), inv, p.eps)));
+#pragma unroll
+          for (int j = 0; j < 2; ++j) y.a[j] = y.a[j] * (r * wt.a[j]), y.b[j] = y.b[j] * (r * wt.b[j]);
+        }
+        rotate(y, tn.c, tn.s, tn.n);
+        if (on) w.store(o + i * HPW * D, y);
+      } else {
+        Head<T, MODE> rd;
+        w.load(rd, d + i * HPW * D);
+        Pairs g = w.get(rd);
+        rotate(g, tn.c, tn.n, tn.s);  // back
+        if (p.qw) {
+          Pairs gw;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) gw.a[j] = g.a[j] * wt.a[j], gw.b[j] = g.b[j] * wt.b[j];
+          const float r = rsqrtf(fmaf(head_sum<LPH>(dot(y, y)), inv, p.eps));
+          const Num<2> m(-(head_sum<LPH>(dot(gw, y)) * inv) * r * r), rr(r);  // - mean(w g xh) r
+          if (on) {
+            Pairs z;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) z.a[j] = y.a[j] * rr, z.b[j] = y.b[j] * rr;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (isq)
+                sq.a[j] = fma(g.a[j], z.a[j], sq.a[j]), sq.b[j] = fma(g.b[j], z.b[j], sq.b[j]);
+              else
+                sk.a[j] = fma(g.a[j], z.a[j], sk.a[j]), sk.b[j] = fma(g.b[j], z.b[j], sk.b[j]);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            g.a[j] = rr * fma(m, y.a[j], gw.a[j]);
+            g.b[j] = rr * fma(m, y.b[j], gw.b[j]);
+          }
+        }
+        if (on) w.store(o + i * HPW * D, g);
+      }
+    }
+    __syncwarp();  // (the stage is filled again by the next copies)
+    it.next(p, groups, dt, db);
+  }
+  if constexpr (BWD) {
+    if (!p.qw) return;
+    if (w.swap) {
+      Pairs x = sq;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) sq.a[j] = x.b[j], sq.b[j] = x.a[j];
+      x = sk;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) sk.a[j] = x.b[j], sk.b[j] = x.a[j];
+    }
+    sum_lanes<LPH>(sq);
+    sum_lanes<LPH>(sk);
+    if (w.sub == 0) w.add_to(part[warp][0], sq), w.add_to(part[warp][1], sk);
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
+      float v = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v += part[j][i / D][i % D];
+      p.part[(long long)blockIdx.x * 2 * D + i] = v;
+    }
   }
 }
 
@@ -539,8 +729,36 @@ int launch_lanes(RotaryParams& p, bool bwd, cudaStream_t s) {
   const int e = launch_dependent(rotary_bwd_kernel<T, LPH, MODE>, grid, 256, 0, s, (const RotaryParams)p);
   return e != 0 || !p.qw ? e : reduce_dw(p, (int)grid, s);
 }
+// 16-byte copies, and enough tokens that each warp of the grid takes several
+template <class T, int LPH>
+bool ring_form(const RotaryParams& p, bool bwd) {
+  auto even = [](const void* x, const long long (&s)[3]) {
+    return reinterpret_cast<uintptr_t>(x) % 16 == 0 && (s[0] | s[1] | s[2]) * (long long)sizeof(T) % 16 == 0;
+  };
+  bool ok = p.D == 8 * LPH && vector_form<T>(p, bwd) && even(p.q, p.qs) && even(p.k, p.ks);
+  if (bwd) ok = ok && even(p.dq, p.dqs) && even(p.dk, p.dks);
+  return ok && (long long)p.T * p.B >= kRingTokens * sm_count();
+}
+template <class T, int LPH, int MODE, bool BWD>
+int launch_ring(const RotaryParams& p, cudaStream_t s) {
+  using C = Ring<T, LPH, BWD>;
+  static int prep[64][5];
+  int e = prepare_launch(prep, rotary_ring_kernel<T, LPH, MODE, BWD>, C::SMEM, 256, 1);
+  if (e != 0) return e;
+  const long long want = ((long long)p.T * p.B + 7) / 8, most = (long long)C::CTAS * sm_count();
+  unsigned grid = (unsigned)(want < most ? want : most);
+  if (BWD && grid > kRotaryParts) grid = kRotaryParts;
+  e = launch_dependent(rotary_ring_kernel<T, LPH, MODE, BWD>, grid, 256, C::SMEM, s, p);
+  return e != 0 || !BWD || !p.qw ? e : reduce_dw(p, (int)grid, s);
+}
+template <class T, int LPH, int MODE>
+int launch_ring(const RotaryParams& p, bool bwd, cudaStream_t s) {
+  return bwd ? launch_ring<T, LPH, MODE, true>(p, s) : launch_ring<T, LPH, MODE, false>(p, s);
+}
 template <class T, int LPH>
 int launch_mode(RotaryParams& p, bool bwd, cudaStream_t s) {
+  if (ring_form<T, LPH>(p, bwd))
+    return p.interleaved ? launch_ring<T, LPH, kNext>(p, bwd, s) : launch_ring<T, LPH, kHalf>(p, bwd, s);
   if (!vector_form<T>(p, bwd)) return launch_lanes<T, LPH, kAny>(p, bwd, s);
   return p.interleaved ? launch_lanes<T, LPH, kNext>(p, bwd, s) : launch_lanes<T, LPH, kHalf>(p, bwd, s);
 }

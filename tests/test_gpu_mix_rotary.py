@@ -73,6 +73,28 @@ def test_shapes(S, T, B, NQ, NK, D, rot, inter, dtype):
     check(S, q, k, wq, wk, freqs, ints(list(range(5, 5 + 1000 * B, 1000))), inter, dtype)
 
 
+# many tokens: the copies' ring; batches of heads that are full, partial and one head alone
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("T,B,NQ,NK,D,rot", [
+    (350, 7, 13, 1, 64, 64), (2500, 1, 12, 12, 64, 16), (3, 811, 7, 2, 128, 128), (1221, 2, 4, 3, 256, 64), (500, 5, 25, 2, 32, 32)])
+def test_many_tokens(S, T, B, NQ, NK, D, rot, inter, dtype):
+    qkv = rand(1, T, B, NQ + NK + 1, D, dtype=dtype, scale=2)
+    w = 1 + rand(3, 2, D, scale=0.2)
+    at = torch.randint(0, 10 ** 6, (B,), generator=torch.Generator().manual_seed(1)).int().cuda()
+    check(S, qkv[:, :, :NQ], qkv[:, :, NQ:NQ + NK], w[0], w[1], S.rotary_frequencies(rot), at, inter, dtype)
+
+
+def test_many_tokens_without_norm_or_rotation(S):
+    q, k, w = rand(1, 900, 3, 5, 64, dtype="bf16"), rand(2, 900, 3, 2, 64, dtype="bf16"), 1 + rand(3, 64, scale=0.2)
+    f = S.rotary_frequencies(64)
+    check(S, q, k, None, None, f, None, False, "bf16")
+    check(S, q, k, w, w, None, None, True, "bf16")
+    free = torch.randint(-2 ** 31, 2 ** 31 - 1, (900, 3), generator=torch.Generator().manual_seed(1)).int().cuda()
+    check(S, q, k, w, w, f, free, False, "bf16")
+    check(S, q[:, :, :0], k, w, w, f, free, False, "bf16")
+
+
 @pytest.mark.parametrize("D", [64, 34])
 def test_without_norm_or_rotation(S, D):
     q, k = rand(1, 6, 3, 4, D, dtype="bf16"), rand(2, 6, 3, 4, D, dtype="bf16")
