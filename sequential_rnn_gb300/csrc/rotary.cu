@@ -34,10 +34,17 @@ __device__ __forceinline__ unsigned long long turns(double f) {
   const long long a = frac == 0.5 ? (long long)(1ull << 63) : __double2ll_rn(frac * 0x1p64);
   return (unsigned long long)a + (unsigned long long)__double2ll_rn(lo * 0x1p64);
 }
-// cos and sin of pos times that
+// cos and sin of pos times that: the quarter turn nearest to the angle, and the Taylor series of the rest (at most 1/8 of a
+// turn, formed from 32 bits: off by less than 2^-31) up to x^9 and x^10, which leave out less than 2 10^-9
 __device__ __forceinline__ void turn(unsigned long long f, long long pos, float& c, float& s) {
-  const long long t = (long long)(f * (unsigned long long)pos);
-  sincospif((float)t * 0x1p-63f, &s, &c);
+  const uint32_t u = (uint32_t)((f * (unsigned long long)pos) >> 32), q = (u + 0x20000000u) >> 30;
+  const float x = (float)(int)(u - (q << 30)) * 0x1.921fb6p-30f;  // 2 pi 2^-32
+  const float z = x * x;
+  const float sx = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
+  const float cx = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+  const float cc = q & 1 ? sx : cx, ss = q & 1 ? cx : sx;
+  c = (q + 1) & 2 ? -cc : cc;
+  s = q & 2 ? -ss : ss;
 }
 
 __device__ __forceinline__ float get1(const float* p) { return *p; }
@@ -291,8 +298,7 @@ struct Consts {
   alignas(16) float w[2][2 * kMaxPairs];
   __device__ void load(const RotaryParams& p) {
     for (int i = threadIdx.x; i < p.rot / 2; i += blockDim.x) freqs[i] = turns(p.freqs[i]);
-    if (p.qw)
-      for (int i = threadIdx.x; i < p.D; i += blockDim.x) w[0][i] = p.qw[i], w[1][i] = p.kw[i];
+    for (int i = threadIdx.x; i < p.D; i += blockDim.x) w[0][i] = p.qw ? p.qw[i] : 1.f, w[1][i] = p.kw ? p.kw[i] : 1.f;
     __syncthreads();
   }
 };
@@ -313,6 +319,7 @@ struct Items {
 };
 
 constexpr int kRingTokens = 16;  // for each SM
+constexpr size_t kRingThree = 72 * 1024, kRingMost = 200 * 1024;  // bytes of a CTA's rings
 constexpr int kBatch = 3, kBatchBwd = 2;  // heads that a lane loads before it uses the first
 
 template <class T, int LPH, int MODE>
@@ -444,33 +451,19 @@ __global__ void __launch_bounds__(256, 2) rotary_bwd_kernel(const RotaryParams p
   }
 }
 
-// Many tokens, heads of 32, 64, 128 or 256 at 16-byte addresses: a warp takes whole tokens, a batch of heads at a time (512
-// bytes of bf16 three times), which asynchronous copies bring into a ring of its own in shared memory, so that up to three
-// batches are on their way while one is worked on and no register holds them.  (Loads into registers: 33 -> 23 us.)
-template <class T, int LPH, bool BWD>
+// Many tokens, heads of 32, 64, 128 or 256 at 16-byte addresses: a warp takes whole tokens, which asynchronous copies bring
+// into a ring of its own in shared memory, so that one or two tokens are on their way while one is worked on and no register
+// holds them.  A sweep is what the warp takes at once: 32 / LPH heads.
+template <class T, int LPH>
 struct Ring {
-  static constexpr int HPW = 32 / LPH, D = 8 * LPH, BATCH = 3, STAGES = !BWD ? 4 : sizeof(T) == 4 ? 2 : 3;
-  static constexpr int SWEEP = 32 * 8 * sizeof(T);            // bytes of one head a lane group: HPW heads
-  static constexpr int PART = BATCH * SWEEP, STAGE = PART * (BWD ? 2 : 1);
-  static constexpr int COPIES = SWEEP / 512;                  // 16-byte copies of a sweep for each lane
-  static constexpr int SMEM = 8 * STAGES * STAGE, CTAS = BWD || sizeof(T) == 4 ? 2 : 3;
+  static constexpr int HPW = 32 / LPH, D = 8 * LPH, SWEEP = 32 * 8 * sizeof(T);
+  static constexpr int E = 16 / sizeof(T), COPIES = SWEEP / 512;  // values of a copy, copies of a sweep for each lane
+  static int sweeps(const RotaryParams& p) { return (p.NQ + HPW - 1) / HPW + (p.NK + HPW - 1) / HPW; }
 };
 
-// a warp's batches of heads, token after token
-struct Item {
-  unsigned t, b;
-  int g;
-  __device__ bool there(const RotaryParams& p) const { return t < (unsigned)p.T; }
-  __device__ void next(const RotaryParams& p, int groups, unsigned dt, unsigned db) {
-    if (++g < groups) return;
-    g = 0, t += dt, b += db;
-    if (b >= (unsigned)p.B) b -= p.B, ++t;
-  }
-};
-
-template <class T, int LPH, int MODE, bool BWD>
-__global__ void __launch_bounds__(256, (Ring<T, LPH, BWD>::CTAS)) rotary_ring_kernel(const RotaryParams p) {
-  using C = Ring<T, LPH, BWD>;
+template <class T, int LPH, int MODE, bool BWD, int STAGES>
+__global__ void __launch_bounds__(256, BWD || sizeof(T) == 4 ? 2 : 3) rotary_ring_kernel(const RotaryParams p) {
+  using C = Ring<T, LPH>;
   constexpr int HPW = C::HPW, D = C::D;
   extern __shared__ __align__(128) char dyn[];
   __shared__ Consts sh;
@@ -479,109 +472,111 @@ __global__ void __launch_bounds__(256, (Ring<T, LPH, BWD>::CTAS)) rotary_ring_ke
   Lanes<LPH, MODE> w(p);
   w.spread(D * sizeof(T));
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  char* const ring = dyn + warp * C::STAGES * C::STAGE;
-  const int nbq = (p.NQ + HPW * C::BATCH - 1) / (HPW * C::BATCH), groups = nbq + (p.NK + HPW * C::BATCH - 1) / (HPW * C::BATCH);
+  const int nq = (p.NQ + HPW - 1) / HPW, nk = (p.NK + HPW - 1) / HPW, size = (nq + nk) * C::SWEEP;
+  char* const ring = dyn + warp * STAGES * size * (BWD ? 2 : 1);
   const unsigned line = blockIdx.x * 8 + warp, lines = gridDim.x * 8, dt = lines / p.B, db = lines % p.B;
-  Item it{line / p.B, line % p.B, 0}, ahead = it;
   depend_wait();
-  // the batch of `ahead` into a stage: lane's 16 bytes of each 512
+  // token (t, b): the one to be copied, then the one to be worked on
+  unsigned at = line / p.B, ab = line % p.B, t = at, b = ab;
+  auto next = [&](unsigned& t, unsigned& b) {
+    t += dt, b += db;
+    if (b >= (unsigned)p.B) b -= p.B, ++t;
+  };
   auto bring = [&](int stage) {
-    if (ahead.there(p)) {
-      const bool isq = ahead.g < nbq;
-      const int h0 = (isq ? ahead.g : ahead.g - nbq) * HPW * C::BATCH, n = (isq ? p.NQ : p.NK) - h0;
+    if (at < (unsigned)p.T) {
+      uint32_t to = smem_u32(ring + stage * size * (BWD ? 2 : 1)) + 16 * lane;
 #pragma unroll
-      for (int k = 0; k < (BWD ? 2 : 1); ++k) {
-        const long long* st = k ? (isq ? p.dqs : p.dks) : (isq ? p.qs : p.ks);
-        const T* x = static_cast<const T*>(k ? (isq ? p.dq : p.dk) : (isq ? p.q : p.k)) + ahead.t * st[0] + ahead.b * st[1] + h0 * st[2];
-        const uint32_t to = smem_u32(ring + stage * C::STAGE + k * C::PART) + 16 * lane;
+      for (int k = 0; k < (BWD ? 4 : 2); ++k) {
+        const long long* st = k == 0 ? p.qs : k == 1 ? p.ks : k == 2 ? p.dqs : p.dks;
+        const void* base = k == 0 ? p.q : k == 1 ? p.k : k == 2 ? p.dq : p.dk;
+        const int H = k % 2 ? p.NK : p.NQ, n = k % 2 ? nk : nq;
+        const T* x = static_cast<const T*>(base) + at * st[0] + ab * st[1];
 #pragma unroll
         for (int c = 0; c < C::COPIES; ++c) {
-          constexpr int E = 16 / sizeof(T);  // values of a copy
-          const int at = (c * 32 + lane) * E, h = at / D;
-          const T* from = x + h * st[2] + at % D;
-#pragma unroll
-          for (int i = 0; i < C::BATCH; ++i)
-            if (i * HPW + h < n) cp_async16(to + i * C::SWEEP + c * 512, from + i * HPW * st[2]);
+          const int v = (c * 32 + lane) * C::E, h = v / D;
+          const T* from = x + h * st[2] + v % D;
+          uint32_t d = to + c * 512;
+#pragma unroll 3
+          for (int i = 0; i < n; ++i) {
+            if (i * HPW + h < H) cp_async16(d, from);
+            from += HPW * st[2], d += C::SWEEP;
+          }
         }
+        to += n * C::SWEEP;
       }
     }
     cp_async_commit();
-    ahead.next(p, groups, dt, db);
+    next(at, ab);
   };
 #pragma unroll
-  for (int k = 0; k < C::STAGES - 1; ++k) bring(k);
+  for (int k = 0; k < STAGES - 1; ++k) bring(k);
   sh.load(p);
   constexpr float inv = 1.f / D;
+  const Pairs wq = w.weights(sh.w[0]), wk = w.weights(sh.w[1]);
   Pairs sq, sk;
 #pragma unroll
   for (int j = 0; j < 2; ++j) sq.a[j] = sq.b[j] = sk.a[j] = sk.b[j] = Num<2>(0.f);
   Turn tn;
-  long long pos = it.there(p) ? position(p, it.t, it.b) : 0;
-  for (int stage = 0; it.there(p); stage = stage + 1 == C::STAGES ? 0 : stage + 1) {
-    bring(stage == 0 ? C::STAGES - 1 : stage - 1);
-    if (it.g == 0) {
-      tn = turn_of<Lanes<LPH, MODE>, LPH>(w, sh.freqs, pos);
-      Item next = it;  // the next token's position, a token ahead
-      next.g = groups - 1;
-      next.next(p, groups, dt, db);
-      if (next.there(p)) pos = position(p, next.t, next.b);
-    }
-    const bool isq = it.g < nbq;
-    const int h0 = (isq ? it.g : it.g - nbq) * HPW * C::BATCH, H = isq ? p.NQ : p.NK, n = H - h0 - w.sub;
-    T* o = static_cast<T*>(isq ? p.qo : p.ko) + (((long long)it.t * p.B + it.b) * H + h0 + w.sub) * D;
-    const Pairs wt = w.weights(sh.w[isq ? 0 : 1]);
-    cp_async_wait<C::STAGES - 1>();
-    __syncwarp();
-    const T* x = reinterpret_cast<const T*>(ring + stage * C::STAGE) + w.sub * D;
-    const T* d = reinterpret_cast<const T*>(ring + stage * C::STAGE + C::PART) + w.sub * D;
+  const bool norm = p.qw != nullptr;  // (without: weights of one, r = 1)
+  auto sweep = [&](const T* x, const T* d, T* o, const Pairs& wt, Pairs& sum, bool on) {
+    Head<T, MODE> raw;
+    w.load(raw, x);
+    Pairs y = w.get(raw);
+    const float r1 = norm ? rsqrtf(fmaf(head_sum<LPH>(dot(y, y)), inv, p.eps)) : 1.f;
+    const Num<2> r(r1);
+    if constexpr (!BWD) {
 #pragma unroll
-    for (int i = 0; i < C::BATCH; ++i) {
-      const bool on = i * HPW < n;  // (what the others compute stays in their own head)
-      Head<T, MODE> raw;
-      w.load(raw, x + i * HPW * D);
-      Pairs y = w.get(raw);
-      if constexpr (!BWD) {
-        if (p.qw) {
-          const Num<2> r(rsqrtf(fmaf(head_sum<LPH>(dot(y, y)), inv, p.eps)));
+      for (int j = 0; j < 2; ++j) y.a[j] = y.a[j] * (r * wt.a[j]), y.b[j] = y.b[j] * (r * wt.b[j]);
+      rotate(y, tn.c, tn.s, tn.n);
+      if (on) w.store(o, y);
+    } else {
+      Head<T, MODE> rd;
+      w.load(rd, d);
+      Pairs g = w.get(rd), gw;
+      rotate(g, tn.c, tn.n, tn.s);  // back
 #pragma unroll
-          for (int j = 0; j < 2; ++j) y.a[j] = y.a[j] * (r * wt.a[j]), y.b[j] = y.b[j] * (r * wt.b[j]);
+      for (int j = 0; j < 2; ++j) gw.a[j] = g.a[j] * wt.a[j], gw.b[j] = g.b[j] * wt.b[j];
+      const float along = head_sum<LPH>(dot(gw, y));
+      const Num<2> m(norm ? -(along * inv) * r1 * r1 : 0.f);  // - mean(w g xh) r
+      if (on)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          sum.a[j] = fma(g.a[j], y.a[j] * r, sum.a[j]);
+          sum.b[j] = fma(g.b[j], y.b[j] * r, sum.b[j]);
         }
-        rotate(y, tn.c, tn.s, tn.n);
-        if (on) w.store(o + i * HPW * D, y);
-      } else {
-        Head<T, MODE> rd;
-        w.load(rd, d + i * HPW * D);
-        Pairs g = w.get(rd);
-        rotate(g, tn.c, tn.n, tn.s);  // back
-        if (p.qw) {
-          Pairs gw;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) gw.a[j] = g.a[j] * wt.a[j], gw.b[j] = g.b[j] * wt.b[j];
-          const float r = rsqrtf(fmaf(head_sum<LPH>(dot(y, y)), inv, p.eps));
-          const Num<2> m(-(head_sum<LPH>(dot(gw, y)) * inv) * r * r), rr(r);  // - mean(w g xh) r
-          if (on) {
-            Pairs z;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) z.a[j] = y.a[j] * rr, z.b[j] = y.b[j] * rr;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (isq)
-                sq.a[j] = fma(g.a[j], z.a[j], sq.a[j]), sq.b[j] = fma(g.b[j], z.b[j], sq.b[j]);
-              else
-                sk.a[j] = fma(g.a[j], z.a[j], sk.a[j]), sk.b[j] = fma(g.b[j], z.b[j], sk.b[j]);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            g.a[j] = rr * fma(m, y.a[j], gw.a[j]);
-            g.b[j] = rr * fma(m, y.b[j], gw.b[j]);
-          }
-        }
-        if (on) w.store(o + i * HPW * D, g);
+      for (int j = 0; j < 2; ++j) {
+        g.a[j] = r * fma(m, y.a[j], gw.a[j]);
+        g.b[j] = r * fma(m, y.b[j], gw.b[j]);
       }
+      if (on) w.store(o, g);
     }
+  };
+  auto heads = [&](const T* x, const T* d, T* o, int n, const Pairs& wt, Pairs& sum) {
+#pragma unroll 3
+    for (int i = n / HPW; i > 0; --i) {
+      sweep(x, d, o, wt, sum, true);
+      x += HPW * D, d += HPW * D, o += HPW * D;
+    }
+    if (n % HPW) sweep(x, d, o, wt, sum, w.sub < n % HPW);  // (what the others compute stays in their own head)
+  };
+  long long pos = t < (unsigned)p.T ? position(p, t, b) : 0;
+  const int mine = w.sub * D;
+  T* qo = static_cast<T*>(p.qo) + (long long)line * p.NQ * D + mine;
+  T* ko = static_cast<T*>(p.ko) + (long long)line * p.NK * D + mine;
+  for (int stage = 0; t < (unsigned)p.T; stage = stage + 1 == STAGES ? 0 : stage + 1) {
+    bring(stage == 0 ? STAGES - 1 : stage - 1);
+    tn = turn_of<Lanes<LPH, MODE>, LPH>(w, sh.freqs, pos);
+    next(t, b);
+    if (t < (unsigned)p.T) pos = position(p, t, b);  // a token ahead
+    cp_async_wait<STAGES - 1>();
+    __syncwarp();
+    const T* x = reinterpret_cast<const T*>(ring + stage * size * (BWD ? 2 : 1)) + mine;
+    const T* d = BWD ? x + size / (int)sizeof(T) : x;
+    heads(x, d, qo, p.NQ, wq, sq);
+    heads(x + nq * HPW * D, d + nq * HPW * D, ko, p.NK, wk, sk);
     __syncwarp();  // (the stage is filled again by the next copies)
-    it.next(p, groups, dt, db);
+    qo += (long long)lines * p.NQ * D, ko += (long long)lines * p.NK * D;
   }
   if constexpr (BWD) {
     if (!p.qw) return;
@@ -737,23 +732,27 @@ bool ring_form(const RotaryParams& p, bool bwd) {
   };
   bool ok = p.D == 8 * LPH && vector_form<T>(p, bwd) && even(p.q, p.qs) && even(p.k, p.ks);
   if (bwd) ok = ok && even(p.dq, p.dqs) && even(p.dk, p.dks);
+  ok = ok && (bwd ? 4 : 2) * 8LL * Ring<T, LPH>::sweeps(p) * Ring<T, LPH>::SWEEP <= kRingMost;
   return ok && (long long)p.T * p.B >= kRingTokens * sm_count();
 }
-template <class T, int LPH, int MODE, bool BWD>
-int launch_ring(const RotaryParams& p, cudaStream_t s) {
-  using C = Ring<T, LPH, BWD>;
+template <class T, int LPH, int MODE, bool BWD, int STAGES>
+int launch_stages(const RotaryParams& p, size_t smem, cudaStream_t s) {
   static int prep[64][5];
-  int e = prepare_launch(prep, rotary_ring_kernel<T, LPH, MODE, BWD>, C::SMEM, 256, 1);
+  int e = prepare_launch(prep, rotary_ring_kernel<T, LPH, MODE, BWD, STAGES>, (uint32_t)smem, 256, 1);
   if (e != 0) return e;
-  const long long want = ((long long)p.T * p.B + 7) / 8, most = (long long)C::CTAS * sm_count();
+  const long long want = ((long long)p.T * p.B + 7) / 8, most = (BWD || sizeof(T) == 4 ? 2LL : 3LL) * sm_count();
   unsigned grid = (unsigned)(want < most ? want : most);
   if (BWD && grid > kRotaryParts) grid = kRotaryParts;
-  e = launch_dependent(rotary_ring_kernel<T, LPH, MODE, BWD>, grid, 256, C::SMEM, s, p);
+  e = launch_dependent(rotary_ring_kernel<T, LPH, MODE, BWD, STAGES>, grid, 256, smem, s, p);
   return e != 0 || !BWD || !p.qw ? e : reduce_dw(p, (int)grid, s);
 }
 template <class T, int LPH, int MODE>
 int launch_ring(const RotaryParams& p, bool bwd, cudaStream_t s) {
-  return bwd ? launch_ring<T, LPH, MODE, true>(p, s) : launch_ring<T, LPH, MODE, false>(p, s);
+  const size_t token = 8 * (size_t)Ring<T, LPH>::sweeps(p) * Ring<T, LPH>::SWEEP;  // of the CTA's eight warps
+  if (bwd) return launch_stages<T, LPH, MODE, true, 2>(p, 4 * token, s);
+  // two tokens on their way where three CTAs still fit an SM
+  return 3 * token <= kRingThree ? launch_stages<T, LPH, MODE, false, 3>(p, 3 * token, s)
+                                 : launch_stages<T, LPH, MODE, false, 2>(p, 2 * token, s);
 }
 template <class T, int LPH>
 int launch_mode(RotaryParams& p, bool bwd, cudaStream_t s) {
