@@ -1,8 +1,8 @@
 // Gated linear recurrence on tiles that TMA brings: head sizes that are multiples of 16 bytes, from a few tokens on (the
 // mathematics and the other sizes: gated.cu).
 //
-// A CTA takes 64 channels of a head of one row, and goes through time in rounds of 64 tokens; the CTAs of a cluster take
-// neighbouring rounds at once.  A control warp keeps a ring of tiles [64 tokens][gates][64 channels] filled.  Eight warps
+// A CTA takes 64 (or 32) channels of a head of one row, and goes through time in rounds of 64 (128) tokens; the CTAs of a cluster take
+// neighbouring rounds at once.  A control warp keeps a ring of tiles [tokens][gates][channels] filled.  Eight warps
 // take a run of 8 tokens each: gates and the run's map c -> A c + U in registers, the map handed to
 // one more warp, which composes the maps in the order of time -- those of the cluster's CTAs after
 // exchanging them by st.async -- and hands every run the state at its start; then the run once more, its results written into
@@ -22,11 +22,10 @@
 namespace srnn {
 namespace {
 
-constexpr int kS = kRunTokens, kW = kRunWarps, kC = kRunChunk, kX = 64;  // channels of a tile
+constexpr int kS = kRunTokens, kW = kRunWarps;
 constexpr int kThreads = 32 * (kW + 2);
 constexpr int kTalk = 32 * (kW + 1);            // threads of the runs and of the maps
 constexpr int kReady = 1, kStart = 2;           // named barriers: maps there, starts there
-constexpr uint32_t kMapBytes = kX * 8;
 // c -> a c + u of two neighbouring channels, as 16 bytes of shared memory
 struct Map2 {
   Num<2> a, u;
@@ -43,23 +42,25 @@ __device__ __forceinline__ Map2 get(const float4* at) {
 }
 
 struct TileMaps {
-  CUtensorMap wx;                 // [T, B, NH G, D], box [64, 1, G, 64]
+  CUtensorMap wx;                 // [T, B, NH G, D], box [TOKENS, 1, G, X]
   CUtensorMap out;                // y, or dWx by runs
-  CUtensorMap dy, stash;          // gradient alone: box [64, 1, 1, 64], [8 runs, 1, 1, 64]
+  CUtensorMap dy, stash;          // gradient alone: box [TOKENS, 1, 1, X], [RUNS, 1, 1, X]
 };
 
-template <class T, int G, bool BWD>
+// X: channels of a tile, 64 or 32; a warp takes 64 / X runs at once, PL lanes each
+template <class T, int G, bool BWD, int X>
 struct Tile {
-  static constexpr uint32_t ROW = kX * sizeof(T), TOK = G * ROW;
-  static constexpr uint32_t WX = kC * TOK, DY = BWD ? kC * ROW : 0, ST = BWD ? kW * kX * 4 : 0;
+  static constexpr int PL = X / 2, RUNS = kW * 64 / X, TOKENS = RUNS * kS;
+  static constexpr uint32_t ROW = X * sizeof(T), TOK = G * ROW, MAPS = X * 8;  // bytes; of a run's maps
+  static constexpr uint32_t WX = TOKENS * TOK, DY = BWD ? TOKENS * ROW : 0, ST = BWD ? RUNS * X * 4 : 0;
   static constexpr uint32_t STAGE = WX + DY + ST;
   // CTAs of an SM, as registers (64 for three, 96 for two) and shared memory allow
   static constexpr int CTAS = !BWD && sizeof(T) == 2 ? 3 : STAGE <= 50 * 1024 ? 2 : 1;
-  static constexpr uint32_t REST = kW * kMapBytes + kW * kX * 4 + 256 + 128 + 2048;
+  static constexpr uint32_t REST = RUNS * MAPS + RUNS * X * 4 + 256 + 128 + 2048;
   static constexpr int FIT = (int)((224 * 1024 / CTAS - REST) / STAGE), STAGES = FIT > 3 ? 3 : FIT;
-  static constexpr uint32_t PART = STAGES * STAGE, START = PART + kW * kMapBytes, BARS = START + kW * kX * 4,
+  static constexpr uint32_t PART = STAGES * STAGE, START = PART + RUNS * MAPS, BARS = START + RUNS * X * 4,
                             ALL = BARS + 256;
-  static constexpr uint32_t smem(int cs) { return ALL + (cs > 1 ? 2 * cs * kMapBytes : 0) + 128; }
+  static constexpr uint32_t smem(int cs) { return ALL + (cs > 1 ? 2 * cs * MAPS : 0) + 128; }
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint32_t bar) {
@@ -126,9 +127,9 @@ __device__ __forceinline__ void put2<float>(uint32_t at, const Num<2>& a) {
 }
 
 // One run of a round, forward: maps first, results second.  FULL: all its tokens count (else the first n do).
-template <class T, int G, bool FULL>
+template <class T, int G, int X, bool FULL>
 struct Forward {
-  using C = Tile<T, G, false>;
+  using C = Tile<T, G, false, X>;
   static constexpr int F = G == 4 ? 1 : 0, Z = F + 1, O = G == 2 ? 0 : F + 2;
   static __device__ __forceinline__ void maps(uint32_t x, int n, Num<2> (&a)[kS], Num<2> (&u)[kS], Num<2>& ma, Num<2>& mu) {
     ma = Num<2>(1.f), mu = Num<2>(0.f);
@@ -156,9 +157,9 @@ struct Forward {
   }
 };
 
-template <class T, int G, bool FULL>
+template <class T, int G, int X, bool FULL>
 struct Backward {
-  using C = Tile<T, G, true>;
+  using C = Tile<T, G, true, X>;
   static constexpr int F = G == 4 ? 1 : 0, Z = F + 1, O = G == 2 ? 0 : F + 2;
   static __device__ __forceinline__ void maps(uint32_t x, uint32_t dy, int n, Num<2> (&a)[kS], Num<2> (&b)[kS], Num<2>& ma,
                                               Num<2>& mu) {
@@ -206,26 +207,27 @@ struct Backward {
   }
 };
 
-template <class T, int G, bool BWD>
-__global__ void __launch_bounds__(kThreads, Tile<T, G, BWD>::CTAS)
+template <class T, int G, bool BWD, int X>
+__global__ void __launch_bounds__(kThreads, (Tile<T, G, BWD, X>::CTAS))
     gated_tile_kernel(const GatedParams p, const __grid_constant__ TileMaps maps) {
-  using C = Tile<T, G, BWD>;
+  using C = Tile<T, G, BWD, X>;
+  constexpr int PL = C::PL;
   extern __shared__ char dyn[];
   __shared__ int gave_up_s;
   const uint32_t sm = (smem_u32(dyn) + 127u) & ~127u;
   char* const sp = dyn + (sm - smem_u32(dyn));
-  float4* const part = reinterpret_cast<float4*>(sp + C::PART);    // maps of the runs: [kW][32 pairs of channels]
+  float4* const part = reinterpret_cast<float4*>(sp + C::PART);    // maps of the runs: [RUNS][PL pairs of channels]
   float2* const start = reinterpret_cast<float2*>(sp + C::START);  // states before them: the same
-  float4* const all = reinterpret_cast<float4*>(sp + C::ALL);      // maps of the CTAs: [2][cs][32]
+  float4* const all = reinterpret_cast<float4*>(sp + C::ALL);      // maps of the CTAs: [2][cs][PL]
   const uint32_t full = sm + C::BARS, empty = full + 8 * C::STAGES, swap = empty + 8 * C::STAGES;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, cs = p.cs;
   const int rank = (int)(blockIdx.x % cs);
   const unsigned id = blockIdx.x / cs;
-  const int b = (int)(id / p.tiles), tile = (int)(id % p.tiles), per = (p.D + kX - 1) / kX;
-  const int head = tile / per, c0 = tile % per * kX;
+  const int b = (int)(id / p.tiles), tile = (int)(id % p.tiles), per = (p.D + X - 1) / X;
+  const int head = tile / per, c0 = tile % per * X, pl = lane % PL, sub = lane / PL;
   depend_launch();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::STAGES; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, kW);
+    for (int i = 0; i < C::STAGES; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, C::RUNS);
     mbar_init(swap, 1), mbar_init(swap + 8, 1);
     gave_up_s = 0;
     fence_mbar_init();
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, Tile<T, G, BWD>::CTAS)
   const Wait wait{p.status, p.timeout_ns, &gave_up_s};
   int len = p.T;
   if (p.lens) len = min(max(p.lens[b], 0), p.T);
-  const int step = cs * kC, rounds = (len + step - 1) / step;
+  const int step = cs * C::TOKENS, rounds = (len + step - 1) / step;
   __syncwarp();
   if (cs > 1) cluster_sync();  // every CTA's barriers are there
   auto round_of = [&](int i) { return BWD ? rounds - 1 - i : i; };
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, Tile<T, G, BWD>::CTAS)
         if (i >= C::STAGES) wait.on(empty + 8 * st, (i / C::STAGES - 1) & 1);
         if (gave_up_s) break;
         const uint32_t at = sm + st * C::STAGE, bar = full + 8 * st;
-        const int t0 = round_of(i) * step + rank * kC;
+        const int t0 = round_of(i) * step + rank * C::TOKENS;
         mbar_arrive_expect_tx(bar, C::STAGE);
         tma_load_4d(at, &maps.wx, c0, head * G, b, t0, bar);
         if (BWD) {
@@ -268,114 +270,134 @@ __global__ void __launch_bounds__(kThreads, Tile<T, G, BWD>::CTAS)
         }
     }
     __syncwarp();
-  } else if (warp == kW) {  // ---- maps: two channels a thread
+  } else if (warp == kW) {  // ---- maps: two channels a thread, the lanes of one `sub` eight runs that follow one another
     const float* from = BWD ? p.dstateT : p.state0;
     float* const to = BWD ? p.dstate0 : p.stateT;
-    const int c = c0 + 2 * lane;  // (D is even)
+    const int c = c0 + 2 * pl;  // (D is even)
     const long long at = (long long)b * p.N + (long long)head * p.D + c;
     Num<2> h(0.f);
     if (from && c < p.D) h.x = make_float2(from[at], from[at + 1]);
+    auto other = [&](const Num<2>& x) {  // of the lane with the same channels
+      Num<2> y;
+      y.x = make_float2(__shfl_xor_sync(0xffffffffu, x.x.x, 16), __shfl_xor_sync(0xffffffffu, x.x.y, 16));
+      return y;
+    };
     for (int i = 0; i < rounds; ++i) {
       bar_sync(kReady, kTalk);
-      Map2 m[kW];
+      Map2 m[8];
 #pragma unroll
-      for (int w = 0; w < kW; ++w) m[w] = get(part + (BWD ? kW - 1 - w : w) * 32 + lane);
+      for (int w = 0; w < 8; ++w) {
+        const int r = sub * 8 + w;
+        m[w] = get(part + (BWD ? C::RUNS - 1 - r : r) * PL + pl);
+      }
       Num<2> in = h;
-      if (cs > 1) {
-        Map2 t = m[0];
+      Map2 t = m[0], first = t;  // of the lane's runs; of those of the lane before it
+      if (cs > 1 || PL == 16) {
 #pragma unroll
-        for (int w = 1; w < kW; ++w) {
+        for (int w = 1; w < 8; ++w) {
           t.u = fma(m[w].a, t.u, m[w].u);
           t.a = m[w].a * t.a;
         }
-        const uint32_t bar = swap + 8 * (i & 1), slot = smem_u32(&all[((i & 1) * cs + rank) * 32 + lane]);
+        if constexpr (PL == 16) {
+          const Map2 o{other(t.a), other(t.u)};
+          first = sub ? o : t;
+          const Map2 last = sub ? t : o;
+          t.u = fma(last.a, first.u, last.u);
+          t.a = last.a * first.a;
+        }
+      }
+      if (cs > 1) {
+        const uint32_t bar = swap + 8 * (i & 1), slot = smem_u32(&all[((i & 1) * cs + rank) * PL + pl]);
         const uint32_t v[4] = {__float_as_uint(t.a.x.x), __float_as_uint(t.a.x.y), __float_as_uint(t.u.x.x),
                                __float_as_uint(t.u.x.y)};
         if (!gave_up_s) {
-          if (lane == 0) mbar_arrive_expect_tx(bar, cs * kMapBytes);
+          if (lane == 0) mbar_arrive_expect_tx(bar, cs * C::MAPS);
           // (a CTA sends round i + 2 after it has round i + 1 from this one, which has then read round i)
-          for (int r = 0; r < cs; ++r) st_async_v4(mapa(slot, (uint32_t)r), v, mapa(bar, (uint32_t)r));
+          for (int r = sub; r < cs; r += 32 / PL) st_async_v4(mapa(slot, (uint32_t)r), v, mapa(bar, (uint32_t)r));
           wait.on<true>(bar, (i >> 1) & 1);
         }
-        const float4* x = all + (i & 1) * cs * 32 + lane;
+        const float4* x = all + (i & 1) * cs * PL + pl;
 #pragma unroll 4
         for (int j = 0; j < cs; ++j) {
           const int r = BWD ? cs - 1 - j : j;
-          const Map2 y = get(x + r * 32);
+          const Map2 y = get(x + r * PL);
           if (r == rank) in = h;
           h = fma(y.a, h, y.u);
         }
+      } else if (PL == 16) {
+        h = fma(t.a, h, t.u);
       }
+      if (PL == 16 && sub) in = fma(first.a, in, first.u);
 #pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        start[(BWD ? kW - 1 - w : w) * 32 + lane] = in.x;
+      for (int w = 0; w < 8; ++w) {
+        const int r = sub * 8 + w;
+        start[(BWD ? C::RUNS - 1 - r : r) * PL + pl] = in.x;
         in = fma(m[w].a, in, m[w].u);
       }
-      if (cs == 1) h = in;
+      if (cs == 1 && PL == 32) h = in;
       bar_arrive(kStart, kTalk);
     }
-    if (to && rank == 0 && c < p.D) to[at] = h.x.x, to[at + 1] = h.x.y;
+    if (to && rank == 0 && sub == 0 && c < p.D) to[at] = h.x.x, to[at + 1] = h.x.y;
   } else {  // ---- runs
-    const uint32_t mine = sm + warp * kS * C::TOK + lane * 2 * sizeof(T);
+    const int run = warp * (32 / PL) + sub;
+    const uint32_t base = sm + run * kS * C::TOK, mine = base + pl * 2 * sizeof(T);
     const long long ystep = (long long)p.B * p.N;
-    const bool on = c0 + 2 * lane < p.D;
-    float* const stash = p.stash + (long long)b * p.N + (long long)head * p.D + c0 + 2 * lane;
+    const bool on = c0 + 2 * pl < p.D, tell = pl == 0;  // tell: the lane that speaks for the run
+    float* const stash = p.stash + (long long)b * p.N + (long long)head * p.D + c0 + 2 * pl;
     int prev = -1;  // the stage whose results are on their way out
-    auto release = [&] {
-      if (prev >= 0 && lane == 0) {
-        bulk_wait_read_all();
-        mbar_arrive(empty + 8 * prev);
-      }
-    };
     for (int i = 0; i < rounds; ++i) {
-      const int st = i % C::STAGES, t0 = round_of(i) * step + rank * kC + warp * kS, n = len - t0;
-      const uint32_t x = mine + st * C::STAGE, dy = sm + st * C::STAGE + C::WX + warp * kS * C::ROW + lane * 2 * sizeof(T);
+      const int st = i % C::STAGES, t0 = round_of(i) * step + rank * C::TOKENS + run * kS, n = len - t0;
+      const uint32_t x = mine + st * C::STAGE;
+      const uint32_t dy = sm + st * C::STAGE + C::WX + run * kS * C::ROW + pl * 2 * sizeof(T);
+      const bool whole = PL == 32 ? n >= kS : __all_sync(0xffffffffu, n >= kS);
       wait.on(full + 8 * st, (i / C::STAGES) & 1);
       Num<2> a[kS], u[kS], ma, mu;
       if constexpr (BWD) {
-        if (n >= kS)
-          Backward<T, G, true>::maps(x, dy, n, a, u, ma, mu);
+        if (whole)
+          Backward<T, G, X, true>::maps(x, dy, n, a, u, ma, mu);
         else
-          Backward<T, G, false>::maps(x, dy, n, a, u, ma, mu);
+          Backward<T, G, X, false>::maps(x, dy, n, a, u, ma, mu);
       } else {
-        if (n >= kS)
-          Forward<T, G, true>::maps(x, n, a, u, ma, mu);
+        if (whole)
+          Forward<T, G, X, true>::maps(x, n, a, u, ma, mu);
         else
-          Forward<T, G, false>::maps(x, n, a, u, ma, mu);
+          Forward<T, G, X, false>::maps(x, n, a, u, ma, mu);
       }
-      put(part + warp * 32 + lane, ma, mu);
+      put(part + run * PL + pl, ma, mu);
+      __syncwarp();
       bar_arrive(kReady, kTalk);
-      release();
+      if (prev >= 0 && tell) {
+        bulk_wait_read_all();
+        mbar_arrive(empty + 8 * prev);
+      }
+      __syncwarp();
       bar_sync(kStart, kTalk);
       Num<2> c;
-      c.x = start[warp * 32 + lane];
+      c.x = start[run * PL + pl];
       if constexpr (BWD) {
-        Num<2> before;
-        const uint32_t sa = sm + st * C::STAGE + C::WX + C::DY + (warp * kX + 2 * lane) * 4;
-        before = get2<float>(sa);
-        if (n >= kS)
-          Backward<T, G, true>::results(x, dy, n, a, u, before, c);
+        const Num<2> before = get2<float>(sm + st * C::STAGE + C::WX + C::DY + (run * X + 2 * pl) * 4);
+        if (whole)
+          Backward<T, G, X, true>::results(x, dy, n, a, u, before, c);
         else
-          Backward<T, G, false>::results(x, dy, n, a, u, before, c);
+          Backward<T, G, X, false>::results(x, dy, n, a, u, before, c);
       } else {
         if (p.stash && on && n > 0) *reinterpret_cast<float2*>(stash + t0 / kS * ystep) = c.x;
-        if (n >= kS)
-          Forward<T, G, true>::results(x, n, a, u, c);
+        if (whole)
+          Forward<T, G, X, true>::results(x, n, a, u, c);
         else
-          Forward<T, G, false>::results(x, n, a, u, c);
+          Forward<T, G, X, false>::results(x, n, a, u, c);
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        if (t0 < p.T) tma_store_4d(&maps.out, c0, BWD ? head * G : head, b, t0, sm + st * C::STAGE + warp * kS * C::TOK);
+      if (tell) {
+        if (t0 < p.T) tma_store_4d(&maps.out, c0, BWD ? head * G : head, b, t0, base + st * C::STAGE);
         bulk_commit();
       }
       prev = st;
     }
     // rows of zeros behind the last round: from a run's place in the first stage, which nothing uses any more
-    long long t = (long long)rounds * step + rank * kC + warp * kS;
-    if (t < p.T) {
-      if (lane == 0) bulk_wait_read_all();
+    if (rounds * (long long)step < p.T) {
+      if (tell) bulk_wait_read_all();
       __syncwarp();
 #pragma unroll
       for (int s = 0; s < kS; ++s)
@@ -383,13 +405,15 @@ __global__ void __launch_bounds__(kThreads, Tile<T, G, BWD>::CTAS)
         for (int j = 0; j < (BWD ? G : 1); ++j) put2<T>(mine + (BWD ? s * C::TOK + j * C::ROW : s * C::ROW), Num<2>(0.f));
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        for (; t < p.T; t += step) tma_store_4d(&maps.out, c0, BWD ? head * G : head, b, (int)t, sm + warp * kS * C::TOK);
+      if (tell) {
+        for (long long t = (long long)rounds * step + rank * C::TOKENS + run * kS; t < p.T; t += step)
+          tma_store_4d(&maps.out, c0, BWD ? head * G : head, b, (int)t, base);
         bulk_commit();
       }
     }
-    if (lane == 0) bulk_wait_all();
+    if (tell) bulk_wait_all();
   }
+  __syncwarp();
   if (cs > 1) {
     __syncthreads();
     cluster_sync();
@@ -410,62 +434,81 @@ EncodeTiledFn encode_fn();  // tc_gemm.cu
 
 namespace {
 
-// [T, B, heads, D] contiguous, boxes of `rows` tokens, `h` heads and 64 channels
-bool encode(CUtensorMap* map, const void* ptr, bool bf16, long long D, long long heads, long long B, long long T, uint32_t h,
-            uint32_t rows) {
+// [T, B, heads, D] contiguous, boxes of `rows` tokens, `h` heads and `x` channels
+bool encode(CUtensorMap* map, const void* ptr, bool bf16, long long D, long long heads, long long B, long long T, uint32_t x,
+            uint32_t h, uint32_t rows) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr || reinterpret_cast<uintptr_t>(ptr) % 16 != 0) return false;
   const cuuint64_t es = bf16 ? 2 : 4, d = (cuuint64_t)D * es;
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)B, (cuuint64_t)T};
   const cuuint64_t strides[3] = {d, d * heads, d * heads * B};
-  const cuuint32_t box[4] = {kX, h, 1, rows}, ones[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {x, h, 1, rows}, ones[4] = {1, 1, 1, 1};
   return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void*>(ptr), dims,
             strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class T, int G, bool BWD>
-int launch_tile(GatedParams p, cudaStream_t s) {
-  using C = Tile<T, G, BWD>;
+template <class T, int G, bool BWD, int X>
+int launch_tile(GatedParams p, int cs, cudaStream_t s) {
+  using C = Tile<T, G, BWD, X>;
   const bool bf16 = sizeof(T) == 2;
   const long long NH = p.N / p.D;
   TileMaps m;
-  bool ok = encode(&m.wx, p.wx, bf16, p.D, NH * G, p.B, p.T, G, kC);
+  bool ok = encode(&m.wx, p.wx, bf16, p.D, NH * G, p.B, p.T, X, G, C::TOKENS);
   if (BWD)
-    ok = ok && encode(&m.out, p.dwx, bf16, p.D, NH * G, p.B, p.T, G, kS) && encode(&m.dy, p.dy, bf16, p.D, NH, p.B, p.T, 1, kC) &&
-         encode(&m.stash, p.stash, false, p.D, NH, p.B, (p.T + kS - 1) / kS, 1, kW);
+    ok = ok && encode(&m.out, p.dwx, bf16, p.D, NH * G, p.B, p.T, X, G, kS) &&
+         encode(&m.dy, p.dy, bf16, p.D, NH, p.B, p.T, X, 1, C::TOKENS) &&
+         encode(&m.stash, p.stash, false, p.D, NH, p.B, (p.T + kS - 1) / kS, X, 1, C::RUNS);
   else
-    ok = ok && encode(&m.out, p.y, bf16, p.D, NH, p.B, p.T, 1, kS) && reinterpret_cast<uintptr_t>(p.stash) % 8 == 0;
+    ok = ok && encode(&m.out, p.y, bf16, p.D, NH, p.B, p.T, X, 1, kS) && reinterpret_cast<uintptr_t>(p.stash) % 8 == 0;
   if (!ok) return kGatedNoTile;
-  p.tiles = (int)(NH * ((p.D + kX - 1) / kX));
-  const long long tiles = (long long)p.tiles * p.B, room = (long long)C::CTAS * sm_count();
-  p.cs = 1;
-  while (p.cs < kGatedCluster && 2 * tiles * p.cs <= room && p.cs * kC < p.T) p.cs *= 2;
-  if (tiles * p.cs > 0x7fffffff) return (int)cudaErrorInvalidConfiguration;
+  p.tiles = (int)(NH * ((p.D + X - 1) / X));
+  p.cs = cs;
+  const long long ctas = (long long)p.tiles * p.B * cs;
+  if (ctas > 0x7fffffff) return (int)cudaErrorInvalidConfiguration;
   static int prep[64][5];
-  const int e = prepare_launch(prep, gated_tile_kernel<T, G, BWD>, C::smem(kGatedCluster), kThreads, p.cs);
+  const int e = prepare_launch(prep, gated_tile_kernel<T, G, BWD, X>, C::smem(kGatedCluster), kThreads, cs);
   if (e != 0) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * p.cs));
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
   // few CTAs: shared memory asked for so that the SMs share them out evenly (a cluster's would pack three to an SM)
-  const uint32_t each = (uint32_t)((tiles * p.cs + sm_count() - 1) / sm_count());
+  const uint32_t each = (uint32_t)((ctas + sm_count() - 1) / sm_count());
   const uint32_t spread = each < (uint32_t)C::CTAS ? 226 * 1024 / (each + 1) + 1024 : 0;
-  cfg.dynamicSmemBytes = spread > C::smem(p.cs) ? spread : C::smem(p.cs);
+  cfg.dynamicSmemBytes = spread > C::smem(cs) ? spread : C::smem(cs);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)p.cs;
+  attr[1].val.clusterDim.x = (unsigned)cs;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.cs > 1 ? 2 : 1;
-  return (int)cudaLaunchKernelEx(&cfg, gated_tile_kernel<T, G, BWD>, (const GatedParams)p, (const TileMaps)m);
+  cfg.numAttrs = cs > 1 ? 2 : 1;
+  return (int)cudaLaunchKernelEx(&cfg, gated_tile_kernel<T, G, BWD, X>, (const GatedParams)p, (const TileMaps)m);
+}
+// CTAs along time: as many as an SM's places hold all at once, and as there are rounds
+template <class C>
+int clusters(const GatedParams& p, long long tiles) {
+  const long long room = (long long)C::CTAS * sm_count();
+  int cs = 1;
+  while (cs < kGatedCluster && 2 * tiles * cs <= room && cs * C::TOKENS < p.T) cs *= 2;
+  return cs;
+}
+template <class T, int G, bool BWD>
+int launch_width(const GatedParams& p, cudaStream_t s) {
+  using Wide = Tile<T, G, BWD, 64>;
+  using Narrow = Tile<T, G, BWD, 32>;
+  const long long rows = (long long)p.N / p.D * p.B, wide = rows * ((p.D + 63) / 64), narrow = rows * ((p.D + 31) / 32);
+  const int cs = clusters<Wide>(p, wide);
+  // 32 channels where 64 would leave lanes without any, or SMs without work although the clusters are as large as they go
+  if (p.T > Wide::TOKENS && (narrow < 2 * wide || (cs == kGatedCluster && 2 * wide * cs <= (long long)Narrow::CTAS * sm_count())))
+    return launch_tile<T, G, BWD, 32>(p, clusters<Narrow>(p, narrow), s);
+  return launch_tile<T, G, BWD, 64>(p, cs, s);
 }
 template <class T, int G>
 int launch_dir(const GatedParams& p, bool bwd, cudaStream_t s) {
-  return bwd ? launch_tile<T, G, true>(p, s) : launch_tile<T, G, false>(p, s);
+  return bwd ? launch_width<T, G, true>(p, s) : launch_width<T, G, false>(p, s);
 }
 template <class T>
 int launch_t(const GatedParams& p, int gates, bool bwd, cudaStream_t s) {
