@@ -25,7 +25,7 @@ namespace {
 constexpr int kS = kRunTokens, kW = kRunWarps;
 constexpr int kThreads = 32 * (kW + 2);
 constexpr int kTalk = 32 * (kW + 1);            // threads of the runs and of the maps
-constexpr int kReady = 1, kStart = 2;           // named barriers: maps there, starts there
+constexpr int kReady = 1, kStart = 3;           // named barriers, a pair of each: maps there, starts there
 // c -> a c + u of two neighbouring channels, as 16 bytes of shared memory
 struct Map2 {
   Num<2> a, u;
@@ -48,17 +48,19 @@ struct TileMaps {
 };
 
 // X: channels of a tile, 64 or 32; a warp takes 64 / X runs at once, PL lanes each
-template <class T, int G, bool BWD, int X>
+template <class T, int G, bool BWD, int X, bool AHEAD>
 struct Tile {
   static constexpr int PL = X / 2, RUNS = kW * 64 / X, TOKENS = RUNS * kS;
   static constexpr uint32_t ROW = X * sizeof(T), TOK = G * ROW, MAPS = X * 8;  // bytes; of a run's maps
   static constexpr uint32_t WX = TOKENS * TOK, DY = BWD ? TOKENS * ROW : 0, ST = BWD ? RUNS * X * 4 : 0;
   static constexpr uint32_t STAGE = WX + DY + ST;
   // CTAs of an SM, as registers (64 for three, 96 for two) and shared memory allow
-  static constexpr int CTAS = !BWD && sizeof(T) == 2 ? 3 : STAGE <= 50 * 1024 ? 2 : 1;
-  static constexpr uint32_t REST = RUNS * MAPS + RUNS * X * 4 + 256 + 128 + 2048;
-  static constexpr int FIT = (int)((224 * 1024 / CTAS - REST) / STAGE), STAGES = FIT > 3 ? 3 : FIT;
-  static constexpr uint32_t PART = STAGES * STAGE, START = PART + RUNS * MAPS, BARS = START + RUNS * X * 4,
+  static constexpr int CTAS = !BWD && sizeof(T) == 2 && !AHEAD ? 3 : STAGE <= (AHEAD ? 24 : 50) * 1024 ? 2 : 1, BUF = AHEAD ? 2 : 1;
+  static constexpr uint32_t REST = BUF * (RUNS * MAPS + RUNS * X * 4) + 256 + 128 +
+                                   (CTAS == 1 ? 2 * kGatedCluster * MAPS : 8 * MAPS);
+  static constexpr int FIT = (int)((224 * 1024 / CTAS - REST) / STAGE), MOST = AHEAD ? 4 : 3, STAGES = FIT > MOST ? MOST : FIT;
+  static_assert(STAGES >= (AHEAD ? 3 : 2), "the tile of a round ahead needs the stage of two rounds before");
+  static constexpr uint32_t PART = STAGES * STAGE, START = PART + BUF * RUNS * MAPS, BARS = START + BUF * RUNS * X * 4,
                             ALL = BARS + 256;
   static constexpr uint32_t smem(int cs) { return ALL + (cs > 1 ? 2 * cs * MAPS : 0) + 128; }
 };
@@ -129,7 +131,7 @@ __device__ __forceinline__ void put2<float>(uint32_t at, const Num<2>& a) {
 // One run of a round, forward: maps first, results second.  FULL: all its tokens count (else the first n do).
 template <class T, int G, int X, bool FULL>
 struct Forward {
-  using C = Tile<T, G, false, X>;
+  using C = Tile<T, G, false, X, false>;  // (the layout is that of both)
   static constexpr int F = G == 4 ? 1 : 0, Z = F + 1, O = G == 2 ? 0 : F + 2;
   static __device__ __forceinline__ void maps(uint32_t x, int n, Num<2> (&a)[kS], Num<2> (&u)[kS], Num<2>& ma, Num<2>& mu) {
     ma = Num<2>(1.f), mu = Num<2>(0.f);
@@ -159,7 +161,7 @@ struct Forward {
 
 template <class T, int G, int X, bool FULL>
 struct Backward {
-  using C = Tile<T, G, true, X>;
+  using C = Tile<T, G, true, X, false>;
   static constexpr int F = G == 4 ? 1 : 0, Z = F + 1, O = G == 2 ? 0 : F + 2;
   static __device__ __forceinline__ void maps(uint32_t x, uint32_t dy, int n, Num<2> (&a)[kS], Num<2> (&b)[kS], Num<2>& ma,
                                               Num<2>& mu) {
@@ -207,10 +209,11 @@ struct Backward {
   }
 };
 
-template <class T, int G, bool BWD, int X>
-__global__ void __launch_bounds__(kThreads, (Tile<T, G, BWD, X>::CTAS))
+// AHEAD: a run's maps are made a round ahead of its results, while the maps of the round before are on their way
+template <class T, int G, bool BWD, int X, bool AHEAD>
+__global__ void __launch_bounds__(kThreads, (Tile<T, G, BWD, X, AHEAD>::CTAS))
     gated_tile_kernel(const GatedParams p, const __grid_constant__ TileMaps maps) {
-  using C = Tile<T, G, BWD, X>;
+  using C = Tile<T, G, BWD, X, AHEAD>;
   constexpr int PL = C::PL;
   extern __shared__ char dyn[];
   __shared__ int gave_up_s;
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<T, G, BWD, X>::CTAS))
   depend_launch();
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, C::RUNS);
-    mbar_init(swap, 1), mbar_init(swap + 8, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(swap + 8 * i, 1);
     gave_up_s = 0;
     fence_mbar_init();
     fence_async_smem();
@@ -282,60 +285,75 @@ __global__ void __launch_bounds__(kThreads, (Tile<T, G, BWD, X>::CTAS))
       y.x = make_float2(__shfl_xor_sync(0xffffffffu, x.x.x, 16), __shfl_xor_sync(0xffffffffu, x.x.y, 16));
       return y;
     };
-    for (int i = 0; i < rounds; ++i) {
-      bar_sync(kReady, kTalk);
-      Map2 m[8];
+    struct Runs {
+      Map2 m[8], t, first;  // the lane's runs; composed: all of the CTA's, those of the lane before it
+    };
+    auto read = [&](int i, Runs& r) {
+      const int buf = AHEAD ? i & 1 : 0;
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
-        const int r = sub * 8 + w;
-        m[w] = get(part + (BWD ? C::RUNS - 1 - r : r) * PL + pl);
+        const int run = sub * 8 + w;
+        r.m[w] = get(part + (buf * C::RUNS + (BWD ? C::RUNS - 1 - run : run)) * PL + pl);
       }
-      Num<2> in = h;
-      Map2 t = m[0], first = t;  // of the lane's runs; of those of the lane before it
-      if (cs > 1 || PL == 16) {
+      if (cs == 1 && PL == 32) return;
+      r.t = r.m[0];
 #pragma unroll
-        for (int w = 1; w < 8; ++w) {
-          t.u = fma(m[w].a, t.u, m[w].u);
-          t.a = m[w].a * t.a;
-        }
-        if constexpr (PL == 16) {
-          const Map2 o{other(t.a), other(t.u)};
-          first = sub ? o : t;
-          const Map2 last = sub ? t : o;
-          t.u = fma(last.a, first.u, last.u);
-          t.a = last.a * first.a;
-        }
+      for (int w = 1; w < 8; ++w) {
+        r.t.u = fma(r.m[w].a, r.t.u, r.m[w].u);
+        r.t.a = r.m[w].a * r.t.a;
       }
+      if constexpr (PL == 16) {
+        const Map2 o{other(r.t.a), other(r.t.u)}, last = sub ? r.t : o;
+        r.first = sub ? o : r.t;
+        r.t.u = fma(last.a, r.first.u, last.u);
+        r.t.a = last.a * r.first.a;
+      }
+    };
+    // A CTA sends round i after it has the maps of round i - 1 from every CTA, which had then read all of round i - 2.  (The
+    // lanes meet at named barriers between one round and the next.)
+    auto send = [&](int i, const Runs& r) {
+      if (cs == 1 || gave_up_s) return;
+      const int buf = i % 2;
+      const uint32_t bar = swap + 8 * buf, slot = smem_u32(&all[(buf * cs + rank) * PL + pl]);
+      const uint32_t v[4] = {__float_as_uint(r.t.a.x.x), __float_as_uint(r.t.a.x.y), __float_as_uint(r.t.u.x.x),
+                             __float_as_uint(r.t.u.x.y)};
+      if (lane == 0) mbar_arrive_expect_tx(bar, cs * C::MAPS);
+      for (int k = sub; k < cs; k += 32 / PL) st_async_v4(mapa(slot, (uint32_t)k), v, mapa(bar, (uint32_t)k));
+    };
+    auto tell_starts = [&](int i, const Runs& r) {
+      Num<2> in = h;
       if (cs > 1) {
-        const uint32_t bar = swap + 8 * (i & 1), slot = smem_u32(&all[((i & 1) * cs + rank) * PL + pl]);
-        const uint32_t v[4] = {__float_as_uint(t.a.x.x), __float_as_uint(t.a.x.y), __float_as_uint(t.u.x.x),
-                               __float_as_uint(t.u.x.y)};
-        if (!gave_up_s) {
-          if (lane == 0) mbar_arrive_expect_tx(bar, cs * C::MAPS);
-          // (a CTA sends round i + 2 after it has round i + 1 from this one, which has then read round i)
-          for (int r = sub; r < cs; r += 32 / PL) st_async_v4(mapa(slot, (uint32_t)r), v, mapa(bar, (uint32_t)r));
-          wait.on<true>(bar, (i >> 1) & 1);
-        }
-        const float4* x = all + (i & 1) * cs * PL + pl;
+        const int buf = i % 2;
+        wait.on<true>(swap + 8 * buf, (i / 2) & 1);
+        const float4* x = all + buf * cs * PL + pl;
 #pragma unroll 4
         for (int j = 0; j < cs; ++j) {
-          const int r = BWD ? cs - 1 - j : j;
-          const Map2 y = get(x + r * PL);
-          if (r == rank) in = h;
+          const int k = BWD ? cs - 1 - j : j;
+          const Map2 y = get(x + k * PL);
+          if (k == rank) in = h;
           h = fma(y.a, h, y.u);
         }
       } else if (PL == 16) {
-        h = fma(t.a, h, t.u);
+        h = fma(r.t.a, h, r.t.u);
       }
-      if (PL == 16 && sub) in = fma(first.a, in, first.u);
+      if (PL == 16 && sub) in = fma(r.first.a, in, r.first.u);
+      const int buf = AHEAD ? i & 1 : 0;
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
-        const int r = sub * 8 + w;
-        start[(BWD ? C::RUNS - 1 - r : r) * PL + pl] = in.x;
-        in = fma(m[w].a, in, m[w].u);
+        const int run = sub * 8 + w;
+        start[(buf * C::RUNS + (BWD ? C::RUNS - 1 - run : run)) * PL + pl] = in.x;
+        in = fma(r.m[w].a, in, r.m[w].u);
       }
       if (cs == 1 && PL == 32) h = in;
-      bar_arrive(kStart, kTalk);
+      __syncwarp();
+      bar_arrive(kStart + buf, kTalk);
+    };
+    for (int i = 0; i < rounds; ++i) {
+      bar_sync(kReady + (AHEAD ? i & 1 : 0), kTalk);
+      Runs r;
+      read(i, r);
+      send(i, r);
+      tell_starts(i, r);
     }
     if (to && rank == 0 && sub == 0 && c < p.D) to[at] = h.x.x, to[at + 1] = h.x.y;
   } else {  // ---- runs
@@ -344,48 +362,61 @@ __global__ void __launch_bounds__(kThreads, (Tile<T, G, BWD, X>::CTAS))
     const long long ystep = (long long)p.B * p.N;
     const bool on = c0 + 2 * pl < p.D, tell = pl == 0;  // tell: the lane that speaks for the run
     float* const stash = p.stash + (long long)b * p.N + (long long)head * p.D + c0 + 2 * pl;
-    int prev = -1;  // the stage whose results are on their way out
-    for (int i = 0; i < rounds; ++i) {
-      const int st = i % C::STAGES, t0 = round_of(i) * step + rank * C::TOKENS + run * kS, n = len - t0;
+    struct Gates {  // of a round
+      Num<2> a[kS], u[kS];
+    };
+    auto first_token = [&](int i) { return round_of(i) * step + rank * C::TOKENS + run * kS; };
+    auto is_whole = [&](int n) { return PL == 32 ? n >= kS : (bool)__all_sync(0xffffffffu, n >= kS); };
+    int out = -1;  // the stage whose results are on their way out
+    auto begin = [&](int i, Gates& g) {
+      const int st = i % C::STAGES, n = len - first_token(i);
       const uint32_t x = mine + st * C::STAGE;
-      const uint32_t dy = sm + st * C::STAGE + C::WX + run * kS * C::ROW + pl * 2 * sizeof(T);
-      const bool whole = PL == 32 ? n >= kS : __all_sync(0xffffffffu, n >= kS);
+      const bool whole = is_whole(n);
       wait.on(full + 8 * st, (i / C::STAGES) & 1);
-      Num<2> a[kS], u[kS], ma, mu;
+      Num<2> ma, mu;
       if constexpr (BWD) {
+        const uint32_t dy = sm + st * C::STAGE + C::WX + run * kS * C::ROW + pl * 2 * sizeof(T);
         if (whole)
-          Backward<T, G, X, true>::maps(x, dy, n, a, u, ma, mu);
+          Backward<T, G, X, true>::maps(x, dy, n, g.a, g.u, ma, mu);
         else
-          Backward<T, G, X, false>::maps(x, dy, n, a, u, ma, mu);
+          Backward<T, G, X, false>::maps(x, dy, n, g.a, g.u, ma, mu);
       } else {
         if (whole)
-          Forward<T, G, X, true>::maps(x, n, a, u, ma, mu);
+          Forward<T, G, X, true>::maps(x, n, g.a, g.u, ma, mu);
         else
-          Forward<T, G, X, false>::maps(x, n, a, u, ma, mu);
+          Forward<T, G, X, false>::maps(x, n, g.a, g.u, ma, mu);
       }
-      put(part + run * PL + pl, ma, mu);
+      const int buf = AHEAD ? i & 1 : 0;
+      put(part + (buf * C::RUNS + run) * PL + pl, ma, mu);
       __syncwarp();
-      bar_arrive(kReady, kTalk);
-      if (prev >= 0 && tell) {
+      bar_arrive(kReady + buf, kTalk);
+      if (out >= 0 && tell) {
         bulk_wait_read_all();
-        mbar_arrive(empty + 8 * prev);
+        mbar_arrive(empty + 8 * out);
       }
+      out = -1;
+    };
+    auto finish = [&](int i, const Gates& g) {
+      const int st = i % C::STAGES, t0 = first_token(i), n = len - t0, buf = AHEAD ? i & 1 : 0;
+      const uint32_t x = mine + st * C::STAGE;
+      const bool whole = is_whole(n);
       __syncwarp();
-      bar_sync(kStart, kTalk);
+      bar_sync(kStart + buf, kTalk);
       Num<2> c;
-      c.x = start[run * PL + pl];
+      c.x = start[(buf * C::RUNS + run) * PL + pl];
       if constexpr (BWD) {
+        const uint32_t dy = sm + st * C::STAGE + C::WX + run * kS * C::ROW + pl * 2 * sizeof(T);
         const Num<2> before = get2<float>(sm + st * C::STAGE + C::WX + C::DY + (run * X + 2 * pl) * 4);
         if (whole)
-          Backward<T, G, X, true>::results(x, dy, n, a, u, before, c);
+          Backward<T, G, X, true>::results(x, dy, n, g.a, g.u, before, c);
         else
-          Backward<T, G, X, false>::results(x, dy, n, a, u, before, c);
+          Backward<T, G, X, false>::results(x, dy, n, g.a, g.u, before, c);
       } else {
         if (p.stash && on && n > 0) *reinterpret_cast<float2*>(stash + t0 / kS * ystep) = c.x;
         if (whole)
-          Forward<T, G, X, true>::results(x, n, a, u, c);
+          Forward<T, G, X, true>::results(x, n, g.a, g.u, c);
         else
-          Forward<T, G, X, false>::results(x, n, a, u, c);
+          Forward<T, G, X, false>::results(x, n, g.a, g.u, c);
       }
       fence_async_smem();
       __syncwarp();
@@ -393,7 +424,24 @@ __global__ void __launch_bounds__(kThreads, (Tile<T, G, BWD, X>::CTAS))
         if (t0 < p.T) tma_store_4d(&maps.out, c0, BWD ? head * G : head, b, t0, base + st * C::STAGE);
         bulk_commit();
       }
-      prev = st;
+      out = st;
+    };
+    if constexpr (AHEAD) {
+      Gates even, odd;
+      if (rounds > 0) begin(0, even);
+      for (int i = 0; i < rounds; i += 2) {
+        if (i + 1 < rounds) begin(i + 1, odd);
+        finish(i, even);
+        if (i + 1 >= rounds) break;
+        if (i + 2 < rounds) begin(i + 2, even);
+        finish(i + 1, odd);
+      }
+    } else {
+      Gates g;
+      for (int i = 0; i < rounds; ++i) {
+        begin(i, g);
+        finish(i, g);
+      }
     }
     // rows of zeros behind the last round: from a run's place in the first stage, which nothing uses any more
     if (rounds * (long long)step < p.T) {
@@ -448,67 +496,123 @@ bool encode(CUtensorMap* map, const void* ptr, bool bf16, long long D, long long
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class T, int G, bool BWD, int X>
-int launch_tile(GatedParams p, int cs, cudaStream_t s) {
-  using C = Tile<T, G, BWD, X>;
-  const bool bf16 = sizeof(T) == 2;
-  const long long NH = p.N / p.D;
-  TileMaps m;
-  bool ok = encode(&m.wx, p.wx, bf16, p.D, NH * G, p.B, p.T, X, G, C::TOKENS);
-  if (BWD)
-    ok = ok && encode(&m.out, p.dwx, bf16, p.D, NH * G, p.B, p.T, X, G, kS) &&
-         encode(&m.dy, p.dy, bf16, p.D, NH, p.B, p.T, X, 1, C::TOKENS) &&
-         encode(&m.stash, p.stash, false, p.D, NH, p.B, (p.T + kS - 1) / kS, X, 1, C::RUNS);
-  else
-    ok = ok && encode(&m.out, p.y, bf16, p.D, NH, p.B, p.T, X, 1, kS) && reinterpret_cast<uintptr_t>(p.stash) % 8 == 0;
-  if (!ok) return kGatedNoTile;
-  p.tiles = (int)(NH * ((p.D + X - 1) / X));
-  p.cs = cs;
-  const long long ctas = (long long)p.tiles * p.B * cs;
-  if (ctas > 0x7fffffff) return (int)cudaErrorInvalidConfiguration;
-  static int prep[64][5];
-  const int e = prepare_launch(prep, gated_tile_kernel<T, G, BWD, X>, C::smem(kGatedCluster), kThreads, cs);
-  if (e != 0) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
-  // few CTAs: shared memory asked for so that the SMs share them out evenly (a cluster's would pack three to an SM)
-  const uint32_t each = (uint32_t)((ctas + sm_count() - 1) / sm_count());
-  const uint32_t spread = each < (uint32_t)C::CTAS ? 226 * 1024 / (each + 1) + 1024 : 0;
-  cfg.dynamicSmemBytes = spread > C::smem(cs) ? spread : C::smem(cs);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cs;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cs > 1 ? 2 : 1;
-  return (int)cudaLaunchKernelEx(&cfg, gated_tile_kernel<T, G, BWD, X>, (const GatedParams)p, (const TileMaps)m);
-}
-// CTAs along time: as many as an SM's places hold all at once, and as there are rounds
-template <class C>
-int clusters(const GatedParams& p, long long tiles) {
-  const long long room = (long long)C::CTAS * sm_count();
-  int cs = 1;
-  while (cs < kGatedCluster && 2 * tiles * cs <= room && cs * C::TOKENS < p.T) cs *= 2;
-  return cs;
-}
+template <class T, int G, bool BWD, int X, bool AHEAD>
+struct Variant {
+  using C = Tile<T, G, BWD, X, AHEAD>;
+  static constexpr auto kernel = gated_tile_kernel<T, G, BWD, X, AHEAD>;
+
+  static void attributes(cudaLaunchAttribute (&attr)[2], int cs) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cs;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  }
+  // the kernel's attributes, once a device; a cudaError_t value
+  static int prepare() {
+    static int prep[64][5];
+    return prepare_launch(prep, kernel, C::smem(kGatedCluster), kThreads, kGatedCluster);
+  }
+  // clusters of cs CTAs that the device holds at once (0: none, or not to be had)
+  static int active(int cs, int dev) {
+    static int known[64][kGatedCluster + 1];  // one more than it, once asked for
+    if (dev >= 64) return 0;
+    if (known[dev][cs] == 0) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(cs);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = C::smem(cs);
+      cudaLaunchAttribute attr[2];
+      attributes(attr, cs);
+      cfg.attrs = attr + 1;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (prepare() != 0 || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+      known[dev][cs] = n + 1;
+    }
+    return known[dev][cs] - 1;
+  }
+  static int launch(GatedParams p, int cs, cudaStream_t s) {
+    const bool bf16 = sizeof(T) == 2;
+    const long long NH = p.N / p.D;
+    TileMaps m;
+    bool ok = encode(&m.wx, p.wx, bf16, p.D, NH * G, p.B, p.T, X, G, C::TOKENS);
+    if (BWD)
+      ok = ok && encode(&m.out, p.dwx, bf16, p.D, NH * G, p.B, p.T, X, G, kS) &&
+           encode(&m.dy, p.dy, bf16, p.D, NH, p.B, p.T, X, 1, C::TOKENS) &&
+           encode(&m.stash, p.stash, false, p.D, NH, p.B, (p.T + kS - 1) / kS, X, 1, C::RUNS);
+    else
+      ok = ok && encode(&m.out, p.y, bf16, p.D, NH, p.B, p.T, X, 1, kS) && reinterpret_cast<uintptr_t>(p.stash) % 8 == 0;
+    if (!ok) return kGatedNoTile;
+    p.tiles = (int)(NH * ((p.D + X - 1) / X));
+    p.cs = cs;
+    const long long ctas = (long long)p.tiles * p.B * cs;
+    if (ctas > 0x7fffffff) return (int)cudaErrorInvalidConfiguration;
+    const int e = prepare();
+    if (e != 0) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kThreads);
+    // few CTAs: shared memory asked for so that the SMs share them out evenly (a cluster's would pack three to an SM)
+    const uint32_t each = (uint32_t)((ctas + sm_count() - 1) / sm_count());
+    const uint32_t spread = each < (uint32_t)C::CTAS ? 226 * 1024 / (each + 1) + 1024 : 0;
+    cfg.dynamicSmemBytes = spread > C::smem(cs) ? spread : C::smem(cs);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attributes(attr, cs);
+    cfg.attrs = attr;
+    cfg.numAttrs = cs > 1 ? 2 : 1;
+    return (int)cudaLaunchKernelEx(&cfg, kernel, (const GatedParams)p, (const TileMaps)m);
+  }
+};
+
+// Which of them, and how many CTAs along time: the one whose rounds end first.  A round of bf16 runs of two gates takes
+// 0.76 us where maps are made ahead, else 0.80 (CTAs by themselves) or 1.13 (clusters), and 0.46 more for each other
+// CTA on the SM; other gates, types and the gradient stretch all of these alike (1.5 to 2 times).  What does not
+// fit the device at once runs after it.
+struct Plan {
+  double cost = 1e30;
+  int variant = 0, cs = 1, dev = 0, sms = sm_count();
+  Plan() { cudaGetDevice(&dev); }
+  template <class V>
+  void consider(int variant_, const GatedParams& p, bool ahead) {
+    using C = typename V::C;
+    const long long tiles = (long long)(p.N / p.D) * ((p.D + 2 * C::PL - 1) / (2 * C::PL)) * p.B;
+    const int chunks = (p.T + C::TOKENS - 1) / C::TOKENS;
+    for (int c = 1; c <= kGatedCluster && c <= chunks; ++c) {
+      const long long room = c == 1 ? (long long)C::CTAS * sms : V::active(c, dev);
+      if (room < 1) continue;
+      auto wave = [&](long long clusters) {
+        if (clusters == 0) return 0.0;
+        const long long each = (clusters * c + sms - 1) / sms;
+        const double k = (double)(each < C::CTAS ? each : C::CTAS);
+        return (chunks + c - 1) / c * ((ahead ? 0.76 : c == 1 ? 0.80 : 1.13) + 0.46 * (k - 1)) + 0.3;
+      };
+      const double t = (double)(tiles / room) * wave(room) + wave(tiles % room);
+      if (t < cost) cost = t, variant = variant_, cs = c;
+    }
+  }
+};
 template <class T, int G, bool BWD>
-int launch_width(const GatedParams& p, cudaStream_t s) {
-  using Wide = Tile<T, G, BWD, 64>;
-  using Narrow = Tile<T, G, BWD, 32>;
-  const long long rows = (long long)p.N / p.D * p.B, wide = rows * ((p.D + 63) / 64), narrow = rows * ((p.D + 31) / 32);
-  const int cs = clusters<Wide>(p, wide);
-  // 32 channels where 64 would leave lanes without any, or SMs without work although the clusters are as large as they go
-  if (p.T > Wide::TOKENS && (narrow < 2 * wide || (cs == kGatedCluster && 2 * wide * cs <= (long long)Narrow::CTAS * sm_count())))
-    return launch_tile<T, G, BWD, 32>(p, clusters<Narrow>(p, narrow), s);
-  return launch_tile<T, G, BWD, 64>(p, cs, s);
+int launch_planned(const GatedParams& p, cudaStream_t s) {
+  Plan plan;
+  plan.consider<Variant<T, G, BWD, 64, false>>(0, p, false);
+  plan.consider<Variant<T, G, BWD, 32, false>>(1, p, false);
+  constexpr bool AHEAD = !BWD && sizeof(T) == 2;  // (the others lack registers or shared memory for it)
+  if constexpr (AHEAD) {
+    plan.consider<Variant<T, G, BWD, 64, true>>(2, p, true);
+    plan.consider<Variant<T, G, BWD, 32, true>>(3, p, true);
+  }
+  switch (plan.variant) {
+    case 0: return Variant<T, G, BWD, 64, false>::launch(p, plan.cs, s);
+    case 1: return Variant<T, G, BWD, 32, false>::launch(p, plan.cs, s);
+    case 2: return Variant<T, G, BWD, 64, AHEAD>::launch(p, plan.cs, s);
+    default: return Variant<T, G, BWD, 32, AHEAD>::launch(p, plan.cs, s);
+  }
 }
 template <class T, int G>
 int launch_dir(const GatedParams& p, bool bwd, cudaStream_t s) {
-  return bwd ? launch_width<T, G, true>(p, s) : launch_width<T, G, false>(p, s);
+  return bwd ? launch_planned<T, G, true>(p, s) : launch_planned<T, G, false>(p, s);
 }
 template <class T>
 int launch_t(const GatedParams& p, int gates, bool bwd, cudaStream_t s) {
