@@ -6,9 +6,8 @@
 // one order and goes through its range again, from its end, where the L2 still holds it.  Bound by bytes: 3 for every
 // byte of gradient past what the L2 keeps.
 //
-// Squares are summed in fp32 for the 64 bytes that a thread takes at a time, and those sums in fp64.  Where
-// such a sum leaves the range in which fp32 keeps its bits (squares that overflow or vanish), its values are
-// squared in fp64.
+// Squares are summed in fp32 for the 64 bytes that a thread takes at a time, and those sums with their rounding errors
+// beside them; fp64, which is slow here (two multiply-adds a clock on an SM), adds the CTAs' and takes the root.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -71,44 +70,59 @@ __device__ __forceinline__ void values(const uint4& r, float (&x)[BF ? 8 : 4]) {
 
 constexpr int kVecs = kClipUnit / 16 / kThreads;  // vectors of a unit that a thread takes
 
-// a thread's sum: fp32 with the rounding errors beside it, and what that cannot hold
+// a sum of fp32 numbers with its rounding errors beside it
 struct Sum {
   float s, c;
-  double d;
   __device__ __forceinline__ void add(float x, float more) {
     const float t = s + x, z = t - s;
     c += (s - (t - z)) + (x - z) + more;
     s = t;
   }
+  __device__ __forceinline__ void over_warp() {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) add(__shfl_xor_sync(0xffffffffu, s, o), __shfl_xor_sync(0xffffffffu, c, o));
+  }
+  // (the error of a sum that is not finite is not a number)
+  __device__ double value() const { return isfinite(s) ? (double)s + (double)c : (double)s; }
 };
-
+// Squares of the values as they are, and of those whose squares would vanish or overflow times 2^100 and 2^-80: a group's
+// sum below 2^-100 may have lost squares below 2^-126 (its values are below 2^-50, the smallest 2^-149); one above
+// 2^90 loses with the factor what is 2^-50 of it.  What is not finite counts among the large ones.
+struct Sums {
+  Sum mid, low, high;
+};
+template <int N>
+__device__ __forceinline__ float squares(const float (&x)[N], float by) {
+  float s[4] = {};
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float y = x[j] * by;
+    s[j % 4] = fmaf(y, y, s[j % 4]);
+  }
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+template <int N>
+__device__ __forceinline__ void add_squares(Sums& sums, const float (&x)[N]) {
+  const float all = squares(x, 1.f);
+  if (all >= 0x1p-100f && all <= 0x1p90f)
+    sums.mid.add(all, 0.f);
+  else if (all < 0x1p-100f)
+    sums.low.add(squares(x, 0x1p100f), 0.f);
+  else
+    sums.high.add(squares(x, 0x1p-80f), 0.f);
+}
 template <bool BF>
-__device__ __forceinline__ void squares(Sum& sum, const uint4 (&r)[kVecs]) {
+__device__ __forceinline__ void add_vectors(Sums& sums, const uint4 (&r)[kVecs]) {
   constexpr int E = BF ? 8 : 4;
-  float s[kVecs] = {};
+  float x[kVecs * E];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    float x[E];
-    values<BF>(r[i], x);
+    float v[E];
+    values<BF>(r[i], v);
 #pragma unroll
-    for (int j = 0; j < E; ++j) s[i] = fmaf(x[j], x[j], s[i]);
+    for (int j = 0; j < E; ++j) x[i * E + j] = v[j];
   }
-  float all = 0.f;
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) all += s[i];
-  if (all >= 0x1p-100f && all <= 0x1p90f) {
-    sum.add(all, 0.f);
-    return;
-  }
-  // (what is below 2^-100 in all may have lost squares below 2^-126; NaN comes here, too)
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    if (((r[i].x | r[i].y | r[i].z | r[i].w) & (BF ? 0x7fff7fffu : 0x7fffffffu)) == 0u) continue;
-    float x[E];
-    values<BF>(r[i], x);
-#pragma unroll
-    for (int j = 0; j < E; ++j) sum.d = fma((double)x[j], (double)x[j], sum.d);
-  }
+  add_squares(sums, x);
 }
 
 // a unit of a tensor: its address and how many values it has
@@ -139,45 +153,44 @@ struct Unit {
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) clip_sum_kernel(const __grid_constant__ Table<N> t, double* part) {
-  __shared__ float2 sh[kThreads / 32];
-  __shared__ double wide[kThreads];
+  __shared__ Sum sh[3][kThreads / 32];
   depend_launch();
   int u0, u1;
   range_of(t, u0, u1);
   int i = tensor_of(t, u0);
   depend_wait();
-  Sum sum{0.f, 0.f, 0.0};
+  Sums sums{};
   for (int u = u0; u < u1; ++u) {
     while (i + 1 < t.n && u >= t.t[i + 1].first) ++i;
     const Unit x(t.t[i], u);
     uint4 r[kVecs];
     x.load(r);
     if (x.bf16)
-      squares<true>(sum, r);
+      add_vectors<true>(sums, r);
     else
-      squares<false>(sum, r);
+      add_vectors<false>(sums, r);
     for (int j = x.rest() + threadIdx.x; j < x.n; j += kThreads) {
-      const double v = x.bf16 ? (double)__bfloat162float(reinterpret_cast<const __nv_bfloat16*>(x.p)[j])
-                              : (double)reinterpret_cast<const float*>(x.p)[j];
-      sum.d = fma(v, v, sum.d);
+      const float v[1] = {x.bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(x.p)[j])
+                                 : reinterpret_cast<const float*>(x.p)[j]};
+      add_squares(sums, v);
     }
   }
-  const bool any = __syncthreads_or(sum.d != 0.0);  // (NaN is not 0)
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float s = __shfl_xor_sync(0xffffffffu, sum.s, o), c = __shfl_xor_sync(0xffffffffu, sum.c, o);
-    sum.add(s, c);
+  const bool more = __syncthreads_or(!(sums.low.s == 0.f && sums.high.s == 0.f));  // (NaN is not 0)
+  sums.mid.over_warp();
+  if (more) sums.low.over_warp(), sums.high.over_warp();
+  if (threadIdx.x % 32 == 0) {
+    const int w = threadIdx.x / 32;
+    sh[0][w] = sums.mid, sh[1][w] = sums.low, sh[2][w] = sums.high;
   }
-  if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = make_float2(sum.s, sum.c);
-  if (any) wide[threadIdx.x] = sum.d;
   __syncthreads();
   if (threadIdx.x < 32) {  // (fp64 is slow: one warp's work)
     double d = 0.0;
-    if (threadIdx.x < kThreads / 32) d = (double)sh[threadIdx.x].x + (double)sh[threadIdx.x].y;
-    if (any)
-      for (int j = threadIdx.x; j < kThreads; j += 32) d += wide[j];
+    if (threadIdx.x < kThreads / 32) {
+      d = sh[0][threadIdx.x].value();
+      if (more) d += sh[1][threadIdx.x].value() * 0x1p-200 + sh[2][threadIdx.x].value() * 0x1p160;
+    }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    for (int o = kThreads / 64; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
     if (threadIdx.x == 0) part[blockIdx.x] = d;
   }
 }
