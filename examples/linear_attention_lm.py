@@ -1,4 +1,4 @@
-"""A residual stack of linear-attention layers and one LSTM layer, served and trained with the
+"""A residual stack of linear-attention, gated and LSTM layers, served and trained with the
 operators of ``sequential_rnn_gb300.lm``.
 
     python examples/linear_attention_lm.py          (needs a GB300)
@@ -7,11 +7,13 @@ Each layer reads the residual stream through the norm (which adds the previous l
 stream and writes 8 bits with scales in the same pass), projects it in 8 bits, and mixes over time:
 
     h, y8 = rms_norm(stream + out);  q, k, v = input_proj_fp8(y8);  o = linear_attention(q, k, v)
-    out   = input_proj_fp8(rms_norm(o));      the LSTM layer takes the projection as its Wx instead
+    out   = input_proj_fp8(rms_norm(o));      the LSTM layer takes the projection as its Wx instead,
+                                              the gated layer (no recurrent matrix) as that of a scan
 
-q, k and v are strided views of one projection.  A prompt runs all tokens at once; after it every
-layer keeps a state ([NH, D, D] or the LSTM's h and c for each sequence), and a decoding step runs
-the same layers on one token, captured once in a CUDA graph.
+q, k and v are strided views of one projection; the rotary layer norms each head of q and k and turns it by its
+token's position on their way to the attention.  A prompt runs all tokens at once; after it every
+layer keeps a state ([NH, D, D], the rotary layer's with its sequences' positions, [NH, D], or the LSTM's h and c
+for each sequence), and a decoding step runs the same layers on one token, captured once in a CUDA graph.
 """
 import os
 import sys
@@ -61,6 +63,60 @@ class LinearLayer:
         return stream, self._out(S.linear_attention_step(q, k, v, self.decay, cache, scale=self.D ** -0.5))
 
 
+class RotaryLayer(LinearLayer):
+    """Linear attention on queries and keys that are normed and turned by their positions."""
+
+    def __init__(self, NH, D, gen):
+        super().__init__(NH, D, gen)
+        self.n_q, self.n_k = torch.ones(D, device="cuda"), torch.ones(D, device="cuda")
+        self.freqs = S.rotary_frequencies(D)
+
+    def _turned(self, q, k, at):
+        return S.head_norm_rotary(q, k, self.n_q, self.n_k, self.freqs, at)
+
+    def prompt(self, stream, out, lens=None):
+        stream, (q, k, v) = self._qkv(stream, out)
+        q, k = self._turned(q, k, None)
+        a = S.linear_attention(q, k, v, self.decay, lens=lens, scale=self.D ** -0.5)
+        T, B = q.shape[:2]
+        at = torch.full((B,), T, dtype=torch.int32, device="cuda") if lens is None else lens.clone()
+        return stream, self._out(a["o"]), (a["state"], at)
+
+    def step(self, stream, out, cache):
+        state, at = cache
+        stream, (q, k, v) = self._qkv(stream, out)
+        q, k = self._turned(q, k, at)
+        at += 1
+        return stream, self._out(S.linear_attention_step(q, k, v, self.decay, state, scale=self.D ** -0.5))
+
+
+class GatedLayer:
+    """A gated linear recurrence on an 8-bit input projection: forget, input and output gates."""
+
+    def __init__(self, NH, D, gen):
+        d = NH * D
+        self.NH, self.D = NH, D
+        self.w = (torch.randn(3 * d, d, generator=gen, device="cuda") * d ** -0.5).bfloat16()
+        self.w8 = S.quantize_weight(self.w)
+        self.bias = torch.zeros(NH, 3, D, device="cuda")
+        self.bias[:, 0] = torch.linspace(0, 6, D, device="cuda")  # memories from two tokens to four hundred
+        self.n = torch.ones(d, device="cuda")
+
+    def _wx(self, stream, out):
+        n = S.rms_norm(stream, self.n, out, quantize=True)
+        wx = S.input_proj_fp8(n["y"], n["scale"], *self.w8, self.bias.flatten(), check=False)
+        return n["h"], wx.view(*wx.shape[:-1], self.NH, 3 * self.D)
+
+    def prompt(self, stream, out, lens=None):
+        stream, wx = self._wx(stream, out)
+        f = S.gated_recurrence(wx, gates="fzo", lens=lens)
+        return stream, f["y"].flatten(-2), f["state"]
+
+    def step(self, stream, out, cache):
+        stream, wx = self._wx(stream, out)
+        return stream, S.gated_recurrence_step(wx, cache, gates="fzo").flatten(-2)
+
+
 class LstmLayer:
     """The head-wise LSTM on an 8-bit input projection."""
 
@@ -90,10 +146,13 @@ class LstmLayer:
         return s[0], o[0]
 
 
+LAYERS = {"linear": LinearLayer, "rotary": RotaryLayer, "gated": GatedLayer, "lstm": LstmLayer}
+
+
 class Model:
     def __init__(self, NH=12, D=64, layers=("linear", "linear", "lstm"), seed=0):
         gen = torch.Generator(device="cuda").manual_seed(seed)
-        self.layers = [(LinearLayer if n == "linear" else LstmLayer)(NH, D, gen) for n in layers]
+        self.layers = [LAYERS[n](NH, D, gen) for n in layers]
         self.norm = torch.ones(NH * D, device="cuda")
 
     def prompt(self, x, lens=None):
@@ -143,9 +202,31 @@ def mixer_loss(x, w, decay, NH, D, target):
     return loss, d["dx"], d["dw"]
 
 
+def training_step(x, w, w_q, w_k, freqs, decay, NH, D, target, limit):
+    """Two mixers side by side on one norm of x [T, B, 5*NH*D]: its first three parts are the queries, keys and values of
+    rotated linear attention, the others the gates of a recurrence; loss sum((o + y) target).  Returns the loss,
+    the weights' gradients clipped to a common norm of `limit`, dx, and that norm before."""
+    T, B, d = *x.shape[:2], NH * D
+    n = S.rms_norm(x, w, train=True)
+    q, k, v = n["y"][..., :3 * d].view(T, B, 3, NH, D).unbind(2)
+    wx = n["y"][..., 3 * d:].contiguous().view(T, B, NH, 2 * D)
+    qt, kt = S.head_norm_rotary(q, k, w_q, w_k, freqs)
+    a = S.linear_attention(qt, kt, v, decay)
+    f = S.gated_recurrence(wx, train=True)
+    loss = ((a["o"].float() + f["y"].float()) * target.float()).sum()
+    ga = S.linear_attention_backward(qt, kt, v, decay, target)
+    gf = S.gated_recurrence_backward(wx, f["stash"], target)
+    gr = S.head_norm_rotary_backward(q, k, w_q, w_k, freqs, None, ga["dq"], ga["dk"])
+    dy = torch.cat([gr["dq"].flatten(2), gr["dk"].flatten(2), ga["dv"].flatten(2), gf["dWx"].flatten(2)], -1)
+    dn = S.rms_norm_backward(dy, n["h"], w, n["rstd"])
+    grads = {"dw": dn["dw"], "dw_q": gr["dwq"], "dw_k": gr["dwk"]}
+    norm = S.clip_grad_norm(list(grads.values()), limit)
+    return loss, grads, dn["dx"], norm
+
+
 def main():
     NH, D, B, T, new = 12, 64, 16, 1024, 128
-    m = Model(NH, D)
+    m = Model(NH, D, layers=("rotary", "gated", "lstm"))
     x = torch.randn(T, B, NH * D, device="cuda").bfloat16()
     for _ in range(3):
         m.prompt(x)
@@ -171,6 +252,12 @@ def main():
                                   torch.ones(3 * NH * D, device="cuda"), decays(NH), NH, D,
                                   torch.randn(T, B, NH, D, device="cuda").bfloat16())
     print(f"training: loss {loss.item():.4g}, |dx| {dx.float().norm().item():.4g}, |dw| {dw.norm().item():.4g}")
+    one = torch.ones(D, device="cuda")
+    loss, grads, _, norm = training_step(torch.randn(T, B, 5 * NH * D, device="cuda").bfloat16(),
+                                         torch.ones(5 * NH * D, device="cuda"), one, one, S.rotary_frequencies(D),
+                                         decays(NH), NH, D, torch.randn(T, B, NH, D, device="cuda").bfloat16(), 1.0)
+    print(f"both mixers: loss {loss.item():.4g}, weights' gradients of norm {norm.item():.4g} clipped to "
+          f"{S.grad_norm(list(grads.values())).item():.4g}")
 
 
 if __name__ == "__main__":

@@ -522,6 +522,9 @@ __global__ void __launch_bounds__(256, BWD || sizeof(T) == 4 ? 2 : 3) rotary_rin
     Head<T, MODE> raw;
     w.load(raw, x);
     Pairs y = w.get(raw);
+    if (BWD && !norm)  // (x does not matter then, whatever it is)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) y.a[j] = y.b[j] = Num<2>(0.f);
     const float r1 = norm ? rsqrtf(fmaf(head_sum<LPH>(dot(y, y)), inv, p.eps)) : 1.f;
     const Num<2> r(r1);
     if constexpr (!BWD) {

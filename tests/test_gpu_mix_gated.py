@@ -98,9 +98,10 @@ def test_constant_gates_keep_a_long_memory(S, gates):
     close(out["state"], f["state"], f["state_err"])
 
 
+@pytest.mark.parametrize("D", [32, 64, 33])
 @pytest.mark.parametrize("gates", ["fz", "ifzo"])
-def test_dead_tokens_do_not_matter(S, gates):
-    T, B, NH, D, lens = 100, 3, 2, 32, [0, 50, 67]
+def test_dead_tokens_do_not_matter(S, gates, D):
+    T, B, NH, lens = 100, 3, 2, [0, 50, 67]
     Wx, s0, dy, ds = inputs(T, B, NH, D, gates, "bf16")
     ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
     bad, bady = Wx.clone(), dy.clone()
@@ -119,8 +120,9 @@ def test_dead_tokens_do_not_matter(S, gates):
     assert torch.equal(res[1][1][0], s0[0]) and torch.equal(res[1][3][0], ds[0])
 
 
-def test_values_that_are_not_finite_stay_in_their_channel(S):
-    T, B, NH, D = 150, 2, 1, 32
+@pytest.mark.parametrize("D", [32, 33])  # on tiles, and value by value
+def test_values_that_are_not_finite_stay_in_their_channel(S, D):
+    T, B, NH = 150, 2, 1
     Wx, s0, dy, ds = inputs(T, B, NH, D, "fz", "f32")
     Wx.view(T, B, 2, D)[..., 0, :].clamp_(-3, 3)
     bad = Wx.clone()

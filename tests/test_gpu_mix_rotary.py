@@ -167,6 +167,16 @@ def test_values_that_are_not_finite_stay_in_their_head(S):
     assert torch.equal(a[0][~hit], b[0][~hit]) and torch.equal(a[1], b[1]) and torch.isnan(b[0][0, 0, 0]).all()
 
 
+@pytest.mark.parametrize("T", [4, 1300])  # batches of heads, and the copies' ring
+def test_without_norm_the_gradient_does_not_look_at_x(S, T):
+    f = S.rotary_frequencies(64)
+    q, d = rand(1, T, 2, 3, 64, dtype="bf16"), rand(2, T, 2, 3, 64, dtype="bf16")
+    bad = torch.full_like(q, float("nan"))
+    bad[::2] = float("inf")
+    a, b = (S.head_norm_rotary_backward(x, x, None, None, f, None, d, d) for x in (q, bad))
+    assert torch.equal(a["dq"], b["dq"]) and torch.equal(a["dk"], b["dk"]) and torch.isfinite(b["dq"]).all()
+
+
 def test_captured_and_repeated(S):
     T, B, NH, D = 50, 4, 6, 128
     q, k, dq, dk = (rand(i, T, B, NH, D, dtype="bf16") for i in range(4))
