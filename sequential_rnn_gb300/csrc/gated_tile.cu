@@ -2,7 +2,7 @@
 // mathematics and the other sizes: gated.cu).
 //
 // A CTA takes 64 (or 32) channels of a head of one row, and goes through time in rounds of 64 (128) tokens; the CTAs of a cluster take
-// neighbouring rounds at once.  A control warp keeps a ring of tiles [tokens][gates][channels] filled.  Eight warps
+// neighbouring rounds at once.  A control warp keeps a ring of tiles [tokens][gates][channels] filled.  Eight warps (four of fp32)
 // take a run of 8 tokens each: gates and the run's map c -> A c + U in registers, the map handed to
 // one more warp, which composes the maps in the order of time -- those of the cluster's CTAs after
 // exchanging them by st.async -- and hands every run the state at its start; then the run once more, its results written into
@@ -22,9 +22,7 @@
 namespace srnn {
 namespace {
 
-constexpr int kS = kRunTokens, kW = kRunWarps;
-constexpr int kThreads = 32 * (kW + 2);
-constexpr int kTalk = 32 * (kW + 1);            // threads of the runs and of the maps
+constexpr int kS = kRunTokens;
 constexpr int kReady = 1, kStart = 3;           // named barriers, a pair of each: maps there, starts there
 // c -> a c + u of two neighbouring channels, as 16 bytes of shared memory
 struct Map2 {
@@ -47,18 +45,22 @@ struct TileMaps {
   CUtensorMap dy, stash;          // gradient alone: box [TOKENS, 1, 1, X], [RUNS, 1, 1, X]
 };
 
-// X: channels of a tile, 64 or 32; a warp takes 64 / X runs at once, PL lanes each
+// X: channels of a tile, 64 or 32; a warp takes 64 / X runs at once, PL lanes each.  W warps for runs: four for fp32, whose
+// tiles would otherwise leave room for one CTA on an SM (training, 2001 x 4 tokens of
+// 6 x 128, ifzo: 79 us with eight, 67 with four)
 template <class T, int G, bool BWD, int X, bool AHEAD>
 struct Tile {
-  static constexpr int PL = X / 2, RUNS = kW * 64 / X, TOKENS = RUNS * kS;
+  static constexpr int W = sizeof(T) == 4 ? 4 : 8, THREADS = 32 * (W + 2), TALK = 32 * (W + 1);  // TALK: of runs and maps
+  static constexpr int PL = X / 2, RUNS = W * 64 / X, TOKENS = RUNS * kS;
   static constexpr uint32_t ROW = X * sizeof(T), TOK = G * ROW, MAPS = X * 8;  // bytes; of a run's maps
   static constexpr uint32_t WX = TOKENS * TOK, DY = BWD ? TOKENS * ROW : 0, ST = BWD ? RUNS * X * 4 : 0;
   static constexpr uint32_t STAGE = WX + DY + ST;
-  // CTAs of an SM, as registers (64 for three, 96 for two) and shared memory allow
-  static constexpr int CTAS = !BWD && sizeof(T) == 2 && !AHEAD ? 3 : STAGE <= (AHEAD ? 24 : 50) * 1024 ? 2 : 1, BUF = AHEAD ? 2 : 1;
-  static constexpr uint32_t REST = BUF * (RUNS * MAPS + RUNS * X * 4) + 256 + 128 +
-                                   (CTAS == 1 ? 2 * kGatedCluster * MAPS : 8 * MAPS);
-  static constexpr int FIT = (int)((224 * 1024 / CTAS - REST) / STAGE), MOST = AHEAD ? 4 : 3, STAGES = FIT > MOST ? MOST : FIT;
+  static constexpr int BUF = AHEAD ? 2 : 1, MOST = AHEAD ? 4 : 3;
+  static constexpr uint32_t REST = BUF * (RUNS * MAPS + RUNS * X * 4) + 256 + 128 + 8 * MAPS, ROOM = 224 * 1024;
+  // CTAs of an SM, as registers (64 a thread for three with W = 8, 96 for two; 112 and 168 with W = 4) and shared memory allow
+  static constexpr bool THREE = !AHEAD && (W == 8 ? !BWD : G < 4 || !BWD) && 3 * (2 * STAGE + REST) <= ROOM;
+  static constexpr int CTAS = THREE ? 3 : 2 * ((AHEAD ? 3 : 2) * STAGE + REST) <= ROOM ? 2 : 1;
+  static constexpr int FIT = (int)((ROOM / CTAS - REST) / STAGE), STAGES = FIT > MOST ? MOST : FIT;
   static_assert(STAGES >= (AHEAD ? 3 : 2), "the tile of a round ahead needs the stage of two rounds before");
   static constexpr uint32_t PART = STAGES * STAGE, START = PART + BUF * RUNS * MAPS, BARS = START + BUF * RUNS * X * 4,
                             ALL = BARS + 256;
@@ -211,7 +213,7 @@ struct Backward {
 
 // AHEAD: a run's maps are made a round ahead of its results, while the maps of the round before are on their way
 template <class T, int G, bool BWD, int X, bool AHEAD>
-__global__ void __launch_bounds__(kThreads, (Tile<T, G, BWD, X, AHEAD>::CTAS))
+__global__ void __launch_bounds__((Tile<T, G, BWD, X, AHEAD>::THREADS), (Tile<T, G, BWD, X, AHEAD>::CTAS))
     gated_tile_kernel(const GatedParams p, const __grid_constant__ TileMaps maps) {
   using C = Tile<T, G, BWD, X, AHEAD>;
   constexpr int PL = C::PL;
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<T, G, BWD, X, AHEAD>::CTAS))
   if (cs > 1) cluster_sync();  // every CTA's barriers are there
   auto round_of = [&](int i) { return BWD ? rounds - 1 - i : i; };
 
-  if (warp == kW + 1) {  // ---- copies
+  if (warp == C::W + 1) {  // ---- copies
     if (lane == 0) {
       tma_prefetch_map(&maps.wx);
       tma_prefetch_map(&maps.out);
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<T, G, BWD, X, AHEAD>::CTAS))
         }
     }
     __syncwarp();
-  } else if (warp == kW) {  // ---- maps: two channels a thread, the lanes of one `sub` eight runs that follow one another
+  } else if (warp == C::W) {  // ---- maps: two channels a thread, the lanes of one `sub` W runs that follow one another
     const float* from = BWD ? p.dstateT : p.state0;
     float* const to = BWD ? p.dstate0 : p.stateT;
     const int c = c0 + 2 * pl;  // (D is even)
@@ -286,19 +288,19 @@ __global__ void __launch_bounds__(kThreads, (Tile<T, G, BWD, X, AHEAD>::CTAS))
       return y;
     };
     struct Runs {
-      Map2 m[8], t, first;  // the lane's runs; composed: all of the CTA's, those of the lane before it
+      Map2 m[C::W], t, first;  // the lane's runs; composed: all of the CTA's, those of the lane before it
     };
     auto read = [&](int i, Runs& r) {
       const int buf = AHEAD ? i & 1 : 0;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        const int run = sub * 8 + w;
+      for (int w = 0; w < C::W; ++w) {
+        const int run = sub * C::W + w;
         r.m[w] = get(part + (buf * C::RUNS + (BWD ? C::RUNS - 1 - run : run)) * PL + pl);
       }
       if (cs == 1 && PL == 32) return;
       r.t = r.m[0];
 #pragma unroll
-      for (int w = 1; w < 8; ++w) {
+      for (int w = 1; w < C::W; ++w) {
         r.t.u = fma(r.m[w].a, r.t.u, r.m[w].u);
         r.t.a = r.m[w].a * r.t.a;
       }
@@ -339,17 +341,17 @@ __global__ void __launch_bounds__(kThreads, (Tile<T, G, BWD, X, AHEAD>::CTAS))
       if (PL == 16 && sub) in = fma(r.first.a, in, r.first.u);
       const int buf = AHEAD ? i & 1 : 0;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        const int run = sub * 8 + w;
+      for (int w = 0; w < C::W; ++w) {
+        const int run = sub * C::W + w;
         start[(buf * C::RUNS + (BWD ? C::RUNS - 1 - run : run)) * PL + pl] = in.x;
         in = fma(r.m[w].a, in, r.m[w].u);
       }
       if (cs == 1 && PL == 32) h = in;
       __syncwarp();
-      bar_arrive(kStart + buf, kTalk);
+      bar_arrive(kStart + buf, C::TALK);
     };
     for (int i = 0; i < rounds; ++i) {
-      bar_sync(kReady + (AHEAD ? i & 1 : 0), kTalk);
+      bar_sync(kReady + (AHEAD ? i & 1 : 0), C::TALK);
       Runs r;
       read(i, r);
       send(i, r);
@@ -389,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<T, G, BWD, X, AHEAD>::CTAS))
       const int buf = AHEAD ? i & 1 : 0;
       put(part + (buf * C::RUNS + run) * PL + pl, ma, mu);
       __syncwarp();
-      bar_arrive(kReady + buf, kTalk);
+      bar_arrive(kReady + buf, C::TALK);
       if (out >= 0 && tell) {
         bulk_wait_read_all();
         mbar_arrive(empty + 8 * out);
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<T, G, BWD, X, AHEAD>::CTAS))
       const uint32_t x = mine + st * C::STAGE;
       const bool whole = is_whole(n);
       __syncwarp();
-      bar_sync(kStart + buf, kTalk);
+      bar_sync(kStart + buf, C::TALK);
       Num<2> c;
       c.x = start[(buf * C::RUNS + run) * PL + pl];
       if constexpr (BWD) {
@@ -511,7 +513,7 @@ struct Variant {
   // the kernel's attributes, once a device; a cudaError_t value
   static int prepare() {
     static int prep[64][5];
-    return prepare_launch(prep, kernel, C::smem(kGatedCluster), kThreads, kGatedCluster);
+    return prepare_launch(prep, kernel, C::smem(kGatedCluster), C::THREADS, kGatedCluster);
   }
   // clusters of cs CTAs that the device holds at once (0: none, or not to be had)
   static int active(int cs, int dev) {
@@ -520,7 +522,7 @@ struct Variant {
     if (known[dev][cs] == 0) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(cs);
-      cfg.blockDim = dim3(kThreads);
+      cfg.blockDim = dim3(C::THREADS);
       cfg.dynamicSmemBytes = C::smem(cs);
       cudaLaunchAttribute attr[2];
       attributes(attr, cs);
@@ -552,7 +554,7 @@ struct Variant {
     if (e != 0) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::THREADS);
     // few CTAs: shared memory asked for so that the SMs share them out evenly (a cluster's would pack three to an SM)
     const uint32_t each = (uint32_t)((ctas + sm_count() - 1) / sm_count());
     const uint32_t spread = each < (uint32_t)C::CTAS ? 226 * 1024 / (each + 1) + 1024 : 0;
