@@ -396,7 +396,7 @@ int rnn_linattn_step(const rnn_linattn_desc_t* desc, const rnn_linattn_strides_t
  * rnn_gated_stash_size bytes.  Gates, states and sums are fp32, y is rounded once.  A value that is not
  * finite reaches its own and later tokens of its row and channel (in the gradient: earlier ones, too) and
  * nothing else; where a product of forget gates underflows, an infinity before it may turn to NaN.
- * Wx, y contiguous; aligned as their element is.  From 32 tokens on, heads of a multiple of 16 bytes at addresses that
+ * Wx, y contiguous; aligned as their element is.  From 65 tokens on, heads of a multiple of 16 bytes at addresses that
  * are run on tiles that the kernels wait for.  workspace: 256-byte aligned, >= 256 bytes (status word at offset 0). */
 typedef enum { RNN_GATES_FZ = 2, RNN_GATES_FZO = 3, RNN_GATES_IFZO = 4 } rnn_gates_t;
 

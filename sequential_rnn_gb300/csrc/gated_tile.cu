@@ -1,4 +1,4 @@
-// Gated linear recurrence on tiles that TMA brings: head sizes that are multiples of 16 bytes, from a few tokens on (the
+// Gated linear recurrence on tiles that TMA brings: head sizes that are multiples of 16 bytes, more than 64 tokens (the
 // mathematics and the other sizes: gated.cu).
 //
 // A CTA takes 64 (or 32) channels of a head of one row, and goes through time in rounds of 64 (128) tokens; the CTAs of a cluster take
@@ -627,6 +627,8 @@ int launch_t(const GatedParams& p, int gates, bool bwd, cudaStream_t s) {
 
 }  // namespace
 
+// (up to 64 tokens, one round, they are no faster than gated.cu's kernels, 16 rows of 12 x 64, fz: 2.95 us against 2.99; with 128
+// 3.6 against 7.0)
 bool gated_takes_tiles(const GatedParams& p, bool bf16) { return p.D % (bf16 ? 8 : 4) == 0 && p.T >= kGatedTileTokens; }
 
 int launch_gated_tile(const GatedParams& p, int gates, bool bf16, bool bwd, cudaStream_t s) {

@@ -166,7 +166,7 @@ struct GatedParams {
 };
 int launch_gated(GatedParams p, int gates, bool bf16, bool bwd, cudaStream_t s);
 // the kernels on tiles: whether the sizes suit them; kGatedNoTile: addresses or strides have no tensor map
-constexpr int kGatedTileTokens = 32;
+constexpr int kGatedTileTokens = 65;
 constexpr int kGatedNoTile = -2;
 bool gated_takes_tiles(const GatedParams& p, bool bf16);
 int launch_gated_tile(const GatedParams& p, int gates, bool bf16, bool bwd, cudaStream_t s);

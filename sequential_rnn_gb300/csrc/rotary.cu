@@ -318,8 +318,8 @@ struct Items {
   }
 };
 
-constexpr int kRingTokens = 16;  // for each SM
-constexpr size_t kRingThree = 72 * 1024, kRingMost = 200 * 1024;  // bytes of a CTA's rings
+constexpr int kRingTokens = 16;               // for each SM
+constexpr size_t kRingMost = 200 * 1024;      // bytes of a CTA's rings
 constexpr int kBatch = 3, kBatchBwd = 2;  // heads that a lane loads before it uses the first
 
 template <class T, int LPH, int MODE>
@@ -452,8 +452,9 @@ __global__ void __launch_bounds__(256, 2) rotary_bwd_kernel(const RotaryParams p
 }
 
 // Many tokens, heads of 32, 64, 128 or 256 at 16-byte addresses: a warp takes whole tokens, which asynchronous copies bring
-// into a ring of its own in shared memory, so that one or two tokens are on their way while one is worked on and no register
-// holds them.  A sweep is what the warp takes at once: 32 / LPH heads.
+// into a ring of its own in shared memory, so that a token is on its way while one is worked on and no register holds it (two on
+// their way, with fewer CTAs on an SM, are no faster: 1024 x 16 tokens of 12 + 12 x 64 heads 20.8 us against 19.6, 1024 x 8 of
+// 16 + 8 x 128 30.9 against 22.5).  A sweep is what the warp takes at once: 32 / LPH heads.
 template <class T, int LPH>
 struct Ring {
   static constexpr int HPW = 32 / LPH, D = 8 * LPH, SWEEP = 32 * 8 * sizeof(T);
@@ -461,10 +462,10 @@ struct Ring {
   static int sweeps(const RotaryParams& p) { return (p.NQ + HPW - 1) / HPW + (p.NK + HPW - 1) / HPW; }
 };
 
-template <class T, int LPH, int MODE, bool BWD, int STAGES>
+template <class T, int LPH, int MODE, bool BWD>
 __global__ void __launch_bounds__(256, BWD || sizeof(T) == 4 ? 2 : 3) rotary_ring_kernel(const RotaryParams p) {
   using C = Ring<T, LPH>;
-  constexpr int HPW = C::HPW, D = C::D;
+  constexpr int HPW = C::HPW, D = C::D, STAGES = 2;
   extern __shared__ __align__(128) char dyn[];
   __shared__ Consts sh;
   __shared__ float part[BWD ? 8 : 1][2][BWD ? D : 1];
@@ -718,8 +719,9 @@ int launch_lanes(RotaryParams& p, bool bwd, cudaStream_t s) {
   const long long tokens = (long long)p.T * p.B;
   const int heads = 32 / LPH * (bwd ? kBatchBwd : kBatch), per_sm = bwd ? 2 : 3;
   const int groups = (p.NQ + heads - 1) / heads + (p.NK + heads - 1) / heads;
-  // few tokens: a warp for each batch of heads, so that the latency of one batch is that of all
-  p.split = tokens < 8LL * per_sm * sm_count();
+  // few tokens: a warp for each batch of heads, so that the latency of one batch is that of all (608 tokens of 12 + 12 x 64
+  // heads 3.6 us against 4.3, 1216 4.5 against 4.4; gradient 1216 8.0 against 9.4, 2432 11.2 against 9.2)
+  p.split = tokens < (bwd ? 16LL : 8LL) * sm_count();
   const long long want = (tokens * (p.split ? groups : 1) + 7) / 8, most = (long long)per_sm * sm_count();
   unsigned grid = (unsigned)(want < most ? want : most);
   if (!bwd) return launch_dependent(rotary_kernel<T, LPH, MODE>, grid, 256, 0, s, (const RotaryParams)p);
@@ -727,7 +729,8 @@ int launch_lanes(RotaryParams& p, bool bwd, cudaStream_t s) {
   const int e = launch_dependent(rotary_bwd_kernel<T, LPH, MODE>, grid, 256, 0, s, (const RotaryParams)p);
   return e != 0 || !p.qw ? e : reduce_dw(p, (int)grid, s);
 }
-// 16-byte copies, and enough tokens that each warp of the grid takes several
+// 16-byte copies, and tokens enough: 4864 of 12 + 12 x 64 heads take 7.9 us against 8.3 by batches (gradient 13.7 against
+// 15.7), 2432 5.6 against 5.9 (9.2 both), 608 4.2 against 4.3, and 3.6 with the batches split
 template <class T, int LPH>
 bool ring_form(const RotaryParams& p, bool bwd) {
   auto even = [](const void* x, const long long (&s)[3]) {
@@ -738,24 +741,21 @@ bool ring_form(const RotaryParams& p, bool bwd) {
   ok = ok && (bwd ? 4 : 2) * 8LL * Ring<T, LPH>::sweeps(p) * Ring<T, LPH>::SWEEP <= kRingMost;
   return ok && (long long)p.T * p.B >= kRingTokens * sm_count();
 }
-template <class T, int LPH, int MODE, bool BWD, int STAGES>
-int launch_stages(const RotaryParams& p, size_t smem, cudaStream_t s) {
+template <class T, int LPH, int MODE, bool BWD>
+int launch_ring(const RotaryParams& p, cudaStream_t s) {
   static int prep[64][5];
-  int e = prepare_launch(prep, rotary_ring_kernel<T, LPH, MODE, BWD, STAGES>, (uint32_t)smem, 256, 1);
+  const size_t smem = (BWD ? 4 : 2) * 8 * (size_t)Ring<T, LPH>::sweeps(p) * Ring<T, LPH>::SWEEP;
+  int e = prepare_launch(prep, rotary_ring_kernel<T, LPH, MODE, BWD>, (uint32_t)smem, 256, 1);
   if (e != 0) return e;
   const long long want = ((long long)p.T * p.B + 7) / 8, most = (BWD || sizeof(T) == 4 ? 2LL : 3LL) * sm_count();
   unsigned grid = (unsigned)(want < most ? want : most);
   if (BWD && grid > kRotaryParts) grid = kRotaryParts;
-  e = launch_dependent(rotary_ring_kernel<T, LPH, MODE, BWD, STAGES>, grid, 256, smem, s, p);
+  e = launch_dependent(rotary_ring_kernel<T, LPH, MODE, BWD>, grid, 256, smem, s, p);
   return e != 0 || !BWD || !p.qw ? e : reduce_dw(p, (int)grid, s);
 }
 template <class T, int LPH, int MODE>
 int launch_ring(const RotaryParams& p, bool bwd, cudaStream_t s) {
-  const size_t token = 8 * (size_t)Ring<T, LPH>::sweeps(p) * Ring<T, LPH>::SWEEP;  // of the CTA's eight warps
-  if (bwd) return launch_stages<T, LPH, MODE, true, 2>(p, 4 * token, s);
-  // two tokens on their way where three CTAs still fit an SM
-  return 3 * token <= kRingThree ? launch_stages<T, LPH, MODE, false, 3>(p, 3 * token, s)
-                                 : launch_stages<T, LPH, MODE, false, 2>(p, 2 * token, s);
+  return bwd ? launch_ring<T, LPH, MODE, true>(p, s) : launch_ring<T, LPH, MODE, false>(p, s);
 }
 template <class T, int LPH>
 int launch_mode(RotaryParams& p, bool bwd, cudaStream_t s) {

@@ -64,13 +64,14 @@ def check(S, T, B, NH, D, gates, dtype, lens=None, state=True, seed=0):
     assert "stash" not in alone and torch.equal(alone["y"], out["y"]) and torch.equal(alone["state"], out["state"])
 
 
-# lengths around a run (8), a CTA's chunk (64) and several rounds of a cluster; sizes with idle lanes and odd channels
+# lengths around a run (8), a round (64) and several rounds of a cluster; sizes on tiles of 64 and 32 channels, with idle lanes,
+# and value by value
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("gates", ["fz", "fzo", "ifzo"])
 @pytest.mark.parametrize("T,B,NH,D", [(1, 1, 1, 1), (0, 2, 3, 8), (7, 2, 2, 33), (8, 3, 1, 64), (9, 1, 5, 40), (64, 2, 2, 32),
                                       (65, 1, 1, 130), (200, 3, 2, 31), (1100, 2, 3, 64), (700, 1, 1, 6),
                                       (32, 2, 2, 8), (100, 4, 3, 136), (2500, 1, 1, 48), (257, 30, 8, 72),
-                                      (1500, 1, 2, 64), (129, 40, 6, 32), (5000, 1, 1, 96)])
+                                      (1500, 1, 2, 64), (129, 40, 6, 32), (5000, 1, 1, 96), (65, 3, 2, 64)])
 def test_shapes(S, T, B, NH, D, gates, dtype):
     check(S, T, B, NH, D, gates, dtype, seed=T + D)
 
