@@ -6,8 +6,8 @@ only marshal arguments: device pointers, sizes and the current CUDA stream.
 ``forward`` / ``backward`` additionally allocate the outputs with torch and
 raise ``RnnError`` on a non-OK status.  Every step of the recurrence runs in
 the library's CUDA kernels; there is no CPU fallback.  ``lm`` adds the operators
-of language models (norm, 8-bit projection, linear attention); its names are
-exported here as well.
+of language models (norm, 8-bit projection, linear attention, gated recurrence, norm
+and rotation of heads, clipping); its names are exported here as well.
 """
 from __future__ import annotations
 
