@@ -248,6 +248,7 @@ __global__ void __launch_bounds__((Tile<T, G, BWD, X, AHEAD>::THREADS), (Tile<T,
   __syncwarp();
   if (cs > 1) cluster_sync();  // every CTA's barriers are there
   auto round_of = [&](int i) { return BWD ? rounds - 1 - i : i; };
+  auto state_at = [&] { return c0 + 2 * pl < p.D ? (long long)b * p.N + (long long)head * p.D + c0 + 2 * pl : -1; };
 
   if (warp == C::W + 1) {  // ---- copies
     if (lane == 0) {
@@ -277,11 +278,9 @@ __global__ void __launch_bounds__((Tile<T, G, BWD, X, AHEAD>::THREADS), (Tile<T,
     __syncwarp();
   } else if (warp == C::W) {  // ---- maps: two channels a thread, the lanes of one `sub` W runs that follow one another
     const float* from = BWD ? p.dstateT : p.state0;
-    float* const to = BWD ? p.dstate0 : p.stateT;
-    const int c = c0 + 2 * pl;  // (D is even)
-    const long long at = (long long)b * p.N + (long long)head * p.D + c;
+    const long long at = state_at();
     Num<2> h(0.f);
-    if (from && c < p.D) h.x = make_float2(from[at], from[at + 1]);
+    if (from && at >= 0) h.x = make_float2(from[at], from[at + 1]);
     auto other = [&](const Num<2>& x) {  // of the lane with the same channels
       Num<2> y;
       y.x = make_float2(__shfl_xor_sync(0xffffffffu, x.x.x, 16), __shfl_xor_sync(0xffffffffu, x.x.y, 16));
@@ -357,7 +356,7 @@ __global__ void __launch_bounds__((Tile<T, G, BWD, X, AHEAD>::THREADS), (Tile<T,
       send(i, r);
       tell_starts(i, r);
     }
-    if (to && rank == 0 && sub == 0 && c < p.D) to[at] = h.x.x, to[at + 1] = h.x.y;
+    part[lane] = make_float4(h.x.x, h.x.y, 0.f, 0.f);  // (this warp's alone by now)
   } else {  // ---- runs
     const int run = warp * (32 / PL) + sub;
     const uint32_t base = sm + run * kS * C::TOK, mine = base + pl * 2 * sizeof(T);
@@ -466,12 +465,15 @@ __global__ void __launch_bounds__((Tile<T, G, BWD, X, AHEAD>::THREADS), (Tile<T,
   __syncwarp();
   if (cs > 1) {
     __syncthreads();
-    cluster_sync();
+    cluster_sync();  // (every CTA has read the initial state, whose place the final one may take)
     if (gave_up_s) {  // (maps that other CTAs sent after this one had given up land)
       const uint64_t since = globaltimer_ns();
       while (globaltimer_ns() - since < 100000ull) __nanosleep(1000);
     }
   }
+  float* const to = BWD ? p.dstate0 : p.stateT;
+  const long long at = state_at();
+  if (warp == C::W && to && rank == 0 && sub == 0 && at >= 0) to[at] = part[lane].x, to[at + 1] = part[lane].y;
 }
 
 }  // namespace
@@ -510,10 +512,12 @@ struct Variant {
     attr[1].val.clusterDim.x = (unsigned)cs;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   }
-  // the kernel's attributes, once a device; a cudaError_t value
+  // the kernel's attributes, once a device; a cudaError_t value.  (Where the device cannot hold a cluster of the largest
+  // size, active() says so, and there are smaller ones.)
   static int prepare() {
     static int prep[64][5];
-    return prepare_launch(prep, kernel, C::smem(kGatedCluster), C::THREADS, kGatedCluster);
+    const int e = prepare_launch(prep, kernel, C::smem(kGatedCluster), C::THREADS, kGatedCluster);
+    return e == -1 ? prepare_launch(prep, kernel, C::smem(kGatedCluster), C::THREADS, 1) : e;
   }
   // clusters of cs CTAs that the device holds at once (0: none, or not to be had)
   static int active(int cs, int dev) {

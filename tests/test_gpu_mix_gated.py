@@ -184,9 +184,10 @@ def test_steps_continue_a_prompt(S):
     close(want["state"], f["state"], f["state_err"])
 
 
-def test_unaligned_views(S):
-    """Contiguous tensors that begin at an odd element."""
-    T, B, NH, D = 30, 2, 1, 32
+@pytest.mark.parametrize("T", [30, 130])  # 130: the aligned ones run on tiles
+def test_unaligned_views(S, T):
+    """Contiguous tensors that begin at an odd element; a stash of the one form in the other's gradient."""
+    B, NH, D = 2, 1, 32
     Wx, s0, dy, ds = inputs(T, B, NH, D, "fz", "bf16")
     buf = torch.empty(Wx.numel() + 1, dtype=torch.bfloat16, device="cuda")
     odd = buf[1:].view(Wx.shape).copy_(Wx)
@@ -196,8 +197,10 @@ def test_unaligned_views(S):
     for o in (a, b):
         close(o["y"], f["y"], f["y_err"], HALF["bf16"])
     g = O.gated_backward(np64(Wx), "fz", np64(dy), np64(s0), np64(ds), fast=True)
-    r = S.gated_recurrence_backward(odd, b["stash"], dy, dstate=ds)
-    close(r["dWx"], g["dWx"], g["dWx_err"], HALF["bf16"])
+    for w, stash in ((odd, b["stash"]), (odd, a["stash"]), (Wx, b["stash"])):
+        r = S.gated_recurrence_backward(w, stash, dy, dstate=ds)
+        close(r["dWx"], g["dWx"], g["dWx_err"], HALF["bf16"])
+        close(r["dstate"], g["dstate"], g["dstate_err"])
 
 
 def test_in_place_states_and_streams(S):
