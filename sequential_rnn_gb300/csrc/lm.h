@@ -196,7 +196,7 @@ struct RotaryParams {
   float* dkw;
   float* part;           // [kRotaryParts, 2, D]
   long long qs[3], ks[3], dqs[3], dks[3];  // strides in elements: token, row, head
-  int T, B, NQ, NK, D, rot, interleaved, per_token, split;
+  int T, B, NQ, NK, D, rot, interleaved, per_token, split, ctas_q;
   float eps;
 };
 int launch_rotary(RotaryParams p, bool bf16, bool bwd, cudaStream_t s);

@@ -10,8 +10,9 @@
 // the number of whole turns (in fp32 position 10^6 would be off by 2^-4 radians).  A frequency is a double
 // (the caller's), its quotient by 2 pi is formed in two doubles.
 //
-// Bound by bytes.  A warp takes a token: the lanes of a head hold 8 columns each, in pairs, and the token's sines and
-// cosines, taken once, serve all heads of q and k.
+// Bound by bytes, and issue slots beside them: 16384 tokens of 12 + 12 x 64 heads in bf16 take 19.7 us, 5.1 TB/s.  A warp takes a
+// token: the lanes of a head hold 8 columns each, in pairs, and the token's sines and cosines, taken once, serve all its
+// heads.  Few tokens are bound by the launch and one pass of latencies: 16 of them 3.5 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -318,8 +319,8 @@ struct Items {
   }
 };
 
-constexpr int kRingTokens = 16;               // for each SM
-constexpr size_t kRingMost = 200 * 1024;      // bytes of a CTA's rings
+constexpr int kRingTokens = 16, kRingTokensBwd = 8;  // for each SM
+constexpr size_t kRingMost = 200 * 1024;             // bytes of a CTA's rings
 constexpr int kBatch = 3, kBatchBwd = 2;  // heads that a lane loads before it uses the first
 
 template <class T, int LPH, int MODE>
@@ -451,30 +452,45 @@ __global__ void __launch_bounds__(256, 2) rotary_bwd_kernel(const RotaryParams p
   }
 }
 
-// Many tokens, heads of 32, 64, 128 or 256 at 16-byte addresses: a warp takes whole tokens, which asynchronous copies bring
-// into a ring of its own in shared memory, so that a token is on its way while one is worked on and no register holds it (two on
+// Many tokens, heads of 32, 64, 128 or 256 at 16-byte addresses: asynchronous copies bring what a warp takes next into a ring
+// of its own in shared memory, so that it is on its way while the warp works and no register holds it (two on
 // their way, with fewer CTAs on an SM, are no faster: 1024 x 16 tokens of 12 + 12 x 64 heads 20.8 us against 19.6, 1024 x 8 of
 // 16 + 8 x 128 30.9 against 22.5).  A sweep is what the warp takes at once: 32 / LPH heads.
 template <class T, int LPH>
 struct Ring {
-  static constexpr int HPW = 32 / LPH, D = 8 * LPH, SWEEP = 32 * 8 * sizeof(T);
+  static constexpr int HPW = 32 / LPH, D = 8 * LPH, SWEEP = 32 * 8 * sizeof(T), STAGES = 2;
   static constexpr int E = 16 / sizeof(T), COPIES = SWEEP / 512;  // values of a copy, copies of a sweep for each lane
-  static int sweeps(const RotaryParams& p) { return (p.NQ + HPW - 1) / HPW + (p.NK + HPW - 1) / HPW; }
+  __host__ __device__ static int sweeps(int heads) { return (heads + HPW - 1) / HPW; }
+  static size_t smem(const RotaryParams& p) { return (size_t)STAGES * 8 * (sweeps(p.NQ) + sweeps(p.NK)) * SWEEP; }
+  // H heads, `stride` apart, brought to `to` (16 bytes a lane)
+  static __device__ __forceinline__ void bring(uint32_t to, const T* x, long long stride, int H, int lane) {
+#pragma unroll
+    for (int c = 0; c < COPIES; ++c) {
+      const int v = (c * 32 + lane) * E, h = v / D;
+      const T* from = x + h * stride + v % D;
+      uint32_t d = to + c * 512 + 16 * lane;
+#pragma unroll 3
+      for (int i = 0; i < H; i += HPW) {
+        if (i + h < H) cp_async16(d, from);
+        from += HPW * stride, d += SWEEP;
+      }
+    }
+  }
 };
 
-template <class T, int LPH, int MODE, bool BWD>
-__global__ void __launch_bounds__(256, BWD || sizeof(T) == 4 ? 2 : 3) rotary_ring_kernel(const RotaryParams p) {
+// A warp takes whole tokens.
+template <class T, int LPH, int MODE>
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) rotary_ring_kernel(const RotaryParams p) {
   using C = Ring<T, LPH>;
-  constexpr int HPW = C::HPW, D = C::D, STAGES = 2;
+  constexpr int HPW = C::HPW, D = C::D, STAGES = C::STAGES;
   extern __shared__ __align__(128) char dyn[];
   __shared__ Consts sh;
-  __shared__ float part[BWD ? 8 : 1][2][BWD ? D : 1];
   depend_launch();
   Lanes<LPH, MODE> w(p);
   w.spread(D * sizeof(T));
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int nq = (p.NQ + HPW - 1) / HPW, nk = (p.NK + HPW - 1) / HPW, size = (nq + nk) * C::SWEEP;
-  char* const ring = dyn + warp * STAGES * size * (BWD ? 2 : 1);
+  const int nq = C::sweeps(p.NQ), nk = C::sweeps(p.NK), size = (nq + nk) * C::SWEEP;
+  char* const ring = dyn + warp * STAGES * size;
   const unsigned line = blockIdx.x * 8 + warp, lines = gridDim.x * 8, dt = lines / p.B, db = lines % p.B;
   depend_wait();
   // token (t, b): the one to be copied, then the one to be worked on
@@ -485,26 +501,9 @@ __global__ void __launch_bounds__(256, BWD || sizeof(T) == 4 ? 2 : 3) rotary_rin
   };
   auto bring = [&](int stage) {
     if (at < (unsigned)p.T) {
-      uint32_t to = smem_u32(ring + stage * size * (BWD ? 2 : 1)) + 16 * lane;
-#pragma unroll
-      for (int k = 0; k < (BWD ? 4 : 2); ++k) {
-        const long long* st = k == 0 ? p.qs : k == 1 ? p.ks : k == 2 ? p.dqs : p.dks;
-        const void* base = k == 0 ? p.q : k == 1 ? p.k : k == 2 ? p.dq : p.dk;
-        const int H = k % 2 ? p.NK : p.NQ, n = k % 2 ? nk : nq;
-        const T* x = static_cast<const T*>(base) + at * st[0] + ab * st[1];
-#pragma unroll
-        for (int c = 0; c < C::COPIES; ++c) {
-          const int v = (c * 32 + lane) * C::E, h = v / D;
-          const T* from = x + h * st[2] + v % D;
-          uint32_t d = to + c * 512;
-#pragma unroll 3
-          for (int i = 0; i < n; ++i) {
-            if (i * HPW + h < H) cp_async16(d, from);
-            from += HPW * st[2], d += C::SWEEP;
-          }
-        }
-        to += n * C::SWEEP;
-      }
+      const uint32_t to = smem_u32(ring + stage * size);
+      C::bring(to, static_cast<const T*>(p.q) + at * p.qs[0] + ab * p.qs[1], p.qs[2], p.NQ, lane);
+      C::bring(to + nq * C::SWEEP, static_cast<const T*>(p.k) + at * p.ks[0] + ab * p.ks[1], p.ks[2], p.NK, lane);
     }
     cp_async_commit();
     next(at, ab);
@@ -514,55 +513,25 @@ __global__ void __launch_bounds__(256, BWD || sizeof(T) == 4 ? 2 : 3) rotary_rin
   sh.load(p);
   constexpr float inv = 1.f / D;
   const Pairs wq = w.weights(sh.w[0]), wk = w.weights(sh.w[1]);
-  Pairs sq, sk;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) sq.a[j] = sq.b[j] = sk.a[j] = sk.b[j] = Num<2>(0.f);
   Turn tn;
   const bool norm = p.qw != nullptr;  // (without: weights of one, r = 1)
-  auto sweep = [&](const T* x, const T* d, T* o, const Pairs& wt, Pairs& sum, bool on) {
+  auto sweep = [&](const T* x, T* o, const Pairs& wt, bool on) {
     Head<T, MODE> raw;
     w.load(raw, x);
     Pairs y = w.get(raw);
-    if (BWD && !norm)  // (x does not matter then, whatever it is)
+    const Num<2> r(norm ? rsqrtf(fmaf(head_sum<LPH>(dot(y, y)), inv, p.eps)) : 1.f);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) y.a[j] = y.b[j] = Num<2>(0.f);
-    const float r1 = norm ? rsqrtf(fmaf(head_sum<LPH>(dot(y, y)), inv, p.eps)) : 1.f;
-    const Num<2> r(r1);
-    if constexpr (!BWD) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) y.a[j] = y.a[j] * (r * wt.a[j]), y.b[j] = y.b[j] * (r * wt.b[j]);
-      rotate(y, tn.c, tn.s, tn.n);
-      if (on) w.store(o, y);
-    } else {
-      Head<T, MODE> rd;
-      w.load(rd, d);
-      Pairs g = w.get(rd), gw;
-      rotate(g, tn.c, tn.n, tn.s);  // back
-#pragma unroll
-      for (int j = 0; j < 2; ++j) gw.a[j] = g.a[j] * wt.a[j], gw.b[j] = g.b[j] * wt.b[j];
-      const float along = head_sum<LPH>(dot(gw, y));
-      const Num<2> m(norm ? -(along * inv) * r1 * r1 : 0.f);  // - mean(w g xh) r
-      if (on)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          sum.a[j] = fma(g.a[j], y.a[j] * r, sum.a[j]);
-          sum.b[j] = fma(g.b[j], y.b[j] * r, sum.b[j]);
-        }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        g.a[j] = r * fma(m, y.a[j], gw.a[j]);
-        g.b[j] = r * fma(m, y.b[j], gw.b[j]);
-      }
-      if (on) w.store(o, g);
-    }
+    for (int j = 0; j < 2; ++j) y.a[j] = y.a[j] * (r * wt.a[j]), y.b[j] = y.b[j] * (r * wt.b[j]);
+    rotate(y, tn.c, tn.s, tn.n);
+    if (on) w.store(o, y);
   };
-  auto heads = [&](const T* x, const T* d, T* o, int n, const Pairs& wt, Pairs& sum) {
+  auto heads = [&](const T* x, T* o, int n, const Pairs& wt) {
 #pragma unroll 3
     for (int i = n / HPW; i > 0; --i) {
-      sweep(x, d, o, wt, sum, true);
-      x += HPW * D, d += HPW * D, o += HPW * D;
+      sweep(x, o, wt, true);
+      x += HPW * D, o += HPW * D;
     }
-    if (n % HPW) sweep(x, d, o, wt, sum, w.sub < n % HPW);  // (what the others compute stays in their own head)
+    if (n % HPW) sweep(x, o, wt, w.sub < n % HPW);  // (what the others compute stays in their own head)
   };
   long long pos = t < (unsigned)p.T ? position(p, t, b) : 0;
   const int mine = w.sub * D;
@@ -575,33 +544,162 @@ __global__ void __launch_bounds__(256, BWD || sizeof(T) == 4 ? 2 : 3) rotary_rin
     if (t < (unsigned)p.T) pos = position(p, t, b);  // a token ahead
     cp_async_wait<STAGES - 1>();
     __syncwarp();
-    const T* x = reinterpret_cast<const T*>(ring + stage * size * (BWD ? 2 : 1)) + mine;
-    const T* d = BWD ? x + size / (int)sizeof(T) : x;
-    heads(x, d, qo, p.NQ, wq, sq);
-    heads(x + nq * HPW * D, d + nq * HPW * D, ko, p.NK, wk, sk);
+    const T* x = reinterpret_cast<const T*>(ring + stage * size) + mine;
+    heads(x, qo, p.NQ, wq);
+    heads(x + nq * HPW * D, ko, p.NK, wk);
     __syncwarp();  // (the stage is filled again by the next copies)
     qo += (long long)lines * p.NQ * D, ko += (long long)lines * p.NK * D;
   }
-  if constexpr (BWD) {
-    if (!p.qw) return;
-    if (w.swap) {
-      Pairs x = sq;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) sq.a[j] = x.b[j], sq.b[j] = x.a[j];
-      x = sk;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) sk.a[j] = x.b[j], sk.b[j] = x.a[j];
+}
+
+// Gradient: a CTA takes q's heads or k's, so that a warp keeps one set of weights and of their gradients' sums, and a warp
+// a group of a token's heads at a time, so that rings hold any number of heads.  8004 tokens of 6 + 6 x 128 heads take
+// 20.6 us with dw's sum (3.7 TB/s; bound by latency, with 16 warps an SM, and issue slots), whole tokens by a warp 22.8; 1024 x 8
+// of 16 + 8 x 128 37 and 48, 1024 x 4 of 8 + 4 x 256 24 and 33, but of 12 + 1 x 64 12.0 and 11.2, where k's sweeps are
+// mostly empty.  (Forward, whole tokens keep fewer registers and take their sines once: 19.7 us against 20.6 for 16384 tokens of
+// 12 + 12 x 64.)  Sixteen warps a CTA, one on an SM: twice eight leave twice the sums (21.4 us), twenty spill (21.2).
+template <class T, int LPH>
+struct Groups {
+  using C = Ring<T, LPH>;
+  // warps; sweeps of a group (192 KB for a CTA; of 2 rather than 3 sweeps 30.7 us for the 8004 tokens above)
+  static constexpr int W = 16, MOST = 6 * 512 / C::SWEEP;
+  int n, sweeps;  // groups of a token, sweeps of each but the last
+  __host__ __device__ explicit Groups(int heads) {
+    const int all = C::sweeps(heads);
+    n = (all + MOST - 1) / MOST;
+    sweeps = n > 0 ? (all + n - 1) / n : 0;
+  }
+  __host__ __device__ int bytes() const { return C::STAGES * 2 * sweeps * C::SWEEP; }  // of a warp
+  // of a token, in half sweeps: a group's sines are that of one
+  int work(int heads) const { return 2 * C::sweeps(heads) + n; }
+};
+
+// ONE: of q and of k, one group at most (20.6 us for the tokens above against 21.5 that keep count of groups)
+template <class T, int LPH, int MODE, bool ONE>
+__global__ void __launch_bounds__(32 * Groups<T, LPH>::W, 1) rotary_ring_bwd_kernel(const RotaryParams p) {
+  using C = Ring<T, LPH>;
+  constexpr int HPW = C::HPW, D = C::D, STAGES = C::STAGES, W = Groups<T, LPH>::W;
+  extern __shared__ __align__(128) char dyn[];
+  __shared__ Consts sh;
+  __shared__ float part[W][D];
+  depend_launch();
+  Lanes<LPH, MODE> w(p);
+  w.spread(D * sizeof(T));
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const bool isk = blockIdx.x >= (unsigned)p.ctas_q;
+  const int H = isk ? p.NK : p.NQ;
+  const long long* const xs = isk ? p.ks : p.qs;
+  const long long* const ds = isk ? p.dks : p.dqs;
+  const T* const x0 = static_cast<const T*>(isk ? p.k : p.q);
+  const T* const d0 = static_cast<const T*>(isk ? p.dk : p.dq);
+  const Groups<T, LPH> gr(H);
+  const int most = gr.sweeps * HPW, size = gr.sweeps * C::SWEEP;
+  char* const ring = dyn + warp * gr.bytes();
+  const unsigned cta = isk ? blockIdx.x - p.ctas_q : blockIdx.x, ctas = isk ? gridDim.x - p.ctas_q : p.ctas_q;
+  const unsigned line = cta * W + warp, lines = ctas * W;
+  depend_wait();
+  struct At {  // a group of a token
+    unsigned t, b, g;
+  };
+  auto place = [&](unsigned i) {
+    const unsigned row = ONE ? i : i / gr.n, t = row / p.B;
+    return At{t, row - t * p.B, ONE ? 0 : i - row * gr.n};
+  };
+  const At step = place(lines);
+  At to = place(line), at = to;  // the one to be copied, the one to be worked on
+  auto next = [&](At& x) {
+    x.t += step.t, x.b += step.b;
+    if (!ONE) {
+      x.g += step.g;
+      if (x.g >= (unsigned)gr.n) x.g -= gr.n, ++x.b;
     }
-    sum_lanes<LPH>(sq);
-    sum_lanes<LPH>(sk);
-    if (w.sub == 0) w.add_to(part[warp][0], sq), w.add_to(part[warp][1], sk);
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
-      float v = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v += part[j][i / D][i % D];
-      p.part[(long long)blockIdx.x * 2 * D + i] = v;
+    if (x.b >= (unsigned)p.B) x.b -= p.B, ++x.t;
+  };
+  auto bring = [&](int stage) {
+    if (to.t < (unsigned)p.T) {
+      const uint32_t a = smem_u32(ring + stage * 2 * size);
+      const int h = ONE ? 0 : to.g * most, n = ONE || H - h < most ? H - h : most;
+      C::bring(a, x0 + to.t * xs[0] + to.b * xs[1] + h * xs[2], xs[2], n, lane);
+      C::bring(a + size, d0 + to.t * ds[0] + to.b * ds[1] + h * ds[2], ds[2], n, lane);
     }
+    cp_async_commit();
+    next(to);
+  };
+#pragma unroll
+  for (int k = 0; k < STAGES - 1; ++k) bring(k);
+  sh.load(p);
+  constexpr float inv = 1.f / D;
+  const Pairs wt = w.weights(sh.w[isk]);
+  Pairs sum;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) sum.a[j] = sum.b[j] = Num<2>(0.f);
+  Turn tn;
+  const bool norm = p.qw != nullptr;  // (without: weights of one, r = 1)
+  auto sweep = [&](const T* x, const T* d, T* o, bool on) {
+    Head<T, MODE> raw, rd;
+    w.load(raw, x);
+    Pairs y = w.get(raw);
+    if (!norm)  // (x does not matter then, whatever it is)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) y.a[j] = y.b[j] = Num<2>(0.f);
+    const float r1 = norm ? rsqrtf(fmaf(head_sum<LPH>(dot(y, y)), inv, p.eps)) : 1.f;
+    const Num<2> r(r1);
+    w.load(rd, d);
+    Pairs g = w.get(rd), gw;
+    rotate(g, tn.c, tn.n, tn.s);  // back
+#pragma unroll
+    for (int j = 0; j < 2; ++j) gw.a[j] = g.a[j] * wt.a[j], gw.b[j] = g.b[j] * wt.b[j];
+    const float along = head_sum<LPH>(dot(gw, y));
+    const Num<2> m(norm ? -(along * inv) * r1 * r1 : 0.f);  // - mean(w g xh) r
+    if (on)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        sum.a[j] = fma(g.a[j], y.a[j] * r, sum.a[j]);
+        sum.b[j] = fma(g.b[j], y.b[j] * r, sum.b[j]);
+      }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      g.a[j] = r * fma(m, y.a[j], gw.a[j]);
+      g.b[j] = r * fma(m, y.b[j], gw.b[j]);
+    }
+    if (on) w.store(o, g);
+  };
+  long long pos = at.t < (unsigned)p.T ? position(p, at.t, at.b) : 0;
+  const int mine = w.sub * D;
+  T* const out = static_cast<T*>(isk ? p.ko : p.qo) + mine;
+  for (int stage = 0; at.t < (unsigned)p.T; stage = stage + 1 == STAGES ? 0 : stage + 1) {
+    bring(stage == 0 ? STAGES - 1 : stage - 1);
+    tn = turn_of<Lanes<LPH, MODE>, LPH>(w, sh.freqs, pos);
+    const int h = ONE ? 0 : at.g * most, n = ONE || H - h < most ? H - h : most;
+    T* o = out + ((long long)(at.t * p.B + at.b) * H + h) * D;
+    next(at);
+    if (at.t < (unsigned)p.T) pos = position(p, at.t, at.b);  // a group ahead
+    cp_async_wait<STAGES - 1>();
+    __syncwarp();
+    const T* x = reinterpret_cast<const T*>(ring + stage * 2 * size) + mine;
+    const T* d = x + size / (int)sizeof(T);
+#pragma unroll 3
+    for (int i = n / HPW; i > 0; --i) {
+      sweep(x, d, o, true);
+      x += HPW * D, d += HPW * D, o += HPW * D;
+    }
+    if (n % HPW) sweep(x, d, o, w.sub < n % HPW);  // (what the others compute stays in their own head)
+    __syncwarp();  // (the stage is filled again by the next copies)
+  }
+  if (!p.qw) return;
+  if (w.swap) {
+    const Pairs x = sum;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) sum.a[j] = x.b[j], sum.b[j] = x.a[j];
+  }
+  sum_lanes<LPH>(sum);
+  if (w.sub == 0) w.add_to(part[warp], sum);
+  __syncthreads();
+  for (int i = threadIdx.x; i < D; i += blockDim.x) {
+    float v = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) v += part[j][i];
+    p.part[(long long)blockIdx.x * 2 * D + isk * D + i] = v;
   }
 }
 
@@ -678,22 +776,27 @@ __global__ void __launch_bounds__(32) rotary_any_kernel(const RotaryParams p) {
   }
 }
 
-// dw[i] = sum of the CTAs' parts in a fixed order: 32 columns a CTA, 32 threads for each
-__global__ void __launch_bounds__(1024) rotary_dw_kernel(const float* part, float* dqw, float* dkw, int parts, int D) {
-  __shared__ float sh[32][33];
+// dw[i] = sum of the CTAs' parts in a fixed order: 8 columns a CTA, 32 threads for each.  q's are of the parts up to end_q,
+// k's of those from first_k on.  (CTAs of 256 threads find room beside those of the kernel before and wait there: 0.4 us less
+// than with 1024)
+__global__ void __launch_bounds__(256) rotary_dw_kernel(const float* part, float* dqw, float* dkw, int parts, int end_q,
+                                                         int first_k, int D) {
+  __shared__ float sh[32][9];
   depend_launch();
   depend_wait();
-  const int x = threadIdx.x % 32, y = threadIdx.x / 32, i = blockIdx.x * 32 + x;
+  const int x = threadIdx.x % 8, y = threadIdx.x / 8, i = blockIdx.x * 8 + x;
   float v = 0.f;
   if (i < 2 * D) {
+    const int n = i < D ? end_q : parts - first_k;
+    const float* at = part + i + (i < D ? 0LL : (long long)first_k * 2 * D);
 #pragma unroll 8
-    for (int j = y; j < parts; j += 32) v += part[(long long)j * 2 * D + i];
+    for (int j = y; j < n; j += 32) v += at[(long long)j * 2 * D];
   }
   sh[y][x] = v;
   __syncthreads();
-  v = head_sum<32>(sh[x][y]);
-  const int c = blockIdx.x * 32 + y;
-  if (x == 0 && c < 2 * D) (c < D ? dqw : dkw)[c % D] = v;
+  v = head_sum<32>(sh[threadIdx.x % 32][threadIdx.x / 32]);
+  const int c = blockIdx.x * 8 + threadIdx.x / 32;
+  if (threadIdx.x % 32 == 0 && c < 2 * D) (c < D ? dqw : dkw)[c % D] = v;
 }
 
 bool at16(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -709,9 +812,9 @@ bool vector_form(const RotaryParams& p, bool bwd) {
   return ok;
 }
 
-int reduce_dw(const RotaryParams& p, int parts, cudaStream_t s) {
-  return launch_dependent(rotary_dw_kernel, (unsigned)((2 * p.D + 31) / 32), 1024, 0, s, (const float*)p.part, p.dqw, p.dkw,
-                          parts, p.D);
+int reduce_dw(const RotaryParams& p, int parts, int end_q, int first_k, cudaStream_t s) {
+  return launch_dependent(rotary_dw_kernel, (unsigned)((2 * p.D + 7) / 8), 256, 0, s, (const float*)p.part, p.dqw, p.dkw,
+                          parts, end_q, first_k, p.D);
 }
 
 template <class T, int LPH, int MODE>
@@ -720,17 +823,18 @@ int launch_lanes(RotaryParams& p, bool bwd, cudaStream_t s) {
   const int heads = 32 / LPH * (bwd ? kBatchBwd : kBatch), per_sm = bwd ? 2 : 3;
   const int groups = (p.NQ + heads - 1) / heads + (p.NK + heads - 1) / heads;
   // few tokens: a warp for each batch of heads, so that the latency of one batch is that of all (608 tokens of 12 + 12 x 64
-  // heads 3.6 us against 4.3, 1216 4.5 against 4.4; gradient 1216 8.0 against 9.4, 2432 11.2 against 9.2)
+  // heads 3.6 us against 4.3, 1216 4.5 against 4.4; gradient 1216 8.0 against 9.4, 2432 11.2 against 9.2, where rings cannot
+  // take them)
   p.split = tokens < (bwd ? 16LL : 8LL) * sm_count();
   const long long want = (tokens * (p.split ? groups : 1) + 7) / 8, most = (long long)per_sm * sm_count();
   unsigned grid = (unsigned)(want < most ? want : most);
   if (!bwd) return launch_dependent(rotary_kernel<T, LPH, MODE>, grid, 256, 0, s, (const RotaryParams)p);
   if (grid > kRotaryParts) grid = kRotaryParts;
   const int e = launch_dependent(rotary_bwd_kernel<T, LPH, MODE>, grid, 256, 0, s, (const RotaryParams)p);
-  return e != 0 || !p.qw ? e : reduce_dw(p, (int)grid, s);
+  return e != 0 || !p.qw ? e : reduce_dw(p, (int)grid, (int)grid, 0, s);
 }
-// 16-byte copies, and tokens enough: 4864 of 12 + 12 x 64 heads take 7.9 us against 8.3 by batches (gradient 13.7 against
-// 15.7), 2432 5.6 against 5.9 (9.2 both), 608 4.2 against 4.3, and 3.6 with the batches split
+// 16-byte copies, and tokens enough: 4864 of 12 + 12 x 64 heads take 7.9 us against 8.3 by batches (gradient 13.5 against
+// 16.0), 2432 5.6 against 5.9 (9.0 against 9.4; 1216 7.1 against 8.2), 608 4.2 against 4.3, and 3.6 with the batches split
 template <class T, int LPH>
 bool ring_form(const RotaryParams& p, bool bwd) {
   auto even = [](const void* x, const long long (&s)[3]) {
@@ -738,24 +842,41 @@ bool ring_form(const RotaryParams& p, bool bwd) {
   };
   bool ok = p.D == 8 * LPH && vector_form<T>(p, bwd) && even(p.q, p.qs) && even(p.k, p.ks);
   if (bwd) ok = ok && even(p.dq, p.dqs) && even(p.dk, p.dks);
-  ok = ok && (bwd ? 4 : 2) * 8LL * Ring<T, LPH>::sweeps(p) * Ring<T, LPH>::SWEEP <= kRingMost;
-  return ok && (long long)p.T * p.B >= kRingTokens * sm_count();
-}
-template <class T, int LPH, int MODE, bool BWD>
-int launch_ring(const RotaryParams& p, cudaStream_t s) {
-  static int prep[64][5];
-  const size_t smem = (BWD ? 4 : 2) * 8 * (size_t)Ring<T, LPH>::sweeps(p) * Ring<T, LPH>::SWEEP;
-  int e = prepare_launch(prep, rotary_ring_kernel<T, LPH, MODE, BWD>, (uint32_t)smem, 256, 1);
-  if (e != 0) return e;
-  const long long want = ((long long)p.T * p.B + 7) / 8, most = (BWD || sizeof(T) == 4 ? 2LL : 3LL) * sm_count();
-  unsigned grid = (unsigned)(want < most ? want : most);
-  if (BWD && grid > kRotaryParts) grid = kRotaryParts;
-  e = launch_dependent(rotary_ring_kernel<T, LPH, MODE, BWD>, grid, 256, smem, s, p);
-  return e != 0 || !BWD || !p.qw ? e : reduce_dw(p, (int)grid, s);
+  ok = ok && (bwd || Ring<T, LPH>::smem(p) <= kRingMost);
+  return ok && (long long)p.T * p.B >= (bwd ? kRingTokensBwd : kRingTokens) * sm_count();
 }
 template <class T, int LPH, int MODE>
-int launch_ring(const RotaryParams& p, bool bwd, cudaStream_t s) {
-  return bwd ? launch_ring<T, LPH, MODE, true>(p, s) : launch_ring<T, LPH, MODE, false>(p, s);
+int launch_ring(const RotaryParams& p, cudaStream_t s) {
+  static int prep[64][5];
+  const size_t smem = Ring<T, LPH>::smem(p);
+  const int e = prepare_launch(prep, rotary_ring_kernel<T, LPH, MODE>, (uint32_t)smem, 256, 1);
+  if (e != 0) return e;
+  const long long want = ((long long)p.T * p.B + 7) / 8, most = (sizeof(T) == 4 ? 2LL : 3LL) * sm_count();
+  return launch_dependent(rotary_ring_kernel<T, LPH, MODE>, (unsigned)(want < most ? want : most), 256, smem, s, p);
+}
+template <class T, int LPH, int MODE, bool ONE>
+int launch_ring_bwd(RotaryParams& p, cudaStream_t s) {
+  using G = Groups<T, LPH>;
+  static int prep[64][5];
+  const G q(p.NQ), k(p.NK);
+  const size_t smem = (size_t)G::W * (q.bytes() > k.bytes() ? q.bytes() : k.bytes());
+  const int e = prepare_launch(prep, rotary_ring_bwd_kernel<T, LPH, MODE, ONE>, (uint32_t)smem, 32 * G::W, 1);
+  if (e != 0) return e;
+  // q's and k's CTAs by their work; at least one for each that has heads
+  const int most = sm_count() < kRotaryParts ? sm_count() : kRotaryParts;
+  const long long wq = q.work(p.NQ), wk = k.work(p.NK);
+  int nq = (int)((most * wq + (wq + wk) / 2) / (wq + wk));
+  if (wq > 0 && wk > 0) nq = nq < 1 ? 1 : nq > most - 1 ? most - 1 : nq;
+  p.ctas_q = nq;
+  const int err = launch_dependent(rotary_ring_bwd_kernel<T, LPH, MODE, ONE>, (unsigned)most, 32 * G::W, smem, s,
+                                   (const RotaryParams)p);
+  return err != 0 || !p.qw ? err : reduce_dw(p, most, nq, nq, s);
+}
+template <class T, int LPH, int MODE>
+int launch_ring(RotaryParams& p, bool bwd, cudaStream_t s) {
+  if (!bwd) return launch_ring<T, LPH, MODE>(p, s);
+  return Groups<T, LPH>(p.NQ).n <= 1 && Groups<T, LPH>(p.NK).n <= 1 ? launch_ring_bwd<T, LPH, MODE, true>(p, s)
+                                                                    : launch_ring_bwd<T, LPH, MODE, false>(p, s);
 }
 template <class T, int LPH>
 int launch_mode(RotaryParams& p, bool bwd, cudaStream_t s) {
@@ -779,7 +900,7 @@ int launch_t(RotaryParams& p, bool bwd, cudaStream_t s) {
   const int grid = (int)(items < kRotaryParts ? items : kRotaryParts);
   const int e = launch_dependent(rotary_any_kernel<T, true>, (unsigned)grid, 32, p.qw ? 8 * (size_t)p.D : 0, s,
                                  (const RotaryParams)p);
-  return e != 0 || !p.qw ? e : reduce_dw(p, grid, s);
+  return e != 0 || !p.qw ? e : reduce_dw(p, grid, grid, 0, s);
 }
 
 }  // namespace

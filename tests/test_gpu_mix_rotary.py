@@ -85,6 +85,18 @@ def test_many_tokens(S, T, B, NQ, NK, D, rot, inter, dtype):
     check(S, qkv[:, :, :NQ], qkv[:, :, NQ:NQ + NK], w[0], w[1], S.rotary_frequencies(rot), at, inter, dtype)
 
 
+# the gradient's groups of heads: several of q's, of k's, of both, the last one smaller; fewer tokens than warps
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("T,B,NQ,NK,D,rot", [
+    (410, 3, 33, 13, 128, 128), (1300, 1, 1, 29, 64, 32), (9, 137, 7, 1, 256, 256), (614, 2, 49, 50, 32, 32), (1, 1219, 8, 0, 256, 64)])
+def test_head_groups(S, T, B, NQ, NK, D, rot, inter, dtype):
+    qkv = rand(1, T, B, NQ + NK, D, dtype=dtype, scale=2)
+    w = 1 + rand(3, 2, D, scale=0.2)
+    free = torch.randint(-10 ** 6, 10 ** 6, (T, B), generator=torch.Generator().manual_seed(1)).int().cuda()
+    check(S, qkv[:, :, :NQ], qkv[:, :, NQ:], w[0], w[1], S.rotary_frequencies(rot), free, inter, dtype)
+
+
 def test_many_tokens_without_norm_or_rotation(S):
     q, k, w = rand(1, 900, 3, 5, 64, dtype="bf16"), rand(2, 900, 3, 2, 64, dtype="bf16"), 1 + rand(3, 64, scale=0.2)
     f = S.rotary_frequencies(64)
