@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(32 * kWarps) gated_fwd_kernel(const GatedParam
   w.lengths(p);
   float h = p.state0 && w.at >= 0 ? p.state0[w.at] : 0.f;
   const int rounds = w.rounds();
+  __syncwarp();  // (the barrier takes a warp's lanes together)
   if (p.cs > 1) cluster_sync();  // every CTA has begun before another one writes to its shared memory
   Run<T, G, V> raw;
   if (rounds > 0) raw.load(wx, w.wstep, p.D, w.len - w.first);
@@ -264,6 +265,7 @@ __global__ void __launch_bounds__(32 * kWarps) gated_bwd_kernel(const GatedParam
   w.lengths(p);
   float h = p.dstateT && w.at >= 0 ? p.dstateT[w.at] : 0.f;  // gradient of the state after the round's last token
   const int rounds = w.rounds();
+  __syncwarp();
   if (p.cs > 1) cluster_sync();
   for (int k = rounds - 1; k >= 0; --k) {
     const int t0 = k * w.steps + w.first, n = w.len - t0;

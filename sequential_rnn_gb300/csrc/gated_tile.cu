@@ -354,6 +354,7 @@ __global__ void __launch_bounds__((Tile<T, G, BWD, X, AHEAD>::THREADS), (Tile<T,
       bar_arrive(kStart + buf, C::TALK);
     };
     for (int i = 0; i < rounds; ++i) {
+      __syncwarp();
       bar_sync(kReady + (AHEAD ? i & 1 : 0), C::TALK);
       Runs r;
       read(i, r);
