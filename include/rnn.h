@@ -472,7 +472,8 @@ int rnn_head_norm_rotary_bwd(const rnn_rotary_desc_t* desc, const rnn_rotary_str
  * them.  max_norm >= 0; INFINITY = the norm alone.  dtypes (rnn_dtype_t), sizes (elements; 0 is allowed) and
  * tensors (device memory, aligned as the element is) are host arrays, read before the call returns.  Unless max_norm is
  * INFINITY no two tensors may overlap (RNN_ERR_INVALID_ARG).  Sums are taken in fixed order, with fp64 above
- * 64 bytes; no square overflows (a norm that fp32 cannot hold is told as infinity, and clipped to max_norm all the same).  A tensor's size is at most 2^40.  Workspace: 256-byte aligned, size below. */
+ * 64 bytes; no square overflows (a norm that fp32 cannot hold is told as infinity, and clipped to max_norm all the same).  A tensor's size is at most 2^40, at most 2^28 tensors,
+ * 2^31 - 1 pieces of 16 KB in all of them.  Workspace: 256-byte aligned, size below. */
 size_t rnn_clip_grad_norm_workspace_size(int32_t n);
 int rnn_clip_grad_norm(int32_t n, const int32_t* dtypes, const int64_t* sizes, void* const* tensors, float max_norm,
                        float* norm, void* workspace, size_t workspace_bytes, void* stream);

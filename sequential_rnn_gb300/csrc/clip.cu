@@ -277,16 +277,13 @@ int launch_n(const ClipParams& p, cudaStream_t s) {
   // the tensors from i on that fit a launch; returns the next one
   auto fill = [&](int i) {
     t.n = 0;
-    long long units = 0;
+    t.units = 0;  // (no more than 32 bits hold: refused before)
     for (; i < p.n && t.n < N; ++i) {
       const long long size = p.sizes[i];
       if (size == 0) continue;
-      const long long per = kClipUnit / (p.dtypes[i] == 1 ? 2 : 4), more = (size + per - 1) / per;
-      if (units + more > 0x7fffffff) break;  // (of one tensor: refused before)
-      t.t[t.n++] = Entry{p.at[i], p.dtypes[i] == 1 ? -size : size, (int)units, 0};
-      units += more;
+      t.t[t.n++] = Entry{p.at[i], p.dtypes[i] == 1 ? -size : size, t.units, 0};
+      t.units += (int)clip_units(size, p.dtypes[i]);
     }
-    t.units = (int)units;
     return i;
   };
   const long long most = (long long)kCtasPerSm * sm_count();

@@ -204,6 +204,11 @@ int launch_rotary(RotaryParams p, bool bf16, bool bwd, cudaStream_t s);
 // ------------------------------------------------------------ clipping --
 constexpr int kClipTensors = 256;  // of a launch: their table is a kernel parameter
 constexpr int kClipUnit = 16384;   // bytes
+constexpr int kClipMost = 1 << 28; // tensors of a call: its partial sums are counted in 32 bits
+inline int64_t clip_units(int64_t size, int dtype) {  // of a tensor; dtype 1: bf16
+  const int64_t per = kClipUnit / (dtype == 1 ? 2 : 4);
+  return (size + per - 1) / per;
+}
 struct ClipParams {
   void* const* at;
   const int64_t* sizes;
@@ -211,7 +216,7 @@ struct ClipParams {
   int n;
   float limit;   // infinite: the norm alone
   float* norm;   // or null
-  double* part;  // clip_parts(n) partial sums
+  double* part;  // clip_parts(n) partial sums: of every launch's CTAs
 };
 int clip_parts(int n);
 int launch_clip(const ClipParams& p, cudaStream_t s);

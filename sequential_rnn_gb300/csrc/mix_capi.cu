@@ -197,19 +197,24 @@ int rnn_head_norm_rotary_bwd(const rnn_rotary_desc_t* d, const rnn_rotary_stride
 }
 
 size_t rnn_clip_grad_norm_workspace_size(int32_t n) {
-  return n < 0 ? 0 : align_up((size_t)clip_parts(n) * sizeof(double), 256);
+  return n < 0 || n > kClipMost ? 0 : align_up((size_t)clip_parts(n) * sizeof(double), 256);
 }
 
 int rnn_clip_grad_norm(int32_t n, const int32_t* dtypes, const int64_t* sizes, void* const* tensors, float max_norm,
                        float* norm, void* workspace, size_t workspace_bytes, void* stream) {
   if (n < 0 || !(max_norm >= 0.f)) return RNN_ERR_INVALID_ARG;
+  if (n > kClipMost) return RNN_ERR_UNSUPPORTED;
   if (n > 0 && (dtypes == nullptr || sizes == nullptr || tensors == nullptr)) return RNN_ERR_INVALID_ARG;
   bool rising = true;
   uintptr_t end = 0;
+  int64_t units = 0;
   for (int32_t i = 0; i < n; ++i) {
     if (!valid_dtype(dtypes[i]) || sizes[i] < 0) return RNN_ERR_INVALID_ARG;
     if (sizes[i] > (int64_t)1 << 40) return RNN_ERR_UNSUPPORTED;
     if (sizes[i] == 0) continue;
+    // (the same tensor may come more than once, so that the device's memory is no bound)
+    units += clip_units(sizes[i], dtypes[i]);
+    if (units > INT32_MAX) return RNN_ERR_UNSUPPORTED;
     if (tensors[i] == nullptr) return RNN_ERR_INVALID_ARG;
     if (!aligned(tensors[i], dtype_bytes(dtypes[i]))) return RNN_ERR_MISALIGNED;
     const uintptr_t at = reinterpret_cast<uintptr_t>(tensors[i]);

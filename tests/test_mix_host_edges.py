@@ -4,6 +4,8 @@ import re
 
 import pytest
 
+from tests.test_mix_host import A, INF, P, W, clip, lib  # noqa: F401 (lib: the fixture)
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sequential_rnn_gb300", "csrc")
 
 
@@ -19,3 +21,17 @@ def test_aligned_barriers_follow_a_joined_warp(name):
     for at in calls:
         before = re.sub(r"if \((p\.)?cs > 1\)( {)?\s*$", "", code[:at].rstrip()).rstrip()  # (the same for all of a CTA)
         assert before.endswith(("__syncwarp();", "__syncthreads();")), code[max(0, at - 200):at + 40]
+
+
+def test_clip_counts_that_pass_32_bits(lib):  # noqa: F811
+    """Units of 16 KB are counted in 32 bits, over all tensors of a call: each launch's partial sums have their place in the
+    workspace, whose size follows from the tensors' number alone."""
+    most = (1 << 40) // 4096 * 4096  # 2^28 units of fp32
+    for n in (8, 16, 17, 256):
+        tensors = [A + i * (most * 4) for i in range(n)]
+        assert clip(lib, tensors, sizes=[most] * n, limit=1.0) == 2, n
+        assert clip(lib, [A] * n, sizes=[most] * n, limit=INF) == 2, n
+    lot = (1 << 28) + 1
+    assert lib.rnn_clip_grad_norm_workspace_size(lot - 1) > 0
+    assert lib.rnn_clip_grad_norm_workspace_size(lot) == lib.rnn_clip_grad_norm_workspace_size((1 << 31) - 1) == 0
+    assert lib.rnn_clip_grad_norm(lot, P(A), P(A), P(A), 1.0, None, P(W), 1 << 40, None) == 2
