@@ -416,10 +416,14 @@ __global__ void __launch_bounds__(256, 2) rotary_bwd_kernel(const RotaryParams p
           for (int j = 0; j < 2; ++j) gw.a[j] = g.a[j] * wt.a[j], gw.b[j] = g.b[j] * wt.b[j];
           const float r = rsqrtf(fmaf(head_sum<LPH>(dot(v, v)), inv, p.eps));
           const Num<2> m(-(head_sum<LPH>(dot(gw, v)) * inv) * r * r), rr(r);  // - mean(w g xh) r
+          if (h < n)  // (others have zeros for x: with eps = 0 an infinite r, whose product is not a number)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              sum.a[j] = fma(g.a[j], v.a[j] * rr, sum.a[j]);
+              sum.b[j] = fma(g.b[j], v.b[j] * rr, sum.b[j]);
+            }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            sum.a[j] = fma(g.a[j], v.a[j] * rr, sum.a[j]);
-            sum.b[j] = fma(g.b[j], v.b[j] * rr, sum.b[j]);
             g.a[j] = rr * fma(m, v.a[j], gw.a[j]);
             g.b[j] = rr * fma(m, v.b[j], gw.b[j]);
           }
