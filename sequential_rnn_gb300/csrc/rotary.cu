@@ -739,12 +739,12 @@ __global__ void __launch_bounds__(32) rotary_any_kernel(const RotaryParams p) {
     const float* w = isq ? p.qw : p.kw;
     const long long pos = position(p, t, b);
     float sum = 0.f, along = 0.f;
-    for (int i = lane; i < p.D / 2; i += 32) {
+    for (int i = lane; w && i < p.D / 2; i += 32) {
       int ia, ib;
       columns(i, ia, ib);
       const float xa = get1(x + ia), xb = get1(x + ib);
       sum = fmaf(xa, xa, fmaf(xb, xb, sum));
-      if (BWD && w) {
+      if (BWD) {
         float c = 1.f, s = 0.f, ga = get1(g + ia), gb = get1(g + ib);
         if (i < half) turn(turns(p.freqs[i]), pos, c, s);
         along = fmaf(fmaf(ga, c, gb * s) * w[ia], xa, fmaf(fmaf(gb, c, -ga * s) * w[ib], xb, along));
@@ -755,20 +755,24 @@ __global__ void __launch_bounds__(32) rotary_any_kernel(const RotaryParams p) {
     for (int i = lane; i < p.D / 2; i += 32) {
       int ia, ib;
       columns(i, ia, ib);
-      const float wa = w ? w[ia] : 1.f, wb = w ? w[ib] : 1.f, xa = get1(x + ia), xb = get1(x + ib);
+      const float wa = w ? w[ia] : 1.f, wb = w ? w[ib] : 1.f;
       float c = 1.f, s = 0.f;
       if (i < half) turn(turns(p.freqs[i]), pos, c, s);
       if (BWD) {
         const float ya = get1(g + ia), yb = get1(g + ib), ga = fmaf(ya, c, yb * s), gb = fmaf(yb, c, -ya * s);
         if (w) {
+          const float xa = get1(x + ia), xb = get1(x + ib);
           float* to = acc + (isq ? 0 : p.D);
           to[ia] = fmaf(ga, xa * r, to[ia]);
           to[ib] = fmaf(gb, xb * r, to[ib]);
+          put1(o + ia, r * fmaf(-m, xa, ga * wa));
+          put1(o + ib, r * fmaf(-m, xb, gb * wb));
+        } else {  // (x does not matter then, whatever it is)
+          put1(o + ia, ga);
+          put1(o + ib, gb);
         }
-        put1(o + ia, r * fmaf(-m, xa, ga * wa));
-        put1(o + ib, r * fmaf(-m, xb, gb * wb));
       } else {
-        const float ya = xa * (r * wa), yb = xb * (r * wb);
+        const float ya = get1(x + ia) * (r * wa), yb = get1(x + ib) * (r * wb);
         put1(o + ia, fmaf(ya, c, -yb * s));
         put1(o + ib, fmaf(yb, c, ya * s));
       }
