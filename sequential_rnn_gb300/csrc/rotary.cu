@@ -60,9 +60,10 @@ __device__ __forceinline__ long long position(const RotaryParams& p, unsigned t,
 
 // A head among LPH lanes, four pairs of columns each: how a lane reaches them.
 //   kHalf   pairs (j, j + rot / 2): two pieces of four neighbouring columns (past rot, two of what is not turned)
-//   kNext   pairs (2 j, 2 j + 1): eight neighbouring columns
+//   kNext   pairs (2 j, 2 j + 1): eight neighbouring columns, all turned or none
+//   kSome   the same where one lane of a head has both (rot no multiple of 8)
 //   kAny    either, pairs LPH apart, value by value: sizes and addresses that are no multiples of four values
-enum : int { kHalf = 0, kNext = 1, kAny = 2 };
+enum : int { kHalf = 0, kNext = 1, kAny = 2, kSome = 3 };
 
 template <class T, int MODE>
 struct Head;  // a lane's raw values
@@ -83,6 +84,8 @@ struct Head<float, kNext> {
   float4 a, b;
 };
 template <class T>
+struct Head<T, kSome> : Head<T, kNext> {};
+template <class T>
 struct Head<T, kAny> {
   T a[4], b[4];
 };
@@ -94,18 +97,21 @@ struct Pairs {
 
 template <int LPH, int MODE>
 struct Lanes {
+  static constexpr bool NEXT = MODE == kNext || MODE == kSome;
   int l, sub;    // lane of the head, the warp's head of it
   int a0, gap;   // vector forms: first column, from the first piece to the second
   int half, D;
   bool inter, on;
   bool swap;     // kHalf: the pair's second value first
+  int live;      // so many of the lane's pairs turn, the first ones
+  bool mixed;    // some lanes have pairs of both kinds (the same for all)
   __device__ explicit Lanes(const RotaryParams& p) {
     const int lane = threadIdx.x % 32;
     l = lane % LPH, sub = lane / LPH;
     half = p.rot / 2, D = p.D, inter = p.interleaved;
     a0 = 0, gap = 4;
     on = 8 * l < D;
-    if (MODE == kNext) {
+    if (NEXT) {
       a0 = 8 * l;
     } else if (MODE == kHalf) {
       if (4 * l < half)
@@ -117,6 +123,11 @@ struct Lanes {
     }
     if (!on && MODE != kAny) a0 = 0;
     swap = false;
+    live = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) live += pair(i) < half ? 1 : 0;
+    mixed = MODE == kAny ? p.rot < D : MODE == kSome;
+    if (!mixed && MODE == kAny) live = 4;
   }
   // The lanes of some heads read their pieces in the other order, so that those that shared memory serves at once
   // (128 bytes) lie in different banks.  row: bytes of a head
@@ -125,7 +136,7 @@ struct Lanes {
     a0 += gap, gap = -gap;
     swap = true;
   }
-  __device__ int step() const { return MODE == kNext ? 4 : gap; }
+  __device__ int step() const { return NEXT ? 4 : gap; }
   // index of the lane's pair i; pairs below `half` turn
   __device__ int pair(int i) const { return MODE == kAny ? l + LPH * i : 4 * l + i; }
   __device__ void columns(int i, int& a, int& b) const {  // kAny
@@ -170,7 +181,7 @@ struct Lanes {
         y[0] = h.a.x, y[1] = h.a.y, y[2] = h.a.z, y[3] = h.a.w, y[4] = h.b.x, y[5] = h.b.y, y[6] = h.b.z, y[7] = h.b.w;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = y[MODE == kNext ? 2 * i : i], v[4 + i] = y[MODE == kNext ? 2 * i + 1 : 4 + i];
+      for (int i = 0; i < 4; ++i) v[i] = y[NEXT ? 2 * i : i], v[4 + i] = y[NEXT ? 2 * i + 1 : 4 + i];
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) r.a[i].x = make_float2(v[2 * i], v[2 * i + 1]), r.b[i].x = make_float2(v[4 + 2 * i], v[5 + 2 * i]);
@@ -190,7 +201,7 @@ struct Lanes {
     } else {
       float y[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[MODE == kNext ? 2 * i : i] = a[i], y[MODE == kNext ? 2 * i + 1 : 4 + i] = b[i];
+      for (int i = 0; i < 4; ++i) y[NEXT ? 2 * i : i] = a[i], y[NEXT ? 2 * i + 1 : 4 + i] = b[i];
       if constexpr (sizeof(T) == 2) {
         *reinterpret_cast<uint2*>(x + a0) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
         *reinterpret_cast<uint2*>(x + a0 + step()) = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
@@ -216,7 +227,7 @@ struct Lanes {
       const float4 x = *reinterpret_cast<const float4*>(w + a0), y = *reinterpret_cast<const float4*>(w + a0 + step());
       const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = v[MODE == kNext ? 2 * i : i], b[i] = v[MODE == kNext ? 2 * i + 1 : 4 + i];
+      for (int i = 0; i < 4; ++i) a[i] = v[NEXT ? 2 * i : i], b[i] = v[NEXT ? 2 * i + 1 : 4 + i];
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) r.a[i].x = make_float2(a[2 * i], a[2 * i + 1]), r.b[i].x = make_float2(b[2 * i], b[2 * i + 1]);
@@ -229,7 +240,7 @@ struct Lanes {
       if (MODE == kAny)
         columns(i, a, b);
       else
-        a = MODE == kNext ? a0 + 2 * i : a0 + i, b = MODE == kNext ? a + 1 : a + gap;
+        a = NEXT ? a0 + 2 * i : a0 + i, b = NEXT ? a + 1 : a + gap;
       if (on && pair(i) < D / 2) sum[a] = r.a[i / 2].get(i % 2), sum[b] = r.b[i / 2].get(i % 2);
     }
   }
@@ -258,12 +269,29 @@ __device__ __forceinline__ Turn turn_of(const L& w, const unsigned long long* fr
   }
   return t;
 }
-__device__ __forceinline__ void rotate(Pairs& x, const Num<2> (&c)[2], const Num<2> (&s)[2], const Num<2> (&n)[2]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
+// Pairs that do not turn keep their values: zero times the other one would be NaN where that is not finite.  (The lane's
+// predicate costs nothing measurable, 1024 x 16 tokens of 12 x 64 19.6 us; a test of each pair where kNext needs none 20.5.)
+template <int LPH, int MODE>
+__device__ __forceinline__ void rotate(const Lanes<LPH, MODE>& w, Pairs& x, const Num<2> (&c)[2], const Num<2> (&s)[2],
+                                       const Num<2> (&n)[2]) {
+  auto two = [&](int i) {
     const Num<2> a = x.a[i], b = x.b[i];
     x.a[i] = fma(b, n[i], a * c[i]);
     x.b[i] = fma(a, s[i], b * c[i]);
+  };
+  if (MODE == kHalf || MODE == kNext || !w.mixed) {
+    if (w.live > 0) {
+      two(0);
+      two(1);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (w.live > 2 * i) {
+        const float a = x.a[i].get(1), b = x.b[i].get(1);
+        two(i);
+        if (w.live == 2 * i + 1) x.a[i].set(1, a), x.b[i].set(1, b);
+      }
   }
 }
 __device__ __forceinline__ float dot(const Pairs& x, const Pairs& y) {
@@ -358,7 +386,7 @@ __global__ void __launch_bounds__(256, 3) rotary_kernel(const RotaryParams p) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) y.a[j] = y.a[j] * (r * wt.a[j]), y.b[j] = y.b[j] * (r * wt.b[j]);
         }
-        rotate(y, tn.c, tn.s, tn.n);
+        rotate(w, y, tn.c, tn.s, tn.n);
         if (w.on && h < n) w.store(o + (long long)h * p.D, y);
       }
     };
@@ -408,7 +436,7 @@ __global__ void __launch_bounds__(256, 2) rotary_bwd_kernel(const RotaryParams p
         if (h0 + i * HPW >= n) break;
         const int h = h0 + i * HPW + w.sub;
         Pairs g = w.get(rd[i]);
-        rotate(g, tn.c, tn.n, tn.s);  // back
+        rotate(w, g, tn.c, tn.n, tn.s);  // back
         if (p.qw) {
           const Pairs v = w.get(rx[i]);
           Pairs gw;
@@ -526,7 +554,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) rotary_ring_kerne
     const Num<2> r(norm ? rsqrtf(fmaf(head_sum<LPH>(dot(y, y)), inv, p.eps)) : 1.f);
 #pragma unroll
     for (int j = 0; j < 2; ++j) y.a[j] = y.a[j] * (r * wt.a[j]), y.b[j] = y.b[j] * (r * wt.b[j]);
-    rotate(y, tn.c, tn.s, tn.n);
+    rotate(w, y, tn.c, tn.s, tn.n);
     if (on) w.store(o, y);
   };
   auto heads = [&](const T* x, T* o, int n, const Pairs& wt) {
@@ -650,7 +678,7 @@ __global__ void __launch_bounds__(32 * Groups<T, LPH>::W, 1) rotary_ring_bwd_ker
     const Num<2> r(r1);
     w.load(rd, d);
     Pairs g = w.get(rd), gw;
-    rotate(g, tn.c, tn.n, tn.s);  // back
+    rotate(w, g, tn.c, tn.n, tn.s);  // back
 #pragma unroll
     for (int j = 0; j < 2; ++j) gw.a[j] = g.a[j] * wt.a[j], gw.b[j] = g.b[j] * wt.b[j];
     const float along = head_sum<LPH>(dot(gw, y));
@@ -726,6 +754,15 @@ __global__ void __launch_bounds__(32) rotary_any_kernel(const RotaryParams p) {
     else
       a = p.rot + i - half, b = a + rest;
   };
+  auto turned = [&](int i, long long pos, float way, float& a, float& b) {  // pair i; way: -1 turns back
+    if (i >= half) return;
+    float c, s;
+    turn(turns(p.freqs[i]), pos, c, s);
+    s *= way;
+    const float a0 = a;
+    a = fmaf(a0, c, -b * s);
+    b = fmaf(b, c, a0 * s);
+  };
   const long long items = (long long)p.T * p.B * H;
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
     const unsigned tb = (unsigned)(it / H), t = tb / p.B, b = tb % p.B;
@@ -745,9 +782,9 @@ __global__ void __launch_bounds__(32) rotary_any_kernel(const RotaryParams p) {
       const float xa = get1(x + ia), xb = get1(x + ib);
       sum = fmaf(xa, xa, fmaf(xb, xb, sum));
       if (BWD) {
-        float c = 1.f, s = 0.f, ga = get1(g + ia), gb = get1(g + ib);
-        if (i < half) turn(turns(p.freqs[i]), pos, c, s);
-        along = fmaf(fmaf(ga, c, gb * s) * w[ia], xa, fmaf(fmaf(gb, c, -ga * s) * w[ib], xb, along));
+        float ga = get1(g + ia), gb = get1(g + ib);
+        turned(i, pos, -1.f, ga, gb);
+        along = fmaf(ga * w[ia], xa, fmaf(gb * w[ib], xb, along));
       }
     }
     const float r = w ? rsqrtf(head_sum<32>(sum) / p.D + p.eps) : 1.f;
@@ -756,10 +793,9 @@ __global__ void __launch_bounds__(32) rotary_any_kernel(const RotaryParams p) {
       int ia, ib;
       columns(i, ia, ib);
       const float wa = w ? w[ia] : 1.f, wb = w ? w[ib] : 1.f;
-      float c = 1.f, s = 0.f;
-      if (i < half) turn(turns(p.freqs[i]), pos, c, s);
       if (BWD) {
-        const float ya = get1(g + ia), yb = get1(g + ib), ga = fmaf(ya, c, yb * s), gb = fmaf(yb, c, -ya * s);
+        float ga = get1(g + ia), gb = get1(g + ib);
+        turned(i, pos, -1.f, ga, gb);
         if (w) {
           const float xa = get1(x + ia), xb = get1(x + ib);
           float* to = acc + (isq ? 0 : p.D);
@@ -772,9 +808,10 @@ __global__ void __launch_bounds__(32) rotary_any_kernel(const RotaryParams p) {
           put1(o + ib, gb);
         }
       } else {
-        const float ya = get1(x + ia) * (r * wa), yb = get1(x + ib) * (r * wb);
-        put1(o + ia, fmaf(ya, c, -yb * s));
-        put1(o + ib, fmaf(yb, c, ya * s));
+        float ya = get1(x + ia) * (r * wa), yb = get1(x + ib) * (r * wb);
+        turned(i, pos, 1.f, ya, yb);
+        put1(o + ia, ya);
+        put1(o + ib, yb);
       }
     }
   }
@@ -889,9 +926,13 @@ int launch_ring(RotaryParams& p, bool bwd, cudaStream_t s) {
 template <class T, int LPH>
 int launch_mode(RotaryParams& p, bool bwd, cudaStream_t s) {
   if (ring_form<T, LPH>(p, bwd))
-    return p.interleaved ? launch_ring<T, LPH, kNext>(p, bwd, s) : launch_ring<T, LPH, kHalf>(p, bwd, s);
+    return !p.interleaved ? launch_ring<T, LPH, kHalf>(p, bwd, s)
+           : p.rot % 8 == 0 ? launch_ring<T, LPH, kNext>(p, bwd, s)
+                            : launch_ring<T, LPH, kSome>(p, bwd, s);
   if (!vector_form<T>(p, bwd)) return launch_lanes<T, LPH, kAny>(p, bwd, s);
-  return p.interleaved ? launch_lanes<T, LPH, kNext>(p, bwd, s) : launch_lanes<T, LPH, kHalf>(p, bwd, s);
+  return !p.interleaved ? launch_lanes<T, LPH, kHalf>(p, bwd, s)
+         : p.rot % 8 == 0 ? launch_lanes<T, LPH, kNext>(p, bwd, s)
+                          : launch_lanes<T, LPH, kSome>(p, bwd, s);
 }
 template <class T>
 int launch_t(RotaryParams& p, bool bwd, cudaStream_t s) {

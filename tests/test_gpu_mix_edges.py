@@ -31,3 +31,54 @@ def test_without_norm_the_gradient_does_not_look_at_x(S, D, T):
     bad[::2] = INF
     a, b = (S.head_norm_rotary_backward(x, x, None, None, f, None, d, d) for x in (q, bad))
     assert torch.equal(a["dq"], b["dq"]) and torch.equal(a["dk"], b["dk"]) and torch.isfinite(b["dq"]).all()
+
+
+# batches of heads (pieces of four, pairs of which some of a lane's turn, value by value), the rings, heads above 256
+PART = [(9, 2, 3, 64, 16, False), (9, 2, 3, 64, 12, True), (9, 2, 3, 64, 20, False), (9, 2, 3, 34, 20, True), (4, 2, 7, 256, 128, False),
+        (700, 2, 3, 64, 16, False), (700, 2, 3, 64, 12, True), (700, 2, 2, 128, 0, False), (9, 1, 2, 128, 0, True),
+        (40, 2, 3, 264, 64, False), (40, 2, 3, 264, 64, True)]
+
+
+def spoilt(x, rot, value):
+    """x with `value` in one column from rot on of every other head, another one in each; and where."""
+    D = x.shape[-1]
+    bad, at = x.clone(), torch.zeros(x.shape, dtype=torch.bool, device="cuda")
+    rows = torch.arange(0, x.numel() // D, 2, device="cuda")
+    cols = rot + (rows // 2) % (D - rot)
+    bad.view(-1, D)[rows, cols] = value
+    at.view(-1, D)[rows, cols] = True
+    return bad, at
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [INF, -INF, NAN])
+@pytest.mark.parametrize("T,B,H,D,rot,inter", PART)
+def test_columns_that_do_not_turn_stay_apart(S, T, B, H, D, rot, inter, value, dtype):
+    """What is not finite in a column past the rotation reaches no other column, without a norm; of the weights' gradients only
+    its own."""
+    x, f = rand(1, T, B, H, D, dtype=dtype), S.rotary_frequencies(rot)
+    bad, at = spoilt(x, rot, value)
+    for call in (lambda v: S.head_norm_rotary(v, v, None, None, f, interleaved=inter),
+                 lambda v: tuple(S.head_norm_rotary_backward(x, x, None, None, f, None, v, v, interleaved=inter).values())):
+        a, b = call(x), call(bad)
+        for y, z in zip(a, b):
+            assert torch.equal(y[~at], z[~at])
+            assert torch.isnan(z[at]).all() if value != value else (z[at] == value).all()
+    w = 1 + rand(3, D, scale=0.2)
+    one = torch.zeros_like(at)
+    one.view(-1, D)[0] = at.view(-1, D)[0]
+    d = torch.where(one, bad, x)
+    a, b = (S.head_norm_rotary_backward(x, x, w, w, f, None, v, v, interleaved=inter) for v in (x, d))
+    for n in ("dwq", "dwk"):
+        keep = torch.arange(D, device="cuda") != rot
+        assert torch.equal(a[n][keep], b[n][keep]) and not torch.isfinite(b[n][rot])
+
+
+@pytest.mark.parametrize("T,B,H,D,rot,inter", PART)
+def test_an_infinity_leaves_zeros_in_columns_that_do_not_turn(S, T, B, H, D, rot, inter):
+    """1 / sqrt(mean x^2) of its head is zero, and so is every finite value's product with it."""
+    x, w = rand(1, T, B, H, D), torch.ones(D, device="cuda")
+    bad, at = spoilt(x, rot, INF)
+    y = S.head_norm_rotary(bad, bad, w, w, S.rotary_frequencies(rot), interleaved=inter)[0]
+    hit = at.any(-1, keepdim=True).expand_as(at).clone()
+    assert torch.isnan(y[at]).all() and (y[hit & ~at] == 0).all()
