@@ -420,6 +420,12 @@ int rnn_gated_bwd(const rnn_gated_desc_t* desc, const void* Wx, const int32_t* l
                   const float* dstateT, void* dWx, float* dstate0, void* workspace, size_t workspace_bytes,
                   void* stream);
 
+/* Launch geometry that rnn_gated_fwd (gradient != 0: rnn_gated_bwd) would use for tensors at aligned addresses:
+ * out[0..6] = grid CTAs, threads per CTA, cluster size, channels of a tile, whether maps are made a round ahead, dynamic
+ * smem bytes, clusters (cluster size 1: CTAs) that the device holds at once; the last four are 0 for the kernels without
+ * tiles, all where nothing is launched. */
+int rnn_gated_config(const rnn_gated_desc_t* desc, int32_t gradient, int32_t* out7);
+
 /* One token (desc->T == 1, Wx [B, NH, G*D]) for each of B rows out of a cache of n_slots states [n_slots, NH, D] fp32,
  * updated in place: row b uses state slots[b] (slots NULL: state b).  A row whose slot is not in [0, n_slots) has no
  * state: its y is zero.  Two rows must not name the same slot.  No workspace, no device status. */

@@ -36,7 +36,7 @@ EXPORTS = ("rnn_workspace_size", "rnn_stash_size", "rnn_fwd", "rnn_bwd", "rnn_re
            "rnn_rms_norm_bwd_workspace_size", "rnn_rms_norm_bwd", "rnn_quantize_weight",
            "rnn_input_proj_fp8", "rnn_linattn_workspace_size", "rnn_linattn_fwd",
            "rnn_linattn_bwd", "rnn_linattn_step", "rnn_gated_stash_size", "rnn_gated_fwd",
-           "rnn_gated_bwd", "rnn_gated_step", "rnn_head_norm_rotary",
+           "rnn_gated_bwd", "rnn_gated_config", "rnn_gated_step", "rnn_head_norm_rotary",
            "rnn_head_norm_rotary_bwd_workspace_size", "rnn_head_norm_rotary_bwd",
            "rnn_clip_grad_norm_workspace_size", "rnn_clip_grad_norm")
 
@@ -109,6 +109,7 @@ _SIGS = {
     "rnn_gated_stash_size": (_SZ, [_GDESC]),
     "rnn_gated_fwd": (_I, [_GDESC] + [_P] * 7 + [_SZ, _P]),
     "rnn_gated_bwd": (_I, [_GDESC] + [_P] * 8 + [_SZ, _P]),
+    "rnn_gated_config": (_I, [_GDESC, _I32, ctypes.POINTER(_I32)]),
     "rnn_gated_step": (_I, [_GDESC] + [_P] * 2 + [_I32] + [_P] * 3),
     "rnn_head_norm_rotary": (_I, [_RDESC, _RST] + [_P] * 9),
     "rnn_head_norm_rotary_bwd_workspace_size": (_SZ, [_RDESC]),

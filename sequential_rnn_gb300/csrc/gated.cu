@@ -380,29 +380,33 @@ int launch_cluster(void (*kern)(A...), unsigned grid, int cs, cudaStream_t s, A.
 }
 
 template <class T, int G, int V>
-int launch_gv(GatedParams& p, bool bwd, cudaStream_t s) {
+int launch_gv(GatedParams& p, bool bwd, cudaStream_t s, GatedInfo* info) {
   p.tiles = (p.N + 32 * V - 1) / (32 * V);
   // CTAs along time until each SM has two (4000 tokens of 2 x 33, fz: 43.5 us by one CTA, 22.6 by four, 12.7 by eight)
   const long long tiles = (long long)p.tiles * p.B, want = 2LL * sm_count();
   p.cs = 1;
   while (p.cs < 8 && tiles * p.cs < want && p.cs * kChunk < p.T) p.cs *= 2;
   if (tiles * p.cs > 0x7fffffff) return (int)cudaErrorInvalidConfiguration;
+  if (info) {
+    *info = GatedInfo{(int)(tiles * p.cs), 32 * kWarps, p.cs, 0, 0, 0, 0};
+    return 0;
+  }
   return launch_cluster(bwd ? gated_bwd_kernel<T, G, V> : gated_fwd_kernel<T, G, V>, (unsigned)(tiles * p.cs), p.cs, s,
                         (const GatedParams)p);
 }
 template <class T, int G>
-int launch_g(GatedParams& p, bool bwd, bool pairs, cudaStream_t s) {
-  return pairs ? launch_gv<T, G, 2>(p, bwd, s) : launch_gv<T, G, 1>(p, bwd, s);
+int launch_g(GatedParams& p, bool bwd, bool pairs, cudaStream_t s, GatedInfo* info) {
+  return pairs ? launch_gv<T, G, 2>(p, bwd, s, info) : launch_gv<T, G, 1>(p, bwd, s, info);
 }
 template <class T>
-int launch_t(GatedParams& p, int gates, bool bwd, cudaStream_t s) {
+int launch_t(GatedParams& p, int gates, bool bwd, cudaStream_t s, GatedInfo* info) {
   auto ok = [](const void* x, size_t n) { return reinterpret_cast<uintptr_t>(x) % n == 0; };
   const bool pairs = p.D % 2 == 0 && ok(p.wx, 2 * sizeof(T)) && ok(p.y, 2 * sizeof(T)) && ok(p.dy, 2 * sizeof(T)) &&
                      ok(p.dwx, 2 * sizeof(T));
   switch (gates) {
-    case 2: return launch_g<T, 2>(p, bwd, pairs, s);
-    case 3: return launch_g<T, 3>(p, bwd, pairs, s);
-    default: return launch_g<T, 4>(p, bwd, pairs, s);
+    case 2: return launch_g<T, 2>(p, bwd, pairs, s, info);
+    case 3: return launch_g<T, 3>(p, bwd, pairs, s, info);
+    default: return launch_g<T, 4>(p, bwd, pairs, s, info);
   }
 }
 
@@ -424,12 +428,12 @@ int step_t(const GatedStepParams& p, int gates, cudaStream_t s) {
 
 }  // namespace
 
-int launch_gated(GatedParams p, int gates, bool bf16, bool bwd, cudaStream_t s) {
+int launch_gated(GatedParams p, int gates, bool bf16, bool bwd, cudaStream_t s, GatedInfo* info) {
   if (gated_takes_tiles(p, bf16)) {
-    const int e = launch_gated_tile(p, gates, bf16, bwd, s);
+    const int e = launch_gated_tile(p, gates, bf16, bwd, s, info);
     if (e != kGatedNoTile) return e;
   }
-  return bf16 ? launch_t<__nv_bfloat16>(p, gates, bwd, s) : launch_t<float>(p, gates, bwd, s);
+  return bf16 ? launch_t<__nv_bfloat16>(p, gates, bwd, s, info) : launch_t<float>(p, gates, bwd, s, info);
 }
 int launch_gated_step(const GatedStepParams& p, int gates, bool bf16, cudaStream_t s) {
   return bf16 ? step_t<__nv_bfloat16>(p, gates, s) : step_t<float>(p, gates, s);

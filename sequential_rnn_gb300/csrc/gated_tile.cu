@@ -524,50 +524,73 @@ struct Variant {
     const int e = prepare_launch(prep, kernel, C::smem(kGatedCluster), C::THREADS, kGatedCluster);
     return e == -1 ? prepare_launch(prep, kernel, C::smem(kGatedCluster), C::THREADS, 1) : e;
   }
-  // clusters of cs CTAs that the device holds at once (0: none, or not to be had)
-  static int active(int cs, int dev) {
-    static int known[64][kGatedCluster + 1];  // one more than it, once asked for
+  // Shared memory of a launch of which `each` CTAs come to an SM: so much that no more of them fit one (a cluster's would pack two
+  // or three to it); 0: what they need.
+  static uint32_t smem_for(int cs, int each) {
+    const uint32_t need = C::smem(cs), spread = each > 0 ? 226 * 1024 / (each + 1) + 1024 : 0;
+    return spread > need ? spread : need;
+  }
+  // clusters of cs CTAs with smem_for(cs, each) that the device holds at once (0: none, or not to be had)
+  static int active(int cs, int each, int dev) {
+    static int known[64][kGatedCluster + 1][C::CTAS];  // one more than it, once asked for
     if (dev >= 64) return 0;
-    if (known[dev][cs] == 0) {
+    int& k = known[dev][cs][each];
+    if (k == 0) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(cs);
       cfg.blockDim = dim3(C::THREADS);
-      cfg.dynamicSmemBytes = C::smem(cs);
+      cfg.dynamicSmemBytes = smem_for(cs, each);
       cudaLaunchAttribute attr[2];
       attributes(attr, cs);
       cfg.attrs = attr + 1;
       cfg.numAttrs = 1;
       int n = 0;
       if (prepare() != 0 || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
-      known[dev][cs] = n + 1;
+      k = n + 1;
     }
-    return known[dev][cs] - 1;
+    return k - 1;
   }
-  static int launch(GatedParams p, int cs, cudaStream_t s) {
+  // Few CTAs are spread evenly over the SMs (one row of 16384 tokens of 2 x 64, ifzo: gradient 25.1 us against 32.5), unless the
+  // clusters then do not all fit at once, which keep to the SMs of one group (12 of 12 CTAs, 16384 tokens of 12 x 32, fz: 25.4 us one
+  // to an SM, of which 8 fit, 17.6 packed).
+  static int each_of(int cs, long long clusters, int dev) {
+    const long long each = (clusters * cs + sm_count() - 1) / sm_count();
+    if (each >= C::CTAS) return 0;
+    return cs == 1 || active(cs, (int)each, dev) >= clusters ? (int)each : 0;
+  }
+  static int launch(GatedParams p, int cs, cudaStream_t s, GatedInfo* info) {
     const bool bf16 = sizeof(T) == 2;
     const long long NH = p.N / p.D;
     TileMaps m;
-    bool ok = encode(&m.wx, p.wx, bf16, p.D, NH * G, p.B, p.T, X, G, C::TOKENS);
-    if (BWD)
-      ok = ok && encode(&m.out, p.dwx, bf16, p.D, NH * G, p.B, p.T, X, G, kS) &&
-           encode(&m.dy, p.dy, bf16, p.D, NH, p.B, p.T, X, 1, C::TOKENS) &&
-           encode(&m.stash, p.stash, false, p.D, NH, p.B, (p.T + kS - 1) / kS, X, 1, C::RUNS);
-    else
-      ok = ok && encode(&m.out, p.y, bf16, p.D, NH, p.B, p.T, X, 1, kS) && reinterpret_cast<uintptr_t>(p.stash) % 8 == 0;
-    if (!ok) return kGatedNoTile;
+    if (!info) {
+      bool ok = encode(&m.wx, p.wx, bf16, p.D, NH * G, p.B, p.T, X, G, C::TOKENS);
+      if (BWD)
+        ok = ok && encode(&m.out, p.dwx, bf16, p.D, NH * G, p.B, p.T, X, G, kS) &&
+             encode(&m.dy, p.dy, bf16, p.D, NH, p.B, p.T, X, 1, C::TOKENS) &&
+             encode(&m.stash, p.stash, false, p.D, NH, p.B, (p.T + kS - 1) / kS, X, 1, C::RUNS);
+      else
+        ok = ok && encode(&m.out, p.y, bf16, p.D, NH, p.B, p.T, X, 1, kS) && reinterpret_cast<uintptr_t>(p.stash) % 8 == 0;
+      if (!ok) return kGatedNoTile;
+    }
     p.tiles = (int)(NH * ((p.D + X - 1) / X));
     p.cs = cs;
-    const long long ctas = (long long)p.tiles * p.B * cs;
+    const long long clusters = (long long)p.tiles * p.B, ctas = clusters * cs;
     if (ctas > 0x7fffffff) return (int)cudaErrorInvalidConfiguration;
     const int e = prepare();
     if (e != 0) return e;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const int each = each_of(cs, clusters, dev);
+    const uint32_t smem = smem_for(cs, each);
+    if (info) {
+      const int held = cs > 1 ? active(cs, each, dev) : (each ? each : C::CTAS) * sm_count();
+      *info = GatedInfo{(int)ctas, C::THREADS, cs, X, AHEAD, (int)smem, held};
+      return 0;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(C::THREADS);
-    // few CTAs: shared memory asked for so that the SMs share them out evenly (a cluster's would pack three to an SM)
-    const uint32_t each = (uint32_t)((ctas + sm_count() - 1) / sm_count());
-    const uint32_t spread = each < (uint32_t)C::CTAS ? 226 * 1024 / (each + 1) + 1024 : 0;
-    cfg.dynamicSmemBytes = spread > C::smem(cs) ? spread : C::smem(cs);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attributes(attr, cs);
@@ -591,7 +614,7 @@ struct Plan {
     const long long tiles = (long long)(p.N / p.D) * ((p.D + 2 * C::PL - 1) / (2 * C::PL)) * p.B;
     const int chunks = (p.T + C::TOKENS - 1) / C::TOKENS;
     for (int c = 1; c <= kGatedCluster && c <= chunks; ++c) {
-      const long long room = c == 1 ? (long long)C::CTAS * sms : V::active(c, dev);
+      const long long room = c == 1 ? (long long)C::CTAS * sms : V::active(c, 0, dev);
       if (room < 1) continue;
       auto wave = [&](long long clusters) {
         if (clusters == 0) return 0.0;
@@ -605,7 +628,7 @@ struct Plan {
   }
 };
 template <class T, int G, bool BWD>
-int launch_planned(const GatedParams& p, cudaStream_t s) {
+int launch_planned(const GatedParams& p, cudaStream_t s, GatedInfo* info) {
   Plan plan;
   plan.consider<Variant<T, G, BWD, 64, false>>(0, p, false);
   plan.consider<Variant<T, G, BWD, 32, false>>(1, p, false);
@@ -615,22 +638,22 @@ int launch_planned(const GatedParams& p, cudaStream_t s) {
     plan.consider<Variant<T, G, BWD, 32, true>>(3, p, true);
   }
   switch (plan.variant) {
-    case 0: return Variant<T, G, BWD, 64, false>::launch(p, plan.cs, s);
-    case 1: return Variant<T, G, BWD, 32, false>::launch(p, plan.cs, s);
-    case 2: return Variant<T, G, BWD, 64, AHEAD>::launch(p, plan.cs, s);
-    default: return Variant<T, G, BWD, 32, AHEAD>::launch(p, plan.cs, s);
+    case 0: return Variant<T, G, BWD, 64, false>::launch(p, plan.cs, s, info);
+    case 1: return Variant<T, G, BWD, 32, false>::launch(p, plan.cs, s, info);
+    case 2: return Variant<T, G, BWD, 64, AHEAD>::launch(p, plan.cs, s, info);
+    default: return Variant<T, G, BWD, 32, AHEAD>::launch(p, plan.cs, s, info);
   }
 }
 template <class T, int G>
-int launch_dir(const GatedParams& p, bool bwd, cudaStream_t s) {
-  return bwd ? launch_planned<T, G, true>(p, s) : launch_planned<T, G, false>(p, s);
+int launch_dir(const GatedParams& p, bool bwd, cudaStream_t s, GatedInfo* info) {
+  return bwd ? launch_planned<T, G, true>(p, s, info) : launch_planned<T, G, false>(p, s, info);
 }
 template <class T>
-int launch_t(const GatedParams& p, int gates, bool bwd, cudaStream_t s) {
+int launch_t(const GatedParams& p, int gates, bool bwd, cudaStream_t s, GatedInfo* info) {
   switch (gates) {
-    case 2: return launch_dir<T, 2>(p, bwd, s);
-    case 3: return launch_dir<T, 3>(p, bwd, s);
-    default: return launch_dir<T, 4>(p, bwd, s);
+    case 2: return launch_dir<T, 2>(p, bwd, s, info);
+    case 3: return launch_dir<T, 3>(p, bwd, s, info);
+    default: return launch_dir<T, 4>(p, bwd, s, info);
   }
 }
 
@@ -640,8 +663,8 @@ int launch_t(const GatedParams& p, int gates, bool bwd, cudaStream_t s) {
 // 3.6 against 7.0)
 bool gated_takes_tiles(const GatedParams& p, bool bf16) { return p.D % (bf16 ? 8 : 4) == 0 && p.T >= kGatedTileTokens; }
 
-int launch_gated_tile(const GatedParams& p, int gates, bool bf16, bool bwd, cudaStream_t s) {
-  return bf16 ? launch_t<__nv_bfloat16>(p, gates, bwd, s) : launch_t<float>(p, gates, bwd, s);
+int launch_gated_tile(const GatedParams& p, int gates, bool bf16, bool bwd, cudaStream_t s, GatedInfo* info) {
+  return bf16 ? launch_t<__nv_bfloat16>(p, gates, bwd, s, info) : launch_t<float>(p, gates, bwd, s, info);
 }
 
 }  // namespace srnn

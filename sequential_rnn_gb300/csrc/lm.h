@@ -164,12 +164,20 @@ struct GatedParams {
   int withhold;         // test: no tile is brought (tile kernels)
   unsigned long long timeout_ns;
 };
-int launch_gated(GatedParams p, int gates, bool bf16, bool bwd, cudaStream_t s);
+struct GatedInfo {  // of a launch
+  int grid, threads, cluster;
+  int tile;  // channels of a tile that TMA brings; 0: the kernels without
+  int ahead; // maps are made a round ahead
+  int smem;
+  int held;   // clusters (cluster 1: CTAs) of it that the device holds at once
+};
+// info: filled in the place of a launch (addresses are taken as aligned); a cudaError_t value
+int launch_gated(GatedParams p, int gates, bool bf16, bool bwd, cudaStream_t s, GatedInfo* info = nullptr);
 // the kernels on tiles: whether the sizes suit them; kGatedNoTile: addresses or strides have no tensor map
 constexpr int kGatedTileTokens = 65;
 constexpr int kGatedNoTile = -2;
 bool gated_takes_tiles(const GatedParams& p, bool bf16);
-int launch_gated_tile(const GatedParams& p, int gates, bool bf16, bool bwd, cudaStream_t s);
+int launch_gated_tile(const GatedParams& p, int gates, bool bf16, bool bwd, cudaStream_t s, GatedInfo* info);
 struct GatedStepParams {
   const void* wx;    // [B, NH, gates D]
   const int* slots;  // [B] or null

@@ -134,6 +134,21 @@ int rnn_gated_bwd(const rnn_gated_desc_t* d, const void* Wx, const int32_t* lens
   return map_launch_error(launch_gated(p, d->gates, d->dtype == RNN_BF16, true, s));
 }
 
+int rnn_gated_config(const rnn_gated_desc_t* d, int32_t gradient, int32_t* out7) {
+  const int e = check_gated(d);
+  if (e != RNN_OK) return e;
+  if (out7 == nullptr) return RNN_ERR_INVALID_ARG;
+  for (int i = 0; i < 7; ++i) out7[i] = 0;
+  if (d->B == 0 || d->NH == 0) return RNN_OK;
+  GatedInfo info{};
+  const GatedParams p = gated_params(d, nullptr, nullptr, nullptr);
+  const int err = launch_gated(p, d->gates, d->dtype == RNN_BF16, gradient != 0, nullptr, &info);
+  if (err != 0) return map_launch_error(err);
+  const int32_t out[7] = {info.grid, info.threads, info.cluster, info.tile, info.ahead, info.smem, info.held};
+  std::copy(out, out + 7, out7);
+  return RNN_OK;
+}
+
 int rnn_gated_step(const rnn_gated_desc_t* d, const void* Wx, const int32_t* slots, int32_t n_slots, float* state,
                    void* y, void* stream) {
   const int e = check_gated(d);

@@ -37,7 +37,7 @@ __all__ = ["rnn_rms_norm", "rnn_rms_norm_bwd_workspace_size", "rnn_rms_norm_bwd"
            "rnn_linattn_fwd", "rnn_linattn_bwd", "rnn_linattn_step", "rms_norm",
            "rms_norm_backward", "quantize_weight", "input_proj_fp8", "linear_attention",
            "linear_attention_backward", "linear_attention_step",
-           "rnn_gated_stash_size", "rnn_gated_fwd", "rnn_gated_bwd", "rnn_gated_step",
+           "rnn_gated_stash_size", "rnn_gated_fwd", "rnn_gated_bwd", "rnn_gated_config", "rnn_gated_step",
            "rnn_head_norm_rotary", "rnn_head_norm_rotary_bwd_workspace_size", "rnn_head_norm_rotary_bwd",
            "rnn_clip_grad_norm_workspace_size", "rnn_clip_grad_norm", "gated_recurrence",
            "gated_recurrence_backward", "gated_recurrence_step", "rotary_frequencies", "head_norm_rotary",
@@ -168,6 +168,14 @@ def rnn_gated_bwd(desc, Wx, lens, stash, dy, dstateT, dWx, dstate0, workspace, s
     return _lib.load().rnn_gated_bwd(ctypes.byref(desc), _at(Wx), _at(lens), _at(stash), _at(dy),
                                      _at(dstateT), _at(dWx), _at(dstate0), _at(workspace),
                                      workspace.nbytes if workspace is not None else 0, _handle(stream))
+
+
+def rnn_gated_config(desc, gradient=False):
+    out = (ctypes.c_int32 * 7)()
+    st = _lib.load().rnn_gated_config(ctypes.byref(desc), int(gradient), out)
+    if st:
+        _raise(st, "rnn_gated_config")
+    return dict(zip(("grid", "threads", "cluster", "tile", "ahead", "smem", "held"), out))
 
 
 def rnn_gated_step(desc, Wx, slots, n_slots, state, y, stream=None) -> int:

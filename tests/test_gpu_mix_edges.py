@@ -82,3 +82,42 @@ def test_an_infinity_leaves_zeros_in_columns_that_do_not_turn(S, T, B, H, D, rot
     y = S.head_norm_rotary(bad, bad, w, w, S.rotary_frequencies(rot), interleaved=inter)[0]
     hit = at.any(-1, keepdim=True).expand_as(at).clone()
     assert torch.isnan(y[at]).all() and (y[hit & ~at] == 0).all()
+
+
+# ------------------------------------------------------- gated recurrence --
+def config(S, T, B, NH, D, gates, dtype, gradient=False):
+    from sequential_rnn_gb300._lib import GATE_COUNTS, rnn_gated_desc_t
+    return S.rnn_gated_config(rnn_gated_desc_t(int(dtype == "bf16"), T, B, NH, D, GATE_COUNTS[gates], 0), gradient)
+
+
+@pytest.mark.parametrize("gradient", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,B,NH,D,gates", [
+    (16384, 1, 12, 32, "fz"), (16384, 1, 3, 128, "fz"), (16384, 1, 12, 64, "fz"), (16384, 1, 8, 64, "fzo"), (8000, 2, 6, 64, "fz"),
+    (8192, 1, 10, 64, "fzo"), (4000, 4, 4, 64, "fz"), (1000, 5, 3, 64, "fz"), (500, 8, 2, 64, "fz"), (16384, 1, 3, 32, "ifzo")])
+def test_planned_clusters_are_there_at_once(S, T, B, NH, D, gates, dtype, gradient):
+    """The plan counts on it at these sizes: no cluster waits for another one to leave, whatever shared memory spreads them."""
+    c = config(S, T, B, NH, D, gates, dtype, gradient)
+    assert c["tile"] and c["grid"] % c["cluster"] == 0 and c["held"] >= c["grid"] // c["cluster"], c
+
+
+# (channels of a tile, maps a round ahead, CTAs of a cluster: 1, up to 8, more)
+@pytest.mark.parametrize("dtype,gradient,T,B,NH,D,kernel", [
+    ("bf16", False, 65, 40, 5, 40, (32, 0, 1)), ("bf16", False, 1000, 40, 1, 8, (32, 0, 8)), ("bf16", False, 1500, 30, 1, 8, (32, 0, 16)),
+    ("bf16", False, 65, 8, 12, 32, (32, 1, 1)), ("bf16", False, 200, 40, 1, 8, (32, 1, 8)), ("bf16", False, 1500, 1, 1, 8, (32, 1, 16)),
+    ("bf16", False, 129, 40, 4, 72, (64, 0, 1)), ("bf16", False, 129, 16, 4, 72, (64, 0, 8)), ("bf16", False, 600, 16, 2, 40, (64, 0, 16)),
+    ("bf16", False, 129, 30, 5, 40, (64, 1, 1)), ("bf16", False, 65, 1, 1, 8, (64, 1, 8)), ("bf16", False, 600, 1, 1, 8, (64, 1, 16)),
+    ("bf16", True, 65, 1, 1, 8, (32, 0, 1)), ("bf16", True, 200, 40, 1, 8, (32, 0, 8)), ("bf16", True, 1500, 1, 1, 8, (32, 0, 16)),
+    ("bf16", True, 129, 16, 4, 72, (64, 0, 1)), ("bf16", True, 129, 1, 1, 8, (64, 0, 8)), ("bf16", True, 600, 1, 1, 8, (64, 0, 16)),
+    *[("f32", g, *size) for g in (False, True) for size in
+      ((65, 40, 5, 40, (32, 0, 1)), (100, 40, 1, 8, (32, 0, 8)), (600, 1, 1, 8, (32, 0, 16)), (65, 30, 5, 40, (64, 0, 1)),
+       (65, 1, 1, 8, (64, 0, 8)), (257, 1, 1, 8, (64, 0, 16)))],
+    ("bf16", False, 65, 3, 2, 33, (0, 0, 8)), ("f32", True, 64, 3, 2, 32, (0, 0, 1))])
+def test_every_planned_kernel(S, dtype, gradient, T, B, NH, D, kernel):
+    """Against the oracle, at sizes that take it (of the device that the plan's rounds were measured on)."""
+    from tests.test_gpu_mix_gated import check as check_gated
+    c = config(S, T, B, NH, D, "fz", dtype, gradient)
+    cluster = next(n for n in (1, 8, 16) if c["cluster"] <= n)
+    assert (c["tile"], c["ahead"], cluster) == kernel, c
+    check_gated(S, T, B, NH, D, "fz", dtype, seed=T + D)
+    check_gated(S, T, B, NH, D, "fz", dtype, lens=[T - (b * 37) % (T + 1) for b in range(B)], seed=T)

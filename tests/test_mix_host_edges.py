@@ -1,10 +1,11 @@
 """Code rules and refusals of the gated recurrence and the clipping that need no GPU."""
+import ctypes
 import os
 import re
 
 import pytest
 
-from tests.test_mix_host import A, INF, P, W, clip, lib  # noqa: F401 (lib: the fixture)
+from tests.test_mix_host import A, INF, P, W, clip, gdesc, lib  # noqa: F401 (lib: the fixture)
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sequential_rnn_gb300", "csrc")
 
@@ -35,3 +36,12 @@ def test_clip_counts_that_pass_32_bits(lib):  # noqa: F811
     assert lib.rnn_clip_grad_norm_workspace_size(lot - 1) > 0
     assert lib.rnn_clip_grad_norm_workspace_size(lot) == lib.rnn_clip_grad_norm_workspace_size((1 << 31) - 1) == 0
     assert lib.rnn_clip_grad_norm(lot, P(A), P(A), P(A), 1.0, None, P(W), 1 << 40, None) == 2
+
+
+@pytest.mark.parametrize("kw", [dict(dtype=2), dict(T=-1), dict(D=0), dict(gates=1), dict(gates=5), dict(flags=1)])
+def test_gated_config_refusals(lib, kw):  # noqa: F811
+    out = (ctypes.c_int32 * 7)(*[9] * 7)
+    assert lib.rnn_gated_config(ctypes.byref(gdesc(**kw)), 0, out) == 1 and list(out) == [9] * 7
+    assert lib.rnn_gated_config(None, 0, out) == lib.rnn_gated_config(ctypes.byref(gdesc()), 0, None) == 1
+    for none in (dict(B=0), dict(NH=0)):
+        assert lib.rnn_gated_config(ctypes.byref(gdesc(**none)), 1, out) == 0 and list(out) == [0] * 7
