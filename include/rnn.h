@@ -404,8 +404,8 @@ typedef struct {
   int32_t dtype; /* rnn_dtype_t of Wx, y, dy, dWx */
   int32_t T, B, NH, D;
   int32_t gates; /* rnn_gates_t: the gates' number G */
-  int32_t flags; /* 0, or RNN_FLAG_TEST_TIMEOUT: rnn_gated_fwd and _bwd at sizes that run on tiles, else
-                    RNN_ERR_UNSUPPORTED */
+  int32_t flags; /* 0, or RNN_FLAG_TEST_TIMEOUT: rnn_gated_fwd and _bwd at sizes and addresses that run on tiles,
+                    else RNN_ERR_UNSUPPORTED */
 } rnn_gated_desc_t;
 
 /* Bytes of the stash: the fp32 state before every eighth token, [ceil(T/8), B, NH, D].  0 on an invalid desc. */

@@ -431,7 +431,7 @@ int step_t(const GatedStepParams& p, int gates, cudaStream_t s) {
 int launch_gated(GatedParams p, int gates, bool bf16, bool bwd, cudaStream_t s, GatedInfo* info) {
   if (gated_takes_tiles(p, bf16)) {
     const int e = launch_gated_tile(p, gates, bf16, bwd, s, info);
-    if (e != kGatedNoTile) return e;
+    if (e != kGatedNoTile || p.withhold) return e;
   }
   return bf16 ? launch_t<__nv_bfloat16>(p, gates, bwd, s, info) : launch_t<float>(p, gates, bwd, s, info);
 }

@@ -171,7 +171,8 @@ struct GatedInfo {  // of a launch
   int smem;
   int held;   // clusters (cluster 1: CTAs) of it that the device holds at once
 };
-// info: filled in the place of a launch (addresses are taken as aligned); a cudaError_t value
+// info: filled in the place of a launch (addresses are taken as aligned); a cudaError_t value, or kGatedNoTile where no tile can
+// be withheld
 int launch_gated(GatedParams p, int gates, bool bf16, bool bwd, cudaStream_t s, GatedInfo* info = nullptr);
 // the kernels on tiles: whether the sizes suit them; kGatedNoTile: addresses or strides have no tensor map
 constexpr int kGatedTileTokens = 65;

@@ -31,6 +31,7 @@ int check_gated(const rnn_gated_desc_t* d) {
 size_t stash_bytes(const rnn_gated_desc_t* d) {
   return (size_t)((d->T + kGatedRun - 1) / kGatedRun) * d->B * d->NH * d->D * sizeof(float);
 }
+int gated_status(int e) { return e == kGatedNoTile ? RNN_ERR_UNSUPPORTED : map_launch_error(e); }
 GatedParams gated_params(const rnn_gated_desc_t* d, const void* Wx, const int32_t* lens, void* workspace) {
   GatedParams p{};
   p.status = static_cast<int*>(workspace);
@@ -111,7 +112,7 @@ int rnn_gated_fwd(const rnn_gated_desc_t* d, const void* Wx, const int32_t* lens
   GatedParams p = gated_params(d, Wx, lens, workspace);
   if (d->flags != 0 && !gated_takes_tiles(p, d->dtype == RNN_BF16)) return RNN_ERR_UNSUPPORTED;
   p.state0 = state0, p.y = y, p.stateT = stateT, p.stash = stash;
-  return map_launch_error(launch_gated(p, d->gates, d->dtype == RNN_BF16, false, s));
+  return gated_status(launch_gated(p, d->gates, d->dtype == RNN_BF16, false, s));
 }
 
 int rnn_gated_bwd(const rnn_gated_desc_t* d, const void* Wx, const int32_t* lens, const float* stash, const void* dy,
@@ -131,7 +132,7 @@ int rnn_gated_bwd(const rnn_gated_desc_t* d, const void* Wx, const int32_t* lens
   GatedParams p = gated_params(d, Wx, lens, workspace);
   if (d->flags != 0 && !gated_takes_tiles(p, d->dtype == RNN_BF16)) return RNN_ERR_UNSUPPORTED;
   p.stash = const_cast<float*>(stash), p.dy = dy, p.dstateT = dstateT, p.dwx = dWx, p.dstate0 = dstate0;
-  return map_launch_error(launch_gated(p, d->gates, d->dtype == RNN_BF16, true, s));
+  return gated_status(launch_gated(p, d->gates, d->dtype == RNN_BF16, true, s));
 }
 
 int rnn_gated_config(const rnn_gated_desc_t* d, int32_t gradient, int32_t* out7) {

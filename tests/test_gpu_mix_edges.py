@@ -121,3 +121,16 @@ def test_every_planned_kernel(S, dtype, gradient, T, B, NH, D, kernel):
     assert (c["tile"], c["ahead"], cluster) == kernel, c
     check_gated(S, T, B, NH, D, "fz", dtype, seed=T + D)
     check_gated(S, T, B, NH, D, "fz", dtype, lens=[T - (b * 37) % (T + 1) for b in range(B)], seed=T)
+
+
+def test_the_timeout_flag_is_refused_where_no_tile_is_brought(S):
+    """Addresses that have no tensor map run on kernels that wait for nothing."""
+    from sequential_rnn_gb300._lib import RNN_FLAG_TEST_TIMEOUT, rnn_gated_desc_t
+    T, B, NH, D = 100, 2, 1, 32
+    d = rnn_gated_desc_t(1, T, B, NH, D, 2, RNN_FLAG_TEST_TIMEOUT)
+    Wx = torch.zeros(T * B * NH * 2 * D + 1, dtype=torch.bfloat16, device="cuda")[1:]
+    y = torch.zeros(T * B * NH * D, dtype=torch.bfloat16, device="cuda")
+    stash = torch.zeros(13 * B * NH * D, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    assert S.rnn_gated_fwd(d, Wx, None, None, y, None, None, ws) == 2
+    assert S.rnn_gated_bwd(d, Wx, None, stash, y, None, torch.empty_like(Wx), None, ws) == 2

@@ -5,7 +5,7 @@ import re
 
 import pytest
 
-from tests.test_mix_host import A, INF, P, W, clip, gdesc, lib  # noqa: F401 (lib: the fixture)
+from tests.test_mix_host import A, INF, P, W, clip, gated, gdesc, lib  # noqa: F401 (lib: the fixture)
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sequential_rnn_gb300", "csrc")
 
@@ -45,3 +45,11 @@ def test_gated_config_refusals(lib, kw):  # noqa: F811
     assert lib.rnn_gated_config(None, 0, out) == lib.rnn_gated_config(ctypes.byref(gdesc()), 0, None) == 1
     for none in (dict(B=0), dict(NH=0)):
         assert lib.rnn_gated_config(ctypes.byref(gdesc(**none)), 1, out) == 0 and list(out) == [0] * 7
+
+
+def test_the_timeout_flag_is_refused_where_no_tile_is_brought(lib):  # noqa: F811
+    for call, names in (("fwd", ("Wx", "y")), ("bwd", ("Wx", "dy", "dWx"))):
+        for n in names:
+            assert gated(lib, call, gdesc(T=100, flags=1 << 30), **{n: A + 2}) == 2, (call, n)
+    assert gated(lib, "fwd", gdesc(T=100, flags=1 << 30), stash=A + 4) == 2
+    assert gated(lib, "bwd", gdesc(T=100, flags=1 << 30), stash=A + 4) == 2
