@@ -148,6 +148,11 @@ void put(PyObject* d, const char* key, PyObject* value) {  // (takes over the re
 }
 void put(PyObject* d, const char* key, const Tensor& t) { put(d, key, THPVariable_Wrap(t)); }
 
+// a tensor that a call has written in place: automatic differentiation that saved it notices (an inference tensor has no version)
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject* pair(const Tensor& a, const Tensor& b) {
   PyObject* t = PyTuple_New(2);
   PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(a));
@@ -440,7 +445,9 @@ PyObject* linear_attention_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      at_of<const int32_t>(slots), n_slots, at_of<float>(&state), o.data_ptr(),
                      current_stream());
   }
-  return st ? status(st) : THPVariable_Wrap(o);
+  if (st) return status(st);
+  written(state);
+  return THPVariable_Wrap(o);
   END_HANDLE_TH_ERRORS
 }
 
@@ -554,7 +561,9 @@ PyObject* gated_recurrence_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     st = api.gated_step(&g.desc, Wx.data_ptr(), at_of<const int32_t>(slots), n_slots, at_of<float>(&state), y.data_ptr(),
                         current_stream());
   }
-  return st ? status(st) : THPVariable_Wrap(y);
+  if (st) return status(st);
+  written(state);
+  return THPVariable_Wrap(y);
   END_HANDLE_TH_ERRORS
 }
 
@@ -709,7 +718,10 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     st = api.clip(count32, types.data(), sizes.data(), at.data(), max_norm, at_of<float>(&norm), ws.data_ptr(), bytes,
                   current_stream());
   }
-  return st ? status(st) : THPVariable_Wrap(norm);
+  if (st) return status(st);
+  if (!std::isinf(max_norm))
+    for (const Tensor& t : held) written(t);
+  return THPVariable_Wrap(norm);
   END_HANDLE_TH_ERRORS
 }
 

@@ -134,3 +134,31 @@ def test_the_timeout_flag_is_refused_where_no_tile_is_brought(S):
     ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
     assert S.rnn_gated_fwd(d, Wx, None, None, y, None, None, ws) == 2
     assert S.rnn_gated_bwd(d, Wx, None, stash, y, None, torch.empty_like(Wx), None, ws) == 2
+
+
+# ------------------------------------------------------ what is written in place --
+def test_what_is_written_in_place_counts_as_changed(S):
+    """Automatic differentiation that saved such a tensor notices; the norm alone writes nothing."""
+    x, none = rand(1, 64), torch.empty(0, device="cuda")
+    leaf = rand(2, 64).requires_grad_()
+    y = (leaf * x).sum()
+    at = x._version
+    S.grad_norm([x])
+    assert x._version == at
+    S.clip_grad_norm([x, none], 1e-3)
+    assert x._version > at
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    state, Wx = rand(3, 4, 2, 8), rand(4, 4, 2, 16)
+    at = state._version
+    S.gated_recurrence_step(Wx, state)
+    assert state._version > at
+    q, memory = rand(6, 4, 2, 8), rand(7, 4, 2, 8, 8)
+    at = memory._version
+    S.linear_attention_step(q, q, q, torch.zeros(2, device="cuda"), memory)
+    assert memory._version > at
+    with torch.inference_mode():  # such tensors have no version
+        z = rand(5, 64)
+        S.clip_grad_norm([z], 1e-3)
+        S.gated_recurrence_step(Wx, state.clone())
+    S.clip_grad_norm([z], 1e-4)
