@@ -79,7 +79,7 @@ class RotaryLayer(LinearLayer):
         q, k = self._turned(q, k, None)
         a = S.linear_attention(q, k, v, self.decay, lens=lens, scale=self.D ** -0.5)
         T, B = q.shape[:2]
-        at = torch.full((B,), T, dtype=torch.int32, device="cuda") if lens is None else lens.clone()
+        at = torch.full((B,), T, dtype=torch.int32, device="cuda") if lens is None else lens.clamp(0, T)
         return stream, self._out(a["o"]), (a["state"], at)
 
     def step(self, stream, out, cache):

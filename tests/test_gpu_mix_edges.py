@@ -162,3 +162,17 @@ def test_what_is_written_in_place_counts_as_changed(S):
         S.clip_grad_norm([z], 1e-3)
         S.gated_recurrence_step(Wx, state.clone())
     S.clip_grad_norm([z], 1e-4)
+
+
+# ------------------------------------------------------------------- example --
+def test_a_rotary_layers_positions_are_its_live_tokens(S):
+    """Lengths beyond the prompt and below zero are taken as its length and none."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import linear_attention_lm as ex
+    m = ex.Model(2, 64, layers=("rotary",), seed=5)
+    x = rand(1, 20, 3, 128, dtype="bf16")
+    _, a = m.prompt(x, ints([20, 0, 7]))
+    _, b = m.prompt(x, ints([25, -4, 7]))
+    assert torch.equal(a[0][0], b[0][0]) and torch.equal(a[0][1], b[0][1]) and a[0][1].tolist() == [20, 0, 7]
