@@ -1,9 +1,11 @@
 """GPU tests of the gated recurrence, the head norm with rotation and the clipping where a lost term or a value that is not
 finite would pass the operators' other tests.  Tolerances as there (the oracle's bounds), or exact."""
+import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_mix_rotary import S, check, ints, rand  # noqa: F401 (S: the fixture)
+from oracle import mix_oracle as O
+from tests.test_gpu_mix_rotary import DT, S, check, close, ints, np64, rand  # noqa: F401 (S: the fixture)
 
 pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
@@ -84,6 +86,90 @@ def test_an_infinity_leaves_zeros_in_columns_that_do_not_turn(S, T, B, H, D, rot
     assert torch.isnan(y[at]).all() and (y[hit & ~at] == 0).all()
 
 
+# shapes of every kernel: batches (lanes that idle, value by value), rings with one group and with several, heads above 256
+TERMS = [(5, 3, 5, 3, 64), (100, 3, 13, 1, 32), (700, 1, 3, 2, 40), (600, 3, 7, 5, 34), (1300, 1, 5, 3, 96), (350, 7, 13, 1, 64),
+         (3, 811, 7, 2, 128), (500, 5, 25, 2, 32), (410, 3, 33, 13, 128), (1300, 1, 1, 29, 64), (9, 137, 7, 1, 256),
+         (614, 2, 49, 50, 32), (1, 1219, 8, 0, 256), (50, 13, 3, 2, 264)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,B,NQ,NK,D", TERMS)
+def test_no_term_of_a_weight_gradient_is_lost(S, T, B, NQ, NK, D, dtype):
+    """With x = dy = 1, eps = 3 and no rotation every term is 1 / sqrt(4): the sum is half their number.  Its error is
+    that of the root (2^-22 of it) and one rounding for each sum on a term's way, of which there are less than 100 (terms of a
+    lane, lanes, warps, CTAs): below a quarter, half a term."""
+    x = [torch.ones(T, B, n, D, dtype=DT[dtype], device="cuda") for n in (NQ, NK)]
+    w = 1 + rand(3, 2, D, scale=0.2)
+    g = S.head_norm_rotary_backward(*x, w[0], w[1], None, None, *x, eps=3.0)
+    for n, H in (("dwq", NQ), ("dwk", NK)):
+        assert T * B * H / 2 * (4 + 100) * 2.0 ** -24 < 0.25
+        assert ((g[n] - T * B * H / 2).abs() < 0.25).all(), (n, g[n])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,B,NQ,NK,D", TERMS)
+def test_a_weight_gradient_of_one_head(S, T, B, NQ, NK, D, dtype):
+    """dy in one head of one token alone, at the ends of tokens and of heads."""
+    q, k = rand(1, T, B, NQ, D, dtype=dtype), rand(2, T, B, NK, D, dtype=dtype)
+    w, f = 1 + rand(3, 2, D, scale=0.2), S.rotary_frequencies(D // 2 * 2)
+    dy = rand(4, 1, 1, 1, D, dtype=dtype)
+    for t, b, h in ((0, 0, 0), (T - 1, B - 1, -1), (T // 2, 0, -1), (T - 1, 0, 0), (0, B - 1, -2), (T // 3, B // 2, 3)):
+        d = [torch.zeros_like(x) for x in (q, k)]
+        for x in d:
+            if x.shape[2]:
+                x[t, b, h % x.shape[2]] = dy
+        g = S.head_norm_rotary_backward(q, k, w[0], w[1], f, None, *d)
+        for i, (n, x) in enumerate((("q", q), ("k", k))):
+            if x.shape[2] == 0:
+                assert (g["dw" + n] == 0).all()
+                continue
+            one = x[t:t + 1, b:b + 1, h % x.shape[2]][:, :, None]
+            _, _, dw, dwe = O.head_norm_rotary_backward(np64(one), np64(w[i]), np64(f), np.array([[t]]), np64(dy), 1e-6, False)
+            close(g["dw" + n], dw, dwe)
+            hit = torch.zeros_like(x, dtype=torch.bool)
+            hit[t, b, h % x.shape[2]] = True
+            assert (g["d" + n][~hit] == 0).all()
+
+
+# ------------------------------------------------------------------ clipping --
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_value_of_a_norm_is_lost(S, dtype):
+    """One value that is not zero, at the ends of vectors, units, tensors and launches' tables: exact norms and factors."""
+    size = [5_000_001, 1, 8192, 4097] + [3 + i % 5 for i in range(300)]
+    flat = [torch.zeros(n, dtype=DT[dtype], device="cuda") for n in size]
+    unit = 16384 // flat[0].element_size()
+    at = [(0, i) for i in (0, 7, 8, unit - 1, unit, 300 * unit - 1, 300 * unit, size[0] // unit * unit, size[0] - 2, size[0] - 1)]
+    at += [(i, n - 1) for i, n in ((1, 1), (2, 8192), (3, 4097), (15, size[15]), (255, size[255]), (256, size[256]), (303, size[303]))]
+    for i, j in at:
+        flat[i][j] = -3.0
+        assert S.grad_norm(flat).item() == 3.0
+        assert S.clip_grad_norm(flat, 0.75).item() == 3.0
+        assert flat[i][j].item() == -0.75 and S.grad_norm(flat).item() == 0.75, (i, j)
+        flat[i][j] = 0.0
+
+
+def test_no_value_of_a_long_tensor_is_lost(S):
+    n = 2 ** 31 + 4099
+    if torch.cuda.get_device_properties(0).total_memory < 20 << 30:
+        pytest.skip("needs 20 GB")
+    x = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    for j in (0, 2 ** 31 - 1, 2 ** 31, n - 1):
+        x[j] = 3.0
+        assert S.clip_grad_norm([x], 1.5).item() == 3.0 and x[j].item() == 1.5
+        x[j] = 0.0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [33, 4096, 100003, 3_000_001, 60_000_000])
+def test_norm_of_many_values(S, n, dtype):
+    """A thread's 64 bytes (32 bf16 values) are summed in four chains of at most 8 in fp32, then in two sums: 10
+    roundings; above them sums carry their rounding errors along, and a CTA's are fp64.  Half of that in the root, and its
+    own rounding: 6 2^-24 (7, with what the carried errors lose)."""
+    x = torch.randn(n, generator=torch.Generator(device="cuda").manual_seed(n), device="cuda", dtype=DT[dtype])
+    want = np.sqrt(sum(float(c.double().square().sum()) for c in x.split(1 << 24)))
+    assert abs(S.grad_norm([x]).item() - want) <= 7 * 2.0 ** -24 * want
+
+
 # ------------------------------------------------------- gated recurrence --
 def config(S, T, B, NH, D, gates, dtype, gradient=False):
     from sequential_rnn_gb300._lib import GATE_COUNTS, rnn_gated_desc_t
@@ -153,7 +239,7 @@ def test_what_is_written_in_place_counts_as_changed(S):
     at = state._version
     S.gated_recurrence_step(Wx, state)
     assert state._version > at
-    q, memory = rand(6, 4, 2, 8), rand(7, 4, 2, 8, 8)
+    q, memory = rand(6, 4, 2, 64), rand(7, 4, 2, 64, 64)
     at = memory._version
     S.linear_attention_step(q, q, q, torch.zeros(2, device="cuda"), memory)
     assert memory._version > at
