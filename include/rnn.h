@@ -437,12 +437,13 @@ int rnn_gated_step(const rnn_gated_desc_t* desc, const void* Wx, const int32_t* 
  *   y = x w / sqrt(mean x^2 + eps);  for j < rot/2 the pair (y1, y2) becomes
  *   (y1 cos - y2 sin, y2 cos + y1 sin) of the angle pos freqs[j]
  * with the pair's columns j and j + rot/2, or 2j and 2j + 1 with RNN_ROTARY_INTERLEAVED; columns from rot on are not
- * turned.  q [T, B, NQ, D], k [T, B, NK, D] in dtype (strided views as for the attention: strides of q and k for
- * (token, row, head), st NULL = contiguous), outputs contiguous in dtype, rounded once.  q_weight, k_weight [D] fp32; both
- * NULL = no norm.  freqs [rot/2] fp64, finite, radians a position (NULL with rot == 0: no rotation).  positions int32:
- * [B], where each row's first token stands, the following ones after it; [T, B] with RNN_ROTARY_PER_TOKEN; NULL = 0 for
+ * turned (y alone, whatever their neighbours hold).  q [T, B, NQ, D], k [T, B, NK, D] in dtype (strided views as for the
+ * attention: strides of q and k for (token, row, head), st NULL = contiguous), outputs contiguous in dtype, rounded once.
+ * q_weight, k_weight [D] fp32; both NULL = no norm.  freqs [rot/2] fp64, below 2^54, radians a position (NULL with
+ * rot == 0: no rotation).  positions int32: [B], where each row's first token stands, the following ones after it; [T, B] with RNN_ROTARY_PER_TOKEN; NULL = 0 for
  * every row.  Any position: angles are formed modulo a turn in 64 bits of fraction.  Squares are summed in fp32: a
- * head with values past 2^63 comes out as zero.
+ * head with values past 2^63 comes out as zero; with eps = 0 one whose values are all below 2^-63 loses bits, below
+ * 2^-75 all of them (infinities, or NaN for zeros).
  * D and rot even, rot <= D <= 4096, T*B at most 2^31 - 1.  Alignment: the element's.  D that is a multiple of 8 up to
  * 256 (and, unless interleaved, rot too) with strides and addresses that are multiples of four values runs the vector
  * kernels. */
@@ -477,8 +478,9 @@ int rnn_head_norm_rotary_bwd(const rnn_rotary_desc_t* desc, const rnn_rotary_str
  * it is finite and above max_norm every value becomes x (max_norm / norm) in place, rounded once; else nothing is written to
  * them.  max_norm >= 0; INFINITY = the norm alone.  dtypes (rnn_dtype_t), sizes (elements; 0 is allowed) and
  * tensors (device memory, aligned as the element is) are host arrays, read before the call returns.  Unless max_norm is
- * INFINITY no two tensors may overlap (RNN_ERR_INVALID_ARG).  Sums are taken in fixed order, with fp64 above
- * 64 bytes; no square overflows (a norm that fp32 cannot hold is told as infinity, and clipped to max_norm all the same).  A tensor's size is at most 2^40, at most 2^28 tensors,
+ * INFINITY no two tensors may overlap (RNN_ERR_INVALID_ARG).  Sums are taken in fixed order: fp32 over 64 bytes, fp32 with
+ * the rounding errors carried along over what a warp takes, fp64 above; no square overflows (a norm that fp32 cannot hold
+ * is told as infinity, and clipped to max_norm all the same).  A tensor's size is at most 2^40, at most 2^28 tensors,
  * 2^31 - 1 pieces of 16 KB in all of them.  Workspace: 256-byte aligned, size below. */
 size_t rnn_clip_grad_norm_workspace_size(int32_t n);
 int rnn_clip_grad_norm(int32_t n, const int32_t* dtypes, const int64_t* sizes, void* const* tensors, float max_norm,

@@ -4,7 +4,7 @@
 // Two kernels over units of 16 KB (the tensors' addresses and sizes come as kernel parameters, so a captured call
 // needs no copy): the sums, one partial a CTA, each CTA a contiguous range of units; then every CTA adds the partials in
 // one order and goes through its range again, from its end, where the L2 still holds it.  Bound by bytes: 3 for every
-// byte of gradient past what the L2 keeps (217 MB take 100-110 us, 5.9-6.5 TB/s of those), and small calls by two kernels'
+// byte of gradient past what the L2 keeps (217 MB take 110 us, 5.9 TB/s of those, 94 the same tensors again), and small calls by two kernels'
 // latencies one after the other (4.7 MB in 6 tensors: 9 us).  Four CTAs on an SM: six take 126 us for the 217 MB; rings of
 // asynchronous copies instead of 64 bytes a thread in registers 118.
 //

@@ -8,9 +8,10 @@
 // exchanging them by st.async -- and hands every run the state at its start; then the run once more, its results written into
 // the tile it came from, from where TMA stores them.  Nothing is read twice and no thread forms an address per token.
 //
-// Bound by issue slots beside the bytes, 24 instructions an element: 16384 tokens of one row of 12 x 64, fz, bf16 take 20 us
-// (3.8 TB/s; 240 CTAs on 152 SMs), 1024 x 16, fzo, 23.7 us (4.5 TB/s) with the states for the gradient, and the
-// gradient 38.9 (4.7 TB/s).
+// Bound by neither bytes nor issue slots alone (24 instructions an element, 44-54% of the slots): 16384 tokens of one row of
+// 12 x 64, fz, bf16 take 20 us (3.8 TB/s), rounds one after the other in 240 CTAs on 152 SMs, of which 64 hold one and the
+// others two; 1024 x 16, fzo, 23.7 us (4.5 TB/s) with the states for the gradient, and the gradient 38.9 (4.7 TB/s; 384 CTAs
+// in 304 places).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -602,8 +603,9 @@ struct Variant {
 
 // Which of them, and how many CTAs along time: the one whose rounds end first.  A round of bf16 runs of two gates takes
 // 0.76 us where maps are made ahead, else 0.80 (CTAs by themselves) or 1.13 (clusters), and 0.46 more for each other
-// CTA on the SM; other gates, types and the gradient stretch all of these alike (1.5 to 2 times).  What does not
-// fit the device at once runs after it.
+// CTA on the SM.  Other gates, types and the gradient take 1.5 to 2 times as long, roughly alike, so that only the
+// wave's 0.3 us weigh too much there; the gradient's and fp32's choices were not timed against all others.  What does
+// not fit the device at once runs after it.
 struct Plan {
   double cost = 1e30;
   int variant = 0, cs = 1, dev = 0, sms = sm_count();

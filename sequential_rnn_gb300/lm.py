@@ -398,8 +398,8 @@ def head_norm_rotary(q, k, q_weight, k_weight, freqs, positions=None, *, eps=1e-
 
     q_weight, k_weight [D] fp32, both None: no norm.  freqs [<= D/2] fp64 (``rotary_frequencies``), None: no
     rotation.  positions int32: [B] where each row's first token stands (the others follow), or [T, B];
-    None: 0.  The pairs are columns j and j + len(freqs), ``interleaved``: 2j and 2j + 1.  Returns (q, k),
-    contiguous.
+    None: 0.  The pairs are columns j and j + len(freqs), ``interleaved``: 2j and 2j + 1; the columns behind them
+    do not turn.  Returns (q, k), contiguous.
     """
     if stream is not None:
         with _on(stream):
