@@ -440,10 +440,10 @@ int rnn_gated_step(const rnn_gated_desc_t* desc, const void* Wx, const int32_t* 
  * turned (y alone, whatever their neighbours hold).  q [T, B, NQ, D], k [T, B, NK, D] in dtype (strided views as for the
  * attention: strides of q and k for (token, row, head), st NULL = contiguous), outputs contiguous in dtype, rounded once.
  * q_weight, k_weight [D] fp32; both NULL = no norm.  freqs [rot/2] fp64, below 2^54, radians a position (NULL with
- * rot == 0: no rotation).  positions int32: [B], where each row's first token stands, the following ones after it; [T, B] with RNN_ROTARY_PER_TOKEN; NULL = 0 for
- * every row.  Any position: angles are formed modulo a turn in 64 bits of fraction.  Squares are summed in fp32: a
- * head with values past 2^63 comes out as zero; with eps = 0 one whose values are all below 2^-63 loses bits, below
- * 2^-75 all of them (infinities, or NaN for zeros).
+ * rot == 0: no rotation).  positions int32: [B], where each row's first token stands, the following ones after it;
+ * [T, B] with RNN_ROTARY_PER_TOKEN; NULL = 0 for every row.  Any position: angles are formed modulo a turn in 64 bits of
+ * fraction.  Squares are summed in fp32: a head with values past 2^63 comes out as zero; with eps = 0 one whose values
+ * are all below 2^-63 loses bits, below 2^-75 all of them (infinities, or NaN for zeros).
  * D and rot even, rot <= D <= 4096, T*B at most 2^31 - 1.  Alignment: the element's.  D that is a multiple of 8 up to
  * 256 (and, unless interleaved, rot too) with strides and addresses that are multiples of four values runs the vector
  * kernels. */

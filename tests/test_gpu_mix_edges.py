@@ -131,6 +131,25 @@ def test_a_weight_gradient_of_one_head(S, T, B, NQ, NK, D, dtype):
             assert (g["d" + n][~hit] == 0).all()
 
 
+def test_a_weight_gradient_of_a_late_head(S):
+    """dy in one head behind 2^31 values, in the last token of a row and in one before it."""
+    if torch.cuda.get_device_properties(0).total_memory < 60 << 30:
+        pytest.skip("needs 60 GB")
+    T, B, NH, D = 4100, 64, 64, 128
+    q = torch.randn(T, B, NH, D, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda", dtype=torch.bfloat16)
+    k, w, f = q[:, :, :2], 1 + rand(3, D, scale=0.2), S.rotary_frequencies(D)
+    d, dy = torch.zeros_like(q), rand(4, 1, 1, 1, D, dtype="bf16")
+    for t, b, h in ((T - 1, B - 1, NH - 1), (T - 2, 0, 1)):
+        d[t, b, h] = dy
+        g = S.head_norm_rotary_backward(q, k, w, w, f, None, d, d[:, :, :2])
+        _, _, dw, dwe = O.head_norm_rotary_backward(np64(q[t:t + 1, b:b + 1, h:h + 1]), np64(w), np64(f), np.array([[t]]), np64(dy),
+                                                    1e-6, False)
+        close(g["dwq"], dw, dwe)
+        close(g["dwk"], dw * (h < 2), dwe)
+        d[t, b, h] = 0
+        del g
+
+
 # ------------------------------------------------------------------ clipping --
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_no_value_of_a_norm_is_lost(S, dtype):
